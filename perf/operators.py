@@ -6,7 +6,8 @@ Four operators, all on BF16 operands:
           lse_t = log sum_v exp z_tv, loss_t = lse_t - z_t,label(t); a label outside [0, vocab) ignores its row (loss 0)
   grad    its gradient: g_tv = alpha dloss_t (exp(z_tv - lse_t) - [v = label(t)]), dX = g W, dW = g^T X
   dgrad   expert products D = A B_g^T with row counts in device memory: gradient to the rows, dA = alpha dD B_g
-  wgrad   the same products: gradient to the experts' matrices, dB_g = alpha dD_g^T A_g (dense training: one group)
+  wgrad   the same products: gradient to the experts' matrices, dB_g = alpha dD_g^T A_g (dense training: one group),
+          written in BF16 or added to FP32 values (accumulation over micro-batches)
 
 Where `own` is true, run() makes the library's calls; where it is false, elementary torch operations in 32 bits.
 """
@@ -46,13 +47,13 @@ def listed():
          "k": 2048, "skew": 0.7},
         # the same few rows: the gradient written for every expert bounds the time
         {"name": "wgrad few rows", "op": "wgrad", "groups": 8, "empty": 1, "rows": 128, "spare": 0, "n": 4096, "k": 7168,
-         "skew": 0.7},
-        # the uneven training batch above
+         "skew": 0.7, "add": False},
+        # the uneven training batch above, one of several micro-batches accumulated in FP32
         {"name": "wgrad ragged", "op": "wgrad", "groups": 64, "empty": 4, "rows": 16000, "spare": 384, "n": 2048,
-         "k": 2048, "skew": 0.7},
+         "k": 2048, "skew": 0.7, "add": True},
         # a large training batch on 8 wide experts
         {"name": "wgrad large", "op": "wgrad", "groups": 8, "empty": 0, "rows": 16384, "spare": 0, "n": 4096, "k": 7168,
-         "skew": 0.4},
+         "skew": 0.4, "add": False},
     ]
 
 
@@ -68,9 +69,12 @@ def draw(rng):
                 "alpha": rng.choice([1.0, 1.0, 0.5])}
     groups = _log(rng, 1, 64)
     empty = rng.randint(0, groups // 4)
-    return {"op": op, "groups": groups, "empty": empty, "rows": _log(rng, max(16, groups), 16384),
+    case = {"op": op, "groups": groups, "empty": empty, "rows": _log(rng, max(16, groups), 16384),
             "spare": rng.choice([0, 0, 1, 130]), "n": 8 * _log(rng, 32, 512), "k": 8 * _log(rng, 32, 512),
             "skew": rng.choice([0.0, 0.4, 0.8])}
+    if op == "wgrad":
+        case["add"] = rng.choice([False, False, True])
+    return case
 
 
 def _sizes(case, seed):
@@ -128,7 +132,10 @@ def prepare(case, seed):
         s["dA"] = torch.empty(cap, k, device="cuda", dtype=BF16)
     else:
         s["A"] = normal(cap, k)
-        s["dB"] = torch.empty(case["groups"], n, k, device="cuda", dtype=BF16)
+        if case["add"]:   # what earlier micro-batches left
+            s["dB"] = torch.randn(case["groups"], n, k, generator=gen, device="cuda") * math.sqrt(rows / case["groups"])
+        else:
+            s["dB"] = torch.empty(case["groups"], n, k, device="cuda", dtype=BF16)
     return s
 
 
@@ -156,6 +163,8 @@ def run(s):
     if op == "dgrad":
         return {"dA": torch.cat([d.float() @ b.float() for d, b in zip(dDs, s["B"])]).to(BF16)}
     As = s["A"][:s["rows"]].split(s["sizes"])
+    if s["add"]:
+        return {"dB": s["dB"].add_(torch.stack([d.float().T @ a.float() for d, a in zip(dDs, As)]))}
     return {"dB": torch.stack([(d.float().T @ a.float()).to(BF16) for d, a in zip(dDs, As)])}
 
 
@@ -171,7 +180,7 @@ def _run_own(s):
     if op == "dgrad":
         tkg.gemm_grouped_dev_bf16_dgrad(s["sizes_dev"], s["dD"], s["B"], s["dA"])
         return {"dA": s["dA"][:s["rows"]]}
-    tkg.gemm_grouped_dev_bf16_wgrad(s["sizes_dev"], s["dD"], s["A"], s["dB"])
+    tkg.gemm_grouped_dev_bf16_wgrad(s["sizes_dev"], s["dD"], s["A"], s["dB"], accumulate=s["add"])
     return {"dB": s["dB"]}
 
 
@@ -182,8 +191,13 @@ def work(case):
             return {"bytes": 2 * (t + v) * h + 16 * t, "flops": 2 * t * v * h}
         return {"bytes": 4 * (t + v) * h + 16 * t, "flops": 6 * t * v * h}
     g, r, n, k = case["groups"], case["rows"], case["n"], case["k"]
-    read = g - case["empty"] if case["op"] == "dgrad" else g   # matrices read (dgrad) or written (wgrad)
-    return {"bytes": 2 * (r * (n + k) + read * n * k) + 4 * g, "flops": 2 * r * n * k}
+    if case["op"] == "dgrad":
+        matrices = 2 * (g - case["empty"])          # read for the experts that have rows
+    elif case["add"]:
+        matrices = 8 * (g - case["empty"])          # read and written back in FP32 where there are rows
+    else:
+        matrices = 2 * g                            # written for every expert
+    return {"bytes": 2 * r * (n + k) + matrices * n * k + 4 * g, "flops": 2 * r * n * k}
 
 
 # ---------------------------------------------------------------- the definitions in 64 bits
@@ -223,5 +237,6 @@ def exact(case, seed):
         for g, B in enumerate(s["B"]):
             out[off[g]:off[g + 1]] = torch.einsum("in,nk->ik", s["dD"][off[g]:off[g + 1]].to(f64), B.to(f64))
         return {"dA": out}
-    return {"dB": torch.stack([torch.einsum("in,ik->nk", s["dD"][off[g]:off[g + 1]].to(f64),
-                                            s["A"][off[g]:off[g + 1]].to(f64)) for g in range(case["groups"])])}
+    dB = torch.stack([torch.einsum("in,ik->nk", s["dD"][off[g]:off[g + 1]].to(f64),
+                                   s["A"][off[g]:off[g + 1]].to(f64)) for g in range(case["groups"])])
+    return {"dB": dB + s["dB"].to(f64) if case["add"] else dB}
