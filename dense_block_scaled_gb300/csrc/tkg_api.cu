@@ -8,6 +8,7 @@
 #include <mutex>
 
 #include "host_common.cuh"
+#include "train_host.cuh"
 
 namespace tkg {
 
@@ -201,6 +202,14 @@ tkg_status encode_3d(CUtensorMap* map, CUtensorMapDataType dtype, const void* ba
                      uint32_t box2) {
   MapKey k{uint32_t(dtype), 3u, uint32_t(CU_TENSOR_MAP_SWIZZLE_NONE), base, {dim0, dim1, dim2},
            {stride1_bytes, stride2_bytes}, {box0, box1, box2}};
+  return encode_cached(map, k);
+}
+
+tkg_status encode_3d_swizzled(CUtensorMap* map, CUtensorMapDataType dtype, const void* base, uint64_t dim0,
+                              uint64_t dim1, uint64_t dim2, uint64_t stride1_bytes, uint64_t stride2_bytes,
+                              uint32_t box0, uint32_t box1, uint32_t box2, CUtensorMapSwizzle swz) {
+  MapKey k{uint32_t(dtype), 3u, uint32_t(swz), base, {dim0, dim1, dim2}, {stride1_bytes, stride2_bytes},
+           {box0, box1, box2}};
   return encode_cached(map, k);
 }
 

@@ -1,0 +1,135 @@
+// train_host.cuh -- host side of train_kernel.cuh: tensor maps of the two operand
+// orders and of the outputs, and the launch.
+#pragma once
+#include "host_common.cuh"
+#include "train_kernel.cuh"
+
+namespace tkg {
+
+// tkg_api.cu: as encode_3d, with a swizzle
+tkg_status encode_3d_swizzled(CUtensorMap* map, CUtensorMapDataType dtype, const void* base, uint64_t dim0,
+                              uint64_t dim1, uint64_t dim2, uint64_t stride1_bytes, uint64_t stride2_bytes,
+                              uint32_t box0, uint32_t box1, uint32_t box2, CUtensorMapSwizzle swz);
+
+inline bool aligned_to(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+
+// k rows of an MN-major box: 64, or all there are rounded up to the MMA's 16 (rows past the end arrive as
+// zeros; a box that runs mostly past the end slows the load stream)
+inline uint32_t mn_box_rows(int k) { return k >= 64 ? 64u : uint32_t((k + 15) / 16 * 16); }
+
+// K-major operand: `rows` rows of k BF16; boxes of 64 k by up to `tile_rows` rows.
+inline tkg_status map_k_major(CUtensorMap* map, const void* base, int rows, int k, size_t row_bytes, int tile_rows) {
+  return encode_2d(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, base, uint64_t(k), uint64_t(rows), row_bytes, 64,
+                   uint32_t(rows < tile_rows ? rows : tile_rows), CU_TENSOR_MAP_SWIZZLE_128B);
+}
+// MN-major operand: k rows of `mn` BF16; boxes of 64 mn by up to 64 k.
+inline tkg_status map_mn_major(CUtensorMap* map, const void* base, int mn, int k, size_t row_bytes) {
+  return encode_2d(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, base, uint64_t(mn), uint64_t(k), row_bytes, 64,
+                   mn_box_rows(k), CU_TENSOR_MAP_SWIZZLE_128B);
+}
+// Output: `parts` matrices of m x n, 32-row x 64-byte store boxes.
+inline tkg_status map_out(CUtensorMap* map, const void* base, int m, int n, int parts, size_t row_bytes,
+                          size_t part_bytes, bool f32) {
+  return encode_3d_swizzled(map, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, base,
+                            uint64_t(n), uint64_t(m), uint64_t(parts), row_bytes, part_bytes, f32 ? 16 : 32, 32, 1,
+                            CU_TENSOR_MAP_SWIZZLE_64B);
+}
+
+// Bytes one stage brings to the full barrier, over the CTAs of the cluster.
+template <bool A_MN, bool B_MN, int EPI, int CG, int GRP>
+uint32_t train_tx_bytes(int m, int n, int k) {
+  using C = TrainConfig<A_MN, B_MN, EPI, CG, GRP>;
+  const int kb = int(GRP == GRP_K ? 64 : mn_box_rows(k));
+  const int a = A_MN ? 2 * kb * 128 : (m < 128 ? m : 128) * 128;
+  const int b = B_MN ? (C::kBRows / 64) * kb * 128 : (n < C::kBRows ? n : C::kBRows) * 128;
+  return uint32_t(CG * (a + b));
+}
+
+// Fills the fields common to every launch and launches.  p.m, n, k, splits (at
+// least 1), split_stages, alpha and the epilogue's own fields are set by the caller.
+template <bool A_MN, bool B_MN, int EPI, int CG, int GRP>
+tkg_status launch_train(const CUtensorMap& tmA, const CUtensorMap& tmB, const CUtensorMap& tmD, TrainParams p,
+                        cudaStream_t stream) {
+  using C = TrainConfig<A_MN, B_MN, EPI, CG, GRP>;
+  auto kern = train_kernel<A_MN, B_MN, EPI, CG, GRP>;
+  // more than half an SM's shared memory: no two CTAs share an SM (each takes all of tensor memory)
+  static_assert(C::kSmemBytes > 118784, "one CTA per SM");
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return TKG_ERR_CUDA;
+  static bool attr_set[64] = {};   // per instantiation and device (idempotent if two threads race)
+  if (!attr_set[dev]) {
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes) != cudaSuccess) {
+      cudaGetLastError();
+      return TKG_ERR_CUDA;
+    }
+    attr_set[dev] = true;
+  }
+  tkg_status st;
+  if ((st = device_status_word(&p.status)) != TKG_OK) return st;
+  const int tmo = option(TKG_OPT_TIMEOUT_MS);
+  p.timeout_ns = 1000000ull * (unsigned long long)(tmo > 0 ? tmo : 1000);
+  p.inject_stall = option(TKG_OPT_INJECT_STALL);
+  p.kstages = ceil_div(p.k, 64);
+  p.tiles_m = ceil_div(p.m, C::kMmaM);
+  p.tiles_n = ceil_div(p.n, C::kBN);
+  p.tx_bytes = train_tx_bytes<A_MN, B_MN, EPI, CG, GRP>(p.m, p.n, p.k);
+  p.raster_group = raster_group(C::kMmaM, GRP == GRP_K ? ceil_div(p.k, p.groups) : p.k, FMT_BF16, p.tiles_m);
+  long long tiles = (long long)p.tiles_m * p.tiles_n;
+  if (GRP == GRP_NONE) tiles *= p.splits;
+  if (GRP == GRP_K) tiles *= p.groups;
+  if (GRP == GRP_ROWS) tiles = (long long)(p.tiles_m + p.groups) * p.tiles_n;   // at most
+  if (tiles * CG > 0x7fffffffLL) return TKG_ERR_UNSUPPORTED;
+  p.num_tiles = int(tiles);
+
+  long long clusters = tiles;   // cluster launch control: one cluster per tile
+  if (!C::kClc) {
+    int resident = 0;
+    if ((st = CG == 2 ? device_max_clusters(2, &resident) : device_sm_count(&resident)) != TKG_OK) return st;
+    if (clusters > resident) clusters = resident;
+  }
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[2];
+  cfg.gridDim = dim3(unsigned(clusters * CG), 1, 1);
+  cfg.blockDim = dim3(C::kThreads, 1, 1);
+  cfg.dynamicSmemBytes = C::kSmemBytes;
+  cfg.stream = stream;
+  int nattr = 0;
+  if (CG == 2) {
+    attr[nattr].id = cudaLaunchAttributeClusterDimension;
+    attr[nattr].val.clusterDim.x = CG;
+    attr[nattr].val.clusterDim.y = 1;
+    attr[nattr].val.clusterDim.z = 1;
+    ++nattr;
+  }
+  attr[nattr].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[nattr].val.programmaticStreamSerializationAllowed = 1;
+  ++nattr;
+  cfg.attrs = attr;
+  cfg.numAttrs = nattr;
+  if (cudaLaunchKernelEx(&cfg, kern, tmA, tmB, tmD, p) != cudaSuccess) {
+    cudaGetLastError();
+    return TKG_ERR_CUDA;
+  }
+  return TKG_OK;
+}
+
+// Launch of a small kernel that waits for the previous grid itself (griddepcontrol.wait).
+template <typename... P, typename... Args>
+tkg_status launch_small(void (*kern)(P...), dim3 grid, dim3 block, cudaStream_t stream, Args... args) {
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.stream = stream;
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, kern, P(args)...) != cudaSuccess) {
+    cudaGetLastError();
+    return TKG_ERR_CUDA;
+  }
+  return TKG_OK;
+}
+
+}  // namespace tkg

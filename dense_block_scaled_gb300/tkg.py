@@ -36,9 +36,14 @@ EXPORTS = [
     "tkg_gemm_grouped_dev_nvfp4", "tkg_grouped_dev_scale_bytes", "tkg_quantize_nvfp4_scaled",
     "tkg_gemm_list_bf16", "tkg_gemm_list_mxfp8", "tkg_gemm_list_nvfp4",
     "tkg_gemm_bf16_strided", "tkg_gemm_mxfp8_strided", "tkg_gemm_nvfp4_strided",
+    "tkg_linear_ce_loss", "tkg_linear_ce_loss_workspace_bytes", "tkg_linear_ce_grad",
+    "tkg_linear_ce_grad_workspace_bytes", "tkg_gemm_grouped_dev_bf16_dgrad", "tkg_gemm_grouped_dev_bf16_wgrad",
+    "tkg_gemm_grouped_dev_bf16_wgrad_workspace_bytes",
 ]
 
 MAX_LIST = 16
+
+GRAD_BF16, GRAD_F32, GRAD_F32_ADD = 0, 1, 2
 
 
 class GemmDesc(ctypes.Structure):
@@ -93,6 +98,20 @@ def load() -> ctypes.CDLL:
             lib.tkg_gemm_nvfp4_strided.argtypes = [i, i, i, vp, i, vp, i, vp, vp, vp, vp, vp, i, f, vp]
             for name in ("tkg_gemm_bf16_strided", "tkg_gemm_mxfp8_strided", "tkg_gemm_nvfp4_strided"):
                 getattr(lib, name).restype = ctypes.c_int
+            sz = ctypes.c_size_t
+            lib.tkg_linear_ce_loss.argtypes = [i, i, i, vp, i, vp, i, vp, f, vp, vp, vp, sz, vp]
+            lib.tkg_linear_ce_loss_workspace_bytes.argtypes = [i, i]
+            lib.tkg_linear_ce_grad.argtypes = [i, i, i, vp, i, vp, i, vp, f, vp, vp, vp, i, vp, i, i, i, vp, sz, vp]
+            lib.tkg_linear_ce_grad_workspace_bytes.argtypes = [i, i, i, i]
+            lib.tkg_gemm_grouped_dev_bf16_dgrad.argtypes = [i, vp, i, i, i, vp, vp, vp, f, vp]
+            lib.tkg_gemm_grouped_dev_bf16_wgrad.argtypes = [i, vp, i, i, i, vp, vp, vp, i, f, vp, sz, vp]
+            lib.tkg_gemm_grouped_dev_bf16_wgrad_workspace_bytes.argtypes = [i]
+            for name in ("tkg_linear_ce_loss", "tkg_linear_ce_grad", "tkg_gemm_grouped_dev_bf16_dgrad",
+                         "tkg_gemm_grouped_dev_bf16_wgrad"):
+                getattr(lib, name).restype = ctypes.c_int
+            for name in ("tkg_linear_ce_loss_workspace_bytes", "tkg_linear_ce_grad_workspace_bytes",
+                         "tkg_gemm_grouped_dev_bf16_wgrad_workspace_bytes"):
+                getattr(lib, name).restype = sz
             lib.tkg_get_device_status.argtypes = [vp]
             lib.tkg_status_string.argtypes = [st]
             lib.tkg_status_string.restype = ctypes.c_char_p
@@ -301,6 +320,138 @@ def gemm_desc(fmt: str, A, B, D, alpha: float = 1.0, sfa=None, sfb=None, ta=None
 def gemm_list(fmt: str, descs, stream=None) -> None:
     """Several independent GEMMs (GemmDesc each, at most MAX_LIST) in one launch."""
     _check(gemm_list_raw(fmt, descs, _stream(stream)), f"tkg_gemm_list_{fmt}")
+
+
+# ---------------------------------------------------------------- training-side operators
+
+def _rows_of(t, name):
+    """A 2-D tensor whose rows may be pitched but are contiguous inside; returns its row pitch in elements."""
+    if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
+        raise ValueError(f"{name}: a matrix with contiguous rows is wanted")
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+
+
+def _want(t, name, dtype, shape):
+    if t.dtype != dtype or tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name}: {dtype} of shape {tuple(shape)} is wanted, got {t.dtype} {tuple(t.shape)}")
+
+
+def _want_dense(t, name, dtype, shape):
+    _want(t, name, dtype, shape)
+    if not t.is_contiguous():
+        raise ValueError(f"{name}: a contiguous tensor is wanted")
+
+
+def _workspace(workspace, nbytes, like, stream):
+    """The caller's workspace, or one from torch's allocator (kept for the work on `stream`)."""
+    import torch
+    if workspace is None:
+        workspace = torch.empty(nbytes, dtype=torch.uint8, device=like.device)
+        if stream is not None:
+            s = torch.cuda.ExternalStream(stream) if isinstance(stream, int) else stream
+            if s != torch.cuda.current_stream():
+                # the memory may have been used by work of the current stream, and must outlive that of `stream`
+                s.wait_stream(torch.cuda.current_stream())
+                workspace.record_stream(s)
+    return workspace, workspace.numel() * workspace.element_size()
+
+
+def linear_ce_loss_workspace_bytes(tokens: int, vocab: int) -> int:
+    return int(load().tkg_linear_ce_loss_workspace_bytes(tokens, vocab))
+
+
+def linear_ce_loss(X, W, labels, loss, lse, alpha: float = 1.0, workspace=None, stream=None) -> None:
+    """Softmax cross entropy of the head alpha * X @ W^T: loss and log-sum-exp per token (FP32), logits never kept.
+
+    X (tokens x hidden bf16), W (vocab x hidden bf16), rows may be pitched; labels int64, outside [0, vocab): ignored."""
+    import torch
+    tokens, hidden = X.shape
+    vocab = W.shape[0]
+    _want(X, "X", torch.bfloat16, (tokens, hidden))
+    _want(W, "W", torch.bfloat16, (vocab, hidden))
+    _want_dense(labels, "labels", torch.int64, (tokens,))
+    _want_dense(loss, "loss", torch.float32, (tokens,))
+    _want_dense(lse, "lse", torch.float32, (tokens,))
+    lib = load()
+    ws, nbytes = _workspace(workspace, lib.tkg_linear_ce_loss_workspace_bytes(tokens, vocab), X, stream)
+    _check(lib.tkg_linear_ce_loss(tokens, vocab, hidden, X.data_ptr(), _rows_of(X, "X"), W.data_ptr(),
+                                  _rows_of(W, "W"), labels.data_ptr(), alpha, loss.data_ptr(), lse.data_ptr(),
+                                  ws.data_ptr(), nbytes, _stream(stream)), "tkg_linear_ce_loss")
+
+
+def linear_ce_grad_workspace_bytes(tokens: int, vocab: int, hidden: int, piece: int = 0) -> int:
+    return int(load().tkg_linear_ce_grad_workspace_bytes(tokens, vocab, hidden, piece))
+
+
+def _grad_type(t, name, accumulate):
+    import torch
+    if t.dtype == torch.bfloat16 and not accumulate:
+        return GRAD_BF16
+    if t.dtype != torch.float32:
+        raise ValueError(f"{name}: bfloat16, or float32 (the type that can accumulate) is wanted, got {t.dtype}")
+    return GRAD_F32_ADD if accumulate else GRAD_F32
+
+
+def linear_ce_grad(X, W, labels, lse, dloss, dX, dW, alpha: float = 1.0, accumulate: bool = False, piece: int = 0,
+                   workspace=None, stream=None) -> None:
+    """Gradient of sum(dloss * loss): dX (tokens x hidden bf16) and dW (vocab x hidden, bf16 or float32); either may
+    be None.  accumulate: add to the float32 dW.  piece: vocabulary entries worked on at a time (0: chosen)."""
+    import torch
+    tokens, hidden = X.shape
+    vocab = W.shape[0]
+    _want(X, "X", torch.bfloat16, (tokens, hidden))
+    _want(W, "W", torch.bfloat16, (vocab, hidden))
+    _want_dense(labels, "labels", torch.int64, (tokens,))
+    _want_dense(lse, "lse", torch.float32, (tokens,))
+    _want_dense(dloss, "dloss", torch.float32, (tokens,))
+    lddx = lddw = gtype = 0
+    if dX is not None:
+        _want(dX, "dX", torch.bfloat16, (tokens, hidden))
+        lddx = _rows_of(dX, "dX")
+    if dW is not None:
+        gtype = _grad_type(dW, "dW", accumulate)
+        _want(dW, "dW", dW.dtype, (vocab, hidden))
+        lddw = _rows_of(dW, "dW")
+    lib = load()
+    ws, nbytes = _workspace(workspace, lib.tkg_linear_ce_grad_workspace_bytes(tokens, vocab, hidden, piece), X, stream)
+    _check(lib.tkg_linear_ce_grad(tokens, vocab, hidden, X.data_ptr(), _rows_of(X, "X"), W.data_ptr(),
+                                  _rows_of(W, "W"), labels.data_ptr(), alpha, lse.data_ptr(), dloss.data_ptr(),
+                                  _ptr(dX), lddx, _ptr(dW), lddw, gtype, piece, ws.data_ptr(), nbytes,
+                                  _stream(stream)), "tkg_linear_ce_grad")
+
+
+def gemm_grouped_dev_bf16_dgrad(sizes_dev, dD, B, dA, alpha: float = 1.0, stream=None) -> None:
+    """Gradient of gemm_grouped_dev_bf16 to its rows: dA (capacity x k) = alpha * dD (capacity x n) @ B_g (n x k)."""
+    import torch
+    groups, (cap, n), k = sizes_dev.numel(), dD.shape, B.shape[-1]
+    _want_dense(sizes_dev, "sizes_dev", torch.int32, (groups,))
+    _want_dense(dD, "dD", torch.bfloat16, (cap, n))
+    _want_dense(B, "B", torch.bfloat16, (groups, n, k))
+    _want_dense(dA, "dA", torch.bfloat16, (cap, k))
+    _check(load().tkg_gemm_grouped_dev_bf16_dgrad(groups, sizes_dev.data_ptr(), cap, n, k, dD.data_ptr(),
+                                                  B.data_ptr(), dA.data_ptr(), alpha, _stream(stream)),
+           "tkg_gemm_grouped_dev_bf16_dgrad")
+
+
+def gemm_grouped_dev_bf16_wgrad_workspace_bytes(groups: int) -> int:
+    return int(load().tkg_gemm_grouped_dev_bf16_wgrad_workspace_bytes(groups))
+
+
+def gemm_grouped_dev_bf16_wgrad(sizes_dev, dD, A, dB, alpha: float = 1.0, accumulate: bool = False, workspace=None,
+                                stream=None) -> None:
+    """Gradient of gemm_grouped_dev_bf16 to the experts: dB_g (n x k, bf16 or float32) = alpha * dD_g^T @ A_g."""
+    import torch
+    groups, (cap, n), k = sizes_dev.numel(), dD.shape, A.shape[-1]
+    _want_dense(sizes_dev, "sizes_dev", torch.int32, (groups,))
+    _want_dense(dD, "dD", torch.bfloat16, (cap, n))
+    _want_dense(A, "A", torch.bfloat16, (cap, k))
+    gtype = _grad_type(dB, "dB", accumulate)
+    _want_dense(dB, "dB", dB.dtype, (groups, n, k))
+    lib = load()
+    ws, nbytes = _workspace(workspace, lib.tkg_gemm_grouped_dev_bf16_wgrad_workspace_bytes(groups), dD, stream)
+    _check(lib.tkg_gemm_grouped_dev_bf16_wgrad(groups, sizes_dev.data_ptr(), cap, n, k, dD.data_ptr(), A.data_ptr(),
+                                               dB.data_ptr(), gtype, alpha, ws.data_ptr(), nbytes, _stream(stream)),
+           "tkg_gemm_grouped_dev_bf16_wgrad")
 
 
 def grouped_dev_scale_bytes(groups: int, m_capacity: int, k: int, block: int) -> int:

@@ -256,6 +256,78 @@ tkg_status tkg_gemm_bf16_from_host(int m, int n, int k, const void *A_host, cons
 tkg_status tkg_gemm_bf16_noalloc(int m, int n, int k, const void *A, const void *B, void *D, float alpha,
                                  cudaStream_t stream);
 
+/* ---- Training-side operators: the loss on a head's product, and gradients.
+ * BF16 operands, FP32 accumulation and statistics.
+ *
+ * Softmax cross entropy of a linear head over a large vocabulary:
+ *   z[t][v] = alpha * sum_h X[t][h] * W[v][h]              (never stored)
+ *   lse[t]  = log sum_v exp z[t][v]
+ *   loss[t] = lse[t] - z[t][labels[t]]
+ * X: tokens x hidden (row pitch ldx), W: vocab x hidden (row pitch ldw), both
+ * bfloat16; labels: 64-bit, one per token.  A label outside [0, vocab) (such as
+ * -100) ignores its row: loss 0 (lse is still that row's).  loss, lse: FP32.
+ *  - Requires hidden % 8 == 0, pitches >= hidden and multiples of 8 elements
+ *    (16 bytes), 16-byte aligned X, W and workspace.  vocab and tokens are free.
+ *  - workspace: device memory, at least tkg_linear_ce_loss_workspace_bytes(),
+ *    contents undefined before and after; calls that may overlap on the GPU
+ *    need one each.
+ *  - tokens == 0: nothing to do.  vocab == 0 or hidden == 0: TKG_ERR_UNSUPPORTED.
+ *  - A workspace that is too small, or a null pointer: TKG_ERR_INVALID_ARG. */
+tkg_status tkg_linear_ce_loss(int tokens, int vocab, int hidden, const void *X, int ldx, const void *W, int ldw,
+                              const long long *labels, float alpha, float *loss, float *lse, void *workspace,
+                              size_t workspace_bytes, cudaStream_t stream);
+size_t tkg_linear_ce_loss_workspace_bytes(int tokens, int vocab);
+
+/* How a weight gradient is written. */
+typedef enum {
+  TKG_GRAD_BF16 = 0,      /* rounded to nearest-even BF16 */
+  TKG_GRAD_F32 = 1,       /* stored as FP32 */
+  TKG_GRAD_F32_ADD = 2    /* added to the FP32 values there (accumulation over micro-batches) */
+} tkg_grad_type;
+
+/* The gradient of sum_t dloss[t] * loss[t]:
+ *   g[t][v] = alpha * dloss[t] * (exp(z[t][v] - lse[t]) - [v == labels[t]]),  0 for ignored rows
+ *   dX = g W  (tokens x hidden BF16, pitch lddx),  dW (+)= g^T X  (vocab x hidden, pitch lddw in elements)
+ * lse: as tkg_linear_ce_loss wrote it; dloss: FP32 per token.  Either of dX and
+ * dW may be NULL (not wanted).  Ignored rows give dX rows of zeros and nothing
+ * to dW, whatever X, lse and dloss hold there (infinities and NaN included).
+ *  - The vocabulary is worked through in pieces of `piece` entries (0: chosen
+ *    from the sizes), z being computed again for each; g exists for one piece at
+ *    a time, in BF16 (the products' operand type: dX and dW carry its relative
+ *    rounding error of at most 2^-9 per term in any output type).
+ *  - workspace: at least tkg_linear_ce_grad_workspace_bytes() with the same
+ *    sizes and piece.  Sums are made in a fixed order: the same inputs give the
+ *    same bits.
+ *  - tokens == 0: dW is zeroed (not for TKG_GRAD_F32_ADD).  Otherwise as
+ *    tkg_linear_ce_loss. */
+tkg_status tkg_linear_ce_grad(int tokens, int vocab, int hidden, const void *X, int ldx, const void *W, int ldw,
+                              const long long *labels, float alpha, const float *lse, const float *dloss, void *dX,
+                              int lddx, void *dW, int lddw, tkg_grad_type dw_type, int piece, void *workspace,
+                              size_t workspace_bytes, cudaStream_t stream);
+size_t tkg_linear_ce_grad_workspace_bytes(int tokens, int vocab, int hidden, int piece);
+
+/* Gradients of tkg_gemm_grouped_dev_bf16 (the same groups, sizes in device
+ * memory, capacity and layouts; o_g is group g's first row):
+ *   dgrad: dA[o_g + i][kk] = bf16_rn(alpha * sum_j dD[o_g + i][j] * B_g[j][kk])
+ *   wgrad: dB_g[j][kk] (+)= alpha * sum_i dD[o_g + i][j] * A[o_g + i][kk]
+ * dD: m_capacity x n, A and dA: m_capacity x k, B and dB: groups x n x k.
+ *  - Rows outside the groups are neither read into results (whatever they hold)
+ *    nor written; counts past m_capacity are cut off.  A group without rows has
+ *    dB_g = 0 (TKG_GRAD_F32_ADD: unchanged).  groups == 1 is the plain product.
+ *  - Requires n % 8 == 0, k % 8 == 0, 16-byte aligned pointers, groups <= 128;
+ *    wgrad's workspace is 128-byte aligned and holds
+ *    tkg_gemm_grouped_dev_bf16_wgrad_workspace_bytes(groups) bytes; calls that
+ *    may overlap on the GPU need one each.
+ *  - dgrad: n == 0 gives TKG_ERR_UNSUPPORTED; k == 0 or m_capacity == 0: nothing
+ *    to do.  wgrad: m_capacity == 0 zeroes dB (not for TKG_GRAD_F32_ADD). */
+tkg_status tkg_gemm_grouped_dev_bf16_dgrad(int groups, const int *m_sizes_dev, int m_capacity, int n, int k,
+                                           const void *dD, const void *B, void *dA, float alpha,
+                                           cudaStream_t stream);
+tkg_status tkg_gemm_grouped_dev_bf16_wgrad(int groups, const int *m_sizes_dev, int m_capacity, int n, int k,
+                                           const void *dD, const void *A, void *dB, tkg_grad_type type, float alpha,
+                                           void *workspace, size_t workspace_bytes, cudaStream_t stream);
+size_t tkg_gemm_grouped_dev_bf16_wgrad_workspace_bytes(int groups);
+
 /* Check builds.  `python -m dense_block_scaled_gb300.build --check` builds the
  * same library as libtkg_check.so with every kernel verifying its internal
  * invariants (tensor-memory column ranges of each MMA, scale copy and
