@@ -2,9 +2,10 @@
 // and its gradient, without the logits ever being kept.
 //
 //   z = alpha X W^T,  lse_t = log sum_v exp z_tv,  loss_t = lse_t - z_t,y(t)
-//   g_tv = alpha dloss_t (exp(z_tv - lse_t) - [v = y(t)]),  dX = g W,  dW = g^T X
+//   g_tv = exp(z_tv - lse_t) - [v = y(t)],  c_t = alpha dloss_t (0 for ignored t)
+//   dX = diag(c) g W,  dW = g^T diag(c) X
 //
-// Loss: one pass over W.  Each 128 logits of a row leave their maximum and sum
+// Loss: one pass over W.  Each 128 logits of a token leave their maximum and sum
 // (8 bytes), which a second kernel joins: (M, S) of parts (m_i, s_i) is M = max m_i,
 // S = sum s_i 2^(m_i - M), in base 2, all in FP32.
 //
@@ -12,8 +13,14 @@
 // (2 T V H flops, against reading T V logits back), g goes to a BF16 workspace of
 // one piece, and two products take it from there: dW's rows of the piece are
 // final, dX grows by one FP32 addition per piece.  dX's product splits its long
-// axis (the vocabulary) over CTAs when T x H has too few tiles; every part has
+// axis (the vocabulary) over clusters when T x H has too few tiles; every part has
 // its own FP32 buffer and the buffers are added in order.
+//
+// The tokens' weights c stay out of g: with a mean over T tokens every label's
+// term would be -c (1 - p), all rounded the same way (up to 2^-8 of the whole
+// gradient when p is small).  dX's rows are multiplied by c in FP32; for dW the
+// rows of X are multiplied by c / max |c| and rounded (exactly X's own rows when
+// the weights are equal, as for a mean), and the sums by max |c| in FP32.
 #include <cmath>
 
 #include "linear_ce.cuh"
@@ -63,46 +70,97 @@ __global__ void __launch_bounds__(1024)
   }
 }
 
-// ---------------------------------------------------------------- rows of X, ignored ones cleared
-// dW = g^T X sums over rows whose g is 0 too; a row that is not a number (a padded
-// position of an attention with nothing to attend to) would make 0 * NaN of it.
-__global__ void __launch_bounds__(256)
+// ---------------------------------------------------------------- rows of X with the tokens' weights
+// out_t = X_t c_t / s, s = max |c_t|, and s itself.  Rows of ignored tokens are
+// zeros whatever they hold: their g is 0, but 0 times a padded position's NaN is not.
+// Every block finds s again from the T weights (at most one block per SM: T x 12
+// bytes from L2 each, against one more launch).
+__global__ void __launch_bounds__(1024)
     ce_rows_kernel(int tokens, int vocab, int hidden, const uint16_t* __restrict__ X, size_t ldx,
-                   const long long* __restrict__ labels, uint16_t* __restrict__ out) {
+                   const long long* __restrict__ labels, const float* __restrict__ dloss, float alpha,
+                   uint16_t* __restrict__ out, float* __restrict__ scale) {
+  __shared__ float s_max[32];
   ptx::pdl_launch_dependents();
   ptx::pdl_wait();
-  const int vec = hidden / 8;   // 16-byte pieces of a row
-  const size_t total = size_t(tokens) * size_t(vec);
-  for (size_t i = size_t(blockIdx.x) * blockDim.x + threadIdx.x; i < total; i += size_t(gridDim.x) * blockDim.x) {
-    const size_t t = i / size_t(vec), c = i - t * size_t(vec);
+  auto weight = [&](int t) {
     const long long y = __ldcg(labels + t);
-    uint4 v = make_uint4(0, 0, 0, 0);
-    if (y >= 0 && y < vocab) v = __ldcg(reinterpret_cast<const uint4*>(X + t * ldx) + c);
-    reinterpret_cast<uint4*>(out)[i] = v;
+    return (y >= 0 && y < vocab) ? alpha * __ldcg(dloss + t) : 0.f;
+  };
+  const int tid = threadIdx.x;
+  float top = 0.f;
+  for (int t = tid; t < tokens; t += 1024) top = fmaxf(top, fabsf(weight(t)));
+#pragma unroll
+  for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+  if ((tid & 31) == 0) s_max[tid >> 5] = top;
+  __syncthreads();
+  top = s_max[tid & 31];
+#pragma unroll
+  for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+  if (blockIdx.x == 0 && tid == 0) *scale = top;
+  // a warp per row
+  const int vec = hidden / 8;
+  for (int t = blockIdx.x * 32 + (tid >> 5); t < tokens; t += gridDim.x * 32) {
+    const long long y = __ldcg(labels + t);
+    const bool kept = y >= 0 && y < vocab;
+    const float w = top == 0.f ? 0.f : __fdiv_rn(weight(t), top);
+    const uint4* src = reinterpret_cast<const uint4*>(X + size_t(t) * ldx);
+    uint4* dst = reinterpret_cast<uint4*>(out + size_t(t) * size_t(hidden));
+#pragma unroll 4
+    for (int c = tid & 31; c < vec; c += 32) {
+      uint4 v = make_uint4(0, 0, 0, 0);
+      if (kept) {
+        v = __ldcg(src + c);
+        if (w != 1.f) {
+          uint32_t* u = reinterpret_cast<uint32_t*>(&v);
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            u[i] = ptx::pack_bf16x2(__uint_as_float(u[i] << 16) * w, __uint_as_float(u[i] & 0xffff0000u) * w);
+        }
+      }
+      dst[c] = v;
+    }
   }
 }
 
 // ---------------------------------------------------------------- dX from its FP32 parts
+// Parts are [hidden][token] (pitch in elements); dX is [token][hidden].  A block
+// adds the parts of 32 tokens x 64 hidden, in order, turns them in shared memory
+// and multiplies by the tokens' weights.
 __global__ void __launch_bounds__(256)
-    ce_dx_kernel(int tokens, int hidden, int parts, const float* __restrict__ part, uint16_t* __restrict__ dX,
-                 size_t lddx) {
+    ce_dx_kernel(int tokens, int vocab, int hidden, int parts, const float* __restrict__ part, size_t pitch,
+                 const long long* __restrict__ labels, const float* __restrict__ dloss, float alpha,
+                 uint16_t* __restrict__ dX, size_t lddx) {
+  __shared__ float s_t[64][33];
   ptx::pdl_launch_dependents();
   ptx::pdl_wait();
-  const int vec = hidden / 8;
-  const size_t total = size_t(tokens) * size_t(vec);
-  for (size_t i = size_t(blockIdx.x) * blockDim.x + threadIdx.x; i < total; i += size_t(gridDim.x) * blockDim.x) {
-    const size_t t = i / size_t(vec), c = i - t * size_t(vec);
-    float s[8] = {};
-#pragma unroll 4
+  const int t0 = blockIdx.x * 32, h0 = blockIdx.y * 64;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const size_t part_len = size_t(hidden) * pitch;
+  float s[8] = {};
+  if (t0 + lane < tokens) {
     for (int p = 0; p < parts; ++p) {
-      const float4* src = reinterpret_cast<const float4*>(part + (size_t(p) * size_t(tokens) * size_t(hidden))) + 2 * i;
-      const float4 a = __ldcg(src), b = __ldcg(src + 1);
-      s[0] += a.x; s[1] += a.y; s[2] += a.z; s[3] += a.w;
-      s[4] += b.x; s[5] += b.y; s[6] += b.z; s[7] += b.w;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int hh = h0 + warp * 8 + i;
+        if (hh < hidden) s[i] += __ldcg(part + size_t(p) * part_len + size_t(hh) * pitch + t0 + lane);
+      }
     }
-    *(reinterpret_cast<uint4*>(dX + t * lddx) + c) =
-        make_uint4(ptx::pack_bf16x2(s[0], s[1]), ptx::pack_bf16x2(s[2], s[3]), ptx::pack_bf16x2(s[4], s[5]),
-                   ptx::pack_bf16x2(s[6], s[7]));
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i) s_t[warp * 8 + i][lane] = s[i];
+  __syncthreads();
+  // 8 lanes per token, 8 hidden (16 bytes) each
+  const int t = t0 + (threadIdx.x >> 3), hh = (threadIdx.x & 7) * 8;
+  if (t < tokens && h0 + hh < hidden) {
+    const long long y = __ldcg(labels + t);
+    const float w = alpha * __ldcg(dloss + t);
+    uint32_t o[4] = {0, 0, 0, 0};
+    if (y >= 0 && y < vocab) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        o[i] = ptx::pack_bf16x2(s_t[hh + 2 * i][threadIdx.x >> 3] * w, s_t[hh + 2 * i + 1][threadIdx.x >> 3] * w);
+    }
+    *reinterpret_cast<uint4*>(dX + size_t(t) * lddx + h0 + hh) = make_uint4(o[0], o[1], o[2], o[3]);
   }
 }
 
@@ -111,18 +169,17 @@ inline size_t round_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 // ---------------------------------------------------------------- plans and workspaces
 // The plans go by the GB300's 152 SMs, so that a workspace's size depends on the
 // problem alone; on fewer SMs they are only less well balanced.
-constexpr int kSms = 152;
+constexpr int kPairs = 76;
 
 struct GradPlan {
   int piece;          // vocabulary entries per piece
   int pieces;
   int parts;          // k parts of dX's product
-  bool dx_f32;        // dX through FP32 parts
-  size_t g_row;       // bytes of one row of g
-  size_t rows_off, g_off, part_off, bytes;
+  size_t tokens_up;   // row pitch of g and of dX's parts, in elements
+  size_t g_off, part_off, scale_off, bytes;   // the weighted rows of X come first
 };
 
-// Vocabulary entries per piece: g (T x piece BF16) of up to 512 MB, a multiple of 256, at least 4096.
+// Vocabulary entries per piece: g (piece x T BF16) of up to 512 MB, a multiple of 256, at least 4096.
 int default_piece(int tokens, int vocab) {
   long long piece = (512ll << 20) / (2ll * tokens) / 256 * 256;
   if (piece < 4096) piece = 4096;
@@ -132,16 +189,14 @@ int default_piece(int tokens, int vocab) {
 // Parts of dX's long axis: the number whose rounds of tiles take least, a part
 // at least 8 stages (512 vocabulary entries) long.
 int dx_parts(int tokens, int hidden, int k) {
-  const int cg = tokens <= 128 ? 1 : 2;
-  const int slots = kSms / cg;
-  const int tiles = ceil_div(tokens, 128 * cg) * ceil_div(hidden, 256);
+  const int tiles = ceil_div(hidden, 256) * ceil_div(tokens, kTrainBN);
   const int stages = ceil_div(k, 64);
   int best = 1;
   double best_time = 1e300;
   for (int s = 1; s <= 32 && (s == 1 || stages / s >= 8); ++s) {
     const int per = ceil_div(stages, s);
     if (ceil_div(stages, per) != s) continue;
-    const double time = double(ceil_div(tiles * s, slots)) * (per + 12);   // about 12 stages' time to start and drain
+    const double time = double(ceil_div(tiles * s, kPairs)) * (per + 12);   // about 12 stages' time to start and drain
     if (time < 0.95 * best_time) {
       best = s;
       best_time = time;
@@ -155,12 +210,11 @@ GradPlan grad_plan(int tokens, int vocab, int hidden, int piece) {
   pl.piece = piece > 0 ? (piece < vocab ? piece : vocab) : default_piece(tokens, vocab);
   pl.pieces = ceil_div(vocab, pl.piece);
   pl.parts = dx_parts(tokens, hidden, pl.piece);
-  pl.dx_f32 = pl.pieces > 1 || pl.parts > 1;
-  pl.g_row = round_up(size_t(pl.piece) * 2, 128);
-  pl.rows_off = 0;
+  pl.tokens_up = round_up(size_t(tokens), 64);
   pl.g_off = round_up(size_t(tokens) * size_t(hidden) * 2, 256);
-  pl.part_off = pl.g_off + round_up(size_t(tokens) * pl.g_row, 256);
-  pl.bytes = pl.part_off + (pl.dx_f32 ? size_t(pl.parts) * size_t(tokens) * size_t(hidden) * 4 : 0);
+  pl.part_off = pl.g_off + round_up(size_t(pl.piece) * pl.tokens_up * 2, 256);
+  pl.scale_off = pl.part_off + size_t(pl.parts) * size_t(hidden) * pl.tokens_up * 4;
+  pl.bytes = pl.scale_off + 16;
   return pl;
 }
 
@@ -180,14 +234,6 @@ tkg_status check_head(int tokens, int vocab, int hidden, const void* X, int ldx,
   return TKG_OK;
 }
 
-tkg_status run_rows(int tokens, int vocab, int hidden, const void* X, int ldx, const long long* labels, void* out,
-                    cudaStream_t stream) {
-  const size_t pieces = size_t(tokens) * size_t(hidden / 8);
-  const unsigned blocks = unsigned(pieces / 256 + 1 < size_t(kSms) * 8 ? pieces / 256 + 1 : size_t(kSms) * 8);
-  return launch_small(ce_rows_kernel, dim3(blocks), dim3(256), stream, tokens, vocab, hidden,
-                      static_cast<const uint16_t*>(X), size_t(ldx), labels, static_cast<uint16_t*>(out));
-}
-
 }  // namespace
 }  // namespace tkg
 
@@ -197,7 +243,7 @@ extern "C" {
 
 size_t tkg_linear_ce_loss_workspace_bytes(int tokens, int vocab) {
   if (tokens < 0 || vocab < 0) return 0;
-  return round_up(size_t(ceil_div(vocab, 256)) * 2 * size_t(tokens) * sizeof(float2), 256) + size_t(tokens) * 4;
+  return round_up(size_t(ceil_div(vocab, 128)) * size_t(tokens) * sizeof(float2), 256) + size_t(tokens) * 4;
 }
 
 tkg_status tkg_linear_ce_loss(int tokens, int vocab, int hidden, const void* X, int ldx, const void* W, int ldw,
@@ -209,10 +255,10 @@ tkg_status tkg_linear_ce_loss(int tokens, int vocab, int hidden, const void* X, 
   if (!loss || !lse || !workspace || workspace_bytes < tkg_linear_ce_loss_workspace_bytes(tokens, vocab))
     return TKG_ERR_INVALID_ARG;
   if (!aligned_to(loss, 4) || !aligned_to(lse, 4) || !aligned_to(workspace, 16)) return TKG_ERR_ALIGNMENT;
-  const int parts = ceil_div(vocab, 256) * 2;
+  const int parts = ceil_div(vocab, 128);
   TrainParams p{};
-  p.m = tokens;
-  p.n = vocab;
+  p.m = vocab;
+  p.n = tokens;
   p.k = hidden;
   p.alpha = alpha;
   p.c2 = alpha * kLog2e;
@@ -262,19 +308,22 @@ tkg_status tkg_linear_ce_grad(int tokens, int vocab, int hidden, const void* X, 
   if (!lse || !dloss || !workspace || workspace_bytes < pl.bytes) return TKG_ERR_INVALID_ARG;
   if (!aligned_to(lse, 4) || !aligned_to(dloss, 4) || !aligned_to(workspace, 16)) return TKG_ERR_ALIGNMENT;
   char* ws = static_cast<char*>(workspace);
-  void* rows = ws + pl.rows_off;
+  uint16_t* rows = reinterpret_cast<uint16_t*>(ws);
   void* G = ws + pl.g_off;
   float* part = reinterpret_cast<float*>(ws + pl.part_off);
-  const bool single = ce_single_cta(tokens);
+  float* scale = reinterpret_cast<float*>(ws + pl.scale_off);
   CUtensorMap tmA, tmB, tmD;
 
-  if (dW && (st = run_rows(tokens, vocab, hidden, X, ldx, labels, rows, stream)) != TKG_OK) return st;
+  if (dW && (st = launch_small(ce_rows_kernel, dim3(unsigned(ceil_div(tokens, 32) < 2 * kPairs ? ceil_div(tokens, 32) : 2 * kPairs)),
+                               dim3(1024), stream, tokens, vocab, hidden, static_cast<const uint16_t*>(X), size_t(ldx),
+                               labels, dloss, alpha, rows, scale)) != TKG_OK)
+    return st;
   for (int i = 0; i < pl.pieces; ++i) {
     const int v0 = i * pl.piece, nv = vocab - v0 < pl.piece ? vocab - v0 : pl.piece;
     const char* Wp = static_cast<const char*>(W) + size_t(v0) * size_t(ldw) * 2;
     TrainParams p{};
-    p.m = tokens;
-    p.n = nv;
+    p.m = nv;
+    p.n = tokens;
     p.k = hidden;
     p.alpha = alpha;
     p.c2 = alpha * kLog2e;
@@ -282,60 +331,53 @@ tkg_status tkg_linear_ce_grad(int tokens, int vocab, int hidden, const void* X, 
     p.vocab = vocab;
     p.labels = labels;
     p.lse = lse;
-    p.dloss = dloss;
-    if ((st = launch_ce_dlogits(X, size_t(ldx) * 2, Wp, size_t(ldw) * 2, G, pl.g_row, p, stream)) != TKG_OK) return st;
+    p.d = G;
+    p.ldd = pl.tokens_up;
+    if ((st = launch_ce_dlogits(X, size_t(ldx) * 2, Wp, size_t(ldw) * 2, p, stream)) != TKG_OK) return st;
     if (dX) {
-      // (parts of) g W of this piece
+      // (parts of) W^T g of this piece: hidden x tokens
       TrainParams q{};
-      q.m = tokens;
-      q.n = hidden;
+      q.m = hidden;
+      q.n = tokens;
       q.k = nv;
+      q.n_tile = train_n_tile(tokens, 16);
       q.alpha = 1.f;
       q.split_stages = ceil_div(ceil_div(nv, 64), pl.parts);
       q.splits = ceil_div(ceil_div(nv, 64), q.split_stages);
       q.accumulate = i > 0;
-      if ((st = map_k_major(&tmA, G, tokens, nv, pl.g_row, 128)) != TKG_OK) return st;
-      if ((st = map_mn_major(&tmB, Wp, hidden, nv, size_t(ldw) * 2)) != TKG_OK) return st;
-      if (pl.dx_f32)
-        st = map_out(&tmD, part, tokens, hidden, pl.parts, size_t(hidden) * 4, size_t(tokens) * size_t(hidden) * 4, true);
-      else
-        st = map_out(&tmD, dX, tokens, hidden, 1, size_t(lddx) * 2, size_t(tokens) * size_t(lddx) * 2, false);
-      if (st != TKG_OK) return st;
-      if (pl.dx_f32)
-        st = single ? launch_train<false, true, EPI_F32, 1, GRP_NONE>(tmA, tmB, tmD, q, stream)
-                    : launch_train<false, true, EPI_F32, 2, GRP_NONE>(tmA, tmB, tmD, q, stream);
-      else
-        st = single ? launch_train<false, true, EPI_BF16, 1, GRP_NONE>(tmA, tmB, tmD, q, stream)
-                    : launch_train<false, true, EPI_BF16, 2, GRP_NONE>(tmA, tmB, tmD, q, stream);
-      if (st != TKG_OK) return st;
+      if ((st = map_mn_major(&tmA, Wp, hidden, nv, size_t(ldw) * 2)) != TKG_OK) return st;
+      if ((st = map_mn_major(&tmB, G, tokens, nv, pl.tokens_up * 2)) != TKG_OK) return st;
+      if ((st = map_out(&tmD, part, hidden, tokens, pl.parts, pl.tokens_up * 4, size_t(hidden) * pl.tokens_up * 4,
+                        true)) != TKG_OK)
+        return st;
+      if ((st = launch_train<true, true, EPI_F32, GRP_NONE>(tmA, tmB, tmD, q, stream)) != TKG_OK) return st;
     }
     if (dW) {
-      // rows [v0, v0 + nv) of dW = g^T X
+      // rows [v0, v0 + nv) of dW = g (c / s X)
       TrainParams q{};
       q.m = nv;
       q.n = hidden;
       q.k = tokens;
+      q.n_tile = train_n_tile(hidden, 32);
       q.alpha = 1.f;
+      q.scale = scale;
       q.splits = 1;
       q.split_stages = ceil_div(tokens, 64);
       q.accumulate = dw_type == TKG_GRAD_F32_ADD;
-      if ((st = map_mn_major(&tmA, G, nv, tokens, pl.g_row)) != TKG_OK) return st;
+      if ((st = map_k_major(&tmA, G, nv, tokens, pl.tokens_up * 2, 128)) != TKG_OK) return st;
       if ((st = map_mn_major(&tmB, rows, hidden, tokens, size_t(hidden) * 2)) != TKG_OK) return st;
       if ((st = map_out(&tmD, static_cast<char*>(dW) + size_t(v0) * size_t(lddw) * es, nv, hidden, 1, size_t(lddw) * es,
                         size_t(nv) * size_t(lddw) * es, es == 4)) != TKG_OK)
         return st;
-      st = es == 2 ? launch_train<true, true, EPI_BF16, 2, GRP_NONE>(tmA, tmB, tmD, q, stream)
-                   : launch_train<true, true, EPI_F32, 2, GRP_NONE>(tmA, tmB, tmD, q, stream);
+      st = es == 2 ? launch_train<false, true, EPI_BF16, GRP_NONE>(tmA, tmB, tmD, q, stream)
+                   : launch_train<false, true, EPI_F32, GRP_NONE>(tmA, tmB, tmD, q, stream);
       if (st != TKG_OK) return st;
     }
   }
-  if (dX && pl.dx_f32) {
-    const size_t pieces = size_t(tokens) * size_t(hidden / 8);
-    const unsigned blocks = unsigned(pieces / 256 + 1 < size_t(kSms) * 8 ? pieces / 256 + 1 : size_t(kSms) * 8);
-    return launch_small(ce_dx_kernel, dim3(blocks), dim3(256), stream, tokens, hidden, pl.parts, part,
-                        static_cast<uint16_t*>(dX), size_t(lddx));
-  }
-  return TKG_OK;
+  if (!dX) return TKG_OK;
+  return launch_small(ce_dx_kernel, dim3(unsigned(ceil_div(tokens, 32)), unsigned(ceil_div(hidden, 64))), dim3(256),
+                      stream, tokens, vocab, hidden, pl.parts, part, pl.tokens_up, labels, dloss, alpha,
+                      static_cast<uint16_t*>(dX), size_t(lddx));
 }
 
 }  // extern "C"

@@ -17,41 +17,32 @@ inline bool aligned_to(const void* p, size_t a) { return (reinterpret_cast<uintp
 // zeros; a box that runs mostly past the end slows the load stream)
 inline uint32_t mn_box_rows(int k) { return k >= 64 ? 64u : uint32_t((k + 15) / 16 * 16); }
 
-// K-major operand: `rows` rows of k BF16; boxes of 64 k by up to `tile_rows` rows.
-inline tkg_status map_k_major(CUtensorMap* map, const void* base, int rows, int k, size_t row_bytes, int tile_rows) {
+// K-major operand: `rows` rows of k BF16; boxes of 64 k by up to `box` rows.
+inline tkg_status map_k_major(CUtensorMap* map, const void* base, int rows, int k, size_t row_bytes, int box) {
   return encode_2d(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, base, uint64_t(k), uint64_t(rows), row_bytes, 64,
-                   uint32_t(rows < tile_rows ? rows : tile_rows), CU_TENSOR_MAP_SWIZZLE_128B);
+                   uint32_t(rows < box ? rows : box), CU_TENSOR_MAP_SWIZZLE_128B);
 }
 // MN-major operand: k rows of `mn` BF16; boxes of 64 mn by up to 64 k.
-inline tkg_status map_mn_major(CUtensorMap* map, const void* base, int mn, int k, size_t row_bytes) {
+inline tkg_status map_mn_major(CUtensorMap* map, const void* base, int mn, int k, size_t row_bytes, int box_rows = 0) {
   return encode_2d(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, base, uint64_t(mn), uint64_t(k), row_bytes, 64,
-                   mn_box_rows(k), CU_TENSOR_MAP_SWIZZLE_128B);
+                   box_rows ? uint32_t(box_rows) : mn_box_rows(k), CU_TENSOR_MAP_SWIZZLE_128B);
 }
-// Output: `parts` matrices of m x n, 32-row x 64-byte store boxes.
+// Output: `parts` matrices of m x n, store boxes of 64 bytes by `rows` rows.
 inline tkg_status map_out(CUtensorMap* map, const void* base, int m, int n, int parts, size_t row_bytes,
-                          size_t part_bytes, bool f32) {
+                          size_t part_bytes, bool f32, int rows = 32) {
   return encode_3d_swizzled(map, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, base,
-                            uint64_t(n), uint64_t(m), uint64_t(parts), row_bytes, part_bytes, f32 ? 16 : 32, 32, 1,
-                            CU_TENSOR_MAP_SWIZZLE_64B);
+                            uint64_t(n), uint64_t(m), uint64_t(parts), row_bytes, part_bytes, f32 ? 16 : 32,
+                            uint32_t(rows), 1, CU_TENSOR_MAP_SWIZZLE_64B);
 }
 
-// Bytes one stage brings to the full barrier, over the CTAs of the cluster.
-template <bool A_MN, bool B_MN, int EPI, int CG, int GRP>
-uint32_t train_tx_bytes(int m, int n, int k) {
-  using C = TrainConfig<A_MN, B_MN, EPI, CG, GRP>;
-  const int kb = int(GRP == GRP_K ? 64 : mn_box_rows(k));
-  const int a = A_MN ? 2 * kb * 128 : (m < 128 ? m : 128) * 128;
-  const int b = B_MN ? (C::kBRows / 64) * kb * 128 : (n < C::kBRows ? n : C::kBRows) * 128;
-  return uint32_t(CG * (a + b));
-}
-
-// Fills the fields common to every launch and launches.  p.m, n, k, splits (at
-// least 1), split_stages, alpha and the epilogue's own fields are set by the caller.
-template <bool A_MN, bool B_MN, int EPI, int CG, int GRP>
+// Fills the fields common to every launch and launches.  The caller sets p.m, n,
+// k, n_tile, alpha, splits and split_stages (GRP_NONE) and the epilogue's own fields.
+template <bool A_MN, bool B_MN, int EPI, int GRP>
 tkg_status launch_train(const CUtensorMap& tmA, const CUtensorMap& tmB, const CUtensorMap& tmD, TrainParams p,
-                        cudaStream_t stream) {
-  using C = TrainConfig<A_MN, B_MN, EPI, CG, GRP>;
-  auto kern = train_kernel<A_MN, B_MN, EPI, CG, GRP>;
+                        cudaStream_t stream,
+                        const std::conditional_t<GRP == GRP_K, TailMaps, NoTail>& tail = {}) {
+  using C = TrainConfig<A_MN, B_MN, EPI, GRP>;
+  auto kern = train_kernel<A_MN, B_MN, EPI, GRP>;
   // more than half an SM's shared memory: no two CTAs share an SM (each takes all of tensor memory)
   static_assert(C::kSmemBytes > 118784, "one CTA per SM");
   int dev = 0;
@@ -70,43 +61,49 @@ tkg_status launch_train(const CUtensorMap& tmA, const CUtensorMap& tmB, const CU
   p.timeout_ns = 1000000ull * (unsigned long long)(tmo > 0 ? tmo : 1000);
   p.inject_stall = option(TKG_OPT_INJECT_STALL);
   p.kstages = ceil_div(p.k, 64);
-  p.tiles_m = ceil_div(p.m, C::kMmaM);
-  p.tiles_n = ceil_div(p.n, C::kBN);
-  p.tx_bytes = train_tx_bytes<A_MN, B_MN, EPI, CG, GRP>(p.m, p.n, p.k);
-  p.raster_group = raster_group(C::kMmaM, GRP == GRP_K ? ceil_div(p.k, p.groups) : p.k, FMT_BF16, p.tiles_m);
+  p.tiles_m = ceil_div(p.m, 256);
+  p.tiles_n = ceil_div(p.n, p.n_tile);
+  // what a stage of one CTA takes and brings: A's 128 rows (fewer when there are fewer) or two chunks, and
+  // its half of B's n_tile
+  const int kb = GRP == GRP_K ? 64 : int(mn_box_rows(p.k));   // k rows of an MN-major box
+  const int half = p.n_tile / 2;
+  const int a_bytes = A_MN ? 2 * kb * 128 : (p.m < 128 ? p.m : 128) * 128;
+  const int b_rows = GRP == GRP_ROWS ? (half + 31) / 32 * 32 : half;
+  const int b_slot = B_MN ? ceil_div(half, 64) * kTrainChunk : b_rows * 128;
+  const int b_bytes = B_MN ? ceil_div(half, 64) * kb * 128 : (p.n < half ? p.n : half) * 128;
+  p.tx_bytes = uint32_t(2 * (a_bytes + (GRP == GRP_ROWS ? 0 : b_bytes)));
+  p.stage_bytes = uint32_t(C::kABytes + b_slot);
+  p.stages = C::kRingBytes / int(p.stage_bytes);
+  if (p.stages > kTrainMaxStages) p.stages = kTrainMaxStages;
+  p.raster_group = raster_group(256, GRP == GRP_K ? ceil_div(p.k, p.groups) : p.k, FMT_BF16, p.tiles_m);
   long long tiles = (long long)p.tiles_m * p.tiles_n;
   if (GRP == GRP_NONE) tiles *= p.splits;
   if (GRP == GRP_K) tiles *= p.groups;
-  if (GRP == GRP_ROWS) tiles = (long long)(p.tiles_m + p.groups) * p.tiles_n;   // at most
-  if (tiles * CG > 0x7fffffffLL) return TKG_ERR_UNSUPPORTED;
+  if (GRP == GRP_ROWS) tiles = (long long)p.tiles_m * (ceil_div(p.n, kTrainBN) + p.groups);   // at most
+  if (tiles * 2 > 0x7fffffffLL) return TKG_ERR_UNSUPPORTED;
   p.num_tiles = int(tiles);
 
   long long clusters = tiles;   // cluster launch control: one cluster per tile
   if (!C::kClc) {
     int resident = 0;
-    if ((st = CG == 2 ? device_max_clusters(2, &resident) : device_sm_count(&resident)) != TKG_OK) return st;
+    if ((st = device_max_clusters(2, &resident)) != TKG_OK) return st;
     if (clusters > resident) clusters = resident;
   }
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[2];
-  cfg.gridDim = dim3(unsigned(clusters * CG), 1, 1);
+  cfg.gridDim = dim3(unsigned(clusters * 2), 1, 1);
   cfg.blockDim = dim3(C::kThreads, 1, 1);
   cfg.dynamicSmemBytes = C::kSmemBytes;
   cfg.stream = stream;
-  int nattr = 0;
-  if (CG == 2) {
-    attr[nattr].id = cudaLaunchAttributeClusterDimension;
-    attr[nattr].val.clusterDim.x = CG;
-    attr[nattr].val.clusterDim.y = 1;
-    attr[nattr].val.clusterDim.z = 1;
-    ++nattr;
-  }
-  attr[nattr].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[nattr].val.programmaticStreamSerializationAllowed = 1;
-  ++nattr;
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = nattr;
-  if (cudaLaunchKernelEx(&cfg, kern, tmA, tmB, tmD, p) != cudaSuccess) {
+  cfg.numAttrs = 2;
+  if (cudaLaunchKernelEx(&cfg, kern, tmA, tmB, tmD, p, tail) != cudaSuccess) {
     cudaGetLastError();
     return TKG_ERR_CUDA;
   }

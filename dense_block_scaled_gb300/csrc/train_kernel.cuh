@@ -4,29 +4,48 @@
 //
 //   D[m][n] = sum_k a(m,k) * b(n,k),  BF16 operands, FP32 accumulation in tensor memory
 //
+// M is the side of the weights (vocabulary, hidden, an expert's columns): long,
+// and the same for every call.  N is, in all but the weight gradients, the side
+// of the tokens: short, ragged, different per group.  An MMA takes any N that is
+// a multiple of 16, so a batch of T tokens is cut into ceil(T / 256) tiles of
+// equal width, T / tiles rounded up to 16, and next to nothing is computed for
+// tokens that do not exist; with the tokens on M (tiles of 256) 777 tokens cost
+// 1024 and 64 experts of 16 to 900 rows 1.4 times their rows (measured at 777 x
+// 50001 x 2048 and 64 experts x 2048 x 2048; see the table of results).
+//
 // Each operand is either K-major (row m holds consecutive k: rows of X, W, dD)
 // or MN-major (row k holds consecutive m or n: the same matrices read for
 // their gradients).  A stage holds 64 k of a tile.  K-major tiles are rows of
 // 128 bytes (64 k), 128-byte swizzle; MN-major tiles are chunks of 64 m (or n)
-// by 64 k, each k a 128-byte row under the same swizzle, so that both kinds
-// take the same shared memory and TMA writes both directly: nothing is ever
-// transposed in memory.  The MMA descriptors carry the difference.
+// by 64 k, each k a 128-byte row under the same swizzle.  TMA writes both
+// directly and the MMA descriptors carry the difference: nothing is ever
+// transposed in memory.
 //
-// Roles (one CTA per SM; CG CTAs per cluster share one MMA when CG == 2), the
-// bounded waits and the abort protocol are those of gemm_kernel.cuh:
+// Roles (one CTA per SM; the two CTAs of a cluster share one MMA of 256 x N),
+// the bounded waits and the abort protocol are those of gemm_kernel.cuh:
 //   warp 0 TMA producer, warp 1 MMA issuer, warp 2 tensor-memory allocation and
 //   the cluster-launch-control tile scheduler, warps 4-11 epilogue.
 // Two 256-column accumulators: a tile's epilogue overlaps the next tile's MMAs.
+// The ring takes as many stages as fit: 6 for 256-wide tiles, up to 12 where few
+// tokens leave most of a stage to the weights (bytes in flight are what a
+// bandwidth-bound call needs).
 //
 // Epilogues (EPI):
-//   LOSS     a thread owns 128 consecutive logits of one row: their maximum and
-//            sum of exponentials in base 2 (one FFMA and one ex2 per logit) and,
-//            where the row's label falls among them, its logit.  8 bytes per 128
-//            logits go to memory, never the logits.
-//   DLOGITS  g = (exp(z - lse) - [v = label]) * alpha * dloss, rounded to BF16 (the
-//            tensor cores' operand type; each g carries a relative error of at
-//            most 2^-9, independent between elements), by TMA into a piece.
+//   LOSS     per token (column) and 128 vocabulary rows: the largest logit and the
+//            sum of exponentials in base 2, and, where the token's label falls among
+//            them, its logit.  A thread holds 8 columns by 4 rows of each 32 x 32
+//            block (the 16x256b load); columns are joined over 8 lanes by exchanging
+//            halves (7 shuffles down for the maximum, 7 back, 7 for the sum, against
+//            a 5-step butterfly per column), then over the four warps in shared
+//            memory.  8 bytes per 128 logits go to memory, never the logits.
+//   DLOGITS  g = exp(z - lse) - [v = label], rounded to BF16 (the tensor cores'
+//            operand type; u = 2^-8, independent between elements) into a piece
+//            [vocabulary][token].  The tokens' weights are left out, so that the
+//            rounding does not hit them all the same way: they multiply dX's rows in
+//            FP32 and, relative to the largest, X's rows for dW.
 //   BF16     alpha * D rounded to nearest even.
+//   BF16_T   the same, transposed: D's columns are rows of the output.  Neighbouring
+//            lanes swap halves (one shuffle per two values) and store 32-bit words.
 //   F32      alpha * D stored, or added by the TMA unit to what is there (one add
 //            per element and launch, so the order of additions is fixed).
 #pragma once
@@ -34,19 +53,23 @@
 
 namespace tkg {
 
-enum : int { EPI_LOSS = 0, EPI_DLOGITS = 1, EPI_BF16 = 2, EPI_F32 = 3 };
-// GRP_ROWS: groups of consecutive output rows, each with its own B; GRP_K: groups
-// of consecutive k, each with its own output matrix.  Row counts in device memory.
+enum : int { EPI_LOSS = 0, EPI_DLOGITS = 1, EPI_BF16 = 2, EPI_F32 = 3, EPI_BF16_T = 4 };
+// GRP_ROWS: groups of consecutive n, each with its own A; GRP_K: groups of
+// consecutive k, each with its own output matrix.  Row counts in device memory.
 enum : int { GRP_NONE = 0, GRP_ROWS = 1, GRP_K = 2 };
 
 struct TrainParams {
-  int m, n, k;                 // output rows and columns, contraction length (GRP_K: row capacity)
+  int m, n, k;                 // output rows and columns, contraction length (GRP_ROWS: n, GRP_K: k is the row capacity)
   int kstages;                 // ceil(k / 64)
   int splits, split_stages;    // k split: part z covers stages [z * split_stages, ...)
   int tiles_m, tiles_n, num_tiles;
+  int n_tile;                  // tile width, a multiple of 16 (GRP_ROWS: per group, by its rows)
   int raster_group;
-  uint32_t tx_bytes;           // bytes landing on the (leader's) full barrier per stage
+  int stages;                  // ring slots, and the bytes of one in each CTA
+  uint32_t stage_bytes;
+  uint32_t tx_bytes;           // bytes landing on the leader's full barrier per stage (GRP_ROWS: of A)
   float alpha;
+  const float* scale;          // device, may be null: multiplies alpha
   unsigned int* status;
   unsigned long long timeout_ns;
   int inject_stall;
@@ -55,16 +78,23 @@ struct TrainParams {
   int vocab0, vocab;           // first vocabulary entry of this piece, and all there are
   const long long* labels;
   const float* lse;
-  const float* dloss;
-  float2* part;                // LOSS: (maximum, sum) per 128 columns and row
-  float* zlabel;               // LOSS: the label's logit per row
-  // F32
-  int accumulate;
+  float2* part;                // LOSS: (maximum, sum) per 128 vocabulary rows and token
+  float* zlabel;               // LOSS: the label's logit per token
+  // outputs written from registers: their first element and row pitch in elements
+  void* d;
+  size_t ldd;
+  int accumulate;              // F32
   // groups
   const int* sizes;            // device
   int groups;
-  void* d;                     // GRP_ROWS: D for the row-masked stores at group ends
-  const uint8_t* maps;         // GRP_K: tensor maps of A and B per group (256 bytes each)
+};
+
+// GRP_K: A and B in boxes of 16, 4 and 1 k rows, for the stage in which a group ends.
+struct TailMaps {
+  CUtensorMap a[3], b[3];
+};
+struct NoTail {
+  int unused;
 };
 
 namespace ptx {
@@ -79,9 +109,33 @@ __device__ __forceinline__ void tma_add_3d(const void* tmap, uint32_t src, int32
                "r"(x), "r"(y), "r"(z), "r"(src)
                : "memory");
 }
-// Before a tensor map written by an earlier kernel is used.
-__device__ __forceinline__ void tmap_acquire(const void* tmap) {
-  asm volatile("fence.proxy.tensormap::generic.acquire.gpu [%0], 128;" ::"l"(tmap) : "memory");
+// 16 lanes x 32 columns into r[H .. H + 16): thread t gets, for i = 0..3, lane t / 4 columns
+// 8 i + 2 (t % 4) + {0, 1} in r[H + 4 i], r[H + 4 i + 1] and lane t / 4 + 8 of the same columns in
+// r[H + 4 i + 2], r[H + 4 i + 3].
+template <int H>
+__device__ __forceinline__ void tmem_ld_16x256b_x4(uint32_t taddr, uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x4.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[H]), "=r"(r[H + 1]), "=r"(r[H + 2]), "=r"(r[H + 3]), "=r"(r[H + 4]), "=r"(r[H + 5]), "=r"(r[H + 6]),
+        "=r"(r[H + 7]), "=r"(r[H + 8]), "=r"(r[H + 9]), "=r"(r[H + 10]), "=r"(r[H + 11]), "=r"(r[H + 12]),
+        "=r"(r[H + 13]), "=r"(r[H + 14]), "=r"(r[H + 15])
+      : "r"(taddr));
+}
+// Waits for this thread's tensor-memory loads; naming the registers keeps what reads them behind the wait.
+__device__ __forceinline__ void tmem_ld_wait_for(uint32_t (&r)[32]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                 "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]),
+                 "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]),
+                 "+r"(r[23]), "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]),
+                 "+r"(r[30]), "+r"(r[31])::"memory");
+}
+// One column: thread i of the warp gets lane i of its quadrant.
+__device__ __forceinline__ uint32_t tmem_ld_32x32b_x1(uint32_t taddr) {
+  uint32_t r;
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];" : "=r"(r) : "r"(taddr));
+  return r;
 }
 __device__ __forceinline__ float ex2(float x) {
   float r;
@@ -97,90 +151,147 @@ __device__ __forceinline__ uint64_t sdesc_mn_sw128(uint32_t addr) {
          (1ull << 46) | (2ull << 61);
 }
 
-template <bool A_MN, bool B_MN, int EPI, int CG, int GRP>
+// Joins the values of a column over the 8 lanes (t / 4) that hold it: of 8 columns
+// each lane keeps half at every step and ends with one, column_of_lane.
+template <typename F>
+__device__ __forceinline__ float fold_columns(const float (&x)[8], int lane, F&& op) {
+  float a[4], b[2];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float r = __shfl_xor_sync(0xffffffffu, (lane & 16) ? x[i] : x[i + 4], 16);
+    a[i] = op((lane & 16) ? x[i + 4] : x[i], r);
+  }
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const float r = __shfl_xor_sync(0xffffffffu, (lane & 8) ? a[i] : a[i + 2], 8);
+    b[i] = op((lane & 8) ? a[i + 2] : a[i], r);
+  }
+  const float r = __shfl_xor_sync(0xffffffffu, (lane & 4) ? b[0] : b[1], 4);
+  return op((lane & 4) ? b[1] : b[0], r);
+}
+// The way back: every lane gets its 8 columns' values from the lanes that hold them.
+__device__ __forceinline__ void unfold_columns(float own, int lane, float (&x)[8]) {
+  float b[2], a[4];
+  const float o = __shfl_xor_sync(0xffffffffu, own, 4);
+  b[0] = (lane & 4) ? o : own;
+  b[1] = (lane & 4) ? own : o;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const float r = __shfl_xor_sync(0xffffffffu, b[i], 8);
+    a[i] = (lane & 8) ? r : b[i];
+    a[i + 2] = (lane & 8) ? b[i] : r;
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float r = __shfl_xor_sync(0xffffffffu, a[i], 16);
+    x[i] = (lane & 16) ? r : a[i];
+    x[i + 4] = (lane & 16) ? a[i] : r;
+  }
+}
+__device__ __forceinline__ int column_of_lane(int lane) {
+  return 16 * ((lane >> 4) & 1) + 8 * ((lane >> 3) & 1) + 2 * (lane & 3) + ((lane >> 2) & 1);
+}
+
+constexpr int kTrainBN = 256;         // widest tile
+constexpr int kTrainMaxStages = 12;
+
+template <bool A_MN, bool B_MN, int EPI, int GRP>
 struct TrainConfig {
   static constexpr int kThreads = 384;
   static constexpr int kEpiWarps = 8;
-  static constexpr int kBN = 256;
-  static constexpr int kMmaM = 128 * CG;
-  static constexpr int kBRows = kBN / CG;           // n of B held by each CTA
-  static constexpr int kStages = CG == 2 ? 6 : 4;
   static constexpr int kAcc = 2;
   static constexpr int kABytes = 128 * 128;
-  static constexpr int kBBytes = kBRows * 128;
-  static constexpr int kStageBytes = kABytes + kBBytes;
   static constexpr int kEpiBufBytes = 32 * 64;      // 32 rows x 32 BF16 (or 16 FP32)
-  static constexpr int kEpiBytes = EPI == EPI_LOSS ? 0 : kEpiWarps * 2 * kEpiBufBytes;
-  static constexpr int kBarOffset = kStages * kStageBytes + kEpiBytes;
-  static constexpr int kNumBars = 2 * kStages + 2 * kAcc + 2 + 4;
-  static constexpr int kSmemBytes = kBarOffset + kNumBars * 8 + 2 * 16 + 16 + 1024;
+  // LOSS: two buffers of (maximum, sum) per quadrant and column; others: two staging boxes per warp
+  static constexpr int kEpiBytes = EPI == EPI_LOSS ? 2 * 4 * kTrainBN * 8 : kEpiWarps * 2 * kEpiBufBytes;
+  static constexpr int kNumBars = 2 * kTrainMaxStages + 2 * kAcc + 2 + 4 + 2;
+  // groups by rank: first tile, first row and rows, the tile count, and the group (a byte each)
+  static constexpr int kTabInts = GRP != GRP_NONE ? 3 * kMaxGroups + 1 + kMaxGroups / 4 : 0;
+  // epilogue buffers, barriers, two scheduler answers, table, 1024-byte alignment; the rest is the ring's
+  static constexpr int kFixedBytes = kEpiBytes + kNumBars * 8 + 2 * 16 + 16 + kTabInts * 4 + 1024;
+  static constexpr int kSmemBytes = 232448 - 16;    // all an SM gives a block, less the two static words
+  static constexpr int kRingBytes = (kSmemBytes - kFixedBytes) / 1024 * 1024;
+  static_assert(kRingBytes >= 6 * 2 * kABytes, "six stages of 256-wide tiles");
   static constexpr bool kClc = GRP != GRP_ROWS;     // GRP_ROWS: the tile count is known on the device only
-  static constexpr int kClcConsumers = CG * (1 + kEpiWarps) + 2;
-  // GRP_ROWS: first tile, first row and rows per group, tile count; GRP_K: group and rows by rank
-  static constexpr int kTabInts = GRP == GRP_ROWS ? 3 * kMaxGroups + 1 : (GRP == GRP_K ? 2 * kMaxGroups : 1);
-  static constexpr uint32_t kIdesc =
-      idesc_f16(kMmaM, kBN) | (A_MN ? 1u << 15 : 0u) | (B_MN ? 1u << 16 : 0u);
-  static_assert(kSmemBytes + kTabInts * 4 + 64 <= 232448, "shared memory overflow");
+  static constexpr int kClcConsumers = 2 * (1 + kEpiWarps) + 2;
+  static constexpr uint32_t kIdesc = idesc_f16(256, kTrainBN) | (A_MN ? 1u << 15 : 0u) | (B_MN ? 1u << 16 : 0u);
 };
+
+// Width of the tiles that `n` columns are cut into.
+__host__ __device__ constexpr int train_n_tile(int n, int multiple) {
+  const int tiles = (n + kTrainBN - 1) / kTrainBN;
+  const int w = tiles > 0 ? (n + tiles - 1) / tiles : multiple;
+  return (w + multiple - 1) / multiple * multiple;
+}
 
 struct TrainTile {
   int mb, nb;
   int a0, b0;        // this CTA's first m of A and first n of B
-  int row_limit;     // output rows at or past this one are not stored
+  int n0, n_end;     // the tile's first column, and where its columns (or its group's) end
+  int nt;            // MMA width
   int z;             // k part (GRP_NONE) or group
-  int ks0, nks;      // first k stage and number of stages
-  int k_end;         // contraction stops here
+  int k0;            // GRP_K: the group's first row
+  int ks0, nks;      // first k stage (from k0) and number of stages
+  int k_end;         // contraction stops here (from k0)
 };
 
-template <bool A_MN, bool B_MN, int EPI, int CG, int GRP>
+template <bool A_MN, bool B_MN, int EPI, int GRP>
 __global__ void __launch_bounds__(384, 1)
     train_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
-                 const __grid_constant__ CUtensorMap tmD, const TrainParams p) {
-  using C = TrainConfig<A_MN, B_MN, EPI, CG, GRP>;
-  constexpr int STAGES = C::kStages;
+                 const __grid_constant__ CUtensorMap tmD, const TrainParams p,
+                 const __grid_constant__ std::conditional_t<GRP == GRP_K, TailMaps, NoTail> tail) {
+  using C = TrainConfig<A_MN, B_MN, EPI, GRP>;
+  constexpr int CG = 2;
   constexpr int ACC = C::kAcc;
   extern __shared__ uint8_t smem_raw[];
   __shared__ uint32_t s_tmem_base;
   __shared__ int s_abort;
-  __shared__ int s_tab[C::kTabInts];
 
   ptx::pdl_launch_dependents();
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
-  const uint32_t rank = (CG == 2) ? ptx::cluster_ctarank() : 0u;
+  const uint32_t rank = ptx::cluster_ctarank();
   const bool leader = rank == 0;
+  const uint32_t nstages = uint32_t(p.stages);
 
   const uint32_t raw = ptx::smem_u32(smem_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;
-  auto stage_a = [&](uint32_t s) { return base + s * uint32_t(C::kStageBytes); };
-  auto stage_b = [&](uint32_t s) { return base + s * uint32_t(C::kStageBytes) + uint32_t(C::kABytes); };
-  const uint32_t epi_base = base + uint32_t(STAGES * C::kStageBytes);
-  const uint32_t bars = base + uint32_t(C::kBarOffset);
+  auto stage_a = [&](uint32_t s) { return base + s * p.stage_bytes; };
+  auto stage_b = [&](uint32_t s) { return base + s * p.stage_bytes + uint32_t(C::kABytes); };
+  const uint32_t epi_base = base + uint32_t(C::kRingBytes);
+  const uint32_t bars = epi_base + uint32_t(C::kEpiBytes);
   auto full_bar = [&](uint32_t s) { return bars + 8u * s; };
-  auto empty_bar = [&](uint32_t s) { return bars + 8u * (uint32_t(STAGES) + s); };
-  auto accf_bar = [&](uint32_t a) { return bars + 8u * (uint32_t(2 * STAGES) + a); };
-  auto acce_bar = [&](uint32_t a) { return bars + 8u * (uint32_t(2 * STAGES + ACC) + a); };
-  const uint32_t drain_bar = bars + uint32_t(8 * (2 * STAGES + 2 * ACC));
+  auto empty_bar = [&](uint32_t s) { return bars + 8u * (uint32_t(kTrainMaxStages) + s); };
+  auto accf_bar = [&](uint32_t a) { return bars + 8u * (uint32_t(2 * kTrainMaxStages) + a); };
+  auto acce_bar = [&](uint32_t a) { return bars + 8u * (uint32_t(2 * kTrainMaxStages + ACC) + a); };
+  const uint32_t drain_bar = bars + uint32_t(8 * (2 * kTrainMaxStages + 2 * ACC));
   const uint32_t never_bar = drain_bar + 8;
   auto clc_full = [&](uint32_t i) { return never_bar + 8u + 8u * i; };
   auto clc_empty = [&](uint32_t i) { return never_bar + 24u + 8u * i; };
-  auto clc_resp = [&](uint32_t i) { return ((never_bar + 40u + 15u) & ~15u) + 16u * i; };
+  auto stat_bar = [&](uint32_t h) { return never_bar + 40u + 8u * h; };   // LOSS: a half's four warps have written
+  auto clc_resp = [&](uint32_t i) { return ((never_bar + 56u + 15u) & ~15u) + 16u * i; };
+  int* s_tab = reinterpret_cast<int*>(smem_raw + (clc_resp(2) - raw));
+  float2* s_stat = reinterpret_cast<float2*>(smem_raw + (epi_base - raw));   // LOSS: [buffer][quadrant][column]
+  enum : int { kTabRow0 = kMaxGroups + 1, kTabRows = 2 * kMaxGroups + 1 };
+  [[maybe_unused]] uint8_t* s_group = reinterpret_cast<uint8_t*>(s_tab + 3 * kMaxGroups + 1);
 
   auto coords = [&](int t) {
     TrainTile tc;
     if constexpr (GRP == GRP_ROWS) {
-      // last group whose first tile is <= t (empty groups are skipped)
+      // last place whose first tile is <= t (groups without rows have none)
       int lo = 0, hi = p.groups;
 #pragma unroll 1
       while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
         if (s_tab[mid] <= t) lo = mid; else hi = mid;
       }
-      const int rows = s_tab[2 * kMaxGroups + lo];
-      tile_coords(t - s_tab[lo], (rows + C::kMmaM - 1) / C::kMmaM, p.tiles_n, p.raster_group, tc.mb, tc.nb);
-      tc.a0 = s_tab[kMaxGroups + lo] + tc.mb * C::kMmaM + int(rank) * 128;
-      tc.row_limit = min(s_tab[kMaxGroups + lo] + rows, p.m);
-      tc.z = lo;
+      const int rows = s_tab[kTabRows + lo], row0 = s_tab[kTabRow0 + lo];
+      tile_coords(t - s_tab[lo], p.tiles_m, (rows + kTrainBN - 1) / kTrainBN, p.raster_group, tc.mb, tc.nb);
+      tc.nt = train_n_tile(rows, 16);
+      tc.n0 = row0 + tc.nb * tc.nt;
+      tc.n_end = min(tc.n0 + tc.nt, row0 + rows);
+      tc.z = s_group[lo];
+      tc.k0 = 0;
       tc.ks0 = 0;
       tc.nks = p.kstages;
       tc.k_end = p.k;
@@ -188,11 +299,14 @@ __global__ void __launch_bounds__(384, 1)
       const int per = p.tiles_m * p.tiles_n;
       const int z = t / per;
       tile_coords(t - z * per, p.tiles_m, p.tiles_n, p.raster_group, tc.mb, tc.nb);
-      tc.a0 = tc.mb * C::kMmaM + int(rank) * 128;
-      tc.row_limit = p.m;
+      tc.nt = p.n_tile;
+      tc.n0 = tc.nb * p.n_tile;
+      tc.n_end = min(tc.n0 + p.n_tile, p.n);
+      tc.k0 = 0;
       if constexpr (GRP == GRP_K) {   // the groups with most rows first
-        tc.z = s_tab[z];
-        tc.k_end = s_tab[kMaxGroups + z];
+        tc.z = s_group[z];
+        tc.k0 = s_tab[kTabRow0 + z];
+        tc.k_end = s_tab[kTabRows + z];
         tc.ks0 = 0;
         tc.nks = (tc.k_end + 63) >> 6;
       } else {
@@ -202,13 +316,14 @@ __global__ void __launch_bounds__(384, 1)
         tc.k_end = p.k;
       }
     }
-    tc.b0 = tc.nb * C::kBN + int(rank) * C::kBRows;
+    tc.a0 = tc.mb * 256 + int(rank) * 128;
+    tc.b0 = tc.n0 + int(rank) * (tc.nt >> 1);
     return tc;
   };
 
   if (threadIdx.x == 0) {
     s_abort = 0;
-    for (uint32_t s = 0; s < uint32_t(STAGES); ++s) {
+    for (uint32_t s = 0; s < nstages; ++s) {
       ptx::mbar_init(full_bar(s), 1);
       ptx::mbar_init(empty_bar(s), 1);
     }
@@ -221,12 +336,11 @@ __global__ void __launch_bounds__(384, 1)
     for (uint32_t i = 0; i < 2; ++i) {
       ptx::mbar_init(clc_full(i), 1);
       ptx::mbar_init(clc_empty(i), C::kClcConsumers);
+      ptx::mbar_init(stat_bar(i), 4);
     }
     ptx::fence_mbar_init();
-    if (GRP != GRP_K) {
-      ptx::prefetch_tmap(&tmA);
-      ptx::prefetch_tmap(&tmB);
-    }
+    ptx::prefetch_tmap(&tmA);
+    ptx::prefetch_tmap(&tmB);
     if (EPI != EPI_LOSS) ptx::prefetch_tmap(&tmD);
   }
   if (warp == 2) {
@@ -236,7 +350,7 @@ __global__ void __launch_bounds__(384, 1)
   ptx::tc_fence_before();
   __syncthreads();
   // see gemm_kernel.cuh: the barriers' initialisation is published by its fence
-  if (CG == 2) ptx::cluster_sync_relaxed();
+  ptx::cluster_sync_relaxed();
   ptx::tc_fence_after();
   const uint32_t tmem = s_tmem_base;
 
@@ -245,53 +359,65 @@ __global__ void __launch_bounds__(384, 1)
   int num_tiles = p.num_tiles;
   if constexpr (GRP != GRP_NONE) {
     ptx::pdl_wait();
-    // sizes may have been cached by this SM before the previous grid wrote them: read through L2
+    // Row ranges: sums stop at the capacity, so that rows past it are cut off and nothing leaves 32 bits.
+    // s_tab[0 .. groups): where each group ends, for now.  The sizes may have been cached by this SM before the
+    // previous grid wrote them: they are read through L2.
     const int g = threadIdx.x;
+    if (warp == 3) {
+      const uint32_t cap = uint32_t(GRP == GRP_ROWS ? p.n : p.k);
+      uint32_t carry = 0;
+#pragma unroll 1
+      for (int g0 = 0; g0 < p.groups; g0 += 32) {
+        uint32_t sr = g0 + lane < p.groups ? min(uint32_t(max(__ldcg(p.sizes + g0 + lane), 0)), cap) : 0u;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const uint32_t x = __shfl_up_sync(0xffffffffu, sr, o);
+          if (lane >= o) sr = min(sr + x, cap);
+        }
+        sr = min(sr + carry, cap);
+        if (g0 + lane < p.groups) s_tab[g0 + lane] = int(sr);
+        carry = __shfl_sync(0xffffffffu, sr, 31);
+      }
+    }
+    __syncthreads();
+    // Places by falling cost of a tile (GRP_ROWS its width, GRP_K its rows): the dear ones go out first, and
+    // what is left at the end is small
+    if (g < p.groups) {
+      const int row0 = g ? s_tab[g - 1] : 0, rows = s_tab[g] - row0;
+      const int mine = GRP == GRP_ROWS ? train_n_tile(rows, 16) : rows;
+      int place = 0;
+      for (int o = 0, before = 0; o < p.groups; ++o) {
+        const int end = s_tab[o];
+        const int other = GRP == GRP_ROWS ? train_n_tile(end - before, 16) : end - before;
+        place += (other > mine || (other == mine && o < g)) ? 1 : 0;
+        before = end;
+      }
+      s_group[place] = uint8_t(g);
+      s_tab[kTabRow0 + place] = row0;
+      s_tab[kTabRows + place] = rows;
+    }
+    __syncthreads();
     if constexpr (GRP == GRP_ROWS) {
       if (warp == 3) {
-        int carry_t = 0, carry_r = 0;
+        int carry = 0;
 #pragma unroll 1
         for (int g0 = 0; g0 < p.groups; g0 += 32) {
-          const int gg = g0 + lane;
-          // sums stop at the capacity: rows past it are cut off, and nothing leaves 32 bits
-          const uint32_t cap = uint32_t(p.m);
-          uint32_t sr = gg < p.groups ? min(uint32_t(max(__ldcg(p.sizes + gg), 0)), cap) : 0u;
-#pragma unroll
-          for (int o = 1; o < 32; o <<= 1) {
-            const uint32_t x = __shfl_up_sync(0xffffffffu, sr, o);
-            if (lane >= o) sr = min(sr + x, cap);
-          }
-          const int end = int(min(uint32_t(carry_r) + sr, cap));
-          int before = __shfl_up_sync(0xffffffffu, end, 1);
-          if (lane == 0) before = carry_r;
-          const int rows = end - before;
-          int tl = ((rows + C::kMmaM - 1) / C::kMmaM) * p.tiles_n;
-          const int mine = tl;
+          const int r = g0 + lane < p.groups ? s_tab[kTabRows + g0 + lane] : 0;
+          const int mine = ((r + kTrainBN - 1) / kTrainBN) * p.tiles_m;
+          int tl = mine;
 #pragma unroll
           for (int o = 1; o < 32; o <<= 1) {
             const int x = __shfl_up_sync(0xffffffffu, tl, o);
             if (lane >= o) tl += x;
           }
-          if (gg < p.groups) {
-            s_tab[gg] = carry_t + tl - mine;
-            s_tab[kMaxGroups + gg] = before;
-            s_tab[2 * kMaxGroups + gg] = rows;
-          }
-          carry_t += __shfl_sync(0xffffffffu, tl, 31);
-          carry_r = __shfl_sync(0xffffffffu, end, 31);
+          if (g0 + lane < p.groups) s_tab[g0 + lane] = carry + tl - mine;
+          carry += __shfl_sync(0xffffffffu, tl, 31);
         }
-        if (lane == 0) s_tab[3 * kMaxGroups] = carry_t;
+        if (lane == 0) s_tab[p.groups] = carry;
       }
-    } else {
-      // (group, rows) by rank, written next to the groups' tensor maps
-      const int* tab = reinterpret_cast<const int*>(p.maps + size_t(p.groups) * 256);
-      if (g < p.groups) {
-        s_tab[g] = __ldcg(tab + g);
-        s_tab[kMaxGroups + g] = __ldcg(tab + kMaxGroups + g);
-      }
+      __syncthreads();
+      num_tiles = s_tab[p.groups];
     }
-    __syncthreads();
-    if constexpr (GRP == GRP_ROWS) num_tiles = s_tab[3 * kMaxGroups];
   }
 
   Ctl ctl;
@@ -340,7 +466,7 @@ __global__ void __launch_bounds__(384, 1)
     if (ptx::elect_one()) {
       const uint64_t pol_a = ptx::policy_evict_normal();
       const uint64_t pol_b = ptx::policy_evict_normal();
-      const uint32_t lead_full0 = (CG == 2) ? ptx::map_to_rank(full_bar(0), 0) : full_bar(0);
+      const uint32_t lead_full0 = ptx::map_to_rank(full_bar(0), 0);
       uint32_t stage = 0, phase = 0;
       uint32_t armed = 0, armed_par = 0;   // stages whose last arming is not yet known complete, and its parity
       bool ok = true;
@@ -351,14 +477,10 @@ __global__ void __launch_bounds__(384, 1)
         const TrainTile tc = coords(t);
         const void* mA = &tmA;
         const void* mB = &tmB;
-        if constexpr (GRP == GRP_K) {
-          mA = p.maps + size_t(tc.z) * 256;
-          mB = p.maps + size_t(tc.z) * 256 + 128;
-          if (tc.nks > 0) {
-            ptx::tmap_acquire(mA);
-            ptx::tmap_acquire(mB);
-          }
-        }
+        // boxes of B: GRP_ROWS 32 rows each (the tiles' widths differ), K-major otherwise one of the tile's
+        // half, MN-major 64 columns each
+        const int nbox = (GRP == GRP_ROWS || B_MN) ? ((tc.nt >> 1) + (B_MN ? 63 : 31)) / (B_MN ? 64 : 32) : 1;
+        const uint32_t txb = GRP == GRP_ROWS ? p.tx_bytes + uint32_t(2 * 32 * 128 * nbox) : p.tx_bytes;
 #pragma unroll 1
         for (int it = 0; it < tc.nks; ++it) {
           const int k0 = (tc.ks0 + it) * 64;
@@ -368,35 +490,62 @@ __global__ void __launch_bounds__(384, 1)
           }
           armed &= ~(1u << stage);
           const uint32_t fb = lead_full0 + 8u * stage;
+          // GRP_K: rows of this stage, when the group ends in it
+          const int last = GRP == GRP_K ? tc.k_end - it * 64 : 64;
           if (leader) {
-            ptx::mbar_arrive_expect_tx(full_bar(stage), p.tx_bytes);
+            // (the rows there are and those up to the MMA's 16, of four chunks in each CTA)
+            ptx::mbar_arrive_expect_tx(full_bar(stage), last < 64 ? uint32_t(2 * 4 * 128) * ((uint32_t(last) + 15u) & ~15u) : txb);
             armed |= 1u << stage;
             armed_par = (armed_par & ~(1u << stage)) | (phase << stage);
           }
-          if (invariant(t < num_tiles && stage < uint32_t(STAGES) && tc.z >= 0 && (tc.a0 % 8 == 0 || !A_MN) &&
-                            tc.b0 % 8 == 0,
+          // a tile of this launch, a ring slot, 16-byte aligned x (TMA's rule), the box inside the stage
+          if (invariant(t < num_tiles && stage < nstages && tc.z >= 0 && (!A_MN || tc.a0 % 8 == 0) &&
+                            (!B_MN || tc.b0 % 8 == 0) && tc.nt >= 16 && tc.nt <= kTrainBN,
                         p.status)) {
+            if (GRP == GRP_K && last < 64) {
+              // The group's last rows, and zeros (rows past the capacity) up to the MMA's 16: what follows in
+              // memory is the next group's and may hold anything.  Boxes of 16, 4 and 1 rows; the 128-byte
+              // swizzle goes by the shared-memory address, so a box may start at any row of a chunk.
+              if constexpr (GRP == GRP_K) {
+                const int up = (last + 15) & ~15;
+                int r = 0;
+#pragma unroll 1
+                while (r < up) {
+                  const int left = (r < last ? last : up) - r;
+                  const int i = left >= 16 ? 0 : (left >= 4 ? 1 : 2);
+                  const int y = r < last ? tc.k0 + k0 + r : p.k;
+#pragma unroll
+                  for (int c = 0; c < 2; ++c) {
+                    const uint32_t at = uint32_t(c * kTrainChunk + r * 128);
+                    ptx::tma_load_2d<CG>(stage_a(stage) + at, &tail.a[i], tc.a0 + c * 64, y, fb, pol_a);
+                    ptx::tma_load_2d<CG>(stage_b(stage) + at, &tail.b[i], tc.b0 + c * 64, y, fb, pol_b);
+                  }
+                  r += i == 0 ? 16 : (i == 1 ? 4 : 1);
+                }
+              }
+            } else {
             if constexpr (A_MN) {
 #pragma unroll
-              for (int c = 0; c < 2; ++c)
-                ptx::tma_load_2d<CG>(stage_a(stage) + uint32_t(c * kTrainChunk), mA, tc.a0 + c * 64, k0, fb, pol_a);
+              for (int c = 0; c < 2; ++c) {
+                const uint32_t dst = stage_a(stage) + uint32_t(c * kTrainChunk);
+                if constexpr (GRP == GRP_ROWS)
+                  ptx::tma_load_3d<CG>(dst, mA, tc.a0 + c * 64, k0, tc.z, fb, pol_a);
+                else
+                  ptx::tma_load_2d<CG>(dst, mA, tc.a0 + c * 64, tc.k0 + k0, fb, pol_a);
+              }
             } else {
               ptx::tma_load_2d<CG>(stage_a(stage), mA, k0, tc.a0, fb, pol_a);
             }
-            if constexpr (B_MN) {
-#pragma unroll
-              for (int c = 0; c < C::kBRows / 64; ++c) {
-                const uint32_t dst = stage_b(stage) + uint32_t(c * kTrainChunk);
-                if constexpr (GRP == GRP_ROWS)
-                  ptx::tma_load_3d<CG>(dst, mB, tc.b0 + c * 64, k0, tc.z, fb, pol_b);
-                else
-                  ptx::tma_load_2d<CG>(dst, mB, tc.b0 + c * 64, k0, fb, pol_b);
-              }
-            } else {
-              ptx::tma_load_2d<CG>(stage_b(stage), mB, k0, tc.b0, fb, pol_b);
+#pragma unroll 1
+            for (int c = 0; c < nbox; ++c) {
+              if constexpr (B_MN)
+                ptx::tma_load_2d<CG>(stage_b(stage) + uint32_t(c * kTrainChunk), mB, tc.b0 + c * 64, tc.k0 + k0, fb, pol_b);
+              else
+                ptx::tma_load_2d<CG>(stage_b(stage) + uint32_t(c * 32 * 128), mB, k0, tc.b0 + c * 32, fb, pol_b);
+            }
             }
           }
-          if (++stage == uint32_t(STAGES)) {
+          if (++stage == nstages) {
             stage = 0;
             phase ^= 1u;
           }
@@ -411,7 +560,7 @@ __global__ void __launch_bounds__(384, 1)
         int dummy = 0;
         quiet.abort_flag = &dummy;
 #pragma unroll 1
-        for (uint32_t s = 0; s < uint32_t(STAGES); ++s)
+        for (uint32_t s = 0; s < nstages; ++s)
           if (armed & (1u << s)) wait_bar<false>(full_bar(s), (armed_par >> s) & 1u, quiet);
       }
     }
@@ -423,18 +572,19 @@ __global__ void __launch_bounds__(384, 1)
       uint32_t stage = 0, phase = 0, acc = 0, accph = 0;
       bool ok = true;
       if (p.inject_stall) ok = wait_bar<false>(never_bar, 0u, ctl);
-      const uint16_t mask = (CG == 2) ? uint16_t(0x3) : uint16_t(0x1);
+      const uint16_t mask = 0x3;
       uint32_t cslot = 0, cphase = 0;
       uint32_t committed = 0;
 #pragma unroll 1
       for (int t = first_tile; t >= 0 && ok;) {
-        if (!wait_bar<CG == 2>(acce_bar(acc), accph ^ 1u, ctl)) {
+        if (!wait_bar<true>(acce_bar(acc), accph ^ 1u, ctl)) {
           ok = false;
           break;
         }
         ptx::tc_fence_after();
-        const uint32_t d_tmem = tmem + acc * uint32_t(C::kBN);
+        const uint32_t d_tmem = tmem + acc * uint32_t(kTrainBN);
         const TrainTile tc = coords(t);
+        const uint32_t idesc = idesc_with_n(C::kIdesc, tc.nt);
 #pragma unroll 1
         for (int it = 0; it < tc.nks; ++it) {
           if (!wait_bar<false>(full_bar(stage), phase, ctl)) {
@@ -444,17 +594,17 @@ __global__ void __launch_bounds__(384, 1)
           const uint64_t adesc = A_MN ? sdesc_mn_sw128(stage_a(stage)) : sdesc_sw128(stage_a(stage));
           const uint64_t bdesc = B_MN ? sdesc_mn_sw128(stage_b(stage)) : sdesc_sw128(stage_b(stage));
           const int left = tc.k_end - (tc.ks0 + it) * 64;   // k past it are zero, or not there
-          const bool stage_ok = invariant(stage < uint32_t(STAGES) && acc < uint32_t(ACC), p.status);
+          const bool stage_ok = invariant(stage < nstages && acc < uint32_t(ACC) && tc.nt <= kTrainBN, p.status);
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
             if (j * 16 >= left || !stage_ok) break;
             // 16 k: 32 bytes along K-major rows, two 8-k groups of 1024 bytes in MN-major chunks
             const uint64_t aoff = A_MN ? uint64_t((j * 2048) >> 4) : uint64_t((j * 32) >> 4);
             const uint64_t boff = B_MN ? uint64_t((j * 2048) >> 4) : uint64_t((j * 32) >> 4);
-            ptx::mma_f16<CG>(d_tmem, adesc + aoff, bdesc + boff, C::kIdesc, (it > 0 || j > 0) ? 1u : 0u);
+            ptx::mma_f16<CG>(d_tmem, adesc + aoff, bdesc + boff, idesc, (it > 0 || j > 0) ? 1u : 0u);
           }
           ptx::tc_commit<CG>(empty_bar(stage), mask);
-          if (++stage == uint32_t(STAGES)) {
+          if (++stage == nstages) {
             stage = 0;
             phase ^= 1u;
           }
@@ -479,7 +629,7 @@ __global__ void __launch_bounds__(384, 1)
 #pragma unroll 1
         for (uint32_t a = 0; a < uint32_t(ACC); ++a) {
           const uint32_t uses = committed / uint32_t(ACC) + (a < committed % uint32_t(ACC) ? 1u : 0u);
-          if (uses) wait_bar<CG == 2>(acce_bar(a), (uses & 1u) ^ 1u, quiet);
+          if (uses) wait_bar<true>(acce_bar(a), (uses & 1u) ^ 1u, quiet);
         }
       }
     }
@@ -493,10 +643,10 @@ __global__ void __launch_bounds__(384, 1)
         uint32_t slot = 0, ph = 0;
 #pragma unroll 1
         while (true) {
-          if (!wait_bar<CG == 2>(clc_empty(slot), ph ^ 1u, ctl)) break;
+          if (!wait_bar<true>(clc_empty(slot), ph ^ 1u, ctl)) break;
           ptx::mbar_arrive_expect_tx(clc_full(slot), 16u);
-          if (CG == 2) ptx::mbar_expect_tx_relaxed_cluster(ptx::map_to_rank(clc_full(slot), 1), 16u);
-          ptx::clc_try_cancel<CG == 2>(clc_resp(slot), clc_full(slot));
+          ptx::mbar_expect_tx_relaxed_cluster(ptx::map_to_rank(clc_full(slot), 1), 16u);
+          ptx::clc_try_cancel<true>(clc_resp(slot), clc_full(slot));
           if (!wait_bar<false>(clc_full(slot), ph, ctl)) break;
           uint32_t x = 0;
           const bool got = ptx::clc_read(clc_resp(slot), x);
@@ -505,7 +655,18 @@ __global__ void __launch_bounds__(384, 1)
             slot = 0;
             ph ^= 1u;
           }
-          if (!got) break;
+          if (!got) {
+            // both CTAs' roles have read the last two answers: no arrival from the other CTA is in flight when
+            // this one leaves and its shared memory goes to the next kernel
+            for (int i = 0; i < 2; ++i) {
+              if (!wait_bar<true>(clc_empty(slot), ph ^ 1u, ctl)) break;
+              if (++slot == 2) {
+                slot = 0;
+                ph ^= 1u;
+              }
+            }
+            break;
+          }
         }
       }
     }
@@ -515,25 +676,21 @@ __global__ void __launch_bounds__(384, 1)
   else if (warp >= 4) {
     const int e = warp - 4;
     const int q = warp & 3;              // accumulator lane quadrant this warp may read
-    const int h = e >> 2;                // columns [0, 128) or [128, 256) of the tile
+    const int h = e >> 2;                // first or second half of the tile's 32-column chunks
     const uint32_t my_buf0 = epi_base + uint32_t(e * 2 * C::kEpiBufBytes);
-    const uint32_t acce_lead0 = (CG == 2) ? ptx::map_to_rank(acce_bar(0), 0) : acce_bar(0);
+    const uint32_t acce_lead0 = ptx::map_to_rank(acce_bar(0), 0);
     if (GRP == GRP_NONE) ptx::pdl_wait();
+    const float alpha = p.scale ? p.alpha * __ldcg(p.scale) : p.alpha;
     uint32_t acc = 0, accph = 0;
     uint32_t cslot = 0, cphase = 0;
-    uint32_t nbuf = 0;                   // staging buffers used so far
-    // one 32-row x 64-byte box from four 16-byte pieces per lane, in the 64-byte swizzle
-    auto stage_box = [&](const uint32_t (&w)[16], auto&& send) {
-      const uint32_t buf = my_buf0 + (nbuf & 1u) * uint32_t(C::kEpiBufBytes);
-      ++nbuf;
+    uint32_t turn = 0;                   // staging boxes (LOSS: tiles) so far
+    // a 2 KB staging box: wait until the store that used it last has read it, fill, send
+    auto stage_box = [&](auto&& fill, auto&& send) {
+      const uint32_t buf = my_buf0 + (turn & 1u) * uint32_t(C::kEpiBufBytes);
+      ++turn;
       if (lane == 0) ptx::bulk_wait_group_read<1>();
       __syncwarp();
-      const uint32_t row_addr = buf + uint32_t(lane * 64);
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const uint32_t chunk = uint32_t(j) ^ ((uint32_t(lane) >> 1) & 3u);
-        ptx::st_shared_v4(row_addr + chunk * 16u, w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
-      }
+      fill(buf);
       ptx::fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) {
@@ -541,159 +698,263 @@ __global__ void __launch_bounds__(384, 1)
         ptx::bulk_commit_group();
       }
     };
+    // a row per lane, four 16-byte pieces in the 64-byte swizzle
+    auto fill_rows = [&](uint32_t buf, const uint32_t (&w)[16]) {
+      const uint32_t row_addr = buf + uint32_t(lane * 64);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const uint32_t chunk = uint32_t(j) ^ ((uint32_t(lane) >> 1) & 3u);
+        ptx::st_shared_v4(row_addr + chunk * 16u, w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
+      }
+    };
 #pragma unroll 1
     for (int t = first_tile; t >= 0;) {
       const TrainTile tc = coords(t);
-      const int row0 = tc.a0 + q * 32;
-      const int row = row0 + lane;
-      const int col0 = tc.nb * C::kBN + h * 128;
-      // the row's label as an offset from this warp's first column (-1: not among its 128)
-      int hit = -1;
-      float l2 = 0.f, coef = 0.f;
-      uint32_t keep = 0;
+      const int nchunks = (tc.nt + 31) >> 5;
+      const int first = h ? (nchunks + 1) >> 1 : 0;                        // this warp's chunks
+      const int nch = h ? nchunks >> 1 : (nchunks + 1) >> 1;
+      const int row0 = tc.a0 + q * 32;                                     // its rows of D
+      const int col0 = tc.n0 + first * 32;                                 // and its first column
+      // Cross entropy: per chunk, of column col0 + 32 c + lane: its label's distance from row0, and for
+      // DLOGITS lse in base 2 and which columns are ignored (uniform masks)
+      int off[4];
+      uint32_t hits[4], gone[4];
+      float l2[4];
       if constexpr (EPI == EPI_LOSS || EPI == EPI_DLOGITS) {
-        if (row < p.m) {
-          const long long y = __ldcg(p.labels + row);
-          const long long off = y - (long long)(p.vocab0) - col0;
-          if (off >= 0 && off < 128 && col0 + int(off) < p.n) hit = int(off);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          const int col = col0 + c * 32 + lane;
+          const bool there = c < nch && col < tc.n_end;
+          const long long y = there ? __ldcg(p.labels + col) : -1;
+          const long long d = y - (long long)(p.vocab0) - row0;
+          const bool kept = y >= 0 && y < p.vocab;
+          const bool hit = kept && d >= 0 && d < 32 && row0 + int(d) < p.m;
+          off[c] = hit ? int(d) : -1;
+          hits[c] = __ballot_sync(0xffffffffu, hit);
           if constexpr (EPI == EPI_DLOGITS) {
-            // rows of ignored labels are cleared by mask, whatever lse, dloss and the row hold
-            l2 = __ldcg(p.lse + row) * 1.4426950408889634f;
-            coef = __ldcg(p.dloss + row) * p.alpha;
-            keep = (y >= 0 && y < p.vocab) ? 0xffffffffu : 0u;
+            l2[c] = there ? __ldcg(p.lse + col) * 1.4426950408889634f : 0.f;
+            gone[c] = __ballot_sync(0xffffffffu, there && !kept);
           }
         }
       }
       if (!wait_bar_warp<false>(accf_bar(acc), accph, ctl)) break;
       ptx::tc_fence_after();
-      const bool idle = !invariant(acc < uint32_t(ACC) && t < num_tiles, p.status);
-      const uint32_t tbase = tmem + (uint32_t(q * 32) << 16) + acc * uint32_t(C::kBN) + uint32_t(h * 128);
-      uint32_t v[4][32];
-      if (!idle) {
+      const bool idle = !invariant(acc < uint32_t(ACC) && t < num_tiles && first * 32 + nch * 32 <= kTrainBN, p.status);
+      const uint32_t tbase = tmem + (uint32_t(q * 32) << 16) + acc * uint32_t(kTrainBN) + uint32_t(first * 32);
+      auto hand_back = [&]() {   // every load of this tile has completed
+        ptx::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          if (leader)
+            ptx::mbar_arrive(acce_bar(acc));
+          else
+            ptx::mbar_arrive_relaxed_cluster(acce_lead0 + 8u * acc);
+        }
+        if (++acc == uint32_t(ACC)) {
+          acc = 0;
+          accph ^= 1u;
+        }
+      };
+      if constexpr (EPI == EPI_LOSS) {
+        float2* stat = s_stat + (turn & 1u) * uint32_t(4 * kTrainBN) + first * 32;
+        const uint32_t stat_phase = (turn & 1u);
+        ++turn;
+        const float c2 = fabsf(p.c2);
+        const int rows_there = p.m - row0 - (lane >> 2);   // of rows 0, 8, 16, 24 past this lane's first
+        const int n = idle ? 0 : nch;
+        // chunk c in v[c & 1]: rows of the lower 16 lanes in the first half, of the upper 16 in the second
+        uint32_t v[2][32];
+        auto load = [&](int c, uint32_t (&r)[32]) {
+          ptx::tmem_ld_16x256b_x4<0>(tbase + uint32_t(c * 32), r);
+          ptx::tmem_ld_16x256b_x4<16>(tbase + (16u << 16) + uint32_t(c * 32), r);
+        };
+        if (n > 0) load(0, v[0]);
 #pragma unroll
-        for (int c = 0; c < 4; ++c) ptx::tmem_ld_32x32b_x32(tbase + uint32_t(c * 32), v[c]);
-      }
-      ptx::tmem_ld_wait();
-      ptx::tc_fence_before();
-      __syncwarp();
-      if (lane == 0) {
-        if (CG == 1 || leader)
-          ptx::mbar_arrive(acce_bar(acc));
-        else
-          ptx::mbar_arrive_relaxed_cluster(acce_lead0 + 8u * acc);
-      }
-      if (++acc == uint32_t(ACC)) {
-        acc = 0;
-        accph ^= 1u;
-      }
-      if (GRP == GRP_K && tc.nks == 0) {   // no rows: the sum is empty, the accumulator undefined
+        for (int c = 0; c < 4; ++c) {
+          if (c >= n) continue;
+          ptx::tmem_ld_wait_for(v[c & 1]);
+          if (c + 1 < n) load(c + 1, v[(c + 1) & 1]);
+          // labels among these 32 rows: about one column in vocab / 32
+#pragma unroll 1
+          for (uint32_t left = hits[c]; left; left &= left - 1) {
+            const int j = __ffs(int(left)) - 1;
+            const int row = __shfl_sync(0xffffffffu, off[c], j);
+            uint32_t z = ptx::tmem_ld_32x32b_x1(tbase + uint32_t(c * 32 + j));
+            asm volatile("tcgen05.wait::ld.sync.aligned;" : "+r"(z)::"memory");
+            if (lane == row) p.zlabel[col0 + c * 32 + j] = __uint_as_float(z) * alpha;
+          }
+          if (c + 1 == n) {
+            hand_back();
+          }
+          // x[4 i + 2 k + e]: column 8 i + 2 (t % 4) + e, row t / 4 + 8 k (k = 0, 1), and 16 more (k = 2, 3)
+          float x[32];
+#pragma unroll
+          for (int j = 0; j < 32; ++j) x[j] = __uint_as_float(v[c & 1][j]);
+          if (p.c2 < 0.f) {
+#pragma unroll
+            for (int j = 0; j < 32; ++j) x[j] = -x[j];
+          }
+          if (rows_there <= 24) {   // rows past the vocabulary's end
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+              if (((j >> 1) & 1) * 8 + (j >> 4) * 16 >= rows_there) x[j] = -INFINITY;
+          }
+          float top[8], sum[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const int j = 4 * (i >> 1) + (i & 1);
+            top[i] = fmaxf(fmaxf(x[j], x[j + 2]), fmaxf(x[j + 16], x[j + 18]));
+          }
+          const float own = fold_columns(top, lane, [](float a, float b) { return fmaxf(a, b); });
+          unfold_columns(own, lane, top);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const int j = 4 * (i >> 1) + (i & 1);
+            const float sub = fabsf(top[i]) == INFINITY ? 0.f : top[i] * c2;   // no inf - inf
+            sum[i] = (ptx::ex2(fmaf(x[j], c2, -sub)) + ptx::ex2(fmaf(x[j + 2], c2, -sub))) +
+                     (ptx::ex2(fmaf(x[j + 16], c2, -sub)) + ptx::ex2(fmaf(x[j + 18], c2, -sub)));
+          }
+          if (c2 == 0.f && rows_there <= 24) {   // scale 0: 0 * -inf is not a number
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              sum[i] = float(rows_there > 0) + float(rows_there > 8) + float(rows_there > 16);
+          }
+          const float s = fold_columns(sum, lane, [](float a, float b) { return a + b; });
+          stat[q * kTrainBN + c * 32 + column_of_lane(lane)] = make_float2(own == -INFINITY ? own : own * c2, s);
+        }
+        if (n == 0) hand_back();
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(stat_bar(h));
+        if (!wait_bar_warp<false>(stat_bar(h), stat_phase, ctl)) break;
+        // the four warps' 32 rows each: warp q joins chunk q
+        const int col = col0 + q * 32 + lane;
+        if (q < nch && !idle && col < tc.n_end && tc.a0 < p.m) {
+          float m = -INFINITY, s = 0.f;
+          float2 x[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            x[i] = stat[i * kTrainBN + q * 32 + lane];
+            m = fmaxf(m, x[i].x);
+          }
+          const float sub = fabsf(m) == INFINITY ? 0.f : m;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) s += x[i].y * ptx::ex2(x[i].x - sub);
+          p.part[size_t(tc.a0 >> 7) * size_t(p.n) + col] = make_float2(m, s);
+        }
+      } else if constexpr (EPI == EPI_DLOGITS) {
+        const int n = idle ? 0 : nch;
+        uint32_t v[2][32];
+        if (n > 0) ptx::tmem_ld_32x32b_x32(tbase, v[0]);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          if (c >= n) continue;
+          const int col = col0 + c * 32;
+          ptx::tmem_ld_wait_for(v[c & 1]);
+          if (c + 1 < n) ptx::tmem_ld_32x32b_x32(tbase + uint32_t(c * 32 + 32), v[(c + 1) & 1]);
+          if (c + 1 == n) hand_back();
+          if (col >= tc.n_end || row0 >= p.m) continue;
+          float g[32];
+#pragma unroll
+          for (int j = 0; j < 32; ++j)
+            g[j] = ptx::ex2(fmaf(__uint_as_float(v[c & 1][j]), p.c2, -__shfl_sync(0xffffffffu, l2[c], j)));
+          if (hits[c]) {
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+              if (((hits[c] >> j) & 1u) && lane == __shfl_sync(0xffffffffu, off[c], j)) g[j] -= 1.f;
+          }
+          if (gone[c]) {   // whatever the logits and lse are there
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+              if ((gone[c] >> j) & 1u) g[j] = 0.f;
+          }
+          uint32_t w[16];
+#pragma unroll
+          for (int j = 0; j < 16; ++j) w[j] = ptx::pack_bf16x2(g[2 * j], g[2 * j + 1]);
+          if (first * 32 + c * 32 + 32 <= tc.nt) {
+            stage_box([&](uint32_t buf) { fill_rows(buf, w); },
+                      [&](uint32_t buf) { ptx::tma_store_3d(&tmD, buf, col, row0, 0); });
+          } else if (row0 + lane < p.m) {   // the tile ends after 16 columns of the chunk (a 32-byte sector)
+            uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.d) + size_t(row0 + lane) * p.ldd + col);
+            dst[0] = make_uint4(w[0], w[1], w[2], w[3]);
+            dst[1] = make_uint4(w[4], w[5], w[6], w[7]);
+          }
+        }
+        if (n == 0) hand_back();
+      } else {
+        uint32_t v[4][32];
 #pragma unroll
         for (int c = 0; c < 4; ++c)
+          if (c < nch && !idle) ptx::tmem_ld_32x32b_x32(tbase + uint32_t(c * 32), v[c]);
+        ptx::tmem_ld_wait();
+        hand_back();
+        if (GRP == GRP_K && tc.nks == 0) {   // no rows: the sum is empty, the accumulator undefined
 #pragma unroll
-          for (int j = 0; j < 32; ++j) v[c][j] = 0u;
-      }
-      if (!idle) {
-        if constexpr (EPI == EPI_LOSS) {
-          const int ncol = p.n - col0;
-          float sum = 0.f, top = -INFINITY;
-          if (ncol > 0) {
-            if (ncol < 128) {   // columns that are not there: the least logit there is
-              const uint32_t low = p.c2 >= 0.f ? 0xff800000u : 0x7f800000u;
+          for (int c = 0; c < 4; ++c)
 #pragma unroll
-              for (int c = 0; c < 4; ++c)
+            for (int j = 0; j < 32; ++j) v[c][j] = 0u;
+        }
 #pragma unroll
-                for (int j = 0; j < 32; ++j)
-                  if (c * 32 + j >= ncol) v[c][j] = low;
-            }
-            // the largest z * c2: by the largest or, for a negative scale, the least z
-            float ext = __uint_as_float(v[0][0]);
-            if (p.c2 >= 0.f) {
-#pragma unroll
-              for (int c = 0; c < 4; ++c)
-#pragma unroll
-                for (int j = 0; j < 32; ++j) ext = fmaxf(ext, __uint_as_float(v[c][j]));
-            } else {
-#pragma unroll
-              for (int c = 0; c < 4; ++c)
-#pragma unroll
-                for (int j = 0; j < 32; ++j) ext = fminf(ext, __uint_as_float(v[c][j]));
-            }
-            top = p.c2 == 0.f ? 0.f : ext * p.c2;
-            const float sub = fabsf(top) == INFINITY ? 0.f : top;   // no inf - inf
-            float s4[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-            for (int c = 0; c < 4; ++c)
-#pragma unroll
-              for (int j = 0; j < 32; ++j) s4[j & 3] += ptx::ex2(fmaf(__uint_as_float(v[c][j]), p.c2, -sub));
-            sum = (s4[0] + s4[1]) + (s4[2] + s4[3]);
-            if (p.c2 == 0.f && ncol < 128) sum = float(ncol);   // scale 0: every logit there is counts 1
-            if (__any_sync(0xffffffffu, hit >= 0)) {
-              float z = 0.f;
-#pragma unroll
-              for (int c = 0; c < 4; ++c)
-#pragma unroll
-                for (int j = 0; j < 32; ++j)
-                  if (hit == c * 32 + j) z = __uint_as_float(v[c][j]);
-              if (hit >= 0) p.zlabel[row] = z * p.alpha;
-            }
-          }
-          if (row < p.m) p.part[size_t(tc.nb * 2 + h) * size_t(p.m) + row] = make_float2(top, sum);
-        } else if constexpr (EPI == EPI_DLOGITS) {
-          const bool any_hit = __any_sync(0xffffffffu, hit >= 0);
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            float g[32];
-#pragma unroll
-            for (int j = 0; j < 32; ++j) g[j] = ptx::ex2(fmaf(__uint_as_float(v[c][j]), p.c2, -l2));
-            if (any_hit) {
-#pragma unroll
-              for (int j = 0; j < 32; ++j)
-                if (hit == c * 32 + j) g[j] -= 1.f;
-            }
-            uint32_t w[16];
-#pragma unroll
-            for (int j = 0; j < 16; ++j) w[j] = ptx::pack_bf16x2(g[2 * j] * coef, g[2 * j + 1] * coef) & keep;
-            if (col0 + c * 32 < p.n && row0 < p.m)
-              stage_box(w, [&](uint32_t buf) { ptx::tma_store_3d(&tmD, buf, col0 + c * 32, row0, 0); });
-          }
-        } else if constexpr (EPI == EPI_BF16) {
-          const int z = GRP == GRP_K ? tc.z : 0;
-          const bool masked = GRP == GRP_ROWS && row0 + 32 > tc.row_limit;
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
+        for (int c = 0; c < 4; ++c) {
+          const int col = col0 + c * 32;
+          if (c >= nch || idle || col >= tc.n_end || row0 >= p.m) continue;
+          if constexpr (EPI == EPI_BF16) {
             uint32_t w[16];
 #pragma unroll
             for (int j = 0; j < 16; ++j)
-              w[j] = ptx::pack_bf16x2(__uint_as_float(v[c][2 * j]) * p.alpha, __uint_as_float(v[c][2 * j + 1]) * p.alpha);
-            const int col = col0 + c * 32;
-            if (masked) {   // a box that crosses the end of its group: row by row
-              if (row < tc.row_limit) {
-                uint16_t* dst = static_cast<uint16_t*>(p.d) + size_t(row) * size_t(p.n) + col;
+              w[j] = ptx::pack_bf16x2(__uint_as_float(v[c][2 * j]) * alpha, __uint_as_float(v[c][2 * j + 1]) * alpha);
+            stage_box([&](uint32_t buf) { fill_rows(buf, w); },
+                      [&](uint32_t buf) { ptx::tma_store_3d(&tmD, buf, col, row0, GRP == GRP_K ? tc.z : 0); });
+          } else if constexpr (EPI == EPI_BF16_T) {
+            // even lanes take column j for rows (lane, lane + 1), odd lanes column j + 1 for rows (lane - 1, lane)
+            uint32_t w[16];
 #pragma unroll
-                for (int j = 0; j < 4; ++j)
-                  if (col + j * 8 < p.n)
-                    *reinterpret_cast<uint4*>(dst + j * 8) = make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
-              }
-            } else if (col < p.n && row0 < p.m) {
-              stage_box(w, [&](uint32_t buf) { ptx::tma_store_3d(&tmD, buf, col, row0, z); });
+            for (int j = 0; j < 16; ++j) {
+              const float x0 = __uint_as_float(v[c][2 * j]) * alpha, x1 = __uint_as_float(v[c][2 * j + 1]) * alpha;
+              const float r = __shfl_xor_sync(0xffffffffu, (lane & 1) ? x0 : x1, 1);
+              w[j] = (lane & 1) ? ptx::pack_bf16x2(r, x1) : ptx::pack_bf16x2(x0, r);
             }
-          }
-        } else {
-          if (!(GRP == GRP_K && p.accumulate && tc.nks == 0)) {   // adding nothing
+            const int there = tc.n_end - col;   // columns of the chunk that are the tile's
+            if (there >= 16) {
+              stage_box(
+                  [&](uint32_t buf) {
 #pragma unroll
-            for (int c = 0; c < 8; ++c) {
+                    for (int j = 0; j < 16; ++j) {
+                      const uint32_t r = uint32_t(2 * j + (lane & 1));
+                      const uint32_t chunk = (uint32_t(lane) >> 3) ^ ((r >> 1) & 3u);
+                      asm volatile("st.shared.b32 [%0], %1;" ::"r"(buf + r * 64u + chunk * 16u + ((uint32_t(lane) >> 1) & 3u) * 4u),
+                                   "r"(w[j])
+                                   : "memory");
+                    }
+                  },
+                  [&](uint32_t buf) {
+                    ptx::tma_store_3d(&tmD, buf, row0, col, 0);
+                    if (there >= 32) ptx::tma_store_3d(&tmD, buf + 1024u, row0, col + 16, 0);
+                  });
+            }
+            if ((there & 15) && there < 32 && row0 + (lane & ~1) < p.m) {   // fewer than 16 before the tile's or group's end
+              uint16_t* dst = static_cast<uint16_t*>(p.d) + row0 + (lane & ~1);
+#pragma unroll
+              for (int j = 0; j < 16; ++j) {
+                const int r = 2 * j + (lane & 1);
+                if (r >= (there & 16) && r < there)
+                  *reinterpret_cast<uint32_t*>(dst + size_t(col + r) * p.ldd) = w[j];
+              }
+            }
+          } else {
+            if (GRP == GRP_K && p.accumulate && tc.nks == 0) continue;   // adding nothing
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+              if (first * 32 + c * 32 + half * 16 >= tc.nt || col + half * 16 >= tc.n_end) continue;
               uint32_t w[16];
 #pragma unroll
-              for (int j = 0; j < 16; ++j)
-                w[j] = __float_as_uint(__uint_as_float(v[c >> 1][(c & 1) * 16 + j]) * p.alpha);
-              const int col = col0 + c * 16;
-              if (col < p.n && row0 < p.m)
-                stage_box(w, [&](uint32_t buf) {
-                  if (p.accumulate)
-                    ptx::tma_add_3d(&tmD, buf, col, row0, tc.z);
-                  else
-                    ptx::tma_store_3d(&tmD, buf, col, row0, tc.z);
-                });
+              for (int j = 0; j < 16; ++j) w[j] = __float_as_uint(__uint_as_float(v[c][half * 16 + j]) * alpha);
+              stage_box([&](uint32_t buf) { fill_rows(buf, w); },
+                        [&](uint32_t buf) {
+                          if (p.accumulate)
+                            ptx::tma_add_3d(&tmD, buf, col + half * 16, row0, tc.z);
+                          else
+                            ptx::tma_store_3d(&tmD, buf, col + half * 16, row0, tc.z);
+                        });
             }
           }
         }
@@ -714,7 +975,7 @@ __global__ void __launch_bounds__(384, 1)
   }
   ptx::tc_fence_before();
   __syncthreads();
-  if (CG == 2) ptx::cluster_sync_relaxed();
+  ptx::cluster_sync_relaxed();
   if (warp == 2) {
     ptx::tc_fence_after();
     ptx::tmem_dealloc<CG>(tmem, 512u);

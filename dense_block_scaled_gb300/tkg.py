@@ -38,7 +38,6 @@ EXPORTS = [
     "tkg_gemm_bf16_strided", "tkg_gemm_mxfp8_strided", "tkg_gemm_nvfp4_strided",
     "tkg_linear_ce_loss", "tkg_linear_ce_loss_workspace_bytes", "tkg_linear_ce_grad",
     "tkg_linear_ce_grad_workspace_bytes", "tkg_gemm_grouped_dev_bf16_dgrad", "tkg_gemm_grouped_dev_bf16_wgrad",
-    "tkg_gemm_grouped_dev_bf16_wgrad_workspace_bytes",
 ]
 
 MAX_LIST = 16
@@ -104,13 +103,11 @@ def load() -> ctypes.CDLL:
             lib.tkg_linear_ce_grad.argtypes = [i, i, i, vp, i, vp, i, vp, f, vp, vp, vp, i, vp, i, i, i, vp, sz, vp]
             lib.tkg_linear_ce_grad_workspace_bytes.argtypes = [i, i, i, i]
             lib.tkg_gemm_grouped_dev_bf16_dgrad.argtypes = [i, vp, i, i, i, vp, vp, vp, f, vp]
-            lib.tkg_gemm_grouped_dev_bf16_wgrad.argtypes = [i, vp, i, i, i, vp, vp, vp, i, f, vp, sz, vp]
-            lib.tkg_gemm_grouped_dev_bf16_wgrad_workspace_bytes.argtypes = [i]
+            lib.tkg_gemm_grouped_dev_bf16_wgrad.argtypes = [i, vp, i, i, i, vp, vp, vp, i, f, vp]
             for name in ("tkg_linear_ce_loss", "tkg_linear_ce_grad", "tkg_gemm_grouped_dev_bf16_dgrad",
                          "tkg_gemm_grouped_dev_bf16_wgrad"):
                 getattr(lib, name).restype = ctypes.c_int
-            for name in ("tkg_linear_ce_loss_workspace_bytes", "tkg_linear_ce_grad_workspace_bytes",
-                         "tkg_gemm_grouped_dev_bf16_wgrad_workspace_bytes"):
+            for name in ("tkg_linear_ce_loss_workspace_bytes", "tkg_linear_ce_grad_workspace_bytes"):
                 getattr(lib, name).restype = sz
             lib.tkg_get_device_status.argtypes = [vp]
             lib.tkg_status_string.argtypes = [st]
@@ -433,12 +430,7 @@ def gemm_grouped_dev_bf16_dgrad(sizes_dev, dD, B, dA, alpha: float = 1.0, stream
            "tkg_gemm_grouped_dev_bf16_dgrad")
 
 
-def gemm_grouped_dev_bf16_wgrad_workspace_bytes(groups: int) -> int:
-    return int(load().tkg_gemm_grouped_dev_bf16_wgrad_workspace_bytes(groups))
-
-
-def gemm_grouped_dev_bf16_wgrad(sizes_dev, dD, A, dB, alpha: float = 1.0, accumulate: bool = False, workspace=None,
-                                stream=None) -> None:
+def gemm_grouped_dev_bf16_wgrad(sizes_dev, dD, A, dB, alpha: float = 1.0, accumulate: bool = False, stream=None) -> None:
     """Gradient of gemm_grouped_dev_bf16 to the experts: dB_g (n x k, bf16 or float32) = alpha * dD_g^T @ A_g."""
     import torch
     groups, (cap, n), k = sizes_dev.numel(), dD.shape, A.shape[-1]
@@ -447,10 +439,8 @@ def gemm_grouped_dev_bf16_wgrad(sizes_dev, dD, A, dB, alpha: float = 1.0, accumu
     _want_dense(A, "A", torch.bfloat16, (cap, k))
     gtype = _grad_type(dB, "dB", accumulate)
     _want_dense(dB, "dB", dB.dtype, (groups, n, k))
-    lib = load()
-    ws, nbytes = _workspace(workspace, lib.tkg_gemm_grouped_dev_bf16_wgrad_workspace_bytes(groups), dD, stream)
-    _check(lib.tkg_gemm_grouped_dev_bf16_wgrad(groups, sizes_dev.data_ptr(), cap, n, k, dD.data_ptr(), A.data_ptr(),
-                                               dB.data_ptr(), gtype, alpha, ws.data_ptr(), nbytes, _stream(stream)),
+    _check(load().tkg_gemm_grouped_dev_bf16_wgrad(groups, sizes_dev.data_ptr(), cap, n, k, dD.data_ptr(),
+                                                  A.data_ptr(), dB.data_ptr(), gtype, alpha, _stream(stream)),
            "tkg_gemm_grouped_dev_bf16_wgrad")
 
 

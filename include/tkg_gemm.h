@@ -314,10 +314,7 @@ size_t tkg_linear_ce_grad_workspace_bytes(int tokens, int vocab, int hidden, int
  *  - Rows outside the groups are neither read into results (whatever they hold)
  *    nor written; counts past m_capacity are cut off.  A group without rows has
  *    dB_g = 0 (TKG_GRAD_F32_ADD: unchanged).  groups == 1 is the plain product.
- *  - Requires n % 8 == 0, k % 8 == 0, 16-byte aligned pointers, groups <= 128;
- *    wgrad's workspace is 128-byte aligned and holds
- *    tkg_gemm_grouped_dev_bf16_wgrad_workspace_bytes(groups) bytes; calls that
- *    may overlap on the GPU need one each.
+ *  - Requires n % 8 == 0, k % 8 == 0, 16-byte aligned pointers, groups <= 128.
  *  - dgrad: n == 0 gives TKG_ERR_UNSUPPORTED; k == 0 or m_capacity == 0: nothing
  *    to do.  wgrad: m_capacity == 0 zeroes dB (not for TKG_GRAD_F32_ADD). */
 tkg_status tkg_gemm_grouped_dev_bf16_dgrad(int groups, const int *m_sizes_dev, int m_capacity, int n, int k,
@@ -325,8 +322,7 @@ tkg_status tkg_gemm_grouped_dev_bf16_dgrad(int groups, const int *m_sizes_dev, i
                                            cudaStream_t stream);
 tkg_status tkg_gemm_grouped_dev_bf16_wgrad(int groups, const int *m_sizes_dev, int m_capacity, int n, int k,
                                            const void *dD, const void *A, void *dB, tkg_grad_type type, float alpha,
-                                           void *workspace, size_t workspace_bytes, cudaStream_t stream);
-size_t tkg_gemm_grouped_dev_bf16_wgrad_workspace_bytes(int groups);
+                                           cudaStream_t stream);
 
 /* Check builds.  `python -m dense_block_scaled_gb300.build --check` builds the
  * same library as libtkg_check.so with every kernel verifying its internal

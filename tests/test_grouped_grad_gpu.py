@@ -215,28 +215,17 @@ def test_sizes_written_on_the_stream_and_other_stream():
     assert torch.equal(dA, ref_dA) and torch.equal(dB, ref_dB)
 
 
-def test_back_to_back_with_one_workspace():
-    # each call's maps and counts are its own although the workspace is shared
+def test_back_to_back():
+    # each call's counts are its own
     ps = [Groups(s, 72, 136, spare=20, seed=i) for i, s in enumerate([[10, 90, 0], [0, 1, 64], [33, 33, 33]])]
-    want = [check_wgrad(p) for p in ps]
-    ws = torch.empty(tkg.gemm_grouped_dev_bf16_wgrad_workspace_bytes(3), dtype=torch.uint8, device="cuda")
-    outs = [torch.full_like(w, GUARD) for w in want]
+    want = [(check_dgrad(p), check_wgrad(p)) for p in ps]
+    outs = [(torch.full_like(a, GUARD), torch.full_like(b, GUARD)) for a, b in want]
     for _ in range(5):
-        for p, o in zip(ps, outs):
-            tkg.gemm_grouped_dev_bf16_wgrad(p.dev, p.dD, p.A, o, alpha=p.alpha, workspace=ws)
-    assert all(torch.equal(o, w) for o, w in zip(outs, want))
-
-
-def test_workspace_bounds():
-    p = Groups([10, 0, 90], 72, 136)
-    want = check_wgrad(p)
-    nbytes = tkg.gemm_grouped_dev_bf16_wgrad_workspace_bytes(3)
-    for fill in (0, 255):
-        room = torch.full((nbytes + 512,), fill, dtype=torch.uint8, device="cuda")
-        dB = torch.empty_like(want)
-        tkg.gemm_grouped_dev_bf16_wgrad(p.dev, p.dD, p.A, dB, alpha=p.alpha, workspace=room[256:256 + nbytes])
-        assert torch.equal(dB, want)
-        assert (room[:256] == fill).all() and (room[256 + nbytes:] == fill).all()
+        for p, (dA, dB) in zip(ps, outs):
+            tkg.gemm_grouped_dev_bf16_dgrad(p.dev, p.dD, p.B, dA, alpha=p.alpha)
+            tkg.gemm_grouped_dev_bf16_wgrad(p.dev, p.dD, p.A, dB, alpha=p.alpha)
+    for got, ref in zip(outs, want):
+        assert torch.equal(got[0], ref[0]) and torch.equal(got[1], ref[1])
 
 
 def test_offsets_past_32_bits():
@@ -280,9 +269,6 @@ def test_refusals():
         tkg.gemm_grouped_dev_bf16_wgrad(p.dev, p.dD, p.A, dB, accumulate=True)
     with pytest.raises(ValueError):
         tkg.gemm_grouped_dev_bf16_wgrad(p.dev, p.dD, p.A[:5], dB)
-    with pytest.raises(tkg.TkgError) as e:
-        tkg.gemm_grouped_dev_bf16_wgrad(p.dev, p.dD, p.A, dB, workspace=torch.empty(8, dtype=torch.uint8, device="cuda"))
-    assert e.value.status == tkg.ERR_INVALID_ARG
     with pytest.raises(tkg.TkgError) as e:   # 60 columns
         tkg.gemm_grouped_dev_bf16_dgrad(p.dev, p.dD[:, :60].contiguous(), p.B[:, :60].contiguous(), dA)
     assert e.value.status == tkg.ERR_ALIGNMENT

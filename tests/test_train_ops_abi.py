@@ -84,8 +84,8 @@ def test_grouped_arguments(lib):
     def dgrad(groups=2, sizes=P, cap=8, n=64, k=64, dD=P, B=P, dA=P):
         return lib.tkg_gemm_grouped_dev_bf16_dgrad(groups, sizes, cap, n, k, dD, B, dA, 1.0, None)
 
-    def wgrad(groups=2, sizes=P, cap=8, n=64, k=64, dD=P, A=P, dB=P, kind=0, ws=P, nbytes=BIG):
-        return lib.tkg_gemm_grouped_dev_bf16_wgrad(groups, sizes, cap, n, k, dD, A, dB, kind, 1.0, ws, nbytes, None)
+    def wgrad(groups=2, sizes=P, cap=8, n=64, k=64, dD=P, A=P, dB=P, kind=0):
+        return lib.tkg_gemm_grouped_dev_bf16_wgrad(groups, sizes, cap, n, k, dD, A, dB, kind, 1.0, None)
 
     for call in (dgrad, wgrad):
         for bad in (dict(groups=0), dict(sizes=None), dict(cap=-1), dict(n=-8), dict(k=-8), dict(dD=None)):
@@ -97,9 +97,6 @@ def test_grouped_arguments(lib):
     assert dgrad(B=ODD) == dgrad(dA=ODD) == tkg.ERR_ALIGNMENT
     assert dgrad(n=0) == tkg.ERR_UNSUPPORTED
     assert dgrad(cap=0, dD=None) == dgrad(k=0, dA=None) == tkg.OK
-    assert wgrad(A=None) == wgrad(dB=None) == wgrad(kind=3) == wgrad(ws=None) == tkg.ERR_INVALID_ARG
-    need = lib.tkg_gemm_grouped_dev_bf16_wgrad_workspace_bytes(2)
-    assert need > 0 and wgrad(nbytes=need - 1) == tkg.ERR_INVALID_ARG
-    assert wgrad(A=ODD) == wgrad(dB=ODD) == wgrad(ws=ODD) == tkg.ERR_ALIGNMENT
+    assert wgrad(A=None) == wgrad(dB=None) == wgrad(kind=3) == tkg.ERR_INVALID_ARG
+    assert wgrad(A=ODD) == wgrad(dB=ODD) == tkg.ERR_ALIGNMENT
     assert wgrad(n=0, dB=None) == wgrad(k=0, dB=None) == wgrad(cap=0, kind=2) == tkg.OK
-    assert lib.tkg_gemm_grouped_dev_bf16_wgrad_workspace_bytes(129) == 0
