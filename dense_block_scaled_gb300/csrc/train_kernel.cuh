@@ -24,7 +24,11 @@
 // Roles (one CTA per SM; the two CTAs of a cluster share one MMA of 256 x N),
 // the bounded waits and the abort protocol are those of gemm_kernel.cuh:
 //   warp 0 TMA producer, warp 1 MMA issuer, warp 2 tensor-memory allocation and
-//   the cluster-launch-control tile scheduler, warps 4-11 epilogue.
+//   the cluster-launch-control tile scheduler, warp 3 the producer of the stages
+//   in which a group of k ends (and the group table), warps 4-19 epilogue: 16,
+//   as the cross-entropy epilogues are bound by latency (with 8 warps they took
+//   8000 cycles for a 256 x 256 tile, twice its MMAs at hidden = 512, at 40% of
+//   the issue slots).
 // Two 256-column accumulators: a tile's epilogue overlaps the next tile's MMAs.
 // The ring takes as many stages as fit: 6 for 256-wide tiles, up to 12 where few
 // tokens leave most of a stage to the weights (bytes in flight are what a
@@ -197,23 +201,26 @@ constexpr int kTrainMaxStages = 12;
 
 template <bool A_MN, bool B_MN, int EPI, int GRP>
 struct TrainConfig {
-  static constexpr int kThreads = 384;
-  static constexpr int kEpiWarps = 8;
+  static constexpr int kEpiWarps = 16;
+  static constexpr int kThreads = 32 * (4 + kEpiWarps);
   static constexpr int kAcc = 2;
   static constexpr int kABytes = 128 * 128;
   static constexpr int kEpiBufBytes = 32 * 64;      // 32 rows x 32 BF16 (or 16 FP32)
-  // LOSS: two buffers of (maximum, sum) per quadrant and column; others: two staging boxes per warp
-  static constexpr int kEpiBytes = EPI == EPI_LOSS ? 2 * 4 * kTrainBN * 8 : kEpiWarps * 2 * kEpiBufBytes;
-  static constexpr int kNumBars = 2 * kTrainMaxStages + 2 * kAcc + 2 + 4 + 2;
-  // groups by rank: first tile, first row and rows, the tile count, and the group (a byte each)
-  static constexpr int kTabInts = GRP != GRP_NONE ? 3 * kMaxGroups + 1 + kMaxGroups / 4 : 0;
+  // LOSS: two buffers of (maximum, sum) per quadrant and column; others: a staging box per warp
+  static constexpr int kEpiBytes = EPI == EPI_LOSS ? 2 * 4 * kTrainBN * 8 : kEpiWarps * kEpiBufBytes;
+  static constexpr int kTailBars = GRP == GRP_K ? kTrainMaxStages : 0;
+  static constexpr int kNumBars = 2 * kTrainMaxStages + 2 * kAcc + 2 + 4 + 4 + kTailBars;
+  // groups by rank: first row, rows, the group (a byte each); GRP_ROWS: first tile, and the tile count
+  static constexpr int kTabInts =
+      GRP == GRP_NONE ? 0 : 2 * kMaxGroups + kMaxGroups / 4 + (GRP == GRP_ROWS ? kMaxGroups + 1 : 0);
   // epilogue buffers, barriers, two scheduler answers, table, 1024-byte alignment; the rest is the ring's
   static constexpr int kFixedBytes = kEpiBytes + kNumBars * 8 + 2 * 16 + 16 + kTabInts * 4 + 1024;
   static constexpr int kSmemBytes = 232448 - 16;    // all an SM gives a block, less the two static words
   static constexpr int kRingBytes = (kSmemBytes - kFixedBytes) / 1024 * 1024;
   static_assert(kRingBytes >= 6 * 2 * kABytes, "six stages of 256-wide tiles");
   static constexpr bool kClc = GRP != GRP_ROWS;     // GRP_ROWS: the tile count is known on the device only
-  static constexpr int kClcConsumers = 2 * (1 + kEpiWarps) + 2;
+  // readers of a scheduler answer: producer (GRP_K: two) and epilogue warps per CTA, MMA issuer and scheduler
+  static constexpr int kClcConsumers = 2 * ((GRP == GRP_K ? 2 : 1) + kEpiWarps) + 2;
   static constexpr uint32_t kIdesc = idesc_f16(256, kTrainBN) | (A_MN ? 1u << 15 : 0u) | (B_MN ? 1u << 16 : 0u);
 };
 
@@ -236,7 +243,7 @@ struct TrainTile {
 };
 
 template <bool A_MN, bool B_MN, int EPI, int GRP>
-__global__ void __launch_bounds__(384, 1)
+__global__ void __launch_bounds__(640, 1)
     train_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                  const __grid_constant__ CUtensorMap tmD, const TrainParams p,
                  const __grid_constant__ std::conditional_t<GRP == GRP_K, TailMaps, NoTail> tail) {
@@ -268,12 +275,13 @@ __global__ void __launch_bounds__(384, 1)
   const uint32_t never_bar = drain_bar + 8;
   auto clc_full = [&](uint32_t i) { return never_bar + 8u + 8u * i; };
   auto clc_empty = [&](uint32_t i) { return never_bar + 24u + 8u * i; };
-  auto stat_bar = [&](uint32_t h) { return never_bar + 40u + 8u * h; };   // LOSS: a half's four warps have written
-  auto clc_resp = [&](uint32_t i) { return ((never_bar + 56u + 15u) & ~15u) + 16u * i; };
+  auto stat_bar = [&](uint32_t h) { return never_bar + 40u + 8u * h; };   // LOSS: a quarter's four warps have written
+  auto tail_go = [&](uint32_t s) { return never_bar + 72u + 8u * s; };     // GRP_K: stage s is warp 3's to fill
+  auto clc_resp = [&](uint32_t i) { return ((never_bar + 72u + 8u * uint32_t(C::kTailBars) + 15u) & ~15u) + 16u * i; };
   int* s_tab = reinterpret_cast<int*>(smem_raw + (clc_resp(2) - raw));
   float2* s_stat = reinterpret_cast<float2*>(smem_raw + (epi_base - raw));   // LOSS: [buffer][quadrant][column]
-  enum : int { kTabRow0 = kMaxGroups + 1, kTabRows = 2 * kMaxGroups + 1 };
-  [[maybe_unused]] uint8_t* s_group = reinterpret_cast<uint8_t*>(s_tab + 3 * kMaxGroups + 1);
+  enum : int { kTabRow0 = 0, kTabRows = kMaxGroups, kTabGroup = 2 * kMaxGroups, kTabTile = kTabGroup + kMaxGroups / 4 };
+  [[maybe_unused]] uint8_t* s_group = reinterpret_cast<uint8_t*>(s_tab + kTabGroup);
 
   auto coords = [&](int t) {
     TrainTile tc;
@@ -283,10 +291,10 @@ __global__ void __launch_bounds__(384, 1)
 #pragma unroll 1
       while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
-        if (s_tab[mid] <= t) lo = mid; else hi = mid;
+        if (s_tab[kTabTile + mid] <= t) lo = mid; else hi = mid;
       }
       const int rows = s_tab[kTabRows + lo], row0 = s_tab[kTabRow0 + lo];
-      tile_coords(t - s_tab[lo], p.tiles_m, (rows + kTrainBN - 1) / kTrainBN, p.raster_group, tc.mb, tc.nb);
+      tile_coords(t - s_tab[kTabTile + lo], p.tiles_m, (rows + kTrainBN - 1) / kTrainBN, p.raster_group, tc.mb, tc.nb);
       tc.nt = train_n_tile(rows, 16);
       tc.n0 = row0 + tc.nb * tc.nt;
       tc.n_end = min(tc.n0 + tc.nt, row0 + rows);
@@ -326,6 +334,7 @@ __global__ void __launch_bounds__(384, 1)
     for (uint32_t s = 0; s < nstages; ++s) {
       ptx::mbar_init(full_bar(s), 1);
       ptx::mbar_init(empty_bar(s), 1);
+      if (GRP == GRP_K) ptx::mbar_init(tail_go(s), 1);
     }
     for (uint32_t a = 0; a < uint32_t(ACC); ++a) {
       ptx::mbar_init(accf_bar(a), 1);
@@ -336,8 +345,8 @@ __global__ void __launch_bounds__(384, 1)
     for (uint32_t i = 0; i < 2; ++i) {
       ptx::mbar_init(clc_full(i), 1);
       ptx::mbar_init(clc_empty(i), C::kClcConsumers);
-      ptx::mbar_init(stat_bar(i), 4);
     }
+    for (uint32_t i = 0; i < 4; ++i) ptx::mbar_init(stat_bar(i), 4);
     ptx::fence_mbar_init();
     ptx::prefetch_tmap(&tmA);
     ptx::prefetch_tmap(&tmB);
@@ -360,8 +369,9 @@ __global__ void __launch_bounds__(384, 1)
   if constexpr (GRP != GRP_NONE) {
     ptx::pdl_wait();
     // Row ranges: sums stop at the capacity, so that rows past it are cut off and nothing leaves 32 bits.
-    // s_tab[0 .. groups): where each group ends, for now.  The sizes may have been cached by this SM before the
+    // s_end: where each group ends (in the epilogue's buffers, not in use yet).  The sizes may have been cached by this SM before the
     // previous grid wrote them: they are read through L2.
+    int* s_end = reinterpret_cast<int*>(smem_raw + (epi_base - raw));
     const int g = threadIdx.x;
     if (warp == 3) {
       const uint32_t cap = uint32_t(GRP == GRP_ROWS ? p.n : p.k);
@@ -375,7 +385,7 @@ __global__ void __launch_bounds__(384, 1)
           if (lane >= o) sr = min(sr + x, cap);
         }
         sr = min(sr + carry, cap);
-        if (g0 + lane < p.groups) s_tab[g0 + lane] = int(sr);
+        if (g0 + lane < p.groups) s_end[g0 + lane] = int(sr);
         carry = __shfl_sync(0xffffffffu, sr, 31);
       }
     }
@@ -383,11 +393,11 @@ __global__ void __launch_bounds__(384, 1)
     // Places by falling cost of a tile (GRP_ROWS its width, GRP_K its rows): the dear ones go out first, and
     // what is left at the end is small
     if (g < p.groups) {
-      const int row0 = g ? s_tab[g - 1] : 0, rows = s_tab[g] - row0;
+      const int row0 = g ? s_end[g - 1] : 0, rows = s_end[g] - row0;
       const int mine = GRP == GRP_ROWS ? train_n_tile(rows, 16) : rows;
       int place = 0;
       for (int o = 0, before = 0; o < p.groups; ++o) {
-        const int end = s_tab[o];
+        const int end = s_end[o];
         const int other = GRP == GRP_ROWS ? train_n_tile(end - before, 16) : end - before;
         place += (other > mine || (other == mine && o < g)) ? 1 : 0;
         before = end;
@@ -410,13 +420,13 @@ __global__ void __launch_bounds__(384, 1)
             const int x = __shfl_up_sync(0xffffffffu, tl, o);
             if (lane >= o) tl += x;
           }
-          if (g0 + lane < p.groups) s_tab[g0 + lane] = carry + tl - mine;
+          if (g0 + lane < p.groups) s_tab[kTabTile + g0 + lane] = carry + tl - mine;
           carry += __shfl_sync(0xffffffffu, tl, 31);
         }
-        if (lane == 0) s_tab[p.groups] = carry;
+        if (lane == 0) s_tab[kTabTile + p.groups] = carry;
       }
       __syncthreads();
-      num_tiles = s_tab[p.groups];
+      num_tiles = s_tab[kTabTile + p.groups];
     }
   }
 
@@ -503,26 +513,7 @@ __global__ void __launch_bounds__(384, 1)
                             (!B_MN || tc.b0 % 8 == 0) && tc.nt >= 16 && tc.nt <= kTrainBN,
                         p.status)) {
             if (GRP == GRP_K && last < 64) {
-              // The group's last rows, and zeros (rows past the capacity) up to the MMA's 16: what follows in
-              // memory is the next group's and may hold anything.  Boxes of 16, 4 and 1 rows; the 128-byte
-              // swizzle goes by the shared-memory address, so a box may start at any row of a chunk.
-              if constexpr (GRP == GRP_K) {
-                const int up = (last + 15) & ~15;
-                int r = 0;
-#pragma unroll 1
-                while (r < up) {
-                  const int left = (r < last ? last : up) - r;
-                  const int i = left >= 16 ? 0 : (left >= 4 ? 1 : 2);
-                  const int y = r < last ? tc.k0 + k0 + r : p.k;
-#pragma unroll
-                  for (int c = 0; c < 2; ++c) {
-                    const uint32_t at = uint32_t(c * kTrainChunk + r * 128);
-                    ptx::tma_load_2d<CG>(stage_a(stage) + at, &tail.a[i], tc.a0 + c * 64, y, fb, pol_a);
-                    ptx::tma_load_2d<CG>(stage_b(stage) + at, &tail.b[i], tc.b0 + c * 64, y, fb, pol_b);
-                  }
-                  r += i == 0 ? 16 : (i == 1 ? 4 : 1);
-                }
-              }
+              ptx::mbar_arrive(tail_go(stage));   // the stage is free and armed: warp 3 loads it
             } else {
             if constexpr (A_MN) {
 #pragma unroll
@@ -635,6 +626,54 @@ __global__ void __launch_bounds__(384, 1)
     }
     __syncwarp();
   }
+  // ------------------------------------------------------------------ producer of the stages where groups end
+  // The group's last rows, and zeros (rows past the capacity) up to the MMA's 16: what follows in memory is the
+  // next group's and may hold anything.  Boxes of 16, 4 and 1 rows, up to 40 copies a stage, beside the main
+  // producer, which goes on with the next tile (8 experts of 2048 rows, 4096 x 7168: 616 us with one producer).
+  // The 128-byte swizzle goes by the shared-memory address, so a box may start at any row of a chunk.
+  else if (warp == 3) {
+    if constexpr (GRP == GRP_K) {
+      if (ptx::elect_one()) {
+        const uint64_t pol = ptx::policy_evict_normal();
+        const uint32_t lead_full0 = ptx::map_to_rank(full_bar(0), 0);
+        uint32_t stage = 0;
+        uint32_t turns = 0;   // parity of each stage's next hand-over
+        bool ok = true;
+        uint32_t cslot = 0, cphase = 0;
+#pragma unroll 1
+        for (int t = first_tile; t >= 0 && ok;) {
+          const TrainTile tc = coords(t);
+          stage = (stage + uint32_t(tc.k_end >> 6)) % nstages;   // past the tile's whole stages
+          const int last = tc.k_end & 63;
+          if (last) {
+            // (a stage is handed over again only after this load has been consumed)
+            if (!wait_bar<false>(tail_go(stage), (turns >> stage) & 1u, ctl)) break;
+            turns ^= 1u << stage;
+            const uint32_t fb = lead_full0 + 8u * stage;
+            const int y0 = tc.k0 + tc.k_end - last, up = (last + 15) & ~15;
+            int r = 0;
+#pragma unroll 1
+            while (r < up) {
+              const int left = (r < last ? last : up) - r;
+              const int i = left >= 16 ? 0 : (left >= 4 ? 1 : 2);
+              const int y = r < last ? y0 + r : p.k;
+#pragma unroll
+              for (int c = 0; c < 2; ++c) {
+                const uint32_t off = uint32_t(c * kTrainChunk + r * 128);
+                ptx::tma_load_2d<CG>(stage_a(stage) + off, &tail.a[i], tc.a0 + c * 64, y, fb, pol);
+                ptx::tma_load_2d<CG>(stage_b(stage) + off, &tail.b[i], tc.b0 + c * 64, y, fb, pol);
+              }
+              r += i == 0 ? 16 : (i == 1 ? 4 : 1);
+            }
+            if (++stage == nstages) stage = 0;
+          }
+          t = next_tile(Lane{}, t, cslot, cphase);
+          if (t == -2) ok = false;
+        }
+      }
+      __syncwarp();
+    }
+  }
   // ------------------------------------------------------------------ tile scheduler
   else if (warp == 2) {
     if constexpr (C::kClc) {
@@ -676,25 +715,23 @@ __global__ void __launch_bounds__(384, 1)
   else if (warp >= 4) {
     const int e = warp - 4;
     const int q = warp & 3;              // accumulator lane quadrant this warp may read
-    const int h = e >> 2;                // first or second half of the tile's 32-column chunks
-    const uint32_t my_buf0 = epi_base + uint32_t(e * 2 * C::kEpiBufBytes);
+    const int h = e >> 2;                // quarter of the tile's 32-column chunks: 2 h and 2 h + 1
+    const uint32_t my_buf = epi_base + uint32_t(e * C::kEpiBufBytes);
     const uint32_t acce_lead0 = ptx::map_to_rank(acce_bar(0), 0);
     if (GRP == GRP_NONE) ptx::pdl_wait();
     const float alpha = p.scale ? p.alpha * __ldcg(p.scale) : p.alpha;
     uint32_t acc = 0, accph = 0;
     uint32_t cslot = 0, cphase = 0;
-    uint32_t turn = 0;                   // staging boxes (LOSS: tiles) so far
-    // a 2 KB staging box: wait until the store that used it last has read it, fill, send
+    [[maybe_unused]] uint32_t turn = 0;  // LOSS: tiles so far
+    // the warp's 2 KB staging box: wait until the store that used it last has read it, fill, send
     auto stage_box = [&](auto&& fill, auto&& send) {
-      const uint32_t buf = my_buf0 + (turn & 1u) * uint32_t(C::kEpiBufBytes);
-      ++turn;
-      if (lane == 0) ptx::bulk_wait_group_read<1>();
+      if (lane == 0) ptx::bulk_wait_group_read<0>();
       __syncwarp();
-      fill(buf);
+      fill(my_buf);
       ptx::fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) {
-        send(buf);
+        send(my_buf);
         ptx::bulk_commit_group();
       }
     };
@@ -707,40 +744,55 @@ __global__ void __launch_bounds__(384, 1)
         ptx::st_shared_v4(row_addr + chunk * 16u, w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
       }
     };
+    // Cross entropy: of the tile's columns col0 + 32 c + lane, the labels (-1: ignored, or no such column) and
+    // for DLOGITS lse in base 2; read one tile ahead
+    int label[2] = {-1, -1}, label_next[2] = {-1, -1};
+    float l2[2] = {0.f, 0.f}, l2_next[2] = {0.f, 0.f};
+    auto read_columns = [&](int t, int (&lab)[2], float (&ls)[2]) {
+      if constexpr (EPI == EPI_LOSS || EPI == EPI_DLOGITS) {
+        const TrainTile tc = coords(t);
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          const int col = tc.n0 + h * 64 + c * 32 + lane;
+          lab[c] = -1;
+          if (col < tc.n_end) {
+            const long long y = __ldcg(p.labels + col);
+            lab[c] = (y >= 0 && y < p.vocab) ? int(y) : -1;
+            if constexpr (EPI == EPI_DLOGITS) ls[c] = __ldcg(p.lse + col);
+          }
+        }
+      }
+    };
+    if (first_tile >= 0) read_columns(first_tile, label_next, l2_next);
 #pragma unroll 1
     for (int t = first_tile; t >= 0;) {
       const TrainTile tc = coords(t);
-      const int nchunks = (tc.nt + 31) >> 5;
-      const int first = h ? (nchunks + 1) >> 1 : 0;                        // this warp's chunks
-      const int nch = h ? nchunks >> 1 : (nchunks + 1) >> 1;
+      const int t_next = __shfl_sync(0xffffffffu, next_tile(Warp{}, t, cslot, cphase), 0);
+      if (t_next == -2) break;
+      const int nch = min(max(((tc.nt + 31) >> 5) - 2 * h, 0), 2);         // this warp's chunks
       const int row0 = tc.a0 + q * 32;                                     // its rows of D
-      const int col0 = tc.n0 + first * 32;                                 // and its first column
-      // Cross entropy: per chunk, of column col0 + 32 c + lane: its label's distance from row0, and for
-      // DLOGITS lse in base 2 and which columns are ignored (uniform masks)
-      int off[4];
-      uint32_t hits[4], gone[4];
-      float l2[4];
+      const int col0 = tc.n0 + h * 64;                                     // and its first column
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        label[c] = label_next[c];
+        l2[c] = l2_next[c] * 1.4426950408889634f;
+      }
+      if (t_next >= 0) read_columns(t_next, label_next, l2_next);
+      // per chunk, uniform masks: columns whose label is among this warp's rows (off: which), ignored columns
+      int off[2];
+      uint32_t hits[2], gone[2];
       if constexpr (EPI == EPI_LOSS || EPI == EPI_DLOGITS) {
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          const int col = col0 + c * 32 + lane;
-          const bool there = c < nch && col < tc.n_end;
-          const long long y = there ? __ldcg(p.labels + col) : -1;
-          const long long d = y - (long long)(p.vocab0) - row0;
-          const bool kept = y >= 0 && y < p.vocab;
-          const bool hit = kept && d >= 0 && d < 32 && row0 + int(d) < p.m;
-          off[c] = hit ? int(d) : -1;
-          hits[c] = __ballot_sync(0xffffffffu, hit);
-          if constexpr (EPI == EPI_DLOGITS) {
-            l2[c] = there ? __ldcg(p.lse + col) * 1.4426950408889634f : 0.f;
-            gone[c] = __ballot_sync(0xffffffffu, there && !kept);
-          }
+        for (int c = 0; c < 2; ++c) {
+          off[c] = label[c] - p.vocab0 - row0;
+          hits[c] = __ballot_sync(0xffffffffu, label[c] >= 0 && off[c] >= 0 && off[c] < 32 && row0 + off[c] < p.m);
+          gone[c] = __ballot_sync(0xffffffffu, label[c] < 0);
         }
       }
       if (!wait_bar_warp<false>(accf_bar(acc), accph, ctl)) break;
       ptx::tc_fence_after();
-      const bool idle = !invariant(acc < uint32_t(ACC) && t < num_tiles && first * 32 + nch * 32 <= kTrainBN, p.status);
-      const uint32_t tbase = tmem + (uint32_t(q * 32) << 16) + acc * uint32_t(kTrainBN) + uint32_t(first * 32);
+      const bool idle = !invariant(acc < uint32_t(ACC) && t < num_tiles && tc.nt <= kTrainBN, p.status);
+      const uint32_t tbase = tmem + (uint32_t(q * 32) << 16) + acc * uint32_t(kTrainBN) + uint32_t(h * 64);
       auto hand_back = [&]() {   // every load of this tile has completed
         ptx::tc_fence_before();
         __syncwarp();
@@ -756,29 +808,25 @@ __global__ void __launch_bounds__(384, 1)
         }
       };
       if constexpr (EPI == EPI_LOSS) {
-        float2* stat = s_stat + (turn & 1u) * uint32_t(4 * kTrainBN) + first * 32;
+        float2* stat = s_stat + (turn & 1u) * uint32_t(4 * kTrainBN) + h * 64;
         const uint32_t stat_phase = (turn & 1u);
         ++turn;
         const float c2 = fabsf(p.c2);
         const int rows_there = p.m - row0 - (lane >> 2);   // of rows 0, 8, 16, 24 past this lane's first
+        const bool edge = row0 + 32 > p.m;
         const int n = idle ? 0 : nch;
-        // chunk c in v[c & 1]: rows of the lower 16 lanes in the first half, of the upper 16 in the second
-        uint32_t v[2][32];
-        auto load = [&](int c, uint32_t (&r)[32]) {
-          ptx::tmem_ld_16x256b_x4<0>(tbase + uint32_t(c * 32), r);
-          ptx::tmem_ld_16x256b_x4<16>(tbase + (16u << 16) + uint32_t(c * 32), r);
-        };
-        if (n > 0) load(0, v[0]);
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          if (c >= n) continue;
-          ptx::tmem_ld_wait_for(v[c & 1]);
-          if (c + 1 < n) load(c + 1, v[(c + 1) & 1]);
+#pragma unroll 1
+        for (int c = 0; c < n; ++c) {
+          // rows of the lower 16 lanes in the first half of v, of the upper 16 in the second
+          uint32_t v[32];
+          ptx::tmem_ld_16x256b_x4<0>(tbase + uint32_t(c * 32), v);
+          ptx::tmem_ld_16x256b_x4<16>(tbase + (16u << 16) + uint32_t(c * 32), v);
+          ptx::tmem_ld_wait_for(v);
           // labels among these 32 rows: about one column in vocab / 32
 #pragma unroll 1
-          for (uint32_t left = hits[c]; left; left &= left - 1) {
+          for (uint32_t left = c ? hits[1] : hits[0]; left; left &= left - 1) {
             const int j = __ffs(int(left)) - 1;
-            const int row = __shfl_sync(0xffffffffu, off[c], j);
+            const int row = __shfl_sync(0xffffffffu, c ? off[1] : off[0], j);
             uint32_t z = ptx::tmem_ld_32x32b_x1(tbase + uint32_t(c * 32 + j));
             asm volatile("tcgen05.wait::ld.sync.aligned;" : "+r"(z)::"memory");
             if (lane == row) p.zlabel[col0 + c * 32 + j] = __uint_as_float(z) * alpha;
@@ -789,12 +837,14 @@ __global__ void __launch_bounds__(384, 1)
           // x[4 i + 2 k + e]: column 8 i + 2 (t % 4) + e, row t / 4 + 8 k (k = 0, 1), and 16 more (k = 2, 3)
           float x[32];
 #pragma unroll
-          for (int j = 0; j < 32; ++j) x[j] = __uint_as_float(v[c & 1][j]);
+          for (int j = 0; j < 32; ++j) x[j] = __uint_as_float(v[j]);
           if (p.c2 < 0.f) {
+            asm volatile("");   // (a branch, not 32 selects)
 #pragma unroll
             for (int j = 0; j < 32; ++j) x[j] = -x[j];
           }
-          if (rows_there <= 24) {   // rows past the vocabulary's end
+          if (edge) {   // rows past the vocabulary's end
+            asm volatile("");
 #pragma unroll
             for (int j = 0; j < 32; ++j)
               if (((j >> 1) & 1) * 8 + (j >> 4) * 16 >= rows_there) x[j] = -INFINITY;
@@ -814,10 +864,10 @@ __global__ void __launch_bounds__(384, 1)
             sum[i] = (ptx::ex2(fmaf(x[j], c2, -sub)) + ptx::ex2(fmaf(x[j + 2], c2, -sub))) +
                      (ptx::ex2(fmaf(x[j + 16], c2, -sub)) + ptx::ex2(fmaf(x[j + 18], c2, -sub)));
           }
-          if (c2 == 0.f && rows_there <= 24) {   // scale 0: 0 * -inf is not a number
+          if (c2 == 0.f && edge) {   // scale 0: 0 * -inf is not a number
 #pragma unroll
             for (int i = 0; i < 8; ++i)
-              sum[i] = float(rows_there > 0) + float(rows_there > 8) + float(rows_there > 16);
+              sum[i] = float(rows_there > 0) + float(rows_there > 8) + float(rows_there > 16) + float(rows_there > 24);
           }
           const float s = fold_columns(sum, lane, [](float a, float b) { return a + b; });
           stat[q * kTrainBN + c * 32 + column_of_lane(lane)] = make_float2(own == -INFINITY ? own : own * c2, s);
@@ -843,34 +893,37 @@ __global__ void __launch_bounds__(384, 1)
         }
       } else if constexpr (EPI == EPI_DLOGITS) {
         const int n = idle ? 0 : nch;
-        uint32_t v[2][32];
-        if (n > 0) ptx::tmem_ld_32x32b_x32(tbase, v[0]);
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          if (c >= n) continue;
+#pragma unroll 1
+        for (int c = 0; c < n; ++c) {
           const int col = col0 + c * 32;
-          ptx::tmem_ld_wait_for(v[c & 1]);
-          if (c + 1 < n) ptx::tmem_ld_32x32b_x32(tbase + uint32_t(c * 32 + 32), v[(c + 1) & 1]);
+          const uint32_t hit = c ? hits[1] : hits[0], none = c ? gone[1] : gone[0];
+          const float lse2 = c ? l2[1] : l2[0];
+          const int at = c ? off[1] : off[0];
+          uint32_t v[32];
+          ptx::tmem_ld_32x32b_x32(tbase + uint32_t(c * 32), v);
+          ptx::tmem_ld_wait_for(v);
           if (c + 1 == n) hand_back();
           if (col >= tc.n_end || row0 >= p.m) continue;
           float g[32];
 #pragma unroll
           for (int j = 0; j < 32; ++j)
-            g[j] = ptx::ex2(fmaf(__uint_as_float(v[c & 1][j]), p.c2, -__shfl_sync(0xffffffffu, l2[c], j)));
-          if (hits[c]) {
+            g[j] = ptx::ex2(fmaf(__uint_as_float(v[j]), p.c2, -__shfl_sync(0xffffffffu, lse2, j)));
+          if (hit) {
+            asm volatile("");   // (a branch, not 32 selects)
 #pragma unroll
             for (int j = 0; j < 32; ++j)
-              if (((hits[c] >> j) & 1u) && lane == __shfl_sync(0xffffffffu, off[c], j)) g[j] -= 1.f;
+              if (((hit >> j) & 1u) && lane == __shfl_sync(0xffffffffu, at, j)) g[j] -= 1.f;
           }
-          if (gone[c]) {   // whatever the logits and lse are there
+          if (none) {   // ignored tokens, whatever their logits and lse are (and columns that are not there)
+            asm volatile("");
 #pragma unroll
             for (int j = 0; j < 32; ++j)
-              if ((gone[c] >> j) & 1u) g[j] = 0.f;
+              if ((none >> j) & 1u) g[j] = 0.f;
           }
           uint32_t w[16];
 #pragma unroll
           for (int j = 0; j < 16; ++j) w[j] = ptx::pack_bf16x2(g[2 * j], g[2 * j + 1]);
-          if (first * 32 + c * 32 + 32 <= tc.nt) {
+          if (h * 64 + c * 32 + 32 <= tc.nt) {
             stage_box([&](uint32_t buf) { fill_rows(buf, w); },
                       [&](uint32_t buf) { ptx::tma_store_3d(&tmD, buf, col, row0, 0); });
           } else if (row0 + lane < p.m) {   // the tile ends after 16 columns of the chunk (a 32-byte sector)
@@ -881,27 +934,25 @@ __global__ void __launch_bounds__(384, 1)
         }
         if (n == 0) hand_back();
       } else {
-        uint32_t v[4][32];
-#pragma unroll
-        for (int c = 0; c < 4; ++c)
-          if (c < nch && !idle) ptx::tmem_ld_32x32b_x32(tbase + uint32_t(c * 32), v[c]);
-        ptx::tmem_ld_wait();
-        hand_back();
-        if (GRP == GRP_K && tc.nks == 0) {   // no rows: the sum is empty, the accumulator undefined
-#pragma unroll
-          for (int c = 0; c < 4; ++c)
-#pragma unroll
-            for (int j = 0; j < 32; ++j) v[c][j] = 0u;
-        }
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
+        const int n = idle ? 0 : nch;
+        const bool nothing = GRP == GRP_K && tc.nks == 0;   // no rows: the sum is empty, the accumulator undefined
+#pragma unroll 1
+        for (int c = 0; c < n; ++c) {
           const int col = col0 + c * 32;
-          if (c >= nch || idle || col >= tc.n_end || row0 >= p.m) continue;
+          uint32_t v[32];
+          ptx::tmem_ld_32x32b_x32(tbase + uint32_t(c * 32), v);
+          ptx::tmem_ld_wait_for(v);
+          if (c + 1 == n) hand_back();
+          if (col >= tc.n_end || row0 >= p.m) continue;
+          if (nothing) {
+#pragma unroll
+            for (int j = 0; j < 32; ++j) v[j] = 0u;
+          }
           if constexpr (EPI == EPI_BF16) {
             uint32_t w[16];
 #pragma unroll
             for (int j = 0; j < 16; ++j)
-              w[j] = ptx::pack_bf16x2(__uint_as_float(v[c][2 * j]) * alpha, __uint_as_float(v[c][2 * j + 1]) * alpha);
+              w[j] = ptx::pack_bf16x2(__uint_as_float(v[2 * j]) * alpha, __uint_as_float(v[2 * j + 1]) * alpha);
             stage_box([&](uint32_t buf) { fill_rows(buf, w); },
                       [&](uint32_t buf) { ptx::tma_store_3d(&tmD, buf, col, row0, GRP == GRP_K ? tc.z : 0); });
           } else if constexpr (EPI == EPI_BF16_T) {
@@ -909,7 +960,7 @@ __global__ void __launch_bounds__(384, 1)
             uint32_t w[16];
 #pragma unroll
             for (int j = 0; j < 16; ++j) {
-              const float x0 = __uint_as_float(v[c][2 * j]) * alpha, x1 = __uint_as_float(v[c][2 * j + 1]) * alpha;
+              const float x0 = __uint_as_float(v[2 * j]) * alpha, x1 = __uint_as_float(v[2 * j + 1]) * alpha;
               const float r = __shfl_xor_sync(0xffffffffu, (lane & 1) ? x0 : x1, 1);
               w[j] = (lane & 1) ? ptx::pack_bf16x2(r, x1) : ptx::pack_bf16x2(x0, r);
             }
@@ -941,13 +992,13 @@ __global__ void __launch_bounds__(384, 1)
               }
             }
           } else {
-            if (GRP == GRP_K && p.accumulate && tc.nks == 0) continue;   // adding nothing
+            if (nothing && p.accumulate) continue;   // adding nothing
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
-              if (first * 32 + c * 32 + half * 16 >= tc.nt || col + half * 16 >= tc.n_end) continue;
+              if (h * 64 + c * 32 + half * 16 >= tc.nt || col + half * 16 >= tc.n_end) continue;
               uint32_t w[16];
 #pragma unroll
-              for (int j = 0; j < 16; ++j) w[j] = __float_as_uint(__uint_as_float(v[c][half * 16 + j]) * alpha);
+              for (int j = 0; j < 16; ++j) w[j] = __float_as_uint(__uint_as_float(v[half * 16 + j]) * alpha);
               stage_box([&](uint32_t buf) { fill_rows(buf, w); },
                         [&](uint32_t buf) {
                           if (p.accumulate)
@@ -958,8 +1009,9 @@ __global__ void __launch_bounds__(384, 1)
             }
           }
         }
+        if (n == 0) hand_back();
       }
-      t = __shfl_sync(0xffffffffu, next_tile(Warp{}, t, cslot, cphase), 0);
+      t = t_next;
     }
     if (EPI != EPI_LOSS && lane == 0) ptx::bulk_wait_group_read<0>();
     __syncwarp();
