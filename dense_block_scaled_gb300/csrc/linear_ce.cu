@@ -32,125 +32,170 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
 // ---------------------------------------------------------------- joining the loss's parts
-// 32 tokens per block; warp w reads parts w, w + 32, ... of its 32 tokens (256
-// contiguous bytes a part), then the block's warps are joined in shared memory.
+// 8 tokens per block (64 contiguous bytes of a part) and 128 threads per token,
+// which read the parts in batches of 4 with the loads in flight together.
+constexpr int kJoinTokens = 8;
 __global__ void __launch_bounds__(1024)
     ce_join_kernel(int tokens, int vocab, int parts, const float2* __restrict__ part, const float* __restrict__ zlabel,
                    const long long* __restrict__ labels, float* __restrict__ loss, float* __restrict__ lse) {
-  __shared__ float s_top[32][33], s_sum[32][33];
+  __shared__ float2 s_part[32][kJoinTokens];
   ptx::pdl_launch_dependents();
   ptx::pdl_wait();
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
-  const int t = blockIdx.x * 32 + lane;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int t = blockIdx.x * kJoinTokens + (lane & 7);
   float top = -INFINITY, sum = 0.f;
+  auto join = [&](float m, float s) {
+    const float up = fmaxf(top, m);
+    const float base = fabsf(up) == INFINITY ? 0.f : up;   // no inf - inf
+    sum = sum * ptx::ex2(top - base) + s * ptx::ex2(m - base);
+    top = up;
+  };
   if (t < tokens) {
-#pragma unroll 4
-    for (int i = warp; i < parts; i += warps) {
-      const float2 x = __ldcg(part + size_t(i) * size_t(tokens) + t);
-      const float m = fmaxf(top, x.x);
-      const float base = fabsf(m) == INFINITY ? 0.f : m;   // no inf - inf
-      sum = sum * ptx::ex2(top - base) + x.y * ptx::ex2(x.x - base);
-      top = m;
+#pragma unroll 1
+    for (int i = threadIdx.x >> 3; i < parts; i += 512) {
+      float2 x[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        x[j] = i + 128 * j < parts ? __ldcg(part + size_t(i + 128 * j) * size_t(tokens) + t)
+                                   : make_float2(-INFINITY, 0.f);
+      const float up = fmaxf(fmaxf(x[0].x, x[1].x), fmaxf(x[2].x, x[3].x));
+      const float base = fabsf(up) == INFINITY ? 0.f : up;
+      float s = 0.f;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) s += x[j].y * ptx::ex2(x[j].x - base);
+      join(up, s);
     }
   }
-  s_top[warp][lane] = top;
-  s_sum[warp][lane] = sum;
+#pragma unroll
+  for (int o = 8; o < 32; o <<= 1) {
+    const float m = __shfl_xor_sync(0xffffffffu, top, o), s = __shfl_xor_sync(0xffffffffu, sum, o);
+    join(m, s);
+  }
+  if (lane < kJoinTokens) s_part[warp][lane] = make_float2(top, sum);
   __syncthreads();
-  if (warp == 0 && t < tokens) {
-    for (int w = 1; w < warps; ++w) {
-      const float m = fmaxf(top, s_top[w][lane]);
-      const float base = fabsf(m) == INFINITY ? 0.f : m;
-      sum = sum * ptx::ex2(top - base) + s_sum[w][lane] * ptx::ex2(s_top[w][lane] - base);
-      top = m;
+  if (warp == 0) {
+    // 4 lanes per token, 8 warps' results each
+    top = -INFINITY;
+    sum = 0.f;
+#pragma unroll
+    for (int w = 0; w < 8; ++w) join(s_part[(lane >> 3) * 8 + w][lane & 7].x, s_part[(lane >> 3) * 8 + w][lane & 7].y);
+#pragma unroll
+    for (int o = 8; o < 32; o <<= 1) {
+      const float m = __shfl_xor_sync(0xffffffffu, top, o), s = __shfl_xor_sync(0xffffffffu, sum, o);
+      join(m, s);
     }
-    const float l = (top + log2f(sum)) * kLn2;
-    const long long y = __ldcg(labels + t);
-    lse[t] = l;
-    loss[t] = (y >= 0 && y < vocab) ? l - __ldcg(zlabel + t) : 0.f;
+    if (lane < kJoinTokens && t < tokens) {
+      const float l = (top + log2f(sum)) * kLn2;
+      const long long y = __ldcg(labels + t);
+      lse[t] = l;
+      loss[t] = (y >= 0 && y < vocab) ? l - __ldcg(zlabel + t) : 0.f;
+    }
   }
 }
 
 // ---------------------------------------------------------------- rows of X with the tokens' weights
 // out_t = X_t c_t / s, s = max |c_t|, and s itself.  Rows of ignored tokens are
 // zeros whatever they hold: their g is 0, but 0 times a padded position's NaN is not.
-// Every block finds s again from the T weights (at most one block per SM: T x 12
-// bytes from L2 each, against one more launch).
-__global__ void __launch_bounds__(1024)
+// Every block finds s again from the T weights (T x 12 bytes from L2 for each of
+// at most two blocks per SM, against one more launch), then takes a row per warp.
+__global__ void __launch_bounds__(256)
     ce_rows_kernel(int tokens, int vocab, int hidden, const uint16_t* __restrict__ X, size_t ldx,
                    const long long* __restrict__ labels, const float* __restrict__ dloss, float alpha,
                    uint16_t* __restrict__ out, float* __restrict__ scale) {
-  __shared__ float s_max[32];
+  __shared__ float s_max[8];
   ptx::pdl_launch_dependents();
   ptx::pdl_wait();
   auto weight = [&](int t) {
     const long long y = __ldcg(labels + t);
-    return (y >= 0 && y < vocab) ? alpha * __ldcg(dloss + t) : 0.f;
+    const float d = __ldcg(dloss + t);
+    return (y >= 0 && y < vocab) ? alpha * d : 0.f;
   };
-  const int tid = threadIdx.x;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   float top = 0.f;
-  for (int t = tid; t < tokens; t += 1024) top = fmaxf(top, fabsf(weight(t)));
+#pragma unroll 8
+  for (int t = tid; t < tokens; t += 256) top = fmaxf(top, fabsf(weight(t)));
 #pragma unroll
   for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-  if ((tid & 31) == 0) s_max[tid >> 5] = top;
+  if (lane == 0) s_max[warp] = top;
   __syncthreads();
-  top = s_max[tid & 31];
+  top = s_max[lane & 7];
 #pragma unroll
-  for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+  for (int o = 4; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
   if (blockIdx.x == 0 && tid == 0) *scale = top;
-  // a warp per row
   const int vec = hidden / 8;
-  for (int t = blockIdx.x * 32 + (tid >> 5); t < tokens; t += gridDim.x * 32) {
+  for (int t = blockIdx.x * 8 + warp; t < tokens; t += gridDim.x * 8) {
     const long long y = __ldcg(labels + t);
     const bool kept = y >= 0 && y < vocab;
     const float w = top == 0.f ? 0.f : __fdiv_rn(weight(t), top);
     const uint4* src = reinterpret_cast<const uint4*>(X + size_t(t) * ldx);
     uint4* dst = reinterpret_cast<uint4*>(out + size_t(t) * size_t(hidden));
-#pragma unroll 4
-    for (int c = tid & 31; c < vec; c += 32) {
-      uint4 v = make_uint4(0, 0, 0, 0);
-      if (kept) {
-        v = __ldcg(src + c);
+    for (int c0 = lane; c0 < vec; c0 += 128) {
+      uint4 v[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        v[j] = kept && c0 + 32 * j < vec ? __ldcg(src + c0 + 32 * j) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
         if (w != 1.f) {
-          uint32_t* u = reinterpret_cast<uint32_t*>(&v);
+          uint32_t* u = reinterpret_cast<uint32_t*>(&v[j]);
 #pragma unroll
           for (int i = 0; i < 4; ++i)
             u[i] = ptx::pack_bf16x2(__uint_as_float(u[i] << 16) * w, __uint_as_float(u[i] & 0xffff0000u) * w);
         }
+        if (c0 + 32 * j < vec) dst[c0 + 32 * j] = v[j];
       }
-      dst[c] = v;
     }
   }
 }
 
 // ---------------------------------------------------------------- dX from its FP32 parts
-// Parts are [hidden][token] (pitch in elements); dX is [token][hidden].  A block
-// adds the parts of 32 tokens x 64 hidden, in order, turns them in shared memory
-// and multiplies by the tokens' weights.
+// Parts are [hidden][token] (pitch a multiple of 64); dX is [token][hidden].  A
+// block adds the parts of 64 tokens x 32 hidden, in order and four parts' loads in
+// flight together, turns them in shared memory and multiplies by the tokens' weights.
 __global__ void __launch_bounds__(256)
     ce_dx_kernel(int tokens, int vocab, int hidden, int parts, const float* __restrict__ part, size_t pitch,
                  const long long* __restrict__ labels, const float* __restrict__ dloss, float alpha,
                  uint16_t* __restrict__ dX, size_t lddx) {
-  __shared__ float s_t[64][33];
+  __shared__ float s_t[32][65];
   ptx::pdl_launch_dependents();
   ptx::pdl_wait();
-  const int t0 = blockIdx.x * 32, h0 = blockIdx.y * 64;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int t0 = blockIdx.x * 64, h0 = blockIdx.y * 32, tid = threadIdx.x;
+  const int tq = (tid & 15) * 4, hr = tid >> 4;   // four tokens, rows hr and hr + 16
+  const float* src = part + size_t(h0 + hr) * pitch + t0 + tq;
   const size_t part_len = size_t(hidden) * pitch;
-  float s[8] = {};
-  if (t0 + lane < tokens) {
-    for (int p = 0; p < parts; ++p) {
+  const bool row[2] = {h0 + hr < hidden, h0 + hr + 16 < hidden};
+  float4 s[2] = {};
+#pragma unroll 1
+  for (int p0 = 0; p0 < parts; p0 += 4) {
+    float4 x[4][2];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int hh = h0 + warp * 8 + i;
-        if (hh < hidden) s[i] += __ldcg(part + size_t(p) * part_len + size_t(hh) * pitch + t0 + lane);
+    for (int p = 0; p < 4; ++p)
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        x[p][i] = p0 + p < parts && row[i]
+                      ? __ldcg(reinterpret_cast<const float4*>(src + size_t(p0 + p) * part_len + size_t(i) * 16 * pitch))
+                      : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int p = 0; p < 4; ++p)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        s[i].x += x[p][i].x;
+        s[i].y += x[p][i].y;
+        s[i].z += x[p][i].z;
+        s[i].w += x[p][i].w;
       }
-    }
   }
 #pragma unroll
-  for (int i = 0; i < 8; ++i) s_t[warp * 8 + i][lane] = s[i];
+  for (int i = 0; i < 2; ++i) {
+    float* d = &s_t[hr + 16 * i][tq];
+    d[0] = s[i].x;
+    d[1] = s[i].y;
+    d[2] = s[i].z;
+    d[3] = s[i].w;
+  }
   __syncthreads();
-  // 8 lanes per token, 8 hidden (16 bytes) each
-  const int t = t0 + (threadIdx.x >> 3), hh = (threadIdx.x & 7) * 8;
+  // 4 threads per token, 8 hidden (16 bytes) each
+  const int t = t0 + (tid >> 2), hh = (tid & 3) * 8;
   if (t < tokens && h0 + hh < hidden) {
     const long long y = __ldcg(labels + t);
     const float w = alpha * __ldcg(dloss + t);
@@ -158,7 +203,7 @@ __global__ void __launch_bounds__(256)
     if (y >= 0 && y < vocab) {
 #pragma unroll
       for (int i = 0; i < 4; ++i)
-        o[i] = ptx::pack_bf16x2(s_t[hh + 2 * i][threadIdx.x >> 3] * w, s_t[hh + 2 * i + 1][threadIdx.x >> 3] * w);
+        o[i] = ptx::pack_bf16x2(s_t[hh + 2 * i][tid >> 2] * w, s_t[hh + 2 * i + 1][tid >> 2] * w);
     }
     *reinterpret_cast<uint4*>(dX + size_t(t) * lddx + h0 + hh) = make_uint4(o[0], o[1], o[2], o[3]);
   }
@@ -268,9 +313,8 @@ tkg_status tkg_linear_ce_loss(int tokens, int vocab, int hidden, const void* X, 
   p.zlabel = reinterpret_cast<float*>(static_cast<char*>(workspace) +
                                       round_up(size_t(parts) * size_t(tokens) * sizeof(float2), 256));
   if ((st = launch_ce_loss(X, size_t(ldx) * 2, W, size_t(ldw) * 2, p, stream)) != TKG_OK) return st;
-  const int warps = parts < 32 ? parts : 32;
-  return launch_small(ce_join_kernel, dim3(unsigned(ceil_div(tokens, 32))), dim3(unsigned(32 * warps)), stream, tokens,
-                      vocab, parts, p.part, p.zlabel, labels, loss, lse);
+  return launch_small(ce_join_kernel, dim3(unsigned(ceil_div(tokens, kJoinTokens))), dim3(1024), stream, tokens, vocab,
+                      parts, p.part, p.zlabel, labels, loss, lse);
 }
 
 size_t tkg_linear_ce_grad_workspace_bytes(int tokens, int vocab, int hidden, int piece) {
@@ -314,10 +358,12 @@ tkg_status tkg_linear_ce_grad(int tokens, int vocab, int hidden, const void* X, 
   float* scale = reinterpret_cast<float*>(ws + pl.scale_off);
   CUtensorMap tmA, tmB, tmD;
 
-  if (dW && (st = launch_small(ce_rows_kernel, dim3(unsigned(ceil_div(tokens, 32) < 2 * kPairs ? ceil_div(tokens, 32) : 2 * kPairs)),
-                               dim3(1024), stream, tokens, vocab, hidden, static_cast<const uint16_t*>(X), size_t(ldx),
-                               labels, dloss, alpha, rows, scale)) != TKG_OK)
-    return st;
+  if (dW) {
+    const int blocks = ceil_div(tokens, 8) < 4 * kPairs ? ceil_div(tokens, 8) : 4 * kPairs;
+    if ((st = launch_small(ce_rows_kernel, dim3(unsigned(blocks)), dim3(256), stream, tokens, vocab, hidden,
+                           static_cast<const uint16_t*>(X), size_t(ldx), labels, dloss, alpha, rows, scale)) != TKG_OK)
+      return st;
+  }
   for (int i = 0; i < pl.pieces; ++i) {
     const int v0 = i * pl.piece, nv = vocab - v0 < pl.piece ? vocab - v0 : pl.piece;
     const char* Wp = static_cast<const char*>(W) + size_t(v0) * size_t(ldw) * 2;
@@ -375,7 +421,7 @@ tkg_status tkg_linear_ce_grad(int tokens, int vocab, int hidden, const void* X, 
     }
   }
   if (!dX) return TKG_OK;
-  return launch_small(ce_dx_kernel, dim3(unsigned(ceil_div(tokens, 32)), unsigned(ceil_div(hidden, 64))), dim3(256),
+  return launch_small(ce_dx_kernel, dim3(unsigned(ceil_div(tokens, 64)), unsigned(ceil_div(hidden, 32))), dim3(256),
                       stream, tokens, vocab, hidden, pl.parts, part, pl.tokens_up, labels, dloss, alpha,
                       static_cast<uint16_t*>(dX), size_t(lddx));
 }
