@@ -36,13 +36,13 @@ tkg_status tkg_gemm_grouped_dev_bf16_dgrad(int groups, const int* m_sizes_dev, i
   if ((st = encode_2d(&tmB, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, dD, uint64_t(n), uint64_t(m_capacity), uint64_t(n) * 2, 64,
                       32, CU_TENSOR_MAP_SWIZZLE_128B)) != TKG_OK)
     return st;
-  if ((st = map_out(&tmD, dA, m_capacity, k, 1, size_t(k) * 2, size_t(m_capacity) * size_t(k) * 2, false, 16)) != TKG_OK)
+  if ((st = map_out(&tmD, dA, m_capacity, k, 1, size_t(k) * 2, size_t(m_capacity) * size_t(k) * 2, false, true)) != TKG_OK)
     return st;
   TrainParams p{};
   p.m = k;
   p.n = m_capacity;
   p.k = n;
-  p.n_tile = m_capacity < kTrainBN ? train_n_tile(m_capacity, 16) : kTrainBN;   // the widest there can be
+  p.n_tile = m_capacity < kTrainBN ? train_n_tile(m_capacity, kTileTokens) : kTrainBN;   // the widest there can be
   p.alpha = alpha;
   p.sizes = m_sizes_dev;
   p.groups = groups;
@@ -83,13 +83,21 @@ tkg_status tkg_gemm_grouped_dev_bf16_wgrad(int groups, const int* m_sizes_dev, i
   p.m = n;
   p.n = k;
   p.k = m_capacity;
-  p.n_tile = train_n_tile(k, 32);
   p.alpha = alpha;
   p.sizes = m_sizes_dev;
   p.groups = groups;
   p.accumulate = type == TKG_GRAD_F32_ADD;
-  if (type == TKG_GRAD_BF16) return launch_train<true, true, EPI_BF16, GRP_K>(tmA, tmB, tmD, p, stream, tail);
-  return launch_train<true, true, EPI_F32, GRP_K>(tmA, tmB, tmD, p, stream, tail);
+  if (type == TKG_GRAD_BF16) {
+    ExtraMaps<EPI_BF16, GRP_K> extra{};
+    static_cast<TailMaps&>(extra) = tail;
+    p.n_tile = train_n_tile(k, kTileBF16);
+    return launch_train<true, true, EPI_BF16, GRP_K>(tmA, tmB, tmD, p, stream, extra);
+  }
+  ExtraMaps<EPI_F32, GRP_K> extra{};
+  static_cast<TailMaps&>(extra) = tail;
+  if ((st = map_prefetch(&extra.d, dB, n, k, groups, size_t(k) * 4, size_t(n) * size_t(k) * 4)) != TKG_OK) return st;
+  p.n_tile = train_n_tile(k, kTileF32);
+  return launch_train<true, true, EPI_F32, GRP_K>(tmA, tmB, tmD, p, stream, extra);
 }
 
 }  // extern "C"

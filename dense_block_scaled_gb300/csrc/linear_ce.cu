@@ -386,7 +386,8 @@ tkg_status tkg_linear_ce_grad(int tokens, int vocab, int hidden, const void* X, 
       q.m = hidden;
       q.n = tokens;
       q.k = nv;
-      q.n_tile = train_n_tile(tokens, 16);
+      q.n_tile = train_n_tile(tokens, kTileF32);
+      q.prefetch_a = 1;
       q.alpha = 1.f;
       q.split_stages = ceil_div(ceil_div(nv, 64), pl.parts);
       q.splits = ceil_div(ceil_div(nv, 64), q.split_stages);
@@ -396,7 +397,11 @@ tkg_status tkg_linear_ce_grad(int tokens, int vocab, int hidden, const void* X, 
       if ((st = map_out(&tmD, part, hidden, tokens, pl.parts, pl.tokens_up * 4, size_t(hidden) * pl.tokens_up * 4,
                         true)) != TKG_OK)
         return st;
-      if ((st = launch_train<true, true, EPI_F32, GRP_NONE>(tmA, tmB, tmD, q, stream)) != TKG_OK) return st;
+      ExtraMaps<EPI_F32, GRP_NONE> extra{};
+      if ((st = map_prefetch(&extra.d, part, hidden, tokens, pl.parts, pl.tokens_up * 4,
+                             size_t(hidden) * pl.tokens_up * 4)) != TKG_OK)
+        return st;
+      if ((st = launch_train<true, true, EPI_F32, GRP_NONE>(tmA, tmB, tmD, q, stream, extra)) != TKG_OK) return st;
     }
     if (dW) {
       // rows [v0, v0 + nv) of dW = g (c / s X)
@@ -404,7 +409,7 @@ tkg_status tkg_linear_ce_grad(int tokens, int vocab, int hidden, const void* X, 
       q.m = nv;
       q.n = hidden;
       q.k = tokens;
-      q.n_tile = train_n_tile(hidden, 32);
+      q.n_tile = train_n_tile(hidden, es == 2 ? kTileBF16 : kTileF32);
       q.alpha = 1.f;
       q.scale = scale;
       q.splits = 1;
@@ -415,8 +420,15 @@ tkg_status tkg_linear_ce_grad(int tokens, int vocab, int hidden, const void* X, 
       if ((st = map_out(&tmD, static_cast<char*>(dW) + size_t(v0) * size_t(lddw) * es, nv, hidden, 1, size_t(lddw) * es,
                         size_t(nv) * size_t(lddw) * es, es == 4)) != TKG_OK)
         return st;
-      st = es == 2 ? launch_train<false, true, EPI_BF16, GRP_NONE>(tmA, tmB, tmD, q, stream)
-                   : launch_train<false, true, EPI_F32, GRP_NONE>(tmA, tmB, tmD, q, stream);
+      if (es == 2) {
+        st = launch_train<false, true, EPI_BF16, GRP_NONE>(tmA, tmB, tmD, q, stream);
+      } else {
+        ExtraMaps<EPI_F32, GRP_NONE> extra{};
+        if ((st = map_prefetch(&extra.d, static_cast<float*>(dW) + size_t(v0) * size_t(lddw), nv, hidden, 1,
+                               size_t(lddw) * 4, size_t(nv) * size_t(lddw) * 4)) != TKG_OK)
+          return st;
+        st = launch_train<false, true, EPI_F32, GRP_NONE>(tmA, tmB, tmD, q, stream, extra);
+      }
       if (st != TKG_OK) return st;
     }
   }

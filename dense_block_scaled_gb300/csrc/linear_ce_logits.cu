@@ -8,7 +8,8 @@ static tkg_status launch_logits(const void* X, size_t x_bytes, const void* W, si
                                 cudaStream_t stream) {
   CUtensorMap tmA, tmB, tmD;
   tkg_status st;
-  p.n_tile = train_n_tile(p.n, 16);
+  p.n_tile = train_n_tile(p.n, kTileTokens);
+  p.prefetch_a = 1;
   if ((st = map_k_major(&tmA, W, p.m, p.k, w_bytes, 128)) != TKG_OK) return st;
   if ((st = map_k_major(&tmB, X, p.n, p.k, x_bytes, p.n_tile / 2)) != TKG_OK) return st;
   tmD = tmA;

@@ -27,20 +27,29 @@ inline tkg_status map_mn_major(CUtensorMap* map, const void* base, int mn, int k
   return encode_2d(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, base, uint64_t(mn), uint64_t(k), row_bytes, 64,
                    box_rows ? uint32_t(box_rows) : mn_box_rows(k), CU_TENSOR_MAP_SWIZZLE_128B);
 }
-// Output: `parts` matrices of m x n, store boxes of 64 bytes by `rows` rows.
+// Output: `parts` matrices of m x n.  Store boxes of 16 rows by 128 bytes, or (turned: D's columns are the
+// output's rows) 16 rows by the 64 bytes of a warp's 32 rows of D.
 inline tkg_status map_out(CUtensorMap* map, const void* base, int m, int n, int parts, size_t row_bytes,
-                          size_t part_bytes, bool f32, int rows = 32) {
+                          size_t part_bytes, bool f32, bool turned = false) {
   return encode_3d_swizzled(map, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, base,
-                            uint64_t(n), uint64_t(m), uint64_t(parts), row_bytes, part_bytes, f32 ? 16 : 32,
-                            uint32_t(rows), 1, CU_TENSOR_MAP_SWIZZLE_64B);
+                            uint64_t(n), uint64_t(m), uint64_t(parts), row_bytes, part_bytes, f32 || turned ? 32 : 64, 16,
+                            1, turned ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B);
 }
+// The same matrices in the boxes that fetch what is added to into L2.
+inline tkg_status map_prefetch(CUtensorMap* map, const void* base, int m, int n, int parts, size_t row_bytes,
+                               size_t part_bytes) {
+  return encode_3d(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, base, uint64_t(n), uint64_t(m), uint64_t(parts), row_bytes,
+                   part_bytes, 256, 32, 1);
+}
+// Multiple that an output's tiles are wide: a store box's columns (turned: the MMA's 16).
+constexpr int kTileBF16 = 64, kTileF32 = 32, kTileTokens = 16;
 
 // Fills the fields common to every launch and launches.  The caller sets p.m, n,
 // k, n_tile, alpha, splits and split_stages (GRP_NONE) and the epilogue's own fields.
 template <bool A_MN, bool B_MN, int EPI, int GRP>
 tkg_status launch_train(const CUtensorMap& tmA, const CUtensorMap& tmB, const CUtensorMap& tmD, TrainParams p,
                         cudaStream_t stream,
-                        const std::conditional_t<GRP == GRP_K, TailMaps, NoTail>& tail = {}) {
+                        const ExtraMaps<EPI, GRP>& extra = {}) {
   using C = TrainConfig<A_MN, B_MN, EPI, GRP>;
   auto kern = train_kernel<A_MN, B_MN, EPI, GRP>;
   // more than half an SM's shared memory: no two CTAs share an SM (each takes all of tensor memory)
@@ -103,7 +112,7 @@ tkg_status launch_train(const CUtensorMap& tmA, const CUtensorMap& tmB, const CU
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  if (cudaLaunchKernelEx(&cfg, kern, tmA, tmB, tmD, p, tail) != cudaSuccess) {
+  if (cudaLaunchKernelEx(&cfg, kern, tmA, tmB, tmD, p, extra) != cudaSuccess) {
     cudaGetLastError();
     return TKG_ERR_CUDA;
   }

@@ -88,6 +88,7 @@ struct TrainParams {
   void* d;
   size_t ldd;
   int accumulate;              // F32
+  int prefetch_a;              // start fetching A before the dependency wait
   // groups
   const int* sizes;            // device
   int groups;
@@ -97,9 +98,17 @@ struct TrainParams {
 struct TailMaps {
   CUtensorMap a[3], b[3];
 };
-struct NoTail {
+// F32: D in boxes of 256 columns by 32 rows, to fetch into L2 what is about to be added to.
+struct PrefetchMap {
+  CUtensorMap d;
+};
+struct NoTail {};
+struct NoPrefetch {
   int unused;
 };
+template <int EPI, int GRP>
+struct ExtraMaps : std::conditional_t<GRP == GRP_K, TailMaps, NoTail>,
+                   std::conditional_t<EPI == EPI_F32, PrefetchMap, NoPrefetch> {};
 
 namespace ptx {
 __device__ __forceinline__ void tma_store_3d(const void* tmap, uint32_t src, int32_t x, int32_t y, int32_t z) {
@@ -246,7 +255,7 @@ template <bool A_MN, bool B_MN, int EPI, int GRP>
 __global__ void __launch_bounds__(640, 1)
     train_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                  const __grid_constant__ CUtensorMap tmD, const TrainParams p,
-                 const __grid_constant__ std::conditional_t<GRP == GRP_K, TailMaps, NoTail> tail) {
+                 const __grid_constant__ ExtraMaps<EPI, GRP> extra) {
   using C = TrainConfig<A_MN, B_MN, EPI, GRP>;
   constexpr int CG = 2;
   constexpr int ACC = C::kAcc;
@@ -372,6 +381,7 @@ __global__ void __launch_bounds__(640, 1)
     // s_end: where each group ends (in the epilogue's buffers, not in use yet).  The sizes may have been cached by this SM before the
     // previous grid wrote them: they are read through L2.
     int* s_end = reinterpret_cast<int*>(smem_raw + (epi_base - raw));
+    int* s_cost = s_end + kMaxGroups;
     const int g = threadIdx.x;
     if (warp == 3) {
       const uint32_t cap = uint32_t(GRP == GRP_ROWS ? p.n : p.k);
@@ -392,15 +402,17 @@ __global__ void __launch_bounds__(640, 1)
     __syncthreads();
     // Places by falling cost of a tile (GRP_ROWS its width, GRP_K its rows): the dear ones go out first, and
     // what is left at the end is small
+    const int row0 = g > 0 && g < p.groups ? s_end[g - 1] : 0;
+    const int rows = g < p.groups ? s_end[g] - row0 : 0;
+    const int cost = GRP == GRP_ROWS ? train_n_tile(rows, 16) : rows;
+    if (g < p.groups) s_cost[g] = cost;
+    __syncthreads();
     if (g < p.groups) {
-      const int row0 = g ? s_end[g - 1] : 0, rows = s_end[g] - row0;
-      const int mine = GRP == GRP_ROWS ? train_n_tile(rows, 16) : rows;
       int place = 0;
-      for (int o = 0, before = 0; o < p.groups; ++o) {
-        const int end = s_end[o];
-        const int other = GRP == GRP_ROWS ? train_n_tile(end - before, 16) : end - before;
-        place += (other > mine || (other == mine && o < g)) ? 1 : 0;
-        before = end;
+#pragma unroll 4
+      for (int o = 0; o < p.groups; ++o) {
+        const int other = s_cost[o];
+        place += (other > cost || (other == cost && o < g)) ? 1 : 0;
       }
       s_group[place] = uint8_t(g);
       s_tab[kTabRow0 + place] = row0;
@@ -481,12 +493,38 @@ __global__ void __launch_bounds__(640, 1)
       uint32_t armed = 0, armed_par = 0;   // stages whose last arming is not yet known complete, and its parity
       bool ok = true;
       uint32_t cslot = 0, cphase = 0;
-      if (GRP == GRP_NONE) ptx::pdl_wait();
+      if constexpr (GRP == GRP_NONE) {
+        // the first tile's first stages of A (the weights, in all but dW) on their way to L2 while the previous
+        // kernel may still run; prefetches read nothing back (see ptx::tma_prefetch_2d)
+        if (p.prefetch_a && first_tile >= 0) {
+          const TrainTile tc = coords(first_tile);
+          const int n = min(tc.nks, 2 * int(nstages));
+#pragma unroll 1
+          for (int it = 0; it < n; ++it) {
+            const int k0 = (tc.ks0 + it) * 64;
+            if constexpr (A_MN) {
+              ptx::tma_prefetch_2d(&tmA, tc.a0, k0);
+              ptx::tma_prefetch_2d(&tmA, tc.a0 + 64, k0);
+            } else {
+              ptx::tma_prefetch_2d(&tmA, k0, tc.a0);
+            }
+          }
+        }
+        ptx::pdl_wait();
+      }
 #pragma unroll 1
       for (int t = first_tile; t >= 0 && ok;) {
         const TrainTile tc = coords(t);
         const void* mA = &tmA;
         const void* mB = &tmB;
+        if constexpr (EPI == EPI_F32) {
+          // what the epilogue will add to, two tiles or so ahead of it: the additions then find their lines in L2
+          if (p.accumulate && tc.nks > 0) {
+#pragma unroll 1
+            for (int r = 0; r < 128 && tc.a0 + r < p.m; r += 32)
+              ptx::tma_prefetch_3d(&extra.d, tc.n0, tc.a0 + r, tc.z);
+          }
+        }
         // boxes of B: GRP_ROWS 32 rows each (the tiles' widths differ), K-major otherwise one of the tile's
         // half, MN-major 64 columns each
         const int nbox = (GRP == GRP_ROWS || B_MN) ? ((tc.nt >> 1) + (B_MN ? 63 : 31)) / (B_MN ? 64 : 32) : 1;
@@ -660,8 +698,8 @@ __global__ void __launch_bounds__(640, 1)
 #pragma unroll
               for (int c = 0; c < 2; ++c) {
                 const uint32_t off = uint32_t(c * kTrainChunk + r * 128);
-                ptx::tma_load_2d<CG>(stage_a(stage) + off, &tail.a[i], tc.a0 + c * 64, y, fb, pol);
-                ptx::tma_load_2d<CG>(stage_b(stage) + off, &tail.b[i], tc.b0 + c * 64, y, fb, pol);
+                ptx::tma_load_2d<CG>(stage_a(stage) + off, &extra.a[i], tc.a0 + c * 64, y, fb, pol);
+                ptx::tma_load_2d<CG>(stage_b(stage) + off, &extra.b[i], tc.b0 + c * 64, y, fb, pol);
               }
               r += i == 0 ? 16 : (i == 1 ? 4 : 1);
             }
@@ -723,7 +761,9 @@ __global__ void __launch_bounds__(640, 1)
     uint32_t acc = 0, accph = 0;
     uint32_t cslot = 0, cphase = 0;
     [[maybe_unused]] uint32_t turn = 0;  // LOSS: tiles so far
-    // the warp's 2 KB staging box: wait until the store that used it last has read it, fill, send
+    // Stores go through the warp's 2 KB of shared memory: wait until the store that used it last has read it,
+    // fill, send.  Rows are written 128 bytes at a time (a lane each, 16 rows to a box): with 64-byte rows a
+    // bandwidth-bound wgrad took 86 us in place of 70 (8 experts, few rows, 4096 x 7168).
     auto stage_box = [&](auto&& fill, auto&& send) {
       if (lane == 0) ptx::bulk_wait_group_read<0>();
       __syncwarp();
@@ -735,13 +775,20 @@ __global__ void __launch_bounds__(640, 1)
         ptx::bulk_commit_group();
       }
     };
-    // a row per lane, four 16-byte pieces in the 64-byte swizzle
-    auto fill_rows = [&](uint32_t buf, const uint32_t (&w)[16]) {
-      const uint32_t row_addr = buf + uint32_t(lane * 64);
+    [[maybe_unused]] auto store_rows = [&](const uint32_t (&w)[32], int row0, auto&& send) {
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const uint32_t chunk = uint32_t(j) ^ ((uint32_t(lane) >> 1) & 3u);
-        ptx::st_shared_v4(row_addr + chunk * 16u, w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
+      for (int half = 0; half < 2; ++half) {
+        if (row0 + half * 16 >= p.m) break;
+        stage_box(
+            [&](uint32_t buf) {
+              if ((lane >> 4) == half) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                  ptx::st_shared_v4(buf + uint32_t((lane & 15) * 128) + ((uint32_t(j) ^ (uint32_t(lane) & 7u)) << 4),
+                                    w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
+              }
+            },
+            [&](uint32_t buf) { send(buf, row0 + half * 16); });
       }
     };
     // Cross entropy: of the tile's columns col0 + 32 c + lane, the labels (-1: ignored, or no such column) and
@@ -778,17 +825,11 @@ __global__ void __launch_bounds__(640, 1)
         l2[c] = l2_next[c] * 1.4426950408889634f;
       }
       if (t_next >= 0) read_columns(t_next, label_next, l2_next);
-      // per chunk, uniform masks: columns whose label is among this warp's rows (off: which), ignored columns
-      int off[2];
-      uint32_t hits[2], gone[2];
-      if constexpr (EPI == EPI_LOSS || EPI == EPI_DLOGITS) {
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          off[c] = label[c] - p.vocab0 - row0;
-          hits[c] = __ballot_sync(0xffffffffu, label[c] >= 0 && off[c] >= 0 && off[c] < 32 && row0 + off[c] < p.m);
-          gone[c] = __ballot_sync(0xffffffffu, label[c] < 0);
-        }
-      }
+      // columns whose label is among this warp's rows (uniform), and each lane's label as such a row
+      [[maybe_unused]] auto among_rows = [&](int lab, int& off) {
+        off = lab - p.vocab0 - row0;
+        return __ballot_sync(0xffffffffu, lab >= 0 && off >= 0 && off < 32 && row0 + off < p.m);
+      };
       if (!wait_bar_warp<false>(accf_bar(acc), accph, ctl)) break;
       ptx::tc_fence_after();
       const bool idle = !invariant(acc < uint32_t(ACC) && t < num_tiles && tc.nt <= kTrainBN, p.status);
@@ -823,10 +864,11 @@ __global__ void __launch_bounds__(640, 1)
           ptx::tmem_ld_16x256b_x4<16>(tbase + (16u << 16) + uint32_t(c * 32), v);
           ptx::tmem_ld_wait_for(v);
           // labels among these 32 rows: about one column in vocab / 32
+          int off;
 #pragma unroll 1
-          for (uint32_t left = c ? hits[1] : hits[0]; left; left &= left - 1) {
+          for (uint32_t left = among_rows(c ? label[1] : label[0], off); left; left &= left - 1) {
             const int j = __ffs(int(left)) - 1;
-            const int row = __shfl_sync(0xffffffffu, c ? off[1] : off[0], j);
+            const int row = __shfl_sync(0xffffffffu, off, j);
             uint32_t z = ptx::tmem_ld_32x32b_x1(tbase + uint32_t(c * 32 + j));
             asm volatile("tcgen05.wait::ld.sync.aligned;" : "+r"(z)::"memory");
             if (lane == row) p.zlabel[col0 + c * 32 + j] = __uint_as_float(z) * alpha;
@@ -893,49 +935,74 @@ __global__ void __launch_bounds__(640, 1)
         }
       } else if constexpr (EPI == EPI_DLOGITS) {
         const int n = idle ? 0 : nch;
-#pragma unroll 1
-        for (int c = 0; c < n; ++c) {
-          const int col = col0 + c * 32;
-          const uint32_t hit = c ? hits[1] : hits[0], none = c ? gone[1] : gone[0];
-          const float lse2 = c ? l2[1] : l2[0];
-          const int at = c ? off[1] : off[0];
+        uint32_t w[32];                  // 64 columns
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          if (c >= n) break;
           uint32_t v[32];
           ptx::tmem_ld_32x32b_x32(tbase + uint32_t(c * 32), v);
           ptx::tmem_ld_wait_for(v);
           if (c + 1 == n) hand_back();
-          if (col >= tc.n_end || row0 >= p.m) continue;
           float g[32];
 #pragma unroll
           for (int j = 0; j < 32; ++j)
-            g[j] = ptx::ex2(fmaf(__uint_as_float(v[j]), p.c2, -__shfl_sync(0xffffffffu, lse2, j)));
-          if (hit) {
+            g[j] = ptx::ex2(fmaf(__uint_as_float(v[j]), p.c2, -__shfl_sync(0xffffffffu, l2[c], j)));
+          int off;
+          const uint32_t hits = among_rows(label[c], off);
+          if (hits) {
             asm volatile("");   // (a branch, not 32 selects)
 #pragma unroll
             for (int j = 0; j < 32; ++j)
-              if (((hit >> j) & 1u) && lane == __shfl_sync(0xffffffffu, at, j)) g[j] -= 1.f;
+              if (((hits >> j) & 1u) && lane == __shfl_sync(0xffffffffu, off, j)) g[j] -= 1.f;
           }
-          if (none) {   // ignored tokens, whatever their logits and lse are (and columns that are not there)
+          const uint32_t gone = __ballot_sync(0xffffffffu, label[c] < 0);
+          if (gone) {   // ignored tokens, whatever their logits and lse are (and columns that are not there)
             asm volatile("");
 #pragma unroll
             for (int j = 0; j < 32; ++j)
-              if ((none >> j) & 1u) g[j] = 0.f;
+              if ((gone >> j) & 1u) g[j] = 0.f;
           }
-          uint32_t w[16];
 #pragma unroll
-          for (int j = 0; j < 16; ++j) w[j] = ptx::pack_bf16x2(g[2 * j], g[2 * j + 1]);
-          if (h * 64 + c * 32 + 32 <= tc.nt) {
-            stage_box([&](uint32_t buf) { fill_rows(buf, w); },
-                      [&](uint32_t buf) { ptx::tma_store_3d(&tmD, buf, col, row0, 0); });
-          } else if (row0 + lane < p.m) {   // the tile ends after 16 columns of the chunk (a 32-byte sector)
-            uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.d) + size_t(row0 + lane) * p.ldd + col);
-            dst[0] = make_uint4(w[0], w[1], w[2], w[3]);
-            dst[1] = make_uint4(w[4], w[5], w[6], w[7]);
-          }
+          for (int j = 0; j < 16; ++j) w[16 * c + j] = ptx::pack_bf16x2(g[2 * j], g[2 * j + 1]);
         }
         if (n == 0) hand_back();
+        if (n > 0 && col0 < tc.n_end && row0 < p.m) {
+          if (h * 64 + 64 <= tc.nt) {
+            store_rows(w, row0, [&](uint32_t buf, int r) { ptx::tma_store_3d(&tmD, buf, col0, r, 0); });
+          } else if (row0 + lane < p.m) {   // the tile ends within the 64: 16 columns (a 32-byte sector) at a time
+            uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.d) + size_t(row0 + lane) * p.ldd + col0);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              if (h * 64 + i * 16 < tc.nt && col0 + i * 16 < tc.n_end) {
+                dst[2 * i] = make_uint4(w[8 * i], w[8 * i + 1], w[8 * i + 2], w[8 * i + 3]);
+                dst[2 * i + 1] = make_uint4(w[8 * i + 4], w[8 * i + 5], w[8 * i + 6], w[8 * i + 7]);
+              }
+          }
+        }
+      } else if constexpr (EPI == EPI_BF16) {   // tiles are a multiple of 64 wide: both chunks, or none
+        uint32_t w[32];
+        if (nch > 0 && !idle) {
+          const bool nothing = GRP == GRP_K && tc.nks == 0;   // no rows: the sum is empty, the accumulator undefined
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            uint32_t v[32];
+            ptx::tmem_ld_32x32b_x32(tbase + uint32_t(c * 32), v);
+            ptx::tmem_ld_wait_for(v);
+#pragma unroll
+            for (int j = 0; j < 16; ++j)
+              w[16 * c + j] = nothing ? 0u
+                                      : ptx::pack_bf16x2(__uint_as_float(v[2 * j]) * alpha,
+                                                         __uint_as_float(v[2 * j + 1]) * alpha);
+          }
+          hand_back();
+          if (col0 < tc.n_end && row0 < p.m)
+            store_rows(w, row0, [&](uint32_t buf, int r) { ptx::tma_store_3d(&tmD, buf, col0, r, GRP == GRP_K ? tc.z : 0); });
+        } else {
+          hand_back();
+        }
       } else {
         const int n = idle ? 0 : nch;
-        const bool nothing = GRP == GRP_K && tc.nks == 0;   // no rows: the sum is empty, the accumulator undefined
+        [[maybe_unused]] const bool nothing = GRP == GRP_K && tc.nks == 0;
 #pragma unroll 1
         for (int c = 0; c < n; ++c) {
           const int col = col0 + c * 32;
@@ -944,18 +1011,7 @@ __global__ void __launch_bounds__(640, 1)
           ptx::tmem_ld_wait_for(v);
           if (c + 1 == n) hand_back();
           if (col >= tc.n_end || row0 >= p.m) continue;
-          if (nothing) {
-#pragma unroll
-            for (int j = 0; j < 32; ++j) v[j] = 0u;
-          }
-          if constexpr (EPI == EPI_BF16) {
-            uint32_t w[16];
-#pragma unroll
-            for (int j = 0; j < 16; ++j)
-              w[j] = ptx::pack_bf16x2(__uint_as_float(v[2 * j]) * alpha, __uint_as_float(v[2 * j + 1]) * alpha);
-            stage_box([&](uint32_t buf) { fill_rows(buf, w); },
-                      [&](uint32_t buf) { ptx::tma_store_3d(&tmD, buf, col, row0, GRP == GRP_K ? tc.z : 0); });
-          } else if constexpr (EPI == EPI_BF16_T) {
+          if constexpr (EPI == EPI_BF16_T) {
             // even lanes take column j for rows (lane, lane + 1), odd lanes column j + 1 for rows (lane - 1, lane)
             uint32_t w[16];
 #pragma unroll
@@ -991,22 +1047,16 @@ __global__ void __launch_bounds__(640, 1)
                   *reinterpret_cast<uint32_t*>(dst + size_t(col + r) * p.ldd) = w[j];
               }
             }
-          } else {
+          } else {   // F32: tiles are a multiple of 32 wide
             if (nothing && p.accumulate) continue;   // adding nothing
 #pragma unroll
-            for (int half = 0; half < 2; ++half) {
-              if (h * 64 + c * 32 + half * 16 >= tc.nt || col + half * 16 >= tc.n_end) continue;
-              uint32_t w[16];
-#pragma unroll
-              for (int j = 0; j < 16; ++j) w[j] = __float_as_uint(__uint_as_float(v[half * 16 + j]) * alpha);
-              stage_box([&](uint32_t buf) { fill_rows(buf, w); },
-                        [&](uint32_t buf) {
-                          if (p.accumulate)
-                            ptx::tma_add_3d(&tmD, buf, col + half * 16, row0, tc.z);
-                          else
-                            ptx::tma_store_3d(&tmD, buf, col + half * 16, row0, tc.z);
-                        });
-            }
+            for (int j = 0; j < 32; ++j) v[j] = nothing ? 0u : __float_as_uint(__uint_as_float(v[j]) * alpha);
+            store_rows(v, row0, [&](uint32_t buf, int r) {
+              if (p.accumulate)
+                ptx::tma_add_3d(&tmD, buf, col, r, tc.z);
+              else
+                ptx::tma_store_3d(&tmD, buf, col, r, tc.z);
+            });
           }
         }
         if (n == 0) hand_back();

@@ -343,13 +343,28 @@ def _refuse(wanted):
             raise ValueError(msg)
 
 
+_kept = threading.local()    # per thread: {device: workspace} for the default stream
+_KEEP_BYTES = 16 << 20
+
+
 def _workspace(workspace, nbytes, like, stream):
-    """(address, bytes, tensor to keep until the call is made) of the caller's workspace, or of one from torch's
-    allocator: on another stream than the current one that memory is tied to the work queued there."""
+    """(address, bytes, tensor to keep until the call is made) of the caller's workspace, or of one of torch's.
+
+    On the default stream small ones are kept per thread and device (asking torch's allocator costs 6 us while work is
+    queued): calls of one thread follow one another there, and that stream is never captured into a graph.  Elsewhere
+    each call takes its own; on another stream than the current one it is tied to the work queued there."""
     import torch
     if workspace is not None:
         return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace
+    small = stream is None and nbytes <= _KEEP_BYTES and _stream(None) == 0
+    if small:
+        kept = _kept.__dict__.get(like.get_device())
+        if kept is not None and kept[1] >= nbytes:
+            return kept
     workspace = torch.empty(nbytes, dtype=torch.uint8, device=like.device)
+    if small:
+        kept = _kept.__dict__[like.get_device()] = (workspace.data_ptr(), nbytes, workspace)
+        return kept
     if stream is not None:
         s = torch.cuda.ExternalStream(stream) if isinstance(stream, int) else stream
         if s != torch.cuda.current_stream():
