@@ -150,60 +150,51 @@ __global__ void __launch_bounds__(256)
 
 // ---------------------------------------------------------------- dX from its FP32 parts
 // Parts are [hidden][token] (pitch a multiple of 64); dX is [token][hidden].  A
-// block adds the parts of 64 tokens x 32 hidden, in order and four parts' loads in
+// block adds the parts of 64 tokens x 16 hidden, in order and eight parts' loads in
 // flight together, turns them in shared memory and multiplies by the tokens' weights.
 __global__ void __launch_bounds__(256)
     ce_dx_kernel(int tokens, int vocab, int hidden, int parts, const float* __restrict__ part, size_t pitch,
                  const long long* __restrict__ labels, const float* __restrict__ dloss, float alpha,
                  uint16_t* __restrict__ dX, size_t lddx) {
-  __shared__ float s_t[32][65];
+  __shared__ float s_t[16][65];
   ptx::pdl_launch_dependents();
   ptx::pdl_wait();
-  const int t0 = blockIdx.x * 64, h0 = blockIdx.y * 32, tid = threadIdx.x;
-  const int tq = (tid & 15) * 4, hr = tid >> 4;   // four tokens, rows hr and hr + 16
+  const int t0 = blockIdx.x * 64, h0 = blockIdx.y * 16, tid = threadIdx.x;
+  const int tq = (tid & 15) * 4, hr = tid >> 4;   // four tokens of one row
   const float* src = part + size_t(h0 + hr) * pitch + t0 + tq;
   const size_t part_len = size_t(hidden) * pitch;
-  const bool row[2] = {h0 + hr < hidden, h0 + hr + 16 < hidden};
-  float4 s[2] = {};
+  const bool row = h0 + hr < hidden;
+  float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 1
-  for (int p0 = 0; p0 < parts; p0 += 4) {
-    float4 x[4][2];
+  for (int p0 = 0; p0 < parts; p0 += 8) {
+    float4 x[8];
 #pragma unroll
-    for (int p = 0; p < 4; ++p)
+    for (int p = 0; p < 8; ++p)
+      x[p] = p0 + p < parts && row ? __ldcg(reinterpret_cast<const float4*>(src + size_t(p0 + p) * part_len))
+                                   : make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-      for (int i = 0; i < 2; ++i)
-        x[p][i] = p0 + p < parts && row[i]
-                      ? __ldcg(reinterpret_cast<const float4*>(src + size_t(p0 + p) * part_len + size_t(i) * 16 * pitch))
-                      : make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-    for (int p = 0; p < 4; ++p)
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        s[i].x += x[p][i].x;
-        s[i].y += x[p][i].y;
-        s[i].z += x[p][i].z;
-        s[i].w += x[p][i].w;
-      }
+    for (int p = 0; p < 8; ++p) {
+      s.x += x[p].x;
+      s.y += x[p].y;
+      s.z += x[p].z;
+      s.w += x[p].w;
+    }
   }
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    float* d = &s_t[hr + 16 * i][tq];
-    d[0] = s[i].x;
-    d[1] = s[i].y;
-    d[2] = s[i].z;
-    d[3] = s[i].w;
-  }
+  s_t[hr][tq] = s.x;
+  s_t[hr][tq + 1] = s.y;
+  s_t[hr][tq + 2] = s.z;
+  s_t[hr][tq + 3] = s.w;
   __syncthreads();
-  // 4 threads per token, 8 hidden (16 bytes) each
-  const int t = t0 + (tid >> 2), hh = (tid & 3) * 8;
-  if (t < tokens && h0 + hh < hidden) {
+  // 2 threads per token, 8 hidden (16 bytes) each
+  const int t = t0 + (tid >> 1), hh = (tid & 1) * 8;
+  if (tid < 128 && t < tokens && h0 + hh < hidden) {
     const long long y = __ldcg(labels + t);
     const float w = alpha * __ldcg(dloss + t);
     uint32_t o[4] = {0, 0, 0, 0};
     if (y >= 0 && y < vocab) {
 #pragma unroll
       for (int i = 0; i < 4; ++i)
-        o[i] = ptx::pack_bf16x2(s_t[hh + 2 * i][tid >> 2] * w, s_t[hh + 2 * i + 1][tid >> 2] * w);
+        o[i] = ptx::pack_bf16x2(s_t[hh + 2 * i][tid >> 1] * w, s_t[hh + 2 * i + 1][tid >> 1] * w);
     }
     *reinterpret_cast<uint4*>(dX + size_t(t) * lddx + h0 + hh) = make_uint4(o[0], o[1], o[2], o[3]);
   }
@@ -387,7 +378,6 @@ tkg_status tkg_linear_ce_grad(int tokens, int vocab, int hidden, const void* X, 
       q.n = tokens;
       q.k = nv;
       q.n_tile = train_n_tile(tokens, kTileF32);
-      q.prefetch_a = 1;
       q.alpha = 1.f;
       q.split_stages = ceil_div(ceil_div(nv, 64), pl.parts);
       q.splits = ceil_div(ceil_div(nv, 64), q.split_stages);
@@ -433,7 +423,7 @@ tkg_status tkg_linear_ce_grad(int tokens, int vocab, int hidden, const void* X, 
     }
   }
   if (!dX) return TKG_OK;
-  return launch_small(ce_dx_kernel, dim3(unsigned(ceil_div(tokens, 64)), unsigned(ceil_div(hidden, 32))), dim3(256),
+  return launch_small(ce_dx_kernel, dim3(unsigned(ceil_div(tokens, 64)), unsigned(ceil_div(hidden, 16))), dim3(256),
                       stream, tokens, vocab, hidden, pl.parts, part, pl.tokens_up, labels, dloss, alpha,
                       static_cast<uint16_t*>(dX), size_t(lddx));
 }

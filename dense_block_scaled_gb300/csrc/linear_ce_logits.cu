@@ -9,7 +9,6 @@ static tkg_status launch_logits(const void* X, size_t x_bytes, const void* W, si
   CUtensorMap tmA, tmB, tmD;
   tkg_status st;
   p.n_tile = train_n_tile(p.n, kTileTokens);
-  p.prefetch_a = 1;
   if ((st = map_k_major(&tmA, W, p.m, p.k, w_bytes, 128)) != TKG_OK) return st;
   if ((st = map_k_major(&tmB, X, p.n, p.k, x_bytes, p.n_tile / 2)) != TKG_OK) return st;
   tmD = tmA;
@@ -18,6 +17,7 @@ static tkg_status launch_logits(const void* X, size_t x_bytes, const void* W, si
     return st;
   p.splits = 1;
   p.split_stages = ceil_div(p.k, 64);
+  if (EPI == EPI_LOSS && p.n <= kNarrowTokens) return launch_train<false, false, EPI, GRP_NONE, true>(tmA, tmB, tmD, p, stream);
   return launch_train<false, false, EPI, GRP_NONE>(tmA, tmB, tmD, p, stream);
 }
 

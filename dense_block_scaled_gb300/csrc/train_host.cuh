@@ -46,14 +46,15 @@ constexpr int kTileBF16 = 64, kTileF32 = 32, kTileTokens = 16;
 
 // Fills the fields common to every launch and launches.  The caller sets p.m, n,
 // k, n_tile, alpha, splits and split_stages (GRP_NONE) and the epilogue's own fields.
-template <bool A_MN, bool B_MN, int EPI, int GRP>
+template <bool A_MN, bool B_MN, int EPI, int GRP, bool NARROW = false>
 tkg_status launch_train(const CUtensorMap& tmA, const CUtensorMap& tmB, const CUtensorMap& tmD, TrainParams p,
                         cudaStream_t stream,
                         const ExtraMaps<EPI, GRP>& extra = {}) {
-  using C = TrainConfig<A_MN, B_MN, EPI, GRP>;
-  auto kern = train_kernel<A_MN, B_MN, EPI, GRP>;
-  // more than half an SM's shared memory: no two CTAs share an SM (each takes all of tensor memory)
-  static_assert(C::kSmemBytes > 118784, "one CTA per SM");
+  using C = TrainConfig<A_MN, B_MN, EPI, GRP, NARROW>;
+  auto kern = train_kernel<A_MN, B_MN, EPI, GRP, NARROW>;
+  // a block that takes all of tensor memory takes more than half of shared memory too, so that no two share an SM
+  static_assert(NARROW || C::kSmemBytes > 118784, "one CTA per SM");
+  if (p.n_tile > C::kBN) return TKG_ERR_UNSUPPORTED;   // (no caller asks for it)
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return TKG_ERR_CUDA;
   static bool attr_set[64] = {};   // per instantiation and device (idempotent if two threads race)
@@ -118,6 +119,9 @@ tkg_status launch_train(const CUtensorMap& tmA, const CUtensorMap& tmB, const CU
   }
   return TKG_OK;
 }
+
+// At most this many tokens take the kernel's narrow form.
+constexpr int kNarrowTokens = 128;
 
 // Launch of a small kernel that waits for the previous grid itself (griddepcontrol.wait).
 template <typename... P, typename... Args>

@@ -34,6 +34,11 @@
 // tokens leave most of a stage to the weights (bytes in flight are what a
 // bandwidth-bound call needs).
 //
+// NARROW (at most 128 tokens, where reading the weights bounds the time): two
+// blocks per SM, each with half the shared and tensor memory and 4 epilogue warps.
+// Twice the tiles run at once, so that few tiles do not leave a thin last round,
+// and one block's set-up and epilogue run under the other's loads.
+//
 // Epilogues (EPI):
 //   LOSS     per token (column) and 128 vocabulary rows: the largest logit and the
 //            sum of exponentials in base 2, and, where the token's label falls among
@@ -88,7 +93,6 @@ struct TrainParams {
   void* d;
   size_t ldd;
   int accumulate;              // F32
-  int prefetch_a;              // start fetching A before the dependency wait
   // groups
   const int* sizes;            // device
   int groups;
@@ -208,15 +212,17 @@ __device__ __forceinline__ int column_of_lane(int lane) {
 constexpr int kTrainBN = 256;         // widest tile
 constexpr int kTrainMaxStages = 12;
 
-template <bool A_MN, bool B_MN, int EPI, int GRP>
+template <bool A_MN, bool B_MN, int EPI, int GRP, bool NARROW>
 struct TrainConfig {
-  static constexpr int kEpiWarps = 16;
+  static constexpr int kBN = NARROW ? 128 : kTrainBN;      // widest tile, and columns of an accumulator
+  static constexpr int kEpiWarps = NARROW ? 4 : 16;
+  static constexpr int kChunks = kBN / 32 / (kEpiWarps / 4);   // 32-column chunks of a tile per epilogue warp
   static constexpr int kThreads = 32 * (4 + kEpiWarps);
   static constexpr int kAcc = 2;
   static constexpr int kABytes = 128 * 128;
   static constexpr int kEpiBufBytes = 32 * 64;      // 32 rows x 32 BF16 (or 16 FP32)
   // LOSS: two buffers of (maximum, sum) per quadrant and column; others: a staging box per warp
-  static constexpr int kEpiBytes = EPI == EPI_LOSS ? 2 * 4 * kTrainBN * 8 : kEpiWarps * kEpiBufBytes;
+  static constexpr int kEpiBytes = EPI == EPI_LOSS ? 2 * 4 * kBN * 8 : kEpiWarps * kEpiBufBytes;
   static constexpr int kTailBars = GRP == GRP_K ? kTrainMaxStages : 0;
   static constexpr int kNumBars = 2 * kTrainMaxStages + 2 * kAcc + 2 + 4 + 4 + kTailBars;
   // groups by rank: first row, rows, the group (a byte each); GRP_ROWS: first tile, and the tile count
@@ -224,13 +230,14 @@ struct TrainConfig {
       GRP == GRP_NONE ? 0 : 2 * kMaxGroups + kMaxGroups / 4 + (GRP == GRP_ROWS ? kMaxGroups + 1 : 0);
   // epilogue buffers, barriers, two scheduler answers, table, 1024-byte alignment; the rest is the ring's
   static constexpr int kFixedBytes = kEpiBytes + kNumBars * 8 + 2 * 16 + 16 + kTabInts * 4 + 1024;
-  static constexpr int kSmemBytes = 232448 - 16;    // all an SM gives a block, less the two static words
+  // all an SM gives a block, or two blocks, less the two static words
+  static constexpr int kSmemBytes = (NARROW ? 116736 - 1024 : 232448) - 16;
   static constexpr int kRingBytes = (kSmemBytes - kFixedBytes) / 1024 * 1024;
-  static_assert(kRingBytes >= 6 * 2 * kABytes, "six stages of 256-wide tiles");
+  static_assert(kRingBytes >= (NARROW ? 4 : 6) * (kABytes + kBN / 2 * 128), "four or six stages of the widest tiles");
   static constexpr bool kClc = GRP != GRP_ROWS;     // GRP_ROWS: the tile count is known on the device only
   // readers of a scheduler answer: producer (GRP_K: two) and epilogue warps per CTA, MMA issuer and scheduler
   static constexpr int kClcConsumers = 2 * ((GRP == GRP_K ? 2 : 1) + kEpiWarps) + 2;
-  static constexpr uint32_t kIdesc = idesc_f16(256, kTrainBN) | (A_MN ? 1u << 15 : 0u) | (B_MN ? 1u << 16 : 0u);
+  static constexpr uint32_t kIdesc = idesc_f16(256, kBN) | (A_MN ? 1u << 15 : 0u) | (B_MN ? 1u << 16 : 0u);
 };
 
 // Width of the tiles that `n` columns are cut into.
@@ -251,12 +258,12 @@ struct TrainTile {
   int k_end;         // contraction stops here (from k0)
 };
 
-template <bool A_MN, bool B_MN, int EPI, int GRP>
-__global__ void __launch_bounds__(640, 1)
+template <bool A_MN, bool B_MN, int EPI, int GRP, bool NARROW>
+__global__ void __launch_bounds__(TrainConfig<A_MN, B_MN, EPI, GRP, NARROW>::kThreads, NARROW ? 2 : 1)
     train_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                  const __grid_constant__ CUtensorMap tmD, const TrainParams p,
                  const __grid_constant__ ExtraMaps<EPI, GRP> extra) {
-  using C = TrainConfig<A_MN, B_MN, EPI, GRP>;
+  using C = TrainConfig<A_MN, B_MN, EPI, GRP, NARROW>;
   constexpr int CG = 2;
   constexpr int ACC = C::kAcc;
   extern __shared__ uint8_t smem_raw[];
@@ -361,8 +368,11 @@ __global__ void __launch_bounds__(640, 1)
     ptx::prefetch_tmap(&tmB);
     if (EPI != EPI_LOSS) ptx::prefetch_tmap(&tmD);
   }
+  // Two narrow blocks share an SM, one of them perhaps of the next kernel: it takes tensor memory only once the
+  // previous kernel is done, as a block that holds some while it waits could keep that kernel from getting its own
+  if (NARROW) ptx::pdl_wait();
   if (warp == 2) {
-    ptx::tmem_alloc<CG>(ptx::smem_u32(&s_tmem_base), 512u);
+    ptx::tmem_alloc<CG>(ptx::smem_u32(&s_tmem_base), uint32_t(2 * C::kBN));
     ptx::tmem_relinquish<CG>();
   }
   ptx::tc_fence_before();
@@ -381,7 +391,7 @@ __global__ void __launch_bounds__(640, 1)
     // s_end: where each group ends (in the epilogue's buffers, not in use yet).  The sizes may have been cached by this SM before the
     // previous grid wrote them: they are read through L2.
     int* s_end = reinterpret_cast<int*>(smem_raw + (epi_base - raw));
-    int* s_cost = s_end + kMaxGroups;
+    [[maybe_unused]] int* s_rows = s_end + kMaxGroups;
     const int g = threadIdx.x;
     if (warp == 3) {
       const uint32_t cap = uint32_t(GRP == GRP_ROWS ? p.n : p.k);
@@ -400,20 +410,23 @@ __global__ void __launch_bounds__(640, 1)
       }
     }
     __syncthreads();
-    // Places by falling cost of a tile (GRP_ROWS its width, GRP_K its rows): the dear ones go out first, and
-    // what is left at the end is small
+    // Places.  GRP_K: by falling row count, so that the long sums go out first and what is left at the end is
+    // small.  GRP_ROWS: as they come; its tiles are within a factor of two of one another, and a mixture of
+    // experts that are bound by reading their matrices (few rows) and by their products keeps both busy (by falling
+    // width 64 uneven experts of 2048 x 2048 took 130 us, as they come 128).
     const int row0 = g > 0 && g < p.groups ? s_end[g - 1] : 0;
     const int rows = g < p.groups ? s_end[g] - row0 : 0;
-    const int cost = GRP == GRP_ROWS ? train_n_tile(rows, 16) : rows;
-    if (g < p.groups) s_cost[g] = cost;
-    __syncthreads();
-    if (g < p.groups) {
-      int place = 0;
+    int place = g;
+    if constexpr (GRP == GRP_K) {
+      if (g < p.groups) s_rows[g] = rows;
+      __syncthreads();
+      if (g < p.groups) {
+        place = 0;
 #pragma unroll 4
-      for (int o = 0; o < p.groups; ++o) {
-        const int other = s_cost[o];
-        place += (other > cost || (other == cost && o < g)) ? 1 : 0;
+        for (int o = 0; o < p.groups; ++o) place += (s_rows[o] > rows || (s_rows[o] == rows && o < g)) ? 1 : 0;
       }
+    }
+    if (g < p.groups) {
       s_group[place] = uint8_t(g);
       s_tab[kTabRow0 + place] = row0;
       s_tab[kTabRows + place] = rows;
@@ -493,25 +506,7 @@ __global__ void __launch_bounds__(640, 1)
       uint32_t armed = 0, armed_par = 0;   // stages whose last arming is not yet known complete, and its parity
       bool ok = true;
       uint32_t cslot = 0, cphase = 0;
-      if constexpr (GRP == GRP_NONE) {
-        // the first tile's first stages of A (the weights, in all but dW) on their way to L2 while the previous
-        // kernel may still run; prefetches read nothing back (see ptx::tma_prefetch_2d)
-        if (p.prefetch_a && first_tile >= 0) {
-          const TrainTile tc = coords(first_tile);
-          const int n = min(tc.nks, 2 * int(nstages));
-#pragma unroll 1
-          for (int it = 0; it < n; ++it) {
-            const int k0 = (tc.ks0 + it) * 64;
-            if constexpr (A_MN) {
-              ptx::tma_prefetch_2d(&tmA, tc.a0, k0);
-              ptx::tma_prefetch_2d(&tmA, tc.a0 + 64, k0);
-            } else {
-              ptx::tma_prefetch_2d(&tmA, k0, tc.a0);
-            }
-          }
-        }
-        ptx::pdl_wait();
-      }
+      if (GRP == GRP_NONE && !NARROW) ptx::pdl_wait();
 #pragma unroll 1
       for (int t = first_tile; t >= 0 && ok;) {
         const TrainTile tc = coords(t);
@@ -548,7 +543,7 @@ __global__ void __launch_bounds__(640, 1)
           }
           // a tile of this launch, a ring slot, 16-byte aligned x (TMA's rule), the box inside the stage
           if (invariant(t < num_tiles && stage < nstages && tc.z >= 0 && (!A_MN || tc.a0 % 8 == 0) &&
-                            (!B_MN || tc.b0 % 8 == 0) && tc.nt >= 16 && tc.nt <= kTrainBN,
+                            (!B_MN || tc.b0 % 8 == 0) && tc.nt >= 16 && tc.nt <= C::kBN,
                         p.status)) {
             if (GRP == GRP_K && last < 64) {
               ptx::mbar_arrive(tail_go(stage));   // the stage is free and armed: warp 3 loads it
@@ -611,7 +606,7 @@ __global__ void __launch_bounds__(640, 1)
           break;
         }
         ptx::tc_fence_after();
-        const uint32_t d_tmem = tmem + acc * uint32_t(kTrainBN);
+        const uint32_t d_tmem = tmem + acc * uint32_t(C::kBN);
         const TrainTile tc = coords(t);
         const uint32_t idesc = idesc_with_n(C::kIdesc, tc.nt);
 #pragma unroll 1
@@ -623,7 +618,7 @@ __global__ void __launch_bounds__(640, 1)
           const uint64_t adesc = A_MN ? sdesc_mn_sw128(stage_a(stage)) : sdesc_sw128(stage_a(stage));
           const uint64_t bdesc = B_MN ? sdesc_mn_sw128(stage_b(stage)) : sdesc_sw128(stage_b(stage));
           const int left = tc.k_end - (tc.ks0 + it) * 64;   // k past it are zero, or not there
-          const bool stage_ok = invariant(stage < nstages && acc < uint32_t(ACC) && tc.nt <= kTrainBN, p.status);
+          const bool stage_ok = invariant(stage < nstages && acc < uint32_t(ACC) && tc.nt <= C::kBN, p.status);
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
             if (j * 16 >= left || !stage_ok) break;
@@ -715,7 +710,7 @@ __global__ void __launch_bounds__(640, 1)
   // ------------------------------------------------------------------ tile scheduler
   else if (warp == 2) {
     if constexpr (C::kClc) {
-      if (GRP == GRP_NONE) ptx::pdl_wait();
+      if (GRP == GRP_NONE && !NARROW) ptx::pdl_wait();
       if (leader && ptx::elect_one()) {
         uint32_t slot = 0, ph = 0;
 #pragma unroll 1
@@ -753,10 +748,10 @@ __global__ void __launch_bounds__(640, 1)
   else if (warp >= 4) {
     const int e = warp - 4;
     const int q = warp & 3;              // accumulator lane quadrant this warp may read
-    const int h = e >> 2;                // quarter of the tile's 32-column chunks: 2 h and 2 h + 1
+    const int h = e >> 2;                // which of the tile's chunks: kChunks from h kChunks
     const uint32_t my_buf = epi_base + uint32_t(e * C::kEpiBufBytes);
     const uint32_t acce_lead0 = ptx::map_to_rank(acce_bar(0), 0);
-    if (GRP == GRP_NONE) ptx::pdl_wait();
+    if (GRP == GRP_NONE && !NARROW) ptx::pdl_wait();
     const float alpha = p.scale ? p.alpha * __ldcg(p.scale) : p.alpha;
     uint32_t acc = 0, accph = 0;
     uint32_t cslot = 0, cphase = 0;
@@ -793,14 +788,14 @@ __global__ void __launch_bounds__(640, 1)
     };
     // Cross entropy: of the tile's columns col0 + 32 c + lane, the labels (-1: ignored, or no such column) and
     // for DLOGITS lse in base 2; read one tile ahead
-    int label[2] = {-1, -1}, label_next[2] = {-1, -1};
-    float l2[2] = {0.f, 0.f}, l2_next[2] = {0.f, 0.f};
-    auto read_columns = [&](int t, int (&lab)[2], float (&ls)[2]) {
+    int label[C::kChunks], label_next[C::kChunks];
+    float l2[C::kChunks] = {}, l2_next[C::kChunks] = {};
+    auto read_columns = [&](int t, int (&lab)[C::kChunks], float (&ls)[C::kChunks]) {
       if constexpr (EPI == EPI_LOSS || EPI == EPI_DLOGITS) {
         const TrainTile tc = coords(t);
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          const int col = tc.n0 + h * 64 + c * 32 + lane;
+        for (int c = 0; c < C::kChunks; ++c) {
+          const int col = tc.n0 + h * C::kChunks * 32 + c * 32 + lane;
           lab[c] = -1;
           if (col < tc.n_end) {
             const long long y = __ldcg(p.labels + col);
@@ -816,15 +811,22 @@ __global__ void __launch_bounds__(640, 1)
       const TrainTile tc = coords(t);
       const int t_next = __shfl_sync(0xffffffffu, next_tile(Warp{}, t, cslot, cphase), 0);
       if (t_next == -2) break;
-      const int nch = min(max(((tc.nt + 31) >> 5) - 2 * h, 0), 2);         // this warp's chunks
+      const int nch = min(max(((tc.nt + 31) >> 5) - C::kChunks * h, 0), C::kChunks);   // this warp's chunks
       const int row0 = tc.a0 + q * 32;                                     // its rows of D
-      const int col0 = tc.n0 + h * 64;                                     // and its first column
+      const int col0 = tc.n0 + h * C::kChunks * 32;                        // and its first column
 #pragma unroll
-      for (int c = 0; c < 2; ++c) {
+      for (int c = 0; c < C::kChunks; ++c) {
         label[c] = label_next[c];
         l2[c] = l2_next[c] * 1.4426950408889634f;
       }
       if (t_next >= 0) read_columns(t_next, label_next, l2_next);
+      // (selects: an array indexed at run time would live in local memory)
+      [[maybe_unused]] auto pick = [](const int (&x)[C::kChunks], int c) {
+        int r = x[0];
+#pragma unroll
+        for (int i = 1; i < C::kChunks; ++i) r = c == i ? x[i] : r;
+        return r;
+      };
       // columns whose label is among this warp's rows (uniform), and each lane's label as such a row
       [[maybe_unused]] auto among_rows = [&](int lab, int& off) {
         off = lab - p.vocab0 - row0;
@@ -832,8 +834,8 @@ __global__ void __launch_bounds__(640, 1)
       };
       if (!wait_bar_warp<false>(accf_bar(acc), accph, ctl)) break;
       ptx::tc_fence_after();
-      const bool idle = !invariant(acc < uint32_t(ACC) && t < num_tiles && tc.nt <= kTrainBN, p.status);
-      const uint32_t tbase = tmem + (uint32_t(q * 32) << 16) + acc * uint32_t(kTrainBN) + uint32_t(h * 64);
+      const bool idle = !invariant(acc < uint32_t(ACC) && t < num_tiles && tc.nt <= C::kBN, p.status);
+      const uint32_t tbase = tmem + (uint32_t(q * 32) << 16) + acc * uint32_t(C::kBN) + uint32_t(h * C::kChunks * 32);
       auto hand_back = [&]() {   // every load of this tile has completed
         ptx::tc_fence_before();
         __syncwarp();
@@ -849,7 +851,7 @@ __global__ void __launch_bounds__(640, 1)
         }
       };
       if constexpr (EPI == EPI_LOSS) {
-        float2* stat = s_stat + (turn & 1u) * uint32_t(4 * kTrainBN) + h * 64;
+        float2* stat = s_stat + (turn & 1u) * uint32_t(4 * C::kBN) + h * C::kChunks * 32;
         const uint32_t stat_phase = (turn & 1u);
         ++turn;
         const float c2 = fabsf(p.c2);
@@ -866,7 +868,7 @@ __global__ void __launch_bounds__(640, 1)
           // labels among these 32 rows: about one column in vocab / 32
           int off;
 #pragma unroll 1
-          for (uint32_t left = among_rows(c ? label[1] : label[0], off); left; left &= left - 1) {
+          for (uint32_t left = among_rows(pick(label, c), off); left; left &= left - 1) {
             const int j = __ffs(int(left)) - 1;
             const int row = __shfl_sync(0xffffffffu, off, j);
             uint32_t z = ptx::tmem_ld_32x32b_x1(tbase + uint32_t(c * 32 + j));
@@ -912,7 +914,7 @@ __global__ void __launch_bounds__(640, 1)
               sum[i] = float(rows_there > 0) + float(rows_there > 8) + float(rows_there > 16) + float(rows_there > 24);
           }
           const float s = fold_columns(sum, lane, [](float a, float b) { return a + b; });
-          stat[q * kTrainBN + c * 32 + column_of_lane(lane)] = make_float2(own == -INFINITY ? own : own * c2, s);
+          stat[q * C::kBN + c * 32 + column_of_lane(lane)] = make_float2(own == -INFINITY ? own : own * c2, s);
         }
         if (n == 0) hand_back();
         __syncwarp();
@@ -925,7 +927,7 @@ __global__ void __launch_bounds__(640, 1)
           float2 x[4];
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            x[i] = stat[i * kTrainBN + q * 32 + lane];
+            x[i] = stat[i * C::kBN + q * 32 + lane];
             m = fmaxf(m, x[i].x);
           }
           const float sub = fabsf(m) == INFINITY ? 0.f : m;
@@ -937,7 +939,7 @@ __global__ void __launch_bounds__(640, 1)
         const int n = idle ? 0 : nch;
         uint32_t w[32];                  // 64 columns
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
+        for (int c = 0; c < C::kChunks; ++c) {
           if (c >= n) break;
           uint32_t v[32];
           ptx::tmem_ld_32x32b_x32(tbase + uint32_t(c * 32), v);
@@ -963,28 +965,30 @@ __global__ void __launch_bounds__(640, 1)
               if ((gone >> j) & 1u) g[j] = 0.f;
           }
 #pragma unroll
-          for (int j = 0; j < 16; ++j) w[16 * c + j] = ptx::pack_bf16x2(g[2 * j], g[2 * j + 1]);
-        }
-        if (n == 0) hand_back();
-        if (n > 0 && col0 < tc.n_end && row0 < p.m) {
-          if (h * 64 + 64 <= tc.nt) {
-            store_rows(w, row0, [&](uint32_t buf, int r) { ptx::tma_store_3d(&tmD, buf, col0, r, 0); });
+          for (int j = 0; j < 16; ++j) w[16 * (c & 1) + j] = ptx::pack_bf16x2(g[2 * j], g[2 * j + 1]);
+          // two chunks, or a last one
+          const int c0 = c & ~1, at = h * C::kChunks * 32 + c0 * 32, col = tc.n0 + at;
+          if (!((c & 1) || c + 1 == n) || col >= tc.n_end || row0 >= p.m) continue;
+          if (at + 64 <= tc.nt) {
+            store_rows(w, row0, [&](uint32_t buf, int r) { ptx::tma_store_3d(&tmD, buf, col, r, 0); });
           } else if (row0 + lane < p.m) {   // the tile ends within the 64: 16 columns (a 32-byte sector) at a time
-            uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.d) + size_t(row0 + lane) * p.ldd + col0);
+            uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.d) + size_t(row0 + lane) * p.ldd + col);
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-              if (h * 64 + i * 16 < tc.nt && col0 + i * 16 < tc.n_end) {
+              if (at + i * 16 < tc.nt && col + i * 16 < tc.n_end) {
                 dst[2 * i] = make_uint4(w[8 * i], w[8 * i + 1], w[8 * i + 2], w[8 * i + 3]);
                 dst[2 * i + 1] = make_uint4(w[8 * i + 4], w[8 * i + 5], w[8 * i + 6], w[8 * i + 7]);
               }
           }
         }
+        if (n == 0) hand_back();
       } else if constexpr (EPI == EPI_BF16) {   // tiles are a multiple of 64 wide: both chunks, or none
+        static_assert(EPI != EPI_BF16 || C::kChunks == 2, "64 columns per warp");
         uint32_t w[32];
         if (nch > 0 && !idle) {
           const bool nothing = GRP == GRP_K && tc.nks == 0;   // no rows: the sum is empty, the accumulator undefined
 #pragma unroll
-          for (int c = 0; c < 2; ++c) {
+          for (int c = 0; c < C::kChunks; ++c) {
             uint32_t v[32];
             ptx::tmem_ld_32x32b_x32(tbase + uint32_t(c * 32), v);
             ptx::tmem_ld_wait_for(v);
@@ -1080,7 +1084,7 @@ __global__ void __launch_bounds__(640, 1)
   ptx::cluster_sync_relaxed();
   if (warp == 2) {
     ptx::tc_fence_after();
-    ptx::tmem_dealloc<CG>(tmem, 512u);
+    ptx::tmem_dealloc<CG>(tmem, uint32_t(2 * C::kBN));
   }
 }
 
