@@ -73,10 +73,9 @@ tkg_status tkg_gemm_grouped_dev_bf16_wgrad(int groups, const int* m_sizes_dev, i
   TailMaps tail;
   if ((st = map_mn_major(&tmA, dD, n, m_capacity, size_t(n) * 2, 64)) != TKG_OK) return st;
   if ((st = map_mn_major(&tmB, A, k, m_capacity, size_t(k) * 2, 64)) != TKG_OK) return st;
-  for (int i = 0; i < 3; ++i) {
-    const int rows = i == 0 ? 16 : (i == 1 ? 4 : 1);
-    if ((st = map_mn_major(&tail.a[i], dD, n, m_capacity, size_t(n) * 2, rows)) != TKG_OK) return st;
-    if ((st = map_mn_major(&tail.b[i], A, k, m_capacity, size_t(k) * 2, rows)) != TKG_OK) return st;
+  for (int i = 0; i < kTailMaps; ++i) {
+    if ((st = map_mn_major(&tail.a[i], dD, n, m_capacity, size_t(n) * 2, 16 >> i)) != TKG_OK) return st;
+    if ((st = map_mn_major(&tail.b[i], A, k, m_capacity, size_t(k) * 2, 16 >> i)) != TKG_OK) return st;
   }
   if ((st = map_out(&tmD, dB, n, k, groups, size_t(k) * es, size_t(n) * size_t(k) * es, es == 4)) != TKG_OK) return st;
   TrainParams p{};
@@ -87,17 +86,22 @@ tkg_status tkg_gemm_grouped_dev_bf16_wgrad(int groups, const int* m_sizes_dev, i
   p.sizes = m_sizes_dev;
   p.groups = groups;
   p.accumulate = type == TKG_GRAD_F32_ADD;
+  // by the rows an expert has on average; additions stay on the narrower tiles, whose epilogues overlap more (8
+  // experts of 1024 and 2048 rows, 4096 x 7168: 446 and 715 us against 473 and 728)
+  const bool dual = type != TKG_GRAD_F32_ADD && train_dual(n, k, groups, ceil_div(ceil_div(m_capacity, groups), 64));
   if (type == TKG_GRAD_BF16) {
     ExtraMaps<EPI_BF16, GRP_K> extra{};
     static_cast<TailMaps&>(extra) = tail;
     p.n_tile = train_n_tile(k, kTileBF16);
-    return launch_train<true, true, EPI_BF16, GRP_K>(tmA, tmB, tmD, p, stream, extra);
+    return dual ? launch_train<true, true, EPI_BF16, GRP_K, SHAPE_DUAL>(tmA, tmB, tmD, p, stream, extra)
+                : launch_train<true, true, EPI_BF16, GRP_K>(tmA, tmB, tmD, p, stream, extra);
   }
   ExtraMaps<EPI_F32, GRP_K> extra{};
   static_cast<TailMaps&>(extra) = tail;
   if ((st = map_prefetch(&extra.d, dB, n, k, groups, size_t(k) * 4, size_t(n) * size_t(k) * 4)) != TKG_OK) return st;
   p.n_tile = train_n_tile(k, kTileF32);
-  return launch_train<true, true, EPI_F32, GRP_K>(tmA, tmB, tmD, p, stream, extra);
+  return dual ? launch_train<true, true, EPI_F32, GRP_K, SHAPE_DUAL>(tmA, tmB, tmD, p, stream, extra)
+              : launch_train<true, true, EPI_F32, GRP_K>(tmA, tmB, tmD, p, stream, extra);
 }
 
 }  // extern "C"

@@ -203,14 +203,14 @@ __global__ void __launch_bounds__(256)
 inline size_t round_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 
 // ---------------------------------------------------------------- plans and workspaces
-// The plans go by the GB300's 152 SMs, so that a workspace's size depends on the
-// problem alone; on fewer SMs they are only less well balanced.
-constexpr int kPairs = 76;
+// The plans go by the GB300's 76 pairs of SMs, so that a workspace's size depends
+// on the problem alone; on fewer SMs they are only less well balanced.
 
 struct GradPlan {
   int piece;          // vocabulary entries per piece
   int pieces;
   int parts;          // k parts of dX's product
+  bool dx_dual;       // on 256 x 512 tiles
   size_t tokens_up;   // row pitch of g and of dX's parts, in elements
   size_t g_off, part_off, scale_off, bytes;   // the weighted rows of X come first
 };
@@ -222,30 +222,33 @@ int default_piece(int tokens, int vocab) {
   return piece < vocab ? int(piece) : vocab;
 }
 
-// Parts of dX's long axis: the number whose rounds of tiles take least, a part
-// at least 8 stages (512 vocabulary entries) long.
-int dx_parts(int tokens, int hidden, int k) {
-  const int tiles = ceil_div(hidden, 256) * ceil_div(tokens, kTrainBN);
+// Parts of dX's long axis and its tiles' shape: what takes least time, a part at
+// least 8 stages (512 vocabulary entries) long.
+void plan_dx(int tokens, int hidden, int k, int* parts, bool* dual) {
   const int stages = ceil_div(k, 64);
-  int best = 1;
-  double best_time = 1e300;
-  for (int s = 1; s <= 32 && (s == 1 || stages / s >= 8); ++s) {
-    const int per = ceil_div(stages, s);
-    if (ceil_div(stages, per) != s) continue;
-    const double time = double(ceil_div(tiles * s, kPairs)) * (per + 12);   // about 12 stages' time to start and drain
-    if (time < 0.95 * best_time) {
-      best = s;
-      best_time = time;
+  const int forced = option(TKG_OPT_BF16_TILE_N);
+  double best = 1e300;
+  for (int d = 0; d < 2; ++d) {
+    if ((forced == 256 && d) || (forced == 512 && !d)) continue;
+    const int tiles = ceil_div(hidden, 256) * ceil_div(tokens, d ? 512 : 256);
+    for (int s = 1; s <= 32 && (s == 1 || stages / s >= 8); ++s) {
+      const int per = ceil_div(stages, s);
+      if (ceil_div(stages, per) != s) continue;
+      const double time = train_rounds(double(tiles) * s) * train_tile_time(per, d != 0);
+      if (time < 0.97 * best) {
+        best = time;
+        *parts = s;
+        *dual = d != 0;
+      }
     }
   }
-  return best;
 }
 
 GradPlan grad_plan(int tokens, int vocab, int hidden, int piece) {
   GradPlan pl{};
   pl.piece = piece > 0 ? (piece < vocab ? piece : vocab) : default_piece(tokens, vocab);
   pl.pieces = ceil_div(vocab, pl.piece);
-  pl.parts = dx_parts(tokens, hidden, pl.piece);
+  plan_dx(tokens, hidden, pl.piece, &pl.parts, &pl.dx_dual);
   pl.tokens_up = round_up(size_t(tokens), 64);
   pl.g_off = round_up(size_t(tokens) * size_t(hidden) * 2, 256);
   pl.part_off = pl.g_off + round_up(size_t(pl.piece) * pl.tokens_up * 2, 256);
@@ -391,7 +394,9 @@ tkg_status tkg_linear_ce_grad(int tokens, int vocab, int hidden, const void* X, 
       if ((st = map_prefetch(&extra.d, part, hidden, tokens, pl.parts, pl.tokens_up * 4,
                              size_t(hidden) * pl.tokens_up * 4)) != TKG_OK)
         return st;
-      if ((st = launch_train<true, true, EPI_F32, GRP_NONE>(tmA, tmB, tmD, q, stream, extra)) != TKG_OK) return st;
+      st = pl.dx_dual ? launch_train<true, true, EPI_F32, GRP_NONE, SHAPE_DUAL>(tmA, tmB, tmD, q, stream, extra)
+                      : launch_train<true, true, EPI_F32, GRP_NONE>(tmA, tmB, tmD, q, stream, extra);
+      if (st != TKG_OK) return st;
     }
     if (dW) {
       // rows [v0, v0 + nv) of dW = g (c / s X)
@@ -411,7 +416,9 @@ tkg_status tkg_linear_ce_grad(int tokens, int vocab, int hidden, const void* X, 
                         size_t(nv) * size_t(lddw) * es, es == 4)) != TKG_OK)
         return st;
       if (es == 2) {
-        st = launch_train<false, true, EPI_BF16, GRP_NONE>(tmA, tmB, tmD, q, stream);
+        st = train_dual(nv, hidden, 1, ceil_div(tokens, 64))
+                 ? launch_train<false, true, EPI_BF16, GRP_NONE, SHAPE_DUAL>(tmA, tmB, tmD, q, stream)
+                 : launch_train<false, true, EPI_BF16, GRP_NONE>(tmA, tmB, tmD, q, stream);
       } else {
         ExtraMaps<EPI_F32, GRP_NONE> extra{};
         if ((st = map_prefetch(&extra.d, static_cast<float*>(dW) + size_t(v0) * size_t(lddw), nv, hidden, 1,

@@ -17,7 +17,8 @@ static tkg_status launch_logits(const void* X, size_t x_bytes, const void* W, si
     return st;
   p.splits = 1;
   p.split_stages = ceil_div(p.k, 64);
-  if (EPI == EPI_LOSS && p.n <= kNarrowTokens) return launch_train<false, false, EPI, GRP_NONE, true>(tmA, tmB, tmD, p, stream);
+  if constexpr (EPI == EPI_LOSS)
+    if (p.n <= kNarrowTokens) return launch_train<false, false, EPI, GRP_NONE, SHAPE_NARROW>(tmA, tmB, tmD, p, stream);
   return launch_train<false, false, EPI, GRP_NONE>(tmA, tmB, tmD, p, stream);
 }
 

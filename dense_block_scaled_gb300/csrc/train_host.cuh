@@ -46,15 +46,16 @@ constexpr int kTileBF16 = 64, kTileF32 = 32, kTileTokens = 16;
 
 // Fills the fields common to every launch and launches.  The caller sets p.m, n,
 // k, n_tile, alpha, splits and split_stages (GRP_NONE) and the epilogue's own fields.
-template <bool A_MN, bool B_MN, int EPI, int GRP, bool NARROW = false>
+template <bool A_MN, bool B_MN, int EPI, int GRP, int SHAPE = SHAPE_WIDE>
 tkg_status launch_train(const CUtensorMap& tmA, const CUtensorMap& tmB, const CUtensorMap& tmD, TrainParams p,
                         cudaStream_t stream,
                         const ExtraMaps<EPI, GRP>& extra = {}) {
-  using C = TrainConfig<A_MN, B_MN, EPI, GRP, NARROW>;
-  auto kern = train_kernel<A_MN, B_MN, EPI, GRP, NARROW>;
+  using C = TrainConfig<A_MN, B_MN, EPI, GRP, SHAPE>;
+  auto kern = train_kernel<A_MN, B_MN, EPI, GRP, SHAPE>;
   // a block that takes all of tensor memory takes more than half of shared memory too, so that no two share an SM
-  static_assert(NARROW || C::kSmemBytes > 118784, "one CTA per SM");
-  if (p.n_tile > C::kBN) return TKG_ERR_UNSUPPORTED;   // (no caller asks for it)
+  static_assert(C::kNarrow || C::kSmemBytes > 118784, "one CTA per SM");
+  if (C::kDual) p.n_tile = 2 * kTrainBN;
+  if (p.n_tile > C::kSubs * C::kBN) return TKG_ERR_UNSUPPORTED;   // (no caller asks for it)
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return TKG_ERR_CUDA;
   static bool attr_set[64] = {};   // per instantiation and device (idempotent if two threads race)
@@ -76,13 +77,12 @@ tkg_status launch_train(const CUtensorMap& tmA, const CUtensorMap& tmB, const CU
   // what a stage of one CTA takes and brings: A's 128 rows (fewer when there are fewer) or two chunks, and
   // its half of B's n_tile
   const int kb = GRP == GRP_K ? 64 : int(mn_box_rows(p.k));   // k rows of an MN-major box
-  const int half = p.n_tile / 2;
+  const int half = p.n_tile / 2 / C::kSubs;
   const int a_bytes = A_MN ? 2 * kb * 128 : (p.m < 128 ? p.m : 128) * 128;
-  const int b_rows = GRP == GRP_ROWS ? (half + 31) / 32 * 32 : half;
-  const int b_slot = B_MN ? ceil_div(half, 64) * kTrainChunk : b_rows * 128;
-  const int b_bytes = B_MN ? ceil_div(half, 64) * kb * 128 : (p.n < half ? p.n : half) * 128;
-  p.tx_bytes = uint32_t(2 * (a_bytes + (GRP == GRP_ROWS ? 0 : b_bytes)));
-  p.stage_bytes = uint32_t(C::kABytes + b_slot);
+  const int b_slot = B_MN ? (GRP == GRP_K ? 2 : ceil_div(half, 64)) * kTrainChunk : (GRP == GRP_ROWS ? (half + 31) / 32 * 32 : half) * 128;
+  p.tx_a = uint32_t(2 * a_bytes);
+  p.tx_box = uint32_t(2 * (B_MN ? kb : (GRP == GRP_ROWS ? 32 : (p.n < half ? p.n : half))) * 128);
+  p.stage_bytes = uint32_t(C::kABytes + C::kSubs * b_slot);
   p.stages = C::kRingBytes / int(p.stage_bytes);
   if (p.stages > kTrainMaxStages) p.stages = kTrainMaxStages;
   p.raster_group = raster_group(256, GRP == GRP_K ? ceil_div(p.k, p.groups) : p.k, FMT_BF16, p.tiles_m);
@@ -118,6 +118,32 @@ tkg_status launch_train(const CUtensorMap& tmA, const CUtensorMap& tmB, const CU
     return TKG_ERR_CUDA;
   }
   return TKG_OK;
+}
+
+// Rounds of `tiles` on the GB300's 76 CTA pairs: whole ones while they are few; with more the clusters have
+// drifted apart and the last one overlaps.
+constexpr int kPairs = 76;
+inline double train_rounds(double tiles) {
+  const double r = tiles / kPairs;
+  return r < 4.0 ? double((long long)(r + 0.999999)) : r + 0.5;
+}
+// Time of a round of tiles in units of a 64-k stage of a 256-wide tile: a 512-wide tile's stage takes 4% less
+// than two, its start and read-out as long as two.  Under the power cap, back to back, 8 groups of 256, 512, 1024
+// and 2048 rows of 4096 x 7168 took 123.7, 200.9, 339 and 610 us in 256-wide tiles and 122.8, 192.0, 327 and 593
+// in 512-wide ones, 8192 rows of 32768 x 4096 1366 and 1308.  Sums of one to three stages have their read-outs
+// exposed on the wide tiles (8 groups of 64 rows: 81 against 92 us).
+inline double train_tile_time(int stages, bool dual) { return dual ? 1.92 * stages + 16 : stages + 8.0; }
+
+// Whether `count` products of m x n with `stages` stages per tile run on 256 x 512 tiles.  TKG_OPT_BF16_TILE_N
+// (256 or 512) decides it instead.
+inline bool train_dual(int m, int n, long long count, int stages) {
+  const int forced = option(TKG_OPT_BF16_TILE_N);
+  if (forced == 512) return true;
+  if (forced == 256) return false;
+  if (stages < 4) return false;
+  const double rows = double(ceil_div(m, 256)) * double(count);
+  return train_rounds(rows * ceil_div(n, 512)) * train_tile_time(stages, true) <
+         train_rounds(rows * ceil_div(n, 256)) * train_tile_time(stages, false);
 }
 
 // At most this many tokens take the kernel's narrow form.

@@ -34,6 +34,10 @@
 // tokens leave most of a stage to the weights (bytes in flight are what a
 // bandwidth-bound call needs).
 //
+// DUAL (weight gradients and dX with long sums): 256 x 512 tiles, A's stage shared by
+// two MMAs.  The SMs read a quarter fewer bytes from L2 for the same products;
+// these kernels run under the power cap, where that shows as clock.
+//
 // NARROW (at most 128 tokens, where reading the weights bounds the time): two
 // blocks per SM, each with half the shared and tensor memory and 4 epilogue warps.
 // Twice the tiles run at once, so that few tiles do not leave a thin last round,
@@ -66,17 +70,19 @@ enum : int { EPI_LOSS = 0, EPI_DLOGITS = 1, EPI_BF16 = 2, EPI_F32 = 3, EPI_BF16_
 // GRP_ROWS: groups of consecutive n, each with its own A; GRP_K: groups of
 // consecutive k, each with its own output matrix.  Row counts in device memory.
 enum : int { GRP_NONE = 0, GRP_ROWS = 1, GRP_K = 2 };
+// Tile shapes: 256 x up to 256; NARROW 256 x up to 128, two blocks per SM; DUAL 256 x 512.
+enum : int { SHAPE_WIDE = 0, SHAPE_NARROW = 1, SHAPE_DUAL = 2 };
 
 struct TrainParams {
   int m, n, k;                 // output rows and columns, contraction length (GRP_ROWS: n, GRP_K: k is the row capacity)
   int kstages;                 // ceil(k / 64)
   int splits, split_stages;    // k split: part z covers stages [z * split_stages, ...)
   int tiles_m, tiles_n, num_tiles;
-  int n_tile;                  // tile width, a multiple of 16 (GRP_ROWS: per group, by its rows)
+  int n_tile;                  // tile width, a multiple of 16 (GRP_ROWS: per group, by its rows; DUAL: 512)
   int raster_group;
   int stages;                  // ring slots, and the bytes of one in each CTA
   uint32_t stage_bytes;
-  uint32_t tx_bytes;           // bytes landing on the leader's full barrier per stage (GRP_ROWS: of A)
+  uint32_t tx_a, tx_box;       // bytes landing on the leader's full barrier per stage: of A, and of one box of B in each CTA
   float alpha;
   const float* scale;          // device, may be null: multiplies alpha
   unsigned int* status;
@@ -98,9 +104,10 @@ struct TrainParams {
   int groups;
 };
 
-// GRP_K: A and B in boxes of 16, 4 and 1 k rows, for the stage in which a group ends.
+// GRP_K: A and B in boxes of 16, 8, 4, 2 and 1 k rows, for the stage in which a group ends.
+constexpr int kTailMaps = 5;
 struct TailMaps {
-  CUtensorMap a[3], b[3];
+  CUtensorMap a[kTailMaps], b[kTailMaps];
 };
 // F32: D in boxes of 256 columns by 32 rows, to fetch into L2 what is about to be added to.
 struct PrefetchMap {
@@ -212,11 +219,15 @@ __device__ __forceinline__ int column_of_lane(int lane) {
 constexpr int kTrainBN = 256;         // widest tile
 constexpr int kTrainMaxStages = 12;
 
-template <bool A_MN, bool B_MN, int EPI, int GRP, bool NARROW>
+template <bool A_MN, bool B_MN, int EPI, int GRP, int SHAPE>
 struct TrainConfig {
-  static constexpr int kBN = NARROW ? 128 : kTrainBN;      // widest tile, and columns of an accumulator
-  static constexpr int kEpiWarps = NARROW ? 4 : 16;
-  static constexpr int kChunks = kBN / 32 / (kEpiWarps / 4);   // 32-column chunks of a tile per epilogue warp
+  static constexpr bool kNarrow = SHAPE == SHAPE_NARROW, kDual = SHAPE == SHAPE_DUAL;
+  static constexpr int kBN = kNarrow ? 128 : kTrainBN;     // columns of an accumulator, and widest MMA
+  static constexpr int kSubs = kDual ? 2 : 1;              // accumulators of a tile
+  static constexpr int kEpiWarps = kNarrow ? 4 : (kDual ? 8 : 16);
+  static constexpr int kChunks = kBN / 32 / (kEpiWarps / 4);   // 32-column chunks of an accumulator per epilogue warp
+  // DUAL: stages at a tile's start and end in which the first accumulator runs ahead of the second
+  static constexpr int kSkew = 2;
   static constexpr int kThreads = 32 * (4 + kEpiWarps);
   static constexpr int kAcc = 2;
   static constexpr int kABytes = 128 * 128;
@@ -231,9 +242,11 @@ struct TrainConfig {
   // epilogue buffers, barriers, two scheduler answers, table, 1024-byte alignment; the rest is the ring's
   static constexpr int kFixedBytes = kEpiBytes + kNumBars * 8 + 2 * 16 + 16 + kTabInts * 4 + 1024;
   // all an SM gives a block, or two blocks, less the two static words
-  static constexpr int kSmemBytes = (NARROW ? 116736 - 1024 : 232448) - 16;
+  static constexpr int kSmemBytes = (kNarrow ? 116736 - 1024 : 232448) - 16;
   static constexpr int kRingBytes = (kSmemBytes - kFixedBytes) / 1024 * 1024;
-  static_assert(kRingBytes >= (NARROW ? 4 : 6) * (kABytes + kBN / 2 * 128), "four or six stages of the widest tiles");
+  static_assert(kRingBytes >= (SHAPE == SHAPE_WIDE ? 6 : 4) * (kABytes + kSubs * kBN / 2 * 128),
+                "four or six stages of the widest tiles");
+  static_assert(!kDual || (B_MN && (EPI == EPI_BF16 || EPI == EPI_F32) && GRP != GRP_ROWS), "not built");
   static constexpr bool kClc = GRP != GRP_ROWS;     // GRP_ROWS: the tile count is known on the device only
   // readers of a scheduler answer: producer (GRP_K: two) and epilogue warps per CTA, MMA issuer and scheduler
   static constexpr int kClcConsumers = 2 * ((GRP == GRP_K ? 2 : 1) + kEpiWarps) + 2;
@@ -249,21 +262,22 @@ __host__ __device__ constexpr int train_n_tile(int n, int multiple) {
 
 struct TrainTile {
   int mb, nb;
-  int a0, b0;        // this CTA's first m of A and first n of B
+  int a0;            // this CTA's first m of A
   int n0, n_end;     // the tile's first column, and where its columns (or its group's) end
   int nt;            // MMA width
+  int subs;          // accumulators
   int z;             // k part (GRP_NONE) or group
   int k0;            // GRP_K: the group's first row
   int ks0, nks;      // first k stage (from k0) and number of stages
   int k_end;         // contraction stops here (from k0)
 };
 
-template <bool A_MN, bool B_MN, int EPI, int GRP, bool NARROW>
-__global__ void __launch_bounds__(TrainConfig<A_MN, B_MN, EPI, GRP, NARROW>::kThreads, NARROW ? 2 : 1)
+template <bool A_MN, bool B_MN, int EPI, int GRP, int SHAPE>
+__global__ void __launch_bounds__(TrainConfig<A_MN, B_MN, EPI, GRP, SHAPE>::kThreads, SHAPE == SHAPE_NARROW ? 2 : 1)
     train_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                  const __grid_constant__ CUtensorMap tmD, const TrainParams p,
                  const __grid_constant__ ExtraMaps<EPI, GRP> extra) {
-  using C = TrainConfig<A_MN, B_MN, EPI, GRP, NARROW>;
+  using C = TrainConfig<A_MN, B_MN, EPI, GRP, SHAPE>;
   constexpr int CG = 2;
   constexpr int ACC = C::kAcc;
   extern __shared__ uint8_t smem_raw[];
@@ -312,6 +326,7 @@ __global__ void __launch_bounds__(TrainConfig<A_MN, B_MN, EPI, GRP, NARROW>::kTh
       const int rows = s_tab[kTabRows + lo], row0 = s_tab[kTabRow0 + lo];
       tile_coords(t - s_tab[kTabTile + lo], p.tiles_m, (rows + kTrainBN - 1) / kTrainBN, p.raster_group, tc.mb, tc.nb);
       tc.nt = train_n_tile(rows, 16);
+      tc.subs = 1;
       tc.n0 = row0 + tc.nb * tc.nt;
       tc.n_end = min(tc.n0 + tc.nt, row0 + rows);
       tc.z = s_group[lo];
@@ -323,9 +338,10 @@ __global__ void __launch_bounds__(TrainConfig<A_MN, B_MN, EPI, GRP, NARROW>::kTh
       const int per = p.tiles_m * p.tiles_n;
       const int z = t / per;
       tile_coords(t - z * per, p.tiles_m, p.tiles_n, p.raster_group, tc.mb, tc.nb);
-      tc.nt = p.n_tile;
+      tc.nt = C::kDual ? kTrainBN : p.n_tile;
       tc.n0 = tc.nb * p.n_tile;
       tc.n_end = min(tc.n0 + p.n_tile, p.n);
+      tc.subs = C::kDual && tc.n_end - tc.n0 > kTrainBN ? 2 : 1;
       tc.k0 = 0;
       if constexpr (GRP == GRP_K) {   // the groups with most rows first
         tc.z = s_group[z];
@@ -341,8 +357,20 @@ __global__ void __launch_bounds__(TrainConfig<A_MN, B_MN, EPI, GRP, NARROW>::kTh
       }
     }
     tc.a0 = tc.mb * 256 + int(rank) * 128;
-    tc.b0 = tc.n0 + int(rank) * (tc.nt >> 1);
     return tc;
+  };
+  // MMA width of a tile's accumulator (the last of a DUAL tile as wide as it has columns, in store boxes), this
+  // CTA's first n of B in it, and the boxes it is loaded in: GRP_ROWS 32 rows each (tiles differ in width),
+  // K-major otherwise one, MN-major 64 columns each (GRP_K: always two)
+  auto width = [&](const TrainTile& tc, int sub) {
+    return C::kDual ? min(kTrainBN, (tc.n_end - tc.n0 - sub * kTrainBN + 31) & ~31) : tc.nt;
+  };
+  auto first_n = [&](const TrainTile& tc, int sub) {
+    return tc.n0 + sub * kTrainBN + int(rank) * (width(tc, sub) >> 1);
+  };
+  auto boxes = [&](const TrainTile& tc, int sub) {
+    if (GRP == GRP_K) return 2;
+    return (GRP == GRP_ROWS || B_MN) ? ((width(tc, sub) >> 1) + (B_MN ? 63 : 31)) / (B_MN ? 64 : 32) : 1;
   };
 
   if (threadIdx.x == 0) {
@@ -370,7 +398,7 @@ __global__ void __launch_bounds__(TrainConfig<A_MN, B_MN, EPI, GRP, NARROW>::kTh
   }
   // Two narrow blocks share an SM, one of them perhaps of the next kernel: it takes tensor memory only once the
   // previous kernel is done, as a block that holds some while it waits could keep that kernel from getting its own
-  if (NARROW) ptx::pdl_wait();
+  if (C::kNarrow) ptx::pdl_wait();
   if (warp == 2) {
     ptx::tmem_alloc<CG>(ptx::smem_u32(&s_tmem_base), uint32_t(2 * C::kBN));
     ptx::tmem_relinquish<CG>();
@@ -479,12 +507,17 @@ __global__ void __launch_bounds__(TrainConfig<A_MN, B_MN, EPI, GRP, NARROW>::kTh
         return -2;
       uint32_t x = 0;
       const bool got = ptx::clc_read(clc_resp(cslot), x);
+      // The slot is overwritten (through the async proxy) once every reader has arrived, so the read has to be over
+      // before the arrival: its address depends on the value read (x is below 2^31).  Without that the role that
+      // arrives last, the MMA issuer, now and then read the answer after next, missed a tile, and the kernel ran
+      // into its wait limit.  (A proxy fence by every reader cost 0.5 us a tile; the scheduler has the one.)
       if constexpr (WARP) __syncwarp();
       if (!WARP || lane == 0) {
+        const uint32_t bar = clc_empty(cslot) + (x >> 31);
         if (leader)
-          ptx::mbar_arrive(clc_empty(cslot));
+          ptx::mbar_arrive(bar);
         else
-          ptx::mbar_arrive_relaxed_cluster(ptx::map_to_rank(clc_empty(cslot), 0));
+          ptx::mbar_arrive_relaxed_cluster(ptx::map_to_rank(bar, 0));
       }
       if (++cslot == 2) {
         cslot = 0;
@@ -506,7 +539,7 @@ __global__ void __launch_bounds__(TrainConfig<A_MN, B_MN, EPI, GRP, NARROW>::kTh
       uint32_t armed = 0, armed_par = 0;   // stages whose last arming is not yet known complete, and its parity
       bool ok = true;
       uint32_t cslot = 0, cphase = 0;
-      if (GRP == GRP_NONE && !NARROW) ptx::pdl_wait();
+      if (GRP == GRP_NONE && !C::kNarrow) ptx::pdl_wait();
 #pragma unroll 1
       for (int t = first_tile; t >= 0 && ok;) {
         const TrainTile tc = coords(t);
@@ -517,13 +550,12 @@ __global__ void __launch_bounds__(TrainConfig<A_MN, B_MN, EPI, GRP, NARROW>::kTh
           if (p.accumulate && tc.nks > 0) {
 #pragma unroll 1
             for (int r = 0; r < 128 && tc.a0 + r < p.m; r += 32)
-              ptx::tma_prefetch_3d(&extra.d, tc.n0, tc.a0 + r, tc.z);
+              for (int sub = 0; sub < tc.subs; ++sub)
+                ptx::tma_prefetch_3d(&extra.d, tc.n0 + sub * kTrainBN, tc.a0 + r, tc.z);
           }
         }
-        // boxes of B: GRP_ROWS 32 rows each (the tiles' widths differ), K-major otherwise one of the tile's
-        // half, MN-major 64 columns each
-        const int nbox = (GRP == GRP_ROWS || B_MN) ? ((tc.nt >> 1) + (B_MN ? 63 : 31)) / (B_MN ? 64 : 32) : 1;
-        const uint32_t txb = GRP == GRP_ROWS ? p.tx_bytes + uint32_t(2 * 32 * 128 * nbox) : p.tx_bytes;
+        const int all_boxes = boxes(tc, 0) + (tc.subs == 2 ? boxes(tc, 1) : 0);
+        const uint32_t txb = p.tx_a + uint32_t(all_boxes) * p.tx_box;
 #pragma unroll 1
         for (int it = 0; it < tc.nks; ++it) {
           const int k0 = (tc.ks0 + it) * 64;
@@ -536,37 +568,44 @@ __global__ void __launch_bounds__(TrainConfig<A_MN, B_MN, EPI, GRP, NARROW>::kTh
           // GRP_K: rows of this stage, when the group ends in it
           const int last = GRP == GRP_K ? tc.k_end - it * 64 : 64;
           if (leader) {
-            // (the rows there are and those up to the MMA's 16, of four chunks in each CTA)
-            ptx::mbar_arrive_expect_tx(full_bar(stage), last < 64 ? uint32_t(2 * 4 * 128) * ((uint32_t(last) + 15u) & ~15u) : txb);
+            // (the rows there are and those up to the MMA's 16, of A's and B's chunks in each CTA)
+            ptx::mbar_arrive_expect_tx(full_bar(stage), last < 64 ? uint32_t(2 * (2 + all_boxes) * 128) *
+                                                                        ((uint32_t(last) + 15u) & ~15u)
+                                                                  : txb);
             armed |= 1u << stage;
             armed_par = (armed_par & ~(1u << stage)) | (phase << stage);
           }
           // a tile of this launch, a ring slot, 16-byte aligned x (TMA's rule), the box inside the stage
           if (invariant(t < num_tiles && stage < nstages && tc.z >= 0 && (!A_MN || tc.a0 % 8 == 0) &&
-                            (!B_MN || tc.b0 % 8 == 0) && tc.nt >= 16 && tc.nt <= C::kBN,
+                            (!B_MN || first_n(tc, 0) % 8 == 0) && tc.nt >= 16 && tc.nt <= C::kBN,
                         p.status)) {
             if (GRP == GRP_K && last < 64) {
               ptx::mbar_arrive(tail_go(stage));   // the stage is free and armed: warp 3 loads it
             } else {
-            if constexpr (A_MN) {
+              if constexpr (A_MN) {
 #pragma unroll
-              for (int c = 0; c < 2; ++c) {
-                const uint32_t dst = stage_a(stage) + uint32_t(c * kTrainChunk);
-                if constexpr (GRP == GRP_ROWS)
-                  ptx::tma_load_3d<CG>(dst, mA, tc.a0 + c * 64, k0, tc.z, fb, pol_a);
-                else
-                  ptx::tma_load_2d<CG>(dst, mA, tc.a0 + c * 64, tc.k0 + k0, fb, pol_a);
+                for (int c = 0; c < 2; ++c) {
+                  const uint32_t dst = stage_a(stage) + uint32_t(c * kTrainChunk);
+                  if constexpr (GRP == GRP_ROWS)
+                    ptx::tma_load_3d<CG>(dst, mA, tc.a0 + c * 64, k0, tc.z, fb, pol_a);
+                  else
+                    ptx::tma_load_2d<CG>(dst, mA, tc.a0 + c * 64, tc.k0 + k0, fb, pol_a);
+                }
+              } else {
+                ptx::tma_load_2d<CG>(stage_a(stage), mA, k0, tc.a0, fb, pol_a);
               }
-            } else {
-              ptx::tma_load_2d<CG>(stage_a(stage), mA, k0, tc.a0, fb, pol_a);
-            }
 #pragma unroll 1
-            for (int c = 0; c < nbox; ++c) {
-              if constexpr (B_MN)
-                ptx::tma_load_2d<CG>(stage_b(stage) + uint32_t(c * kTrainChunk), mB, tc.b0 + c * 64, tc.k0 + k0, fb, pol_b);
-              else
-                ptx::tma_load_2d<CG>(stage_b(stage) + uint32_t(c * 32 * 128), mB, k0, tc.b0 + c * 32, fb, pol_b);
-            }
+              for (int sub = 0; sub < tc.subs; ++sub) {
+                const uint32_t dst = stage_b(stage) + uint32_t(sub * kTrainBN / 2 * 128);
+                const int b0 = first_n(tc, sub), nbox = boxes(tc, sub);
+#pragma unroll 1
+                for (int c = 0; c < nbox; ++c) {
+                  if constexpr (B_MN)
+                    ptx::tma_load_2d<CG>(dst + uint32_t(c * kTrainChunk), mB, b0 + c * 64, tc.k0 + k0, fb, pol_b);
+                  else
+                    ptx::tma_load_2d<CG>(dst + uint32_t(c * 32 * 128), mB, k0, b0 + c * 32, fb, pol_b);
+                }
+              }
             }
           }
           if (++stage == nstages) {
@@ -593,52 +632,109 @@ __global__ void __launch_bounds__(TrainConfig<A_MN, B_MN, EPI, GRP, NARROW>::kTh
   // ------------------------------------------------------------------ MMA issuer
   else if (warp == 1) {
     if (leader && ptx::elect_one()) {
-      uint32_t stage = 0, phase = 0, acc = 0, accph = 0;
+      uint32_t stage = 0, phase = 0, acc = 0;
+      uint32_t accbits = 0;           // parity of each accumulator's next use
+      uint32_t uses0 = 0, uses1 = 0;
       bool ok = true;
       if (p.inject_stall) ok = wait_bar<false>(never_bar, 0u, ctl);
       const uint16_t mask = 0x3;
       uint32_t cslot = 0, cphase = 0;
-      uint32_t committed = 0;
+      // the four MMAs of stage s (the tile's stage `it`) into one accumulator
+      auto issue = [&](const TrainTile& tc, uint32_t s, int it, uint32_t acc, uint32_t sub) {
+        const uint64_t adesc = A_MN ? sdesc_mn_sw128(stage_a(s)) : sdesc_sw128(stage_a(s));
+        const uint32_t b = stage_b(s) + sub * uint32_t(kTrainBN / 2 * 128);
+        const uint64_t bdesc = B_MN ? sdesc_mn_sw128(b) : sdesc_sw128(b);
+        const uint32_t idesc = idesc_with_n(C::kIdesc, width(tc, int(sub)));
+        const int left = tc.k_end - (tc.ks0 + it) * 64;   // k past it are zero, or not there
+        const bool stage_ok = invariant(s < nstages && acc < uint32_t(ACC) && tc.nt <= C::kBN, p.status);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          if (j * 16 >= left || !stage_ok) break;
+          // 16 k: 32 bytes along K-major rows, two 8-k groups of 1024 bytes in MN-major chunks
+          const uint64_t aoff = A_MN ? uint64_t((j * 2048) >> 4) : uint64_t((j * 32) >> 4);
+          const uint64_t boff = B_MN ? uint64_t((j * 2048) >> 4) : uint64_t((j * 32) >> 4);
+          ptx::mma_f16<CG>(tmem + acc * uint32_t(C::kBN), adesc + aoff, bdesc + boff, idesc, (it > 0 || j > 0) ? 1u : 0u);
+        }
+      };
+      auto acc_free = [&](uint32_t acc) {   // the epilogue has handed it back
+        if (!wait_bar<true>(acce_bar(acc), ((accbits >> acc) & 1u) ^ 1u, ctl)) return false;
+        accbits ^= 1u << acc;
+        if (acc) ++uses1; else ++uses0;
+        ptx::tc_fence_after();
+        return true;
+      };
+      auto advance = [&](uint32_t& s) {
+        if (++s == nstages) s = 0;
+        return s == 0;
+      };
 #pragma unroll 1
       for (int t = first_tile; t >= 0 && ok;) {
-        if (!wait_bar<true>(acce_bar(acc), accph ^ 1u, ctl)) {
-          ok = false;
-          break;
-        }
-        ptx::tc_fence_after();
-        const uint32_t d_tmem = tmem + acc * uint32_t(C::kBN);
         const TrainTile tc = coords(t);
-        const uint32_t idesc = idesc_with_n(C::kIdesc, tc.nt);
-#pragma unroll 1
-        for (int it = 0; it < tc.nks; ++it) {
-          if (!wait_bar<false>(full_bar(stage), phase, ctl)) {
+        if constexpr (!C::kDual) {
+          if (!acc_free(acc)) {
             ok = false;
             break;
           }
-          const uint64_t adesc = A_MN ? sdesc_mn_sw128(stage_a(stage)) : sdesc_sw128(stage_a(stage));
-          const uint64_t bdesc = B_MN ? sdesc_mn_sw128(stage_b(stage)) : sdesc_sw128(stage_b(stage));
-          const int left = tc.k_end - (tc.ks0 + it) * 64;   // k past it are zero, or not there
-          const bool stage_ok = invariant(stage < nstages && acc < uint32_t(ACC) && tc.nt <= C::kBN, p.status);
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            if (j * 16 >= left || !stage_ok) break;
-            // 16 k: 32 bytes along K-major rows, two 8-k groups of 1024 bytes in MN-major chunks
-            const uint64_t aoff = A_MN ? uint64_t((j * 2048) >> 4) : uint64_t((j * 32) >> 4);
-            const uint64_t boff = B_MN ? uint64_t((j * 2048) >> 4) : uint64_t((j * 32) >> 4);
-            ptx::mma_f16<CG>(d_tmem, adesc + aoff, bdesc + boff, idesc, (it > 0 || j > 0) ? 1u : 0u);
+#pragma unroll 1
+          for (int it = 0; it < tc.nks; ++it) {
+            if (!wait_bar<false>(full_bar(stage), phase, ctl)) {
+              ok = false;
+              break;
+            }
+            issue(tc, stage, it, acc, 0);
+            ptx::tc_commit<CG>(empty_bar(stage), mask);
+            if (advance(stage)) phase ^= 1u;
           }
-          ptx::tc_commit<CG>(empty_bar(stage), mask);
-          if (++stage == nstages) {
-            stage = 0;
-            phase ^= 1u;
+          if (!ok) break;
+          ptx::tc_commit<CG>(accf_bar(acc), mask);
+          acc ^= 1u;
+        } else {
+          // Both accumulators take every stage, but the first runs kSkew stages ahead at the start, while the
+          // second is still being read out, and finishes kSkew stages early, so that its read-out begins under
+          // the second's last MMAs.  A stage is given back when the second has used it.
+          const bool two = tc.subs == 2;
+          const int lead = two ? min(C::kSkew, tc.nks) : 0, trail = two ? min(C::kSkew, tc.nks - lead) : 0;
+          ok = acc_free(0);
+          uint32_t behind = stage;      // the second accumulator's next stage
+#pragma unroll 1
+          for (int it = 0; it < tc.nks && ok; ++it) {
+            if (!wait_bar<false>(full_bar(stage), phase, ctl)) {
+              ok = false;
+              break;
+            }
+            if (it == lead && two) {    // catch up
+              if (!acc_free(1)) {
+                ok = false;
+                break;
+              }
+              for (int i = 0; i < lead; ++i) {
+                issue(tc, behind, i, 1, 1);
+                ptx::tc_commit<CG>(empty_bar(behind), mask);
+                advance(behind);
+              }
+            }
+            issue(tc, stage, it, 0, 0);
+            if (!two || (it >= lead && it < tc.nks - trail)) {
+              if (two) issue(tc, stage, it, 1, 1);
+              ptx::tc_commit<CG>(empty_bar(stage), mask);
+              advance(behind);
+            }
+            if (advance(stage)) phase ^= 1u;
           }
-        }
-        if (!ok) break;
-        ptx::tc_commit<CG>(accf_bar(acc), mask);
-        ++committed;
-        if (++acc == uint32_t(ACC)) {
-          acc = 0;
-          accph ^= 1u;
+          if (!ok) break;
+          ptx::tc_commit<CG>(accf_bar(0), mask);
+          if (two) {
+            if (tc.nks <= lead && !acc_free(1)) {   // no stage came after the lead: it has not caught up
+              ok = false;
+              break;
+            }
+            for (int i = tc.nks <= lead ? 0 : tc.nks - trail; i < tc.nks; ++i) {
+              issue(tc, behind, i, 1, 1);
+              ptx::tc_commit<CG>(empty_bar(behind), mask);
+              advance(behind);
+            }
+            ptx::tc_commit<CG>(accf_bar(1), mask);
+          }
         }
         t = next_tile(Lane{}, t, cslot, cphase);
         if (t == -2) ok = false;
@@ -650,79 +746,84 @@ __global__ void __launch_bounds__(TrainConfig<A_MN, B_MN, EPI, GRP, NARROW>::kTh
       quiet.abort_flag = &dummy;
       wait_bar<false>(drain_bar, 0u, quiet);
       if (ok) {
-#pragma unroll 1
-        for (uint32_t a = 0; a < uint32_t(ACC); ++a) {
-          const uint32_t uses = committed / uint32_t(ACC) + (a < committed % uint32_t(ACC) ? 1u : 0u);
-          if (uses) wait_bar<true>(acce_bar(a), (uses & 1u) ^ 1u, quiet);
-        }
+        if (uses0) wait_bar<true>(acce_bar(0), (uses0 & 1u) ^ 1u, quiet);
+        if (uses1) wait_bar<true>(acce_bar(1), (uses1 & 1u) ^ 1u, quiet);
       }
     }
     __syncwarp();
   }
   // ------------------------------------------------------------------ producer of the stages where groups end
   // The group's last rows, and zeros (rows past the capacity) up to the MMA's 16: what follows in memory is the
-  // next group's and may hold anything.  Boxes of 16, 4 and 1 rows, up to 40 copies a stage, beside the main
-  // producer, which goes on with the next tile (8 experts of 2048 rows, 4096 x 7168: 616 us with one producer).
-  // The 128-byte swizzle goes by the shared-memory address, so a box may start at any row of a chunk.
+  // next group's and may hold anything.  Boxes of 16, 8, 4, 2 and 1 rows, up to 40 copies a stage, beside the main
+  // producer, which goes on with the next tile (issued by that one too they made 8 experts of 2048 rows, 4096 x
+  // 7168, 6% longer).  One lane issues them in a short loop: one copy per lane, or the loop with its bounds computed
+  // inside, took 106 us in place of 80 on 8 experts of few rows.  The 128-byte swizzle goes by the shared-memory
+  // address, so a box may start at any row of a chunk.
   else if (warp == 3) {
     if constexpr (GRP == GRP_K) {
-      if (ptx::elect_one()) {
-        const uint64_t pol = ptx::policy_evict_normal();
-        const uint32_t lead_full0 = ptx::map_to_rank(full_bar(0), 0);
-        uint32_t stage = 0;
-        uint32_t turns = 0;   // parity of each stage's next hand-over
-        bool ok = true;
-        uint32_t cslot = 0, cphase = 0;
+      const uint64_t pol = ptx::policy_evict_normal();
+      const uint32_t lead_full0 = ptx::map_to_rank(full_bar(0), 0);
+      uint32_t stage = 0;
+      uint32_t turns = 0;   // parity of each stage's next hand-over
+      uint32_t cslot = 0, cphase = 0;
 #pragma unroll 1
-        for (int t = first_tile; t >= 0 && ok;) {
-          const TrainTile tc = coords(t);
-          stage = (stage + uint32_t(tc.k_end >> 6)) % nstages;   // past the tile's whole stages
-          const int last = tc.k_end & 63;
-          if (last) {
-            // (a stage is handed over again only after this load has been consumed)
-            if (!wait_bar<false>(tail_go(stage), (turns >> stage) & 1u, ctl)) break;
-            turns ^= 1u << stage;
-            const uint32_t fb = lead_full0 + 8u * stage;
-            const int y0 = tc.k0 + tc.k_end - last, up = (last + 15) & ~15;
+      for (int t = first_tile; t >= 0;) {
+        const TrainTile tc = coords(t);
+        stage = (stage + uint32_t(tc.k_end >> 6)) % nstages;   // past the tile's whole stages
+        const int last = tc.k_end & 63;
+        if (last) {
+          // (a stage is handed over again only after this load has been consumed)
+          if (!wait_bar_warp<false>(tail_go(stage), (turns >> stage) & 1u, ctl)) break;
+          turns ^= 1u << stage;
+          const uint32_t fb = lead_full0 + 8u * stage;
+          const int n0 = first_n(tc, 0), n1 = first_n(tc, 1), y0 = tc.k0 + tc.k_end - last, up = (last + 15) & ~15;
+          if (ptx::elect_one()) {
             int r = 0;
 #pragma unroll 1
             while (r < up) {
               const int left = (r < last ? last : up) - r;
-              const int i = left >= 16 ? 0 : (left >= 4 ? 1 : 2);
+              const int i = left >= 16 ? 0 : (left >= 8 ? 1 : (left >= 4 ? 2 : (left >= 2 ? 3 : 4)));
               const int y = r < last ? y0 + r : p.k;
 #pragma unroll
               for (int c = 0; c < 2; ++c) {
                 const uint32_t off = uint32_t(c * kTrainChunk + r * 128);
                 ptx::tma_load_2d<CG>(stage_a(stage) + off, &extra.a[i], tc.a0 + c * 64, y, fb, pol);
-                ptx::tma_load_2d<CG>(stage_b(stage) + off, &extra.b[i], tc.b0 + c * 64, y, fb, pol);
+                ptx::tma_load_2d<CG>(stage_b(stage) + off, &extra.b[i], n0 + c * 64, y, fb, pol);
               }
-              r += i == 0 ? 16 : (i == 1 ? 4 : 1);
+              if (C::kDual && tc.subs == 2) {
+#pragma unroll
+                for (int c = 0; c < 2; ++c)
+                  ptx::tma_load_2d<CG>(stage_b(stage) + uint32_t(kTrainBN / 2 * 128 + c * kTrainChunk + r * 128), &extra.b[i],
+                                       n1 + c * 64, y, fb, pol);
+              }
+              r += 16 >> i;
             }
-            if (++stage == nstages) stage = 0;
           }
-          t = next_tile(Lane{}, t, cslot, cphase);
-          if (t == -2) ok = false;
+          __syncwarp();
+          if (++stage == nstages) stage = 0;
         }
+        t = __shfl_sync(0xffffffffu, next_tile(Warp{}, t, cslot, cphase), 0);
       }
-      __syncwarp();
     }
+    __syncwarp();
   }
   // ------------------------------------------------------------------ tile scheduler
   else if (warp == 2) {
     if constexpr (C::kClc) {
-      if (GRP == GRP_NONE && !NARROW) ptx::pdl_wait();
+      if (GRP == GRP_NONE && !C::kNarrow) ptx::pdl_wait();
       if (leader && ptx::elect_one()) {
         uint32_t slot = 0, ph = 0;
 #pragma unroll 1
         while (true) {
           if (!wait_bar<true>(clc_empty(slot), ph ^ 1u, ctl)) break;
+          ptx::fence_proxy_async_smem();   // the readers' loads, then the answer's store
           ptx::mbar_arrive_expect_tx(clc_full(slot), 16u);
           ptx::mbar_expect_tx_relaxed_cluster(ptx::map_to_rank(clc_full(slot), 1), 16u);
           ptx::clc_try_cancel<true>(clc_resp(slot), clc_full(slot));
           if (!wait_bar<false>(clc_full(slot), ph, ctl)) break;
           uint32_t x = 0;
           const bool got = ptx::clc_read(clc_resp(slot), x);
-          ptx::mbar_arrive(clc_empty(slot));
+          ptx::mbar_arrive(clc_empty(slot) + (x >> 31));
           if (++slot == 2) {
             slot = 0;
             ph ^= 1u;
@@ -751,14 +852,16 @@ __global__ void __launch_bounds__(TrainConfig<A_MN, B_MN, EPI, GRP, NARROW>::kTh
     const int h = e >> 2;                // which of the tile's chunks: kChunks from h kChunks
     const uint32_t my_buf = epi_base + uint32_t(e * C::kEpiBufBytes);
     const uint32_t acce_lead0 = ptx::map_to_rank(acce_bar(0), 0);
-    if (GRP == GRP_NONE && !NARROW) ptx::pdl_wait();
+    if (GRP == GRP_NONE && !C::kNarrow) ptx::pdl_wait();
     const float alpha = p.scale ? p.alpha * __ldcg(p.scale) : p.alpha;
-    uint32_t acc = 0, accph = 0;
+    uint32_t acc = 0;
+    uint32_t accbits = 0;                // parity of each accumulator's next use
     uint32_t cslot = 0, cphase = 0;
+    bool alive = true;
     [[maybe_unused]] uint32_t turn = 0;  // LOSS: tiles so far
     // Stores go through the warp's 2 KB of shared memory: wait until the store that used it last has read it,
     // fill, send.  Rows are written 128 bytes at a time (a lane each, 16 rows to a box): with 64-byte rows a
-    // bandwidth-bound wgrad took 86 us in place of 70 (8 experts, few rows, 4096 x 7168).
+    // bandwidth-bound wgrad took 84 us in place of 79 (8 experts, few rows, 4096 x 7168).
     auto stage_box = [&](auto&& fill, auto&& send) {
       if (lane == 0) ptx::bulk_wait_group_read<0>();
       __syncwarp();
@@ -807,19 +910,28 @@ __global__ void __launch_bounds__(TrainConfig<A_MN, B_MN, EPI, GRP, NARROW>::kTh
     };
     if (first_tile >= 0) read_columns(first_tile, label_next, l2_next);
 #pragma unroll 1
-    for (int t = first_tile; t >= 0;) {
-      const TrainTile tc = coords(t);
+    for (int t = first_tile; t >= 0 && alive;) {
+      const TrainTile tile = coords(t);
       const int t_next = __shfl_sync(0xffffffffu, next_tile(Warp{}, t, cslot, cphase), 0);
       if (t_next == -2) break;
-      const int nch = min(max(((tc.nt + 31) >> 5) - C::kChunks * h, 0), C::kChunks);   // this warp's chunks
-      const int row0 = tc.a0 + q * 32;                                     // its rows of D
-      const int col0 = tc.n0 + h * C::kChunks * 32;                        // and its first column
 #pragma unroll
       for (int c = 0; c < C::kChunks; ++c) {
         label[c] = label_next[c];
         l2[c] = l2_next[c] * 1.4426950408889634f;
       }
       if (t_next >= 0) read_columns(t_next, label_next, l2_next);
+#pragma unroll 1
+      for (int sub = 0; sub < (C::kDual ? tile.subs : 1); ++sub) {
+      TrainTile tc = tile;               // the columns of one accumulator
+      if constexpr (C::kDual) {
+        acc = uint32_t(sub);
+        tc.nt = width(tile, sub);
+        tc.n0 += sub * kTrainBN;
+        tc.n_end = min(tile.n_end, tc.n0 + kTrainBN);
+      }
+      const int nch = min(max(((tc.nt + 31) >> 5) - C::kChunks * h, 0), C::kChunks);   // this warp's chunks
+      const int row0 = tc.a0 + q * 32;                                     // its rows of D
+      const int col0 = tc.n0 + h * C::kChunks * 32;                        // and its first column
       // (selects: an array indexed at run time would live in local memory)
       [[maybe_unused]] auto pick = [](const int (&x)[C::kChunks], int c) {
         int r = x[0];
@@ -832,7 +944,10 @@ __global__ void __launch_bounds__(TrainConfig<A_MN, B_MN, EPI, GRP, NARROW>::kTh
         off = lab - p.vocab0 - row0;
         return __ballot_sync(0xffffffffu, lab >= 0 && off >= 0 && off < 32 && row0 + off < p.m);
       };
-      if (!wait_bar_warp<false>(accf_bar(acc), accph, ctl)) break;
+      if (!wait_bar_warp<false>(accf_bar(acc), (accbits >> acc) & 1u, ctl)) {
+        alive = false;
+        break;
+      }
       ptx::tc_fence_after();
       const bool idle = !invariant(acc < uint32_t(ACC) && t < num_tiles && tc.nt <= C::kBN, p.status);
       const uint32_t tbase = tmem + (uint32_t(q * 32) << 16) + acc * uint32_t(C::kBN) + uint32_t(h * C::kChunks * 32);
@@ -845,10 +960,8 @@ __global__ void __launch_bounds__(TrainConfig<A_MN, B_MN, EPI, GRP, NARROW>::kTh
           else
             ptx::mbar_arrive_relaxed_cluster(acce_lead0 + 8u * acc);
         }
-        if (++acc == uint32_t(ACC)) {
-          acc = 0;
-          accph ^= 1u;
-        }
+        accbits ^= 1u << acc;
+        if (!C::kDual) acc ^= 1u;
       };
       if constexpr (EPI == EPI_LOSS) {
         float2* stat = s_stat + (turn & 1u) * uint32_t(4 * C::kBN) + h * C::kChunks * 32;
@@ -919,7 +1032,10 @@ __global__ void __launch_bounds__(TrainConfig<A_MN, B_MN, EPI, GRP, NARROW>::kTh
         if (n == 0) hand_back();
         __syncwarp();
         if (lane == 0) ptx::mbar_arrive(stat_bar(h));
-        if (!wait_bar_warp<false>(stat_bar(h), stat_phase, ctl)) break;
+        if (!wait_bar_warp<false>(stat_bar(h), stat_phase, ctl)) {
+          alive = false;
+          break;
+        }
         // the four warps' 32 rows each: warp q joins chunk q
         const int col = col0 + q * 32 + lane;
         if (q < nch && !idle && col < tc.n_end && tc.a0 < p.m) {
@@ -982,15 +1098,16 @@ __global__ void __launch_bounds__(TrainConfig<A_MN, B_MN, EPI, GRP, NARROW>::kTh
           }
         }
         if (n == 0) hand_back();
-      } else if constexpr (EPI == EPI_BF16) {   // tiles are a multiple of 64 wide: both chunks, or none
-        static_assert(EPI != EPI_BF16 || C::kChunks == 2, "64 columns per warp");
-        uint32_t w[32];
-        if (nch > 0 && !idle) {
-          const bool nothing = GRP == GRP_K && tc.nks == 0;   // no rows: the sum is empty, the accumulator undefined
+      } else if constexpr (EPI == EPI_BF16) {   // tiles are a multiple of 64 wide: chunks in pairs
+        const int n = idle ? 0 : nch;
+        const bool nothing = GRP == GRP_K && tc.nks == 0;   // no rows: the sum is empty, the accumulator undefined
+#pragma unroll 1
+        for (int c0 = 0; c0 < n; c0 += 2) {
+          uint32_t w[32];
 #pragma unroll
-          for (int c = 0; c < C::kChunks; ++c) {
+          for (int c = 0; c < 2; ++c) {
             uint32_t v[32];
-            ptx::tmem_ld_32x32b_x32(tbase + uint32_t(c * 32), v);
+            ptx::tmem_ld_32x32b_x32(tbase + uint32_t((c0 + c) * 32), v);
             ptx::tmem_ld_wait_for(v);
 #pragma unroll
             for (int j = 0; j < 16; ++j)
@@ -998,12 +1115,12 @@ __global__ void __launch_bounds__(TrainConfig<A_MN, B_MN, EPI, GRP, NARROW>::kTh
                                       : ptx::pack_bf16x2(__uint_as_float(v[2 * j]) * alpha,
                                                          __uint_as_float(v[2 * j + 1]) * alpha);
           }
-          hand_back();
-          if (col0 < tc.n_end && row0 < p.m)
-            store_rows(w, row0, [&](uint32_t buf, int r) { ptx::tma_store_3d(&tmD, buf, col0, r, GRP == GRP_K ? tc.z : 0); });
-        } else {
-          hand_back();
+          if (c0 + 2 >= n) hand_back();
+          const int col = col0 + c0 * 32;
+          if (col < tc.n_end && row0 < p.m)
+            store_rows(w, row0, [&](uint32_t buf, int r) { ptx::tma_store_3d(&tmD, buf, col, r, GRP == GRP_K ? tc.z : 0); });
         }
+        if (n == 0) hand_back();
       } else {
         const int n = idle ? 0 : nch;
         [[maybe_unused]] const bool nothing = GRP == GRP_K && tc.nks == 0;
@@ -1064,6 +1181,7 @@ __global__ void __launch_bounds__(TrainConfig<A_MN, B_MN, EPI, GRP, NARROW>::kTh
           }
         }
         if (n == 0) hand_back();
+      }
       }
       t = t_next;
     }

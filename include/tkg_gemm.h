@@ -402,7 +402,9 @@ typedef enum {
   TKG_OPT_RASTER_GROUP = 9,   /* M-blocks per tile-order band (0: sized from L2 and K) */
   TKG_OPT_BF16_TILE_N = 10,   /* BF16 CTA-pair tile width: 256 (two accumulator buffers) or
                                   512 (dual accumulate: two N=256 MMAs share each A tile);
-                                  0: automatic */
+                                  0: automatic.  Also of tkg_linear_ce_grad's products and
+                                  tkg_gemm_grouped_dev_bf16_wgrad (set before asking for a
+                                  workspace's size) */
   TKG_OPT_TAIL_SPLIT = 11,    /* plain GEMMs on the persistent kernel: 0 splits the last partial
                                   wave of tiles into half-width tiles when those still fit one
                                   wave; 1 never; 2 splits every tile (a test of the half tiles) */

@@ -20,7 +20,7 @@ GUARD = 7.0
 def _healthy():
     yield
     assert tkg.device_status() == tkg.OK
-    tkg.set_option(tkg.OPT_CTA_GROUP, 0)
+    tkg.set_option(tkg.OPT_BF16_TILE_N, 0)
 
 
 def cut(sizes, cap):
@@ -101,11 +101,18 @@ def test_both_gradients_match_formulas(sizes, n, k):
     check_wgrad(p)
 
 
-@pytest.mark.parametrize("cta_group", [1, 2])
-def test_dgrad_both_cta_groups(cta_group):
-    tkg.set_option(tkg.OPT_CTA_GROUP, cta_group)
-    check_dgrad(Groups([3, 200, 0, 129, 40], 264, 520, spare=70))
-    check_dgrad(Groups([5, 6], 72, 80))
+@pytest.mark.parametrize("tile_n", [256, 512])
+@pytest.mark.parametrize("sizes,n,k", [([3, 200, 0, 129, 40], 264, 520), ([5, 6], 72, 80), ([700, 65, 1, 0], 1000, 1288),
+                                       ([640], 512, 768), ([31, 33], 8, 2056)])
+def test_wgrad_both_tile_widths(sizes, n, k, tile_n):
+    tkg.set_option(tkg.OPT_BF16_TILE_N, tile_n)
+    p = Groups(sizes, n, k, spare=70)
+    check_wgrad(p)
+    g = check_wgrad(p, F32)
+    acc = torch.ones_like(g)
+    tkg.gemm_grouped_dev_bf16_wgrad(p.dev, p.dD, p.A, acc, accumulate=True)
+    for i, (_, m) in enumerate(p.spans):
+        assert torch.equal(acc[i], 1 + g[i] if m else torch.ones_like(g[i]))
 
 
 @pytest.mark.parametrize("sizes", [[40, 0, 300], [1, 2, 3], [0, 0]])
