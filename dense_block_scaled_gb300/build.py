@@ -22,7 +22,8 @@ LIB = os.path.join(PKG, "libtkg.so")
 BUILD_CHECK = os.path.join(PKG, "_build_check")
 LIB_CHECK = os.path.join(PKG, "libtkg_check.so")
 SOURCES = ["tkg_api.cu", "quantize.cu", "gemm_bf16.cu", "gemm_mxfp8.cu", "gemm_nvfp4.cu", "gemm_noalloc.cu",
-           "gemm_grouped.cu", "host_pipeline.cu", "gemm_list.cu", "linear_ce.cu", "linear_ce_logits.cu", "grouped_grad.cu"]
+           "gemm_grouped.cu", "host_pipeline.cu", "gemm_list.cu", "linear_ce.cu", "linear_ce_logits.cu",
+           "linear_ce_few.cu", "grouped_grad.cu"]
 HEADERS = ["ptx.cuh", "gemm_kernel.cuh", "gemm_splitk.cuh", "host_common.cuh", "train_kernel.cuh", "train_host.cuh",
            "linear_ce.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]

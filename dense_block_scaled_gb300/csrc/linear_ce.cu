@@ -5,7 +5,8 @@
 //   g_tv = exp(z_tv - lse_t) - [v = y(t)],  c_t = alpha dloss_t (0 for ignored t)
 //   dX = diag(c) g W,  dW = g^T diag(c) X
 //
-// Loss: one pass over W.  Each 128 logits of a token leave their maximum and sum
+// Loss: one pass over W (of at most 8 tokens without tensor cores, linear_ce_few.cu).
+// Each 128 logits of a token leave their maximum and sum
 // (8 bytes), which a second kernel joins: (M, S) of parts (m_i, s_i) is M = max m_i,
 // S = sum s_i 2^(m_i - M), in base 2, all in FP32.
 //
@@ -257,6 +258,13 @@ GradPlan grad_plan(int tokens, int vocab, int hidden, int piece) {
   return pl;
 }
 
+// One (maximum, sum) per token and 128 vocabulary rows, or per block of the kernel for few tokens.
+size_t loss_part_bytes(int tokens, int vocab) {
+  int parts = ceil_div(vocab, 128);
+  if (tokens <= kFewTokens && parts < kFewMaxBlocks) parts = kFewMaxBlocks;
+  return round_up(size_t(parts) * size_t(tokens) * sizeof(float2), 256);
+}
+
 tkg_status check_head(int tokens, int vocab, int hidden, const void* X, int ldx, const void* W, int ldw,
                       const long long* labels, bool* empty) {
   *empty = false;
@@ -282,7 +290,7 @@ extern "C" {
 
 size_t tkg_linear_ce_loss_workspace_bytes(int tokens, int vocab) {
   if (tokens < 0 || vocab < 0) return 0;
-  return round_up(size_t(ceil_div(vocab, 128)) * size_t(tokens) * sizeof(float2), 256) + size_t(tokens) * 4;
+  return loss_part_bytes(tokens, vocab) + size_t(tokens) * 4;
 }
 
 tkg_status tkg_linear_ce_loss(int tokens, int vocab, int hidden, const void* X, int ldx, const void* W, int ldw,
@@ -294,7 +302,8 @@ tkg_status tkg_linear_ce_loss(int tokens, int vocab, int hidden, const void* X, 
   if (!loss || !lse || !workspace || workspace_bytes < tkg_linear_ce_loss_workspace_bytes(tokens, vocab))
     return TKG_ERR_INVALID_ARG;
   if (!aligned_to(loss, 4) || !aligned_to(lse, 4) || !aligned_to(workspace, 16)) return TKG_ERR_ALIGNMENT;
-  const int parts = ceil_div(vocab, 128);
+  const int few = option(TKG_OPT_CTA_GROUP) ? 0 : ce_few_blocks(tokens, vocab, hidden);
+  const int parts = few ? few : ceil_div(vocab, 128);
   TrainParams p{};
   p.m = vocab;
   p.n = tokens;
@@ -304,10 +313,11 @@ tkg_status tkg_linear_ce_loss(int tokens, int vocab, int hidden, const void* X, 
   p.vocab = vocab;
   p.labels = labels;
   p.part = static_cast<float2*>(workspace);
-  p.zlabel = reinterpret_cast<float*>(static_cast<char*>(workspace) +
-                                      round_up(size_t(parts) * size_t(tokens) * sizeof(float2), 256));
-  if ((st = launch_ce_loss(X, size_t(ldx) * 2, W, size_t(ldw) * 2, p, stream)) != TKG_OK) return st;
-  return launch_small(ce_join_kernel, dim3(unsigned(ceil_div(tokens, kJoinTokens))), dim3(1024), stream, tokens, vocab,
+  p.zlabel = reinterpret_cast<float*>(static_cast<char*>(workspace) + loss_part_bytes(tokens, vocab));
+  st = few ? launch_ce_few(X, size_t(ldx), W, size_t(ldw), p, few, stream)
+           : launch_ce_loss(X, size_t(ldx) * 2, W, size_t(ldw) * 2, p, stream);
+  if (st != TKG_OK) return st;
+  return launch_small(ce_join_kernel, dim3(unsigned(ceil_div(tokens, kJoinTokens))), dim3(1024), stream, 0u, tokens, vocab,
                       parts, p.part, p.zlabel, labels, loss, lse);
 }
 
@@ -354,7 +364,7 @@ tkg_status tkg_linear_ce_grad(int tokens, int vocab, int hidden, const void* X, 
 
   if (dW) {
     const int blocks = ceil_div(tokens, 8) < 4 * kPairs ? ceil_div(tokens, 8) : 4 * kPairs;
-    if ((st = launch_small(ce_rows_kernel, dim3(unsigned(blocks)), dim3(256), stream, tokens, vocab, hidden,
+    if ((st = launch_small(ce_rows_kernel, dim3(unsigned(blocks)), dim3(256), stream, 0u, tokens, vocab, hidden,
                            static_cast<const uint16_t*>(X), size_t(ldx), labels, dloss, alpha, rows, scale)) != TKG_OK)
       return st;
   }
@@ -431,7 +441,7 @@ tkg_status tkg_linear_ce_grad(int tokens, int vocab, int hidden, const void* X, 
   }
   if (!dX) return TKG_OK;
   return launch_small(ce_dx_kernel, dim3(unsigned(ceil_div(tokens, 64)), unsigned(ceil_div(hidden, 16))), dim3(256),
-                      stream, tokens, vocab, hidden, pl.parts, part, pl.tokens_up, labels, dloss, alpha,
+                      stream, 0u, tokens, vocab, hidden, pl.parts, part, pl.tokens_up, labels, dloss, alpha,
                       static_cast<uint16_t*>(dX), size_t(lddx));
 }
 

@@ -151,11 +151,12 @@ constexpr int kNarrowTokens = 128;
 
 // Launch of a small kernel that waits for the previous grid itself (griddepcontrol.wait).
 template <typename... P, typename... Args>
-tkg_status launch_small(void (*kern)(P...), dim3 grid, dim3 block, cudaStream_t stream, Args... args) {
+tkg_status launch_small(void (*kern)(P...), dim3 grid, dim3 block, cudaStream_t stream, unsigned smem, Args... args) {
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[1];
   cfg.gridDim = grid;
   cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;

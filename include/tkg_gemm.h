@@ -386,7 +386,8 @@ tkg_status tkg_quantize_nvfp4_scaled(int rows, int k, const float *X, void *Q, v
 
 /* Process-wide tuning and test options (all default to 0 = automatic). */
 typedef enum {
-  TKG_OPT_CTA_GROUP = 1,      /* 0 auto, 1 single-CTA MMA, 2 CTA-pair MMA */
+  TKG_OPT_CTA_GROUP = 1,      /* 0 auto, 1 single-CTA MMA, 2 CTA-pair MMA (either: tkg_linear_ce_loss
+                                  on tensor cores for few tokens too) */
   TKG_OPT_SINGLE_STAGE = 2,   /* 1: run the one-stage pipeline build (a test of the ring) */
   TKG_OPT_TIMEOUT_MS = 3,     /* bound on every device wait, milliseconds (0: 1000) */
   TKG_OPT_INJECT_STALL = 4,   /* 1: the MMA role waits on a barrier nothing arrives on

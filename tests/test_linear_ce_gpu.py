@@ -29,6 +29,7 @@ def _healthy():
     yield
     assert tkg.device_status() == tkg.OK
     tkg.set_option(tkg.OPT_BF16_TILE_N, 0)
+    tkg.set_option(tkg.OPT_CTA_GROUP, 0)
 
 
 class Head:
@@ -131,6 +132,17 @@ def test_grad_matches_definition(tokens, vocab, hidden):
     check_grad(Head(tokens, vocab, hidden))
 
 
+@pytest.mark.parametrize("cta_group", [0, 2])   # 2: tensor cores for few tokens too
+@pytest.mark.parametrize("tokens,vocab,hidden", [(1, 5000, 2056), (2, 31, 8), (3, 777, 136), (4, 1001, 4104), (5, 33, 264),
+                                                 (6, 4097, 520), (7, 10000, 1024), (8, 2049, 2048), (8, 300, 2056),
+                                                 (1, 9, 16640), (9, 600, 256)])
+def test_loss_of_few_tokens(tokens, vocab, hidden, cta_group):
+    tkg.set_option(tkg.OPT_CTA_GROUP, cta_group)
+    check_loss(Head(tokens, vocab, hidden, seed=5, ignored=0.1))
+    check_loss(Head(tokens, vocab, hidden, seed=6, alpha=-0.5))
+    check_loss(Head(tokens, vocab, hidden, seed=7, alpha=0.0))
+
+
 @pytest.mark.parametrize("tile_n", [256, 512])
 @pytest.mark.parametrize("tokens,vocab,hidden,piece", [(5, 333, 64, 0), (130, 700, 264, 0), (300, 1300, 128, 512),
                                                        (777, 900, 1032, 0), (1100, 2100, 520, 1000)])
@@ -231,7 +243,7 @@ def test_all_rows_ignored():
     assert torch.equal(acc, keep)
 
 
-@pytest.mark.parametrize("tokens", [20, 333])
+@pytest.mark.parametrize("tokens", [7, 20, 333])
 def test_ignored_rows_may_hold_anything(tokens):
     clean = Head(tokens, 800, 128, ignored=0.5)
     lse = clean.forward()[2].float()
