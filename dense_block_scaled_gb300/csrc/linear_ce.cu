@@ -95,10 +95,10 @@ __global__ void __launch_bounds__(1024)
 }
 
 // ---------------------------------------------------------------- rows of X with the tokens' weights
-// out_t = X_t c_t / s, s = max |c_t|, and s itself.  Rows of ignored tokens are
-// zeros whatever they hold: their g is 0, but 0 times a padded position's NaN is not.
-// Every block finds s again from the T weights (T x 12 bytes from L2 for each of
-// at most two blocks per SM, against one more launch), then takes a row per warp.
+// ce_weighted_row for every token, and s.  Every block finds s again from the T
+// weights (T x 12 bytes from L2 for each of at most two blocks per SM, against one
+// more launch), then takes a row per warp.  For heads with too few tiles to deal
+// the rows over (see rows_on_the_side).
 __global__ void __launch_bounds__(256)
     ce_rows_kernel(int tokens, int vocab, int hidden, const uint16_t* __restrict__ X, size_t ldx,
                    const long long* __restrict__ labels, const float* __restrict__ dloss, float alpha,
@@ -106,15 +106,10 @@ __global__ void __launch_bounds__(256)
   __shared__ float s_max[8];
   ptx::pdl_launch_dependents();
   ptx::pdl_wait();
-  auto weight = [&](int t) {
-    const long long y = __ldcg(labels + t);
-    const float d = __ldcg(dloss + t);
-    return (y >= 0 && y < vocab) ? alpha * d : 0.f;
-  };
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   float top = 0.f;
 #pragma unroll 8
-  for (int t = tid; t < tokens; t += 256) top = fmaxf(top, fabsf(weight(t)));
+  for (int t = tid; t < tokens; t += 256) top = fmaxf(top, fabsf(ce_weight(t, vocab, labels, dloss, alpha)));
 #pragma unroll
   for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
   if (lane == 0) s_max[warp] = top;
@@ -123,30 +118,8 @@ __global__ void __launch_bounds__(256)
 #pragma unroll
   for (int o = 4; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
   if (blockIdx.x == 0 && tid == 0) *scale = top;
-  const int vec = hidden / 8;
-  for (int t = blockIdx.x * 8 + warp; t < tokens; t += gridDim.x * 8) {
-    const long long y = __ldcg(labels + t);
-    const bool kept = y >= 0 && y < vocab;
-    const float w = top == 0.f ? 0.f : __fdiv_rn(weight(t), top);
-    const uint4* src = reinterpret_cast<const uint4*>(X + size_t(t) * ldx);
-    uint4* dst = reinterpret_cast<uint4*>(out + size_t(t) * size_t(hidden));
-    for (int c0 = lane; c0 < vec; c0 += 128) {
-      uint4 v[4];
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-        v[j] = kept && c0 + 32 * j < vec ? __ldcg(src + c0 + 32 * j) : make_uint4(0, 0, 0, 0);
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        if (w != 1.f) {
-          uint32_t* u = reinterpret_cast<uint32_t*>(&v[j]);
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            u[i] = ptx::pack_bf16x2(__uint_as_float(u[i] << 16) * w, __uint_as_float(u[i] & 0xffff0000u) * w);
-        }
-        if (c0 + 32 * j < vec) dst[c0 + 32 * j] = v[j];
-      }
-    }
-  }
+  for (int t = blockIdx.x * 8 + warp; t < tokens; t += gridDim.x * 8)
+    ce_weighted_row(t, lane, vocab, hidden, X, ldx, labels, dloss, alpha, top, out);
 }
 
 // ---------------------------------------------------------------- dX from its FP32 parts
@@ -258,6 +231,13 @@ GradPlan grad_plan(int tokens, int vocab, int hidden, int piece) {
   return pl;
 }
 
+// Whether a spare warp of the logits' blocks writes the weighted rows of X: it takes about a microsecond per 2 KB
+// of row, and two of them should stay behind a tile's time, a microsecond per 256 hidden or more.
+bool rows_on_the_side(int tokens, int piece, int hidden) {
+  const double tiles = double(ceil_div(piece, 256)) * ceil_div(tokens, kTrainBN);
+  return tokens / tiles <= 4.0 && tokens <= 16384;
+}
+
 // One (maximum, sum) per token and 128 vocabulary rows, or per block of the kernel for few tokens.
 size_t loss_part_bytes(int tokens, int vocab) {
   int parts = ceil_div(vocab, 128);
@@ -362,7 +342,8 @@ tkg_status tkg_linear_ce_grad(int tokens, int vocab, int hidden, const void* X, 
   float* scale = reinterpret_cast<float*>(ws + pl.scale_off);
   CUtensorMap tmA, tmB, tmD;
 
-  if (dW) {
+  const bool on_the_side = dW && rows_on_the_side(tokens, pl.piece, hidden);
+  if (dW && !on_the_side) {
     const int blocks = ceil_div(tokens, 8) < 4 * kPairs ? ceil_div(tokens, 8) : 4 * kPairs;
     if ((st = launch_small(ce_rows_kernel, dim3(unsigned(blocks)), dim3(256), stream, 0u, tokens, vocab, hidden,
                            static_cast<const uint16_t*>(X), size_t(ldx), labels, dloss, alpha, rows, scale)) != TKG_OK)
@@ -383,6 +364,13 @@ tkg_status tkg_linear_ce_grad(int tokens, int vocab, int hidden, const void* X, 
     p.lse = lse;
     p.d = G;
     p.ldd = pl.tokens_up;
+    if (on_the_side && i == 0) {
+      p.x = static_cast<const uint16_t*>(X);
+      p.ldx = size_t(ldx);
+      p.dloss = dloss;
+      p.rows = rows;
+      p.rows_scale = scale;
+    }
     if ((st = launch_ce_dlogits(X, size_t(ldx) * 2, Wp, size_t(ldw) * 2, p, stream)) != TKG_OK) return st;
     if (dX) {
       // (parts of) W^T g of this piece: hidden x tokens

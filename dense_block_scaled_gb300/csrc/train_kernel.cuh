@@ -25,7 +25,8 @@
 // the bounded waits and the abort protocol are those of gemm_kernel.cuh:
 //   warp 0 TMA producer, warp 1 MMA issuer, warp 2 tensor-memory allocation and
 //   the cluster-launch-control tile scheduler, warp 3 the producer of the stages
-//   in which a group of k ends (and the group table), warps 4-19 epilogue: 16,
+//   in which a group of k ends (and the group table; with DLOGITS, the weighted
+//   rows of X), warps 4-19 epilogue: 16,
 //   as the cross-entropy epilogues are bound by latency (with 8 warps they took
 //   8000 cycles for a 256 x 256 tile, twice its MMAs at hidden = 512, at 40% of
 //   the issue slots).
@@ -95,6 +96,12 @@ struct TrainParams {
   const float* lse;
   float2* part;                // LOSS: (maximum, sum) per 128 vocabulary rows and token
   float* zlabel;               // LOSS: the label's logit per token
+  // DLOGITS: the rows of X with the tokens' weights (see ce_weighted_row), written on the side; null: not wanted
+  const uint16_t* x;
+  size_t ldx;
+  const float* dloss;
+  uint16_t* rows;
+  float* rows_scale;
   // outputs written from registers: their first element and row pitch in elements
   void* d;
   size_t ldd;
@@ -216,6 +223,42 @@ __device__ __forceinline__ int column_of_lane(int lane) {
   return 16 * ((lane >> 4) & 1) + 8 * ((lane >> 3) & 1) + 2 * (lane & 3) + ((lane >> 2) & 1);
 }
 
+// ---- rows of X with the tokens' weights: row t times c_t / s with c_t = alpha dloss_t (0 for ignored tokens) and
+// s = max |c_t|.  Rows of ignored tokens are zeros whatever they hold: their g is 0, but 0 times a padded position's
+// NaN is not.
+__device__ __forceinline__ float ce_weight(int t, int vocab, const long long* labels, const float* dloss, float alpha) {
+  const long long y = __ldcg(labels + t);
+  const float d = __ldcg(dloss + t);
+  return (y >= 0 && y < vocab) ? alpha * d : 0.f;
+}
+// One row, by a warp.
+__device__ __forceinline__ void ce_weighted_row(int t, int lane, int vocab, int hidden, const uint16_t* X, size_t ldx,
+                                                const long long* labels, const float* dloss, float alpha, float top,
+                                                uint16_t* out) {
+  const long long y = __ldcg(labels + t);
+  const bool kept = y >= 0 && y < vocab;
+  const float w = top == 0.f ? 0.f : __fdiv_rn(ce_weight(t, vocab, labels, dloss, alpha), top);
+  const uint4* src = reinterpret_cast<const uint4*>(X + size_t(t) * ldx);
+  uint4* dst = reinterpret_cast<uint4*>(out + size_t(t) * size_t(hidden));
+  const int vec = hidden / 8;
+  for (int c0 = lane; c0 < vec; c0 += 128) {
+    uint4 v[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      v[j] = kept && c0 + 32 * j < vec ? __ldcg(src + c0 + 32 * j) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      if (w != 1.f) {
+        uint32_t* u = reinterpret_cast<uint32_t*>(&v[j]);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          u[i] = ptx::pack_bf16x2(__uint_as_float(u[i] << 16) * w, __uint_as_float(u[i] & 0xffff0000u) * w);
+      }
+      if (c0 + 32 * j < vec) dst[c0 + 32 * j] = v[j];
+    }
+  }
+}
+
 constexpr int kTrainBN = 256;         // widest tile
 constexpr int kTrainMaxStages = 12;
 
@@ -248,8 +291,8 @@ struct TrainConfig {
                 "four or six stages of the widest tiles");
   static_assert(!kDual || (B_MN && (EPI == EPI_BF16 || EPI == EPI_F32) && GRP != GRP_ROWS), "not built");
   static constexpr bool kClc = GRP != GRP_ROWS;     // GRP_ROWS: the tile count is known on the device only
-  // readers of a scheduler answer: producer (GRP_K: two) and epilogue warps per CTA, MMA issuer and scheduler
-  static constexpr int kClcConsumers = 2 * ((GRP == GRP_K ? 2 : 1) + kEpiWarps) + 2;
+  // readers of a scheduler answer: producer, warp 3 where it has tiles' work, epilogue warps; MMA issuer and scheduler
+  static constexpr int kClcConsumers = 2 * ((GRP == GRP_K || EPI == EPI_DLOGITS ? 2 : 1) + kEpiWarps) + 2;
   static constexpr uint32_t kIdesc = idesc_f16(256, kBN) | (A_MN ? 1u << 15 : 0u) | (B_MN ? 1u << 16 : 0u);
 };
 
@@ -801,6 +844,30 @@ __global__ void __launch_bounds__(TrainConfig<A_MN, B_MN, EPI, GRP, SHAPE>::kThr
           }
           __syncwarp();
           if (++stage == nstages) stage = 0;
+        }
+        t = __shfl_sync(0xffffffffu, next_tile(Warp{}, t, cslot, cphase), 0);
+      }
+    }
+    if constexpr (EPI == EPI_DLOGITS) {
+      // The weighted rows of X for dW, dealt over the tiles (a launch before this one cost 5 us of the 98 that the
+      // gradient of 128 tokens x 32768 x 2048 takes)
+      ptx::pdl_wait();
+      float top = 0.f;
+      if (p.rows) {
+#pragma unroll 4
+        for (int t = lane; t < p.n; t += 32) top = fmaxf(top, fabsf(ce_weight(t, p.vocab, p.labels, p.dloss, p.alpha)));
+#pragma unroll
+        for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+      }
+      uint32_t cslot = 0, cphase = 0;
+#pragma unroll 1
+      for (int t = first_tile; t >= 0;) {
+        if (p.rows) {
+          const int begin = int((long long)p.n * t / num_tiles), end = int((long long)p.n * (t + 1) / num_tiles);
+#pragma unroll 1
+          for (int row = begin + int(rank); row < end; row += 2)
+            ce_weighted_row(row, lane, p.vocab, p.k, p.x, p.ldx, p.labels, p.dloss, p.alpha, top, p.rows);
+          if (t == 0 && leader && lane == 0) *p.rows_scale = top;
         }
         t = __shfl_sync(0xffffffffu, next_tile(Warp{}, t, cslot, cphase), 0);
       }

@@ -421,17 +421,22 @@ def linear_ce_grad(X, W, labels, lse, dloss, dX, dW, alpha: float = 1.0, accumul
     """Gradient of sum(dloss * loss): dX (tokens x hidden bf16) and dW (vocab x hidden, bf16 or float32); either may
     be None.  accumulate: add to the float32 dW.  piece: vocabulary entries worked on at a time (0: chosen)."""
     import torch
-    (tokens, hidden), vocab = X.shape, W.shape[0]
-    wanted = [("X", X, torch.bfloat16, (tokens, hidden), True), ("W", W, torch.bfloat16, (vocab, hidden), True),
-              ("labels", labels, torch.int64, (tokens,), False), ("lse", lse, torch.float32, (tokens,), False),
-              ("dloss", dloss, torch.float32, (tokens,), False)]
-    gtype = GRAD_BF16
-    if dX is not None:
-        wanted.append(("dX", dX, torch.bfloat16, (tokens, hidden), True))
-    if dW is not None:
-        gtype = _grad_type(dW, "dW", accumulate)
-        wanted.append(("dW", dW, dW.dtype, (vocab, hidden), True))
-    _refuse(wanted)
+    (tokens, hidden), vocab, row = X.shape, W.shape[0], labels.shape
+    gtype = GRAD_BF16 if dW is None else _grad_type(dW, "dW", accumulate)
+    if not (X.dtype is W.dtype is torch.bfloat16 and labels.dtype is torch.int64
+            and lse.dtype is dloss.dtype is torch.float32 and W.shape[1] == hidden and row == lse.shape == dloss.shape
+            and row == (tokens,) and X.is_contiguous() and W.is_contiguous() and labels.is_contiguous()
+            and lse.is_contiguous() and dloss.is_contiguous()
+            and (dX is None or (dX.dtype is torch.bfloat16 and dX.shape == X.shape and dX.is_contiguous()))
+            and (dW is None or (dW.shape == W.shape and dW.is_contiguous()))):
+        wanted = [("X", X, torch.bfloat16, (tokens, hidden), True), ("W", W, torch.bfloat16, (vocab, hidden), True),
+                  ("labels", labels, torch.int64, (tokens,), False), ("lse", lse, torch.float32, (tokens,), False),
+                  ("dloss", dloss, torch.float32, (tokens,), False)]
+        if dX is not None:
+            wanted.append(("dX", dX, torch.bfloat16, (tokens, hidden), True))
+        if dW is not None:
+            wanted.append(("dW", dW, dW.dtype, (vocab, hidden), True))
+        _refuse(wanted)
     lib = load()
     at, nbytes, _keep = _workspace(workspace, lib.tkg_linear_ce_grad_workspace_bytes(tokens, vocab, hidden, piece), X,
                                    stream)
