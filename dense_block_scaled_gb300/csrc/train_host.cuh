@@ -148,6 +148,10 @@ inline bool train_dual(int m, int n, long long count, int stages) {
 
 // At most this many tokens take the kernel's narrow form.
 constexpr int kNarrowTokens = 128;
+// Stages (64 k each) that one accumulator of a logit sums.  Tensor memory adds towards zero, so a sum's error grows
+// with its length: of lse, relative, 6.3e-7 at 2048 products and 1.3e-6 at 4096 in one sum.  Sums of at most 2048
+// are added in the epilogue's registers.
+constexpr int kSumStages = 32;
 
 // Launch of a small kernel that waits for the previous grid itself (griddepcontrol.wait).
 template <typename... P, typename... Args>

@@ -10,8 +10,9 @@
 // a multiple of 16, so a batch of T tokens is cut into ceil(T / 256) tiles of
 // equal width, T / tiles rounded up to 16, and next to nothing is computed for
 // tokens that do not exist; with the tokens on M (tiles of 256) 777 tokens cost
-// 1024 and 64 experts of 16 to 900 rows 1.4 times their rows (measured at 777 x
-// 50001 x 2048 and 64 experts x 2048 x 2048; see the table of results).
+// 1024 and 64 uneven experts of 250 rows on average 1.4 times their rows (loss of
+// 777 x 50001 x 2048: 129 us against 112; rows' gradient of 64 experts x 2048 x
+// 2048, 16000 rows: 144 against 126).
 //
 // Each operand is either K-major (row m holds consecutive k: rows of X, W, dD)
 // or MN-major (row k holds consecutive m or n: the same matrices read for
@@ -24,9 +25,9 @@
 // Roles (one CTA per SM; the two CTAs of a cluster share one MMA of 256 x N),
 // the bounded waits and the abort protocol are those of gemm_kernel.cuh:
 //   warp 0 TMA producer, warp 1 MMA issuer, warp 2 tensor-memory allocation and
-//   the cluster-launch-control tile scheduler, warp 3 the producer of the stages
-//   in which a group of k ends (and the group table; with DLOGITS, the weighted
-//   rows of X), warps 4-19 epilogue: 16,
+//   the cluster-launch-control tile scheduler, warp 3 the group table and
+//   the producer of the stages in which a group of k ends (with DLOGITS: the weighted
+//   rows of X), warps 4-19 epilogue: 16 (DUAL 8, NARROW 4),
 //   as the cross-entropy epilogues are bound by latency (with 8 warps they took
 //   8000 cycles for a 256 x 256 tile, twice its MMAs at hidden = 512, at 40% of
 //   the issue slots).
@@ -39,10 +40,18 @@
 // two MMAs.  The SMs read a quarter fewer bytes from L2 for the same products;
 // these kernels run under the power cap, where that shows as clock.
 //
-// NARROW (at most 128 tokens, where reading the weights bounds the time): two
+// SUMS (logits of the loss with hidden > 2048): tensor memory adds towards zero, so a
+// sum's error grows with its length.  An accumulator takes at most 2048 products; the
+// epilogue gathers such sums in registers (64 a thread) and hands the accumulator back
+// before it turns to the exponentials.  lse of 4096 x 131072 x 4096: 5.7e-7 off
+// (relative) against 1.2e-6 in one sum, 2497 against 2480 us.
+//
+// NARROW (loss of 5 to 128 tokens, where reading the weights bounds the time): two
 // blocks per SM, each with half the shared and tensor memory and 4 epilogue warps.
 // Twice the tiles run at once, so that few tiles do not leave a thin last round,
-// and one block's set-up and epilogue run under the other's loads.
+// and one block's set-up and epilogue run under the other's loads.  Two sums at most,
+// in the two accumulators; past 4096 products SUMS (128 x 32768 x 8192: 96.9 us, in two
+// longer sums here 93.7).
 //
 // Epilogues (EPI):
 //   LOSS     per token (column) and 128 vocabulary rows: the largest logit and the
@@ -72,12 +81,14 @@ enum : int { EPI_LOSS = 0, EPI_DLOGITS = 1, EPI_BF16 = 2, EPI_F32 = 3, EPI_BF16_
 // consecutive k, each with its own output matrix.  Row counts in device memory.
 enum : int { GRP_NONE = 0, GRP_ROWS = 1, GRP_K = 2 };
 // Tile shapes: 256 x up to 256; NARROW 256 x up to 128, two blocks per SM; DUAL 256 x 512.
-enum : int { SHAPE_WIDE = 0, SHAPE_NARROW = 1, SHAPE_DUAL = 2 };
+// SUMS (LOSS): WIDE with sums longer than one accumulator takes.
+enum : int { SHAPE_WIDE = 0, SHAPE_NARROW = 1, SHAPE_DUAL = 2, SHAPE_SUMS = 3 };
 
 struct TrainParams {
   int m, n, k;                 // output rows and columns, contraction length (GRP_ROWS: n, GRP_K: k is the row capacity)
   int kstages;                 // ceil(k / 64)
   int splits, split_stages;    // k split: part z covers stages [z * split_stages, ...)
+  int sum_stages;              // LOSS: stages summed in one accumulator; the epilogue adds the next to it
   int tiles_m, tiles_n, num_tiles;
   int n_tile;                  // tile width, a multiple of 16 (GRP_ROWS: per group, by its rows; DUAL: 512)
   int raster_group;
@@ -140,18 +151,20 @@ __device__ __forceinline__ void tma_add_3d(const void* tmap, uint32_t src, int32
                "r"(x), "r"(y), "r"(z), "r"(src)
                : "memory");
 }
-// 16 lanes x 32 columns into r[H .. H + 16): thread t gets, for i = 0..3, lane t / 4 columns
-// 8 i + 2 (t % 4) + {0, 1} in r[H + 4 i], r[H + 4 i + 1] and lane t / 4 + 8 of the same columns in
-// r[H + 4 i + 2], r[H + 4 i + 3].
-template <int H>
-__device__ __forceinline__ void tmem_ld_16x256b_x4(uint32_t taddr, uint32_t (&r)[32]) {
+// 16 lanes x 32 columns: thread t gets, for i = 0..3, lane t / 4 columns 8 i + 2 (t % 4) + {0, 1} in r[4 i],
+// r[4 i + 1] and lane t / 4 + 8 of the same columns in r[4 i + 2], r[4 i + 3].
+__device__ __forceinline__ void tmem_ld_16x256b_x4(uint32_t taddr, uint32_t (&r)[16]) {
   asm volatile(
       "tcgen05.ld.sync.aligned.16x256b.x4.b32 "
       "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
-      : "=r"(r[H]), "=r"(r[H + 1]), "=r"(r[H + 2]), "=r"(r[H + 3]), "=r"(r[H + 4]), "=r"(r[H + 5]), "=r"(r[H + 6]),
-        "=r"(r[H + 7]), "=r"(r[H + 8]), "=r"(r[H + 9]), "=r"(r[H + 10]), "=r"(r[H + 11]), "=r"(r[H + 12]),
-        "=r"(r[H + 13]), "=r"(r[H + 14]), "=r"(r[H + 15])
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
       : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_ld_wait_for(uint32_t (&r)[16]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                 "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])::"memory");
 }
 // Waits for this thread's tensor-memory loads; naming the registers keeps what reads them behind the wait.
 __device__ __forceinline__ void tmem_ld_wait_for(uint32_t (&r)[32]) {
@@ -161,12 +174,6 @@ __device__ __forceinline__ void tmem_ld_wait_for(uint32_t (&r)[32]) {
                  "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]),
                  "+r"(r[23]), "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]),
                  "+r"(r[30]), "+r"(r[31])::"memory");
-}
-// One column: thread i of the warp gets lane i of its quadrant.
-__device__ __forceinline__ uint32_t tmem_ld_32x32b_x1(uint32_t taddr) {
-  uint32_t r;
-  asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];" : "=r"(r) : "r"(taddr));
-  return r;
 }
 __device__ __forceinline__ float ex2(float x) {
   float r;
@@ -287,7 +294,7 @@ struct TrainConfig {
   // all an SM gives a block, or two blocks, less the two static words
   static constexpr int kSmemBytes = (kNarrow ? 116736 - 1024 : 232448) - 16;
   static constexpr int kRingBytes = (kSmemBytes - kFixedBytes) / 1024 * 1024;
-  static_assert(kRingBytes >= (SHAPE == SHAPE_WIDE ? 6 : 4) * (kABytes + kSubs * kBN / 2 * 128),
+  static_assert(kRingBytes >= (SHAPE == SHAPE_WIDE || SHAPE == SHAPE_SUMS ? 6 : 4) * (kABytes + kSubs * kBN / 2 * 128),
                 "four or six stages of the widest tiles");
   static_assert(!kDual || (B_MN && (EPI == EPI_BF16 || EPI == EPI_F32) && GRP != GRP_ROWS), "not built");
   static constexpr bool kClc = GRP != GRP_ROWS;     // GRP_ROWS: the tile count is known on the device only
@@ -682,8 +689,8 @@ __global__ void __launch_bounds__(TrainConfig<A_MN, B_MN, EPI, GRP, SHAPE>::kThr
       if (p.inject_stall) ok = wait_bar<false>(never_bar, 0u, ctl);
       const uint16_t mask = 0x3;
       uint32_t cslot = 0, cphase = 0;
-      // the four MMAs of stage s (the tile's stage `it`) into one accumulator
-      auto issue = [&](const TrainTile& tc, uint32_t s, int it, uint32_t acc, uint32_t sub) {
+      // the four MMAs of stage s (the tile's stage `it`) into one accumulator, whose sum starts at stage `from`
+      auto issue = [&](const TrainTile& tc, uint32_t s, int it, uint32_t acc, uint32_t sub, int from = 0) {
         const uint64_t adesc = A_MN ? sdesc_mn_sw128(stage_a(s)) : sdesc_sw128(stage_a(s));
         const uint32_t b = stage_b(s) + sub * uint32_t(kTrainBN / 2 * 128);
         const uint64_t bdesc = B_MN ? sdesc_mn_sw128(b) : sdesc_sw128(b);
@@ -696,7 +703,7 @@ __global__ void __launch_bounds__(TrainConfig<A_MN, B_MN, EPI, GRP, SHAPE>::kThr
           // 16 k: 32 bytes along K-major rows, two 8-k groups of 1024 bytes in MN-major chunks
           const uint64_t aoff = A_MN ? uint64_t((j * 2048) >> 4) : uint64_t((j * 32) >> 4);
           const uint64_t boff = B_MN ? uint64_t((j * 2048) >> 4) : uint64_t((j * 32) >> 4);
-          ptx::mma_f16<CG>(tmem + acc * uint32_t(C::kBN), adesc + aoff, bdesc + boff, idesc, (it > 0 || j > 0) ? 1u : 0u);
+          ptx::mma_f16<CG>(tmem + acc * uint32_t(C::kBN), adesc + aoff, bdesc + boff, idesc, (it > from || j > 0) ? 1u : 0u);
         }
       };
       auto acc_free = [&](uint32_t acc) {   // the epilogue has handed it back
@@ -714,23 +721,29 @@ __global__ void __launch_bounds__(TrainConfig<A_MN, B_MN, EPI, GRP, SHAPE>::kThr
       for (int t = first_tile; t >= 0 && ok;) {
         const TrainTile tc = coords(t);
         if constexpr (!C::kDual) {
-          if (!acc_free(acc)) {
-            ok = false;
-            break;
-          }
+          int it = 0;
 #pragma unroll 1
-          for (int it = 0; it < tc.nks; ++it) {
-            if (!wait_bar<false>(full_bar(stage), phase, ctl)) {
+          do {   // (one turn, but for LOSS)
+            if (!acc_free(acc)) {
               ok = false;
               break;
             }
-            issue(tc, stage, it, acc, 0);
-            ptx::tc_commit<CG>(empty_bar(stage), mask);
-            if (advance(stage)) phase ^= 1u;
-          }
+            const int from = it, to = EPI == EPI_LOSS ? min(it + p.sum_stages, tc.nks) : tc.nks;
+#pragma unroll 1
+            for (; it < to; ++it) {
+              if (!wait_bar<false>(full_bar(stage), phase, ctl)) {
+                ok = false;
+                break;
+              }
+              issue(tc, stage, it, acc, 0, from);
+              ptx::tc_commit<CG>(empty_bar(stage), mask);
+              if (advance(stage)) phase ^= 1u;
+            }
+            if (!ok) break;
+            ptx::tc_commit<CG>(accf_bar(acc), mask);
+            acc ^= 1u;
+          } while (it < tc.nks);
           if (!ok) break;
-          ptx::tc_commit<CG>(accf_bar(acc), mask);
-          acc ^= 1u;
         } else {
           // Both accumulators take every stage, but the first runs kSkew stages ahead at the start, while the
           // second is still being read out, and finishes kSkew stages early, so that its read-out begins under
@@ -928,7 +941,7 @@ __global__ void __launch_bounds__(TrainConfig<A_MN, B_MN, EPI, GRP, SHAPE>::kThr
     [[maybe_unused]] uint32_t turn = 0;  // LOSS: tiles so far
     // Stores go through the warp's 2 KB of shared memory: wait until the store that used it last has read it,
     // fill, send.  Rows are written 128 bytes at a time (a lane each, 16 rows to a box): with 64-byte rows a
-    // bandwidth-bound wgrad took 84 us in place of 79 (8 experts, few rows, 4096 x 7168).
+    // bandwidth-bound weight gradient took 84 us in place of 79 (8 experts, 128 rows, 4096 x 7168).
     auto stage_box = [&](auto&& fill, auto&& send) {
       if (lane == 0) ptx::bulk_wait_group_read<0>();
       __syncwarp();
@@ -1011,13 +1024,18 @@ __global__ void __launch_bounds__(TrainConfig<A_MN, B_MN, EPI, GRP, SHAPE>::kThr
         off = lab - p.vocab0 - row0;
         return __ballot_sync(0xffffffffu, lab >= 0 && off >= 0 && off < 32 && row0 + off < p.m);
       };
-      if (!wait_bar_warp<false>(accf_bar(acc), (accbits >> acc) & 1u, ctl)) {
+      auto acc_ready = [&]() {
+        if (!wait_bar_warp<false>(accf_bar(acc), (accbits >> acc) & 1u, ctl)) return false;
+        ptx::tc_fence_after();
+        return true;
+      };
+      if (!acc_ready()) {
         alive = false;
         break;
       }
-      ptx::tc_fence_after();
       const bool idle = !invariant(acc < uint32_t(ACC) && t < num_tiles && tc.nt <= C::kBN, p.status);
-      const uint32_t tbase = tmem + (uint32_t(q * 32) << 16) + acc * uint32_t(C::kBN) + uint32_t(h * C::kChunks * 32);
+      const uint32_t tq = tmem + (uint32_t(q * 32) << 16) + uint32_t(h * C::kChunks * 32);
+      [[maybe_unused]] const uint32_t tbase = tq + acc * uint32_t(C::kBN);
       auto hand_back = [&]() {   // every load of this tile has completed
         ptx::tc_fence_before();
         __syncwarp();
@@ -1038,30 +1056,35 @@ __global__ void __launch_bounds__(TrainConfig<A_MN, B_MN, EPI, GRP, SHAPE>::kThr
         const int rows_there = p.m - row0 - (lane >> 2);   // of rows 0, 8, 16, 24 past this lane's first
         const bool edge = row0 + 32 > p.m;
         const int n = idle ? 0 : nch;
-#pragma unroll 1
-        for (int c = 0; c < n; ++c) {
-          // rows of the lower 16 lanes in the first half of v, of the upper 16 in the second
-          uint32_t v[32];
-          ptx::tmem_ld_16x256b_x4<0>(tbase + uint32_t(c * 32), v);
-          ptx::tmem_ld_16x256b_x4<16>(tbase + (16u << 16) + uint32_t(c * 32), v);
-          ptx::tmem_ld_wait_for(v);
+        // x[4 i + 2 k + e]: column 8 i + 2 (t % 4) + e, row t / 4 + 8 k (k = 0, 1), and, from x[16] on, 16 rows on
+        auto read = [&](int c, uint32_t a, bool first, float (&x)[32]) {
+          const uint32_t from = tq + a * uint32_t(C::kBN) + uint32_t(c * 32);
+          uint32_t v[2][16];
+          ptx::tmem_ld_16x256b_x4(from, v[0]);
+          if (SHAPE != SHAPE_SUMS) ptx::tmem_ld_16x256b_x4(from + (16u << 16), v[1]);
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {
+            // (SUMS has no registers for both halves beside the sums)
+            if (SHAPE == SHAPE_SUMS && u == 1) ptx::tmem_ld_16x256b_x4(from + (16u << 16), v[1]);
+            ptx::tmem_ld_wait_for(v[u]);
+#pragma unroll
+            for (int j = 0; j < 16; ++j)
+              x[16 * u + j] = first ? __uint_as_float(v[u][j]) : x[16 * u + j] + __uint_as_float(v[u][j]);
+          }
+        };
+        auto reduce = [&](int c, float (&x)[32]) {
           // labels among these 32 rows: about one column in vocab / 32
           int off;
 #pragma unroll 1
           for (uint32_t left = among_rows(pick(label, c), off); left; left &= left - 1) {
             const int j = __ffs(int(left)) - 1;
             const int row = __shfl_sync(0xffffffffu, off, j);
-            uint32_t z = ptx::tmem_ld_32x32b_x1(tbase + uint32_t(c * 32 + j));
-            asm volatile("tcgen05.wait::ld.sync.aligned;" : "+r"(z)::"memory");
-            if (lane == row) p.zlabel[col0 + c * 32 + j] = __uint_as_float(z) * alpha;
-          }
-          if (c + 1 == n) {
-            hand_back();
-          }
-          // x[4 i + 2 k + e]: column 8 i + 2 (t % 4) + e, row t / 4 + 8 k (k = 0, 1), and 16 more (k = 2, 3)
-          float x[32];
+            const int at = 4 * (j >> 3) + 2 * ((row >> 3) & 1) + (j & 1) + 16 * (row >> 4);
+            float z = x[0];
 #pragma unroll
-          for (int j = 0; j < 32; ++j) x[j] = __uint_as_float(v[j]);
+            for (int i = 1; i < 32; ++i) z = at == i ? x[i] : z;
+            if (lane == 4 * (row & 7) + ((j >> 1) & 3)) p.zlabel[col0 + c * 32 + j] = z * alpha;
+          }
           if (p.c2 < 0.f) {
             asm volatile("");   // (a branch, not 32 selects)
 #pragma unroll
@@ -1095,8 +1118,53 @@ __global__ void __launch_bounds__(TrainConfig<A_MN, B_MN, EPI, GRP, SHAPE>::kThr
           }
           const float s = fold_columns(sum, lane, [](float a, float b) { return a + b; });
           stat[q * C::kBN + c * 32 + column_of_lane(lane)] = make_float2(own == -INFINITY ? own : own * c2, s);
+        };
+        if constexpr (SHAPE != SHAPE_SUMS) {
+          const bool two = C::kNarrow && p.sum_stages < tc.nks;   // sums, in both accumulators
+          if (two) {
+            acc ^= 1u;
+            if (!acc_ready()) {
+              alive = false;
+              break;
+            }
+            acc ^= 1u;
+          }
+#pragma unroll 1
+          for (int c = 0; c < n; ++c) {
+            float x[32];
+            read(c, acc, true, x);
+            if (two) read(c, acc ^ 1u, false, x);
+            if (c + 1 == n) {
+              hand_back();
+              if (two) hand_back();
+            }
+            reduce(c, x);
+          }
+          if (n == 0) {
+            hand_back();
+            if (two) hand_back();
+          }
+        } else {
+          // the sums gather in registers, and the accumulators go back as soon as they are read
+          float x[C::kChunks][32];
+#pragma unroll 1
+          for (int done = 0;;) {
+#pragma unroll
+            for (int c = 0; c < C::kChunks; ++c)
+              if (c < n) read(c, acc, done == 0, x[c]);
+            hand_back();
+            done += p.sum_stages;
+            if (done >= tc.nks) break;
+            if (!acc_ready()) {
+              alive = false;
+              break;
+            }
+          }
+          if (!alive) break;
+#pragma unroll
+          for (int c = 0; c < C::kChunks; ++c)
+            if (c < n) reduce(c, x[c]);
         }
-        if (n == 0) hand_back();
         __syncwarp();
         if (lane == 0) ptx::mbar_arrive(stat_bar(h));
         if (!wait_bar_warp<false>(stat_bar(h), stat_phase, ctl)) {

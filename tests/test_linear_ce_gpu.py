@@ -132,6 +132,27 @@ def test_grad_matches_definition(tokens, vocab, hidden):
     check_grad(Head(tokens, vocab, hidden))
 
 
+@pytest.mark.parametrize("tokens,vocab,hidden", [(40, 300, 2048), (40, 300, 2056), (128, 1001, 4096), (100, 300, 4104),
+                                                 (130, 700, 2056), (300, 20000, 4104), (129, 400, 12296)])
+def test_loss_of_long_sums(tokens, vocab, hidden):
+    check_loss(Head(tokens, vocab, hidden, seed=8))
+    check_loss(Head(tokens, vocab, hidden, seed=9, alpha=-0.5))
+
+
+@pytest.mark.parametrize("tokens", [7, 200])
+def test_long_sums_keep_their_precision(tokens):
+    """Products of one sign, 16384 of them: the accumulator loses less than 2^-23 of itself at each of the 128 steps of
+    16 products that it takes, and is half of its sum on average, so less than 2^-17 in all; the sums' additions and lse
+    come to less than 2^-20."""
+    h = Head(tokens, 300, 16384, seed=10, ignored=0.0)
+    h.X, h.W = h.X.abs(), h.W.abs() / 64
+    z, _, lse, loss, _ = h.forward()
+    got_loss, got_lse = run_loss(h)
+    zmax = z.max(dim=1).values
+    within(got_lse, lse, (2.0 ** -17 + 2.0 ** -20) * zmax.clamp(min=1.0) + 2.0 ** -20 * lse.abs(), "lse")
+    within(got_loss, loss, 2 * (2.0 ** -17 + 2.0 ** -20) * zmax.clamp(min=1.0) + 2.0 ** -19 * lse.abs(), "loss")
+
+
 @pytest.mark.parametrize("cta_group", [0, 2])   # 2: tensor cores for few tokens too
 @pytest.mark.parametrize("tokens,vocab,hidden", [(1, 5000, 2056), (2, 31, 8), (3, 777, 136), (4, 1001, 4104), (5, 33, 264),
                                                  (6, 4097, 520), (7, 10000, 1024), (8, 2049, 2048), (8, 300, 2056),
