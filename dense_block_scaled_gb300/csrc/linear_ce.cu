@@ -5,9 +5,8 @@
 //   g_tv = exp(z_tv - lse_t) - [v = y(t)],  c_t = alpha dloss_t (0 for ignored t)
 //   dX = diag(c) g W,  dW = g^T diag(c) X
 //
-// Loss: one pass over W (of at most 8 tokens without tensor cores, linear_ce_few.cu).
-// Each 128 logits of a token leave their maximum and sum
-// (8 bytes), which a second kernel joins: (M, S) of parts (m_i, s_i) is M = max m_i,
+// Loss: one pass over W (of at most 4 tokens perhaps without tensor cores, linear_ce_few.cu).
+// Each 128 logits of a token leave their maximum and sum (8 bytes), which a second kernel joins: (M, S) of parts (m_i, s_i) is M = max m_i,
 // S = sum s_i 2^(m_i - M), in base 2, all in FP32.
 //
 // Gradient: the vocabulary in pieces.  Per piece the logits are computed again

@@ -11,6 +11,7 @@ Helpers accept torch tensors only as carriers of device memory and streams.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import threading
 
@@ -347,7 +348,7 @@ _kept = threading.local()    # per thread: {device: workspace} for the default s
 _KEEP_BYTES = 16 << 20
 
 
-def _workspace(workspace, nbytes, like, stream):
+def _workspace(workspace, nbytes, like, stream, handle):
     """(address, bytes, tensor to keep until the call is made) of the caller's workspace, or of one of torch's.
 
     On the default stream small ones are kept per thread and device (asking torch's allocator costs 6 us while work is
@@ -356,7 +357,7 @@ def _workspace(workspace, nbytes, like, stream):
     import torch
     if workspace is not None:
         return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace
-    small = stream is None and nbytes <= _KEEP_BYTES and _stream(None) == 0
+    small = stream is None and nbytes <= _KEEP_BYTES and handle == 0
     if small:
         kept = _kept.__dict__.get(like.get_device())
         if kept is not None and kept[1] >= nbytes:
@@ -379,6 +380,7 @@ def _pitch(t, width):
     return t.stride(0) if t.size(0) > 1 else width
 
 
+@functools.lru_cache(maxsize=256)   # (a ctypes call costs 0.6 us)
 def linear_ce_loss_workspace_bytes(tokens: int, vocab: int) -> int:
     return int(load().tkg_linear_ce_loss_workspace_bytes(tokens, vocab))
 
@@ -396,11 +398,11 @@ def linear_ce_loss(X, W, labels, loss, lse, alpha: float = 1.0, workspace=None, 
         _refuse((("X", X, torch.bfloat16, (tokens, hidden), True), ("W", W, torch.bfloat16, (vocab, hidden), True),
                  ("labels", labels, torch.int64, (tokens,), False), ("loss", loss, torch.float32, (tokens,), False),
                  ("lse", lse, torch.float32, (tokens,), False)))
-    lib = load()
-    at, nbytes, _keep = _workspace(workspace, lib.tkg_linear_ce_loss_workspace_bytes(tokens, vocab), X, stream)
+    lib, handle = load(), _stream(stream)
+    at, nbytes, _keep = _workspace(workspace, linear_ce_loss_workspace_bytes(tokens, vocab), X, stream, handle)
     _check(lib.tkg_linear_ce_loss(tokens, vocab, hidden, X.data_ptr(), _pitch(X, hidden), W.data_ptr(),
                                   _pitch(W, hidden), labels.data_ptr(), alpha, loss.data_ptr(), lse.data_ptr(), at,
-                                  nbytes, _stream(stream)), "tkg_linear_ce_loss")
+                                  nbytes, handle), "tkg_linear_ce_loss")
 
 
 def linear_ce_grad_workspace_bytes(tokens: int, vocab: int, hidden: int, piece: int = 0) -> int:
@@ -437,14 +439,14 @@ def linear_ce_grad(X, W, labels, lse, dloss, dX, dW, alpha: float = 1.0, accumul
         if dW is not None:
             wanted.append(("dW", dW, dW.dtype, (vocab, hidden), True))
         _refuse(wanted)
-    lib = load()
+    lib, handle = load(), _stream(stream)
     at, nbytes, _keep = _workspace(workspace, lib.tkg_linear_ce_grad_workspace_bytes(tokens, vocab, hidden, piece), X,
-                                   stream)
+                                   stream, handle)
     _check(lib.tkg_linear_ce_grad(tokens, vocab, hidden, X.data_ptr(), _pitch(X, hidden), W.data_ptr(),
                                   _pitch(W, hidden), labels.data_ptr(), alpha, lse.data_ptr(), dloss.data_ptr(),
                                   _ptr(dX), 0 if dX is None else _pitch(dX, hidden), _ptr(dW),
                                   0 if dW is None else _pitch(dW, hidden), gtype, piece, at, nbytes,
-                                  _stream(stream)), "tkg_linear_ce_grad")
+                                  handle), "tkg_linear_ce_grad")
 
 
 def gemm_grouped_dev_bf16_dgrad(sizes_dev, dD, B, dA, alpha: float = 1.0, stream=None) -> None:

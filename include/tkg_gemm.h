@@ -293,8 +293,11 @@ typedef enum {
  * to dW, whatever X, lse and dloss hold there (infinities and NaN included).
  *  - The vocabulary is worked through in pieces of `piece` entries (0: chosen
  *    from the sizes), z being computed again for each; g exists for one piece at
- *    a time, in BF16 (the products' operand type: dX and dW carry its relative
- *    rounding error of at most 2^-9 per term in any output type).
+ *    a time, without alpha * dloss[t], in BF16 (the products' operand type: dX and
+ *    dW carry its relative rounding error of at most 2^-8 per term in any output
+ *    type).  alpha * dloss[t] multiplies dX's rows in FP32 and, relative to the
+ *    largest, the rows of X that dW is made of, which are rounded to BF16 again
+ *    (the same rows where all weights are equal, as for a mean).
  *  - workspace: at least tkg_linear_ce_grad_workspace_bytes() with the same
  *    sizes and piece.  Sums are made in a fixed order: the same inputs give the
  *    same bits.
