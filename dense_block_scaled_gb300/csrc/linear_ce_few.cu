@@ -8,8 +8,9 @@
 // shared memory) serves four rows, and up to four pieces of 256 columns of all
 // four are on their way (16 warps per SM with 8 KB each; 45 KB per SM cover HBM's
 // latency at full rate, half of that measured 31 us where this takes 26).  The
-// 4 x T sums are joined over the lanes, each pair (row, token) then belongs to
-// one lane, which keeps its running maximum and sum; a block leaves one
+// 4 x T sums are joined over the lanes by exchanging halves (16 shuffles for the 16
+// sums of four tokens, against 80 in butterflies: 4000 x 2112 9.8 us against 10.9),
+// each pair (row, token) then belongs to one lane, which keeps its running maximum and sum; a block leaves one
 // (maximum, sum) per token.
 //
 // Bound by HBM: 1 token x 32768 x 2048 takes 25.9 us (134 MB, 19.8 us at the
@@ -56,9 +57,10 @@ __global__ void __launch_bounds__(kFewThreads, 2)
     lo[32] = make_float4(__uint_as_float(v.z << 16), __uint_as_float(v.z & 0xffff0000u), __uint_as_float(v.w << 16),
                          __uint_as_float(v.w & 0xffff0000u));
   }
-  // lane r TT + t keeps the running maximum and sum of rows r (mod 4) and token t
-  const int my_t = lane % TT, my_r = lane / TT;
-  const bool mine = lane < kFewRows * TT && my_t < tokens;
+  // lane (r TT + t) (32 / kSums) keeps the running maximum and sum of rows r (mod 4) and token t
+  constexpr int kSums = kFewRows * TT, kApart = 32 / kSums;
+  const int my_t = lane / kApart % TT, my_r = lane / kApart / TT;
+  const bool mine = lane % kApart == 0 && my_t < tokens;
   const long long label = mine ? __ldcg(labels + my_t) : -1;
   __syncthreads();
 
@@ -118,16 +120,24 @@ __global__ void __launch_bounds__(kFewThreads, 2)
         }
       }
     }
-    float z = 0.f;
+    // the sums over the lanes: each step exchanges halves while a lane has more than one sum, so that lane l ends
+    // with sum l / (32 / kSums)
+    float v[kSums];
 #pragma unroll
-    for (int r = 0; r < kFewRows; ++r)
+    for (int i = 0; i < kSums; ++i) v[i] = acc[i / TT][i % TT];
 #pragma unroll
-      for (int t = 0; t < TT; ++t) {
-        float s = acc[r][t];
+    for (int n = kSums / 2, o = 16; o; n >>= 1, o >>= 1) {
+      if (n) {
 #pragma unroll
-        for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-        if (lane == r * TT + t) z = s;
+        for (int i = 0; i < n; ++i) {
+          const float r = __shfl_xor_sync(0xffffffffu, (lane & o) ? v[i] : v[i + n], o);
+          v[i] = ((lane & o) ? v[i + n] : v[i]) + r;
+        }
+      } else {
+        v[0] += __shfl_xor_sync(0xffffffffu, v[0], o);
       }
+    }
+    const float z = v[0];
     if (mine && row + my_r < end) {
       if (label == row + my_r) zlabel[my_t] = z * alpha;
       const float y = z * c2, up = fmaxf(top, y);
@@ -144,11 +154,11 @@ __global__ void __launch_bounds__(kFewThreads, 2)
     top = up;
   };
 #pragma unroll
-  for (int o = TT; o < kFewRows * TT; o <<= 1) {
+  for (int o = TT * kApart; o < 32; o <<= 1) {
     const float m = __shfl_xor_sync(0xffffffffu, top, o), s = __shfl_xor_sync(0xffffffffu, sum, o);
     join(m, s);
   }
-  if (lane < TT) s_part[warp][lane] = make_float2(top, sum);
+  if (lane % kApart == 0 && my_r == 0) s_part[warp][my_t] = make_float2(top, sum);
   __syncthreads();
   if (threadIdx.x < TT && int(threadIdx.x) < tokens) {
     top = -INFINITY;
@@ -185,8 +195,8 @@ int ce_few_blocks(int tokens, int vocab, int hidden) {
   const int tt = few_width(tokens);
   if (tokens > kFewTokens || tt * ((hidden + 255) / 256) * 256 > kFewElements) return 0;
   // One token at any vocabulary; with more the multiply-adds cost more than idle SMs do, past 16384 entries for
-  // two (hidden 2048: 4000 entries 10.4 us against 13.7 on tiles, 16384 17.6 against 17.9, 32768 30.2 against 27.5)
-  // and past 8192 for four (4000 entries 11.9 against 13.7, 16384 19.8 against 17.8).
+  // two (hidden 2112, replayed from a graph: 32768 entries 32.9 us against 26.9 on tiles; 16384 at hidden 512 6.4)
+  // and past 8192 for four (8000 entries 10.7 us, 10457 16.4 against 13.5 on tiles; hidden 512 5.9, 7.2 against 7.8).
   if (tt > 1 && (long long)vocab * tt > 32768) return 0;
   const int blocks = ceil_div(vocab, kFewRows * (kFewThreads / 32));   // four rows a warp at least
   return blocks < kFewMaxBlocks ? blocks : kFewMaxBlocks;
