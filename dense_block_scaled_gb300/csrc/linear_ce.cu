@@ -235,7 +235,8 @@ GradPlan grad_plan(int tokens, int vocab, int hidden, int piece) {
 }
 
 // Whether a spare warp of the logits' blocks writes the weighted rows of X: it takes about a microsecond per 2 KB
-// of row, and two of them should stay behind a tile's time, a microsecond per 256 hidden or more.
+// of row, and two of them (half of the tile's four) should stay behind a tile's time, a microsecond per 256 hidden or
+// more.  Every such warp first finds the largest of the T weights, 512 loads at 16384 tokens.
 bool rows_on_the_side(int tokens, int piece, int hidden) {
   const double tiles = double(ceil_div(piece, 256)) * ceil_div(tokens, kTrainBN);
   return tokens / tiles <= 4.0 && tokens <= 16384;

@@ -21,7 +21,7 @@ static tkg_status launch_logits(const void* X, size_t x_bytes, const void* W, si
     const int sums = ceil_div(p.split_stages, kSumStages);
     p.sum_stages = ceil_div(p.split_stages, sums);
     // the narrow form has no registers for more sums than its two accumulators
-    if (p.n <= kNarrowTokens && sums <= 2)
+    if (train_narrow(p.n, ceil_div(p.m, 256)) && sums <= 2)
       return launch_train<false, false, EPI, GRP_NONE, SHAPE_NARROW>(tmA, tmB, tmD, p, stream);
     if (sums > 1) return launch_train<false, false, EPI, GRP_NONE, SHAPE_SUMS>(tmA, tmB, tmD, p, stream);
   }

@@ -139,6 +139,13 @@ def test_loss_of_long_sums(tokens, vocab, hidden):
     check_loss(Head(tokens, vocab, hidden, seed=9, alpha=-0.5))
 
 
+@pytest.mark.parametrize("tokens,vocab,hidden", [(5, 19713, 64), (17, 20001, 4096), (40, 20000, 2056), (64, 33333, 264),
+                                                 (65, 20000, 264), (128, 20000, 4104), (33, 40000, 2048)])
+def test_loss_of_few_tokens_and_many_entries(tokens, vocab, hidden):
+    check_loss(Head(tokens, vocab, hidden, seed=11))
+    check_loss(Head(tokens, vocab, hidden, seed=12, alpha=-0.5, ignored=0.9))
+
+
 @pytest.mark.parametrize("tokens", [7, 200])
 def test_long_sums_keep_their_precision(tokens):
     """Products of one sign, 16384 of them: the accumulator loses less than 2^-23 of itself at each of the 128 steps of
