@@ -25,6 +25,9 @@ static tkg_status launch_logits(const void* X, size_t x_bytes, const void* W, si
       return launch_train<false, false, EPI, GRP_NONE, SHAPE_NARROW>(tmA, tmB, tmD, p, stream);
     if (sums > 1) return launch_train<false, false, EPI, GRP_NONE, SHAPE_SUMS>(tmA, tmB, tmD, p, stream);
   }
+  if constexpr (EPI == EPI_DLOGITS)
+    if (train_narrow(p.n, ceil_div(p.m, 256)))
+      return launch_train<false, false, EPI, GRP_NONE, SHAPE_NARROW>(tmA, tmB, tmD, p, stream);
   return launch_train<false, false, EPI, GRP_NONE>(tmA, tmB, tmD, p, stream);
 }
 

@@ -146,11 +146,13 @@ inline bool train_dual(int m, int n, long long count, int stages) {
          train_rounds(rows * ceil_div(n, 256)) * train_tile_time(stages, false);
 }
 
-// Whether the loss of n tokens runs in the kernel's narrow form, given its tiles.  It needs more of them than there are
-// pairs of SMs: 16 tokens take 32.5 us narrow and 46.9 wide at 20000 x 4096, 162.8 and 175.2 at 131072 x 4096, 8.7 and
-// 10.7 at 50000 x 256, but 13.1 and 12.7 at 8000 x 2048.  Past 64 tokens its four epilogue warps tell (a block has a
-// quarter of the wide form's), and it pays while it spares a thin second round: 128 tokens 13.4 and 15.4 us at
-// 23000 x 1024, 44.4 and 49.2 at 27000 x 4096, but 30.5 and 29.1 at 32768 x 2048 and 76.0 and 72.2 at 40000 x 4096.
+// Whether the logits of n tokens run in the kernel's narrow form, given their tiles.  It needs more
+// of them than there are pairs of SMs: the loss of 16 tokens takes 32.5 us narrow and 46.9 wide at 20000 x 4096, 162.8 and
+// 175.2 at 131072 x 4096, 8.7 and 10.7 at 50000 x 256, but 13.1 and 12.7 at 8000 x 2048.  Past 64 tokens its four
+// epilogue warps tell (a block has a quarter of the wide form's), and it pays while it spares a thin second round:
+// 128 tokens 13.4 and 15.4 us at 23000 x 1024, 44.4 and 49.2 at 27000 x 4096, but 30.5 and 29.1 at 32768 x 2048
+// and 76.0 and 72.2 at 40000 x 4096.  The gradient's logits go the same way (dX and dW of 40 tokens x 21648 x 1024
+// 41.8 and 44.4 us, of 128 x 20000 x 4096 108.6 and 116.2, of 128 x 27000 x 1024 50.1 and 48.6).
 constexpr int kNarrowTokens = 128;
 inline bool train_narrow(int n, int tiles) {
   return n <= kNarrowTokens && tiles > kPairs && (n <= kNarrowTokens / 2 || 2 * tiles <= 3 * kPairs);

@@ -46,11 +46,11 @@
 // before it turns to the exponentials.  lse of 4096 x 131072 x 4096: 5.7e-7 off
 // (relative) against 1.2e-6 in one sum, 2497 against 2480 us.
 //
-// NARROW (loss of at most 128 tokens with more tiles than pairs of SMs, where reading the
+// NARROW (logits of at most 128 tokens with more tiles than pairs of SMs, where reading the
 // weights bounds the time): two blocks per SM, each with half the shared memory and 4
 // epilogue warps.  Twice the tiles run at once, so that few tiles do not leave a thin last
-// round, and one block's set-up and epilogue run under the other's loads.  Two sums at
-// most, in the two accumulators.
+// round, and one block's set-up and epilogue run under the other's loads.  Of the loss
+// two sums at most, in the two accumulators.
 //
 // Epilogues (EPI):
 //   LOSS     per token (column) and 128 vocabulary rows: the largest logit and the

@@ -146,6 +146,13 @@ def test_loss_of_few_tokens_and_many_entries(tokens, vocab, hidden):
     check_loss(Head(tokens, vocab, hidden, seed=12, alpha=-0.5, ignored=0.9))
 
 
+@pytest.mark.parametrize("tokens,vocab,hidden,piece", [(5, 19713, 64, 0), (40, 20000, 264, 0), (64, 25000, 136, 20000),
+                                                       (128, 20000, 72, 0), (1, 19999, 520, 0)])
+def test_grad_of_few_tokens_and_many_entries(tokens, vocab, hidden, piece):
+    check_grad(Head(tokens, vocab, hidden, seed=13), piece=piece)
+    check_grad(Head(tokens, vocab, hidden, seed=14, alpha=-0.5, ignored=0.9), dtype=F32, piece=piece)
+
+
 @pytest.mark.parametrize("tokens", [7, 200])
 def test_long_sums_keep_their_precision(tokens):
     """Products of one sign, 16384 of them: the accumulator loses less than 2^-23 of itself at each of the 128 steps of
