@@ -664,10 +664,11 @@ __global__ void __launch_bounds__(384, 1)
       const bool got = ptx::clc_read(clc_resp(cslot), x);
       __syncwarp();
       if (lane == 0) {
+        const uint32_t bar = ptx::clc_read_done(clc_empty(cslot), x);
         if (leader)
-          ptx::mbar_arrive(clc_empty(cslot));
+          ptx::mbar_arrive(bar);
         else
-          ptx::mbar_arrive_relaxed_cluster(ptx::map_to_rank(clc_empty(cslot), 0));
+          ptx::mbar_arrive_relaxed_cluster(ptx::map_to_rank(bar, 0));
       }
       if (++cslot == 2) {
         cslot = 0;
@@ -686,10 +687,11 @@ __global__ void __launch_bounds__(384, 1)
       if (!wait_bar<false>(clc_full(cslot), cphase, ctl)) return -2;
       uint32_t x = 0;
       const bool got = ptx::clc_read(clc_resp(cslot), x);
+      const uint32_t bar = ptx::clc_read_done(clc_empty(cslot), x);
       if (leader)
-        ptx::mbar_arrive(clc_empty(cslot));
+        ptx::mbar_arrive(bar);
       else
-        ptx::mbar_arrive_relaxed_cluster(ptx::map_to_rank(clc_empty(cslot), 0));
+        ptx::mbar_arrive_relaxed_cluster(ptx::map_to_rank(bar, 0));
       if (++cslot == 2) {
         cslot = 0;
         cphase ^= 1u;
@@ -936,6 +938,7 @@ __global__ void __launch_bounds__(384, 1)
         while (true) {
           // the answer slot is free once every role has read its last answer
           if (!wait_bar<CG == 2>(clc_empty(slot), ph ^ 1u, ctl)) break;
+          ptx::fence_proxy_async_smem();   // the readers' loads, then the answer's store
           ptx::mbar_arrive_expect_tx(clc_full(slot), 16u);
           if (CG == 2) ptx::mbar_expect_tx_relaxed_cluster(ptx::map_to_rank(clc_full(slot), 1), 16u);
           ptx::clc_try_cancel<CG == 2>(clc_resp(slot), clc_full(slot));
@@ -943,12 +946,23 @@ __global__ void __launch_bounds__(384, 1)
           if (!wait_bar<false>(clc_full(slot), ph, ctl)) break;
           uint32_t x = 0;
           const bool got = ptx::clc_read(clc_resp(slot), x);
-          ptx::mbar_arrive(clc_empty(slot));
+          ptx::mbar_arrive(ptx::clc_read_done(clc_empty(slot), x));
           if (++slot == 2) {
             slot = 0;
             ph ^= 1u;
           }
-          if (!got) break;
+          if (!got) {
+            // both CTAs' roles have read the last two answers: no arrival from the other CTA is in flight when
+            // this one leaves and its shared memory goes to the next kernel
+            for (int i = 0; i < 2; ++i) {
+              if (!wait_bar<CG == 2>(clc_empty(slot), ph ^ 1u, ctl)) break;
+              if (++slot == 2) {
+                slot = 0;
+                ph ^= 1u;
+              }
+            }
+            break;
+          }
         }
       }
     }

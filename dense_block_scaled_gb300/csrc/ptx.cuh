@@ -161,6 +161,13 @@ __device__ __forceinline__ bool clc_read(uint32_t resp, uint32_t& first_ctaid_x)
   first_ctaid_x = x;
   return ok != 0;
 }
+// Where a reader of an answer arrives to give its slot (whose barrier is `bar`) back.  The slot is refilled through the
+// async proxy once every reader has arrived, and an arrival does not wait for earlier loads; its address therefore
+// depends on the value read (below 2^31), so that the read is over before it.  Otherwise a late reader may see the
+// answer after next and work on a tile that is not its own.
+__device__ __forceinline__ uint32_t clc_read_done(uint32_t bar, uint32_t first_ctaid_x) {
+  return bar + (first_ctaid_x >> 31);
+}
 
 // ---------------------------------------------------------------- programmatic dependent launch
 // Let the next kernel in the stream start launching its CTAs.

@@ -556,13 +556,12 @@ __global__ void __launch_bounds__(TrainConfig<A_MN, B_MN, EPI, GRP, SHAPE>::kThr
         return -2;
       uint32_t x = 0;
       const bool got = ptx::clc_read(clc_resp(cslot), x);
-      // The slot is overwritten (through the async proxy) once every reader has arrived, so the read has to be over
-      // before the arrival: its address depends on the value read (x is below 2^31).  Without that the role that
+      // The read is over before the arrival (see clc_read_done).  Without that the role that
       // arrives last, the MMA issuer, now and then read the answer after next, missed a tile, and the kernel ran
       // into its wait limit.  (A proxy fence by every reader cost 0.5 us a tile; the scheduler has the one.)
       if constexpr (WARP) __syncwarp();
       if (!WARP || lane == 0) {
-        const uint32_t bar = clc_empty(cslot) + (x >> 31);
+        const uint32_t bar = ptx::clc_read_done(clc_empty(cslot), x);
         if (leader)
           ptx::mbar_arrive(bar);
         else
@@ -902,7 +901,7 @@ __global__ void __launch_bounds__(TrainConfig<A_MN, B_MN, EPI, GRP, SHAPE>::kThr
           if (!wait_bar<false>(clc_full(slot), ph, ctl)) break;
           uint32_t x = 0;
           const bool got = ptx::clc_read(clc_resp(slot), x);
-          ptx::mbar_arrive(clc_empty(slot) + (x >> 31));
+          ptx::mbar_arrive(ptx::clc_read_done(clc_empty(slot), x));
           if (++slot == 2) {
             slot = 0;
             ph ^= 1u;
