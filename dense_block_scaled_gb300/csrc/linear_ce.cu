@@ -116,9 +116,10 @@ __global__ void __launch_bounds__(256)
   top = s_max[lane & 7];
 #pragma unroll
   for (int o = 4; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-  if (blockIdx.x == 0 && tid == 0) *scale = top;
+  const float s = ce_scale(top);
+  if (blockIdx.x == 0 && tid == 0) *scale = s;
   for (int t = blockIdx.x * 8 + warp; t < tokens; t += gridDim.x * 8)
-    ce_weighted_row(t, lane, vocab, hidden, X, ldx, labels, dloss, alpha, top, out);
+    ce_weighted_row(t, lane, vocab, hidden, X, ldx, labels, dloss, alpha, s, out);
 }
 
 // ---------------------------------------------------------------- dX from its FP32 parts

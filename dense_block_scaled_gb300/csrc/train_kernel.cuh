@@ -230,8 +230,10 @@ __device__ __forceinline__ int column_of_lane(int lane) {
 }
 
 // ---- rows of X with the tokens' weights: row t times c_t / s with c_t = alpha dloss_t (0 for ignored tokens) and
-// s = max |c_t|.  Rows of ignored tokens are zeros whatever they hold: their g is 0, but 0 times a padded position's
-// NaN is not.
+// s = max |c_t|, or 1 where that maximum (which leaves NaN out) is no scale: with s = 0 or infinite the product of the
+// row and s would not be c_t's, and a weight that is not a number has to reach dW.  Rows of ignored tokens are zeros
+// whatever they hold: their g is 0, but 0 times a padded position's NaN is not.
+__device__ __forceinline__ float ce_scale(float top) { return top > 0.f && top < INFINITY ? top : 1.f; }
 __device__ __forceinline__ float ce_weight(int t, int vocab, const long long* labels, const float* dloss, float alpha) {
   const long long y = __ldcg(labels + t);
   const float d = __ldcg(dloss + t);
@@ -239,11 +241,11 @@ __device__ __forceinline__ float ce_weight(int t, int vocab, const long long* la
 }
 // One row, by a warp.
 __device__ __forceinline__ void ce_weighted_row(int t, int lane, int vocab, int hidden, const uint16_t* X, size_t ldx,
-                                                const long long* labels, const float* dloss, float alpha, float top,
+                                                const long long* labels, const float* dloss, float alpha, float s,
                                                 uint16_t* out) {
   const long long y = __ldcg(labels + t);
   const bool kept = y >= 0 && y < vocab;
-  const float w = top == 0.f ? 0.f : __fdiv_rn(ce_weight(t, vocab, labels, dloss, alpha), top);
+  const float w = __fdiv_rn(ce_weight(t, vocab, labels, dloss, alpha), s);
   const uint4* src = reinterpret_cast<const uint4*>(X + size_t(t) * ldx);
   uint4* dst = reinterpret_cast<uint4*>(out + size_t(t) * size_t(hidden));
   const int vec = hidden / 8;
@@ -870,6 +872,7 @@ __global__ void __launch_bounds__(TrainConfig<A_MN, B_MN, EPI, GRP, SHAPE>::kThr
 #pragma unroll
         for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
       }
+      const float s = ce_scale(top);
       uint32_t cslot = 0, cphase = 0;
 #pragma unroll 1
       for (int t = first_tile; t >= 0;) {
@@ -877,8 +880,8 @@ __global__ void __launch_bounds__(TrainConfig<A_MN, B_MN, EPI, GRP, SHAPE>::kThr
           const int begin = int((long long)p.n * t / num_tiles), end = int((long long)p.n * (t + 1) / num_tiles);
 #pragma unroll 1
           for (int row = begin + int(rank); row < end; row += 2)
-            ce_weighted_row(row, lane, p.vocab, p.k, p.x, p.ldx, p.labels, p.dloss, p.alpha, top, p.rows);
-          if (t == 0 && leader && lane == 0) *p.rows_scale = top;
+            ce_weighted_row(row, lane, p.vocab, p.k, p.x, p.ldx, p.labels, p.dloss, p.alpha, s, p.rows);
+          if (t == 0 && leader && lane == 0) *p.rows_scale = s;
         }
         t = __shfl_sync(0xffffffffu, next_tile(Warp{}, t, cslot, cphase), 0);
       }
