@@ -7,7 +7,9 @@
 //
 // Loss: one pass over W (of at most 4 tokens perhaps without tensor cores, linear_ce_few.cu).
 // Each 128 logits of a token leave their maximum and sum (8 bytes), which a second kernel joins: (M, S) of parts (m_i, s_i) is M = max m_i,
-// S = sum s_i 2^(m_i - M), in base 2, all in FP32.
+// S = sum s_i e^(m_i - M), all in FP32.  The maxima stay logits as they are and only differences go to base 2, so
+// lse = M + log S has S >= 1 and is the label's own logit where that one dominates: a loss is never below 0 (with
+// maxima kept in base 2 the losses of such tokens were off by up to 1e-7 of the logit, either way).
 //
 // Gradient: the vocabulary in pieces.  Per piece the logits are computed again
 // (2 T V H flops, against reading T V logits back), g goes to a BF16 workspace of
@@ -28,9 +30,6 @@
 namespace tkg {
 namespace {
 
-constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kLn2 = 0.6931471805599453f;
-
 // ---------------------------------------------------------------- joining the loss's parts
 // 8 tokens per block (64 contiguous bytes of a part) and 128 threads per token,
 // which read the parts in batches of 4 with the loads in flight together.
@@ -44,12 +43,6 @@ __global__ void __launch_bounds__(1024)
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int t = blockIdx.x * kJoinTokens + (lane & 7);
   float top = -INFINITY, sum = 0.f;
-  auto join = [&](float m, float s) {
-    const float up = fmaxf(top, m);
-    const float base = fabsf(up) == INFINITY ? 0.f : up;   // no inf - inf
-    sum = sum * ptx::ex2(top - base) + s * ptx::ex2(m - base);
-    top = up;
-  };
   if (t < tokens) {
 #pragma unroll 1
     for (int i = threadIdx.x >> 3; i < parts; i += 512) {
@@ -59,17 +52,17 @@ __global__ void __launch_bounds__(1024)
         x[j] = i + 128 * j < parts ? __ldcg(part + size_t(i + 128 * j) * size_t(tokens) + t)
                                    : make_float2(-INFINITY, 0.f);
       const float up = fmaxf(fmaxf(x[0].x, x[1].x), fmaxf(x[2].x, x[3].x));
-      const float base = fabsf(up) == INFINITY ? 0.f : up;
+      const float base = fabsf(up) == INFINITY ? 0.f : up;   // no inf - inf
       float s = 0.f;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) s += x[j].y * ptx::ex2(x[j].x - base);
-      join(up, s);
+      for (int j = 0; j < 4; ++j) s += x[j].y * ptx::ex2((x[j].x - base) * kLog2e);
+      ce_join(top, sum, up, s);
     }
   }
 #pragma unroll
   for (int o = 8; o < 32; o <<= 1) {
     const float m = __shfl_xor_sync(0xffffffffu, top, o), s = __shfl_xor_sync(0xffffffffu, sum, o);
-    join(m, s);
+    ce_join(top, sum, m, s);
   }
   if (lane < kJoinTokens) s_part[warp][lane] = make_float2(top, sum);
   __syncthreads();
@@ -78,14 +71,17 @@ __global__ void __launch_bounds__(1024)
     top = -INFINITY;
     sum = 0.f;
 #pragma unroll
-    for (int w = 0; w < 8; ++w) join(s_part[(lane >> 3) * 8 + w][lane & 7].x, s_part[(lane >> 3) * 8 + w][lane & 7].y);
+    for (int w = 0; w < 8; ++w) {
+      const float2 x = s_part[(lane >> 3) * 8 + w][lane & 7];
+      ce_join(top, sum, x.x, x.y);
+    }
 #pragma unroll
     for (int o = 8; o < 32; o <<= 1) {
       const float m = __shfl_xor_sync(0xffffffffu, top, o), s = __shfl_xor_sync(0xffffffffu, sum, o);
-      join(m, s);
+      ce_join(top, sum, m, s);
     }
     if (lane < kJoinTokens && t < tokens) {
-      const float l = (top + log2f(sum)) * kLn2;
+      const float l = top + logf(sum);
       const long long y = __ldcg(labels + t);
       lse[t] = l;
       loss[t] = (y >= 0 && y < vocab) ? l - __ldcg(zlabel + t) : 0.f;

@@ -27,7 +27,7 @@ constexpr int kFewRows = 4;
 template <int TT, int DEPTH>
 __global__ void __launch_bounds__(kFewThreads, 2)
     ce_few_kernel(int tokens, int vocab, int hidden, const uint16_t* __restrict__ X, size_t ldx,
-                  const uint16_t* __restrict__ W, size_t ldw, const long long* __restrict__ labels, float alpha, float c2,
+                  const uint16_t* __restrict__ W, size_t ldw, const long long* __restrict__ labels, float alpha,
                   float2* __restrict__ part, float* __restrict__ zlabel) {
   // 256 columns at a time: [columns / 256][token][half of a lane's 8 columns][lane][4], so that a quarter of a
   // warp reads 128 contiguous bytes
@@ -64,7 +64,7 @@ __global__ void __launch_bounds__(kFewThreads, 2)
   const long long label = mine ? __ldcg(labels + my_t) : -1;
   __syncthreads();
 
-  float top = -INFINITY, sum = 0.f;   // of z c2, in base 2
+  float top = -INFINITY, sum = 0.f;   // largest logit, and the sum of exponentials relative to it
 
   // DEPTH pieces of 256 columns in flight; a group of four rows takes a multiple of DEPTH steps (the ones past its
   // columns are zeros)
@@ -139,31 +139,23 @@ __global__ void __launch_bounds__(kFewThreads, 2)
     }
     const float z = v[0];
     if (mine && row + my_r < end) {
-      if (label == row + my_r) zlabel[my_t] = z * alpha;
-      const float y = z * c2, up = fmaxf(top, y);
-      const float base = fabsf(up) == INFINITY ? 0.f : up;   // no inf - inf
-      sum = sum * ptx::ex2(top - base) + ptx::ex2(y - base);
-      top = up;
+      const float y = z * alpha;
+      if (label == row + my_r) zlabel[my_t] = y;
+      ce_join(top, sum, y, 1.f);
     }
   }
   // over the four rows' lanes, then over the block's warps
-  auto join = [&](float m, float s) {
-    const float up = fmaxf(top, m);
-    const float base = fabsf(up) == INFINITY ? 0.f : up;
-    sum = sum * ptx::ex2(top - base) + s * ptx::ex2(m - base);
-    top = up;
-  };
 #pragma unroll
   for (int o = TT * kApart; o < 32; o <<= 1) {
     const float m = __shfl_xor_sync(0xffffffffu, top, o), s = __shfl_xor_sync(0xffffffffu, sum, o);
-    join(m, s);
+    ce_join(top, sum, m, s);
   }
   if (lane % kApart == 0 && my_r == 0) s_part[warp][my_t] = make_float2(top, sum);
   __syncthreads();
   if (threadIdx.x < TT && int(threadIdx.x) < tokens) {
     top = -INFINITY;
     sum = 0.f;
-    for (int w = 0; w < kFewThreads / 32; ++w) join(s_part[w][threadIdx.x].x, s_part[w][threadIdx.x].y);
+    for (int w = 0; w < kFewThreads / 32; ++w) ce_join(top, sum, s_part[w][threadIdx.x].x, s_part[w][threadIdx.x].y);
     part[size_t(blockIdx.x) * size_t(tokens) + threadIdx.x] = make_float2(top, sum);
   }
 }
@@ -183,7 +175,7 @@ tkg_status launch_few(int blocks, int smem, const TrainParams& p, const void* X,
     attr_set[dev] = true;
   }
   return launch_small(kern, dim3(unsigned(blocks)), dim3(kFewThreads), stream, unsigned(smem), p.n, p.m, p.k,
-                      static_cast<const uint16_t*>(X), ldx, static_cast<const uint16_t*>(W), ldw, p.labels, p.alpha, p.c2,
+                      static_cast<const uint16_t*>(X), ldx, static_cast<const uint16_t*>(W), ldw, p.labels, p.alpha,
                       p.part, p.zlabel);
 }
 

@@ -53,8 +53,8 @@
 // two sums at most, in the two accumulators.
 //
 // Epilogues (EPI):
-//   LOSS     per token (column) and 128 vocabulary rows: the largest logit and the
-//            sum of exponentials in base 2, and, where the token's label falls among
+//   LOSS     per token (column) and 128 vocabulary rows: the largest logit, the
+//            sum of exponentials relative to it, and, where the token's label falls among
 //            them, its logit.  A thread holds 8 columns by 4 rows of each 32 x 32
 //            block (the 16x256b load); columns are joined over 8 lanes by exchanging
 //            halves (7 shuffles down for the maximum, 7 back, 7 for the sum, against
@@ -227,6 +227,16 @@ __device__ __forceinline__ void unfold_columns(float own, int lane, float (&x)[8
 }
 __device__ __forceinline__ int column_of_lane(int lane) {
   return 16 * ((lane >> 4) & 1) + 8 * ((lane >> 3) & 1) + 2 * (lane & 3) + ((lane >> 2) & 1);
+}
+
+// ---- joins a maximum and the sum of exponentials relative to it, (top, sum), with another, (m, s): one of the two
+// factors is 1, exactly
+constexpr float kLog2e = 1.4426950408889634f;
+__device__ __forceinline__ void ce_join(float& top, float& sum, float m, float s) {
+  const float d = m == top ? 0.f : m - top;   // (infinities of one sign: not their difference)
+  const float e = ptx::ex2(-fabsf(d) * kLog2e);
+  sum = m > top ? fmaf(sum, e, s) : fmaf(s, e, sum);
+  top = fmaxf(top, m);
 }
 
 // ---- rows of X with the tokens' weights: row t times c_t / s with c_t = alpha dloss_t (0 for ignored tokens) and
@@ -1105,12 +1115,14 @@ __global__ void __launch_bounds__(TrainConfig<A_MN, B_MN, EPI, GRP, SHAPE>::kThr
           }
           const float own = fold_columns(top, lane, [](float a, float b) { return fmaxf(a, b); });
           unfold_columns(own, lane, top);
+          // Differences first: the largest logit then counts as exactly 1, and a sum of at least 1 with that logit
+          // beside it gives an lse that is not below any logit
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
             const int j = 4 * (i >> 1) + (i & 1);
-            const float sub = fabsf(top[i]) == INFINITY ? 0.f : top[i] * c2;   // no inf - inf
-            sum[i] = (ptx::ex2(fmaf(x[j], c2, -sub)) + ptx::ex2(fmaf(x[j + 2], c2, -sub))) +
-                     (ptx::ex2(fmaf(x[j + 16], c2, -sub)) + ptx::ex2(fmaf(x[j + 18], c2, -sub)));
+            const float sub = fabsf(top[i]) == INFINITY ? 0.f : top[i];   // no inf - inf
+            sum[i] = (ptx::ex2((x[j] - sub) * c2) + ptx::ex2((x[j + 2] - sub) * c2)) +
+                     (ptx::ex2((x[j + 16] - sub) * c2) + ptx::ex2((x[j + 18] - sub) * c2));
           }
           if (c2 == 0.f && edge) {   // scale 0: 0 * -inf is not a number
 #pragma unroll
@@ -1118,7 +1130,7 @@ __global__ void __launch_bounds__(TrainConfig<A_MN, B_MN, EPI, GRP, SHAPE>::kThr
               sum[i] = float(rows_there > 0) + float(rows_there > 8) + float(rows_there > 16) + float(rows_there > 24);
           }
           const float s = fold_columns(sum, lane, [](float a, float b) { return a + b; });
-          stat[q * C::kBN + c * 32 + column_of_lane(lane)] = make_float2(own == -INFINITY ? own : own * c2, s);
+          stat[q * C::kBN + c * 32 + column_of_lane(lane)] = make_float2(own == -INFINITY ? own : own * fabsf(alpha), s);
         };
         if constexpr (SHAPE != SHAPE_SUMS) {
           const bool two = C::kNarrow && p.sum_stages < tc.nks;   // sums, in both accumulators
@@ -1184,7 +1196,7 @@ __global__ void __launch_bounds__(TrainConfig<A_MN, B_MN, EPI, GRP, SHAPE>::kThr
           }
           const float sub = fabsf(m) == INFINITY ? 0.f : m;
 #pragma unroll
-          for (int i = 0; i < 4; ++i) s += x[i].y * ptx::ex2(x[i].x - sub);
+          for (int i = 0; i < 4; ++i) s += x[i].y * ptx::ex2((x[i].x - sub) * kLog2e);
           p.part[size_t(tc.a0 >> 7) * size_t(p.n) + col] = make_float2(m, s);
         }
       } else if constexpr (EPI == EPI_DLOGITS) {

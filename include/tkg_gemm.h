@@ -262,7 +262,7 @@ tkg_status tkg_gemm_bf16_noalloc(int m, int n, int k, const void *A, const void 
  * Softmax cross entropy of a linear head over a large vocabulary:
  *   z[t][v] = alpha * sum_h X[t][h] * W[v][h]              (never stored)
  *   lse[t]  = log sum_v exp z[t][v]
- *   loss[t] = lse[t] - z[t][labels[t]]
+ *   loss[t] = lse[t] - z[t][labels[t]]                     (never below 0)
  * X: tokens x hidden (row pitch ldx), W: vocab x hidden (row pitch ldw), both
  * bfloat16; labels: 64-bit, one per token.  A label outside [0, vocab) (such as
  * -100) ignores its row: loss 0 (lse is still that row's).  loss, lse: FP32.

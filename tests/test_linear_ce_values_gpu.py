@@ -65,3 +65,78 @@ def test_zero_weights_give_zero_gradients():
         h.dloss[:] = 0
         gX, dW = weight_gradient(h, h.forward()[2].float(), "add", True)
         assert (gX == 0).all() and (dW == 1).all()
+
+
+def product_error(h):
+    """Largest error of each token's logits: products are exact, and the accumulator of 16-product steps loses less than
+    2^-23 of what it holds, at most the sum of magnitudes, at each; two roundings more (the scale, a sum of sums)."""
+    mag = abs(h.alpha) * (h.X.to(F64).abs() @ h.W.to(F64).abs().T).max(dim=1).values
+    return (h.shape[2] / 16 + 2) * 2.0 ** -23 * mag
+
+
+# forms of the loss: a few tokens without tensor cores, and on them (cta_group 2); narrow, wide, and sums in parts
+LOSS_FORMS = [(1, 3000, 264, 0), (3, 1001, 4104, 0), (4, 777, 256, 2), (20, 20003, 256, 0), (40, 20000, 4104, 0),
+              (100, 1500, 520, 0), (300, 700, 4104, 0), (513, 2049, 64, 0), (2, 1, 64, 0), (90, 1, 64, 0)]
+
+
+@pytest.mark.parametrize("alpha", [1.0, -0.5, 3.0])
+@pytest.mark.parametrize("tokens,vocab,hidden,cta_group", LOSS_FORMS)
+def test_loss_to_its_last_bits(tokens, vocab, hidden, cta_group, alpha):
+    """lse moves by no more than its logits; exponentials 2^-21 each, their sums' additions under 40 roundings: 2^-18 in
+    all.  The definition's loss is not negative, and neither is the kernel's."""
+    tkg.set_option(tkg.OPT_CTA_GROUP, cta_group)
+    h = Head(tokens, vocab, hidden, alpha=alpha, ignored=0.0, seed=21)
+    _, _, lse, loss, _ = h.forward()
+    got, got_lse = run_loss(h)
+    tol = product_error(h) + 2.0 ** -18 + 2.0 ** -23 * lse.abs()
+    assert ((got_lse.to(F64) - lse).abs() <= tol).all()
+    assert ((got.to(F64) - loss).abs() <= 2 * tol).all()
+    assert (got >= 0).all()
+
+
+@pytest.mark.parametrize("alpha", [1.0, -0.5])
+@pytest.mark.parametrize("scale", [0.25, 1.0])
+@pytest.mark.parametrize("tokens,vocab,hidden,cta_group", [f for f in LOSS_FORMS if f[1] > f[0]])
+def test_loss_of_tokens_the_model_is_sure_of(tokens, vocab, hidden, cta_group, scale, alpha):
+    """A label whose row is the token's own: its logit is above the others by more than 30, whose exponentials vanish
+    beside it in 32 bits, so that lse is that logit and the loss exactly 0."""
+    tkg.set_option(tkg.OPT_CTA_GROUP, cta_group)
+    h = Head(tokens, vocab, hidden, alpha=alpha, ignored=0.0, seed=22, spread=1e-3)
+    h.y = torch.randperm(vocab, device="cuda")[:tokens]
+    # powers of two: the rows stay exact; logits of 64 to 256 whatever hidden is
+    h.W[h.y] = (h.X.float() * (scale / alpha * 2.0 ** (8 - round(torch.log2(torch.tensor(float(hidden))).item())))).to(BF16)
+    z, _, lse, loss, _ = h.forward()
+    own = z.gather(1, h.y[:, None])[:, 0]
+    rest = z.scatter(1, h.y[:, None], float("-inf")).max(dim=1).values
+    sure = own - rest > 30
+    assert sure.any()
+    got, got_lse = run_loss(h)
+    assert (got[sure] == 0).all() and (got >= 0).all()
+    assert ((got_lse.to(F64) - lse).abs() <= product_error(h) + 2.0 ** -18 + 2.0 ** -23 * lse.abs()).all()
+
+
+@pytest.mark.parametrize("tokens,vocab,hidden,cta_group", LOSS_FORMS)
+def test_infinities_in_rows_that_count(tokens, vocab, hidden, cta_group):
+    tkg.set_option(tkg.OPT_CTA_GROUP, cta_group)
+    clean = Head(tokens, vocab, hidden, ignored=0.0, seed=23)
+    want, want_lse = run_loss(clean)
+    for where in ("one", "all"):
+        h = Head(tokens, vocab, hidden, ignored=0.0, seed=23)
+        at = tokens // 2
+        h.W[:, 0] = torch.where(h.W[:, 0] == 0, torch.ones_like(h.W[:, 0]), h.W[:, 0])
+        if where == "all":   # every logit of the token -inf: nothing to sum
+            h.W[:, 0] = -h.W[:, 0].abs()
+            h.X[at] = 0
+        h.X[at, 0] = float("inf")
+        z = h.X[at].to(F64) * h.W.to(F64)
+        z = torch.where((h.X[at] == 0)[None, :], torch.zeros_like(z), z).sum(dim=1)
+        lse = torch.logsumexp(z, 0)
+        loss = lse - z[h.y[at]]
+        got, got_lse = run_loss(h)
+        assert torch.equal(torch.nan_to_num(got_lse[at].to(F64), nan=0.5, posinf=2.0, neginf=-2.0),
+                           torch.nan_to_num(lse, nan=0.5, posinf=2.0, neginf=-2.0))
+        assert torch.equal(torch.nan_to_num(got[at].to(F64), nan=0.5, posinf=2.0, neginf=-2.0),
+                           torch.nan_to_num(loss, nan=0.5, posinf=2.0, neginf=-2.0))
+        if where == "one":
+            rest = torch.arange(tokens, device="cuda") != at
+            assert torch.equal(got[rest], want[rest]) and torch.equal(got_lse[rest], want_lse[rest])
