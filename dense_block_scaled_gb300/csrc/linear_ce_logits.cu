@@ -13,21 +13,16 @@ static tkg_status launch_logits(const void* X, size_t x_bytes, const void* W, si
   if ((st = map_k_major(&tmB, X, p.n, p.k, x_bytes, p.n_tile / 2)) != TKG_OK) return st;
   tmD = tmA;
   if (EPI == EPI_DLOGITS &&
-      (st = map_out(&tmD, p.d, p.m, p.n, 1, p.ldd * 2, size_t(p.m) * p.ldd * 2, false)) != TKG_OK)
+      (st = map_out(&tmD, p.d, p.m, p.n, 1, p.ldd * 2, size_t(p.m) * p.ldd * 2, false, true)) != TKG_OK)
     return st;
   p.splits = 1;
   p.split_stages = ceil_div(p.k, 64);
-  if constexpr (EPI == EPI_LOSS) {
-    const int sums = ceil_div(p.split_stages, kSumStages);
-    p.sum_stages = ceil_div(p.split_stages, sums);
-    // the narrow form has no registers for more sums than its two accumulators
-    if (train_narrow(p.n, ceil_div(p.m, 256)) && sums <= 2)
-      return launch_train<false, false, EPI, GRP_NONE, SHAPE_NARROW>(tmA, tmB, tmD, p, stream);
-    if (sums > 1) return launch_train<false, false, EPI, GRP_NONE, SHAPE_SUMS>(tmA, tmB, tmD, p, stream);
-  }
-  if constexpr (EPI == EPI_DLOGITS)
-    if (train_narrow(p.n, ceil_div(p.m, 256)))
-      return launch_train<false, false, EPI, GRP_NONE, SHAPE_NARROW>(tmA, tmB, tmD, p, stream);
+  const int sums = ceil_div(p.split_stages, kSumStages);
+  p.sum_stages = ceil_div(p.split_stages, sums);
+  // the narrow form has no registers for more sums than its two accumulators
+  if (train_narrow(p.n, ceil_div(p.m, 256)) && sums <= 2)
+    return launch_train<false, false, EPI, GRP_NONE, SHAPE_NARROW>(tmA, tmB, tmD, p, stream);
+  if (sums > 1) return launch_train<false, false, EPI, GRP_NONE, SHAPE_SUMS>(tmA, tmB, tmD, p, stream);
   return launch_train<false, false, EPI, GRP_NONE>(tmA, tmB, tmD, p, stream);
 }
 

@@ -27,13 +27,13 @@ inline tkg_status map_mn_major(CUtensorMap* map, const void* base, int mn, int k
   return encode_2d(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, base, uint64_t(mn), uint64_t(k), row_bytes, 64,
                    box_rows ? uint32_t(box_rows) : mn_box_rows(k), CU_TENSOR_MAP_SWIZZLE_128B);
 }
-// Output: `parts` matrices of m x n.  Store boxes of 16 rows by 128 bytes, or (turned: D's columns are the
-// output's rows) 16 rows by the 64 bytes of a warp's 32 rows of D.
+// Output: `parts` matrices of m x n.  Store boxes of 16 rows by 128 bytes, or (half: BF16 in 32 columns, a chunk of
+// DLOGITS or, turned, a warp's 32 rows of D) by 64 bytes.
 inline tkg_status map_out(CUtensorMap* map, const void* base, int m, int n, int parts, size_t row_bytes,
-                          size_t part_bytes, bool f32, bool turned = false) {
+                          size_t part_bytes, bool f32, bool half = false) {
   return encode_3d_swizzled(map, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, base,
-                            uint64_t(n), uint64_t(m), uint64_t(parts), row_bytes, part_bytes, f32 || turned ? 32 : 64, 16,
-                            1, turned ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B);
+                            uint64_t(n), uint64_t(m), uint64_t(parts), row_bytes, part_bytes, f32 || half ? 32 : 64, 16,
+                            1, half ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B);
 }
 // The same matrices in the boxes that fetch what is added to into L2.
 inline tkg_status map_prefetch(CUtensorMap* map, const void* base, int m, int n, int parts, size_t row_bytes,
@@ -159,7 +159,8 @@ inline bool train_narrow(int n, int tiles) {
 }
 // Stages (64 k each) that one accumulator of a logit sums.  Tensor memory adds towards zero, so a sum's error grows
 // with its length: of lse, relative, 6.3e-7 at 2048 products and 1.3e-6 at 4096 in one sum.  Sums of at most 2048
-// are added in the epilogue's registers.
+// are added in the epilogue's registers.  The gradient's logits are the loss's, bit for bit: where lse is the label's
+// own logit, g is exactly 0.
 constexpr int kSumStages = 32;
 
 // Launch of a small kernel that waits for the previous grid itself (griddepcontrol.wait).

@@ -40,7 +40,7 @@
 // two MMAs.  The SMs read a quarter fewer bytes from L2 for the same products;
 // these kernels run under the power cap, where that shows as clock.
 //
-// SUMS (logits of the loss with hidden > 2048): tensor memory adds towards zero, so a
+// SUMS (logits with hidden > 2048): tensor memory adds towards zero, so a
 // sum's error grows with its length.  An accumulator takes at most 2048 products; the
 // epilogue gathers such sums in registers (64 a thread) and hands the accumulator back
 // before it turns to the exponentials.  lse of 4096 x 131072 x 4096: 5.7e-7 off
@@ -49,8 +49,8 @@
 // NARROW (logits of at most 128 tokens with more tiles than pairs of SMs, where reading the
 // weights bounds the time): two blocks per SM, each with half the shared memory and 4
 // epilogue warps.  Twice the tiles run at once, so that few tiles do not leave a thin last
-// round, and one block's set-up and epilogue run under the other's loads.  Of the loss
-// two sums at most, in the two accumulators.
+// round, and one block's set-up and epilogue run under the other's loads.
+// Two sums at most, in the two accumulators.
 //
 // Epilogues (EPI):
 //   LOSS     per token (column) and 128 vocabulary rows: the largest logit, the
@@ -80,14 +80,14 @@ enum : int { EPI_LOSS = 0, EPI_DLOGITS = 1, EPI_BF16 = 2, EPI_F32 = 3, EPI_BF16_
 // consecutive k, each with its own output matrix.  Row counts in device memory.
 enum : int { GRP_NONE = 0, GRP_ROWS = 1, GRP_K = 2 };
 // Tile shapes: 256 x up to 256; NARROW 256 x up to 128, two blocks per SM; DUAL 256 x 512.
-// SUMS (LOSS): WIDE with sums longer than one accumulator takes.
+// SUMS (logits): WIDE with sums longer than one accumulator takes.
 enum : int { SHAPE_WIDE = 0, SHAPE_NARROW = 1, SHAPE_DUAL = 2, SHAPE_SUMS = 3 };
 
 struct TrainParams {
   int m, n, k;                 // output rows and columns, contraction length (GRP_ROWS: n, GRP_K: k is the row capacity)
   int kstages;                 // ceil(k / 64)
   int splits, split_stages;    // k split: part z covers stages [z * split_stages, ...)
-  int sum_stages;              // LOSS: stages summed in one accumulator; the epilogue adds the next to it
+  int sum_stages;              // logits: stages summed in one accumulator; the epilogue adds the next to it
   int tiles_m, tiles_n, num_tiles;
   int n_tile;                  // tile width, a multiple of 16 (GRP_ROWS: per group, by its rows; DUAL: 512)
   int raster_group;
@@ -155,6 +155,15 @@ __device__ __forceinline__ void tma_add_3d(const void* tmap, uint32_t src, int32
 __device__ __forceinline__ void tmem_ld_16x256b_x4(uint32_t taddr, uint32_t (&r)[16]) {
   asm volatile(
       "tcgen05.ld.sync.aligned.16x256b.x4.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+}
+// 32 lanes x 16 columns: thread t gets its lane's
+__device__ __forceinline__ void tmem_ld_32x32b_x16(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
       "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
       : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
         "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
@@ -289,6 +298,7 @@ struct TrainConfig {
   static constexpr int kChunks = kBN / 32 / (kEpiWarps / 4);   // 32-column chunks of an accumulator per epilogue warp
   // DUAL: stages at a tile's start and end in which the first accumulator runs ahead of the second
   static constexpr int kSkew = 2;
+  static constexpr bool kLogits = EPI == EPI_LOSS || EPI == EPI_DLOGITS;
   static constexpr int kThreads = 32 * (4 + kEpiWarps);
   static constexpr int kAcc = 2;
   static constexpr int kABytes = 128 * 128;
@@ -733,12 +743,12 @@ __global__ void __launch_bounds__(TrainConfig<A_MN, B_MN, EPI, GRP, SHAPE>::kThr
         if constexpr (!C::kDual) {
           int it = 0;
 #pragma unroll 1
-          do {   // (one turn, but for LOSS)
+          do {   // (one turn, but for long logits)
             if (!acc_free(acc)) {
               ok = false;
               break;
             }
-            const int from = it, to = EPI == EPI_LOSS ? min(it + p.sum_stages, tc.nks) : tc.nks;
+            const int from = it, to = C::kLogits ? min(it + p.sum_stages, tc.nks) : tc.nks;
 #pragma unroll 1
             for (; it < to; ++it) {
               if (!wait_bar<false>(full_bar(stage), phase, ctl)) {
@@ -981,9 +991,9 @@ __global__ void __launch_bounds__(TrainConfig<A_MN, B_MN, EPI, GRP, SHAPE>::kThr
       }
     };
     // Cross entropy: of the tile's columns col0 + 32 c + lane, the labels (-1: ignored, or no such column) and
-    // for DLOGITS lse in base 2; read one tile ahead
+    // for DLOGITS lse; read one tile ahead
     int label[C::kChunks], label_next[C::kChunks];
-    float l2[C::kChunks] = {}, l2_next[C::kChunks] = {};
+    float lse[C::kChunks] = {}, lse_next[C::kChunks] = {};
     auto read_columns = [&](int t, int (&lab)[C::kChunks], float (&ls)[C::kChunks]) {
       if constexpr (EPI == EPI_LOSS || EPI == EPI_DLOGITS) {
         const TrainTile tc = coords(t);
@@ -999,7 +1009,7 @@ __global__ void __launch_bounds__(TrainConfig<A_MN, B_MN, EPI, GRP, SHAPE>::kThr
         }
       }
     };
-    if (first_tile >= 0) read_columns(first_tile, label_next, l2_next);
+    if (first_tile >= 0) read_columns(first_tile, label_next, lse_next);
 #pragma unroll 1
     for (int t = first_tile; t >= 0 && alive;) {
       const TrainTile tile = coords(t);
@@ -1008,9 +1018,9 @@ __global__ void __launch_bounds__(TrainConfig<A_MN, B_MN, EPI, GRP, SHAPE>::kThr
 #pragma unroll
       for (int c = 0; c < C::kChunks; ++c) {
         label[c] = label_next[c];
-        l2[c] = l2_next[c] * 1.4426950408889634f;
+        lse[c] = lse_next[c];
       }
-      if (t_next >= 0) read_columns(t_next, label_next, l2_next);
+      if (t_next >= 0) read_columns(t_next, label_next, lse_next);
 #pragma unroll 1
       for (int sub = 0; sub < (C::kDual ? tile.subs : 1); ++sub) {
       TrainTile tc = tile;               // the columns of one accumulator
@@ -1059,6 +1069,29 @@ __global__ void __launch_bounds__(TrainConfig<A_MN, B_MN, EPI, GRP, SHAPE>::kThr
         accbits ^= 1u << acc;
         if (!C::kDual) acc ^= 1u;
       };
+      // SUMS: this warp's sums gather in registers, and each accumulator goes back as soon as it is read
+      [[maybe_unused]] auto gather = [&](int n, auto&& read, float (&x)[C::kChunks][32]) {
+#pragma unroll 1
+        for (int done = 0;;) {
+#pragma unroll
+          for (int c = 0; c < C::kChunks; ++c)
+            if (c < n) read(c, acc, done == 0, x[c]);
+          hand_back();
+          done += p.sum_stages;
+          if (done >= tc.nks) return true;
+          if (!acc_ready()) return false;
+        }
+      };
+      // NARROW: a tile's two sums lie in the two accumulators
+      [[maybe_unused]] const bool two = C::kNarrow && p.sum_stages < tc.nks;
+      if (two) {
+        acc ^= 1u;
+        if (!acc_ready()) {
+          alive = false;
+          break;
+        }
+        acc ^= 1u;
+      }
       if constexpr (EPI == EPI_LOSS) {
         float2* stat = s_stat + (turn & 1u) * uint32_t(4 * C::kBN) + h * C::kChunks * 32;
         const uint32_t stat_phase = (turn & 1u);
@@ -1133,15 +1166,6 @@ __global__ void __launch_bounds__(TrainConfig<A_MN, B_MN, EPI, GRP, SHAPE>::kThr
           stat[q * C::kBN + c * 32 + column_of_lane(lane)] = make_float2(own == -INFINITY ? own : own * fabsf(alpha), s);
         };
         if constexpr (SHAPE != SHAPE_SUMS) {
-          const bool two = C::kNarrow && p.sum_stages < tc.nks;   // sums, in both accumulators
-          if (two) {
-            acc ^= 1u;
-            if (!acc_ready()) {
-              alive = false;
-              break;
-            }
-            acc ^= 1u;
-          }
 #pragma unroll 1
           for (int c = 0; c < n; ++c) {
             float x[32];
@@ -1158,22 +1182,11 @@ __global__ void __launch_bounds__(TrainConfig<A_MN, B_MN, EPI, GRP, SHAPE>::kThr
             if (two) hand_back();
           }
         } else {
-          // the sums gather in registers, and the accumulators go back as soon as they are read
           float x[C::kChunks][32];
-#pragma unroll 1
-          for (int done = 0;;) {
-#pragma unroll
-            for (int c = 0; c < C::kChunks; ++c)
-              if (c < n) read(c, acc, done == 0, x[c]);
-            hand_back();
-            done += p.sum_stages;
-            if (done >= tc.nks) break;
-            if (!acc_ready()) {
-              alive = false;
-              break;
-            }
+          if (!gather(n, read, x)) {
+            alive = false;
+            break;
           }
-          if (!alive) break;
 #pragma unroll
           for (int c = 0; c < C::kChunks; ++c)
             if (c < n) reduce(c, x[c]);
@@ -1201,18 +1214,33 @@ __global__ void __launch_bounds__(TrainConfig<A_MN, B_MN, EPI, GRP, SHAPE>::kThr
         }
       } else if constexpr (EPI == EPI_DLOGITS) {
         const int n = idle ? 0 : nch;
-        uint32_t w[32];                  // 64 columns
+        auto read = [&](int c, uint32_t a, bool first, float (&x)[32]) {
+          const uint32_t from = tq + a * uint32_t(C::kBN) + uint32_t(c * 32);
+          if (SHAPE == SHAPE_WIDE) {
+            uint32_t v[32];
+            ptx::tmem_ld_32x32b_x32(from, v);
+            ptx::tmem_ld_wait_for(v);
 #pragma unroll
-        for (int c = 0; c < C::kChunks; ++c) {
-          if (c >= n) break;
-          uint32_t v[32];
-          ptx::tmem_ld_32x32b_x32(tbase + uint32_t(c * 32), v);
-          ptx::tmem_ld_wait_for(v);
-          if (c + 1 == n) hand_back();
-          float g[32];
+            for (int j = 0; j < 32; ++j) x[j] = __uint_as_float(v[j]);
+          } else {   // (no registers for a second 32 beside what it is added to)
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+              uint32_t v[16];
+              ptx::tmem_ld_32x32b_x16(from + uint32_t(16 * u), v);
+              ptx::tmem_ld_wait_for(v);
+#pragma unroll
+              for (int j = 0; j < 16; ++j)
+                x[16 * u + j] = first ? __uint_as_float(v[j]) : x[16 * u + j] + __uint_as_float(v[j]);
+            }
+          }
+        };
+        auto write = [&](int c, float (&g)[32]) {
+          // The logit rounded as the loss has it (__fmul_rn: not fused), and then its difference: the label's
+          // exp(z - lse) - 1 is 0 where lse is that logit, and the rounding of z log2(e) (2^-24 of the logit's
+          // size) stays out of every g
 #pragma unroll
           for (int j = 0; j < 32; ++j)
-            g[j] = ptx::ex2(fmaf(__uint_as_float(v[j]), p.c2, -__shfl_sync(0xffffffffu, l2[c], j)));
+            g[j] = ptx::ex2((__fmul_rn(g[j], alpha) - __shfl_sync(0xffffffffu, lse[c], j)) * kLog2e);
           int off;
           const uint32_t hits = among_rows(label[c], off);
           if (hits) {
@@ -1228,24 +1256,56 @@ __global__ void __launch_bounds__(TrainConfig<A_MN, B_MN, EPI, GRP, SHAPE>::kThr
             for (int j = 0; j < 32; ++j)
               if ((gone >> j) & 1u) g[j] = 0.f;
           }
+          uint32_t w[16];
 #pragma unroll
-          for (int j = 0; j < 16; ++j) w[16 * (c & 1) + j] = ptx::pack_bf16x2(g[2 * j], g[2 * j + 1]);
-          // two chunks, or a last one
-          const int c0 = c & ~1, at = h * C::kChunks * 32 + c0 * 32, col = tc.n0 + at;
-          if (!((c & 1) || c + 1 == n) || col >= tc.n_end || row0 >= p.m) continue;
-          if (at + 64 <= tc.nt) {
-            store_rows(w, row0, [&](uint32_t buf, int r) { ptx::tma_store_3d(&tmD, buf, col, r, 0); });
-          } else if (row0 + lane < p.m) {   // the tile ends within the 64: 16 columns (a 32-byte sector) at a time
+          for (int j = 0; j < 16; ++j) w[j] = ptx::pack_bf16x2(g[2 * j], g[2 * j + 1]);
+          const int at = h * C::kChunks * 32 + c * 32, col = tc.n0 + at;
+          if (col >= tc.n_end || row0 >= p.m) return;
+          if (at + 32 <= tc.nt) {
+            stage_box(
+                [&](uint32_t buf) {
+#pragma unroll
+                  for (int j = 0; j < 4; ++j)
+                    ptx::st_shared_v4(buf + uint32_t(lane * 64) + ((uint32_t(j) ^ ((uint32_t(lane) >> 1) & 3u)) << 4),
+                                      w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
+                },
+                [&](uint32_t buf) {
+                  ptx::tma_store_3d(&tmD, buf, col, row0, 0);
+                  if (row0 + 16 < p.m) ptx::tma_store_3d(&tmD, buf + 1024u, col, row0 + 16, 0);
+                });
+          } else if (row0 + lane < p.m) {   // the tile ends within the 32: its 16 columns (a 32-byte sector)
             uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.d) + size_t(row0 + lane) * p.ldd + col);
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-              if (at + i * 16 < tc.nt && col + i * 16 < tc.n_end) {
-                dst[2 * i] = make_uint4(w[8 * i], w[8 * i + 1], w[8 * i + 2], w[8 * i + 3]);
-                dst[2 * i + 1] = make_uint4(w[8 * i + 4], w[8 * i + 5], w[8 * i + 6], w[8 * i + 7]);
-              }
+            dst[0] = make_uint4(w[0], w[1], w[2], w[3]);
+            dst[1] = make_uint4(w[4], w[5], w[6], w[7]);
           }
+        };
+        if constexpr (SHAPE != SHAPE_SUMS) {
+#pragma unroll
+          for (int c = 0; c < C::kChunks; ++c) {
+            if (c >= n) break;
+            float x[32];
+            read(c, acc, true, x);
+            if (two) read(c, acc ^ 1u, false, x);
+            if (c + 1 == n) {
+              hand_back();
+              if (two) hand_back();
+            }
+            write(c, x);
+          }
+          if (n == 0) {
+            hand_back();
+            if (two) hand_back();
+          }
+        } else {
+          float x[C::kChunks][32];
+          if (!gather(n, read, x)) {
+            alive = false;
+            break;
+          }
+#pragma unroll
+          for (int c = 0; c < C::kChunks; ++c)
+            if (c < n) write(c, x[c]);
         }
-        if (n == 0) hand_back();
       } else if constexpr (EPI == EPI_BF16) {   // tiles are a multiple of 64 wide: chunks in pairs
         const int n = idle ? 0 : nch;
         const bool nothing = GRP == GRP_K && tc.nks == 0;   // no rows: the sum is empty, the accumulator undefined

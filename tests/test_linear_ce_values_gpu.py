@@ -140,3 +140,32 @@ def test_infinities_in_rows_that_count(tokens, vocab, hidden, cta_group):
         if where == "one":
             rest = torch.arange(tokens, device="cuda") != at
             assert torch.equal(got[rest], want[rest]) and torch.equal(got_lse[rest], want_lse[rest])
+
+
+# forms of the gradient's logits: wide, narrow, and both with sums in parts
+GRAD_FORMS = [(40, 700, 264), (300, 1500, 64), (20, 20003, 256), (40, 20000, 4104), (300, 700, 4104), (130, 900, 8200)]
+
+
+@pytest.mark.parametrize("alpha", [1.0, -0.5, 0.37])
+@pytest.mark.parametrize("tokens,vocab,hidden", GRAD_FORMS)
+def test_gradient_of_tokens_the_model_is_sure_of(tokens, vocab, hidden, alpha):
+    """Where lse is the label's own logit, g is exactly 0 there: what a sure token gives to dX and its label's row of dW
+    is the other logits' exponentials, here below e^-30.  (10% of them: logits off by 2^-7 in the worst case.)"""
+    tkg.set_option(tkg.OPT_CTA_GROUP, 2)   # logits of the same kernel for the loss of few tokens
+    h = Head(tokens, vocab, hidden, alpha=alpha, ignored=0.0, seed=24, spread=1e-3)
+    h.y = torch.randperm(vocab, device="cuda")[:tokens]
+    scale = 2.0 ** round(7.5 - torch.log2(torch.tensor(abs(alpha) * hidden)).item())
+    h.W[h.y] = (h.X.float() * (scale if alpha > 0 else -scale)).to(BF16)   # logits of about 128 to 256
+    z, _, lse, _, _ = h.forward()
+    loss, got_lse = run_loss(h)
+    others = torch.exp(z - lse[:, None]).scatter(1, h.y[:, None], 0.0)
+    sure = (loss == 0) & (others.sum(dim=1) < 2.0 ** -30)
+    assert sure.any()
+    dX, dW = run_grad(h, got_lse, dtype=F32)
+    w = (h.dloss.to(F64) * abs(alpha))[:, None]
+    # an ulp of BF16 for g, another for the weighted rows and the result
+    boundX = 1.1 * (w * others) @ h.W.to(F64).abs() + 1e-30
+    boundW = 1.1 * (w * others).T @ h.X.to(F64).abs() + 1e-30
+    # a token that is not sure has a g of its own in its label's row only
+    assert (dX[sure].to(F64).abs() <= boundX[sure]).all()
+    assert (dW[h.y[sure]].to(F64).abs() <= boundW[h.y[sure]]).all()
