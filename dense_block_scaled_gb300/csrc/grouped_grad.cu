@@ -100,6 +100,12 @@ tkg_status tkg_gemm_grouped_dev_bf16_wgrad(int groups, const int* m_sizes_dev, i
   static_cast<TailMaps&>(extra) = tail;
   if ((st = map_prefetch(&extra.d, dB, n, k, groups, size_t(k) * 4, size_t(n) * size_t(k) * 4)) != TKG_OK) return st;
   p.n_tile = train_n_tile(k, kTileF32);
+  p.sum_stages = kSumStages;
+  // A group's sum may be longer than one accumulator takes (16384 positive terms in one were off by 6.7e-5 of the sum,
+  // in parts by 2.6e-6).  8 experts of 2048 rows, 4096 x 7168: stored 656 us in place of 633 (in 512-wide tiles), added 696
+  // of 686; 64 experts of 250 rows, 2048 x 2048: 187 of 206 and 409 of 404.
+  if (m_capacity > 64 * kSumStages)
+    return launch_train<true, true, EPI_F32, GRP_K, SHAPE_SUMS>(tmA, tmB, tmD, p, stream, extra);
   return dual ? launch_train<true, true, EPI_F32, GRP_K, SHAPE_DUAL>(tmA, tmB, tmD, p, stream, extra)
               : launch_train<true, true, EPI_F32, GRP_K>(tmA, tmB, tmD, p, stream, extra);
 }

@@ -423,7 +423,10 @@ tkg_status tkg_linear_ce_grad(int tokens, int vocab, int hidden, const void* X, 
         if ((st = map_prefetch(&extra.d, static_cast<float*>(dW) + size_t(v0) * size_t(lddw), nv, hidden, 1,
                                size_t(lddw) * 4, size_t(nv) * size_t(lddw) * 4)) != TKG_OK)
           return st;
-        st = launch_train<false, true, EPI_F32, GRP_NONE>(tmA, tmB, tmD, q, stream, extra);
+        const int sums = ceil_div(q.split_stages, kSumStages);
+        q.sum_stages = ceil_div(q.split_stages, sums);
+        st = sums > 1 ? launch_train<false, true, EPI_F32, GRP_NONE, SHAPE_SUMS>(tmA, tmB, tmD, q, stream, extra)
+                      : launch_train<false, true, EPI_F32, GRP_NONE>(tmA, tmB, tmD, q, stream, extra);
       }
       if (st != TKG_OK) return st;
     }

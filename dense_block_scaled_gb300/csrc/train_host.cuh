@@ -157,10 +157,12 @@ constexpr int kNarrowTokens = 128;
 inline bool train_narrow(int n, int tiles) {
   return n <= kNarrowTokens && tiles > kPairs && (n <= kNarrowTokens / 2 || 2 * tiles <= 3 * kPairs);
 }
-// Stages (64 k each) that one accumulator of a logit sums.  Tensor memory adds towards zero, so a sum's error grows
-// with its length: of lse, relative, 6.3e-7 at 2048 products and 1.3e-6 at 4096 in one sum.  Sums of at most 2048
-// are added in the epilogue's registers.  The gradient's logits are the loss's, bit for bit: where lse is the label's
-// own logit, g is exactly 0.
+// Stages (64 k each) that one accumulator sums where the result is FP32 (logits, FP32 weight gradients).  Tensor memory
+// adds towards zero, so a sum's error grows with its length: terms of one sign lose 3e-6 of it over 2048 terms,
+// 6.7e-5 over 16384 and 1.5e-4 over 30000; of lse, 6.3e-7 at 2048 products and 1.3e-6 at 4096 in one sum.
+// Sums of at most 2048 are added in the epilogue's registers.  The gradient's logits are the loss's, bit for bit: where
+// lse is the label's own logit, g is exactly 0.  BF16 results, dX from its FP32 parts among them, take one sum each:
+// what it loses is 1/30 of their own rounding's 2^-9 at 16384 terms of one sign, and less where signs differ.
 constexpr int kSumStages = 32;
 
 // Launch of a small kernel that waits for the previous grid itself (griddepcontrol.wait).

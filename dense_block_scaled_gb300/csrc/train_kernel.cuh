@@ -40,10 +40,10 @@
 // two MMAs.  The SMs read a quarter fewer bytes from L2 for the same products;
 // these kernels run under the power cap, where that shows as clock.
 //
-// SUMS (logits with hidden > 2048): tensor memory adds towards zero, so a
-// sum's error grows with its length.  An accumulator takes at most 2048 products; the
-// epilogue gathers such sums in registers (64 a thread) and hands the accumulator back
-// before it turns to the exponentials.  lse of 4096 x 131072 x 4096: 5.7e-7 off
+// SUMS (logits and FP32 weight gradients of more than 2048 products): tensor memory adds
+// towards zero, so a sum's error grows with its length.  An accumulator takes at most 2048
+// products; the epilogue gathers such sums in registers (64 a thread) and hands the
+// accumulator back before it turns to the rest.  lse of 4096 x 131072 x 4096: 5.7e-7 off
 // (relative) against 1.2e-6 in one sum, 2497 against 2480 us.
 //
 // NARROW (logits of at most 128 tokens with more tiles than pairs of SMs, where reading the
@@ -80,14 +80,14 @@ enum : int { EPI_LOSS = 0, EPI_DLOGITS = 1, EPI_BF16 = 2, EPI_F32 = 3, EPI_BF16_
 // consecutive k, each with its own output matrix.  Row counts in device memory.
 enum : int { GRP_NONE = 0, GRP_ROWS = 1, GRP_K = 2 };
 // Tile shapes: 256 x up to 256; NARROW 256 x up to 128, two blocks per SM; DUAL 256 x 512.
-// SUMS (logits): WIDE with sums longer than one accumulator takes.
+// SUMS: WIDE with sums longer than one accumulator takes.
 enum : int { SHAPE_WIDE = 0, SHAPE_NARROW = 1, SHAPE_DUAL = 2, SHAPE_SUMS = 3 };
 
 struct TrainParams {
   int m, n, k;                 // output rows and columns, contraction length (GRP_ROWS: n, GRP_K: k is the row capacity)
   int kstages;                 // ceil(k / 64)
   int splits, split_stages;    // k split: part z covers stages [z * split_stages, ...)
-  int sum_stages;              // logits: stages summed in one accumulator; the epilogue adds the next to it
+  int sum_stages;              // NARROW, SUMS: stages summed in one accumulator; the epilogue adds the next to it
   int tiles_m, tiles_n, num_tiles;
   int n_tile;                  // tile width, a multiple of 16 (GRP_ROWS: per group, by its rows; DUAL: 512)
   int raster_group;
@@ -160,14 +160,15 @@ __device__ __forceinline__ void tmem_ld_16x256b_x4(uint32_t taddr, uint32_t (&r)
         "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
       : "r"(taddr));
 }
-// 32 lanes x 16 columns: thread t gets its lane's
-__device__ __forceinline__ void tmem_ld_32x32b_x16(uint32_t taddr, uint32_t (&r)[16]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
-      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-      : "r"(taddr));
+// 32 lanes x 8 columns: thread t gets its lane's
+__device__ __forceinline__ void tmem_ld_32x32b_x8(uint32_t taddr, uint32_t (&r)[8]) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+               : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_ld_wait_for(uint32_t (&r)[8]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7])::"memory");
 }
 __device__ __forceinline__ void tmem_ld_wait_for(uint32_t (&r)[16]) {
   asm volatile("tcgen05.wait::ld.sync.aligned;"
@@ -298,7 +299,7 @@ struct TrainConfig {
   static constexpr int kChunks = kBN / 32 / (kEpiWarps / 4);   // 32-column chunks of an accumulator per epilogue warp
   // DUAL: stages at a tile's start and end in which the first accumulator runs ahead of the second
   static constexpr int kSkew = 2;
-  static constexpr bool kLogits = EPI == EPI_LOSS || EPI == EPI_DLOGITS;
+  static constexpr bool kSums = kNarrow || SHAPE == SHAPE_SUMS;   // sums longer than one accumulator takes
   static constexpr int kThreads = 32 * (4 + kEpiWarps);
   static constexpr int kAcc = 2;
   static constexpr int kABytes = 128 * 128;
@@ -743,12 +744,12 @@ __global__ void __launch_bounds__(TrainConfig<A_MN, B_MN, EPI, GRP, SHAPE>::kThr
         if constexpr (!C::kDual) {
           int it = 0;
 #pragma unroll 1
-          do {   // (one turn, but for long logits)
+          do {   // (one turn, but for long sums)
             if (!acc_free(acc)) {
               ok = false;
               break;
             }
-            const int from = it, to = C::kLogits ? min(it + p.sum_stages, tc.nks) : tc.nks;
+            const int from = it, to = C::kSums ? min(it + p.sum_stages, tc.nks) : tc.nks;
 #pragma unroll 1
             for (; it < to; ++it) {
               if (!wait_bar<false>(full_bar(stage), phase, ctl)) {
@@ -1069,17 +1070,34 @@ __global__ void __launch_bounds__(TrainConfig<A_MN, B_MN, EPI, GRP, SHAPE>::kThr
         accbits ^= 1u << acc;
         if (!C::kDual) acc ^= 1u;
       };
-      // SUMS: this warp's sums gather in registers, and each accumulator goes back as soon as it is read
+      // SUMS: this warp's sums gather in registers, and each accumulator goes back as soon as it is read.  (From 0:
+      // taking the first as it is selects for every register, and spilled.)
       [[maybe_unused]] auto gather = [&](int n, auto&& read, float (&x)[C::kChunks][32]) {
+#pragma unroll
+        for (int c = 0; c < C::kChunks; ++c)
+#pragma unroll
+          for (int j = 0; j < 32; ++j) x[c][j] = 0.f;
 #pragma unroll 1
         for (int done = 0;;) {
 #pragma unroll
           for (int c = 0; c < C::kChunks; ++c)
-            if (c < n) read(c, acc, done == 0, x[c]);
+            if (c < n) read(c, acc, false, x[c]);
           hand_back();
           done += p.sum_stages;
           if (done >= tc.nks) return true;
           if (!acc_ready()) return false;
+        }
+      };
+      // 32 columns of this lane's row, alone or added to x: 8 at a time, as there are no registers for 32 more
+      [[maybe_unused]] auto read_row = [&](int c, uint32_t a, bool first, float (&x)[32]) {
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          uint32_t v[8];
+          ptx::tmem_ld_32x32b_x8(tq + a * uint32_t(C::kBN) + uint32_t(c * 32 + u * 8), v);
+          ptx::tmem_ld_wait_for(v);
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            x[8 * u + j] = first ? __uint_as_float(v[j]) : x[8 * u + j] + __uint_as_float(v[j]);
         }
       };
       // NARROW: a tile's two sums lie in the two accumulators
@@ -1215,23 +1233,14 @@ __global__ void __launch_bounds__(TrainConfig<A_MN, B_MN, EPI, GRP, SHAPE>::kThr
       } else if constexpr (EPI == EPI_DLOGITS) {
         const int n = idle ? 0 : nch;
         auto read = [&](int c, uint32_t a, bool first, float (&x)[32]) {
-          const uint32_t from = tq + a * uint32_t(C::kBN) + uint32_t(c * 32);
-          if (SHAPE == SHAPE_WIDE) {
+          if constexpr (SHAPE == SHAPE_WIDE) {
             uint32_t v[32];
-            ptx::tmem_ld_32x32b_x32(from, v);
+            ptx::tmem_ld_32x32b_x32(tq + a * uint32_t(C::kBN) + uint32_t(c * 32), v);
             ptx::tmem_ld_wait_for(v);
 #pragma unroll
             for (int j = 0; j < 32; ++j) x[j] = __uint_as_float(v[j]);
-          } else {   // (no registers for a second 32 beside what it is added to)
-#pragma unroll
-            for (int u = 0; u < 2; ++u) {
-              uint32_t v[16];
-              ptx::tmem_ld_32x32b_x16(from + uint32_t(16 * u), v);
-              ptx::tmem_ld_wait_for(v);
-#pragma unroll
-              for (int j = 0; j < 16; ++j)
-                x[16 * u + j] = first ? __uint_as_float(v[j]) : x[16 * u + j] + __uint_as_float(v[j]);
-            }
+          } else {
+            read_row(c, a, first, x);
           }
         };
         auto write = [&](int c, float (&g)[32]) {
@@ -1332,14 +1341,9 @@ __global__ void __launch_bounds__(TrainConfig<A_MN, B_MN, EPI, GRP, SHAPE>::kThr
       } else {
         const int n = idle ? 0 : nch;
         [[maybe_unused]] const bool nothing = GRP == GRP_K && tc.nks == 0;
-#pragma unroll 1
-        for (int c = 0; c < n; ++c) {
+        auto write = [&](int c, uint32_t (&v)[32]) {
           const int col = col0 + c * 32;
-          uint32_t v[32];
-          ptx::tmem_ld_32x32b_x32(tbase + uint32_t(c * 32), v);
-          ptx::tmem_ld_wait_for(v);
-          if (c + 1 == n) hand_back();
-          if (col >= tc.n_end || row0 >= p.m) continue;
+          if (col >= tc.n_end || row0 >= p.m) return;
           if constexpr (EPI == EPI_BF16_T) {
             // even lanes take column j for rows (lane, lane + 1), odd lanes column j + 1 for rows (lane - 1, lane)
             uint32_t w[16];
@@ -1377,7 +1381,7 @@ __global__ void __launch_bounds__(TrainConfig<A_MN, B_MN, EPI, GRP, SHAPE>::kThr
               }
             }
           } else {   // F32: tiles are a multiple of 32 wide
-            if (nothing && p.accumulate) continue;   // adding nothing
+            if (nothing && p.accumulate) return;   // adding nothing
 #pragma unroll
             for (int j = 0; j < 32; ++j) v[j] = nothing ? 0u : __float_as_uint(__uint_as_float(v[j]) * alpha);
             store_rows(v, row0, [&](uint32_t buf, int r) {
@@ -1387,8 +1391,33 @@ __global__ void __launch_bounds__(TrainConfig<A_MN, B_MN, EPI, GRP, SHAPE>::kThr
                 ptx::tma_store_3d(&tmD, buf, col, r, tc.z);
             });
           }
+        };
+        if constexpr (SHAPE != SHAPE_SUMS) {
+#pragma unroll 1
+          for (int c = 0; c < n; ++c) {
+            uint32_t v[32];
+            ptx::tmem_ld_32x32b_x32(tbase + uint32_t(c * 32), v);
+            ptx::tmem_ld_wait_for(v);
+            if (c + 1 == n) hand_back();
+            write(c, v);
+          }
+          if (n == 0) hand_back();
+        } else {
+          float x[C::kChunks][32];
+          if (!gather(n, read_row, x)) {
+            alive = false;
+            break;
+          }
+#pragma unroll
+          for (int c = 0; c < C::kChunks; ++c) {
+            if (c < n) {
+              uint32_t v[32];
+#pragma unroll
+              for (int j = 0; j < 32; ++j) v[j] = __float_as_uint(x[c][j]);
+              write(c, v);
+            }
+          }
         }
-        if (n == 0) hand_back();
       }
       }
       t = t_next;

@@ -315,6 +315,8 @@ size_t tkg_linear_ce_grad_workspace_bytes(int tokens, int vocab, int hidden, int
  *   dgrad: dA[o_g + i][kk] = bf16_rn(alpha * sum_j dD[o_g + i][j] * B_g[j][kk])
  *   wgrad: dB_g[j][kk] (+)= alpha * sum_i dD[o_g + i][j] * A[o_g + i][kk]
  * dD: m_capacity x n, A and dA: m_capacity x k, B and dB: groups x n x k.
+ *  - FP32 results (and tkg_linear_ce_grad's) are sums of sums of at most 2048
+ *    products, added in FP32 registers.
  *  - Rows outside the groups are neither read into results (whatever they hold)
  *    nor written; counts past m_capacity are cut off.  A group without rows has
  *    dB_g = 0 (TKG_GRAD_F32_ADD: unchanged).  groups == 1 is the plain product.
@@ -409,7 +411,8 @@ typedef enum {
                                   512 (dual accumulate: two N=256 MMAs share each A tile);
                                   0: automatic.  Also of tkg_linear_ce_grad's products and
                                   tkg_gemm_grouped_dev_bf16_wgrad (set before asking for a
-                                  workspace's size) */
+                                  workspace's size), but for FP32 weight gradients that
+                                  may sum more than 2048 rows (always 256) */
   TKG_OPT_TAIL_SPLIT = 11,    /* plain GEMMs on the persistent kernel: 0 splits the last partial
                                   wave of tiles into half-width tiles when those still fit one
                                   wave; 1 never; 2 splits every tile (a test of the half tiles) */
