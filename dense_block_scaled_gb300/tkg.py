@@ -147,11 +147,12 @@ def _ptr(t):
     return t.data_ptr()
 
 
-def _stream(stream):
+def _stream(stream, dev=None):
+    """The handle of `stream`, or of the current stream (of GPU `dev`, where the caller knows the current one)."""
     if stream is None:
         import torch
         # the current stream's handle without a Stream object (2.7 us less per call)
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device() if dev is None else dev)
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -337,11 +338,23 @@ def _wrong(name, t, dtype, shape, pitched):
 
 
 def _refuse(wanted):
-    """Raises ValueError for the first of (name, tensor, dtype, shape, rows may be pitched) that does not hold."""
+    """Raises ValueError for the first of (name, tensor, dtype, shape, rows may be pitched) that does not hold, or that
+    is not on the current GPU: an address of the host's, or of another GPU, would reach the kernel as one of this."""
     for w in wanted:
         msg = _wrong(*w)
         if msg:
             raise ValueError(msg)
+    _off_gpu([(w[0], w[1]) for w in wanted])
+
+
+def _off_gpu(named):
+    for name, t in named:
+        if t.get_device() < 0:
+            raise ValueError(f"{name}: a tensor on the GPU is wanted, got one on {t.device}")
+    import torch
+    for name, t in named:
+        if t.get_device() != torch.cuda.current_device():
+            raise ValueError(f"{name}: on {t.device}, but the current GPU is cuda:{torch.cuda.current_device()}")
 
 
 _kept = threading.local()    # per thread: {device: workspace} for the default stream
@@ -356,6 +369,10 @@ def _workspace(workspace, nbytes, like, stream, handle):
     each call takes its own; on another stream than the current one it is tied to the work queued there."""
     import torch
     if workspace is not None:
+        if workspace.get_device() != like.get_device():
+            _off_gpu([("workspace", workspace)])
+        if not workspace.is_contiguous():
+            raise ValueError("workspace: a contiguous tensor is wanted")
         return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace
     small = stream is None and nbytes <= _KEEP_BYTES and handle == 0
     if small:
@@ -390,15 +407,16 @@ def linear_ce_loss(X, W, labels, loss, lse, alpha: float = 1.0, workspace=None, 
 
     X (tokens x hidden bf16), W (vocab x hidden bf16), rows may be pitched; labels int64, outside [0, vocab): ignored."""
     import torch
-    (tokens, hidden), vocab, row = X.shape, W.shape[0], labels.shape
-    if not (X.dtype is W.dtype is torch.bfloat16 and labels.dtype is torch.int64
+    (tokens, hidden), vocab, row, dev = X.shape, W.shape[0], labels.shape, X.get_device()
+    if not (-1 < dev == torch.cuda.current_device() == W.get_device() == labels.get_device() == loss.get_device()
+            == lse.get_device() and X.dtype is W.dtype is torch.bfloat16 and labels.dtype is torch.int64
             and loss.dtype is lse.dtype is torch.float32 and W.shape[1] == hidden and row == loss.shape == lse.shape
             and row == (tokens,) and X.is_contiguous() and W.is_contiguous() and labels.is_contiguous()
             and loss.is_contiguous() and lse.is_contiguous()):
         _refuse((("X", X, torch.bfloat16, (tokens, hidden), True), ("W", W, torch.bfloat16, (vocab, hidden), True),
                  ("labels", labels, torch.int64, (tokens,), False), ("loss", loss, torch.float32, (tokens,), False),
                  ("lse", lse, torch.float32, (tokens,), False)))
-    lib, handle = load(), _stream(stream)
+    lib, handle = load(), _stream(stream, dev)
     at, nbytes, _keep = _workspace(workspace, linear_ce_loss_workspace_bytes(tokens, vocab), X, stream, handle)
     _check(lib.tkg_linear_ce_loss(tokens, vocab, hidden, X.data_ptr(), _pitch(X, hidden), W.data_ptr(),
                                   _pitch(W, hidden), labels.data_ptr(), alpha, loss.data_ptr(), lse.data_ptr(), at,
@@ -423,14 +441,16 @@ def linear_ce_grad(X, W, labels, lse, dloss, dX, dW, alpha: float = 1.0, accumul
     """Gradient of sum(dloss * loss): dX (tokens x hidden bf16) and dW (vocab x hidden, bf16 or float32); either may
     be None.  accumulate: add to the float32 dW.  piece: vocabulary entries worked on at a time (0: chosen)."""
     import torch
-    (tokens, hidden), vocab, row = X.shape, W.shape[0], labels.shape
+    (tokens, hidden), vocab, row, dev = X.shape, W.shape[0], labels.shape, X.get_device()
     gtype = GRAD_BF16 if dW is None else _grad_type(dW, "dW", accumulate)
-    if not (X.dtype is W.dtype is torch.bfloat16 and labels.dtype is torch.int64
+    if not (-1 < dev == torch.cuda.current_device() == W.get_device() == labels.get_device() == lse.get_device()
+            == dloss.get_device() and X.dtype is W.dtype is torch.bfloat16 and labels.dtype is torch.int64
             and lse.dtype is dloss.dtype is torch.float32 and W.shape[1] == hidden and row == lse.shape == dloss.shape
             and row == (tokens,) and X.is_contiguous() and W.is_contiguous() and labels.is_contiguous()
             and lse.is_contiguous() and dloss.is_contiguous()
-            and (dX is None or (dX.dtype is torch.bfloat16 and dX.shape == X.shape and dX.is_contiguous()))
-            and (dW is None or (dW.shape == W.shape and dW.is_contiguous()))):
+            and (dX is None or (dX.dtype is torch.bfloat16 and dX.shape == X.shape and dX.is_contiguous()
+                                and dX.get_device() == dev))
+            and (dW is None or (dW.shape == W.shape and dW.is_contiguous() and dW.get_device() == dev))):
         wanted = [("X", X, torch.bfloat16, (tokens, hidden), True), ("W", W, torch.bfloat16, (vocab, hidden), True),
                   ("labels", labels, torch.int64, (tokens,), False), ("lse", lse, torch.float32, (tokens,), False),
                   ("dloss", dloss, torch.float32, (tokens,), False)]
@@ -439,7 +459,7 @@ def linear_ce_grad(X, W, labels, lse, dloss, dX, dW, alpha: float = 1.0, accumul
         if dW is not None:
             wanted.append(("dW", dW, dW.dtype, (vocab, hidden), True))
         _refuse(wanted)
-    lib, handle = load(), _stream(stream)
+    lib, handle = load(), _stream(stream, dev)
     at, nbytes, _keep = _workspace(workspace, lib.tkg_linear_ce_grad_workspace_bytes(tokens, vocab, hidden, piece), X,
                                    stream, handle)
     _check(lib.tkg_linear_ce_grad(tokens, vocab, hidden, X.data_ptr(), _pitch(X, hidden), W.data_ptr(),
@@ -452,14 +472,15 @@ def linear_ce_grad(X, W, labels, lse, dloss, dX, dW, alpha: float = 1.0, accumul
 def gemm_grouped_dev_bf16_dgrad(sizes_dev, dD, B, dA, alpha: float = 1.0, stream=None) -> None:
     """Gradient of gemm_grouped_dev_bf16 to its rows: dA (capacity x k) = alpha * dD (capacity x n) @ B_g (n x k)."""
     import torch
-    groups, (cap, n), k = sizes_dev.shape[0], dD.shape, B.shape[-1]
-    if not (dD.dtype is B.dtype is dA.dtype is torch.bfloat16 and sizes_dev.dtype is torch.int32
+    groups, (cap, n), k, dev = sizes_dev.shape[0], dD.shape, B.shape[-1], dD.get_device()
+    if not (-1 < dev == torch.cuda.current_device() == sizes_dev.get_device() == B.get_device() == dA.get_device()
+            and dD.dtype is B.dtype is dA.dtype is torch.bfloat16 and sizes_dev.dtype is torch.int32
             and sizes_dev.dim() == 1 and B.shape == (groups, n, k) and dA.shape == (cap, k) and dD.is_contiguous()
             and B.is_contiguous() and dA.is_contiguous() and sizes_dev.is_contiguous()):
         _refuse((("sizes_dev", sizes_dev, torch.int32, (groups,), False), ("dD", dD, torch.bfloat16, (cap, n), False),
                  ("B", B, torch.bfloat16, (groups, n, k), False), ("dA", dA, torch.bfloat16, (cap, k), False)))
     _check(load().tkg_gemm_grouped_dev_bf16_dgrad(groups, sizes_dev.data_ptr(), cap, n, k, dD.data_ptr(),
-                                                  B.data_ptr(), dA.data_ptr(), alpha, _stream(stream)),
+                                                  B.data_ptr(), dA.data_ptr(), alpha, _stream(stream, dev)),
            "tkg_gemm_grouped_dev_bf16_dgrad")
 
 
@@ -467,15 +488,16 @@ def gemm_grouped_dev_bf16_wgrad(sizes_dev, dD, A, dB, alpha: float = 1.0, accumu
     """Gradient of gemm_grouped_dev_bf16 to the experts: dB_g (n x k, bf16 or float32) = alpha * dD_g^T @ A_g.
     accumulate: add to the float32 dB."""
     import torch
-    groups, (cap, n), k = sizes_dev.shape[0], dD.shape, A.shape[-1]
+    groups, (cap, n), k, dev = sizes_dev.shape[0], dD.shape, A.shape[-1], dD.get_device()
     gtype = _grad_type(dB, "dB", accumulate)
-    if not (dD.dtype is A.dtype is torch.bfloat16 and sizes_dev.dtype is torch.int32 and sizes_dev.dim() == 1
+    if not (-1 < dev == torch.cuda.current_device() == sizes_dev.get_device() == A.get_device() == dB.get_device()
+            and dD.dtype is A.dtype is torch.bfloat16 and sizes_dev.dtype is torch.int32 and sizes_dev.dim() == 1
             and A.shape == (cap, k) and dB.shape == (groups, n, k) and dD.is_contiguous() and A.is_contiguous()
             and dB.is_contiguous() and sizes_dev.is_contiguous()):
         _refuse((("sizes_dev", sizes_dev, torch.int32, (groups,), False), ("dD", dD, torch.bfloat16, (cap, n), False),
                  ("A", A, torch.bfloat16, (cap, k), False), ("dB", dB, dB.dtype, (groups, n, k), False)))
     _check(load().tkg_gemm_grouped_dev_bf16_wgrad(groups, sizes_dev.data_ptr(), cap, n, k, dD.data_ptr(),
-                                                  A.data_ptr(), dB.data_ptr(), gtype, alpha, _stream(stream)),
+                                                  A.data_ptr(), dB.data_ptr(), gtype, alpha, _stream(stream, dev)),
            "tkg_gemm_grouped_dev_bf16_wgrad")
 
 
