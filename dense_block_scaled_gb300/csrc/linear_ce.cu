@@ -122,7 +122,8 @@ __global__ void __launch_bounds__(256)
 // Parts are [hidden][token] (pitch a multiple of 64); dX is [token][hidden].  A
 // block adds the parts of 64 tokens x 16 hidden, in order and eight parts' loads in
 // flight together, turns them in shared memory and multiplies by the tokens' weights.
-// With SPLIT = 2 (few blocks) each half of its threads adds half of the parts.
+// With SPLIT = 2 (few blocks) each half of its threads adds half of the parts.  Rows past
+// the 65535 blocks of the grid's second dimension are in its third.
 template <int SPLIT>
 __global__ void __launch_bounds__(256 * SPLIT)
     ce_dx_kernel(int tokens, int vocab, int hidden, int parts, const float* __restrict__ part, size_t pitch,
@@ -131,7 +132,7 @@ __global__ void __launch_bounds__(256 * SPLIT)
   __shared__ float s_t[SPLIT][16][65];
   ptx::pdl_launch_dependents();
   ptx::pdl_wait();
-  const int t0 = blockIdx.x * 64, h0 = blockIdx.y * 16, tid = threadIdx.x;
+  const int t0 = blockIdx.x * 64, h0 = (blockIdx.z * gridDim.y + blockIdx.y) * 16, tid = threadIdx.x;
   const int tq = (tid & 15) * 4, hr = (tid >> 4) & 15, half = tid >> 8;   // four tokens of one row
   const int share = SPLIT == 2 ? (parts + 1) / 2 : parts, first = half * share, end = min(parts, first + share);
   const float* src = part + size_t(h0 + hr) * pitch + t0 + tq;
@@ -434,8 +435,9 @@ tkg_status tkg_linear_ce_grad(int tokens, int vocab, int hidden, const void* X, 
   if (!dX) return TKG_OK;
   // Half of the parts per thread where there are few blocks: 40 tokens x 21648 x 1024 (64 blocks) 43.0 us in place of
   // 46.1, 200 x 5000 x 768 (192) 27.4 of 28.8, but 128 x 32768 x 2048 (256) 95.0 of 92.3 (from a graph)
-  const dim3 grid(unsigned(ceil_div(tokens, 64)), unsigned(ceil_div(hidden, 16)));
-  const bool few = (long long)grid.x * grid.y <= 3 * kPairs;
+  const int across = ceil_div(tokens, 64), down = ceil_div(hidden, 16), deep = ceil_div(down, 65535);
+  const bool few = (long long)across * down <= 3 * kPairs;
+  const dim3 grid(unsigned(across), unsigned(ceil_div(down, deep)), unsigned(deep));
   return launch_small(few ? ce_dx_kernel<2> : ce_dx_kernel<1>, grid, dim3(few ? 512 : 256), stream, 0u, tokens, vocab,
                       hidden, pl.parts, part, pl.tokens_up, labels, dloss, alpha, static_cast<uint16_t*>(dX),
                       size_t(lddx));

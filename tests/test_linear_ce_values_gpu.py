@@ -169,3 +169,15 @@ def test_gradient_of_tokens_the_model_is_sure_of(tokens, vocab, hidden, alpha):
     # a token that is not sure has a g of its own in its label's row only
     assert (dX[sure].to(F64).abs() <= boundX[sure]).all()
     assert (dW[h.y[sure]].to(F64).abs() <= boundW[h.y[sure]]).all()
+
+
+def test_a_very_wide_head():
+    # more rows of dX's parts than one grid dimension past the first has blocks
+    tokens, vocab, hidden = 3, 9, 16 * 65536 + 8
+    h = Head(tokens, vocab, hidden, ignored=0.0, seed=25)
+    z, _, lse, loss, _ = h.forward()
+    got, got_lse = run_loss(h)
+    tol = product_error(h) + 2.0 ** -18 + 2.0 ** -23 * lse.abs()
+    assert ((got_lse.to(F64) - lse).abs() <= tol).all() and ((got.to(F64) - loss).abs() <= 2 * tol).all()
+    dX, eX, (gX, gW) = *(h.gradient()[i] for i in (0, 2)), run_grad(h, lse.float())
+    assert ((gX.to(F64) - dX).abs() <= eX).all()
