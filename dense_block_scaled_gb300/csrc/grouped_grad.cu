@@ -7,7 +7,7 @@ namespace {
 
 tkg_status check_groups(int groups, const int* sizes, int capacity, int n, int k) {
   if (groups < 1 || !sizes || capacity < 0 || n < 0 || k < 0) return TKG_ERR_INVALID_ARG;
-  if (groups > kMaxGroups) return TKG_ERR_UNSUPPORTED;
+  if (groups > kMaxGroups || capacity > kMaxSize || n > kMaxSize || k > kMaxSize) return TKG_ERR_UNSUPPORTED;
   if (!aligned_to(sizes, 4) || n % 8 != 0 || k % 8 != 0) return TKG_ERR_ALIGNMENT;
   return TKG_OK;
 }

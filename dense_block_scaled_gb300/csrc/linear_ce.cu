@@ -252,6 +252,7 @@ tkg_status check_head(int tokens, int vocab, int hidden, const void* X, int ldx,
   *empty = false;
   if (tokens < 0 || vocab < 0 || hidden < 0) return TKG_ERR_INVALID_ARG;
   if (vocab == 0 || hidden == 0) return TKG_ERR_UNSUPPORTED;   // a softmax over nothing; an empty product
+  if (tokens > kMaxSize || vocab > kMaxSize || hidden > kMaxSize) return TKG_ERR_UNSUPPORTED;
   if (hidden % 8 != 0) return TKG_ERR_ALIGNMENT;
   if (tokens == 0) {
     *empty = true;
@@ -271,7 +272,7 @@ using namespace tkg;
 extern "C" {
 
 size_t tkg_linear_ce_loss_workspace_bytes(int tokens, int vocab) {
-  if (tokens < 0 || vocab < 0) return 0;
+  if (tokens < 0 || vocab < 0 || tokens > kMaxSize || vocab > kMaxSize) return 0;
   return loss_part_bytes(tokens, vocab) + size_t(tokens) * 4;
 }
 
@@ -306,6 +307,7 @@ tkg_status tkg_linear_ce_loss(int tokens, int vocab, int hidden, const void* X, 
 size_t tkg_linear_ce_grad_workspace_bytes(int tokens, int vocab, int hidden, int piece) {
   if (tokens < 0 || vocab < 0 || hidden < 0 || piece < 0) return 0;
   if (tokens == 0 || vocab == 0 || hidden == 0) return 0;
+  if (tokens > kMaxSize || vocab > kMaxSize || hidden > kMaxSize) return 0;
   return grad_plan(tokens, vocab, hidden, piece).bytes;
 }
 

@@ -13,6 +13,10 @@ tkg_status encode_3d_swizzled(CUtensorMap* map, CUtensorMapDataType dtype, const
 
 inline bool aligned_to(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
+// Largest size of the training-side operators: indexes run past a size by less than 2^16 where tiles and grids are
+// rounded up, and are 32 bits.
+constexpr int kMaxSize = 0x7fff0000;
+
 // k rows of an MN-major box: 64, or all there are rounded up to the MMA's 16 (rows past the end arrive as
 // zeros; a box that runs mostly past the end slows the load stream)
 inline uint32_t mn_box_rows(int k) { return k >= 64 ? 64u : uint32_t((k + 15) / 16 * 16); }

@@ -330,6 +330,8 @@ def gemm_list(fmt: str, descs, stream=None) -> None:
 def _wrong(name, t, dtype, shape, pitched):
     if t.dtype != dtype or tuple(t.shape) != tuple(shape):
         return f"{name}: {dtype} of shape {tuple(shape)} is wanted, got {t.dtype} {tuple(t.shape)}"
+    if max(shape) >> 31 or (len(shape) == 2 and shape[0] > 1 and t.stride(0) >> 31):
+        return f"{name}: sizes and row pitches below 2^31 are wanted, got {tuple(shape)} in strides {t.stride()}"
     if pitched and len(shape) == 2 and (shape[1] <= 1 or t.stride(1) == 1):
         return None
     if not t.is_contiguous():
@@ -409,7 +411,8 @@ def linear_ce_loss(X, W, labels, loss, lse, alpha: float = 1.0, workspace=None, 
     import torch
     (tokens, hidden), vocab, row, dev = X.shape, W.shape[0], labels.shape, X.get_device()
     if not (-1 < dev == torch.cuda.current_device() == W.get_device() == labels.get_device() == loss.get_device()
-            == lse.get_device() and X.dtype is W.dtype is torch.bfloat16 and labels.dtype is torch.int64
+            == lse.get_device() and not (tokens | vocab | hidden) >> 31
+            and X.dtype is W.dtype is torch.bfloat16 and labels.dtype is torch.int64
             and loss.dtype is lse.dtype is torch.float32 and W.shape[1] == hidden and row == loss.shape == lse.shape
             and row == (tokens,) and X.is_contiguous() and W.is_contiguous() and labels.is_contiguous()
             and loss.is_contiguous() and lse.is_contiguous()):
@@ -444,7 +447,8 @@ def linear_ce_grad(X, W, labels, lse, dloss, dX, dW, alpha: float = 1.0, accumul
     (tokens, hidden), vocab, row, dev = X.shape, W.shape[0], labels.shape, X.get_device()
     gtype = GRAD_BF16 if dW is None else _grad_type(dW, "dW", accumulate)
     if not (-1 < dev == torch.cuda.current_device() == W.get_device() == labels.get_device() == lse.get_device()
-            == dloss.get_device() and X.dtype is W.dtype is torch.bfloat16 and labels.dtype is torch.int64
+            == dloss.get_device() and not (tokens | vocab | hidden) >> 31
+            and X.dtype is W.dtype is torch.bfloat16 and labels.dtype is torch.int64
             and lse.dtype is dloss.dtype is torch.float32 and W.shape[1] == hidden and row == lse.shape == dloss.shape
             and row == (tokens,) and X.is_contiguous() and W.is_contiguous() and labels.is_contiguous()
             and lse.is_contiguous() and dloss.is_contiguous()
@@ -474,6 +478,7 @@ def gemm_grouped_dev_bf16_dgrad(sizes_dev, dD, B, dA, alpha: float = 1.0, stream
     import torch
     groups, (cap, n), k, dev = sizes_dev.shape[0], dD.shape, B.shape[-1], dD.get_device()
     if not (-1 < dev == torch.cuda.current_device() == sizes_dev.get_device() == B.get_device() == dA.get_device()
+            and not (cap | n | k) >> 31
             and dD.dtype is B.dtype is dA.dtype is torch.bfloat16 and sizes_dev.dtype is torch.int32
             and sizes_dev.dim() == 1 and B.shape == (groups, n, k) and dA.shape == (cap, k) and dD.is_contiguous()
             and B.is_contiguous() and dA.is_contiguous() and sizes_dev.is_contiguous()):
@@ -491,6 +496,7 @@ def gemm_grouped_dev_bf16_wgrad(sizes_dev, dD, A, dB, alpha: float = 1.0, accumu
     groups, (cap, n), k, dev = sizes_dev.shape[0], dD.shape, A.shape[-1], dD.get_device()
     gtype = _grad_type(dB, "dB", accumulate)
     if not (-1 < dev == torch.cuda.current_device() == sizes_dev.get_device() == A.get_device() == dB.get_device()
+            and not (cap | n | k) >> 31
             and dD.dtype is A.dtype is torch.bfloat16 and sizes_dev.dtype is torch.int32 and sizes_dev.dim() == 1
             and A.shape == (cap, k) and dB.shape == (groups, n, k) and dD.is_contiguous() and A.is_contiguous()
             and dB.is_contiguous() and sizes_dev.is_contiguous()):

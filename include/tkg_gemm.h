@@ -268,6 +268,8 @@ tkg_status tkg_gemm_bf16_noalloc(int m, int n, int k, const void *A, const void 
  * -100) ignores its row: loss 0 (lse is still that row's).  loss, lse: FP32.
  *  - Requires hidden % 8 == 0, pitches >= hidden and multiples of 8 elements
  *    (16 bytes), 16-byte aligned X, W and workspace.  vocab and tokens are free.
+ *    Sizes past 2^31 - 2^16: TKG_ERR_UNSUPPORTED (and workspace size 0), here and
+ *    in the gradients below.
  *  - workspace: device memory, at least tkg_linear_ce_loss_workspace_bytes(),
  *    contents undefined before and after; calls that may overlap on the GPU
  *    need one each.
