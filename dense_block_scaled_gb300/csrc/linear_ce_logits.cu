@@ -20,7 +20,8 @@ static tkg_status launch_logits(const void* X, size_t x_bytes, const void* W, si
   const int sums = ceil_div(p.split_stages, kSumStages);
   p.sum_stages = ceil_div(p.split_stages, sums);
   // the narrow form has no registers for more sums than its two accumulators
-  if (train_narrow(p.n, ceil_div(p.m, 256)) && sums <= 2)
+  const int tiles = ceil_div(p.m, 256);
+  if ((EPI == EPI_LOSS ? train_narrow(p.n, tiles) : train_narrow_gradient(p.n, p.k, tiles)) && sums <= 2)
     return launch_train<false, false, EPI, GRP_NONE, SHAPE_NARROW>(tmA, tmB, tmD, p, stream);
   if (sums > 1) return launch_train<false, false, EPI, GRP_NONE, SHAPE_SUMS>(tmA, tmB, tmD, p, stream);
   return launch_train<false, false, EPI, GRP_NONE>(tmA, tmB, tmD, p, stream);

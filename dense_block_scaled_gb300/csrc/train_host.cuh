@@ -150,16 +150,24 @@ inline bool train_dual(int m, int n, long long count, int stages) {
          train_rounds(rows * ceil_div(n, 256)) * train_tile_time(stages, false);
 }
 
-// Whether the logits of n tokens run in the kernel's narrow form, given their tiles.  It needs more
-// of them than there are pairs of SMs: the loss of 16 tokens takes 32.5 us narrow and 46.9 wide at 20000 x 4096, 162.8 and
+// Whether the loss's logits of n tokens run in the kernel's narrow form, given their tiles.  It needs more
+// of them than there are pairs of SMs: 16 tokens take 32.5 us narrow and 46.9 wide at 20000 x 4096, 162.8 and
 // 175.2 at 131072 x 4096, 8.7 and 10.7 at 50000 x 256, but 13.1 and 12.7 at 8000 x 2048.  Past 64 tokens its four
 // epilogue warps tell (a block has a quarter of the wide form's), and it pays while it spares a thin second round:
 // 128 tokens 13.4 and 15.4 us at 23000 x 1024, 44.4 and 49.2 at 27000 x 4096, but 30.5 and 29.1 at 32768 x 2048
-// and 76.0 and 72.2 at 40000 x 4096.  The gradient's logits go the same way (dX and dW of 40 tokens x 21648 x 1024
-// 41.8 and 44.4 us, of 128 x 20000 x 4096 108.6 and 116.2, of 128 x 27000 x 1024 50.1 and 48.6).
+// and 76.0 and 72.2 at 40000 x 4096.
 constexpr int kNarrowTokens = 128;
 inline bool train_narrow(int n, int tiles) {
   return n <= kNarrowTokens && tiles > kPairs && (n <= kNarrowTokens / 2 || 2 * tiles <= 3 * kPairs);
+}
+// The same of the gradient's logits, whose epilogue does more per logit and writes them: the narrow form pays only where it
+// spares a thin second round, and where the sums are long for the tokens.  dX and dW, narrow and wide: 40 tokens x
+// 21648 x 1024 43.4 and 44.8 us, 64 x 25000 x 2048 69.7 and 70.7, 128 x 20000 x 4096 110.0 and 115.8, 1 x 19713 x 768
+// 37.0 and 37.9; but (more tiles) 128 x 29000 x 4096 154.3 and 147.0, 40 x 32768 x 2048 95.0 and 93.6, (shorter sums)
+// 128 x 20000 x 2048 69.1 and 67.8, 128 x 27000 x 1024 53.4 and 48.3, 16 x 21648 x 512 31.1 and 30.6, 1 x 20000 x 256
+// 25.7 and 24.9.
+inline bool train_narrow_gradient(int n, int hidden, int tiles) {
+  return n <= kNarrowTokens && tiles > kPairs && 3 * tiles <= 4 * kPairs && hidden >= 768 && hidden >= 24 * n;
 }
 // Stages (64 k each) that one accumulator sums where the result is FP32 (logits, FP32 weight gradients).  Tensor memory
 // adds towards zero, so a sum's error grows with its length: terms of one sign lose 3e-6 of it over 2048 terms,

@@ -4,7 +4,7 @@ import pytest
 import torch
 
 from dense_block_scaled_gb300 import tkg
-from test_linear_ce_gpu import BF16, F32, F64, Head, run_grad, run_loss
+from test_linear_ce_gpu import BF16, F32, F64, Head, check_grad, run_grad, run_loss
 
 pytestmark = pytest.mark.gpu
 
@@ -143,7 +143,15 @@ def test_infinities_in_rows_that_count(tokens, vocab, hidden, cta_group):
 
 
 # forms of the gradient's logits: wide, narrow, and both with sums in parts
-GRAD_FORMS = [(40, 700, 264), (300, 1500, 64), (20, 20003, 256), (40, 20000, 4104), (300, 700, 4104), (130, 900, 8200)]
+GRAD_FORMS = [(40, 700, 264), (300, 1500, 64), (20, 20003, 256), (20, 20003, 1024), (40, 20000, 4096), (40, 20000, 4104),
+              (300, 700, 4104), (130, 900, 8200)]
+
+
+@pytest.mark.parametrize("tokens,vocab,hidden", [(1, 19713, 768), (32, 20003, 768), (40, 21648, 1032), (70, 19800, 2056),
+                                                 (128, 24000, 4096)])
+def test_gradient_in_the_narrow_form(tokens, vocab, hidden):
+    check_grad(Head(tokens, vocab, hidden, seed=26))
+    check_grad(Head(tokens, vocab, hidden, seed=27, alpha=-0.5, ignored=0.9), dtype=F32)
 
 
 @pytest.mark.parametrize("alpha", [1.0, -0.5, 0.37])
