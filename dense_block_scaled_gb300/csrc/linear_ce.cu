@@ -198,7 +198,10 @@ int default_piece(int tokens, int vocab) {
 }
 
 // Parts of dX's long axis and its tiles' shape: what takes least time, a part at
-// least 8 stages (512 vocabulary entries) long.
+// least 8 stages (512 vocabulary entries) long, and 32 at most.  dX with at least 4, 8 and 16 stages: 1 token x 1500 x
+// 256 10.5, 11.0 and 14.3 us, 1 x 6000 x 1024 18.2, 16.4 and 17.2; with at most 32 and 64 parts: 1 x 32768 x 256 18.5
+// and 20.9, 64 x 131072 x 256 42.5 and 38.5.  More parts, or the wide tiles, have to gain 3%, as the time leaves out
+// adding the parts: without that 64 x 131072 x 2048 takes 195 us in place of 169, 777 x 131072 x 1024 340 of 295.
 void plan_dx(int tokens, int hidden, int k, int* parts, bool* dual) {
   const int stages = ceil_div(k, 64);
   const int forced = option(TKG_OPT_BF16_TILE_N);
@@ -232,12 +235,14 @@ GradPlan grad_plan(int tokens, int vocab, int hidden, int piece) {
   return pl;
 }
 
-// Whether a spare warp of the logits' blocks writes the weighted rows of X: it takes about a microsecond per 2 KB
-// of row, and two of them (half of the tile's four) should stay behind a tile's time, a microsecond per 256 hidden or
-// more.  Every such warp first finds the largest of the T weights, 512 loads at 16384 tokens.
+// Whether a spare warp of the logits' blocks writes the weighted rows of X, and not a kernel before them.  Its rows and
+// the search for the largest of the T weights, which every such warp makes, have to stay behind the tiles' products:
+// dW of 128 tokens x 16384 x 1024 takes 22.6 us (26.9 with the kernel), 2048 x 32768 x 256 78.8 (80.9), 6000 x 32768 x
+// 2048 994 (1008); but with many rows to a tile 8192 x 8000 x 256 125.8 (103.5), and with many weights and short products
+// 4096 x 32768 x 256 152.7 (148.5), 16384 x 65536 x 256 1143 (1117).
 bool rows_on_the_side(int tokens, int piece, int hidden) {
   const double tiles = double(ceil_div(piece, 256)) * ceil_div(tokens, kTrainBN);
-  return tokens / tiles <= 4.0 && tokens <= 16384;
+  return tokens / tiles <= 4.0 && tokens <= (hidden >= 2048 ? 16384 : 2048);
 }
 
 // One (maximum, sum) per token and 128 vocabulary rows, or per block of the kernel for few tokens.
@@ -436,7 +441,8 @@ tkg_status tkg_linear_ce_grad(int tokens, int vocab, int hidden, const void* X, 
   }
   if (!dX) return TKG_OK;
   // Half of the parts per thread where there are few blocks: 40 tokens x 21648 x 1024 (64 blocks) 43.0 us in place of
-  // 46.1, 200 x 5000 x 768 (192) 27.4 of 28.8, but 128 x 32768 x 2048 (256) 95.0 of 92.3 (from a graph)
+  // 46.1, 200 x 5000 x 768 (192) 27.4 of 28.8, but 128 x 32768 x 2048 (256) 95.0 of 92.3 (from a graph); dX alone of 777
+  // x 32768 x 256 (208) 45.8 of 47.5, of 16 x 32768 x 4096 (256) 104 of 96
   const int across = ceil_div(tokens, 64), down = ceil_div(hidden, 16), deep = ceil_div(down, 65535);
   const bool few = (long long)across * down <= 3 * kPairs;
   const dim3 grid(unsigned(across), unsigned(ceil_div(down, deep)), unsigned(deep));
