@@ -1024,401 +1024,407 @@ __global__ void __launch_bounds__(TrainConfig<A_MN, B_MN, EPI, GRP, SHAPE>::kThr
       if (t_next >= 0) read_columns(t_next, label_next, lse_next);
 #pragma unroll 1
       for (int sub = 0; sub < (C::kDual ? tile.subs : 1); ++sub) {
-      TrainTile tc = tile;               // the columns of one accumulator
-      if constexpr (C::kDual) {
-        acc = uint32_t(sub);
-        tc.nt = width(tile, sub);
-        tc.n0 += sub * kTrainBN;
-        tc.n_end = min(tile.n_end, tc.n0 + kTrainBN);
-      }
-      const int nch = min(max(((tc.nt + 31) >> 5) - C::kChunks * h, 0), C::kChunks);   // this warp's chunks
-      const int row0 = tc.a0 + q * 32;                                     // its rows of D
-      const int col0 = tc.n0 + h * C::kChunks * 32;                        // and its first column
-      // (selects: an array indexed at run time would live in local memory)
-      [[maybe_unused]] auto pick = [](const int (&x)[C::kChunks], int c) {
-        int r = x[0];
-#pragma unroll
-        for (int i = 1; i < C::kChunks; ++i) r = c == i ? x[i] : r;
-        return r;
-      };
-      // columns whose label is among this warp's rows (uniform), and each lane's label as such a row
-      [[maybe_unused]] auto among_rows = [&](int lab, int& off) {
-        off = lab - p.vocab0 - row0;
-        return __ballot_sync(0xffffffffu, lab >= 0 && off >= 0 && off < 32 && row0 + off < p.m);
-      };
-      auto acc_ready = [&]() {
-        if (!wait_bar_warp<false>(accf_bar(acc), (accbits >> acc) & 1u, ctl)) return false;
-        ptx::tc_fence_after();
-        return true;
-      };
-      if (!acc_ready()) {
-        alive = false;
-        break;
-      }
-      const bool idle = !invariant(acc < uint32_t(ACC) && t < num_tiles && tc.nt <= C::kBN, p.status);
-      const uint32_t tq = tmem + (uint32_t(q * 32) << 16) + uint32_t(h * C::kChunks * 32);
-      [[maybe_unused]] const uint32_t tbase = tq + acc * uint32_t(C::kBN);
-      auto hand_back = [&]() {   // every load of this tile has completed
-        ptx::tc_fence_before();
-        __syncwarp();
-        if (lane == 0) {
-          if (leader)
-            ptx::mbar_arrive(acce_bar(acc));
-          else
-            ptx::mbar_arrive_relaxed_cluster(acce_lead0 + 8u * acc);
+        TrainTile tc = tile;               // the columns of one accumulator
+        if constexpr (C::kDual) {
+          acc = uint32_t(sub);
+          tc.nt = width(tile, sub);
+          tc.n0 += sub * kTrainBN;
+          tc.n_end = min(tile.n_end, tc.n0 + kTrainBN);
         }
-        accbits ^= 1u << acc;
-        if (!C::kDual) acc ^= 1u;
-      };
-      // SUMS: this warp's sums gather in registers, and each accumulator goes back as soon as it is read.  (From 0:
-      // taking the first as it is selects for every register, and spilled.)
-      [[maybe_unused]] auto gather = [&](int n, auto&& read, float (&x)[C::kChunks][32]) {
+        const int nch = min(max(((tc.nt + 31) >> 5) - C::kChunks * h, 0), C::kChunks);   // this warp's chunks
+        const int row0 = tc.a0 + q * 32;                                     // its rows of D
+        const int col0 = tc.n0 + h * C::kChunks * 32;                        // and its first column
+        // (selects: an array indexed at run time would live in local memory)
+        [[maybe_unused]] auto pick = [](const int (&x)[C::kChunks], int c) {
+          int r = x[0];
 #pragma unroll
-        for (int c = 0; c < C::kChunks; ++c)
-#pragma unroll
-          for (int j = 0; j < 32; ++j) x[c][j] = 0.f;
-#pragma unroll 1
-        for (int done = 0;;) {
-#pragma unroll
-          for (int c = 0; c < C::kChunks; ++c)
-            if (c < n) read(c, acc, false, x[c]);
-          hand_back();
-          done += p.sum_stages;
-          if (done >= tc.nks) return true;
-          if (!acc_ready()) return false;
-        }
-      };
-      // 32 columns of this lane's row, alone or added to x: 8 at a time, as there are no registers for 32 more
-      [[maybe_unused]] auto read_row = [&](int c, uint32_t a, bool first, float (&x)[32]) {
-#pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          uint32_t v[8];
-          ptx::tmem_ld_32x32b_x8(tq + a * uint32_t(C::kBN) + uint32_t(c * 32 + u * 8), v);
-          ptx::tmem_ld_wait_for(v);
-#pragma unroll
-          for (int j = 0; j < 8; ++j)
-            x[8 * u + j] = first ? __uint_as_float(v[j]) : x[8 * u + j] + __uint_as_float(v[j]);
-        }
-      };
-      // NARROW: a tile's two sums lie in the two accumulators
-      [[maybe_unused]] const bool two = C::kNarrow && p.sum_stages < tc.nks;
-      if (two) {
-        acc ^= 1u;
+          for (int i = 1; i < C::kChunks; ++i) r = c == i ? x[i] : r;
+          return r;
+        };
+        // columns whose label is among this warp's rows (uniform), and each lane's label as such a row
+        [[maybe_unused]] auto among_rows = [&](int lab, int& off) {
+          off = lab - p.vocab0 - row0;
+          return __ballot_sync(0xffffffffu, lab >= 0 && off >= 0 && off < 32 && row0 + off < p.m);
+        };
+        auto acc_ready = [&]() {
+          if (!wait_bar_warp<false>(accf_bar(acc), (accbits >> acc) & 1u, ctl)) return false;
+          ptx::tc_fence_after();
+          return true;
+        };
         if (!acc_ready()) {
           alive = false;
           break;
         }
-        acc ^= 1u;
-      }
-      if constexpr (EPI == EPI_LOSS) {
-        float2* stat = s_stat + (turn & 1u) * uint32_t(4 * C::kBN) + h * C::kChunks * 32;
-        const uint32_t stat_phase = (turn & 1u);
-        ++turn;
-        const float c2 = fabsf(p.c2);
-        const int rows_there = p.m - row0 - (lane >> 2);   // of rows 0, 8, 16, 24 past this lane's first
-        const bool edge = row0 + 32 > p.m;
-        const int n = idle ? 0 : nch;
-        // x[4 i + 2 k + e]: column 8 i + 2 (t % 4) + e, row t / 4 + 8 k (k = 0, 1), and, from x[16] on, 16 rows on
-        auto read = [&](int c, uint32_t a, bool first, float (&x)[32]) {
-          const uint32_t from = tq + a * uint32_t(C::kBN) + uint32_t(c * 32);
-          uint32_t v[2][16];
-          ptx::tmem_ld_16x256b_x4(from, v[0]);
-          if (SHAPE != SHAPE_SUMS) ptx::tmem_ld_16x256b_x4(from + (16u << 16), v[1]);
-#pragma unroll
-          for (int u = 0; u < 2; ++u) {
-            // (SUMS has no registers for both halves beside the sums)
-            if (SHAPE == SHAPE_SUMS && u == 1) ptx::tmem_ld_16x256b_x4(from + (16u << 16), v[1]);
-            ptx::tmem_ld_wait_for(v[u]);
-#pragma unroll
-            for (int j = 0; j < 16; ++j)
-              x[16 * u + j] = first ? __uint_as_float(v[u][j]) : x[16 * u + j] + __uint_as_float(v[u][j]);
+        const bool idle = !invariant(acc < uint32_t(ACC) && t < num_tiles && tc.nt <= C::kBN, p.status);
+        const uint32_t tq = tmem + (uint32_t(q * 32) << 16) + uint32_t(h * C::kChunks * 32);
+        [[maybe_unused]] const uint32_t tbase = tq + acc * uint32_t(C::kBN);
+        auto hand_back = [&]() {   // every load of this tile has completed
+          ptx::tc_fence_before();
+          __syncwarp();
+          if (lane == 0) {
+            if (leader)
+              ptx::mbar_arrive(acce_bar(acc));
+            else
+              ptx::mbar_arrive_relaxed_cluster(acce_lead0 + 8u * acc);
           }
+          accbits ^= 1u << acc;
+          if (!C::kDual) acc ^= 1u;
         };
-        auto reduce = [&](int c, float (&x)[32]) {
-          // labels among these 32 rows: about one column in vocab / 32
-          int off;
+        // SUMS: this warp's sums gather in registers, and each accumulator goes back as soon as it is read.  (From 0:
+        // taking the first as it is selects for every register, and spilled.)
+        [[maybe_unused]] auto gather = [&](int n, auto&& read, float (&x)[C::kChunks][32]) {
+#pragma unroll
+          for (int c = 0; c < C::kChunks; ++c)
+#pragma unroll
+            for (int j = 0; j < 32; ++j) x[c][j] = 0.f;
 #pragma unroll 1
-          for (uint32_t left = among_rows(pick(label, c), off); left; left &= left - 1) {
-            const int j = __ffs(int(left)) - 1;
-            const int row = __shfl_sync(0xffffffffu, off, j);
-            const int at = 4 * (j >> 3) + 2 * ((row >> 3) & 1) + (j & 1) + 16 * (row >> 4);
-            float z = x[0];
+          for (int done = 0;;) {
 #pragma unroll
-            for (int i = 1; i < 32; ++i) z = at == i ? x[i] : z;
-            if (lane == 4 * (row & 7) + ((j >> 1) & 3)) p.zlabel[col0 + c * 32 + j] = z * alpha;
-          }
-          if (p.c2 < 0.f) {
-            asm volatile("");   // (a branch, not 32 selects)
-#pragma unroll
-            for (int j = 0; j < 32; ++j) x[j] = -x[j];
-          }
-          if (edge) {   // rows past the vocabulary's end
-            asm volatile("");
-#pragma unroll
-            for (int j = 0; j < 32; ++j)
-              if (((j >> 1) & 1) * 8 + (j >> 4) * 16 >= rows_there) x[j] = -INFINITY;
-          }
-          float top[8], sum[8];
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const int j = 4 * (i >> 1) + (i & 1);
-            top[i] = fmaxf(fmaxf(x[j], x[j + 2]), fmaxf(x[j + 16], x[j + 18]));
-          }
-          const float own = fold_columns(top, lane, [](float a, float b) { return fmaxf(a, b); });
-          unfold_columns(own, lane, top);
-          // Differences first: the largest logit then counts as exactly 1, and a sum of at least 1 with that logit
-          // beside it gives an lse that is not below any logit
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const int j = 4 * (i >> 1) + (i & 1);
-            const float sub = fabsf(top[i]) == INFINITY ? 0.f : top[i];   // no inf - inf
-            sum[i] = (ptx::ex2((x[j] - sub) * c2) + ptx::ex2((x[j + 2] - sub) * c2)) +
-                     (ptx::ex2((x[j + 16] - sub) * c2) + ptx::ex2((x[j + 18] - sub) * c2));
-          }
-          if (c2 == 0.f && edge) {   // scale 0: 0 * -inf is not a number
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-              sum[i] = float(rows_there > 0) + float(rows_there > 8) + float(rows_there > 16) + float(rows_there > 24);
-          }
-          const float s = fold_columns(sum, lane, [](float a, float b) { return a + b; });
-          stat[q * C::kBN + c * 32 + column_of_lane(lane)] = make_float2(own == -INFINITY ? own : own * fabsf(alpha), s);
-        };
-        if constexpr (SHAPE != SHAPE_SUMS) {
-#pragma unroll 1
-          for (int c = 0; c < n; ++c) {
-            float x[32];
-            read(c, acc, true, x);
-            if (two) read(c, acc ^ 1u, false, x);
-            if (c + 1 == n) {
-              hand_back();
-              if (two) hand_back();
-            }
-            reduce(c, x);
-          }
-          if (n == 0) {
+            for (int c = 0; c < C::kChunks; ++c)
+              if (c < n) read(c, acc, false, x[c]);
             hand_back();
-            if (two) hand_back();
+            done += p.sum_stages;
+            if (done >= tc.nks) return true;
+            if (!acc_ready()) return false;
           }
-        } else {
-          float x[C::kChunks][32];
-          if (!gather(n, read, x)) {
+        };
+        // 32 columns of this lane's row, alone or added to x: 8 at a time, as there are no registers for 32 more
+        [[maybe_unused]] auto read_row = [&](int c, uint32_t a, bool first, float (&x)[32]) {
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            uint32_t v[8];
+            ptx::tmem_ld_32x32b_x8(tq + a * uint32_t(C::kBN) + uint32_t(c * 32 + u * 8), v);
+            ptx::tmem_ld_wait_for(v);
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+              x[8 * u + j] = first ? __uint_as_float(v[j]) : x[8 * u + j] + __uint_as_float(v[j]);
+          }
+        };
+        // NARROW: a tile's two sums lie in the two accumulators
+        [[maybe_unused]] const bool two = C::kNarrow && p.sum_stages < tc.nks;
+        if (two) {
+          acc ^= 1u;
+          if (!acc_ready()) {
             alive = false;
             break;
           }
-#pragma unroll
-          for (int c = 0; c < C::kChunks; ++c)
-            if (c < n) reduce(c, x[c]);
+          acc ^= 1u;
         }
-        __syncwarp();
-        if (lane == 0) ptx::mbar_arrive(stat_bar(h));
-        if (!wait_bar_warp<false>(stat_bar(h), stat_phase, ctl)) {
-          alive = false;
-          break;
-        }
-        // the four warps' 32 rows each: warp q joins chunk q
-        const int col = col0 + q * 32 + lane;
-        if (q < nch && !idle && col < tc.n_end && tc.a0 < p.m) {
-          float m = -INFINITY, s = 0.f;
-          float2 x[4];
+        if constexpr (EPI == EPI_LOSS) {
+          float2* stat = s_stat + (turn & 1u) * uint32_t(4 * C::kBN) + h * C::kChunks * 32;
+          const uint32_t stat_phase = (turn & 1u);
+          ++turn;
+          const float c2 = fabsf(p.c2);
+          const int rows_there = p.m - row0 - (lane >> 2);   // of rows 0, 8, 16, 24 past this lane's first
+          const bool edge = row0 + 32 > p.m;
+          const int n = idle ? 0 : nch;
+          // x[4 i + 2 k + e]: column 8 i + 2 (t % 4) + e, row t / 4 + 8 k (k = 0, 1), and, from x[16] on, 16 rows on
+          auto read = [&](int c, uint32_t a, bool first, float (&x)[32]) {
+            const uint32_t from = tq + a * uint32_t(C::kBN) + uint32_t(c * 32);
+            uint32_t v[2][16];
+            ptx::tmem_ld_16x256b_x4(from, v[0]);
+            if (SHAPE != SHAPE_SUMS) ptx::tmem_ld_16x256b_x4(from + (16u << 16), v[1]);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            x[i] = stat[i * C::kBN + q * 32 + lane];
-            m = fmaxf(m, x[i].x);
-          }
-          const float sub = fabsf(m) == INFINITY ? 0.f : m;
+            for (int u = 0; u < 2; ++u) {
+              // (SUMS has no registers for both halves beside the sums)
+              if (SHAPE == SHAPE_SUMS && u == 1) ptx::tmem_ld_16x256b_x4(from + (16u << 16), v[1]);
+              ptx::tmem_ld_wait_for(v[u]);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) s += x[i].y * ptx::ex2((x[i].x - sub) * kLog2e);
-          p.part[size_t(tc.a0 >> 7) * size_t(p.n) + col] = make_float2(m, s);
-        }
-      } else if constexpr (EPI == EPI_DLOGITS) {
-        const int n = idle ? 0 : nch;
-        auto read = [&](int c, uint32_t a, bool first, float (&x)[32]) {
-          if constexpr (SHAPE == SHAPE_WIDE) {
-            uint32_t v[32];
-            ptx::tmem_ld_32x32b_x32(tq + a * uint32_t(C::kBN) + uint32_t(c * 32), v);
-            ptx::tmem_ld_wait_for(v);
+              for (int j = 0; j < 16; ++j)
+                x[16 * u + j] = first ? __uint_as_float(v[u][j]) : x[16 * u + j] + __uint_as_float(v[u][j]);
+            }
+          };
+          auto reduce = [&](int c, float (&x)[32]) {
+            // labels among these 32 rows: about one column in vocab / 32
+            int off;
+#pragma unroll 1
+            for (uint32_t left = among_rows(pick(label, c), off); left; left &= left - 1) {
+              const int j = __ffs(int(left)) - 1;
+              const int row = __shfl_sync(0xffffffffu, off, j);
+              const int at = 4 * (j >> 3) + 2 * ((row >> 3) & 1) + (j & 1) + 16 * (row >> 4);
+              float z = x[0];
 #pragma unroll
-            for (int j = 0; j < 32; ++j) x[j] = __uint_as_float(v[j]);
+              for (int i = 1; i < 32; ++i) z = at == i ? x[i] : z;
+              if (lane == 4 * (row & 7) + ((j >> 1) & 3)) p.zlabel[col0 + c * 32 + j] = z * alpha;
+            }
+            if (p.c2 < 0.f) {
+              asm volatile("");   // (a branch, not 32 selects)
+#pragma unroll
+              for (int j = 0; j < 32; ++j) x[j] = -x[j];
+            }
+            if (edge) {   // rows past the vocabulary's end
+              asm volatile("");
+#pragma unroll
+              for (int j = 0; j < 32; ++j)
+                if (((j >> 1) & 1) * 8 + (j >> 4) * 16 >= rows_there) x[j] = -INFINITY;
+            }
+            float top[8], sum[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const int j = 4 * (i >> 1) + (i & 1);
+              top[i] = fmaxf(fmaxf(x[j], x[j + 2]), fmaxf(x[j + 16], x[j + 18]));
+            }
+            const float own = fold_columns(top, lane, [](float a, float b) { return fmaxf(a, b); });
+            unfold_columns(own, lane, top);
+            // Differences first: the largest logit then counts as exactly 1, and a sum of at least 1 with that logit
+            // beside it gives an lse that is not below any logit
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const int j = 4 * (i >> 1) + (i & 1);
+              const float sub = fabsf(top[i]) == INFINITY ? 0.f : top[i];   // no inf - inf
+              sum[i] = (ptx::ex2((x[j] - sub) * c2) + ptx::ex2((x[j + 2] - sub) * c2)) +
+                       (ptx::ex2((x[j + 16] - sub) * c2) + ptx::ex2((x[j + 18] - sub) * c2));
+            }
+            if (c2 == 0.f && edge) {   // scale 0: 0 * -inf is not a number
+#pragma unroll
+              for (int i = 0; i < 8; ++i)
+                sum[i] = float(rows_there > 0) + float(rows_there > 8) + float(rows_there > 16) +
+                         float(rows_there > 24);
+            }
+            const float s = fold_columns(sum, lane, [](float a, float b) { return a + b; });
+            stat[q * C::kBN + c * 32 + column_of_lane(lane)] =
+                make_float2(own == -INFINITY ? own : own * fabsf(alpha), s);
+          };
+          if constexpr (SHAPE != SHAPE_SUMS) {
+#pragma unroll 1
+            for (int c = 0; c < n; ++c) {
+              float x[32];
+              read(c, acc, true, x);
+              if (two) read(c, acc ^ 1u, false, x);
+              if (c + 1 == n) {
+                hand_back();
+                if (two) hand_back();
+              }
+              reduce(c, x);
+            }
+            if (n == 0) {
+              hand_back();
+              if (two) hand_back();
+            }
           } else {
-            read_row(c, a, first, x);
-          }
-        };
-        auto write = [&](int c, float (&g)[32]) {
-          // The logit rounded as the loss has it (__fmul_rn: not fused), and then its difference: the label's
-          // exp(z - lse) - 1 is 0 where lse is that logit, and the rounding of z log2(e) (2^-24 of the logit's
-          // size) stays out of every g
-#pragma unroll
-          for (int j = 0; j < 32; ++j)
-            g[j] = ptx::ex2((__fmul_rn(g[j], alpha) - __shfl_sync(0xffffffffu, lse[c], j)) * kLog2e);
-          int off;
-          const uint32_t hits = among_rows(label[c], off);
-          if (hits) {
-            asm volatile("");   // (a branch, not 32 selects)
-#pragma unroll
-            for (int j = 0; j < 32; ++j)
-              if (((hits >> j) & 1u) && lane == __shfl_sync(0xffffffffu, off, j)) g[j] -= 1.f;
-          }
-          const uint32_t gone = __ballot_sync(0xffffffffu, label[c] < 0);
-          if (gone) {   // ignored tokens, whatever their logits and lse are (and columns that are not there)
-            asm volatile("");
-#pragma unroll
-            for (int j = 0; j < 32; ++j)
-              if ((gone >> j) & 1u) g[j] = 0.f;
-          }
-          uint32_t w[16];
-#pragma unroll
-          for (int j = 0; j < 16; ++j) w[j] = ptx::pack_bf16x2(g[2 * j], g[2 * j + 1]);
-          const int at = h * C::kChunks * 32 + c * 32, col = tc.n0 + at;
-          if (col >= tc.n_end || row0 >= p.m) return;
-          if (at + 32 <= tc.nt) {
-            stage_box(
-                [&](uint32_t buf) {
-#pragma unroll
-                  for (int j = 0; j < 4; ++j)
-                    ptx::st_shared_v4(buf + uint32_t(lane * 64) + ((uint32_t(j) ^ ((uint32_t(lane) >> 1) & 3u)) << 4),
-                                      w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
-                },
-                [&](uint32_t buf) {
-                  ptx::tma_store_3d(&tmD, buf, col, row0, 0);
-                  if (row0 + 16 < p.m) ptx::tma_store_3d(&tmD, buf + 1024u, col, row0 + 16, 0);
-                });
-          } else if (row0 + lane < p.m) {   // the tile ends within the 32: its 16 columns (a 32-byte sector)
-            uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.d) + size_t(row0 + lane) * p.ldd + col);
-            dst[0] = make_uint4(w[0], w[1], w[2], w[3]);
-            dst[1] = make_uint4(w[4], w[5], w[6], w[7]);
-          }
-        };
-        if constexpr (SHAPE != SHAPE_SUMS) {
-#pragma unroll
-          for (int c = 0; c < C::kChunks; ++c) {
-            if (c >= n) break;
-            float x[32];
-            read(c, acc, true, x);
-            if (two) read(c, acc ^ 1u, false, x);
-            if (c + 1 == n) {
-              hand_back();
-              if (two) hand_back();
+            float x[C::kChunks][32];
+            if (!gather(n, read, x)) {
+              alive = false;
+              break;
             }
-            write(c, x);
+#pragma unroll
+            for (int c = 0; c < C::kChunks; ++c)
+              if (c < n) reduce(c, x[c]);
           }
-          if (n == 0) {
-            hand_back();
-            if (two) hand_back();
-          }
-        } else {
-          float x[C::kChunks][32];
-          if (!gather(n, read, x)) {
+          __syncwarp();
+          if (lane == 0) ptx::mbar_arrive(stat_bar(h));
+          if (!wait_bar_warp<false>(stat_bar(h), stat_phase, ctl)) {
             alive = false;
             break;
           }
+          // the four warps' 32 rows each: warp q joins chunk q
+          const int col = col0 + q * 32 + lane;
+          if (q < nch && !idle && col < tc.n_end && tc.a0 < p.m) {
+            float m = -INFINITY, s = 0.f;
+            float2 x[4];
 #pragma unroll
-          for (int c = 0; c < C::kChunks; ++c)
-            if (c < n) write(c, x[c]);
-        }
-      } else if constexpr (EPI == EPI_BF16) {   // tiles are a multiple of 64 wide: chunks in pairs
-        const int n = idle ? 0 : nch;
-        const bool nothing = GRP == GRP_K && tc.nks == 0;   // no rows: the sum is empty, the accumulator undefined
-#pragma unroll 1
-        for (int c0 = 0; c0 < n; c0 += 2) {
-          uint32_t w[32];
+            for (int i = 0; i < 4; ++i) {
+              x[i] = stat[i * C::kBN + q * 32 + lane];
+              m = fmaxf(m, x[i].x);
+            }
+            const float sub = fabsf(m) == INFINITY ? 0.f : m;
 #pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            uint32_t v[32];
-            ptx::tmem_ld_32x32b_x32(tbase + uint32_t((c0 + c) * 32), v);
-            ptx::tmem_ld_wait_for(v);
-#pragma unroll
-            for (int j = 0; j < 16; ++j)
-              w[16 * c + j] = nothing ? 0u
-                                      : ptx::pack_bf16x2(__uint_as_float(v[2 * j]) * alpha,
-                                                         __uint_as_float(v[2 * j + 1]) * alpha);
+            for (int i = 0; i < 4; ++i) s += x[i].y * ptx::ex2((x[i].x - sub) * kLog2e);
+            p.part[size_t(tc.a0 >> 7) * size_t(p.n) + col] = make_float2(m, s);
           }
-          if (c0 + 2 >= n) hand_back();
-          const int col = col0 + c0 * 32;
-          if (col < tc.n_end && row0 < p.m)
-            store_rows(w, row0, [&](uint32_t buf, int r) { ptx::tma_store_3d(&tmD, buf, col, r, GRP == GRP_K ? tc.z : 0); });
-        }
-        if (n == 0) hand_back();
-      } else {
-        const int n = idle ? 0 : nch;
-        [[maybe_unused]] const bool nothing = GRP == GRP_K && tc.nks == 0;
-        auto write = [&](int c, uint32_t (&v)[32]) {
-          const int col = col0 + c * 32;
-          if (col >= tc.n_end || row0 >= p.m) return;
-          if constexpr (EPI == EPI_BF16_T) {
-            // even lanes take column j for rows (lane, lane + 1), odd lanes column j + 1 for rows (lane - 1, lane)
+        } else if constexpr (EPI == EPI_DLOGITS) {
+          const int n = idle ? 0 : nch;
+          auto read = [&](int c, uint32_t a, bool first, float (&x)[32]) {
+            if constexpr (SHAPE == SHAPE_WIDE) {
+              uint32_t v[32];
+              ptx::tmem_ld_32x32b_x32(tq + a * uint32_t(C::kBN) + uint32_t(c * 32), v);
+              ptx::tmem_ld_wait_for(v);
+#pragma unroll
+              for (int j = 0; j < 32; ++j) x[j] = __uint_as_float(v[j]);
+            } else {
+              read_row(c, a, first, x);
+            }
+          };
+          auto write = [&](int c, float (&g)[32]) {
+            // The logit rounded as the loss has it (__fmul_rn: not fused), and then its difference: the label's
+            // exp(z - lse) - 1 is 0 where lse is that logit, and the rounding of z log2(e) (2^-24 of the logit's
+            // size) stays out of every g
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+              g[j] = ptx::ex2((__fmul_rn(g[j], alpha) - __shfl_sync(0xffffffffu, lse[c], j)) * kLog2e);
+            int off;
+            const uint32_t hits = among_rows(label[c], off);
+            if (hits) {
+              asm volatile("");   // (a branch, not 32 selects)
+#pragma unroll
+              for (int j = 0; j < 32; ++j)
+                if (((hits >> j) & 1u) && lane == __shfl_sync(0xffffffffu, off, j)) g[j] -= 1.f;
+            }
+            const uint32_t gone = __ballot_sync(0xffffffffu, label[c] < 0);
+            if (gone) {   // ignored tokens, whatever their logits and lse are (and columns that are not there)
+              asm volatile("");
+#pragma unroll
+              for (int j = 0; j < 32; ++j)
+                if ((gone >> j) & 1u) g[j] = 0.f;
+            }
             uint32_t w[16];
 #pragma unroll
-            for (int j = 0; j < 16; ++j) {
-              const float x0 = __uint_as_float(v[2 * j]) * alpha, x1 = __uint_as_float(v[2 * j + 1]) * alpha;
-              const float r = __shfl_xor_sync(0xffffffffu, (lane & 1) ? x0 : x1, 1);
-              w[j] = (lane & 1) ? ptx::pack_bf16x2(r, x1) : ptx::pack_bf16x2(x0, r);
-            }
-            const int there = tc.n_end - col;   // columns of the chunk that are the tile's
-            if (there >= 16) {
+            for (int j = 0; j < 16; ++j) w[j] = ptx::pack_bf16x2(g[2 * j], g[2 * j + 1]);
+            const int at = h * C::kChunks * 32 + c * 32, col = tc.n0 + at;
+            if (col >= tc.n_end || row0 >= p.m) return;
+            if (at + 32 <= tc.nt) {
               stage_box(
                   [&](uint32_t buf) {
 #pragma unroll
-                    for (int j = 0; j < 16; ++j) {
-                      const uint32_t r = uint32_t(2 * j + (lane & 1));
-                      const uint32_t chunk = (uint32_t(lane) >> 3) ^ ((r >> 1) & 3u);
-                      asm volatile("st.shared.b32 [%0], %1;" ::"r"(buf + r * 64u + chunk * 16u + ((uint32_t(lane) >> 1) & 3u) * 4u),
-                                   "r"(w[j])
-                                   : "memory");
-                    }
+                    for (int j = 0; j < 4; ++j)
+                      ptx::st_shared_v4(buf + uint32_t(lane * 64) + ((uint32_t(j) ^ ((uint32_t(lane) >> 1) & 3u)) << 4),
+                                        w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
                   },
                   [&](uint32_t buf) {
-                    ptx::tma_store_3d(&tmD, buf, row0, col, 0);
-                    if (there >= 32) ptx::tma_store_3d(&tmD, buf + 1024u, row0, col + 16, 0);
+                    ptx::tma_store_3d(&tmD, buf, col, row0, 0);
+                    if (row0 + 16 < p.m) ptx::tma_store_3d(&tmD, buf + 1024u, col, row0 + 16, 0);
                   });
+            } else if (row0 + lane < p.m) {   // the tile ends within the 32: its 16 columns (a 32-byte sector)
+              uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.d) + size_t(row0 + lane) * p.ldd + col);
+              dst[0] = make_uint4(w[0], w[1], w[2], w[3]);
+              dst[1] = make_uint4(w[4], w[5], w[6], w[7]);
             }
-            if ((there & 15) && there < 32 && row0 + (lane & ~1) < p.m) {   // fewer than 16 before the tile's or group's end
-              uint16_t* dst = static_cast<uint16_t*>(p.d) + row0 + (lane & ~1);
+          };
+          if constexpr (SHAPE != SHAPE_SUMS) {
 #pragma unroll
-              for (int j = 0; j < 16; ++j) {
-                const int r = 2 * j + (lane & 1);
-                if (r >= (there & 16) && r < there)
-                  *reinterpret_cast<uint32_t*>(dst + size_t(col + r) * p.ldd) = w[j];
+            for (int c = 0; c < C::kChunks; ++c) {
+              if (c >= n) break;
+              float x[32];
+              read(c, acc, true, x);
+              if (two) read(c, acc ^ 1u, false, x);
+              if (c + 1 == n) {
+                hand_back();
+                if (two) hand_back();
               }
+              write(c, x);
             }
-          } else {   // F32: tiles are a multiple of 32 wide
-            if (nothing && p.accumulate) return;   // adding nothing
+            if (n == 0) {
+              hand_back();
+              if (two) hand_back();
+            }
+          } else {
+            float x[C::kChunks][32];
+            if (!gather(n, read, x)) {
+              alive = false;
+              break;
+            }
 #pragma unroll
-            for (int j = 0; j < 32; ++j) v[j] = nothing ? 0u : __float_as_uint(__uint_as_float(v[j]) * alpha);
-            store_rows(v, row0, [&](uint32_t buf, int r) {
-              if (p.accumulate)
-                ptx::tma_add_3d(&tmD, buf, col, r, tc.z);
-              else
-                ptx::tma_store_3d(&tmD, buf, col, r, tc.z);
-            });
+            for (int c = 0; c < C::kChunks; ++c)
+              if (c < n) write(c, x[c]);
           }
-        };
-        if constexpr (SHAPE != SHAPE_SUMS) {
+        } else if constexpr (EPI == EPI_BF16) {   // tiles are a multiple of 64 wide: chunks in pairs
+          const int n = idle ? 0 : nch;
+          const bool nothing = GRP == GRP_K && tc.nks == 0;   // no rows: the sum is empty, the accumulator undefined
 #pragma unroll 1
-          for (int c = 0; c < n; ++c) {
-            uint32_t v[32];
-            ptx::tmem_ld_32x32b_x32(tbase + uint32_t(c * 32), v);
-            ptx::tmem_ld_wait_for(v);
-            if (c + 1 == n) hand_back();
-            write(c, v);
+          for (int c0 = 0; c0 < n; c0 += 2) {
+            uint32_t w[32];
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+              uint32_t v[32];
+              ptx::tmem_ld_32x32b_x32(tbase + uint32_t((c0 + c) * 32), v);
+              ptx::tmem_ld_wait_for(v);
+#pragma unroll
+              for (int j = 0; j < 16; ++j)
+                w[16 * c + j] = nothing ? 0u
+                                        : ptx::pack_bf16x2(__uint_as_float(v[2 * j]) * alpha,
+                                                           __uint_as_float(v[2 * j + 1]) * alpha);
+            }
+            if (c0 + 2 >= n) hand_back();
+            const int col = col0 + c0 * 32;
+            if (col < tc.n_end && row0 < p.m)
+              store_rows(w, row0, [&](uint32_t buf, int r) {
+                ptx::tma_store_3d(&tmD, buf, col, r, GRP == GRP_K ? tc.z : 0);
+              });
           }
           if (n == 0) hand_back();
         } else {
-          float x[C::kChunks][32];
-          if (!gather(n, read_row, x)) {
-            alive = false;
-            break;
-          }
+          const int n = idle ? 0 : nch;
+          [[maybe_unused]] const bool nothing = GRP == GRP_K && tc.nks == 0;
+          auto write = [&](int c, uint32_t (&v)[32]) {
+            const int col = col0 + c * 32;
+            if (col >= tc.n_end || row0 >= p.m) return;
+            if constexpr (EPI == EPI_BF16_T) {
+              // even lanes take column j for rows (lane, lane + 1), odd lanes column j + 1 for rows (lane - 1, lane)
+              uint32_t w[16];
 #pragma unroll
-          for (int c = 0; c < C::kChunks; ++c) {
-            if (c < n) {
+              for (int j = 0; j < 16; ++j) {
+                const float x0 = __uint_as_float(v[2 * j]) * alpha, x1 = __uint_as_float(v[2 * j + 1]) * alpha;
+                const float r = __shfl_xor_sync(0xffffffffu, (lane & 1) ? x0 : x1, 1);
+                w[j] = (lane & 1) ? ptx::pack_bf16x2(r, x1) : ptx::pack_bf16x2(x0, r);
+              }
+              const int there = tc.n_end - col;   // columns of the chunk that are the tile's
+              if (there >= 16) {
+                stage_box(
+                    [&](uint32_t buf) {
+#pragma unroll
+                      for (int j = 0; j < 16; ++j) {
+                        const uint32_t r = uint32_t(2 * j + (lane & 1));
+                        const uint32_t chunk = (uint32_t(lane) >> 3) ^ ((r >> 1) & 3u);
+                        asm volatile("st.shared.b32 [%0], %1;" ::"r"(buf + r * 64u + chunk * 16u +
+                                                                     ((uint32_t(lane) >> 1) & 3u) * 4u),
+                                     "r"(w[j])
+                                     : "memory");
+                      }
+                    },
+                    [&](uint32_t buf) {
+                      ptx::tma_store_3d(&tmD, buf, row0, col, 0);
+                      if (there >= 32) ptx::tma_store_3d(&tmD, buf + 1024u, row0, col + 16, 0);
+                    });
+              }
+              // fewer than 16 before the tile's or group's end
+              if ((there & 15) && there < 32 && row0 + (lane & ~1) < p.m) {
+                uint16_t* dst = static_cast<uint16_t*>(p.d) + row0 + (lane & ~1);
+#pragma unroll
+                for (int j = 0; j < 16; ++j) {
+                  const int r = 2 * j + (lane & 1);
+                  if (r >= (there & 16) && r < there)
+                    *reinterpret_cast<uint32_t*>(dst + size_t(col + r) * p.ldd) = w[j];
+                }
+              }
+            } else {   // F32: tiles are a multiple of 32 wide
+              if (nothing && p.accumulate) return;   // adding nothing
+#pragma unroll
+              for (int j = 0; j < 32; ++j) v[j] = nothing ? 0u : __float_as_uint(__uint_as_float(v[j]) * alpha);
+              store_rows(v, row0, [&](uint32_t buf, int r) {
+                if (p.accumulate)
+                  ptx::tma_add_3d(&tmD, buf, col, r, tc.z);
+                else
+                  ptx::tma_store_3d(&tmD, buf, col, r, tc.z);
+              });
+            }
+          };
+          if constexpr (SHAPE != SHAPE_SUMS) {
+#pragma unroll 1
+            for (int c = 0; c < n; ++c) {
               uint32_t v[32];
-#pragma unroll
-              for (int j = 0; j < 32; ++j) v[j] = __float_as_uint(x[c][j]);
+              ptx::tmem_ld_32x32b_x32(tbase + uint32_t(c * 32), v);
+              ptx::tmem_ld_wait_for(v);
+              if (c + 1 == n) hand_back();
               write(c, v);
+            }
+            if (n == 0) hand_back();
+          } else {
+            float x[C::kChunks][32];
+            if (!gather(n, read_row, x)) {
+              alive = false;
+              break;
+            }
+#pragma unroll
+            for (int c = 0; c < C::kChunks; ++c) {
+              if (c < n) {
+                uint32_t v[32];
+#pragma unroll
+                for (int j = 0; j < 32; ++j) v[j] = __float_as_uint(x[c][j]);
+                write(c, v);
+              }
             }
           }
         }
-      }
       }
       t = t_next;
     }

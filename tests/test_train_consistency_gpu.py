@@ -83,3 +83,33 @@ def test_infinities_in_rows_that_count_reach_the_gradients():
         assert torch.equal(torch.isnan(dW), torch.isnan(g.T @ h.X.to(F64)))
         rest = torch.arange(tokens, device="cuda") != 1
         assert torch.equal(dX[rest], clean[0][rest])
+
+
+def test_long_forms_time_out_and_recover():
+    # sums in parts (logits, FP32 weight gradients), two blocks to an SM: every role's waits end
+    wide, narrow = Head(200, 700, 4104, seed=34), Head(20, 20003, 4096, seed=35)
+    lse = {h: h.forward()[2].float() for h in (wide, narrow)}
+    dev = torch.tensor([2100, 0, 900], dtype=torch.int32, device="cuda")
+    dD, A = (torch.randn(3000, w, device="cuda").to(BF16) for w in (264, 520))
+    dB = torch.zeros(3, 264, 520, device="cuda")
+
+    def calls():
+        for h in (wide, narrow):
+            yield lambda: run_loss(h)
+            yield lambda: run_grad(h, lse[h])
+        yield lambda: tkg.gemm_grouped_dev_bf16_wgrad(dev, dD, A, dB, accumulate=True)
+
+    want = [f() for f in calls()]
+    dB.zero_()
+    try:
+        tkg.set_option(tkg.OPT_TIMEOUT_MS, 100)
+        tkg.set_option(tkg.OPT_INJECT_STALL, 1)
+        for f in calls():
+            f()
+            assert tkg.device_status() == tkg.ERR_TIMEOUT
+    finally:
+        tkg.set_option(tkg.OPT_INJECT_STALL, 0)
+        tkg.set_option(tkg.OPT_TIMEOUT_MS, 0)
+    for f, w in zip(calls(), want):
+        got = f()
+        assert w is None or all(torch.equal(a, b) for a, b in zip(got, w))
