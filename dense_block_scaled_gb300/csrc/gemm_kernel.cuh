@@ -649,7 +649,7 @@ __global__ void __launch_bounds__(384, 1)
   // Cluster launch control: the grid holds one cluster per tile; a running
   // cluster takes over a cluster that has not started yet (its tile is that
   // cluster's index).  The pair leader's scheduler lane asks; every role reads
-  // the answer from its own CTA's copy and releases it.  Returns -1 when no
+  // the answer from its own CTA's copy and releases it (but not the last).  Returns -1 when no
   // tile is left, -2 when the kernel is aborting.  next_tile is called by a
   // whole converged warp (every lane waits and reads, lane 0 releases),
   // next_tile_lane by a role that runs in one elected lane.
@@ -663,7 +663,7 @@ __global__ void __launch_bounds__(384, 1)
       uint32_t x = 0;
       const bool got = ptx::clc_read(clc_resp(cslot), x);
       __syncwarp();
-      if (lane == 0) {
+      if (got && lane == 0) {
         const uint32_t bar = ptx::clc_read_done(clc_empty(cslot), x);
         if (leader)
           ptx::mbar_arrive(bar);
@@ -688,10 +688,12 @@ __global__ void __launch_bounds__(384, 1)
       uint32_t x = 0;
       const bool got = ptx::clc_read(clc_resp(cslot), x);
       const uint32_t bar = ptx::clc_read_done(clc_empty(cslot), x);
-      if (leader)
-        ptx::mbar_arrive(bar);
-      else
-        ptx::mbar_arrive_relaxed_cluster(ptx::map_to_rank(bar, 0));
+      if (got) {
+        if (leader)
+          ptx::mbar_arrive(bar);
+        else
+          ptx::mbar_arrive_relaxed_cluster(ptx::map_to_rank(bar, 0));
+      }
       if (++cslot == 2) {
         cslot = 0;
         cphase ^= 1u;
@@ -946,21 +948,17 @@ __global__ void __launch_bounds__(384, 1)
           if (!wait_bar<false>(clc_full(slot), ph, ctl)) break;
           uint32_t x = 0;
           const bool got = ptx::clc_read(clc_resp(slot), x);
-          ptx::mbar_arrive(ptx::clc_read_done(clc_empty(slot), x));
+          if (got) ptx::mbar_arrive(ptx::clc_read_done(clc_empty(slot), x));
           if (++slot == 2) {
             slot = 0;
             ph ^= 1u;
           }
           if (!got) {
-            // both CTAs' roles have read the last two answers: no arrival from the other CTA is in flight when
-            // this one leaves and its shared memory goes to the next kernel
-            for (int i = 0; i < 2; ++i) {
-              if (!wait_bar<CG == 2>(clc_empty(slot), ph ^ 1u, ctl)) break;
-              if (++slot == 2) {
-                slot = 0;
-                ph ^= 1u;
-              }
-            }
+            // Both CTAs' roles have read the answer before the last, and for the last, which is not refilled, they do
+            // not arrive: no arrival from the other CTA is in flight when this one leaves and its shared memory goes
+            // to the next kernel.  (The answer before is a tile old; waiting for readers of the last would put their
+            // arrivals' way between the last store and the exit.)
+            wait_bar<CG == 2>(clc_empty(slot), ph ^ 1u, ctl);
             break;
           }
         }

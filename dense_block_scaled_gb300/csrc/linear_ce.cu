@@ -93,7 +93,7 @@ __global__ void __launch_bounds__(1024)
 // ce_weighted_row for every token, and s.  Every block finds s again from the T
 // weights (T x 12 bytes from L2 for each of at most two blocks per SM, against one
 // more launch), then takes a row per warp.  For heads with too few tiles to deal
-// the rows over (see rows_on_the_side).
+// the rows over, or too many weights (see rows_on_the_side).
 __global__ void __launch_bounds__(256)
     ce_rows_kernel(int tokens, int vocab, int hidden, const uint16_t* __restrict__ X, size_t ldx,
                    const long long* __restrict__ labels, const float* __restrict__ dloss, float alpha,

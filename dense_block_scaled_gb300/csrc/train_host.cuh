@@ -45,7 +45,7 @@ inline tkg_status map_prefetch(CUtensorMap* map, const void* base, int m, int n,
   return encode_3d(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, base, uint64_t(n), uint64_t(m), uint64_t(parts), row_bytes,
                    part_bytes, 256, 32, 1);
 }
-// Multiple that an output's tiles are wide: a store box's columns (turned: the MMA's 16).
+// Multiple that an output's tiles are wide: a store box's columns (of tokens: the MMA's 16).
 constexpr int kTileBF16 = 64, kTileF32 = 32, kTileTokens = 16;
 
 // Fills the fields common to every launch and launches.  The caller sets p.m, n,

@@ -49,4 +49,11 @@ def test_the_refill_follows_a_proxy_fence(name):
 def test_the_scheduler_leaves_after_the_last_reads(name):
     src = code(name)
     last = src[src.index("if (!got)", src.index("ptx::clc_try_cancel")):]
-    assert re.match(r"if \(!got\) \{\s*for \(int i = 0; i < 2; \+\+i\) \{\s*if \(!wait_bar<[^>]*>\(clc_empty\(slot\)", last)
+    both = re.match(r"if \(!got\) \{\s*for \(int i = 0; i < 2; \+\+i\) \{\s*if \(!wait_bar<[^>]*>\(clc_empty\(slot\)", last)
+    one = re.match(r"if \(!got\) \{\s*wait_bar<[^>]*>\(clc_empty\(slot\), ph \^ 1u, ctl\);\s*break;", last)
+    assert both or one
+    if one:   # of the answer before the last; then nobody may arrive for the last
+        arrivals = [m.start() for m in re.finditer(r"clc_read_done\(clc_empty\(", src)]
+        assert len(arrivals) >= 3
+        for at in arrivals:
+            assert re.search(r"if \(got( && lane == 0)?\)", src[at - 120:at + 120])
