@@ -300,7 +300,7 @@ typedef enum {
  *    type).  alpha * dloss[t] multiplies dX's rows in FP32 and, relative to the
  *    largest, the rows of X that dW is made of, which are rounded to BF16 again
  *    (the same rows where all weights are equal, as for a mean).  Weights that are
-    NaN or infinite reach dX and dW as the formula has them.
+ *    NaN or infinite reach dX and dW as the formula has them.
  *  - workspace: at least tkg_linear_ce_grad_workspace_bytes() with the same
  *    sizes and piece.  Sums are made in a fixed order: the same inputs give the
  *    same bits.
