@@ -14,7 +14,7 @@
 // (maximum, sum) per token.
 //
 // Bound by HBM: 1 token x 32768 x 2048 takes 25.9 us (134 MB, 19.8 us at the
-// copy rate; 26.8 on tensor-core tiles), x 131072 x 4096 158 us (6.8 TB/s), x 4000
+// copy rate; 26.8 on tensor-core tiles), x 131072 x 4096 156 us (6.9 TB/s), x 4000
 // x 2048 9.2 us (13.9 on tiles).
 #include "linear_ce.cuh"
 
