@@ -1,5 +1,7 @@
 // grouped_grad.cu -- gradients of the expert-grouped products (row counts in
-// device memory): dA = alpha dD B_g per group of rows, dB_g = alpha dD_g^T A_g.
+// device memory): dA = alpha dD B_g per group of rows, dB_g = alpha dD_g^T A_g;
+// the latter also with A's rows saved in 8 bits.
+#include "mxfp8.cuh"
 #include "train_host.cuh"
 
 namespace tkg {
@@ -10,6 +12,39 @@ tkg_status check_groups(int groups, const int* sizes, int capacity, int n, int k
   if (groups > kMaxGroups || capacity > kMaxSize || n > kMaxSize || k > kMaxSize) return TKG_ERR_UNSUPPORTED;
   if (!aligned_to(sizes, 4) || n % 8 != 0 || k % 8 != 0) return TKG_ERR_ALIGNMENT;
   return TKG_OK;
+}
+
+// Rows saved in 8 bits, in the groups' order, as BF16 (exactly: a code's 4 significant bits and a power of two): row r is
+// that of token slots[r] / topk, or r.  A warp per row and 512 columns: 16 codes to a lane.
+__global__ void __launch_bounds__(256) unpack_rows_kernel(int rows, int k, int tokens, int topk,
+                                                          const uint8_t* __restrict__ Q, const uint8_t* __restrict__ sf,
+                                                          const int* __restrict__ slots, uint16_t* __restrict__ out) {
+  ptx::pdl_launch_dependents();
+  const int lane = threadIdx.x & 31, per_row = (k + 511) / 512;
+  const long long task = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
+  const int r = int(task / per_row), c = int(task - (long long)r * per_row) * 512 + lane * 16;
+  ptx::pdl_wait();
+  if (r >= rows || c >= k) return;
+  int t = r;
+  if (slots) {
+    const int s = __ldcg(slots + r);
+    t = s < 0 ? -1 : s / topk;
+  }
+  uint4 w[2] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
+  if (t >= 0 && t < tokens) {
+    const uint4 q = __ldg(reinterpret_cast<const uint4*>(Q + size_t(t) * size_t(k) + c));
+    const float s = e8m0_value(__ldg(sf + (size_t(t) * size_t(k) + c) / 32));
+    const uint32_t u[4] = {q.x, q.y, q.z, q.w};
+    uint32_t* o = reinterpret_cast<uint32_t*>(w);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float2 v = e4m3x2_values(u[i / 2] >> (16 * (i & 1)));
+      o[i] = ptx::pack_bf16x2(v.x * s, v.y * s);
+    }
+  }
+  uint4* dst = reinterpret_cast<uint4*>(out + size_t(r) * size_t(k) + c);
+  dst[0] = w[0];
+  dst[1] = w[1];
 }
 
 }  // namespace
@@ -108,6 +143,37 @@ tkg_status tkg_gemm_grouped_dev_bf16_wgrad(int groups, const int* m_sizes_dev, i
     return launch_train<true, true, EPI_F32, GRP_K, SHAPE_SUMS>(tmA, tmB, tmD, p, stream, extra);
   return dual ? launch_train<true, true, EPI_F32, GRP_K, SHAPE_DUAL>(tmA, tmB, tmD, p, stream, extra)
               : launch_train<true, true, EPI_F32, GRP_K>(tmA, tmB, tmD, p, stream, extra);
+}
+
+size_t tkg_gemm_grouped_dev_mxfp8_wgrad_workspace_bytes(int m_capacity, int k) {
+  if (m_capacity < 0 || k < 0 || m_capacity > kMaxSize || k > kMaxSize) return 0;
+  return size_t(m_capacity) * size_t(k) * 2 + 16;
+}
+
+tkg_status tkg_gemm_grouped_dev_mxfp8_wgrad(int groups, const int* m_sizes_dev, int m_capacity, int n, int k,
+                                            const void* dD, int tokens, const void* Q, const void* sf, const int* slots,
+                                            int topk, void* dB, tkg_grad_type type, float alpha, void* workspace,
+                                            size_t workspace_bytes, cudaStream_t stream) {
+  tkg_status st = check_groups(groups, m_sizes_dev, m_capacity, n, k);
+  if (st != TKG_OK) return st;
+  if (tokens < 0 || topk < 1) return TKG_ERR_INVALID_ARG;
+  if (tokens > kMaxSize) return TKG_ERR_UNSUPPORTED;
+  if (k % 32 != 0 || !aligned_to(Q, 16) || !aligned_to(slots, 4) || !aligned_to(workspace, 16)) return TKG_ERR_ALIGNMENT;
+  const bool some = m_capacity > 0 && n > 0 && k > 0;
+  if (some) {
+    if (!dD || (tokens > 0 && (!Q || !sf)) || !dB || !workspace ||
+        workspace_bytes < tkg_gemm_grouped_dev_mxfp8_wgrad_workspace_bytes(m_capacity, k) ||
+        (type != TKG_GRAD_BF16 && type != TKG_GRAD_F32 && type != TKG_GRAD_F32_ADD))
+      return TKG_ERR_INVALID_ARG;
+    if (!aligned_to(dD, 16) || !aligned_to(dB, 16)) return TKG_ERR_ALIGNMENT;
+    const long long blocks = ((long long)m_capacity * ceil_div(k, 512) + 7) / 8;
+    if (blocks > kMaxSize) return TKG_ERR_UNSUPPORTED;
+    st = launch_small(unpack_rows_kernel, dim3(unsigned(blocks)), dim3(256), stream, 0u, m_capacity, k, tokens, topk,
+                      static_cast<const uint8_t*>(Q), static_cast<const uint8_t*>(sf), slots,
+                      static_cast<uint16_t*>(workspace));
+    if (st != TKG_OK) return st;
+  }
+  return tkg_gemm_grouped_dev_bf16_wgrad(groups, m_sizes_dev, m_capacity, n, k, dD, workspace, dB, type, alpha, stream);
 }
 
 }  // extern "C"

@@ -15,6 +15,7 @@
 #include <cstdint>
 
 #include "host_common.cuh"
+#include "mxfp8.cuh"
 
 namespace tkg {
 
@@ -22,13 +23,6 @@ namespace tkg {
 __device__ __forceinline__ size_t sf_tiled_offset(int r, int kb, int ka) {
   return (size_t(r >> 7) * size_t(ka) + size_t(kb >> 2)) * 512u + size_t(r & 31) * 16u +
          size_t((r & 127) >> 5) * 4u + size_t(kb & 3);
-}
-
-// Two FP32 -> E4M3 (RNE, saturating); `lo` lands in the low byte.
-__device__ __forceinline__ uint32_t cvt_e4m3x2(float lo, float hi) {
-  uint16_t r;
-  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
-  return r;
 }
 
 // Two FP32 -> E2M1 (RNE, saturating); `lo` lands in the low nibble.
@@ -45,17 +39,6 @@ __device__ __forceinline__ float e4m3_value(uint32_t s) {
   const uint32_t e = (s >> 3) & 0xFu, m = s & 7u;
   if (e == 0) return __fmul_rn(float(m), 1.0f / 512.0f);
   return __uint_as_float(((e + 120u) << 23) | (m << 20));
-}
-
-// MXFP8 scale exponent: smallest e with 448 * 2^e >= amax, clamped to [-127, 127].
-// With amax = M * 2^E (M in [1, 2)), 448 = 1.75 * 2^8, that is
-// e = E - 8 + (M > 1.75); subnormal or zero amax gives -127.
-__device__ __forceinline__ int mx_exponent(float amax) {
-  const uint32_t u = __float_as_uint(amax);
-  const int eb = int((u >> 23) & 0xFFu);
-  if (eb == 0) return -127;
-  int e = (eb - 127) - 8 + (((u & 0x7FFFFFu) > 0x600000u) ? 1 : 0);
-  return e < -127 ? -127 : (e > 127 ? 127 : e);
 }
 
 // Each warp walks its own contiguous range of passes, and every lane keeps the

@@ -39,11 +39,16 @@ EXPORTS = [
     "tkg_gemm_bf16_strided", "tkg_gemm_mxfp8_strided", "tkg_gemm_nvfp4_strided",
     "tkg_linear_ce_loss", "tkg_linear_ce_loss_workspace_bytes", "tkg_linear_ce_grad",
     "tkg_linear_ce_grad_workspace_bytes", "tkg_gemm_grouped_dev_bf16_dgrad", "tkg_gemm_grouped_dev_bf16_wgrad",
+    "tkg_moe_route", "tkg_moe_route_workspace_bytes", "tkg_moe_route_grad", "tkg_moe_dispatch", "tkg_moe_combine",
+    "tkg_checkpoint_mxfp8", "tkg_swiglu", "tkg_swiglu_grad", "tkg_gemm_grouped_dev_mxfp8_wgrad",
+    "tkg_gemm_grouped_dev_mxfp8_wgrad_workspace_bytes",
 ]
 
 MAX_LIST = 16
 
 GRAD_BF16, GRAD_F32, GRAD_F32_ADD = 0, 1, 2
+TYPE_BF16, TYPE_F32 = 0, 1
+SCORES = {"softmax": 0, "sigmoid": 1}
 
 
 class GemmDesc(ctypes.Structure):
@@ -52,6 +57,13 @@ class GemmDesc(ctypes.Structure):
                 ("A", ctypes.c_void_p), ("B", ctypes.c_void_p), ("sfa", ctypes.c_void_p), ("sfb", ctypes.c_void_p),
                 ("tensor_scale_a", ctypes.c_void_p), ("tensor_scale_b", ctypes.c_void_p),
                 ("D", ctypes.c_void_p), ("alpha", ctypes.c_float)]
+
+
+class RouteRule(ctypes.Structure):
+    """tkg_route_rule: how the router's logits become choices and weights."""
+    _fields_ = [("scores", ctypes.c_int), ("groups", ctypes.c_int), ("topk_groups", ctypes.c_int),
+                ("renormalise", ctypes.c_int), ("scale", ctypes.c_float)]
+
 
 _lock = threading.Lock()
 _lib = None
@@ -109,6 +121,22 @@ def load() -> ctypes.CDLL:
                          "tkg_gemm_grouped_dev_bf16_wgrad"):
                 getattr(lib, name).restype = ctypes.c_int
             for name in ("tkg_linear_ce_loss_workspace_bytes", "tkg_linear_ce_grad_workspace_bytes"):
+                getattr(lib, name).restype = sz
+            rule = ctypes.POINTER(RouteRule)
+            lib.tkg_moe_route.argtypes = [i, i, i, vp, i, i, rule, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]
+            lib.tkg_moe_route_workspace_bytes.argtypes = [i, i]
+            lib.tkg_moe_route_grad.argtypes = [i, i, i, vp, i, i, rule, vp, vp, vp, i, vp]
+            lib.tkg_moe_dispatch.argtypes = [i, i, i, vp, i, vp, i, vp, i, vp]
+            lib.tkg_moe_combine.argtypes = [i, i, i, vp, i, i, vp, vp, vp, i, vp]
+            lib.tkg_checkpoint_mxfp8.argtypes = [i, i, vp, i, vp, vp, vp]
+            lib.tkg_swiglu.argtypes = [i, i, vp, i, vp, i, vp, vp, vp]
+            lib.tkg_swiglu_grad.argtypes = [i, i, vp, vp, vp, i, vp, i, vp, vp, i, vp, i, vp, vp]
+            lib.tkg_gemm_grouped_dev_mxfp8_wgrad.argtypes = [i, vp, i, i, i, vp, i, vp, vp, vp, i, vp, i, f, vp, sz, vp]
+            lib.tkg_gemm_grouped_dev_mxfp8_wgrad_workspace_bytes.argtypes = [i, i]
+            for name in ("tkg_moe_route", "tkg_moe_route_grad", "tkg_moe_dispatch", "tkg_moe_combine",
+                         "tkg_checkpoint_mxfp8", "tkg_swiglu", "tkg_swiglu_grad", "tkg_gemm_grouped_dev_mxfp8_wgrad"):
+                getattr(lib, name).restype = ctypes.c_int
+            for name in ("tkg_moe_route_workspace_bytes", "tkg_gemm_grouped_dev_mxfp8_wgrad_workspace_bytes"):
                 getattr(lib, name).restype = sz
             lib.tkg_get_device_status.argtypes = [vp]
             lib.tkg_status_string.argtypes = [st]
@@ -505,6 +533,227 @@ def gemm_grouped_dev_bf16_wgrad(sizes_dev, dD, A, dB, alpha: float = 1.0, accumu
     _check(load().tkg_gemm_grouped_dev_bf16_wgrad(groups, sizes_dev.data_ptr(), cap, n, k, dD.data_ptr(),
                                                   A.data_ptr(), dB.data_ptr(), gtype, alpha, _stream(stream, dev)),
            "tkg_gemm_grouped_dev_bf16_wgrad")
+
+
+# ---------------------------------------------------------------- a mixture-of-experts block
+
+@functools.lru_cache(maxsize=64)
+def _rule(scores, groups, topk_groups, renormalise, scale):
+    if scores not in SCORES:
+        raise ValueError(f"scores: one of {sorted(SCORES)} is wanted, got {scores!r}")
+    return ctypes.byref(RouteRule(SCORES[scores], groups, topk_groups, int(bool(renormalise)), scale))
+
+
+@functools.lru_cache(maxsize=256)
+def moe_route_workspace_bytes(tokens: int, experts: int) -> int:
+    return int(load().tkg_moe_route_workspace_bytes(tokens, experts))
+
+
+def _logit_type(t, name):
+    import torch
+    if t.dtype is not torch.bfloat16 and t.dtype is not torch.float32:
+        raise ValueError(f"{name}: bfloat16 or float32 is wanted, got {t.dtype}")
+    return TYPE_F32 if t.dtype is torch.float32 else TYPE_BF16
+
+
+def moe_route(logits, ids, weights, sizes, rows, slots, bias=None, keep=None, scores: str = "softmax", groups: int = 1,
+              topk_groups: int = 1, renormalise: bool = True, scale: float = 1.0, workspace=None, stream=None) -> None:
+    """Chooses ids.shape[1] experts per token by the router's logits (tokens x experts, bf16 or float32, rows may be
+    pitched) and lays the choices out in expert order.
+
+    scores: "softmax" or "sigmoid"; bias (experts, float32): added for the choice alone; groups, topk_groups: the choice
+    is limited to the best groups of consecutive experts; weights: the chosen scores, over their sum if renormalise,
+    times scale; keep (tokens, bool or uint8): False for tokens that are not routed.  Written: ids, rows (tokens x topk
+    int32; -1: not routed), weights (float32), sizes (experts, int32), slots (tokens * topk int32; -1 past the last row)."""
+    import torch
+    (tokens, experts), (_, topk), dev = logits.shape, ids.shape, logits.get_device()
+    kind, shape, i32 = _logit_type(logits, "logits"), ids.shape, torch.int32
+    if not (-1 < dev == torch.cuda.current_device() == ids.get_device() == weights.get_device() == sizes.get_device()
+            == rows.get_device() == slots.get_device() and not (tokens | experts | tokens * topk) >> 31
+            and ids.dtype is rows.dtype is sizes.dtype is slots.dtype is i32 and weights.dtype is torch.float32
+            and shape == weights.shape == rows.shape and shape[0] == tokens and sizes.shape == (experts,)
+            and slots.shape == (tokens * topk,) and logits.is_contiguous() and ids.is_contiguous()
+            and weights.is_contiguous() and rows.is_contiguous() and sizes.is_contiguous() and slots.is_contiguous()
+            and (bias is None or (bias.dtype is torch.float32 and bias.shape == (experts,) and bias.is_contiguous()
+                                  and bias.get_device() == dev))
+            and (keep is None or (keep.dtype in (torch.bool, torch.uint8) and keep.shape == (tokens,)
+                                  and keep.is_contiguous() and keep.get_device() == dev))):
+        wanted = [("logits", logits, logits.dtype, (tokens, experts), True), ("ids", ids, i32, (tokens, topk), False),
+                  ("weights", weights, torch.float32, (tokens, topk), False), ("sizes", sizes, i32, (experts,), False),
+                  ("rows", rows, i32, (tokens, topk), False), ("slots", slots, i32, (tokens * topk,), False)]
+        if bias is not None:
+            wanted.append(("bias", bias, torch.float32, (experts,), False))
+        if keep is not None:
+            wanted.append(("keep", keep, torch.uint8 if keep.dtype is torch.uint8 else torch.bool, (tokens,), False))
+        _refuse(wanted)
+    lib, handle = load(), _stream(stream, dev)
+    at, nbytes, _keep = _workspace(workspace, moe_route_workspace_bytes(tokens, experts), logits, stream, handle)
+    _check(lib.tkg_moe_route(tokens, experts, topk, logits.data_ptr(), kind, _pitch(logits, experts),
+                             _rule(scores, groups, topk_groups, renormalise, scale), _ptr(bias), _ptr(keep),
+                             ids.data_ptr(), weights.data_ptr(), sizes.data_ptr(), rows.data_ptr(), slots.data_ptr(), at,
+                             nbytes, handle), "tkg_moe_route")
+
+
+def moe_route_grad(logits, ids, dweights, dlogits, scores: str = "softmax", renormalise: bool = True,
+                   scale: float = 1.0, stream=None) -> None:
+    """Gradient of moe_route's weights to the logits, the choice being fixed: dlogits (as logits), all of it written."""
+    import torch
+    (tokens, experts), (_, topk), dev = logits.shape, ids.shape, logits.get_device()
+    kind = _logit_type(logits, "logits")
+    if not (-1 < dev == torch.cuda.current_device() == ids.get_device() == dweights.get_device()
+            == dlogits.get_device() and not (tokens | experts | tokens * topk) >> 31 and ids.dtype is torch.int32
+            and dweights.dtype is torch.float32 and dlogits.dtype is logits.dtype and ids.shape == dweights.shape
+            and ids.shape[0] == tokens and dlogits.shape == logits.shape and logits.is_contiguous()
+            and ids.is_contiguous() and dweights.is_contiguous() and dlogits.is_contiguous()):
+        _refuse((("logits", logits, logits.dtype, (tokens, experts), True), ("ids", ids, torch.int32, (tokens, topk), False),
+                 ("dweights", dweights, torch.float32, (tokens, topk), False),
+                 ("dlogits", dlogits, logits.dtype, (tokens, experts), True)))
+    _check(load().tkg_moe_route_grad(tokens, experts, topk, logits.data_ptr(), kind, _pitch(logits, experts),
+                                     _rule(scores, 1, 1, renormalise, scale), ids.data_ptr(), dweights.data_ptr(),
+                                     dlogits.data_ptr(), _pitch(dlogits, experts), _stream(stream, dev)),
+           "tkg_moe_route_grad")
+
+
+def moe_dispatch(X, rows, out, stream=None) -> None:
+    """out[rows[t, j]] = X[t] (bf16): tokens' rows into expert order; other rows of out are left as they were.  The
+    gradient of moe_combine without weights."""
+    import torch
+    (tokens, hidden), (_, topk), cap, dev = X.shape, rows.shape, out.shape[0], X.get_device()
+    if not (-1 < dev == torch.cuda.current_device() == rows.get_device() == out.get_device()
+            and not (tokens | hidden | cap | tokens * topk) >> 31 and X.dtype is out.dtype is torch.bfloat16
+            and rows.dtype is torch.int32 and rows.shape[0] == tokens and out.shape[1] == hidden and X.is_contiguous()
+            and rows.is_contiguous() and out.is_contiguous()):
+        _refuse((("X", X, torch.bfloat16, (tokens, hidden), True), ("rows", rows, torch.int32, (tokens, topk), False),
+                 ("out", out, torch.bfloat16, (cap, hidden), True)))
+    _check(load().tkg_moe_dispatch(tokens, topk, hidden, X.data_ptr(), _pitch(X, hidden), rows.data_ptr(), cap,
+                                   out.data_ptr(), _pitch(out, hidden), _stream(stream, dev)), "tkg_moe_dispatch")
+
+
+def moe_combine(O, rows, Y, weights=None, stream=None) -> None:
+    """Y[t] = sum_j weights[t, j] * O[rows[t, j]] (bf16, sums in float32; weights float32, None: 1).  Without weights the
+    gradient of moe_dispatch."""
+    import torch
+    (tokens, hidden), (_, topk), cap, dev = Y.shape, rows.shape, O.shape[0], Y.get_device()
+    if not (-1 < dev == torch.cuda.current_device() == rows.get_device() == O.get_device()
+            and not (tokens | hidden | cap | tokens * topk) >> 31 and O.dtype is Y.dtype is torch.bfloat16
+            and rows.dtype is torch.int32 and rows.shape[0] == tokens and O.shape[1] == hidden and O.is_contiguous()
+            and rows.is_contiguous() and Y.is_contiguous()
+            and (weights is None or (weights.dtype is torch.float32 and weights.shape == rows.shape
+                                     and weights.is_contiguous() and weights.get_device() == dev))):
+        wanted = [("O", O, torch.bfloat16, (cap, hidden), True), ("rows", rows, torch.int32, (tokens, topk), False),
+                  ("Y", Y, torch.bfloat16, (tokens, hidden), True)]
+        if weights is not None:
+            wanted.append(("weights", weights, torch.float32, (tokens, topk), False))
+        _refuse(wanted)
+    _check(load().tkg_moe_combine(tokens, topk, hidden, O.data_ptr(), _pitch(O, hidden), cap, rows.data_ptr(),
+                                  _ptr(weights), Y.data_ptr(), _pitch(Y, hidden), _stream(stream, dev)),
+           "tkg_moe_combine")
+
+
+def checkpoint_mxfp8(X, Q, sf, stream=None) -> None:
+    """Rows of X (bf16) in 8 bits: Q (rows x k, uint8 E4M3 codes), sf (rows x k / 32, uint8 E8M0), both row-major."""
+    import torch
+    (rows, k), dev = X.shape, X.get_device()
+    if not (-1 < dev == torch.cuda.current_device() == Q.get_device() == sf.get_device() and not (rows | k) >> 31
+            and X.dtype is torch.bfloat16 and Q.dtype is sf.dtype is torch.uint8 and Q.shape == X.shape
+            and sf.shape == (rows, k // 32) and X.is_contiguous() and Q.is_contiguous() and sf.is_contiguous()):
+        _refuse((("X", X, torch.bfloat16, (rows, k), True), ("Q", Q, torch.uint8, (rows, k), False),
+                 ("sf", sf, torch.uint8, (rows, k // 32), False)))
+    _check(load().tkg_checkpoint_mxfp8(rows, k, X.data_ptr(), _pitch(X, k), Q.data_ptr(), sf.data_ptr(),
+                                       _stream(stream, dev)), "tkg_checkpoint_mxfp8")
+
+
+def swiglu(GU, H, Q=None, sf=None, stream=None) -> None:
+    """H = silu(g) * u of rows GU = [g | u] (bf16); with Q (rows x 2 inner) and sf (rows x 2 inner / 32) also GU's
+    checkpoint in 8 bits."""
+    import torch
+    (rows, inner), dev = H.shape, H.get_device()
+    if (Q is None) != (sf is None):
+        raise ValueError("Q, sf: both or neither are wanted")
+    if not (-1 < dev == torch.cuda.current_device() == GU.get_device() and not (rows | 2 * inner) >> 31
+            and GU.dtype is H.dtype is torch.bfloat16 and GU.shape == (rows, 2 * inner) and GU.is_contiguous()
+            and H.is_contiguous()
+            and (Q is None or (Q.dtype is sf.dtype is torch.uint8 and Q.shape == GU.shape
+                               and sf.shape == (rows, 2 * inner // 32) and Q.is_contiguous() and sf.is_contiguous()
+                               and Q.get_device() == sf.get_device() == dev))):
+        wanted = [("GU", GU, torch.bfloat16, (rows, 2 * inner), True), ("H", H, torch.bfloat16, (rows, inner), True)]
+        if Q is not None:
+            wanted += [("Q", Q, torch.uint8, (rows, 2 * inner), False),
+                       ("sf", sf, torch.uint8, (rows, 2 * inner // 32), False)]
+        _refuse(wanted)
+    _check(load().tkg_swiglu(rows, inner, GU.data_ptr(), _pitch(GU, 2 * inner), H.data_ptr(), _pitch(H, inner), _ptr(Q),
+                             _ptr(sf), _stream(stream, dev)), "tkg_swiglu")
+
+
+def swiglu_grad(Q, sf, dH, dGU, H=None, slots=None, weights=None, dweights=None, stream=None) -> None:
+    """Gradient of swiglu from its checkpoint: dGU (rows x 2 inner, bf16) and, if given, H = weight * silu(g) * u and
+    dweights.  Row r is choice slots[r] (None: r) of weights (any shape, float32; None: 1); dH is the gradient without
+    the weight.  Rows whose choice is negative or past the weights are left as they were."""
+    import torch
+    (rows, inner), dev = dH.shape, dH.get_device()
+    choices = 0x7fff0000 if weights is None else weights.numel()
+    if dweights is not None and weights is None:
+        raise ValueError("dweights: wanted only together with weights")
+    if not (-1 < dev == torch.cuda.current_device() == Q.get_device() == sf.get_device() == dGU.get_device()
+            and not (rows | 2 * inner | choices) >> 31 and dH.dtype is dGU.dtype is torch.bfloat16
+            and Q.dtype is sf.dtype is torch.uint8 and Q.shape == dGU.shape == (rows, 2 * inner)
+            and sf.shape == (rows, 2 * inner // 32) and dH.is_contiguous() and dGU.is_contiguous() and Q.is_contiguous()
+            and sf.is_contiguous()
+            and (H is None or (H.dtype is torch.bfloat16 and H.shape == dH.shape and H.is_contiguous()
+                               and H.get_device() == dev))
+            and (slots is None or (slots.dtype is torch.int32 and slots.shape == (rows,) and slots.is_contiguous()
+                                   and slots.get_device() == dev))
+            and (weights is None or (weights.dtype is torch.float32 and weights.is_contiguous()
+                                     and weights.get_device() == dev))
+            and (dweights is None or (dweights.dtype is torch.float32 and dweights.shape == weights.shape
+                                      and dweights.is_contiguous() and dweights.get_device() == dev))):
+        wanted = [("Q", Q, torch.uint8, (rows, 2 * inner), False), ("sf", sf, torch.uint8, (rows, 2 * inner // 32), False),
+                  ("dH", dH, torch.bfloat16, (rows, inner), True), ("dGU", dGU, torch.bfloat16, (rows, 2 * inner), True)]
+        if H is not None:
+            wanted.append(("H", H, torch.bfloat16, (rows, inner), True))
+        if slots is not None:
+            wanted.append(("slots", slots, torch.int32, (rows,), False))
+        if weights is not None:
+            wanted.append(("weights", weights, torch.float32, weights.shape, False))
+        if dweights is not None:
+            wanted.append(("dweights", dweights, torch.float32, weights.shape, False))
+        _refuse(wanted)
+    _check(load().tkg_swiglu_grad(rows, inner, Q.data_ptr(), sf.data_ptr(), dH.data_ptr(), _pitch(dH, inner), _ptr(slots),
+                                  choices, _ptr(weights), dGU.data_ptr(), _pitch(dGU, 2 * inner), _ptr(H),
+                                  0 if H is None else _pitch(H, inner), _ptr(dweights), _stream(stream, dev)),
+           "tkg_swiglu_grad")
+
+
+@functools.lru_cache(maxsize=256)
+def gemm_grouped_dev_mxfp8_wgrad_workspace_bytes(m_capacity: int, k: int) -> int:
+    return int(load().tkg_gemm_grouped_dev_mxfp8_wgrad_workspace_bytes(m_capacity, k))
+
+
+def gemm_grouped_dev_mxfp8_wgrad(sizes_dev, dD, Q, sf, dB, slots=None, topk: int = 1, alpha: float = 1.0,
+                                 accumulate: bool = False, workspace=None, stream=None) -> None:
+    """gemm_grouped_dev_bf16_wgrad with A's rows from an 8-bit checkpoint Q, sf (tokens x k): row r is the checkpoint's
+    row slots[r] // topk (slots None: r).  accumulate: add to the float32 dB."""
+    import torch
+    groups, (cap, n), (tokens, k), dev = sizes_dev.shape[0], dD.shape, Q.shape, dD.get_device()
+    gtype = _grad_type(dB, "dB", accumulate)
+    if not (-1 < dev == torch.cuda.current_device() == sizes_dev.get_device() == Q.get_device() == sf.get_device()
+            == dB.get_device() and not (cap | n | k | tokens) >> 31 and dD.dtype is torch.bfloat16
+            and Q.dtype is sf.dtype is torch.uint8 and sizes_dev.dtype is torch.int32 and sizes_dev.dim() == 1
+            and sf.shape == (tokens, k // 32) and dB.shape == (groups, n, k) and dD.is_contiguous() and Q.is_contiguous()
+            and sf.is_contiguous() and dB.is_contiguous() and sizes_dev.is_contiguous()
+            and (slots is None or (slots.dtype is torch.int32 and slots.shape == (cap,) and slots.is_contiguous()
+                                   and slots.get_device() == dev))):
+        wanted = [("sizes_dev", sizes_dev, torch.int32, (groups,), False), ("dD", dD, torch.bfloat16, (cap, n), False),
+                  ("Q", Q, torch.uint8, (tokens, k), False), ("sf", sf, torch.uint8, (tokens, k // 32), False),
+                  ("dB", dB, dB.dtype, (groups, n, k), False)]
+        if slots is not None:
+            wanted.append(("slots", slots, torch.int32, (cap,), False))
+        _refuse(wanted)
+    lib, handle = load(), _stream(stream, dev)
+    at, nbytes, _keep = _workspace(workspace, gemm_grouped_dev_mxfp8_wgrad_workspace_bytes(cap, k), dD, stream, handle)
+    _check(lib.tkg_gemm_grouped_dev_mxfp8_wgrad(groups, sizes_dev.data_ptr(), cap, n, k, dD.data_ptr(), tokens,
+                                                Q.data_ptr(), sf.data_ptr(), _ptr(slots), topk, dB.data_ptr(), gtype,
+                                                alpha, at, nbytes, handle), "tkg_gemm_grouped_dev_mxfp8_wgrad")
 
 
 def grouped_dev_scale_bytes(groups: int, m_capacity: int, k: int, block: int) -> int:

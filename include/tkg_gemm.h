@@ -332,6 +332,106 @@ tkg_status tkg_gemm_grouped_dev_bf16_wgrad(int groups, const int *m_sizes_dev, i
                                            const void *dD, const void *A, void *dB, tkg_grad_type type, float alpha,
                                            cudaStream_t stream);
 
+/* ---- A mixture-of-experts block around the grouped products: routing, rows to
+ * expert order and back, the gated activation between two products, and what
+ * the backward pass needs of both saved in 8 bits.
+ *
+ * Routing.  logits: tokens x experts, BF16 or FP32, row pitch ld (any).
+ *   s = softmax(z) or sigmoid(z), c = s + bias  (bias: FP32 per expert, or NULL)
+ *   groups > 1: experts / groups consecutive experts form a group; the
+ *     topk_groups groups whose two largest c have the largest sum stay
+ *   the topk largest c of the experts left are chosen, in falling order; ties,
+ *     of groups too, go to the lowest index
+ *   weight_j = scale * s_j, or renormalised scale * s_j / sum_i s_i over the chosen
+ * The choice is that of the exact scores: where FP32 does not decide between two
+ * neighbours they are computed again in 64 bits, and without bias and groups the
+ * logits themselves are compared.  NaN comes after every number; a row (softmax),
+ * or sum of the chosen (renormalised), of zeros gives weights 0.
+ * keep (or NULL): a byte per token; 0 for one that is not routed (padding).
+ * Written: ids and weights (tokens x topk; not routed: -1 and 0);
+ *   sizes (experts): the rows of each expert, as tkg_gemm_grouped_dev_* take them;
+ *   rows (tokens x topk): the choice's row in expert order (by expert, then by
+ *     token), -1 if not routed; slots (tokens * topk): the choice t * topk + j in
+ *     each row, -1 past the last row.
+ *  - experts <= 512 (the grouped products take 128), topk <= 32 and <= the experts
+ *    left, groups <= 32 and a divisor of experts; else TKG_ERR_INVALID_ARG where it
+ *    makes no sense, TKG_ERR_UNSUPPORTED where it is too much.
+ *  - workspace as for tkg_linear_ce_loss, tkg_moe_route_workspace_bytes().
+ *  - tokens == 0: sizes is zeroed.  Nothing depends on the order of execution. */
+typedef enum { TKG_TYPE_BF16 = 0, TKG_TYPE_F32 = 1 } tkg_type;
+typedef enum { TKG_SCORES_SOFTMAX = 0, TKG_SCORES_SIGMOID = 1 } tkg_scores;
+typedef struct {
+  tkg_scores scores;
+  int groups, topk_groups;   /* 1, 1: no groups */
+  int renormalise;           /* 0 or 1 */
+  float scale;
+} tkg_route_rule;
+
+tkg_status tkg_moe_route(int tokens, int experts, int topk, const void *logits, tkg_type type, int ld,
+                         const tkg_route_rule *rule, const float *bias, const unsigned char *keep, int *ids,
+                         float *weights, int *sizes, int *rows, int *slots, void *workspace, size_t workspace_bytes,
+                         cudaStream_t stream);
+size_t tkg_moe_route_workspace_bytes(int tokens, int experts);
+
+/* The gradient of sum dweights * weights to the logits, the choice being fixed:
+ * dlogits (type and shape of logits, pitch lddz), every element written.  ids as
+ * tkg_moe_route wrote them (distinct in a row; outside [0, experts): no
+ * gradient).  Of rule, scores, renormalise and scale are read. */
+tkg_status tkg_moe_route_grad(int tokens, int experts, int topk, const void *logits, tkg_type type, int ld,
+                              const tkg_route_rule *rule, const int *ids, const float *dweights, void *dlogits, int lddz,
+                              cudaStream_t stream);
+
+/* Tokens' rows into expert order and back (rows as tkg_moe_route wrote them):
+ *   dispatch: out[rows[t][j]] = X[t]
+ *   combine:  Y[t] = bf16_rn(sum_j weights[t][j] * O[rows[t][j]]), FP32 sums in the
+ *             order of j; weights NULL: 1.
+ * Each is the other's gradient (combine without weights).  X, Y: tokens x hidden,
+ * out, O: capacity x hidden, BF16 with row pitches.  A place outside [0, capacity)
+ * is left out: dispatch writes no other rows, combine reads no other.
+ *  - Requires hidden and pitches % 8 == 0, 16-byte aligned matrices, topk <= 32. */
+tkg_status tkg_moe_dispatch(int tokens, int topk, int hidden, const void *X, int ldx, const int *rows, int capacity,
+                            void *out, int ldo, cudaStream_t stream);
+tkg_status tkg_moe_combine(int tokens, int topk, int hidden, const void *O, int ldo, int capacity, const int *rows,
+                           const float *weights, void *Y, int ldy, cudaStream_t stream);
+
+/* 8-bit checkpoints: rows kept for the backward pass as MXFP8 (the rule of
+ * tkg_quantize_mxfp8 applied to BF16 rows), codes Q (rows x k bytes) and scales sf
+ * (rows x k / 32 bytes), both row-major: a row can be read by itself.
+ * tkg_scales_to_tiled makes of sf what the MXFP8 GEMMs take.  Each value is off by
+ * at most 2^-4 of itself, or 2^-10 of the scale for small ones.
+ * Requires k % 32 == 0, ldx % 8 == 0, 16-byte aligned X and Q. */
+tkg_status tkg_checkpoint_mxfp8(int rows, int k, const void *X, int ldx, void *Q, void *sf, cudaStream_t stream);
+
+/* Gated activation of rows [g | u] (2 * inner columns, BF16):
+ *   H = bf16_rn(silu(g) * u), silu(x) = x / (1 + exp(-x))
+ * and, unless Q and sf are NULL, the checkpoint of [g | u] (rows x 2 inner).
+ * Requires inner % 8 == 0 (with a checkpoint inner % 32 == 0), pitches % 8 == 0. */
+tkg_status tkg_swiglu(int rows, int inner, const void *GU, int ldgu, void *H, int ldh, void *Q, void *sf,
+                      cudaStream_t stream);
+
+/* Its gradient, from the checkpoint.  Row r belongs to choice c = slots[r] (NULL:
+ * r) with router weight w = weights[c] (NULL: 1); dH is the gradient to h without
+ * the weight, dH[r] = dY[token] W2 (so no expert output has to be kept):
+ *   dGU[r] = w dH [u sigma(g) (1 + g (1 - sigma(g))) | silu(g)]
+ *   H[r]   = w silu(g) u      (or NULL; what the second product's gradient takes)
+ *   dweights[c] = sum over the columns of dH silu(g) u   (FP32, fixed order; or NULL)
+ * with g, u as saved.  Rows whose choice is outside [0, choices) are neither read
+ * nor written.  Requires inner % 32 == 0, pitches % 8 == 0. */
+tkg_status tkg_swiglu_grad(int rows, int inner, const void *Q, const void *sf, const void *dH, int lddh, const int *slots,
+                           int choices, const float *weights, void *dGU, int lddgu, void *H, int ldh, float *dweights,
+                           cudaStream_t stream);
+
+/* tkg_gemm_grouped_dev_bf16_wgrad with A's rows from a checkpoint of `tokens` rows
+ * (Q, sf): row r is that of token slots[r] / topk (slots NULL: r), so that one saved
+ * row serves all of its token's experts.  A row whose token is outside [0, tokens)
+ * adds nothing.  The values are exact in BF16.  slots: m_capacity of them.
+ * Requires k % 32 == 0; workspace as for tkg_linear_ce_loss. */
+tkg_status tkg_gemm_grouped_dev_mxfp8_wgrad(int groups, const int *m_sizes_dev, int m_capacity, int n, int k,
+                                            const void *dD, int tokens, const void *Q, const void *sf, const int *slots,
+                                            int topk, void *dB, tkg_grad_type type, float alpha, void *workspace,
+                                            size_t workspace_bytes, cudaStream_t stream);
+size_t tkg_gemm_grouped_dev_mxfp8_wgrad_workspace_bytes(int m_capacity, int k);
+
 /* Check builds.  `python -m dense_block_scaled_gb300.build --check` builds the
  * same library as libtkg_check.so with every kernel verifying its internal
  * invariants (tensor-memory column ranges of each MMA, scale copy and
