@@ -32,8 +32,8 @@ __global__ void __launch_bounds__(256) unpack_rows_kernel(int rows, int k, int t
   }
   uint4 w[2] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
   if (t >= 0 && t < tokens) {
-    const uint4 q = __ldg(reinterpret_cast<const uint4*>(Q + size_t(t) * size_t(k) + c));
-    const float s = e8m0_value(__ldg(sf + (size_t(t) * size_t(k) + c) / 32));
+    const uint4 q = __ldcg(reinterpret_cast<const uint4*>(Q + size_t(t) * size_t(k) + c));
+    const float s = e8m0_value(__ldcg(sf + (size_t(t) * size_t(k) + c) / 32));
     const uint32_t u[4] = {q.x, q.y, q.z, q.w};
     uint32_t* o = reinterpret_cast<uint32_t*>(w);
 #pragma unroll

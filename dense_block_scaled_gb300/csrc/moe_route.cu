@@ -8,31 +8,39 @@
 //   sizes_e = tokens that chose e;  rows(t, j) = place of (t, j) among all choices ordered by expert, then by token;
 //   slots(rows(t, j)) = t topk + j
 //
-// Two kernels.  route_choose_kernel: a warp per token, each lane a run of consecutive experts, so that the lowest lane
-// with a value also has the lowest index.  A choice is one integer maximum over the warp (redux) of keys that are
-// ordered as the values are.  Within a block of tokens, the rank of (t, e) is the number of earlier tokens that chose e:
-// a population count of one bit per token and expert.  The block leaves its ranks (in `rows`) and its count per expert.
-// route_place_kernel: adds what earlier blocks and experts have.  A single block of tokens does both at once.
-// Nothing depends on the order of atomics: those are integer sums and bit sets.
+// Two kernels.  route_choose_kernel: a warp per token, each lane a run of consecutive experts, sorted by value and index;
+// a choice is an integer maximum over the warp (redux) of keys that are ordered as the values are, a minimum of the
+// indices that have it, and a step along one lane's run.  Within a block of tokens, the rank of (t, e) is the number of
+// earlier tokens that chose e: a population count of one bit per token and expert.  The block leaves its ranks (in
+// `rows`) and its count per expert.  route_place_kernel: adds what earlier blocks and experts have.  A single block of
+// tokens does both at once.  Nothing depends on the order of atomics: those are bit sets.
 //
-// Without bias and groups the logits themselves decide (both scores rise with them).  Otherwise FP32 scores decide,
-// whose error is below the `near` of each value; where two neighbours around a choice are closer than that, and not of
-// the same logit and bias, the token is chosen again in 64 bits, so that the choice is that of the exact scores.
+// Without bias and groups the logits themselves decide (both scores rise with them).  Otherwise FP32 scores decide
+// wherever they are further apart than they can be wrong; where two around a choice are closer, and not of the same logit
+// and bias, the candidates are ordered again in 64 bits, so that the choice is that of the exact scores.
 #include "train_host.cuh"
 
 namespace tkg {
 namespace {
 
-constexpr int kRouteWarps = 16;            // per block
-constexpr int kRouteTokens = 32;           // tokens ranked at a time: one bit each
+// Warps per block: as many as the registers of a lane's run allow, for a token's choice is a long chain of short steps.
+template <int PER>
+constexpr int kRouteWarps = PER <= 8 ? 32 : 16;
+constexpr int kRouteWords = 4;             // 32 tokens each, ranked at a time
+constexpr int kRouteTokens = 32 * kRouteWords;
 constexpr int kMaxRouteExperts = 512, kMaxTopk = 32, kMaxRouteGroups = 32;
-constexpr int kRouteBlocks = 608;          // blocks of tokens at most (four per SM)
-constexpr int kPlaceBlocks = 64, kPlaceThreads = 512;
-constexpr int kPlaceEach = (kRouteBlocks + kPlaceBlocks - 1) / kPlaceBlocks;   // blocks of tokens per placing block
+constexpr int kRouteBlocks = 152;          // blocks of tokens at most: one per SM
+constexpr int kRouteAlone = 64;            // tokens at most that one block takes alone
+constexpr int kPlaceThreads = 512, kPlaceEach = 7;
+constexpr int kPlaceEntries = 1024;        // choices that a placing block takes, about
 
 struct RouteParams {
   int tokens, experts, topk;
-  int groups, per_group, topk_groups;
+  int groups, per_group, topk_groups, lanes_per_group;
+  uint32_t inverse;           // ceil(2^32 / per_group): e / per_group is the high word of e * inverse (e < 512)
+  __device__ __forceinline__ int group_of(int e) const {
+    return per_group == 1 ? e : int(__umulhi(uint32_t(e), inverse));
+  }
   int sigmoid, renormalise;
   float scale;
   const void* logits;
@@ -44,8 +52,8 @@ struct RouteParams {
   int* sizes;
   int* rows;
   int* slots;
-  int* counts;                // [blocks][experts]
-  int per_block;              // tokens, a multiple of kRouteTokens
+  uint16_t* counts;           // [blocks][experts, rounded up to 8]
+  int per_block;              // tokens, a multiple of 32
   int blocks;
 };
 
@@ -57,6 +65,10 @@ __device__ __forceinline__ uint32_t key_of(float x) {
 __device__ __forceinline__ unsigned long long key_of(double x) {
   const unsigned long long u = (unsigned long long)__double_as_longlong(x + 0.0);
   return x != x ? 1ull : ((u >> 63) ? ~u : u | (1ull << 63));
+}
+// The value of a key (0 for -0).
+__device__ __forceinline__ float value_of(uint32_t k) {
+  return __uint_as_float((k & 0x80000000u) ? k & 0x7fffffffu : (k == 1u ? 0x7fc00000u : ~k));
 }
 __device__ __forceinline__ uint32_t warp_max(uint32_t k) { return __reduce_max_sync(0xffffffffu, k); }
 __device__ __forceinline__ unsigned long long warp_max(unsigned long long k) {
@@ -74,6 +86,10 @@ __device__ __forceinline__ float warp_fmax(float x) {
 #pragma unroll
   for (int o = 16; o; o >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
   return x;
+}
+// (of numbers that are not negative)
+__device__ __forceinline__ float warp_most(float x) {
+  return __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(x)));
 }
 __device__ __forceinline__ float exp_of(float x) { return expf(x); }
 __device__ __forceinline__ double exp_of(double x) { return exp(x); }
@@ -122,236 +138,427 @@ __device__ __forceinline__ void load_run(const L* row, int lane, int experts, fl
   }
 }
 
-// Scores of a lane's run.
-template <int PER, typename F>
-__device__ __forceinline__ void scores(const float (&z)[PER], int lane, int experts, bool sigmoid, F (&s)[PER]) {
-  if (sigmoid) {
+// What is subtracted from a row's logits (their maximum, or 0 for a row of nothing but -inf).
+template <int PER>
+__device__ __forceinline__ float softmax_top(const float (&z)[PER]) {
+  float top = z[0];
 #pragma unroll
-    for (int i = 0; i < PER; ++i) s[i] = F(1) / (F(1) + exp_of(-F(z[i])));
+  for (int i = 1; i < PER; ++i) top = fmaxf(top, z[i]);
+  top = warp_fmax(top);
+  return top == -INFINITY ? 0.f : top;
+}
+// The exponentials of a lane's run and their sum over the row: 1 where all of them are 0.
+template <int PER, typename F, typename E>
+__device__ __forceinline__ F softmax_sum(const float (&z)[PER], int lane, int experts, float top, F (&e)[PER], E&& exponential) {
+  F sum = F(0);
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    e[i] = exponential(F(z[i]) - F(top));
+    sum += lane * PER + i < experts ? e[i] : F(0);
+  }
+  sum = warp_sum(sum);
+  return sum == F(0) ? F(1) : sum;
+}
+template <typename F>
+__device__ __forceinline__ F sigmoid_of(F z) { return F(1) / (F(1) + exp_of(-z)); }
+
+// Choice scores c = s + b of a lane's run, for the choice alone: in FP32 by approximate exponentials and quotients (a
+// correctly rounded quotient and exp took 20 instructions each).  `wrong`: what each may be off by.
+//   sigmoid, absolute, in units of 2^-24: 1 - s times s (at most 1/4) of ex2's 4 and of its argument's rounding, |z| s (1 - s)
+//     < 1/4; the sum's 1, the reciprocal's 2: together below 2^-21.
+//   softmax, in the same units of the largest score: ex2's 4 and, with x the distance to the largest logit, its argument's
+//     two roundings, 2 x e^-x < 1; of the sum, weighted by the scores, the same with sum 2 p x <= 2 log 512 < 13, and 21
+//     additions; the reciprocal's and the product's 3: together below 2^-18.
+//   The sum s + b is rounded (infinite biases are not).
+template <int PER>
+__device__ __forceinline__ void choice_scores(const RouteParams& p, const float (&z)[PER], const float* s_bias, int lane,
+                                              float most_bias, float (&c)[PER], float& wrong) {
+  float most;
+  auto bias = [&](int i) { return lane * PER + i < p.experts ? s_bias[lane * PER + i] : 0.f; };
+  auto reciprocal = [](float x) {
+    float r;
+    asm("rcp.approx.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+  };
+  if (p.sigmoid) {
+#pragma unroll
+    for (int i = 0; i < PER; ++i) c[i] = reciprocal(1.f + ptx::ex2(z[i] * -kLog2e)) + bias(i);
+    most = 1.f;
+    wrong = 0x1p-21f;
   } else {
-    float top = z[0];
+    float e[PER];
+    const float sum = softmax_sum(z, lane, p.experts, softmax_top(z), e, [](float x) { return ptx::ex2(x * kLog2e); });
+    most = reciprocal(sum);
 #pragma unroll
-    for (int i = 1; i < PER; ++i) top = fmaxf(top, z[i]);
-    top = warp_fmax(top);
-    const F sub = top == -INFINITY ? F(0) : F(top);   // (a row of nothing but -inf has scores 0)
-    F sum = F(0);
+    for (int i = 0; i < PER; ++i) c[i] = fmaf(e[i], most, bias(i));
+    wrong = most * 0x1p-18f;
+  }
+  wrong += (most + most_bias) * 0x1p-24f;
+}
+template <int PER>
+__device__ __forceinline__ void choice_scores(const RouteParams& p, const float (&z)[PER], const float (&bias)[PER], int lane,
+                                              double (&c)[PER]) {
+  if (p.sigmoid) {
 #pragma unroll
-    for (int i = 0; i < PER; ++i) {
-      s[i] = exp_of(F(z[i]) - sub);
-      sum += lane * PER + i < experts ? s[i] : F(0);
-    }
-    sum = warp_sum(sum);
-    if (sum == F(0)) sum = F(1);
+    for (int i = 0; i < PER; ++i) c[i] = sigmoid_of(double(z[i])) + double(bias[i]);
+  } else {
+    const double sum = softmax_sum(z, lane, p.experts, softmax_top(z), c, [](double x) { return exp(x); });
 #pragma unroll
-    for (int i = 0; i < PER; ++i) s[i] /= sum;
+    for (int i = 0; i < PER; ++i) c[i] = c[i] / sum + double(bias[i]);
   }
 }
 
-// What may be wrong with an FP32 score, relative to it.  sigmoid: exp's and the quotient's errors and the sum's rounding,
-// a few 2^-24.  softmax: the difference to the largest logit, at most 88 where the score is not 0, is rounded to 2^-24
-// of itself and stands in the exponent: 2^-17.5, and the same few.
-__device__ __forceinline__ float wrong_of(bool sigmoid) { return sigmoid ? 0x1p-20f : 0x1p-16f; }
-// ... and, in all, with a choice score c = s + b, whose sum is rounded.
-__device__ __forceinline__ float near_of(float c, float s, bool sigmoid) {
-  return s * wrong_of(sigmoid) + fabsf(c) * 0x1p-22f;
+// The larger and the smaller of two keys with their indices (ties: the lower index is the larger).
+template <typename K>
+__device__ __forceinline__ void order_two(K& a, int& ia, K& b, int& ib) {
+  const bool swap = b > a || (b == a && ib < ia);
+  const K k = swap ? a : b;
+  const int i = swap ? ia : ib;
+  a = swap ? b : a;
+  ia = swap ? ib : ia;
+  b = k;
+  ib = i;
+}
+// Batcher's odd-even merge sort: calls order(a, b) for places a < b of a lane's run.
+template <int PER, typename O>
+__device__ __forceinline__ void sort_places(O&& order) {
+#pragma unroll
+  for (int p = 1; p < PER; p *= 2)
+#pragma unroll
+    for (int k = p; k >= 1; k /= 2)
+#pragma unroll
+      for (int j = k % p; j + k < PER; j += 2 * k)
+#pragma unroll
+        for (int i = 0; i < k; ++i)
+          if (i + j + k < PER && (i + j) / (2 * p) == (i + j + k) / (2 * p)) order(i + j, i + j + k);
+}
+template <int PER, typename K>
+__device__ __forceinline__ void sort_run(K (&key)[PER], int (&at)[PER]) {
+  sort_places<PER>([&](int a, int b) { order_two(key[a], at[a], key[b], at[b]); });
+}
+template <int PER>
+__device__ __forceinline__ void sort_run(uint32_t (&key)[PER]) {
+  sort_places<PER>([&](int a, int b) {
+    const uint32_t x = max(key[a], key[b]);
+    key[b] = min(key[a], key[b]);
+    key[a] = x;
+  });
 }
 
-// The choice of a token by values c (a lane's run; NaN last): lane j < topk gets the j-th expert.  `exact` is cleared
-// where FP32 values do not decide.  `box`: per warp, for the groups.
-template <int PER, typename F>
-__device__ __forceinline__ int choose(const RouteParams& p, const float (&z)[PER], const F (&s)[PER], const F (&c)[PER],
-                                      bool by_logit, int lane, F* box, bool& exact) {
-  using K = decltype(key_of(F(0)));
-  constexpr bool kCheck = sizeof(F) == 4;
-  K key[PER];
+// Clears the keys of experts outside the best groups; false where the values do not decide between two groups.  Each
+// group has `per` lanes, its first keeps its value; `box` (a row per warp) carries the values to them.
+template <int PER, typename F, typename K>
+__device__ __forceinline__ bool keep_groups(const RouteParams& p, const F (&c)[PER], K (&key)[PER], float wrong, int lane,
+                                            F* box) {
+  __syncwarp();
 #pragma unroll
-  for (int i = 0; i < PER; ++i) key[i] = lane * PER + i < p.experts ? key_of(c[i]) : K(0);
-  if (p.topk_groups < p.groups) {
-    __syncwarp();
-#pragma unroll
-    for (int i = 0; i < PER; ++i) {
-      const int e = lane * PER + i;
-      if (e < p.experts) box[e + e / 32] = c[i];
-    }
-    __syncwarp();
-    // lane g: its group's two largest
-    F a = -INFINITY, b = -INFINITY;
-    bool lost = false;   // (NaN)
-    if (lane < p.groups) {
+  for (int i = 0; i < PER; ++i) {
+    const int e = lane * PER + i;
+    if (e < p.experts) box[e + e / 32] = c[i];
+  }
+  __syncwarp();
+  const int per = p.lanes_per_group, shift = __popc(per - 1);
+  const int g = lane >> shift;
+  F a = -INFINITY, b = -INFINITY;   // the two largest
+  int lost = 0;                     // (NaN)
+  if (g < p.groups) {
+    int e = g * p.per_group + (lane & (per - 1));
+    const int end = (g + 1) * p.per_group;
 #pragma unroll 4
-      for (int i = 0; i < p.per_group; ++i) {
-        const int e = lane * p.per_group + i;
-        const F x = box[e + e / 32];
-        lost |= x != x;
-        b = x > a ? a : (x > b ? x : b);
-        a = x > a ? x : a;
-      }
-    }
-    const F sum = p.per_group > 1 ? (lost ? F(NAN) : a + b) : (lost ? F(NAN) : a);
-    K mine = lane < p.groups ? key_of(sum) : K(0);
-    uint32_t stay = 0;
-    F last = F(0);
-#pragma unroll 1
-    for (int g = 0; g <= p.topk_groups; ++g) {
-      const K m = warp_max(mine);
-      const int at = __ffs(int(__ballot_sync(0xffffffffu, mine == m))) - 1;
-      const F v = __shfl_sync(0xffffffffu, sum, at);
-      if (g == p.topk_groups) {
-        // (the four scores in them: with a bias not known here, at most 4, or 1 of softmax)
-        if constexpr (kCheck) {
-          const float both = fabsf(v) + fabsf(last);
-          const float sums = p.bias ? (p.sigmoid ? 4.f : 1.f) : both;
-          if (fabsf(last - v) <= sums * wrong_of(p.sigmoid != 0) + both * 0x1p-21f) exact = false;
-        }
-        break;
-      }
-      last = v;
-      stay |= 1u << at;
-      if (lane == at) mine = K(0);
-    }
-#pragma unroll
-    for (int i = 0; i < PER; ++i) {
-      const int e = lane * PER + i;
-      if (e < p.experts && !((stay >> (e / p.per_group)) & 1u)) key[i] = K(0);
+    for (; e < end; e += per) {
+      const F x = box[e + e / 32];
+      lost |= x != x;
+      const F low = x > a ? a : x;
+      a = x > a ? x : a;
+      b = low > b ? low : b;
     }
   }
-  int id = 0;
-  float prev_c = 0.f, prev_z = 0.f, prev_b = 0.f, prev_s = 0.f;
-  K top = key[0];
-#pragma unroll
-  for (int i = 1; i < PER; ++i) top = key[i] > top ? key[i] : top;
-  // one more than topk where neighbours are to be compared
-  const int picks = kCheck && !by_logit ? p.topk + 1 : p.topk;
 #pragma unroll 1
-  for (int j = 0; j < picks; ++j) {
-    const K m = warp_max(top);
-    if (m == K(0)) break;   // (no expert is left to compare with)
-    const int at = __ffs(int(__ballot_sync(0xffffffffu, top == m))) - 1;
-    int which = 0;
+  for (int o = 1; o < per; o *= 2) {
+    const F c2 = __shfl_xor_sync(0xffffffffu, a, o), d2 = __shfl_xor_sync(0xffffffffu, b, o);
+    lost |= __shfl_xor_sync(0xffffffffu, lost, o);
+    const F low = c2 > a ? a : c2, high = d2 > b ? d2 : b;
+    a = c2 > a ? c2 : a;
+    b = low > high ? low : high;
+  }
+  const bool holds = g < p.groups && (lane & (per - 1)) == 0;
+  const F sum = lost ? F(NAN) : (p.per_group > 1 ? a + b : a);
+  const K mine = holds ? key_of(sum) : K(0);
+  int rank = 0;   // groups before this one
+#pragma unroll 4
+  for (int o = 0; o < p.groups; ++o) {
+    const K other = __shfl_sync(0xffffffffu, mine, o << shift);
+    rank += other > mine || (other == mine && o < g) ? 1 : 0;
+  }
+  const uint32_t stay = __ballot_sync(0xffffffffu, holds && rank < p.topk_groups);
+  int of = p.group_of(lane * PER), left = (of + 1) * p.per_group - lane * PER;   // a run's groups
 #pragma unroll
-    for (int i = PER - 1; i >= 0; --i)
-      if (key[i] == m) which = i;
-    const int e = __shfl_sync(0xffffffffu, lane * PER + which, at);
-    if (lane == j) id = e;
-    if (lane == at) {
-      top = K(0);
+  for (int i = 0; i < PER; ++i) {
+    if (left == 0) {
+      ++of;
+      left = p.per_group;
+    }
+    --left;
+    if (lane * PER + i < p.experts && !((stay >> (of << shift)) & 1u)) key[i] = K(0);
+  }
+  // the last group that stays and the first that goes: each sum of two is off by both's error and its rounding
+  const uint32_t in = __ballot_sync(0xffffffffu, holds && rank == p.topk_groups - 1);
+  const uint32_t out = __ballot_sync(0xffffffffu, holds && rank == p.topk_groups);
+  const F last = __shfl_sync(0xffffffffu, sum, __ffs(int(in)) - 1), first = __shfl_sync(0xffffffffu, sum, __ffs(int(out)) - 1);
+  return float(last - first) > 4.f * wrong + (fabsf(float(last)) + fabsf(float(first))) * 0x1p-24f;
+}
+
+template <typename L>
+__device__ __forceinline__ float logit_at(const RouteParams& p, int t, int e) {
+  const L* row = static_cast<const L*>(p.logits) + size_t(t) * p.ld;
+  if constexpr (sizeof(L) == 4)
+    return __ldcg(reinterpret_cast<const float*>(row) + e);
+  else
+    return __uint_as_float(uint32_t(__ldcg(reinterpret_cast<const unsigned short*>(row) + e)) << 16);
+}
+__device__ __forceinline__ float bias_at(const RouteParams& p, int e) { return p.bias ? __ldcg(p.bias + e) : 0.f; }
+
+// The order of n candidates (lane j < n: expert id) by their exact scores; lane j gets the j-th.  Rare: kept out of the
+// way of the registers of the rest.
+template <typename L>
+__device__ __noinline__ int order_again(const RouteParams& p, int t, int n, int id, int lane) {
+  double c = 0.0;
+  const float z = lane < n ? logit_at<L>(p, t, id) : 0.f;
+  const float b = lane < n ? bias_at(p, id) : 0.f;
+  if (p.sigmoid) {
+    c = sigmoid_of(double(z)) + double(b);
+  } else {
+    float top = -INFINITY;
+    for (int e = lane; e < p.experts; e += 32) top = fmaxf(top, logit_at<L>(p, t, e));
+    top = warp_fmax(top);
+    const double sub = top == -INFINITY ? 0.0 : double(top);
+    double sum = 0.0;
+    for (int e = lane; e < p.experts; e += 32) sum += exp(double(logit_at<L>(p, t, e)) - sub);
+    sum = warp_sum(sum);
+    c = exp(double(z) - sub) / (sum == 0.0 ? 1.0 : sum) + double(b);
+  }
+  const unsigned long long mine = key_of(c);
+  int rank = 0, out = 0;
+#pragma unroll 1
+  for (int i = 0; i < n; ++i) {
+    const unsigned long long other = __shfl_sync(0xffffffffu, mine, i);
+    const int e = __shfl_sync(0xffffffffu, id, i);
+    rank += other > mine || (other == mine && e < id) ? 1 : 0;
+  }
+#pragma unroll 1
+  for (int i = 0; i < n; ++i) {
+    const int r = __shfl_sync(0xffffffffu, rank, i), e = __shfl_sync(0xffffffffu, id, i);
+    if (r == lane) out = e;
+  }
+  return out;
+}
+
+// The choice of token t by values c (a lane's run; NaN last), each off by at most `wrong` (negative: exact): lane j < topk
+// gets the j-th expert and, where the values are its logits, `value` its logit.  -1 in all lanes where the values do not
+// decide between groups, or between more than 32 candidates (the caller then asks with 64 bits).
+template <int PER, typename L, typename F>
+__device__ __forceinline__ int choose(const RouteParams& p, int t, const F (&c)[PER], float wrong, int lane, F* box,
+                                      float& value) {
+  using K = decltype(key_of(F(0)));
+  const bool sure = wrong < 0.f;
+  K key[PER];
+  int at[PER];
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    key[i] = lane * PER + i < p.experts ? key_of(c[i]) : K(0);
+    at[i] = lane * PER + i;
+  }
+  if (p.topk_groups < p.groups && !keep_groups(p, c, key, wrong, lane, box) && !sure) return -1;
+  sort_run(key, at);
+  int id = 0, j = 0, picks = p.topk;
+  K mine = K(0), last = K(0);
+  bool close = false;   // two of the chosen are too near, or (below) one of the rest is to the last of them
+  auto same = [&](int a, int b) {   // of the same logit and bias, so of the same score
+    return logit_at<L>(p, t, a) == logit_at<L>(p, t, b) && bias_at(p, a) == bias_at(p, b);
+  };
+  int e = 0;
+#pragma unroll 1
+  for (;;) {
+#pragma unroll 1
+    for (; j < picks; ++j) {
+      const K m = warp_max(key[0]);
+      const int before = e;
+      e = int(__reduce_min_sync(0xffffffffu, key[0] == m ? uint32_t(at[0]) : 0xffffffffu));
+      if (lane == j) {
+        id = e;
+        mine = m;
+      }
+      if (!sure && j > 0) {
+        if constexpr (sizeof(K) == 4)
+          if (!(value_of(last) - value_of(m) > 2.f * wrong) && !same(before, e)) close = true;
+      }
+      last = m;
+      const bool step = at[0] == e && key[0] == m;
 #pragma unroll
       for (int i = 0; i < PER; ++i) {
-        if (i == which) key[i] = K(0);
-        top = key[i] > top ? key[i] : top;
+        key[i] = step ? (i + 1 < PER ? key[i + 1 < PER ? i + 1 : 0] : K(0)) : key[i];
+        at[i] = step && i + 1 < PER ? at[i + 1 < PER ? i + 1 : 0] : at[i];
       }
     }
-    if constexpr (kCheck) {
-      if (!by_logit) {
-        float cc = c[0], zz = z[0], ss = s[0];
+    if (sure || picks > p.topk) break;
+    if constexpr (sizeof(K) == 4) {
+      // Of the rest, those near the last of the chosen may belong before it.  (One of the same logit and bias as the
+      // last does not, unless the chosen are ordered again.)
+      const K least = key_of(value_of(last) - 2.f * wrong);
+      if (!__any_sync(0xffffffffu, key[0] != K(0) && key[0] >= least)) break;
+      int near = 0;
+      bool other = close;
 #pragma unroll
-        for (int i = 1; i < PER; ++i)
-          if (which == i) cc = c[i], zz = z[i], ss = s[i];
-        cc = __shfl_sync(0xffffffffu, cc, at);
-        zz = __shfl_sync(0xffffffffu, zz, at);
-        ss = __shfl_sync(0xffffffffu, ss, at);
-        const float bb = p.bias ? __ldg(p.bias + e) : 0.f;
-        if (j > 0 && !(prev_c - cc > near_of(prev_c, prev_s, p.sigmoid != 0) + near_of(cc, ss, p.sigmoid != 0)) && !(zz == prev_z && bb == prev_b))
-          exact = false;
-        prev_c = cc, prev_z = zz, prev_b = bb, prev_s = ss;
-      }
+      for (int i = 0; i < PER; ++i)
+        if (key[i] != K(0) && key[i] >= least) {
+          ++near;
+          other |= !same(e, at[i]);
+        }
+      if (!__any_sync(0xffffffffu, other)) break;
+      close = true;
+      picks = p.topk + __reduce_add_sync(0xffffffffu, near);
+      if (picks > 32) return -1;
     }
+  }
+  if constexpr (sizeof(K) == 4) {
+    if (close) id = order_again<L>(p, t, j, id, lane);
+    value = value_of(mine);
   }
   return id;
 }
 
-// The same in 64 bits: rare, and kept out of the way of the registers of the rest.
+// The choice by BF16 logits: key and index share a word, so that one maximum gives both.
 template <int PER>
-__device__ __noinline__ int choose_again(const RouteParams& p, const float* z_in, int lane, double* box) {
-  float z[PER];
-  double s[PER], c[PER];
-#pragma unroll
-  for (int i = 0; i < PER; ++i) z[i] = z_in[i];
-  scores(z, lane, p.experts, p.sigmoid != 0, s);
+__device__ __forceinline__ int choose_packed(const RouteParams& p, const float (&z)[PER], int lane, float& value) {
+  uint32_t key[PER];
 #pragma unroll
   for (int i = 0; i < PER; ++i) {
     const int e = lane * PER + i;
-    c[i] = s[i] + (p.bias && e < p.experts ? double(__ldg(p.bias + e)) : 0.0);
+    const uint32_t k = z[i] != z[i] ? 1u : key_of(z[i]) >> 16;   // (-inf has 0x7f)
+    key[i] = e < p.experts ? (k << 16) | uint32_t(0xffff - e) : 0u;
   }
-  bool exact = true;
-  return choose(p, z, s, c, false, lane, box, exact);
+  sort_run(key);
+  int id = 0;
+  uint32_t mine = 0;
+#pragma unroll 1
+  for (int j = 0; j < p.topk; ++j) {
+    const uint32_t m = warp_max(key[0]);
+    if (lane == j) mine = m;
+    const bool step = key[0] == m;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) key[i] = step ? (i + 1 < PER ? key[i + 1 < PER ? i + 1 : 0] : 0u) : key[i];
+  }
+  id = lane < p.topk ? int(0xffffu - (mine & 0xffffu)) : 0;
+  const uint32_t k = mine >> 16;
+  value = __uint_as_float((k & 0x8000u) ? (k & 0x7fffu) << 16 : (k == 1u ? 0x7fc00000u : (~k & 0xffffu) << 16));
+  return id;
 }
 
-template <int PER, typename L, bool WIDE>
-__global__ void __launch_bounds__(32 * kRouteWarps) route_choose_kernel(const RouteParams p) {
+// The same by all scores in 64 bits: rare too.
+template <int PER, typename L>
+__device__ __noinline__ int choose_again(const RouteParams& p, int t, int lane, double* box) {
+  float z[PER], bias[PER], unused;
+  double c[PER];
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    const int e = lane * PER + i;
+    z[i] = e < p.experts ? logit_at<L>(p, t, e) : -INFINITY;
+    bias[i] = e < p.experts ? bias_at(p, e) : 0.f;
+  }
+  choice_scores(p, z, bias, lane, c);
+  return choose<PER, L>(p, t, c, -1.f, lane, box, unused);
+}
+
+// BY_LOGIT: no bias and no limit to groups.
+template <int PER, typename L, bool WIDE, bool BY_LOGIT>
+__global__ void __launch_bounds__(32 * kRouteWarps<PER>) route_choose_kernel(const RouteParams p) {
   extern __shared__ int s_dyn[];
-  // bits of the tokens that chose an expert, how many did before, and, for the groups, a row of values per warp
-  uint32_t* s_bits = reinterpret_cast<uint32_t*>(s_dyn);
-  int* s_count = s_dyn + p.experts;
-  int* s_first = s_count + p.experts;   // (one block of tokens: each expert's first row)
-  __shared__ int s_ids[kRouteTokens * kMaxTopk];
+  // bits of the tokens that chose an expert, how many did before, each expert's first row (one block of tokens), and, for
+  // the groups, a row of values per warp
+  uint32_t* s_bits = reinterpret_cast<uint32_t*>(s_dyn);   // [experts][kRouteWords]
+  int* s_count = s_dyn + p.experts * kRouteWords;
   __shared__ int s_total;
   ptx::pdl_launch_dependents();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  double* box = reinterpret_cast<double*>(s_dyn + (3 * p.experts + 1) / 2 * 2) + warp * (p.experts + p.experts / 32 + 1);
+  float* s_bias = reinterpret_cast<float*>(s_count + p.experts);
+  int* s_ids = s_count + 2 * p.experts;                      // [kRouteTokens][topk]
+  const int tokens_there = min(kRouteTokens, p.per_block), warps = blockDim.x >> 5;
+  double* box = reinterpret_cast<double*>(s_dyn + (p.experts * (kRouteWords + 2) + tokens_there * p.topk + 1) / 2 * 2) +
+                warp * (p.experts + p.experts / 32 + 1);
   for (int e = threadIdx.x; e < p.experts; e += blockDim.x) s_count[e] = 0;
-  const bool by_logit = !p.bias && p.topk_groups == p.groups;
   const int begin = blockIdx.x * p.per_block, end = min(p.tokens, begin + p.per_block);
+  float most_bias = 0.f;   // the largest that takes a rounding
+  if constexpr (!BY_LOGIT) {
+    ptx::pdl_wait();
+    // (through shared memory: 32 warps' runs straight from L2 are 32 times its sectors, all the same ones, 20 us)
+    for (int e = threadIdx.x; e < p.experts; e += blockDim.x) s_bias[e] = bias_at(p, e);
+    __syncthreads();
+    for (int e = lane; e < p.experts; e += 32) {
+      const float b = fabsf(s_bias[e]);
+      if (b < INFINITY) most_bias = fmaxf(most_bias, b);
+    }
+    most_bias = warp_most(most_bias);
+  }
   ptx::pdl_wait();
+  auto rank_of = [&](int e, int i) {   // tokens of this chunk before i that chose e
+    int n = __popc(s_bits[e * kRouteWords + (i >> 5)] & ((1u << (i & 31)) - 1u));
+    for (int w = 0; w < (i >> 5); ++w) n += __popc(s_bits[e * kRouteWords + w]);
+    return n;
+  };
+  auto count_of = [&](int e) {
+    int n = 0;
+#pragma unroll
+    for (int w = 0; w < kRouteWords; ++w) n += __popc(s_bits[e * kRouteWords + w]);
+    return n;
+  };
 #pragma unroll 1
   for (int t0 = begin; t0 < end; t0 += kRouteTokens) {
     const int there = min(kRouteTokens, end - t0);
-    for (int e = threadIdx.x; e < p.experts; e += blockDim.x) s_bits[e] = 0;
+    for (int e = threadIdx.x; e < p.experts * kRouteWords; e += blockDim.x) s_bits[e] = 0;
     __syncthreads();
 #pragma unroll 1
-    for (int i = warp; i < there; i += kRouteWarps) {
+    for (int i = warp; i < there; i += warps) {
       const int t = t0 + i;
       const bool kept = !p.keep || __ldcg(p.keep + t) != 0;
       int id = -1;
       float w = 0.f;
       if (kept) {
-        float z[PER];
+        float z[PER], zj = 0.f, sub = 0.f, sum = 1.f;
         load_run<PER, L, WIDE>(static_cast<const L*>(p.logits) + size_t(t) * p.ld, lane, p.experts, z);
-        bool exact = true;
-        float s[PER];
-        if (by_logit) {
-          if (!p.renormalise || p.sigmoid) {
-            scores(z, lane, p.experts, p.sigmoid != 0, s);
-          } else {
-#pragma unroll
-            for (int k = 0; k < PER; ++k) s[k] = 0.f;   // (not needed)
-          }
-          id = choose(p, z, s, z, true, lane, reinterpret_cast<float*>(box), exact);
+        if (!p.sigmoid && !p.renormalise) {
+          float e[PER];
+          sub = softmax_top(z);
+          sum = softmax_sum(z, lane, p.experts, sub, e, [](float x) { return expf(x); });
+        }
+        if constexpr (BY_LOGIT && sizeof(L) == 2) {
+          id = choose_packed(p, z, lane, zj);
+        } else if constexpr (BY_LOGIT) {
+          id = choose<PER, L>(p, t, z, -1.f, lane, reinterpret_cast<float*>(box), zj);
         } else {
-          float c[PER];
-          scores(z, lane, p.experts, p.sigmoid != 0, s);
-#pragma unroll
-          for (int k = 0; k < PER; ++k) {
-            const int e = lane * PER + k;
-            c[k] = s[k] + (p.bias && e < p.experts ? __ldg(p.bias + e) : 0.f);
-          }
-          id = choose(p, z, s, c, false, lane, reinterpret_cast<float*>(box), exact);
-          if (!exact) {
-            float again[PER];
-#pragma unroll
-            for (int k = 0; k < PER; ++k) again[k] = z[k];
-            id = choose_again<PER>(p, again, lane, box);
-          }
+          float c[PER], wrong;
+          choice_scores(p, z, s_bias, lane, most_bias, c, wrong);
+          id = choose<PER, L>(p, t, c, wrong, lane, reinterpret_cast<float*>(box), zj);
+          if (__shfl_sync(0xffffffffu, id, 0) < 0) id = choose_again<PER, L>(p, t, lane, box);
+          zj = logit_at<L>(p, t, id);
         }
-        // lane j: its expert's logit and score, from the lane that holds them
-        const int from = id / PER, which = id % PER;
-        float zj = 0.f, sj = 0.f;
-#pragma unroll
-        for (int k = 0; k < PER; ++k) {
-          const float a = __shfl_sync(0xffffffffu, z[k], from), b = __shfl_sync(0xffffffffu, s[k], from);
-          if (which == k) zj = a, sj = b;
-        }
+        // lane j: its expert's score
         const bool mine = lane < p.topk;
-        if (p.renormalise) {
-          if (!p.sigmoid) {   // relative to the largest of the chosen: none of them is lost
-            const float top = warp_fmax(mine ? zj : -INFINITY);
-            sj = expf(zj - (top == -INFINITY ? 0.f : top));
+        if (p.sigmoid) {
+          w = sigmoid_of(zj);
+        } else {
+          if (p.renormalise) {   // relative to the largest of the chosen: none of them is lost
+            sub = warp_fmax(mine ? zj : -INFINITY);
+            if (sub == -INFINITY) sub = 0.f;
           }
-          const float sum = warp_sum(mine ? sj : 0.f);
-          sj = sum == 0.f ? 0.f : __fdiv_rn(sj, sum);
+          w = expf(zj - sub);
+          if (!p.renormalise) w = __fdiv_rn(w, sum);
         }
-        w = sj * p.scale;
-        if (mine) atomicOr(s_bits + id, 1u << i);
+        if (p.renormalise) {
+          const float all = warp_sum(mine ? w : 0.f);
+          w = all == 0.f ? 0.f : __fdiv_rn(w, all);
+        }
+        w *= p.scale;
+        if (mine) atomicOr(s_bits + id * kRouteWords + (i >> 5), 1u << (i & 31));
       }
       if (lane < p.topk) {
         s_ids[i * p.topk + lane] = id;
@@ -363,24 +570,25 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_choose_kernel(const Ro
     // ranks within the block of tokens
     if (p.blocks > 1) {
       for (int i = threadIdx.x; i < there * p.topk; i += blockDim.x) {
-        const int e = s_ids[i], t = i / p.topk;
-        p.rows[size_t(t0) * p.topk + i] = e < 0 ? -1 : s_count[e] + __popc(s_bits[e] & ((1u << t) - 1u));
+        const int e = s_ids[i];
+        p.rows[size_t(t0) * p.topk + i] = e < 0 ? -1 : s_count[e] + rank_of(e, i / p.topk);
       }
       __syncthreads();
-      for (int e = threadIdx.x; e < p.experts; e += blockDim.x) s_count[e] += __popc(s_bits[e]);
+      for (int e = threadIdx.x; e < p.experts; e += blockDim.x) s_count[e] += count_of(e);
+      __syncthreads();
     }
   }
   if (p.blocks > 1) {
-    __syncthreads();
-    for (int e = threadIdx.x; e < p.experts; e += blockDim.x)
-      p.counts[size_t(blockIdx.x) * p.experts + e] = s_count[e];
+    const int width = (p.experts + 7) / 8 * 8;
+    for (int e = threadIdx.x; e < width; e += blockDim.x)
+      p.counts[size_t(blockIdx.x) * width + e] = uint16_t(e < p.experts ? s_count[e] : 0);
     return;
   }
   // the only block, with all of the tokens' bits
   if (warp == 0) {
     int carry = 0;
     for (int e0 = 0; e0 < p.experts; e0 += 32) {
-      const int e = e0 + lane, n = e < p.experts ? __popc(s_bits[e]) : 0;
+      const int e = e0 + lane, n = e < p.experts ? count_of(e) : 0;
       int x = n;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -388,7 +596,7 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_choose_kernel(const Ro
         if (lane >= o) x += y;
       }
       if (e < p.experts) {
-        s_first[e] = carry + x - n;
+        s_count[e] = carry + x - n;
         p.sizes[e] = n;
       }
       carry += __shfl_sync(0xffffffffu, x, 31);
@@ -398,82 +606,118 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_choose_kernel(const Ro
   __syncthreads();
   const int all = p.tokens * p.topk;
   for (int i = threadIdx.x; i < all; i += blockDim.x) {
-    const int e = s_ids[i], t = i / p.topk;
-    const int row = e < 0 ? -1 : s_first[e] + __popc(s_bits[e] & ((1u << t) - 1u));
+    const int e = s_ids[i];
+    const int row = e < 0 ? -1 : s_count[e] + rank_of(e, i / p.topk);
     p.rows[i] = row;
     if (row >= 0) p.slots[row] = i;
     if (i >= s_total) p.slots[i] = -1;
   }
 }
 
-// Block b places the choices of the blocks of tokens [b each, (b + 1) each).
+// Block b places the choices of the blocks of tokens [b each, (b + 1) each).  It adds up all counts itself: 16-byte loads
+// of 8 experts, all of a thread's on their way at once.
 __global__ void __launch_bounds__(kPlaceThreads) route_place_kernel(const RouteParams p, int each) {
-  extern __shared__ int s_base[];       // [each][experts]: first row of an expert's choices of a block of tokens
-  __shared__ int s_total[kMaxRouteExperts], s_before[kMaxRouteExperts];
-  __shared__ int s_all;
+  // sums of a thread's counts: of all blocks, and of the earlier ones; then [each][experts]: first row of an expert's
+  // choices of a block of tokens
+  __shared__ __align__(16) int s_part[2][kPlaceThreads * 8];
+  __shared__ int s_warp[kPlaceThreads / 32];
+  int* s_base = s_part[0];
+  static_assert(kMaxRouteExperts <= kPlaceThreads, "a thread per expert");
+  static_assert(kPlaceEach * kMaxRouteExperts <= 2 * kPlaceThreads * 8, "the first rows fit in the sums' place");
   ptx::pdl_launch_dependents();
   const int first = blockIdx.x * each, mine = min(each, p.blocks - first);
   const int lane = threadIdx.x & 31;
-  for (int e = threadIdx.x; e < p.experts; e += kPlaceThreads) s_total[e] = s_before[e] = 0;
-  ptx::pdl_wait();
-  __syncthreads();
-  // all counts, in pieces of rows: threads of a piece take neighbouring experts
-  const int width = (p.experts + 31) / 32 * 32, pieces = max(1, kPlaceThreads / width);
-  for (int x = threadIdx.x; x < width * pieces; x += kPlaceThreads) {
-    const int e = x % width, piece = x / width;
-    if (e >= p.experts) continue;
-    int total = 0, before = 0;
-#pragma unroll 8
-    for (int b = piece; b < p.blocks; b += pieces) {
-      const int n = __ldcg(p.counts + size_t(b) * p.experts + e);
-      total += n;
-      before += b < first ? n : 0;
-      if (b >= first && b < first + mine) s_base[(b - first) * p.experts + e] = n;
-    }
-    atomicAdd(s_total + e, total);
-    atomicAdd(s_before + e, before);
-  }
-  __syncthreads();
-  if (threadIdx.x < 32) {
-    int carry = 0;
-    for (int e0 = 0; e0 < p.experts; e0 += 32) {
-      const int e = e0 + lane, n = e < p.experts ? s_total[e] : 0;
-      int x = n;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int y = __shfl_up_sync(0xffffffffu, x, o);
-        if (lane >= o) x += y;
-      }
-      if (e < p.experts) {
-        s_before[e] += carry + x - n;
-        if (blockIdx.x == 0) p.sizes[e] = n;
-      }
-      carry += __shfl_sync(0xffffffffu, x, 31);
-    }
-    if (lane == 0) s_all = carry;
-  }
-  __syncthreads();
-  for (int e = threadIdx.x; e < p.experts; e += kPlaceThreads) {
-    int row = s_before[e];
-    for (int b = 0; b < mine; ++b) {
-      const int n = s_base[b * p.experts + e];
-      s_base[b * p.experts + e] = row;
-      row += n;
-    }
-  }
-  __syncthreads();
+  const int vecs = (p.experts + 7) / 8, groups = kPlaceThreads / vecs;
+  const int vec = threadIdx.x % vecs, group = threadIdx.x / vecs;
+  int total[8] = {}, before[8] = {};
   const long long begin = (long long)first * p.per_block * p.topk;
   const long long end = min((long long)p.tokens, (long long)(first + mine) * p.per_block) * p.topk;
   const int per = p.per_block * p.topk;
-  for (long long i = begin + threadIdx.x; i < end; i += kPlaceThreads) {
-    const int e = __ldcg(p.ids + i);
+  ptx::pdl_wait();
+  // a thread's first choices and its expert's counts in the block's own blocks of tokens, on their way with the rest
+  constexpr int kAhead = 4;
+  int ahead_id[kAhead], ahead_rank[kAhead], own[kPlaceEach];
+#pragma unroll
+  for (int a = 0; a < kAhead; ++a) {
+    const long long i = begin + threadIdx.x + a * kPlaceThreads;
+    ahead_id[a] = i < end ? __ldcg(p.ids + i) : -1;
+    ahead_rank[a] = i < end ? __ldcg(p.rows + i) : 0;
+  }
+  const int mine_e = threadIdx.x;
+#pragma unroll
+  for (int b = 0; b < kPlaceEach; ++b)
+    own[b] = b < mine && mine_e < p.experts ? int(__ldcg(p.counts + size_t(first + b) * (vecs * 8) + mine_e)) : 0;
+  if (group < groups) {
+#pragma unroll 8
+    for (int b = group; b < p.blocks; b += groups) {
+      const uint4 v = __ldcg(reinterpret_cast<const uint4*>(p.counts) + size_t(b) * vecs + vec);
+      const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int lo = int(u[i] & 0xffffu), hi = int(u[i] >> 16);
+        total[2 * i] += lo;
+        total[2 * i + 1] += hi;
+        before[2 * i] += b < first ? lo : 0;
+        before[2 * i + 1] += b < first ? hi : 0;
+      }
+    }
+    int4* to = reinterpret_cast<int4*>(&s_part[0][(group * vecs + vec) * 8]);
+    to[0] = make_int4(total[0], total[1], total[2], total[3]);
+    to[1] = make_int4(total[4], total[5], total[6], total[7]);
+    to = reinterpret_cast<int4*>(&s_part[1][(group * vecs + vec) * 8]);
+    to[0] = make_int4(before[0], before[1], before[2], before[3]);
+    to[1] = make_int4(before[4], before[5], before[6], before[7]);
+  }
+  __syncthreads();
+  // a thread per expert
+  int all_of = 0, earlier = 0;
+  if (mine_e < p.experts) {
+#pragma unroll 8
+    for (int g = 0; g < groups; ++g) {
+      all_of += s_part[0][g * vecs * 8 + mine_e];
+      earlier += s_part[1][g * vecs * 8 + mine_e];
+    }
+  }
+  int upto = all_of;   // of this and the warp's earlier experts
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, upto, o);
+    if (lane >= o) upto += y;
+  }
+  if (lane == 31) s_warp[threadIdx.x >> 5] = upto;
+  __syncthreads();
+  int row = upto - all_of + earlier, sum = 0;
+#pragma unroll
+  for (int w = 0; w < kPlaceThreads / 32; ++w) {
+    row += w < int(threadIdx.x >> 5) ? s_warp[w] : 0;
+    sum += s_warp[w];
+  }
+  if (mine_e < p.experts) {
+    if (blockIdx.x == 0) p.sizes[mine_e] = all_of;
+#pragma unroll
+    for (int b = 0; b < kPlaceEach; ++b) {
+      if (b < mine) s_base[b * p.experts + mine_e] = row;
+      row += own[b];
+    }
+  }
+  const int s_all = sum;
+  __syncthreads();
+  auto place = [&](long long i, int e, int rank) {
     if (e >= 0) {
-      const int row = s_base[int(i - begin) / per * p.experts + e] + __ldcg(p.rows + i);
+      const int row = s_base[int(i - begin) / per * p.experts + e] + rank;
       p.rows[i] = row;
       p.slots[row] = int(i);
     }
     if (i >= s_all) p.slots[i] = -1;
+  };
+#pragma unroll
+  for (int a = 0; a < kAhead; ++a) {
+    const long long i = begin + threadIdx.x + a * kPlaceThreads;
+    if (i < end) place(i, ahead_id[a], ahead_rank[a]);
   }
+#pragma unroll 1
+  for (long long i = begin + threadIdx.x + kAhead * kPlaceThreads; i < end; i += kPlaceThreads)
+    place(i, __ldcg(p.ids + i), __ldcg(p.rows + i));
 }
 
 // dz of one token per warp.  With a_j the chosen scores, da_j their gradients:
@@ -625,9 +869,11 @@ tkg_status with_run(int experts, const void* a, size_t lda, const void* b, size_
   return pick(std::integral_constant<int, 16>{});
 }
 
+// Tokens in one block while that takes less time than a second kernel; past that, blocks of 32 at least, one per SM,
+// and of no more than 16 bits can count.
 void route_blocks(int tokens, int* blocks, int* per_block) {
-  const int chunks = ceil_div(tokens, kRouteTokens);
-  *per_block = ceil_div(chunks, kRouteBlocks) * kRouteTokens;
+  *per_block = tokens <= kRouteAlone ? (tokens + 31) / 32 * 32 : ceil_div(ceil_div(tokens, kRouteBlocks), 32) * 32;
+  if (*per_block > 65504) *per_block = 65504;
   *blocks = ceil_div(tokens, *per_block);
 }
 
@@ -645,30 +891,35 @@ template <typename L>
 tkg_status launch_route(RouteParams p, cudaStream_t stream) {
   return with_run<L>(p.experts, p.logits, p.ld, p.logits, p.ld, [&](auto per, auto wide) {
     constexpr int PER = decltype(per)::value;
-    unsigned smem = unsigned((3 * p.experts + 1) / 2 * 2) * 4u;
+    const int there = p.per_block < kRouteTokens ? p.per_block : kRouteTokens;
+    unsigned smem = unsigned((p.experts * (kRouteWords + 2) + there * p.topk + 1) / 2 * 2) * 4u;
     // values of the groups' choice, one row per warp, as large as its second time in 64 bits needs
-    if (p.topk_groups < p.groups) smem += unsigned(kRouteWarps * (p.experts + p.experts / 32 + 1)) * 8u;
-    auto kern = route_choose_kernel<PER, L, decltype(wide)::value>;
-    if (smem > 40000) {
-      static bool set[64] = {};   // per instantiation and device
+    if (p.topk_groups < p.groups) smem += unsigned(kRouteWarps<PER> * (p.experts + p.experts / 32 + 1)) * 8u;
+    const bool by_logit = !p.bias && p.topk_groups == p.groups;
+    auto kern = by_logit ? route_choose_kernel<PER, L, decltype(wide)::value, true>
+                         : route_choose_kernel<PER, L, decltype(wide)::value, false>;
+    if (smem > 48000) {
+      static bool sets[2][64] = {};   // per instantiation and device
+      bool* set = sets[by_logit];
       int dev = 0;
       if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return TKG_ERR_CUDA;
       if (!set[dev]) {
-        if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 81920) != cudaSuccess) {
+        if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 102400) != cudaSuccess) {
           cudaGetLastError();
           return TKG_ERR_CUDA;
         }
         set[dev] = true;
       }
     }
-    tkg_status st = launch_small(kern, dim3(unsigned(p.blocks)), dim3(32 * kRouteWarps), stream, smem, p);
+    const int warps = p.tokens < 4 ? 4 : (p.tokens < kRouteWarps<PER> ? p.tokens : kRouteWarps<PER>);
+    tkg_status st = launch_small(kern, dim3(unsigned(p.blocks)), dim3(32u * unsigned(warps)), stream, smem, p);
     if (st != TKG_OK || p.blocks == 1) return st;
-    const int each = ceil_div(p.blocks, kPlaceBlocks);
-    return launch_small(route_place_kernel, dim3(unsigned(ceil_div(p.blocks, each))), dim3(kPlaceThreads), stream,
-                        unsigned(each * p.experts) * 4u, p, each);
+    int each = kPlaceEntries / (p.per_block * p.topk);
+    each = each < 1 ? 1 : (each > kPlaceEach ? kPlaceEach : each);
+    return launch_small(route_place_kernel, dim3(unsigned(ceil_div(p.blocks, each))), dim3(kPlaceThreads), stream, 0u, p,
+                        each);
   });
 }
-static_assert(kPlaceEach * kMaxRouteExperts * 4 + 2 * kMaxRouteExperts * 4 + 16 <= 49152, "shared memory of the placing blocks");
 
 }  // namespace
 }  // namespace tkg
@@ -681,7 +932,7 @@ size_t tkg_moe_route_workspace_bytes(int tokens, int experts) {
   if (tokens < 0 || experts < 1 || experts > kMaxRouteExperts || tokens > kMaxSize) return 0;
   int blocks = 0, per_block = 0;
   if (tokens > 0) route_blocks(tokens, &blocks, &per_block);
-  return size_t(blocks > 1 ? blocks : 0) * size_t(experts) * 4 + 16;
+  return size_t(blocks > 1 ? blocks : 0) * size_t((experts + 7) / 8 * 8) * 2 + 16;
 }
 
 tkg_status tkg_moe_route(int tokens, int experts, int topk, const void* logits, tkg_type type, int ld,
@@ -725,7 +976,10 @@ tkg_status tkg_moe_route(int tokens, int experts, int topk, const void* logits, 
   p.sizes = sizes;
   p.rows = rows;
   p.slots = slots;
-  p.counts = static_cast<int*>(workspace);
+  p.counts = static_cast<uint16_t*>(workspace);
+  p.lanes_per_group = 1;
+  while (2 * p.lanes_per_group * groups <= 32) p.lanes_per_group *= 2;
+  p.inverse = uint32_t((0x100000000ull + unsigned(p.per_group) - 1) / unsigned(p.per_group));
   route_blocks(tokens, &p.blocks, &p.per_block);
   return type == TKG_TYPE_F32 ? launch_route<F32>(p, stream) : launch_route<BF16>(p, stream);
 }

@@ -25,7 +25,7 @@ __global__ void __launch_bounds__(kRowThreads) dispatch_kernel(int vecs, int top
   const int v = blockIdx.y * kRowThreads + threadIdx.x;
   if (v >= vecs) return;
   ptx::pdl_wait();
-  const uint4 x = __ldcs(reinterpret_cast<const uint4*>(X + t * ldx) + v);
+  const uint4 x = __ldcg(reinterpret_cast<const uint4*>(X + t * ldx) + v);
 #pragma unroll 4
   for (int j = 0; j < topk; ++j) {
     const int r = __ldcg(rows + t * topk + j);
@@ -55,7 +55,7 @@ __global__ void __launch_bounds__(kRowThreads) combine_kernel(int vecs, int topk
       if (j0 + j < topk) {
         const int r = __ldcg(rows + t * topk + j0 + j);
         if (r >= 0 && r < capacity) {
-          x[j] = __ldcs(reinterpret_cast<const uint4*>(O + size_t(r) * ldo) + v);
+          x[j] = __ldcg(reinterpret_cast<const uint4*>(O + size_t(r) * ldo) + v);
           w[j] = weights ? __ldcg(weights + t * topk + j0 + j) : 1.f;
         }
       }

@@ -96,7 +96,7 @@ __global__ void __launch_bounds__(32 * kWarps) save_kernel(int rows, int k, cons
   uint4 v[kSavePieces];
 #pragma unroll
   for (int i = 0; i < kSavePieces; ++i)
-    v[i] = at.row[i] >= 0 && at.col[i] < k ? __ldcs(reinterpret_cast<const uint4*>(X + size_t(at.row[i]) * ldx + at.col[i]))
+    v[i] = at.row[i] >= 0 && at.col[i] < k ? __ldcg(reinterpret_cast<const uint4*>(X + size_t(at.row[i]) * ldx + at.col[i]))
                                            : make_uint4(0, 0, 0, 0);
 #pragma unroll
   for (int i = 0; i < kSavePieces; ++i) {
@@ -127,7 +127,7 @@ __global__ void __launch_bounds__(32 * kWarps)
 #pragma unroll
     for (int b = 0; b < 2; ++b)
       v[i][b] = at.row[i] >= 0 && at.col[i] < inner
-                    ? __ldcs(reinterpret_cast<const uint4*>(GU + size_t(at.row[i]) * ldgu + b * inner + at.col[i]))
+                    ? __ldcg(reinterpret_cast<const uint4*>(GU + size_t(at.row[i]) * ldgu + b * inner + at.col[i]))
                     : make_uint4(0, 0, 0, 0);
 #pragma unroll
   for (int i = 0; i < kGatePieces; ++i) {
@@ -189,10 +189,10 @@ __global__ void __launch_bounds__(32 * kWarps) swiglu_grad_kernel(const GateGrad
     uint16_t* dx = p.dGU + size_t(row) * p.lddgu;
 #pragma unroll 2
     for (int c = part * kPiece + lane * 8; c < p.inner; c += p.split * kPiece) {
-      const uint2 qg = __ldcs(reinterpret_cast<const uint2*>(q + c));
-      const uint2 qu = __ldcs(reinterpret_cast<const uint2*>(q + p.inner + c));
-      const uint32_t sg = __ldcs(sf + c / 32), su = __ldcs(sf + (p.inner + c) / 32);
-      const uint4 vd = __ldcs(reinterpret_cast<const uint4*>(dh + c));
+      const uint2 qg = __ldcg(reinterpret_cast<const uint2*>(q + c));
+      const uint2 qu = __ldcg(reinterpret_cast<const uint2*>(q + p.inner + c));
+      const uint32_t sg = __ldcg(sf + c / 32), su = __ldcg(sf + (p.inner + c) / 32);
+      const uint4 vd = __ldcg(reinterpret_cast<const uint4*>(dh + c));
       float g[8], u[8], d[8], h[8];
       from_codes(qg, sg, g);
       from_codes(qu, su, u);
