@@ -2,7 +2,8 @@
 
 One step, all on the device and with no host synchronisation between the calls:
 
-  router        top-1 expert per token; tokens put in expert order, row counts left in device memory
+  router        tkg.moe_route, tkg.moe_dispatch (top-1 expert per token; tokens put in expert order, row counts left in
+                device memory)
   forward       D_g = A_g B_g^T            tkg.gemm_grouped_dev_bf16     (expert products)
                 Y = A + D                  (residual)
                 loss, lse                  tkg.linear_ce_loss            (head and cross entropy, logits never kept)
@@ -53,10 +54,12 @@ class Model:
             ids = torch.randint(0, self.vocab, (self.tokens,), generator=self.gen, device="cuda")
             x = self.E[ids].to(BF16)
             # tokens in expert order, and how many each expert has
-            expert = (x.float() @ self.R).argmax(dim=1)
-            order = expert.argsort(stable=True)
-            sizes = torch.bincount(expert, minlength=self.experts).to(torch.int32)
-            ids, A = ids[order], x[order]
+            i32 = lambda *s: torch.empty(*s, dtype=torch.int32, device="cuda")
+            expert, rows, sizes, order = i32(self.tokens, 1), i32(self.tokens, 1), i32(self.experts), i32(self.tokens)
+            tkg.moe_route(x.float() @ self.R, expert, torch.empty(self.tokens, 1, device="cuda"), sizes, rows, order)
+            A = torch.empty_like(x)
+            tkg.moe_dispatch(x, rows, A)
+            ids = ids[order.long()]
             labels = self.succ[ids]
             # forward
             D = torch.empty_like(A)
