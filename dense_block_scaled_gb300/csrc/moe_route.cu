@@ -8,16 +8,19 @@
 //   sizes_e = tokens that chose e;  rows(t, j) = place of (t, j) among all choices ordered by expert, then by token;
 //   slots(rows(t, j)) = t topk + j
 //
-// Two kernels.  route_choose_kernel: a warp per token, each lane a run of consecutive experts, sorted by value and index;
-// a choice is an integer maximum over the warp (redux) of keys that are ordered as the values are, a minimum of the
-// indices that have it, and a step along one lane's run.  Within a block of tokens, the rank of (t, e) is the number of
-// earlier tokens that chose e: a population count of one bit per token and expert.  The block leaves its ranks (in
-// `rows`) and its count per expert.  route_place_kernel: adds what earlier blocks and experts have.  A single block of
-// tokens does both at once.  Nothing depends on the order of atomics: those are bit sets.
+// Two kernels.  route_choose_kernel: a warp per token, each lane a run of consecutive experts.  The topk-th largest of the
+// lanes' largest values bounds the topk-th value from below; what is not below that, about topk + 1 candidates, is
+// gathered, one to a lane, and ranked by comparing all with all.  (BF16 logits that decide by themselves: value and index
+// share a word, each lane sorts its run, and every choice is one integer maximum over the warp.)  Within a block of tokens,
+// the rank of (t, e) is the number of earlier tokens that chose e: a population count of one bit per token and expert.  The
+// block leaves its ranks (in `rows`) and its count per expert.  route_place_kernel: adds what earlier blocks and experts
+// have.  A single block of tokens does both at once.  Nothing depends on the order of atomics: those are bit sets.
 //
 // Without bias and groups the logits themselves decide (both scores rise with them).  Otherwise FP32 scores decide
 // wherever they are further apart than they can be wrong; where two around a choice are closer, and not of the same logit
 // and bias, the candidates are ordered again in 64 bits, so that the choice is that of the exact scores.
+#include <cfloat>
+
 #include "train_host.cuh"
 
 namespace tkg {
@@ -30,13 +33,15 @@ constexpr int kRouteWords = 4;             // 32 tokens each, ranked at a time
 constexpr int kRouteTokens = 32 * kRouteWords;
 constexpr int kMaxRouteExperts = 512, kMaxTopk = 32, kMaxRouteGroups = 32;
 constexpr int kRouteBlocks = 152;          // blocks of tokens at most: one per SM
+constexpr int kFewTopk = 16;               // choices for which the candidates are hardly ever more than 32
 constexpr int kRouteAlone = 64;            // tokens at most that one block takes alone
 constexpr int kPlaceThreads = 512, kPlaceEach = 7;
 constexpr int kPlaceEntries = 1024;        // choices that a placing block takes, about
 
 struct RouteParams {
   int tokens, experts, topk;
-  int groups, per_group, topk_groups, lanes_per_group;
+  int groups, per_group, topk_groups;
+  int lanes_per_group, whole_runs;   // a group is that many lanes' runs; otherwise that many lanes read it
   uint32_t inverse;           // ceil(2^32 / per_group): e / per_group is the high word of e * inverse (e < 512)
   __device__ __forceinline__ int group_of(int e) const {
     return per_group == 1 ? e : int(__umulhi(uint32_t(e), inverse));
@@ -173,8 +178,17 @@ __device__ __forceinline__ F sigmoid_of(F z) { return F(1) / (F(1) + exp_of(-z))
 template <int PER>
 __device__ __forceinline__ void choice_scores(const RouteParams& p, const float (&z)[PER], const float* s_bias, int lane,
                                               float most_bias, float (&c)[PER], float& wrong) {
-  float most;
-  auto bias = [&](int i) { return lane * PER + i < p.experts ? s_bias[lane * PER + i] : 0.f; };
+  float most, b[PER];
+  if constexpr (PER >= 4) {
+#pragma unroll
+    for (int i = 0; i < PER / 4; ++i) {
+      const float4 v = reinterpret_cast<const float4*>(s_bias)[lane * (PER / 4) + i];
+      b[4 * i] = v.x, b[4 * i + 1] = v.y, b[4 * i + 2] = v.z, b[4 * i + 3] = v.w;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < PER; ++i) b[i] = s_bias[lane * PER + i];
+  }
   auto reciprocal = [](float x) {
     float r;
     asm("rcp.approx.f32 %0, %1;" : "=f"(r) : "f"(x));
@@ -182,7 +196,7 @@ __device__ __forceinline__ void choice_scores(const RouteParams& p, const float 
   };
   if (p.sigmoid) {
 #pragma unroll
-    for (int i = 0; i < PER; ++i) c[i] = reciprocal(1.f + ptx::ex2(z[i] * -kLog2e)) + bias(i);
+    for (int i = 0; i < PER; ++i) c[i] = reciprocal(1.f + ptx::ex2(z[i] * -kLog2e)) + b[i];
     most = 1.f;
     wrong = 0x1p-21f;
   } else {
@@ -190,7 +204,7 @@ __device__ __forceinline__ void choice_scores(const RouteParams& p, const float 
     const float sum = softmax_sum(z, lane, p.experts, softmax_top(z), e, [](float x) { return ptx::ex2(x * kLog2e); });
     most = reciprocal(sum);
 #pragma unroll
-    for (int i = 0; i < PER; ++i) c[i] = fmaf(e[i], most, bias(i));
+    for (int i = 0; i < PER; ++i) c[i] = fmaf(e[i], most, b[i]);
     wrong = most * 0x1p-18f;
   }
   wrong += (most + most_bias) * 0x1p-24f;
@@ -245,32 +259,39 @@ __device__ __forceinline__ void sort_run(uint32_t (&key)[PER]) {
   });
 }
 
-// Clears the keys of experts outside the best groups; false where the values do not decide between two groups.  Each
-// group has `per` lanes, its first keeps its value; `box` (a row per warp) carries the values to them.
-template <int PER, typename F, typename K>
-__device__ __forceinline__ bool keep_groups(const RouteParams& p, const F (&c)[PER], K (&key)[PER], float wrong, int lane,
-                                            F* box) {
-  __syncwarp();
-#pragma unroll
-  for (int i = 0; i < PER; ++i) {
-    const int e = lane * PER + i;
-    if (e < p.experts) box[e + e / 32] = c[i];
-  }
-  __syncwarp();
+// Which of a lane's run are in the best groups (a bit each); `clear` is false where the values do not decide between two
+// groups, or one is not a number.  Each group has some lanes, its first holds its value: they are its runs' own, or read
+// it from `box` (a row per warp).
+template <int PER, typename F>
+__device__ __forceinline__ uint32_t keep_groups(const RouteParams& p, const F (&c)[PER], float wrong, int lane, F* box,
+                                                bool& clear) {
+  using K = decltype(key_of(F(0)));
   const int per = p.lanes_per_group, shift = __popc(per - 1);
   const int g = lane >> shift;
   F a = -INFINITY, b = -INFINITY;   // the two largest
   int lost = 0;                     // (NaN)
-  if (g < p.groups) {
-    int e = g * p.per_group + (lane & (per - 1));
-    const int end = (g + 1) * p.per_group;
+  auto take = [&](F x) {
+    lost |= x != x;
+    const F low = x > a ? a : x;
+    a = x > a ? x : a;
+    b = low > b ? low : b;
+  };
+  if (p.whole_runs) {
+#pragma unroll
+    for (int i = 0; i < PER; ++i) take(c[i]);
+    if (g >= p.groups) lost = 0;
+  } else {
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      const int e = lane * PER + i;
+      if (e < p.experts) box[e + e / 32] = c[i];
+    }
+    __syncwarp();
+    if (g < p.groups) {
+      const int end = (g + 1) * p.per_group;
 #pragma unroll 4
-    for (; e < end; e += per) {
-      const F x = box[e + e / 32];
-      lost |= x != x;
-      const F low = x > a ? a : x;
-      a = x > a ? x : a;
-      b = low > b ? low : b;
+      for (int e = g * p.per_group + (lane & (per - 1)); e < end; e += per) take(box[e + e / 32]);
     }
   }
 #pragma unroll 1
@@ -291,6 +312,13 @@ __device__ __forceinline__ bool keep_groups(const RouteParams& p, const F (&c)[P
     rank += other > mine || (other == mine && o < g) ? 1 : 0;
   }
   const uint32_t stay = __ballot_sync(0xffffffffu, holds && rank < p.topk_groups);
+  // the last group that stays and the first that goes: each sum of two is off by both's error and its rounding
+  const uint32_t in = __ballot_sync(0xffffffffu, holds && rank == p.topk_groups - 1);
+  const uint32_t out = __ballot_sync(0xffffffffu, holds && rank == p.topk_groups);
+  const F last = __shfl_sync(0xffffffffu, sum, __ffs(int(in)) - 1), first = __shfl_sync(0xffffffffu, sum, __ffs(int(out)) - 1);
+  clear = float(last - first) > 4.f * wrong + (fabsf(float(last)) + fabsf(float(first))) * 0x1p-24f;
+  if (p.whole_runs) return (stay >> (g << shift)) & 1u ? 0xffffffffu : 0u;
+  uint32_t kept = 0;
   int of = p.group_of(lane * PER), left = (of + 1) * p.per_group - lane * PER;   // a run's groups
 #pragma unroll
   for (int i = 0; i < PER; ++i) {
@@ -299,13 +327,9 @@ __device__ __forceinline__ bool keep_groups(const RouteParams& p, const F (&c)[P
       left = p.per_group;
     }
     --left;
-    if (lane * PER + i < p.experts && !((stay >> (of << shift)) & 1u)) key[i] = K(0);
+    if (lane * PER + i < p.experts) kept |= ((stay >> (of << shift)) & 1u) << i;
   }
-  // the last group that stays and the first that goes: each sum of two is off by both's error and its rounding
-  const uint32_t in = __ballot_sync(0xffffffffu, holds && rank == p.topk_groups - 1);
-  const uint32_t out = __ballot_sync(0xffffffffu, holds && rank == p.topk_groups);
-  const F last = __shfl_sync(0xffffffffu, sum, __ffs(int(in)) - 1), first = __shfl_sync(0xffffffffu, sum, __ffs(int(out)) - 1);
-  return float(last - first) > 4.f * wrong + (fabsf(float(last)) + fabsf(float(first))) * 0x1p-24f;
+  return kept;
 }
 
 template <typename L>
@@ -353,29 +377,89 @@ __device__ __noinline__ int order_again(const RouteParams& p, int t, int n, int 
   return out;
 }
 
-// The choice of token t by values c (a lane's run; NaN last), each off by at most `wrong` (negative: exact): lane j < topk
-// gets the j-th expert and, where the values are its logits, `value` its logit.  -1 in all lanes where the values do not
-// decide between groups, or between more than 32 candidates (the caller then asks with 64 bits).
+// Whether two experts have the same logit and bias, so the same score.
+template <typename L>
+__device__ __forceinline__ bool same_score(const RouteParams& p, int t, int a, int b) {
+  return logit_at<L>(p, t, a) == logit_at<L>(p, t, b) && bias_at(p, a) == bias_at(p, b);
+}
+
+// The choice of token t by values c (a lane's run), each off by at most `wrong` (negative: exact): lane j < topk gets the
+// j-th expert and, where the values are its logits, `value` its logit.  -1 in all lanes where there are more than 32
+// candidates, or values among them that are no number above -infinity.  `few`: 32 places per warp.
+template <int PER, typename L>
+__device__ __forceinline__ int choose_few(const RouteParams& p, int t, const float (&c)[PER], float wrong, int lane,
+                                          float2* few, float& value) {
+  // the topk-th largest of the lanes' largest values, or -infinity (of equal ones all go at once: then it is less)
+  float most = c[0];
+#pragma unroll
+  for (int i = 1; i < PER; ++i) most = fmaxf(most, c[i]);
+  uint32_t mine = key_of(fmaxf(most, -INFINITY)), bound = 0;
+#pragma unroll 1
+  for (int j = 0; j < p.topk; ++j) {
+    bound = warp_max(mine);
+    if (mine == bound) mine = 0;
+  }
+  const float margin = wrong > 0.f ? 2.f * wrong : 0.f;
+  const float least = bound > key_of(-INFINITY) ? value_of(bound) - margin : -FLT_MAX;
+  int count = 0;
+#pragma unroll
+  for (int i = 0; i < PER; ++i) count += c[i] >= least ? 1 : 0;
+  int upto = count;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, upto, o);
+    if (lane >= o) upto += y;
+  }
+  const int n = __shfl_sync(0xffffffffu, upto, 31);
+  if (n > 32 || n < p.topk) return -1;
+  float2* to = few + (upto - count);
+  __syncwarp();
+#pragma unroll
+  for (int i = 0; i < PER; ++i)
+    if (c[i] >= least) *to++ = make_float2(c[i], __int_as_float(lane * PER + i));
+  __syncwarp();
+  const float2 own = few[lane];   // (past n: whatever is there)
+  int rank = 0;
+#pragma unroll 4
+  for (int i = 0; i < n; ++i) {
+    const float2 o = few[i];
+    rank += o.x > own.x || (o.x == own.x && __float_as_int(o.y) < __float_as_int(own.y)) ? 1 : 0;
+  }
+  __syncwarp();
+  if (lane < n) few[rank] = own;
+  __syncwarp();
+  const float2 me = few[lane], next = few[lane < 31 ? lane + 1 : 31];
+  int id = lane < n ? __float_as_int(me.y) : 0;
+  value = me.x;
+  if (wrong >= 0.f) {
+    // neighbours that are too near, as far as they may belong before the last of the chosen
+    const bool near = lane + 1 < n && next.x >= few[p.topk - 1].x - margin && !(me.x - next.x > margin);
+    if (__any_sync(0xffffffffu, near)) {
+      const bool close = near && !same_score<L>(p, t, id, __float_as_int(next.y));
+      if (__any_sync(0xffffffffu, close)) id = order_again<L>(p, t, n, id, lane);
+    }
+  }
+  return id;
+}
+
+// The same for any values (NaN last) and number of candidates, in FP32 or by exact ones in 64 bits (`wrong` negative): a
+// choice at a time.  -1 in all lanes where FP32 does not decide between more than 32 candidates.
 template <int PER, typename L, typename F>
-__device__ __forceinline__ int choose(const RouteParams& p, int t, const F (&c)[PER], float wrong, int lane, F* box,
-                                      float& value) {
+__device__ __forceinline__ int choose_any(const RouteParams& p, int t, const F (&c)[PER], uint32_t kept, float wrong,
+                                          int lane) {
   using K = decltype(key_of(F(0)));
   const bool sure = wrong < 0.f;
   K key[PER];
   int at[PER];
 #pragma unroll
   for (int i = 0; i < PER; ++i) {
-    key[i] = lane * PER + i < p.experts ? key_of(c[i]) : K(0);
+    key[i] = lane * PER + i < p.experts && ((kept >> i) & 1u) ? key_of(c[i]) : K(0);
     at[i] = lane * PER + i;
   }
-  if (p.topk_groups < p.groups && !keep_groups(p, c, key, wrong, lane, box) && !sure) return -1;
   sort_run(key, at);
   int id = 0, j = 0, picks = p.topk;
-  K mine = K(0), last = K(0);
+  K last = K(0);
   bool close = false;   // two of the chosen are too near, or (below) one of the rest is to the last of them
-  auto same = [&](int a, int b) {   // of the same logit and bias, so of the same score
-    return logit_at<L>(p, t, a) == logit_at<L>(p, t, b) && bias_at(p, a) == bias_at(p, b);
-  };
   int e = 0;
 #pragma unroll 1
   for (;;) {
@@ -384,13 +468,10 @@ __device__ __forceinline__ int choose(const RouteParams& p, int t, const F (&c)[
       const K m = warp_max(key[0]);
       const int before = e;
       e = int(__reduce_min_sync(0xffffffffu, key[0] == m ? uint32_t(at[0]) : 0xffffffffu));
-      if (lane == j) {
-        id = e;
-        mine = m;
-      }
+      if (lane == j) id = e;
       if (!sure && j > 0) {
         if constexpr (sizeof(K) == 4)
-          if (!(value_of(last) - value_of(m) > 2.f * wrong) && !same(before, e)) close = true;
+          if (!(value_of(last) - value_of(m) > 2.f * wrong) && !same_score<L>(p, t, before, e)) close = true;
       }
       last = m;
       const bool step = at[0] == e && key[0] == m;
@@ -412,7 +493,7 @@ __device__ __forceinline__ int choose(const RouteParams& p, int t, const F (&c)[
       for (int i = 0; i < PER; ++i)
         if (key[i] != K(0) && key[i] >= least) {
           ++near;
-          other |= !same(e, at[i]);
+          other |= !same_score<L>(p, t, e, at[i]);
         }
       if (!__any_sync(0xffffffffu, other)) break;
       close = true;
@@ -420,10 +501,8 @@ __device__ __forceinline__ int choose(const RouteParams& p, int t, const F (&c)[
       if (picks > 32) return -1;
     }
   }
-  if constexpr (sizeof(K) == 4) {
+  if constexpr (sizeof(K) == 4)
     if (close) id = order_again<L>(p, t, j, id, lane);
-    value = value_of(mine);
-  }
   return id;
 }
 
@@ -454,24 +533,41 @@ __device__ __forceinline__ int choose_packed(const RouteParams& p, const float (
   return id;
 }
 
-// The same by all scores in 64 bits: rare too.
+// The choice where choose_few does not apply: rare, and kept out of the way of the registers of the rest.
 template <int PER, typename L>
-__device__ __noinline__ int choose_again(const RouteParams& p, int t, int lane, double* box) {
-  float z[PER], bias[PER], unused;
-  double c[PER];
+__device__ __noinline__ int choose_slowly(const RouteParams& p, int t, bool by_logit, const float* s_bias, float most_bias,
+                                          int lane, double* box) {
+  float z[PER];
+  bool clear = true;
 #pragma unroll
   for (int i = 0; i < PER; ++i) {
     const int e = lane * PER + i;
     z[i] = e < p.experts ? logit_at<L>(p, t, e) : -INFINITY;
-    bias[i] = e < p.experts ? bias_at(p, e) : 0.f;
   }
+  if (by_logit) return choose_any<PER, L>(p, t, z, 0xffffffffu, -1.f, lane);
+  const bool limited = p.topk_groups < p.groups;
+  {
+    float c[PER], wrong;
+    uint32_t kept = 0xffffffffu;
+    choice_scores(p, z, s_bias, lane, most_bias, c, wrong);
+    if (limited) kept = keep_groups(p, c, wrong, lane, reinterpret_cast<float*>(box), clear);
+    const int id = clear ? choose_any<PER, L>(p, t, c, kept, wrong, lane) : -1;
+    if (__shfl_sync(0xffffffffu, id, 0) >= 0) return id;
+  }
+  double c[PER];
+  uint32_t kept = 0xffffffffu;
+  float bias[PER];
+#pragma unroll
+  for (int i = 0; i < PER; ++i) bias[i] = s_bias[lane * PER + i];
   choice_scores(p, z, bias, lane, c);
-  return choose<PER, L>(p, t, c, -1.f, lane, box, unused);
+  if (limited) kept = keep_groups(p, c, 0.f, lane, box, clear);
+  return choose_any<PER, L>(p, t, c, kept, -1.f, lane);
 }
 
 // BY_LOGIT: no bias and no limit to groups.
 template <int PER, typename L, bool WIDE, bool BY_LOGIT>
 __global__ void __launch_bounds__(32 * kRouteWarps<PER>) route_choose_kernel(const RouteParams p) {
+  constexpr bool kPacked = BY_LOGIT && sizeof(L) == 2;
   extern __shared__ int s_dyn[];
   // bits of the tokens that chose an expert, how many did before, each expert's first row (one block of tokens), and, for
   // the groups, a row of values per warp
@@ -480,10 +576,11 @@ __global__ void __launch_bounds__(32 * kRouteWarps<PER>) route_choose_kernel(con
   __shared__ int s_total;
   ptx::pdl_launch_dependents();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  float* s_bias = reinterpret_cast<float*>(s_count + p.experts);
-  int* s_ids = s_count + 2 * p.experts;                      // [kRouteTokens][topk]
+  __shared__ __align__(16) float s_bias[BY_LOGIT ? 4 : 32 * PER];
+  __shared__ float2 s_few[kPacked ? 1 : kRouteWarps<PER>][32];
+  int* s_ids = s_count + p.experts;                          // [kRouteTokens][topk]
   const int tokens_there = min(kRouteTokens, p.per_block), warps = blockDim.x >> 5;
-  double* box = reinterpret_cast<double*>(s_dyn + (p.experts * (kRouteWords + 2) + tokens_there * p.topk + 1) / 2 * 2) +
+  double* box = reinterpret_cast<double*>(s_dyn + (p.experts * (kRouteWords + 1) + tokens_there * p.topk + 1) / 2 * 2) +
                 warp * (p.experts + p.experts / 32 + 1);
   for (int e = threadIdx.x; e < p.experts; e += blockDim.x) s_count[e] = 0;
   const int begin = blockIdx.x * p.per_block, end = min(p.tokens, begin + p.per_block);
@@ -491,7 +588,7 @@ __global__ void __launch_bounds__(32 * kRouteWarps<PER>) route_choose_kernel(con
   if constexpr (!BY_LOGIT) {
     ptx::pdl_wait();
     // (through shared memory: 32 warps' runs straight from L2 are 32 times its sectors, all the same ones, 20 us)
-    for (int e = threadIdx.x; e < p.experts; e += blockDim.x) s_bias[e] = bias_at(p, e);
+    for (int e = threadIdx.x; e < 32 * PER; e += blockDim.x) s_bias[e] = e < p.experts ? bias_at(p, e) : 0.f;
     __syncthreads();
     for (int e = lane; e < p.experts; e += 32) {
       const float b = fabsf(s_bias[e]);
@@ -530,16 +627,25 @@ __global__ void __launch_bounds__(32 * kRouteWarps<PER>) route_choose_kernel(con
           sub = softmax_top(z);
           sum = softmax_sum(z, lane, p.experts, sub, e, [](float x) { return expf(x); });
         }
-        if constexpr (BY_LOGIT && sizeof(L) == 2) {
+        if constexpr (kPacked) {
           id = choose_packed(p, z, lane, zj);
-        } else if constexpr (BY_LOGIT) {
-          id = choose<PER, L>(p, t, z, -1.f, lane, reinterpret_cast<float*>(box), zj);
         } else {
-          float c[PER], wrong;
-          choice_scores(p, z, s_bias, lane, most_bias, c, wrong);
-          id = choose<PER, L>(p, t, c, wrong, lane, reinterpret_cast<float*>(box), zj);
-          if (__shfl_sync(0xffffffffu, id, 0) < 0) id = choose_again<PER, L>(p, t, lane, box);
-          zj = logit_at<L>(p, t, id);
+          float c[PER], wrong = -1.f;
+          bool clear = true;
+#pragma unroll
+          for (int k = 0; k < PER; ++k) c[k] = z[k];
+          if constexpr (!BY_LOGIT) {
+            choice_scores(p, z, s_bias, lane, most_bias, c, wrong);
+            uint32_t kept = 0xffffffffu;
+            if (p.topk_groups < p.groups) kept = keep_groups(p, c, wrong, lane, reinterpret_cast<float*>(box), clear);
+#pragma unroll
+            for (int k = 0; k < PER; ++k)
+              if (lane * PER + k >= p.experts || !((kept >> k) & 1u)) c[k] = -INFINITY;
+          }
+          id = clear && p.topk <= kFewTopk ? choose_few<PER, L>(p, t, c, wrong, lane, s_few[warp], zj) : -1;
+          const bool slow = __shfl_sync(0xffffffffu, id, 0) < 0;
+          if (slow) id = choose_slowly<PER, L>(p, t, BY_LOGIT, s_bias, most_bias, lane, box);
+          if (!BY_LOGIT || slow) zj = logit_at<L>(p, t, id);
         }
         // lane j: its expert's score
         const bool mine = lane < p.topk;
@@ -889,16 +995,24 @@ tkg_status check_route(int tokens, int experts, int topk, const void* logits, tk
 
 template <typename L>
 tkg_status launch_route(RouteParams p, cudaStream_t stream) {
-  return with_run<L>(p.experts, p.logits, p.ld, p.logits, p.ld, [&](auto per, auto wide) {
+  return with_run<L>(p.experts, p.logits, p.ld, p.logits, p.ld, [&, p](auto per, auto wide) mutable {
     constexpr int PER = decltype(per)::value;
+    // groups of whole runs, a power of two of them: their lanes need no shared memory
+    const int runs = p.per_group / PER;
+    p.whole_runs = p.per_group % PER == 0 && (runs & (runs - 1)) == 0;
+    p.lanes_per_group = 1;
+    if (p.whole_runs)
+      p.lanes_per_group = runs;
+    else
+      while (2 * p.lanes_per_group * p.groups <= 32) p.lanes_per_group *= 2;
     const int there = p.per_block < kRouteTokens ? p.per_block : kRouteTokens;
-    unsigned smem = unsigned((p.experts * (kRouteWords + 2) + there * p.topk + 1) / 2 * 2) * 4u;
+    unsigned smem = unsigned((p.experts * (kRouteWords + 1) + there * p.topk + 1) / 2 * 2) * 4u;
     // values of the groups' choice, one row per warp, as large as its second time in 64 bits needs
-    if (p.topk_groups < p.groups) smem += unsigned(kRouteWarps<PER> * (p.experts + p.experts / 32 + 1)) * 8u;
+    if (p.topk_groups < p.groups && !p.whole_runs) smem += unsigned(kRouteWarps<PER> * (p.experts + p.experts / 32 + 1)) * 8u;
     const bool by_logit = !p.bias && p.topk_groups == p.groups;
     auto kern = by_logit ? route_choose_kernel<PER, L, decltype(wide)::value, true>
                          : route_choose_kernel<PER, L, decltype(wide)::value, false>;
-    if (smem > 48000) {
+    if (smem > 36000) {   // (beside 10 KB of its own)
       static bool sets[2][64] = {};   // per instantiation and device
       bool* set = sets[by_logit];
       int dev = 0;
@@ -977,8 +1091,6 @@ tkg_status tkg_moe_route(int tokens, int experts, int topk, const void* logits, 
   p.rows = rows;
   p.slots = slots;
   p.counts = static_cast<uint16_t*>(workspace);
-  p.lanes_per_group = 1;
-  while (2 * p.lanes_per_group * groups <= 32) p.lanes_per_group *= 2;
   p.inverse = uint32_t((0x100000000ull + unsigned(p.per_group) - 1) / unsigned(p.per_group));
   route_blocks(tokens, &p.blocks, &p.per_block);
   return type == TKG_TYPE_F32 ? launch_route<F32>(p, stream) : launch_route<BF16>(p, stream);
