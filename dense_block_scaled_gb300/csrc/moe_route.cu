@@ -26,13 +26,17 @@
 namespace tkg {
 namespace {
 
-// Warps per block: as many as the registers of a lane's run allow, for a token's choice is a long chain of short steps.
-template <int PER>
-constexpr int kRouteWarps = PER <= 8 ? 32 : 16;
+// Warps per block: as many as the registers of a lane's run allow, for a token's choice is a long chain of short steps;
+// and the blocks of an SM: two where BF16 logits decide by themselves (16384 x 128 15 us, with one 21; the others' FP32
+// choice takes 64 registers, and 16384 x 256 in groups 32 us with one, 37 in twice as many blocks).
+template <int PER, bool PACKED>
+constexpr int kRouteWarps = PER <= 8 || PACKED ? 32 : 16;
+template <int PER, bool PACKED>
+constexpr int kRouteOnSM = PACKED && PER <= 4 ? 2 : 1;
 constexpr int kRouteWords = 4;             // 32 tokens each, ranked at a time
 constexpr int kRouteTokens = 32 * kRouteWords;
 constexpr int kMaxRouteExperts = 512, kMaxTopk = 32, kMaxRouteGroups = 32;
-constexpr int kRouteBlocks = 152;          // blocks of tokens at most: one per SM
+constexpr int kSMs = 152;                  // (blocks of tokens at most: kRouteOnSM times as many)
 constexpr int kFewTopk = 16;               // choices for which the candidates are hardly ever more than 32
 constexpr int kRouteAlone = 64;            // tokens at most that one block takes alone
 constexpr int kPlaceThreads = 512, kPlaceEach = 7;
@@ -97,7 +101,34 @@ __device__ __forceinline__ float warp_most(float x) {
   return __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(x)));
 }
 __device__ __forceinline__ float exp_of(float x) { return expf(x); }
-__device__ __forceinline__ double exp_of(double x) { return exp(x); }
+// exp in 64 bits, without a branch, so that several run side by side (CUDA's took 1 us each here, one after the other), by
+// the reduction of Cody and Waite, log 2 in two parts, and the Taylor series:
+// x = n log 2 + r with |r| <= log(2) / 2, the series of e^r to r^13 (its rest is below 2^-58), and 2^n in two halves, as a
+// subnormal result takes two steps.  Infinities and NaN come out as they should: n is kept within what the halves can hold.
+__device__ __forceinline__ double exp_of(double x) {
+  const double top = 6755399441055744.0;   // 1.5 2^52: adding it rounds to a whole number
+  const double y = fma(fmin(fmax(x, -800.0), 800.0), 1.4426950408889634, top);
+  const int n = __double2loint(y);
+  const double m = y - top;
+  const double r = fma(m, -2.3190468138462996e-17, fma(m, -0.6931471805599453, fmin(fmax(x, -800.0), 800.0)));
+  double e = 1.0 / 6227020800.0;
+  e = fma(e, r, 1.0 / 479001600.0);
+  e = fma(e, r, 1.0 / 39916800.0);
+  e = fma(e, r, 1.0 / 3628800.0);
+  e = fma(e, r, 1.0 / 362880.0);
+  e = fma(e, r, 1.0 / 40320.0);
+  e = fma(e, r, 1.0 / 5040.0);
+  e = fma(e, r, 1.0 / 720.0);
+  e = fma(e, r, 1.0 / 120.0);
+  e = fma(e, r, 1.0 / 24.0);
+  e = fma(e, r, 1.0 / 6.0);
+  e = fma(e, r, 0.5);
+  e = fma(e, r, 1.0);
+  e = fma(e, r, 1.0);
+  const int h = n >> 1;
+  e = e * __hiloint2double((1023 + h) << 20, 0) * __hiloint2double((1023 + n - h) << 20, 0);
+  return x != x ? x : e;
+}
 
 // A lane's run of logits, in FP32; -inf past the end.  WIDE: rows allow loads of the whole run.
 template <int PER, typename L, bool WIDE>
@@ -216,7 +247,7 @@ __device__ __forceinline__ void choice_scores(const RouteParams& p, const float 
 #pragma unroll
     for (int i = 0; i < PER; ++i) c[i] = sigmoid_of(double(z[i])) + double(bias[i]);
   } else {
-    const double sum = softmax_sum(z, lane, p.experts, softmax_top(z), c, [](double x) { return exp(x); });
+    const double sum = softmax_sum(z, lane, p.experts, softmax_top(z), c, [](double x) { return exp_of(x); });
 #pragma unroll
     for (int i = 0; i < PER; ++i) c[i] = c[i] / sum + double(bias[i]);
   }
@@ -259,12 +290,146 @@ __device__ __forceinline__ void sort_run(uint32_t (&key)[PER]) {
   });
 }
 
-// Which of a lane's run are in the best groups (a bit each); `clear` is false where the values do not decide between two
-// groups, or one is not a number.  Each group has some lanes, its first holds its value: they are its runs' own, or read
-// it from `box` (a row per warp).
-template <int PER, typename F>
-__device__ __forceinline__ uint32_t keep_groups(const RouteParams& p, const F (&c)[PER], float wrong, int lane, F* box,
-                                                bool& clear) {
+template <typename L>
+__device__ __forceinline__ float logit_at(const RouteParams& p, int t, int e) {
+  const L* row = static_cast<const L*>(p.logits) + size_t(t) * p.ld;
+  if constexpr (sizeof(L) == 4)
+    return __ldcg(reinterpret_cast<const float*>(row) + e);
+  else
+    return __uint_as_float(uint32_t(__ldcg(reinterpret_cast<const unsigned short*>(row) + e)) << 16);
+}
+__device__ __forceinline__ float bias_at(const RouteParams& p, int e) { return p.bias ? __ldcg(p.bias + e) : 0.f; }
+
+// Candidates' scores (lane j < n: logit z) are made again in 64 bits.  These are slow here (16 cycles for an instruction of
+// an SM), and softmax has a sum over the row: that is first made of FP32 exponentials, whose arguments' roundings are put
+// back, added in 64 bits, so that it is off by little more than exp's 2 ulp, `kSumWrong` of itself.  It scales all
+// scores alike, so the order of two values c = s + b is right if they differ by more than that share of their
+// scores' difference; only else all of its terms are made in 64 bits.
+constexpr double kSumWrong = 0x1p-21;
+struct Again {
+  double score;
+  bool exact;
+};
+template <int PER, typename L>
+__device__ __forceinline__ Again score_again(const RouteParams& p, int t, float zj, int lane, bool exact) {
+  if (p.sigmoid) return {sigmoid_of(double(zj)), true};
+  float z[PER];
+#pragma unroll
+  for (int i = 0; i < PER; ++i) z[i] = lane * PER + i < p.experts ? logit_at<L>(p, t, lane * PER + i) : -INFINITY;
+  const float top = softmax_top(z);
+  double sum = 0.0;
+  if (exact) {
+#pragma unroll
+    for (int i = 0; i < PER; ++i) sum += exp_of(double(z[i]) - double(top));
+  } else {
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      const float x = z[i] - top, back = z[i] - x, lost = (z[i] - (x + back)) + (back - top);
+      const float e = expf(x);
+      sum += z[i] == -INFINITY ? 0.0 : double(fmaf(e, lost, e));
+    }
+  }
+  sum = warp_sum(sum);
+  return {exp_of(double(zj) - double(top)) / (sum == 0.0 ? 1.0 : sum), exact};
+}
+__device__ __forceinline__ bool in_order(const Again& by, double c0, double s0, double c1, double s1) {
+  return by.exact || fabs(c0 - c1) > fabs(s0 - s1) * kSumWrong;
+}
+
+// The order of n candidates (lane j < n: expert id) by their exact scores; lane j gets the j-th.  Rare: kept out of the
+// way of the registers of the rest.
+template <int PER, typename L>
+__device__ __noinline__ int order_again(const RouteParams& p, int t, int n, int id, int lane) {
+  const float z = lane < n ? logit_at<L>(p, t, id) : 0.f;
+  const float b = lane < n ? bias_at(p, id) : 0.f;
+  int out = 0;
+#pragma unroll 1
+  for (int turn = 0; turn < 2; ++turn) {
+    const Again by = score_again<PER, L>(p, t, z, lane, turn > 0);
+    const double c = by.score + double(b);
+    const unsigned long long mine = key_of(c);
+    int rank = 0, from = 0;
+#pragma unroll 1
+    for (int i = 0; i < n; ++i) {
+      const unsigned long long other = __shfl_sync(0xffffffffu, mine, i);
+      const int e = __shfl_sync(0xffffffffu, id, i);
+      rank += other > mine || (other == mine && e < id) ? 1 : 0;
+    }
+#pragma unroll 1
+    for (int i = 0; i < n; ++i)
+      if (__shfl_sync(0xffffffffu, rank, i) == lane) from = i;
+    out = __shfl_sync(0xffffffffu, id, from);
+    // lane j has the j-th: neighbours, but those of the same logit and bias, have to be in order
+    const double cj = __shfl_sync(0xffffffffu, c, from), sj = __shfl_sync(0xffffffffu, by.score, from);
+    const float zj = __shfl_sync(0xffffffffu, z, from), bj = __shfl_sync(0xffffffffu, b, from);
+    const double cn = __shfl_down_sync(0xffffffffu, cj, 1), sn = __shfl_down_sync(0xffffffffu, sj, 1);
+    const float zn = __shfl_down_sync(0xffffffffu, zj, 1), bn = __shfl_down_sync(0xffffffffu, bj, 1);
+    const bool fine = lane + 1 >= n || in_order(by, cj, sj, cn, sn) || (zj == zn && bj == bn);
+    if (by.exact || __all_sync(0xffffffffu, fine)) break;
+  }
+  return out;
+}
+
+// Which groups stay, where FP32 does not tell: `open` of those that the n candidates for their two largest scores (lane j <
+// n: expert id) are of.  Returns a bit per group's first lane.
+template <int PER, typename L>
+__device__ __noinline__ uint32_t groups_again(const RouteParams& p, int t, int n, int id, int open, int shift, int lane) {
+  const float z = lane < n ? logit_at<L>(p, t, id) : 0.f;
+  const double b = lane < n ? double(bias_at(p, id)) : 0.0;
+  const int g = p.group_of(id);
+  uint32_t stay = 0;
+#pragma unroll 1
+  for (int turn = 0; turn < 2; ++turn) {
+    const Again by = score_again<PER, L>(p, t, z, lane, turn > 0);
+    const double c = by.score + b;
+    const unsigned long long mine = key_of(c);
+    int rank = 0;   // within its group
+    bool fine = true;
+#pragma unroll 1
+    for (int i = 0; i < n; ++i) {
+      const unsigned long long other = __shfl_sync(0xffffffffu, mine, i);
+      const double ci = __shfl_sync(0xffffffffu, c, i), si = __shfl_sync(0xffffffffu, by.score, i);
+      const int gi = __shfl_sync(0xffffffffu, g, i), e = __shfl_sync(0xffffffffu, id, i);
+      if (gi == g && e != id) {
+        rank += other > mine || (other == mine && e < id) ? 1 : 0;
+        fine &= in_order(by, c, by.score, ci, si);
+      }
+    }
+    const bool counts = lane < n && rank < 2, leads = lane < n && rank == 0;
+    double two = 0.0, scores = 0.0;   // of the group
+#pragma unroll 1
+    for (int i = 0; i < n; ++i) {
+      const double ci = __shfl_sync(0xffffffffu, counts ? c : 0.0, i);
+      const double si = __shfl_sync(0xffffffffu, counts ? by.score : 0.0, i);
+      if (__shfl_sync(0xffffffffu, g, i) == g) {
+        two += ci;
+        scores += si;
+      }
+    }
+    const unsigned long long whole = key_of(two);
+    int before = 0;   // groups before its group
+#pragma unroll 1
+    for (int i = 0; i < n; ++i) {
+      const int gi = __shfl_sync(0xffffffffu, leads ? g : -1, i);
+      const unsigned long long other = __shfl_sync(0xffffffffu, whole, i);
+      const double ti = __shfl_sync(0xffffffffu, two, i), si = __shfl_sync(0xffffffffu, scores, i);
+      if (gi >= 0 && gi != g) {
+        before += other > whole || (other == whole && gi < g) ? 1 : 0;
+        fine &= in_order(by, two, scores, ti, si);
+      }
+    }
+    stay = __reduce_or_sync(0xffffffffu, leads && before < open ? 1u << (g << shift) : 0u);
+    if (by.exact || __all_sync(0xffffffffu, fine || lane >= n)) break;
+  }
+  return stay;
+}
+
+// Which of a lane's run are in the best groups (a bit each); `clear` is false where that is not decided, or a value is not
+// a number.  Each group has some lanes, its first holds its value: they are its runs' own, or read it from `box` (a row per
+// warp).  `few`: places for candidates, or null.
+template <int PER, typename L, typename F>
+__device__ __forceinline__ uint32_t keep_groups(const RouteParams& p, int t, const F (&c)[PER], float wrong, int lane, F* box,
+                                                float2* few, bool& clear) {
   using K = decltype(key_of(F(0)));
   const int per = p.lanes_per_group, shift = __popc(per - 1);
   const int g = lane >> shift;
@@ -311,70 +476,58 @@ __device__ __forceinline__ uint32_t keep_groups(const RouteParams& p, const F (&
     const K other = __shfl_sync(0xffffffffu, mine, o << shift);
     rank += other > mine || (other == mine && o < g) ? 1 : 0;
   }
-  const uint32_t stay = __ballot_sync(0xffffffffu, holds && rank < p.topk_groups);
+  uint32_t stay = __ballot_sync(0xffffffffu, holds && rank < p.topk_groups);
   // the last group that stays and the first that goes: each sum of two is off by both's error and its rounding
   const uint32_t in = __ballot_sync(0xffffffffu, holds && rank == p.topk_groups - 1);
   const uint32_t out = __ballot_sync(0xffffffffu, holds && rank == p.topk_groups);
   const F last = __shfl_sync(0xffffffffu, sum, __ffs(int(in)) - 1), first = __shfl_sync(0xffffffffu, sum, __ffs(int(out)) - 1);
-  clear = float(last - first) > 4.f * wrong + (fabsf(float(last)) + fabsf(float(first))) * 0x1p-24f;
+  const float margin = 4.f * wrong + (fabsf(float(last)) + fabsf(float(first))) * 0x1p-23f;
+  clear = float(last - first) > margin;
+  if constexpr (sizeof(F) == 4) {
+    if (!clear && p.whole_runs && few && fabsf(last) < INFINITY && fabsf(first) < INFINITY &&
+        !__any_sync(0xffffffffu, lost != 0)) {
+      // groups that are clearly above the first that goes stay, those clearly below the last that stays go; the others'
+      // candidates for their two largest are made again
+      const uint32_t sure = __ballot_sync(0xffffffffu, holds && sum - first > margin);
+      const uint32_t near = __ballot_sync(0xffffffffu, holds && !(sum - first > margin) && !(last - sum > margin));
+      const bool mine_near = (near >> (g << shift)) & 1u;
+      const float least = (p.per_group > 1 ? b : a) - 2.f * wrong;
+      int count = 0;
+#pragma unroll
+      for (int i = 0; i < PER; ++i) count += mine_near && c[i] >= least ? 1 : 0;
+      const int n = __reduce_add_sync(0xffffffffu, count);
+      if (n <= 32) {
+        int upto = count;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const int y = __shfl_up_sync(0xffffffffu, upto, o);
+          if (lane >= o) upto += y;
+        }
+        float2* to = few + (upto - count);
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < PER; ++i)
+          if (mine_near && c[i] >= least) *to++ = make_float2(0.f, __int_as_float(lane * PER + i));
+        __syncwarp();
+        const int id = lane < n ? __float_as_int(few[lane].y) : 0;
+        stay = sure | groups_again<PER, L>(p, t, n, id, p.topk_groups - __popc(sure), shift, lane);
+        clear = true;
+      }
+    }
+  }
   if (p.whole_runs) return (stay >> (g << shift)) & 1u ? 0xffffffffu : 0u;
   uint32_t kept = 0;
-  int of = p.group_of(lane * PER), left = (of + 1) * p.per_group - lane * PER;   // a run's groups
+  int in_group = p.group_of(lane * PER), left = (in_group + 1) * p.per_group - lane * PER;   // a run's groups
 #pragma unroll
   for (int i = 0; i < PER; ++i) {
     if (left == 0) {
-      ++of;
+      ++in_group;
       left = p.per_group;
     }
     --left;
-    if (lane * PER + i < p.experts) kept |= ((stay >> (of << shift)) & 1u) << i;
+    if (lane * PER + i < p.experts) kept |= ((stay >> (in_group << shift)) & 1u) << i;
   }
   return kept;
-}
-
-template <typename L>
-__device__ __forceinline__ float logit_at(const RouteParams& p, int t, int e) {
-  const L* row = static_cast<const L*>(p.logits) + size_t(t) * p.ld;
-  if constexpr (sizeof(L) == 4)
-    return __ldcg(reinterpret_cast<const float*>(row) + e);
-  else
-    return __uint_as_float(uint32_t(__ldcg(reinterpret_cast<const unsigned short*>(row) + e)) << 16);
-}
-__device__ __forceinline__ float bias_at(const RouteParams& p, int e) { return p.bias ? __ldcg(p.bias + e) : 0.f; }
-
-// The order of n candidates (lane j < n: expert id) by their exact scores; lane j gets the j-th.  Rare: kept out of the
-// way of the registers of the rest.
-template <typename L>
-__device__ __noinline__ int order_again(const RouteParams& p, int t, int n, int id, int lane) {
-  double c = 0.0;
-  const float z = lane < n ? logit_at<L>(p, t, id) : 0.f;
-  const float b = lane < n ? bias_at(p, id) : 0.f;
-  if (p.sigmoid) {
-    c = sigmoid_of(double(z)) + double(b);
-  } else {
-    float top = -INFINITY;
-    for (int e = lane; e < p.experts; e += 32) top = fmaxf(top, logit_at<L>(p, t, e));
-    top = warp_fmax(top);
-    const double sub = top == -INFINITY ? 0.0 : double(top);
-    double sum = 0.0;
-    for (int e = lane; e < p.experts; e += 32) sum += exp(double(logit_at<L>(p, t, e)) - sub);
-    sum = warp_sum(sum);
-    c = exp(double(z) - sub) / (sum == 0.0 ? 1.0 : sum) + double(b);
-  }
-  const unsigned long long mine = key_of(c);
-  int rank = 0, out = 0;
-#pragma unroll 1
-  for (int i = 0; i < n; ++i) {
-    const unsigned long long other = __shfl_sync(0xffffffffu, mine, i);
-    const int e = __shfl_sync(0xffffffffu, id, i);
-    rank += other > mine || (other == mine && e < id) ? 1 : 0;
-  }
-#pragma unroll 1
-  for (int i = 0; i < n; ++i) {
-    const int r = __shfl_sync(0xffffffffu, rank, i), e = __shfl_sync(0xffffffffu, id, i);
-    if (r == lane) out = e;
-  }
-  return out;
 }
 
 // Whether two experts have the same logit and bias, so the same score.
@@ -436,7 +589,7 @@ __device__ __forceinline__ int choose_few(const RouteParams& p, int t, const flo
     const bool near = lane + 1 < n && next.x >= few[p.topk - 1].x - margin && !(me.x - next.x > margin);
     if (__any_sync(0xffffffffu, near)) {
       const bool close = near && !same_score<L>(p, t, id, __float_as_int(next.y));
-      if (__any_sync(0xffffffffu, close)) id = order_again<L>(p, t, n, id, lane);
+      if (__any_sync(0xffffffffu, close)) id = order_again<PER, L>(p, t, n, id, lane);
     }
   }
   return id;
@@ -502,7 +655,7 @@ __device__ __forceinline__ int choose_any(const RouteParams& p, int t, const F (
     }
   }
   if constexpr (sizeof(K) == 4)
-    if (close) id = order_again<L>(p, t, j, id, lane);
+    if (close) id = order_again<PER, L>(p, t, j, id, lane);
   return id;
 }
 
@@ -536,7 +689,7 @@ __device__ __forceinline__ int choose_packed(const RouteParams& p, const float (
 // The choice where choose_few does not apply: rare, and kept out of the way of the registers of the rest.
 template <int PER, typename L>
 __device__ __noinline__ int choose_slowly(const RouteParams& p, int t, bool by_logit, const float* s_bias, float most_bias,
-                                          int lane, double* box) {
+                                          int lane, double* box, float2* few) {
   float z[PER];
   bool clear = true;
 #pragma unroll
@@ -550,7 +703,7 @@ __device__ __noinline__ int choose_slowly(const RouteParams& p, int t, bool by_l
     float c[PER], wrong;
     uint32_t kept = 0xffffffffu;
     choice_scores(p, z, s_bias, lane, most_bias, c, wrong);
-    if (limited) kept = keep_groups(p, c, wrong, lane, reinterpret_cast<float*>(box), clear);
+    if (limited) kept = keep_groups<PER, L>(p, t, c, wrong, lane, reinterpret_cast<float*>(box), few, clear);
     const int id = clear ? choose_any<PER, L>(p, t, c, kept, wrong, lane) : -1;
     if (__shfl_sync(0xffffffffu, id, 0) >= 0) return id;
   }
@@ -560,13 +713,13 @@ __device__ __noinline__ int choose_slowly(const RouteParams& p, int t, bool by_l
 #pragma unroll
   for (int i = 0; i < PER; ++i) bias[i] = s_bias[lane * PER + i];
   choice_scores(p, z, bias, lane, c);
-  if (limited) kept = keep_groups(p, c, 0.f, lane, box, clear);
+  if (limited) kept = keep_groups<PER, L>(p, t, c, 0.f, lane, box, nullptr, clear);
   return choose_any<PER, L>(p, t, c, kept, -1.f, lane);
 }
 
 // BY_LOGIT: no bias and no limit to groups.
 template <int PER, typename L, bool WIDE, bool BY_LOGIT>
-__global__ void __launch_bounds__(32 * kRouteWarps<PER>) route_choose_kernel(const RouteParams p) {
+__global__ void __launch_bounds__(32 * kRouteWarps<PER, BY_LOGIT && sizeof(L) == 2>) route_choose_kernel(const RouteParams p) {
   constexpr bool kPacked = BY_LOGIT && sizeof(L) == 2;
   extern __shared__ int s_dyn[];
   // bits of the tokens that chose an expert, how many did before, each expert's first row (one block of tokens), and, for
@@ -577,7 +730,7 @@ __global__ void __launch_bounds__(32 * kRouteWarps<PER>) route_choose_kernel(con
   ptx::pdl_launch_dependents();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   __shared__ __align__(16) float s_bias[BY_LOGIT ? 4 : 32 * PER];
-  __shared__ float2 s_few[kPacked ? 1 : kRouteWarps<PER>][32];
+  __shared__ float2 s_few[kPacked ? 1 : kRouteWarps<PER, kPacked>][32];
   int* s_ids = s_count + p.experts;                          // [kRouteTokens][topk]
   const int tokens_there = min(kRouteTokens, p.per_block), warps = blockDim.x >> 5;
   double* box = reinterpret_cast<double*>(s_dyn + (p.experts * (kRouteWords + 1) + tokens_there * p.topk + 1) / 2 * 2) +
@@ -637,14 +790,15 @@ __global__ void __launch_bounds__(32 * kRouteWarps<PER>) route_choose_kernel(con
           if constexpr (!BY_LOGIT) {
             choice_scores(p, z, s_bias, lane, most_bias, c, wrong);
             uint32_t kept = 0xffffffffu;
-            if (p.topk_groups < p.groups) kept = keep_groups(p, c, wrong, lane, reinterpret_cast<float*>(box), clear);
+            if (p.topk_groups < p.groups)
+              kept = keep_groups<PER, L>(p, t, c, wrong, lane, reinterpret_cast<float*>(box), s_few[warp], clear);
 #pragma unroll
             for (int k = 0; k < PER; ++k)
               if (lane * PER + k >= p.experts || !((kept >> k) & 1u)) c[k] = -INFINITY;
           }
           id = clear && p.topk <= kFewTopk ? choose_few<PER, L>(p, t, c, wrong, lane, s_few[warp], zj) : -1;
           const bool slow = __shfl_sync(0xffffffffu, id, 0) < 0;
-          if (slow) id = choose_slowly<PER, L>(p, t, BY_LOGIT, s_bias, most_bias, lane, box);
+          if (slow) id = choose_slowly<PER, L>(p, t, BY_LOGIT, s_bias, most_bias, lane, box, s_few[warp]);
           if (!BY_LOGIT || slow) zj = logit_at<L>(p, t, id);
         }
         // lane j: its expert's score
@@ -975,10 +1129,10 @@ tkg_status with_run(int experts, const void* a, size_t lda, const void* b, size_
   return pick(std::integral_constant<int, 16>{});
 }
 
-// Tokens in one block while that takes less time than a second kernel; past that, blocks of 32 at least, one per SM,
+// Tokens in one block while that takes less time than a second kernel; past that, blocks of 32 at least, `most` of them,
 // and of no more than 16 bits can count.
-void route_blocks(int tokens, int* blocks, int* per_block) {
-  *per_block = tokens <= kRouteAlone ? (tokens + 31) / 32 * 32 : ceil_div(ceil_div(tokens, kRouteBlocks), 32) * 32;
+void route_blocks(int tokens, int most, int* blocks, int* per_block) {
+  *per_block = tokens <= kRouteAlone ? (tokens + 31) / 32 * 32 : ceil_div(ceil_div(tokens, most), 32) * 32;
   if (*per_block > 65504) *per_block = 65504;
   *blocks = ceil_div(tokens, *per_block);
 }
@@ -1005,11 +1159,14 @@ tkg_status launch_route(RouteParams p, cudaStream_t stream) {
       p.lanes_per_group = runs;
     else
       while (2 * p.lanes_per_group * p.groups <= 32) p.lanes_per_group *= 2;
+    const bool by_logit = !p.bias && p.topk_groups == p.groups;
+    const bool packed = by_logit && sizeof(L) == 2;
+    const int most_warps = packed ? kRouteWarps<PER, true> : kRouteWarps<PER, false>;
+    route_blocks(p.tokens, kSMs * (packed ? kRouteOnSM<PER, true> : kRouteOnSM<PER, false>), &p.blocks, &p.per_block);
     const int there = p.per_block < kRouteTokens ? p.per_block : kRouteTokens;
     unsigned smem = unsigned((p.experts * (kRouteWords + 1) + there * p.topk + 1) / 2 * 2) * 4u;
     // values of the groups' choice, one row per warp, as large as its second time in 64 bits needs
-    if (p.topk_groups < p.groups && !p.whole_runs) smem += unsigned(kRouteWarps<PER> * (p.experts + p.experts / 32 + 1)) * 8u;
-    const bool by_logit = !p.bias && p.topk_groups == p.groups;
+    if (p.topk_groups < p.groups && !p.whole_runs) smem += unsigned(most_warps * (p.experts + p.experts / 32 + 1)) * 8u;
     auto kern = by_logit ? route_choose_kernel<PER, L, decltype(wide)::value, true>
                          : route_choose_kernel<PER, L, decltype(wide)::value, false>;
     if (smem > 36000) {   // (beside 10 KB of its own)
@@ -1025,7 +1182,7 @@ tkg_status launch_route(RouteParams p, cudaStream_t stream) {
         set[dev] = true;
       }
     }
-    const int warps = p.tokens < 4 ? 4 : (p.tokens < kRouteWarps<PER> ? p.tokens : kRouteWarps<PER>);
+    const int warps = p.tokens < 4 ? 4 : (p.tokens < most_warps ? p.tokens : most_warps);
     tkg_status st = launch_small(kern, dim3(unsigned(p.blocks)), dim3(32u * unsigned(warps)), stream, smem, p);
     if (st != TKG_OK || p.blocks == 1) return st;
     int each = kPlaceEntries / (p.per_block * p.topk);
@@ -1045,7 +1202,7 @@ extern "C" {
 size_t tkg_moe_route_workspace_bytes(int tokens, int experts) {
   if (tokens < 0 || experts < 1 || experts > kMaxRouteExperts || tokens > kMaxSize) return 0;
   int blocks = 0, per_block = 0;
-  if (tokens > 0) route_blocks(tokens, &blocks, &per_block);
+  if (tokens > 0) route_blocks(tokens, 2 * kSMs, &blocks, &per_block);   // the most there can be
   return size_t(blocks > 1 ? blocks : 0) * size_t((experts + 7) / 8 * 8) * 2 + 16;
 }
 
@@ -1092,7 +1249,6 @@ tkg_status tkg_moe_route(int tokens, int experts, int topk, const void* logits, 
   p.slots = slots;
   p.counts = static_cast<uint16_t*>(workspace);
   p.inverse = uint32_t((0x100000000ull + unsigned(p.per_group) - 1) / unsigned(p.per_group));
-  route_blocks(tokens, &p.blocks, &p.per_block);
   return type == TKG_TYPE_F32 ? launch_route<F32>(p, stream) : launch_route<BF16>(p, stream);
 }
 

@@ -166,6 +166,33 @@ def test_choices_that_fp32_does_not_decide(scores, groups, stay):
     assert not torch.equal(order(wrong)[0, :8], ids[0].long()) or groups > 1
 
 
+@pytest.mark.parametrize("scores", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("experts,groups,stay,topk", [(256, 8, 4, 8), (128, 8, 3, 4), (64, 32, 5, 4), (60, 6, 2, 4), (24, 24, 3, 3)])
+def test_groups_that_fp32_does_not_decide(scores, experts, groups, stay, topk):
+    # biases that make the groups' sums of two all but equal, a few members' or all; rows alike but for tiny differences
+    per = experts // groups
+    z = normal(1, experts, seed=6, scale=0.5)
+    s = scores_of(z.to(F64), scores)[0].unflatten(0, (groups, per))
+    two = s.sort(dim=1, descending=True).values[:, :2].sum(dim=1)
+    bias = ((2.0 - two) / min(2, per))[:, None].expand(-1, per).flatten().to(F32)
+    rows = z.repeat(200, 1)
+    rows[100:] += normal(100, experts, seed=7, scale=1e-6)
+    check(rows, topk, bias=bias, scores=scores, groups=groups, topk_groups=stay)
+    spread = bias + normal(experts, seed=8, scale=0.3) * (torch.arange(experts, device="cuda") // per % 2)
+    check(rows, topk, bias=spread, scores=scores, groups=groups, topk_groups=stay)
+    level = (1.0 - s.flatten()).to(F32)          # every expert all but equal
+    check(rows, topk, bias=level, scores=scores, groups=groups, topk_groups=stay)
+
+
+@pytest.mark.parametrize("seed", range(4))
+@pytest.mark.parametrize("scores", ["softmax", "sigmoid"])
+def test_many_rows_with_a_bias(scores, seed):
+    # of 30000 rows a few hundred have two scores that FP32 does not tell apart
+    check(normal(30000, 256, seed=seed), 8, bias=normal(256, scale=0.05, seed=seed), scores=scores)
+    check(normal(30000, 256, seed=seed), 8, bias=normal(256, scale=0.05, seed=seed), scores=scores, groups=8, topk_groups=4)
+    check(normal(30000, 128, seed=seed), 6, scores=scores, groups=8, topk_groups=4, renormalise=False)
+
+
 def test_logits_closer_than_scores_tell():
     # distinct logits whose FP32 (and 64-bit) scores are equal: the logits decide
     z = torch.full((3, 64), -200.0, device="cuda")
