@@ -248,7 +248,7 @@ class Product:
         A, o = self.A(), 0
         for i, m in enumerate(self.sizes):
             d, a = self.dD[o:o + m].to(F64), A[o:o + m]
-            ref, mag = alpha * (d.T @ a), alpha * (d.abs().T @ a.abs())
+            ref, mag = alpha * (d.T @ a), abs(alpha) * (d.abs().T @ a.abs())
             room = 1e-5 * mag + (2.0 ** -7 if dtype == BF16 else 2.0 ** -23) * ref.abs()
             assert ((dB[i].to(F64) - ref).abs() <= room).all(), i
             o += m

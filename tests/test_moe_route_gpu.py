@@ -44,8 +44,12 @@ def choice(logits, topk, scores="softmax", bias=None, groups=1, topk_groups=1, k
         by = c.unflatten(1, (groups, -1))
         best = by.sort(dim=2, descending=True).values[:, :, :2].sum(dim=2)
         stay = torch.zeros_like(best, dtype=torch.bool).scatter_(1, order(best)[:, :topk_groups], True)
-        c = torch.where(stay[:, :, None], by, torch.full_like(by, -torch.inf)).flatten(1)
-    ids = order(c)[:, :topk]
+        # of the groups that stay alone: one of their experts may have -inf itself
+        ids = order(c)
+        inside = stay.repeat_interleave(by.shape[2], dim=1).gather(1, ids)
+        ids = ids.gather(1, torch.sort(inside.to(torch.int8), dim=1, descending=True, stable=True).indices)[:, :topk]
+    else:
+        ids = order(c)[:, :topk]
     return ids if keep is None else torch.where(keep[:, None].bool(), ids, -1)
 
 
@@ -229,6 +233,32 @@ def test_nan_comes_last():
     assert w[4].isnan().all() and torch.equal(ids.long(), choice(z, 8))
     ids, w, *_ = route(z, 8, renormalise=False)
     assert w.isnan().all()
+
+
+@pytest.mark.parametrize("groups,stay", [(1, 1), (8, 3), (4, 4)])
+@pytest.mark.parametrize("scores", ["softmax", "sigmoid"])
+def test_infinite_and_far_biases(scores, groups, stay):
+    kw = dict(scores=scores, groups=groups, topk_groups=stay)
+    z = normal(100, 64)
+    out = torch.zeros(64, device="cuda")
+    out[::3] = -torch.inf                       # experts out of service, more than are left to choose in some groups
+    check(z, 6, bias=out, **kw)
+    check(z, 20, bias=out, **kw)
+    out[5] = torch.inf
+    check(z, 6, bias=out, **kw)
+    check(z, 6, bias=torch.where(out == -torch.inf, -1e30, normal(64, scale=1e3)), **kw)
+    out[7] = float("nan")
+    ids, *_ = route(z, 6, bias=out, **kw)
+    if groups == 1:
+        assert torch.equal(ids.long(), choice(z, 6, bias=out, **kw))
+    z[3, 9] = torch.inf
+    z[4] = torch.inf
+    z[5, :60] = float("nan")
+    out = torch.zeros(64, device="cuda")
+    ids, w, sizes, rows, slots = route(z, 6, bias=out, **kw)
+    assert ((ids >= 0) & (ids < 64)).all() and int(sizes.sum()) == 600 and (ids.sort(dim=1).values.diff(dim=1) > 0).all()
+    if scores == "sigmoid" and groups == 1:
+        assert torch.equal(ids.long(), choice(z, 6, bias=out, **kw))
 
 
 @pytest.mark.parametrize("dtype", [BF16, F32], ids=["bf16", "f32"])
