@@ -1,5 +1,4 @@
-// moe_route.cu -- routing of tokens to experts: scores, choice, weights, and each choice's row in expert order; and the
-// weights' gradient to the router's logits.
+// moe_route.cu -- routing of tokens to experts: scores, choice, weights, and each choice's row in expert order.
 //
 //   s = softmax(z) or sigmoid(z)  (a row of logits per token),  c = s + bias
 //   the topk_groups groups (consecutive experts) with the largest sum of their two largest c stay; of their experts the
@@ -21,7 +20,7 @@
 // and bias, the candidates are ordered again in 64 bits, so that the choice is that of the exact scores.
 #include <cfloat>
 
-#include "train_host.cuh"
+#include "moe_route.cuh"
 
 namespace tkg {
 namespace {
@@ -35,36 +34,11 @@ template <int PER, bool PACKED>
 constexpr int kRouteOnSM = PACKED && PER <= 4 ? 2 : 1;
 constexpr int kRouteWords = 4;             // 32 tokens each, ranked at a time
 constexpr int kRouteTokens = 32 * kRouteWords;
-constexpr int kMaxRouteExperts = 512, kMaxTopk = 32, kMaxRouteGroups = 32;
 constexpr int kSMs = 152;                  // (blocks of tokens at most: kRouteOnSM times as many)
 constexpr int kFewTopk = 16;               // choices for which the candidates are hardly ever more than 32
 constexpr int kRouteAlone = 64;            // tokens at most that one block takes alone
 constexpr int kPlaceThreads = 512, kPlaceEach = 7;
 constexpr int kPlaceEntries = 1024;        // choices that a placing block takes, about
-
-struct RouteParams {
-  int tokens, experts, topk;
-  int groups, per_group, topk_groups;
-  int lanes_per_group, whole_runs;   // a group is that many lanes' runs; otherwise that many lanes read it
-  uint32_t inverse;           // ceil(2^32 / per_group): e / per_group is the high word of e * inverse (e < 512)
-  __device__ __forceinline__ int group_of(int e) const {
-    return per_group == 1 ? e : int(__umulhi(uint32_t(e), inverse));
-  }
-  int sigmoid, renormalise;
-  float scale;
-  const void* logits;
-  size_t ld;                  // elements
-  const float* bias;          // may be null
-  const uint8_t* keep;        // may be null
-  int* ids;
-  float* weights;
-  int* sizes;
-  int* rows;
-  int* slots;
-  uint16_t* counts;           // [blocks][experts, rounded up to 8]
-  int per_block;              // tokens, a multiple of 32
-  int blocks;
-};
 
 // Keys that are ordered as the values: NaN below every number, 0 is no value at all.  (x + 0: -0 is 0.)
 __device__ __forceinline__ uint32_t key_of(float x) {
@@ -84,17 +58,6 @@ __device__ __forceinline__ unsigned long long warp_max(unsigned long long k) {
   const uint32_t hi = __reduce_max_sync(0xffffffffu, uint32_t(k >> 32));
   const uint32_t lo = __reduce_max_sync(0xffffffffu, uint32_t(k >> 32) == hi ? uint32_t(k) : 0u);
   return ((unsigned long long)hi << 32) | lo;
-}
-template <typename F>
-__device__ __forceinline__ F warp_sum(F x) {
-#pragma unroll
-  for (int o = 16; o; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
-  return x;
-}
-__device__ __forceinline__ float warp_fmax(float x) {
-#pragma unroll
-  for (int o = 16; o; o >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
-  return x;
 }
 // (of numbers that are not negative)
 __device__ __forceinline__ float warp_most(float x) {
@@ -130,59 +93,6 @@ __device__ __forceinline__ double exp_of(double x) {
   return x != x ? x : e;
 }
 
-// A lane's run of logits, in FP32; -inf past the end.  WIDE: rows allow loads of the whole run.
-template <int PER, typename L, bool WIDE>
-__device__ __forceinline__ void load_run(const L* row, int lane, int experts, float (&z)[PER]) {
-  constexpr int kBytes = PER * int(sizeof(L));
-  const int e0 = lane * PER;
-  if constexpr (WIDE) {   // experts is a multiple of PER
-    constexpr int kWords = kBytes / 4;
-    uint32_t w[kWords > 0 ? kWords : 1] = {};
-    if (e0 < experts) {
-      if constexpr (kBytes >= 16) {
-#pragma unroll
-        for (int i = 0; i < kBytes / 16; ++i) {
-          const uint4 v = __ldcg(reinterpret_cast<const uint4*>(row + e0) + i);
-          w[4 * i] = v.x, w[4 * i + 1] = v.y, w[4 * i + 2] = v.z, w[4 * i + 3] = v.w;
-        }
-      } else if constexpr (kBytes == 8) {
-        const uint2 v = __ldcg(reinterpret_cast<const uint2*>(row + e0));
-        w[0] = v.x, w[1] = v.y;
-      } else {
-        w[0] = __ldcg(reinterpret_cast<const unsigned int*>(row + e0));
-      }
-    }
-#pragma unroll
-    for (int i = 0; i < PER; ++i) {
-      if constexpr (sizeof(L) == 4)
-        z[i] = __uint_as_float(w[i]);
-      else
-        z[i] = __uint_as_float((i & 1) ? (w[i / 2] & 0xffff0000u) : (w[i / 2] << 16));
-      if (e0 >= experts) z[i] = -INFINITY;
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < PER; ++i) {
-      z[i] = -INFINITY;
-      if (e0 + i < experts) {
-        if constexpr (sizeof(L) == 4)
-          z[i] = __ldcg(reinterpret_cast<const float*>(row) + e0 + i);
-        else
-          z[i] = __uint_as_float(uint32_t(__ldcg(reinterpret_cast<const unsigned short*>(row) + e0 + i)) << 16);
-      }
-    }
-  }
-}
-
-// What is subtracted from a row's logits (their maximum, or 0 for a row of nothing but -inf).
-template <int PER>
-__device__ __forceinline__ float softmax_top(const float (&z)[PER]) {
-  float top = z[0];
-#pragma unroll
-  for (int i = 1; i < PER; ++i) top = fmaxf(top, z[i]);
-  top = warp_fmax(top);
-  return top == -INFINITY ? 0.f : top;
-}
 // The exponentials of a lane's run and their sum over the row: 1 where all of them are 0.
 template <int PER, typename F, typename E>
 __device__ __forceinline__ F softmax_sum(const float (&z)[PER], int lane, int experts, float top, F (&e)[PER], E&& exponential) {
@@ -290,14 +200,6 @@ __device__ __forceinline__ void sort_run(uint32_t (&key)[PER]) {
   });
 }
 
-template <typename L>
-__device__ __forceinline__ float logit_at(const RouteParams& p, int t, int e) {
-  const L* row = static_cast<const L*>(p.logits) + size_t(t) * p.ld;
-  if constexpr (sizeof(L) == 4)
-    return __ldcg(reinterpret_cast<const float*>(row) + e);
-  else
-    return __uint_as_float(uint32_t(__ldcg(reinterpret_cast<const unsigned short*>(row) + e)) << 16);
-}
 __device__ __forceinline__ float bias_at(const RouteParams& p, int e) { return p.bias ? __ldcg(p.bias + e) : 0.f; }
 
 // Candidates' scores (lane j < n: logit z) are made again in 64 bits.  These are slow here (16 cycles for an instruction of
@@ -980,171 +882,12 @@ __global__ void __launch_bounds__(kPlaceThreads) route_place_kernel(const RouteP
     place(i, __ldcg(p.ids + i), __ldcg(p.rows + i));
 }
 
-// dz of one token per warp.  With a_j the chosen scores, da_j their gradients:
-//   plain          da_j = scale dw_j
-//   renormalised   da_j = scale / A (dw_j - sum_i dw_i a_i / A),  A = sum_i a_i
-//   softmax        dz_e = s_e (da_e - sum_j da_j a_j);  renormalised that sum is 0 and
-//                  dz_j = scale p_j (dw_j - sum_i dw_i p_i) with p the softmax of the chosen alone
-//   sigmoid        dz_e = da_e s_e (1 - s_e)
-template <int PER, typename L, bool WIDE>
-__global__ void __launch_bounds__(256) route_grad_kernel(const RouteParams p, const float* dweights, void* dlogits,
-                                                         size_t ldd) {
-  ptx::pdl_launch_dependents();
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int t = blockIdx.x * 8 + warp;
-  if (t >= p.tokens) return;
-  ptx::pdl_wait();
-  const bool mine = lane < p.topk;
-  const int id = mine ? __ldcg(p.ids + size_t(t) * p.topk + lane) : -1;
-  const bool chosen = id >= 0 && id < p.experts;
-  const L* row = static_cast<const L*>(p.logits) + size_t(t) * p.ld;
-  const float dw = chosen ? __ldcg(dweights + size_t(t) * p.topk + lane) : 0.f;
-  float zj = -INFINITY;
-  if (chosen) {
-    if constexpr (sizeof(L) == 4)
-      zj = __ldcg(reinterpret_cast<const float*>(row) + id);
-    else
-      zj = __uint_as_float(uint32_t(__ldcg(reinterpret_cast<const unsigned short*>(row) + id)) << 16);
-  }
-  const bool full = !p.sigmoid && !p.renormalise && __any_sync(0xffffffffu, chosen);   // every logit has a gradient
-  float out[PER];
-  float dz = 0.f;   // lane j: of the j-th choice
-#pragma unroll
-  for (int i = 0; i < PER; ++i) out[i] = 0.f;
-  if (full) {
-    float z[PER], top;
-    load_run<PER, L, WIDE>(row, lane, p.experts, z);
-    top = z[0];
-#pragma unroll
-    for (int i = 1; i < PER; ++i) top = fmaxf(top, z[i]);
-    top = warp_fmax(top);
-    const float sub = top == -INFINITY ? 0.f : top;
-    float sum = 0.f;
-#pragma unroll
-    for (int i = 0; i < PER; ++i) {
-      out[i] = expf(z[i] - sub);
-      sum += lane * PER + i < p.experts ? out[i] : 0.f;
-    }
-    sum = warp_sum(sum);
-    if (sum == 0.f) sum = 1.f;
-    const float inv = __fdiv_rn(1.f, sum);
-    const float a = chosen ? expf(zj - sub) * inv : 0.f;
-    const float da = dw * p.scale;
-    const float dot = warp_sum(chosen ? da * a : 0.f);
-#pragma unroll
-    for (int i = 0; i < PER; ++i) out[i] = -(out[i] * inv) * dot;
-    dz = a * (da - dot);
-  } else if (!p.sigmoid) {
-    const float top = warp_fmax(zj);
-    const float e = chosen ? expf(zj - (top == -INFINITY ? 0.f : top)) : 0.f;
-    const float sum = warp_sum(e);
-    const float pj = sum == 0.f ? 0.f : __fdiv_rn(e, sum);
-    const float dot = warp_sum(chosen ? pj * dw : 0.f);
-    dz = p.scale * pj * (dw - dot);
-  } else {
-    const float a = chosen ? __fdiv_rn(1.f, 1.f + expf(-zj)) : 0.f;
-    const float b = chosen ? __fdiv_rn(1.f, 1.f + expf(zj)) : 0.f;   // 1 - a, also where a rounds to 1
-    float da = dw * p.scale;
-    if (p.renormalise) {
-      const float sum = warp_sum(a);
-      const float pj = sum == 0.f ? 0.f : __fdiv_rn(a, sum);
-      const float dot = warp_sum(chosen ? pj * dw : 0.f);
-      dz = p.scale * pj * (dw - dot) * b;
-    } else {
-      dz = da * a * b;
-    }
-  }
-  const uint32_t who = __ballot_sync(0xffffffffu, chosen);
-#pragma unroll 1
-  for (uint32_t left = who; left; left &= left - 1) {
-    const int j = __ffs(int(left)) - 1;
-    const int e = __shfl_sync(0xffffffffu, id, j);
-    const float v = __shfl_sync(0xffffffffu, dz, j);
-    if (e / PER == lane) {
-#pragma unroll
-      for (int i = 0; i < PER; ++i)
-        if (e % PER == i) out[i] = v;
-    }
-  }
-  L* dst = static_cast<L*>(dlogits) + size_t(t) * ldd + lane * PER;
-  if constexpr (WIDE) {
-    if (lane * PER >= p.experts) return;
-    constexpr int kBytes = PER * int(sizeof(L)), kWords = kBytes >= 4 ? kBytes / 4 : 1;
-    uint32_t w[kWords];
-#pragma unroll
-    for (int i = 0; i < kWords; ++i) {
-      if constexpr (sizeof(L) == 4)
-        w[i] = __float_as_uint(out[i]);
-      else
-        w[i] = ptx::pack_bf16x2(out[2 * i], out[(2 * i + 1) % PER]);
-    }
-    if constexpr (kBytes >= 16) {
-#pragma unroll
-      for (int i = 0; i < kBytes / 16; ++i)
-        reinterpret_cast<uint4*>(dst)[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
-    } else if constexpr (kBytes == 8) {
-      *reinterpret_cast<uint2*>(dst) = make_uint2(w[0], w[1]);
-    } else {
-      *reinterpret_cast<uint32_t*>(dst) = w[0];
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < PER; ++i)
-      if (lane * PER + i < p.experts) {
-        if constexpr (sizeof(L) == 4)
-          reinterpret_cast<float*>(dst)[i] = out[i];
-        else
-          reinterpret_cast<unsigned short*>(dst)[i] = (unsigned short)(ptx::pack_bf16x2(out[i], 0.f) & 0xffffu);
-      }
-  }
-}
-
-struct F32 {
-  float v;
-};
-struct BF16 {
-  unsigned short v;
-};
-
-// Calls f with a lane's run length and whether rows allow loads of whole runs: runs divide the row, and each starts on
-// a multiple of its bytes (of 16 past that).
-template <typename L, typename F>
-tkg_status with_run(int experts, const void* a, size_t lda, const void* b, size_t ldb, F&& f) {
-  auto pick = [&](auto per) {
-    constexpr int PER = decltype(per)::value;
-    constexpr int kBytes = PER * int(sizeof(L));
-    constexpr size_t kAlign = kBytes > 16 ? 16 : kBytes;
-    if constexpr (kBytes >= 4) {
-      if (experts % PER == 0 && aligned_to(a, kAlign) && aligned_to(b, kAlign) && lda * sizeof(L) % kAlign == 0 &&
-          ldb * sizeof(L) % kAlign == 0)
-        return f(per, std::true_type{});
-    }
-    return f(per, std::false_type{});
-  };
-  const int need = ceil_div(experts, 32);
-  if (need <= 1) return pick(std::integral_constant<int, 1>{});
-  if (need <= 2) return pick(std::integral_constant<int, 2>{});
-  if (need <= 4) return pick(std::integral_constant<int, 4>{});
-  if (need <= 8) return pick(std::integral_constant<int, 8>{});
-  return pick(std::integral_constant<int, 16>{});
-}
-
 // Tokens in one block while that takes less time than a second kernel; past that, blocks of 32 at least, `most` of them,
 // and of no more than 16 bits can count.
 void route_blocks(int tokens, int most, int* blocks, int* per_block) {
   *per_block = tokens <= kRouteAlone ? (tokens + 31) / 32 * 32 : ceil_div(ceil_div(tokens, most), 32) * 32;
   if (*per_block > 65504) *per_block = 65504;
   *blocks = ceil_div(tokens, *per_block);
-}
-
-tkg_status check_route(int tokens, int experts, int topk, const void* logits, tkg_type type, int ld, tkg_scores sc) {
-  if (tokens < 0 || experts < 1 || topk < 1 || topk > experts || ld < experts) return TKG_ERR_INVALID_ARG;
-  if (type != TKG_TYPE_BF16 && type != TKG_TYPE_F32) return TKG_ERR_INVALID_ARG;
-  if (sc != TKG_SCORES_SOFTMAX && sc != TKG_SCORES_SIGMOID) return TKG_ERR_INVALID_ARG;
-  if (experts > kMaxRouteExperts || topk > kMaxTopk || (long long)tokens * topk > kMaxSize) return TKG_ERR_UNSUPPORTED;
-  if (tokens > 0 && !logits) return TKG_ERR_INVALID_ARG;
-  if (!aligned_to(logits, type == TKG_TYPE_F32 ? 4 : 2)) return TKG_ERR_ALIGNMENT;
-  return TKG_OK;
 }
 
 template <typename L>
@@ -1250,37 +993,6 @@ tkg_status tkg_moe_route(int tokens, int experts, int topk, const void* logits, 
   p.counts = static_cast<uint16_t*>(workspace);
   p.inverse = uint32_t((0x100000000ull + unsigned(p.per_group) - 1) / unsigned(p.per_group));
   return type == TKG_TYPE_F32 ? launch_route<F32>(p, stream) : launch_route<BF16>(p, stream);
-}
-
-tkg_status tkg_moe_route_grad(int tokens, int experts, int topk, const void* logits, tkg_type type, int ld,
-                              const tkg_route_rule* rule, const int* ids, const float* dweights, void* dlogits, int lddz,
-                              cudaStream_t stream) {
-  if (!rule) return TKG_ERR_INVALID_ARG;
-  tkg_status st = check_route(tokens, experts, topk, logits, type, ld, rule->scores);
-  if (st != TKG_OK) return st;
-  if (lddz < experts || (rule->renormalise != 0 && rule->renormalise != 1)) return TKG_ERR_INVALID_ARG;
-  if (tokens == 0) return TKG_OK;
-  if (!ids || !dweights || !dlogits) return TKG_ERR_INVALID_ARG;
-  if (!aligned_to(ids, 4) || !aligned_to(dweights, 4) || !aligned_to(dlogits, type == TKG_TYPE_F32 ? 4 : 2))
-    return TKG_ERR_ALIGNMENT;
-  RouteParams p{};
-  p.tokens = tokens;
-  p.experts = experts;
-  p.topk = topk;
-  p.sigmoid = rule->scores == TKG_SCORES_SIGMOID;
-  p.renormalise = rule->renormalise;
-  p.scale = rule->scale;
-  p.logits = logits;
-  p.ld = size_t(ld);
-  p.ids = const_cast<int*>(ids);
-  auto go = [&](auto type_tag) {
-    using L = decltype(type_tag);
-    return with_run<L>(experts, logits, size_t(ld), dlogits, size_t(lddz), [&](auto per, auto wide) {
-      return launch_small(route_grad_kernel<decltype(per)::value, L, decltype(wide)::value>,
-                          dim3(unsigned(ceil_div(tokens, 8))), dim3(256), stream, 0u, p, dweights, dlogits, size_t(lddz));
-    });
-  };
-  return type == TKG_TYPE_F32 ? go(F32{}) : go(BF16{});
 }
 
 }  // extern "C"

@@ -10,6 +10,7 @@
 // row is read once and sent to all its places, and all of a token's rows of O are on their way together.  Dispatch of 8192
 // tokens x 8 x 4096 92 us (604 MB, 89 at the copy rate); combine of 5003 x 8 x 4096 58 us (54), of 5003 x 6 x 2056 with 30%
 // of the tokens padding 20 us (16).
+#include "rows.cuh"
 #include "train_host.cuh"
 
 namespace tkg {
@@ -20,10 +21,9 @@ constexpr int kMaxChoices = 32;
 
 // A thread's token and 16 bytes of its row; false past the last token.
 __device__ __forceinline__ bool place_of(int tokens, int vecs, int& t, int& v) {
-  const long long first = (long long)blockIdx.x * kRowThreads;
-  const int t0 = int(first / vecs);
-  const unsigned x = unsigned(first - (long long)t0 * vecs) + threadIdx.x;
-  const unsigned more = x / unsigned(vecs);
+  int t0, v0;
+  divide((unsigned long long)blockIdx.x * kRowThreads, unsigned(vecs), t0, v0);
+  const unsigned x = unsigned(v0) + threadIdx.x, more = x / unsigned(vecs);
   t = t0 + int(more);
   v = int(x - more * unsigned(vecs));
   return t < tokens;

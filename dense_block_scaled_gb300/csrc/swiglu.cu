@@ -11,6 +11,7 @@
 // checkpoint 151 us (1082 MB, 159 at the copy rate), without 111 (118); 8192 x 4096 to 8 bits 16.5 us (15.0); the
 // gradient of 16004 rows x 1408, 30% of them padding, 28.2 us (23.4), of 65536 rows 101 (96).
 #include "mxfp8.cuh"
+#include "rows.cuh"
 #include "train_host.cuh"
 
 namespace tkg {
@@ -98,36 +99,15 @@ __device__ __forceinline__ Two two_of_codes(uint32_t codes, Two scale) {
   return two(f.x, f.y) * scale;
 }
 
-// Walks `COUNT` consecutive pieces of the rows' pieces from the warp's first on.
-template <int COUNT, int kWarps>
-struct Pieces {
-  int row[COUNT], col[COUNT];   // a lane's first column; row -1: past the end
-  __device__ __forceinline__ Pieces(int rows, int width, int lane) {
-    const int per_row = (width + kPiece - 1) / kPiece;
-    const long long first = ((long long)blockIdx.x * kWarps + (threadIdx.x >> 5)) * COUNT;
-    int r = int(first / per_row), piece = int(first - (long long)r * per_row);
-#pragma unroll
-    for (int i = 0; i < COUNT; ++i) {
-      row[i] = r < rows ? r : -1;
-      col[i] = piece * kPiece + lane * 8;
-      if (++piece == per_row) {
-        piece = 0;
-        ++r;
-      }
-    }
-  }
-};
-template <int COUNT, int kWarps>
-long long pieces_blocks(int rows, int width) {
-  return ((long long)rows * ceil_div(width, kPiece) + COUNT * kWarps - 1) / (COUNT * kWarps);
-}
-
 constexpr int kSavePieces = 2;
+using SavePieces = Pieces<kSavePieces, kSaveWarps, kPiece>;
 __global__ void __launch_bounds__(32 * kSaveWarps) save_kernel(int rows, int k, const uint16_t* __restrict__ X, size_t ldx,
                                                            uint8_t* __restrict__ Q, uint8_t* __restrict__ sf) {
   ptx::pdl_launch_dependents();
   const int lane = threadIdx.x & 31;
-  const Pieces<kSavePieces, kSaveWarps> at(rows, k, lane);
+  SavePieces at(rows, k);
+#pragma unroll
+  for (int i = 0; i < kSavePieces; ++i) at.col[i] += lane * 8;
   ptx::pdl_wait();
   uint4 v[kSavePieces];
 #pragma unroll
@@ -149,13 +129,16 @@ __global__ void __launch_bounds__(32 * kSaveWarps) save_kernel(int rows, int k, 
 }
 
 constexpr int kGatePieces = 1;
+using GatePieces = Pieces<kGatePieces, kGateWarps, kPiece>;
 template <bool SAVE>
 __global__ void __launch_bounds__(32 * kGateWarps)
     swiglu_kernel(int rows, int inner, const uint16_t* __restrict__ GU, size_t ldgu, uint16_t* __restrict__ H, size_t ldh,
                   uint8_t* __restrict__ Q, uint8_t* __restrict__ sf) {
   ptx::pdl_launch_dependents();
   const int lane = threadIdx.x & 31;
-  const Pieces<kGatePieces, kGateWarps> at(rows, inner, lane);
+  GatePieces at(rows, inner);
+#pragma unroll
+  for (int i = 0; i < kGatePieces; ++i) at.col[i] += lane * 8;
   ptx::pdl_wait();
   uint4 v[kGatePieces][2];
 #pragma unroll
@@ -299,7 +282,7 @@ tkg_status tkg_checkpoint_mxfp8(int rows, int k, const void* X, int ldx, void* Q
   if (k % 32 != 0 || ldx % 8 != 0 || !aligned_to(X, 16) || !aligned_to(Q, 16)) return TKG_ERR_ALIGNMENT;
   if (rows == 0) return TKG_OK;
   if (!X || !Q || !sf) return TKG_ERR_INVALID_ARG;
-  const long long blocks = pieces_blocks<kSavePieces, kSaveWarps>(rows, k);
+  const long long blocks = SavePieces::blocks(rows, k);
   if (!size_ok(blocks)) return TKG_ERR_UNSUPPORTED;
   return launch_small(save_kernel, dim3(unsigned(blocks)), dim3(32 * kSaveWarps), stream, 0u, rows, k,
                       static_cast<const uint16_t*>(X), size_t(ldx), static_cast<uint8_t*>(Q), static_cast<uint8_t*>(sf));
@@ -316,7 +299,7 @@ tkg_status tkg_swiglu(int rows, int inner, const void* GU, int ldgu, void* H, in
     return TKG_ERR_ALIGNMENT;
   if (rows == 0) return TKG_OK;
   if (!GU || !H) return TKG_ERR_INVALID_ARG;
-  const long long blocks = pieces_blocks<kGatePieces, kGateWarps>(rows, inner);
+  const long long blocks = GatePieces::blocks(rows, inner);
   if (!size_ok(blocks)) return TKG_ERR_UNSUPPORTED;
   return launch_small(Q ? swiglu_kernel<true> : swiglu_kernel<false>, dim3(unsigned(blocks)), dim3(32 * kGateWarps), stream, 0u,
                       rows, inner, static_cast<const uint16_t*>(GU), size_t(ldgu), static_cast<uint16_t*>(H), size_t(ldh),
