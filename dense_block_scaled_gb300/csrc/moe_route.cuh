@@ -1,18 +1,17 @@
-// moe_route.cuh -- what routing (moe_route.cu) and its gradient (moe_route_grad.cu) share: a warp has a token's row of
+// moe_route.cuh -- what routing (moe_route.cu, moe_choose.cuh) and its gradient (moe_route_grad.cu) share: a warp has a token's row of
 // logits, each lane a run of consecutive experts.
 #pragma once
 #include "train_host.cuh"
 
 namespace tkg {
-namespace {
 
 constexpr int kMaxRouteExperts = 512, kMaxTopk = 32, kMaxRouteGroups = 32;
 
 // Types of the logits.
-struct F32 {
+struct LogitF32 {
   float v;
 };
-struct BF16 {
+struct LogitBF16 {
   unsigned short v;
 };
 
@@ -113,6 +112,20 @@ __device__ __forceinline__ float logit_at(const RouteParams& p, int t, int e) {
     return __uint_as_float(uint32_t(__ldcg(reinterpret_cast<const unsigned short*>(row) + e)) << 16);
 }
 // ---- host
+constexpr int kSMs = 152;
+constexpr int kRouteAlone = 64;   // tokens at most that one block takes alone
+// Tokens in one block while that takes less time than a second kernel; past that, blocks of 32 at least, `most` of them,
+// and of no more than 16 bits can count.
+inline void route_blocks(int tokens, int most, int* blocks, int* per_block) {
+  *per_block = tokens <= kRouteAlone ? (tokens + 31) / 32 * 32 : ceil_div(ceil_div(tokens, most), 32) * 32;
+  if (*per_block > 65504) *per_block = 65504;
+  *blocks = ceil_div(tokens, *per_block);
+}
+
+// moe_choose_bf16.cu, moe_choose_f32.cu: the choices of all tokens; sets p's blocks of tokens.
+tkg_status launch_choose_bf16(RouteParams& p, cudaStream_t stream);
+tkg_status launch_choose_f32(RouteParams& p, cudaStream_t stream);
+
 // Calls f with a lane's run length and whether rows allow loads of whole runs: runs divide the row, and each starts on
 // a multiple of its bytes (of 16 past that).
 template <typename L, typename F>
@@ -146,5 +159,4 @@ inline tkg_status check_route(int tokens, int experts, int topk, const void* log
   return TKG_OK;
 }
 
-}  // namespace
 }  // namespace tkg

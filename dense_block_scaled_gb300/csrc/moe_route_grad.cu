@@ -162,7 +162,7 @@ tkg_status tkg_moe_route_grad(int tokens, int experts, int topk, const void* log
                           dim3(unsigned(ceil_div(tokens, 8))), dim3(256), stream, 0u, p, dweights, dlogits, size_t(lddz));
     });
   };
-  return type == TKG_TYPE_F32 ? go(F32{}) : go(BF16{});
+  return type == TKG_TYPE_F32 ? go(LogitF32{}) : go(LogitBF16{});
 }
 
 }  // extern "C"
