@@ -536,6 +536,7 @@ def gemm_grouped_dev_bf16_wgrad(sizes_dev, dD, A, dB, alpha: float = 1.0, accumu
 
 
 # ---------------------------------------------------------------- a mixture-of-experts block
+# As above; the current GPU is asked for without torch's check that CUDA is initialised (0.1 us), as a tensor is on one.
 
 @functools.lru_cache(maxsize=64)
 def _rule(scores, groups, topk_groups, renormalise, scale):
@@ -567,8 +568,8 @@ def moe_route(logits, ids, weights, sizes, rows, slots, bias=None, keep=None, sc
     int32; -1: not routed), weights (float32), sizes (experts, int32), slots (tokens * topk int32; -1 past the last row)."""
     import torch
     (tokens, experts), (_, topk), dev = logits.shape, ids.shape, logits.get_device()
-    kind, shape, i32 = _logit_type(logits, "logits"), ids.shape, torch.int32
-    if not (-1 < dev == torch.cuda.current_device() == ids.get_device() == weights.get_device() == sizes.get_device()
+    kind, shape, i32, ld = _logit_type(logits, "logits"), ids.shape, torch.int32, experts
+    if not (-1 < dev == torch._C._cuda_getDevice() == ids.get_device() == weights.get_device() == sizes.get_device()
             == rows.get_device() == slots.get_device() and not (tokens | experts | tokens * topk) >> 31
             and ids.dtype is rows.dtype is sizes.dtype is slots.dtype is i32 and weights.dtype is torch.float32
             and shape == weights.shape == rows.shape and shape[0] == tokens and sizes.shape == (experts,)
@@ -586,9 +587,12 @@ def moe_route(logits, ids, weights, sizes, rows, slots, bias=None, keep=None, sc
         if keep is not None:
             wanted.append(("keep", keep, torch.uint8 if keep.dtype is torch.uint8 else torch.bool, (tokens,), False))
         _refuse(wanted)
+        ld = _pitch(logits, experts)
+    if type(scale) is not float:   # (a rule is kept by its values: not by a tensor that may change)
+        scale = float(scale)
     lib, handle = load(), _stream(stream, dev)
     at, nbytes, _keep = _workspace(workspace, moe_route_workspace_bytes(tokens, experts), logits, stream, handle)
-    _check(lib.tkg_moe_route(tokens, experts, topk, logits.data_ptr(), kind, _pitch(logits, experts),
+    _check(lib.tkg_moe_route(tokens, experts, topk, logits.data_ptr(), kind, ld,
                              _rule(scores, groups, topk_groups, renormalise, scale), _ptr(bias), _ptr(keep),
                              ids.data_ptr(), weights.data_ptr(), sizes.data_ptr(), rows.data_ptr(), slots.data_ptr(), at,
                              nbytes, handle), "tkg_moe_route")
@@ -599,8 +603,8 @@ def moe_route_grad(logits, ids, dweights, dlogits, scores: str = "softmax", reno
     """Gradient of moe_route's weights to the logits, the choice being fixed: dlogits (as logits), all of it written."""
     import torch
     (tokens, experts), (_, topk), dev = logits.shape, ids.shape, logits.get_device()
-    kind = _logit_type(logits, "logits")
-    if not (-1 < dev == torch.cuda.current_device() == ids.get_device() == dweights.get_device()
+    kind, ld, lddz = _logit_type(logits, "logits"), experts, experts
+    if not (-1 < dev == torch._C._cuda_getDevice() == ids.get_device() == dweights.get_device()
             == dlogits.get_device() and not (tokens | experts | tokens * topk) >> 31 and ids.dtype is torch.int32
             and dweights.dtype is torch.float32 and dlogits.dtype is logits.dtype and ids.shape == dweights.shape
             and ids.shape[0] == tokens and dlogits.shape == logits.shape and logits.is_contiguous()
@@ -608,9 +612,12 @@ def moe_route_grad(logits, ids, dweights, dlogits, scores: str = "softmax", reno
         _refuse((("logits", logits, logits.dtype, (tokens, experts), True), ("ids", ids, torch.int32, (tokens, topk), False),
                  ("dweights", dweights, torch.float32, (tokens, topk), False),
                  ("dlogits", dlogits, logits.dtype, (tokens, experts), True)))
-    _check(load().tkg_moe_route_grad(tokens, experts, topk, logits.data_ptr(), kind, _pitch(logits, experts),
+        ld, lddz = _pitch(logits, experts), _pitch(dlogits, experts)
+    if type(scale) is not float:
+        scale = float(scale)
+    _check(load().tkg_moe_route_grad(tokens, experts, topk, logits.data_ptr(), kind, ld,
                                      _rule(scores, 1, 1, renormalise, scale), ids.data_ptr(), dweights.data_ptr(),
-                                     dlogits.data_ptr(), _pitch(dlogits, experts), _stream(stream, dev)),
+                                     dlogits.data_ptr(), lddz, _stream(stream, dev)),
            "tkg_moe_route_grad")
 
 
@@ -619,14 +626,16 @@ def moe_dispatch(X, rows, out, stream=None) -> None:
     gradient of moe_combine without weights."""
     import torch
     (tokens, hidden), (_, topk), cap, dev = X.shape, rows.shape, out.shape[0], X.get_device()
-    if not (-1 < dev == torch.cuda.current_device() == rows.get_device() == out.get_device()
+    ldx = ldo = hidden
+    if not (-1 < dev == torch._C._cuda_getDevice() == rows.get_device() == out.get_device()
             and not (tokens | hidden | cap | tokens * topk) >> 31 and X.dtype is out.dtype is torch.bfloat16
             and rows.dtype is torch.int32 and rows.shape[0] == tokens and out.shape[1] == hidden and X.is_contiguous()
             and rows.is_contiguous() and out.is_contiguous()):
         _refuse((("X", X, torch.bfloat16, (tokens, hidden), True), ("rows", rows, torch.int32, (tokens, topk), False),
                  ("out", out, torch.bfloat16, (cap, hidden), True)))
-    _check(load().tkg_moe_dispatch(tokens, topk, hidden, X.data_ptr(), _pitch(X, hidden), rows.data_ptr(), cap,
-                                   out.data_ptr(), _pitch(out, hidden), _stream(stream, dev)), "tkg_moe_dispatch")
+        ldx, ldo = _pitch(X, hidden), _pitch(out, hidden)
+    _check(load().tkg_moe_dispatch(tokens, topk, hidden, X.data_ptr(), ldx, rows.data_ptr(), cap, out.data_ptr(), ldo,
+                                   _stream(stream, dev)), "tkg_moe_dispatch")
 
 
 def moe_combine(O, rows, Y, weights=None, stream=None) -> None:
@@ -634,7 +643,8 @@ def moe_combine(O, rows, Y, weights=None, stream=None) -> None:
     gradient of moe_dispatch."""
     import torch
     (tokens, hidden), (_, topk), cap, dev = Y.shape, rows.shape, O.shape[0], Y.get_device()
-    if not (-1 < dev == torch.cuda.current_device() == rows.get_device() == O.get_device()
+    ldo = ldy = hidden
+    if not (-1 < dev == torch._C._cuda_getDevice() == rows.get_device() == O.get_device()
             and not (tokens | hidden | cap | tokens * topk) >> 31 and O.dtype is Y.dtype is torch.bfloat16
             and rows.dtype is torch.int32 and rows.shape[0] == tokens and O.shape[1] == hidden and O.is_contiguous()
             and rows.is_contiguous() and Y.is_contiguous()
@@ -645,21 +655,23 @@ def moe_combine(O, rows, Y, weights=None, stream=None) -> None:
         if weights is not None:
             wanted.append(("weights", weights, torch.float32, (tokens, topk), False))
         _refuse(wanted)
-    _check(load().tkg_moe_combine(tokens, topk, hidden, O.data_ptr(), _pitch(O, hidden), cap, rows.data_ptr(),
-                                  _ptr(weights), Y.data_ptr(), _pitch(Y, hidden), _stream(stream, dev)),
-           "tkg_moe_combine")
+        ldo, ldy = _pitch(O, hidden), _pitch(Y, hidden)
+    _check(load().tkg_moe_combine(tokens, topk, hidden, O.data_ptr(), ldo, cap, rows.data_ptr(),
+                                  None if weights is None else weights.data_ptr(), Y.data_ptr(), ldy,
+                                  _stream(stream, dev)), "tkg_moe_combine")
 
 
 def checkpoint_mxfp8(X, Q, sf, stream=None) -> None:
     """Rows of X (bf16) in 8 bits: Q (rows x k, uint8 E4M3 codes), sf (rows x k / 32, uint8 E8M0), both row-major."""
     import torch
-    (rows, k), dev = X.shape, X.get_device()
-    if not (-1 < dev == torch.cuda.current_device() == Q.get_device() == sf.get_device() and not (rows | k) >> 31
+    (rows, k), dev, ldx = X.shape, X.get_device(), X.shape[1]
+    if not (-1 < dev == torch._C._cuda_getDevice() == Q.get_device() == sf.get_device() and not (rows | k) >> 31
             and X.dtype is torch.bfloat16 and Q.dtype is sf.dtype is torch.uint8 and Q.shape == X.shape
             and sf.shape == (rows, k // 32) and X.is_contiguous() and Q.is_contiguous() and sf.is_contiguous()):
         _refuse((("X", X, torch.bfloat16, (rows, k), True), ("Q", Q, torch.uint8, (rows, k), False),
                  ("sf", sf, torch.uint8, (rows, k // 32), False)))
-    _check(load().tkg_checkpoint_mxfp8(rows, k, X.data_ptr(), _pitch(X, k), Q.data_ptr(), sf.data_ptr(),
+        ldx = _pitch(X, k)
+    _check(load().tkg_checkpoint_mxfp8(rows, k, X.data_ptr(), ldx, Q.data_ptr(), sf.data_ptr(),
                                        _stream(stream, dev)), "tkg_checkpoint_mxfp8")
 
 
@@ -668,9 +680,10 @@ def swiglu(GU, H, Q=None, sf=None, stream=None) -> None:
     checkpoint in 8 bits."""
     import torch
     (rows, inner), dev = H.shape, H.get_device()
+    ldgu, ldh = 2 * inner, inner
     if (Q is None) != (sf is None):
         raise ValueError("Q, sf: both or neither are wanted")
-    if not (-1 < dev == torch.cuda.current_device() == GU.get_device() and not (rows | 2 * inner) >> 31
+    if not (-1 < dev == torch._C._cuda_getDevice() == GU.get_device() and not (rows | 2 * inner) >> 31
             and GU.dtype is H.dtype is torch.bfloat16 and GU.shape == (rows, 2 * inner) and GU.is_contiguous()
             and H.is_contiguous()
             and (Q is None or (Q.dtype is sf.dtype is torch.uint8 and Q.shape == GU.shape
@@ -681,8 +694,9 @@ def swiglu(GU, H, Q=None, sf=None, stream=None) -> None:
             wanted += [("Q", Q, torch.uint8, (rows, 2 * inner), False),
                        ("sf", sf, torch.uint8, (rows, 2 * inner // 32), False)]
         _refuse(wanted)
-    _check(load().tkg_swiglu(rows, inner, GU.data_ptr(), _pitch(GU, 2 * inner), H.data_ptr(), _pitch(H, inner), _ptr(Q),
-                             _ptr(sf), _stream(stream, dev)), "tkg_swiglu")
+        ldgu, ldh = _pitch(GU, 2 * inner), _pitch(H, inner)
+    _check(load().tkg_swiglu(rows, inner, GU.data_ptr(), ldgu, H.data_ptr(), ldh, _ptr(Q), _ptr(sf), _stream(stream, dev)),
+           "tkg_swiglu")
 
 
 def swiglu_grad(Q, sf, dH, dGU, H=None, slots=None, weights=None, dweights=None, stream=None) -> None:
@@ -692,9 +706,10 @@ def swiglu_grad(Q, sf, dH, dGU, H=None, slots=None, weights=None, dweights=None,
     import torch
     (rows, inner), dev = dH.shape, dH.get_device()
     choices = 0x7fff0000 if weights is None else weights.numel()
+    lddh, lddgu, ldh = inner, 2 * inner, inner
     if dweights is not None and weights is None:
         raise ValueError("dweights: wanted only together with weights")
-    if not (-1 < dev == torch.cuda.current_device() == Q.get_device() == sf.get_device() == dGU.get_device()
+    if not (-1 < dev == torch._C._cuda_getDevice() == Q.get_device() == sf.get_device() == dGU.get_device()
             and not (rows | 2 * inner | choices) >> 31 and dH.dtype is dGU.dtype is torch.bfloat16
             and Q.dtype is sf.dtype is torch.uint8 and Q.shape == dGU.shape == (rows, 2 * inner)
             and sf.shape == (rows, 2 * inner // 32) and dH.is_contiguous() and dGU.is_contiguous() and Q.is_contiguous()
@@ -718,10 +733,10 @@ def swiglu_grad(Q, sf, dH, dGU, H=None, slots=None, weights=None, dweights=None,
         if dweights is not None:
             wanted.append(("dweights", dweights, torch.float32, weights.shape, False))
         _refuse(wanted)
-    _check(load().tkg_swiglu_grad(rows, inner, Q.data_ptr(), sf.data_ptr(), dH.data_ptr(), _pitch(dH, inner), _ptr(slots),
-                                  choices, _ptr(weights), dGU.data_ptr(), _pitch(dGU, 2 * inner), _ptr(H),
-                                  0 if H is None else _pitch(H, inner), _ptr(dweights), _stream(stream, dev)),
-           "tkg_swiglu_grad")
+        lddh, lddgu, ldh = _pitch(dH, inner), _pitch(dGU, 2 * inner), inner if H is None else _pitch(H, inner)
+    _check(load().tkg_swiglu_grad(rows, inner, Q.data_ptr(), sf.data_ptr(), dH.data_ptr(), lddh, _ptr(slots), choices,
+                                  _ptr(weights), dGU.data_ptr(), lddgu, _ptr(H), ldh, _ptr(dweights),
+                                  _stream(stream, dev)), "tkg_swiglu_grad")
 
 
 @functools.lru_cache(maxsize=256)
@@ -736,7 +751,7 @@ def gemm_grouped_dev_mxfp8_wgrad(sizes_dev, dD, Q, sf, dB, slots=None, topk: int
     import torch
     groups, (cap, n), (tokens, k), dev = sizes_dev.shape[0], dD.shape, Q.shape, dD.get_device()
     gtype = _grad_type(dB, "dB", accumulate)
-    if not (-1 < dev == torch.cuda.current_device() == sizes_dev.get_device() == Q.get_device() == sf.get_device()
+    if not (-1 < dev == torch._C._cuda_getDevice() == sizes_dev.get_device() == Q.get_device() == sf.get_device()
             == dB.get_device() and not (cap | n | k | tokens) >> 31 and dD.dtype is torch.bfloat16
             and Q.dtype is sf.dtype is torch.uint8 and sizes_dev.dtype is torch.int32 and sizes_dev.dim() == 1
             and sf.shape == (tokens, k // 32) and dB.shape == (groups, n, k) and dD.is_contiguous() and Q.is_contiguous()

@@ -387,7 +387,8 @@ tkg_status tkg_moe_route_grad(int tokens, int experts, int topk, const void *log
  *             order of j; weights NULL: 1.
  * Each is the other's gradient (combine without weights).  X, Y: tokens x hidden,
  * out, O: capacity x hidden, BF16 with row pitches.  A place outside [0, capacity)
- * is left out: dispatch writes no other rows, combine reads no other.
+ * is left out: dispatch writes no other rows, combine reads no other.  Places are
+ * distinct for dispatch (of one named twice, either token's row is written).
  *  - Requires hidden and pitches % 8 == 0, 16-byte aligned matrices, topk <= 32. */
 tkg_status tkg_moe_dispatch(int tokens, int topk, int hidden, const void *X, int ldx, const int *rows, int capacity,
                             void *out, int ldo, cudaStream_t stream);
@@ -416,7 +417,7 @@ tkg_status tkg_swiglu(int rows, int inner, const void *GU, int ldgu, void *H, in
  *   H[r]   = w silu(g) u      (or NULL; what the second product's gradient takes)
  *   dweights[c] = sum over the columns of dH silu(g) u   (FP32, fixed order; or NULL)
  * with g, u as saved.  Rows whose choice is outside [0, choices) are neither read
- * nor written.  Requires inner % 32 == 0, pitches % 8 == 0. */
+ * nor written; choices are distinct where dweights is wanted.  Requires inner % 32 == 0, pitches % 8 == 0. */
 tkg_status tkg_swiglu_grad(int rows, int inner, const void *Q, const void *sf, const void *dH, int lddh, const int *slots,
                            int choices, const float *weights, void *dGU, int lddgu, void *H, int ldh, float *dweights,
                            cudaStream_t stream);

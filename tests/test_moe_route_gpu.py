@@ -310,6 +310,16 @@ def test_gradient_where_nothing_was_chosen_or_all_is_masked():
             assert (out == 0).all()
 
 
+def test_a_scale_that_is_not_a_float():
+    z = normal(5, 64)
+    scale = torch.tensor(2.0)
+    _, a, *_ = route(z, 4, scale=scale)
+    scale.mul_(2)
+    _, b, *_ = route(z, 4, scale=scale)
+    _, c, *_ = route(z, 4, scale=4)
+    assert torch.equal(b, 2 * a) and torch.equal(b, c)
+
+
 def test_no_tokens_and_a_captured_call():
     z = normal(0, 64)
     _, _, sizes, _, _ = route(z, 4)
