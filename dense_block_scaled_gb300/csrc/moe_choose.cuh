@@ -120,7 +120,7 @@ __device__ __forceinline__ void choice_scores(const RouteParams& p, const float 
   }
   auto reciprocal = [](float x) {
     float r;
-    asm("rcp.approx.f32 %0, %1;" : "=f"(r) : "f"(x));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
     return r;
   };
   if (p.sigmoid) {
@@ -239,13 +239,13 @@ __device__ __noinline__ int order_again(const RouteParams& p, int t, int n, int 
     const double c = by.score + double(b);
     const unsigned long long mine = key_of(c);
     int rank = 0, from = 0;
-#pragma unroll 1
+#pragma unroll 4
     for (int i = 0; i < n; ++i) {
       const unsigned long long other = __shfl_sync(0xffffffffu, mine, i);
       const int e = __shfl_sync(0xffffffffu, id, i);
       rank += other > mine || (other == mine && e < id) ? 1 : 0;
     }
-#pragma unroll 1
+#pragma unroll 4
     for (int i = 0; i < n; ++i)
       if (__shfl_sync(0xffffffffu, rank, i) == lane) from = i;
     out = __shfl_sync(0xffffffffu, id, from);
@@ -327,9 +327,14 @@ __device__ __forceinline__ uint32_t keep_groups(const RouteParams& p, int t, con
   int lost = 0;                     // (NaN)
   auto take = [&](F x) {
     lost |= x != x;
-    const F low = x > a ? a : x;
-    a = x > a ? x : a;
-    b = low > b ? low : b;
+    if constexpr (sizeof(F) == 4) {
+      b = fmaxf(b, fminf(a, x));
+      a = fmaxf(a, x);
+    } else {   // (64-bit minima and maxima are calls)
+      const F low = x > a ? a : x;
+      a = x > a ? x : a;
+      b = low > b ? low : b;
+    }
   };
   if (p.whole_runs) {
 #pragma unroll
@@ -478,7 +483,8 @@ __device__ __forceinline__ int choose_few(const RouteParams& p, int t, const flo
     // neighbours that are too near, as far as they may belong before the last of the chosen
     const bool near = lane + 1 < n && next.x >= few[p.topk - 1].x - margin && !(me.x - next.x > margin);
     if (__any_sync(0xffffffffu, near)) {
-      const bool close = near && !same_score<L>(p, t, id, __float_as_int(next.y));
+      // (the same logit and bias give the same value)
+      const bool close = near && (me.x != next.x || !same_score<L>(p, t, id, __float_as_int(next.y)));
       if (__any_sync(0xffffffffu, close)) id = order_again<PER, L>(p, t, n, id, lane);
     }
   }
@@ -682,9 +688,10 @@ __global__ void __launch_bounds__(32 * kRouteWarps<PER, BY_LOGIT && sizeof(L) ==
             uint32_t kept = 0xffffffffu;
             if (p.topk_groups < p.groups)
               kept = keep_groups<PER, L>(p, t, c, wrong, lane, reinterpret_cast<float*>(box), s_few[warp], clear);
+            if (WIDE && lane * PER >= p.experts) kept = 0;   // (whole runs)
 #pragma unroll
             for (int k = 0; k < PER; ++k)
-              if (lane * PER + k >= p.experts || !((kept >> k) & 1u)) c[k] = -INFINITY;
+              if ((!WIDE && lane * PER + k >= p.experts) || !(kept & (1u << k))) c[k] = -INFINITY;
           }
           id = clear && p.topk <= kFewTopk ? choose_few<PER, L>(p, t, c, wrong, lane, s_few[warp], zj) : -1;
           const bool slow = __shfl_sync(0xffffffffu, id, 0) < 0;
