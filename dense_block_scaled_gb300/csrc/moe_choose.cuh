@@ -618,18 +618,19 @@ template <int PER, typename L, bool WIDE, bool BY_LOGIT>
 __global__ void __launch_bounds__(32 * kRouteWarps<PER, BY_LOGIT && sizeof(L) == 2>) route_choose_kernel(const RouteParams p) {
   constexpr bool kPacked = BY_LOGIT && sizeof(L) == 2;
   extern __shared__ int s_dyn[];
-  // bits of the tokens that chose an expert, how many did before, each expert's first row (one block of tokens), and, for
-  // the groups, a row of values per warp
+  // bits of the tokens that chose an expert, how many did before, each expert's first row (one block of tokens or cluster),
+  // the choices, and, for the groups, a row of values per warp
   uint32_t* s_bits = reinterpret_cast<uint32_t*>(s_dyn);   // [experts][kRouteWords]
   int* s_count = s_dyn + p.experts * kRouteWords;
-  __shared__ int s_total;
+  __shared__ int s_warp[32];
   ptx::pdl_launch_dependents();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   __shared__ __align__(16) float s_bias[BY_LOGIT ? 4 : 32 * PER];
   __shared__ float2 s_few[kPacked ? 1 : kRouteWarps<PER, kPacked>][32];
-  int* s_ids = s_count + p.experts;                          // [kRouteTokens][topk]
+  int* s_first = s_count + p.experts;
+  int* s_ids = s_first + p.experts;                          // [kRouteTokens][topk]
   const int tokens_there = min(kRouteTokens, p.per_block), warps = blockDim.x >> 5;
-  double* box = reinterpret_cast<double*>(s_dyn + (p.experts * (kRouteWords + 1) + tokens_there * p.topk + 1) / 2 * 2) +
+  double* box = reinterpret_cast<double*>(s_dyn + (p.experts * (kRouteWords + 2) + tokens_there * p.topk + 1) / 2 * 2) +
                 warp * (p.experts + p.experts / 32 + 1);
   for (int e = threadIdx.x; e < p.experts; e += blockDim.x) s_count[e] = 0;
   const int begin = blockIdx.x * p.per_block, end = min(p.tokens, begin + p.per_block);
@@ -725,7 +726,7 @@ __global__ void __launch_bounds__(32 * kRouteWarps<PER, BY_LOGIT && sizeof(L) ==
     }
     __syncthreads();
     // ranks within the block of tokens
-    if (p.blocks > 1) {
+    if (p.blocks > p.cluster) {
       for (int i = threadIdx.x; i < there * p.topk; i += blockDim.x) {
         const int e = s_ids[i];
         p.rows[size_t(t0) * p.topk + i] = e < 0 ? -1 : s_count[e] + rank_of(e, i / p.topk);
@@ -735,39 +736,72 @@ __global__ void __launch_bounds__(32 * kRouteWarps<PER, BY_LOGIT && sizeof(L) ==
       __syncthreads();
     }
   }
-  if (p.blocks > 1) {
+  if (p.blocks > p.cluster) {
     const int width = (p.experts + 7) / 8 * 8;
     for (int e = threadIdx.x; e < width; e += blockDim.x)
       p.counts[size_t(blockIdx.x) * width + e] = uint16_t(e < p.experts ? s_count[e] : 0);
     return;
   }
-  // the only block, with all of the tokens' bits
-  if (warp == 0) {
-    int carry = 0;
-    for (int e0 = 0; e0 < p.experts; e0 += 32) {
-      const int e = e0 + lane, n = e < p.experts ? count_of(e) : 0;
-      int x = n;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int y = __shfl_up_sync(0xffffffffu, x, o);
-        if (lane >= o) x += y;
-      }
-      if (e < p.experts) {
-        s_count[e] = carry + x - n;
-        p.sizes[e] = n;
-      }
-      carry += __shfl_sync(0xffffffffu, x, 31);
-    }
-    if (lane == 0) s_total = carry;
+  // One block, or a cluster of them, has all of the tokens' bits: each adds up the others' counts through their shared
+  // memory, a thread per expert.
+  if (p.cluster > 1) {
+    for (int e = threadIdx.x; e < p.experts; e += blockDim.x) s_count[e] = count_of(e);
+    __syncthreads();
+    ptx::cluster_sync();
   }
-  __syncthreads();
-  const int all = p.tokens * p.topk;
+  int carry = 0;
+  for (int e0 = 0; e0 < p.experts; e0 += blockDim.x) {   // (one turn but for a few tokens and many experts)
+    const int e = e0 + threadIdx.x;
+    int n = 0, before = 0;
+    if (e < p.experts) {
+      if (p.cluster == 1) {
+        n = count_of(e);
+      } else {
+        const uint32_t mine = ptx::smem_u32(s_count + e);
+        int of[kMaxCluster];
+#pragma unroll
+        for (int r = 0; r < kMaxCluster; ++r)
+          of[r] = r < p.cluster ? ptx::ld_cluster(ptx::map_to_rank(mine, uint32_t(r))) : 0;
+#pragma unroll
+        for (int r = 0; r < kMaxCluster; ++r) {
+          n += of[r];
+          before += r < int(blockIdx.x) ? of[r] : 0;
+        }
+      }
+    }
+    int upto = n;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, upto, o);
+      if (lane >= o) upto += y;
+    }
+    if (lane == 31) s_warp[warp] = upto;
+    __syncthreads();
+    int sum = 0, below = 0;
+    const int used = min(warps, (p.experts - e0 + 31) / 32);   // warps that have experts
+#pragma unroll 4
+    for (int w = 0; w < used; ++w) {
+      below += w < warp ? s_warp[w] : 0;
+      sum += s_warp[w];
+    }
+    if (e < p.experts) {
+      s_first[e] = carry + below + upto - n + before;
+      if (blockIdx.x == 0) p.sizes[e] = n;
+    }
+    carry += sum;
+    __syncthreads();
+  }
+  const int base = begin * p.topk, all = (end - begin) * p.topk;
   for (int i = threadIdx.x; i < all; i += blockDim.x) {
     const int e = s_ids[i];
-    const int row = e < 0 ? -1 : s_count[e] + rank_of(e, i / p.topk);
-    p.rows[i] = row;
-    if (row >= 0) p.slots[row] = i;
-    if (i >= s_total) p.slots[i] = -1;
+    const int row = e < 0 ? -1 : s_first[e] + rank_of(e, i / p.topk);
+    p.rows[base + i] = row;
+    if (row >= 0) p.slots[row] = base + i;
+    if (base + i >= carry) p.slots[base + i] = -1;
+  }
+  if (p.cluster > 1) {   // no block leaves while another reads its counts
+    __syncthreads();
+    ptx::cluster_sync();
   }
 }
 
@@ -787,8 +821,9 @@ tkg_status launch_choose(RouteParams& p, cudaStream_t stream) {
     const bool packed = by_logit && sizeof(L) == 2;
     const int most_warps = packed ? kRouteWarps<PER, true> : kRouteWarps<PER, false>;
     route_blocks(p.tokens, kSMs * (packed ? kRouteOnSM<PER, true> : kRouteOnSM<PER, false>), &p.blocks, &p.per_block);
+    p.cluster = p.tokens <= kRouteCluster ? p.blocks : 1;
     const int there = p.per_block < kRouteTokens ? p.per_block : kRouteTokens;
-    unsigned smem = unsigned((p.experts * (kRouteWords + 1) + there * p.topk + 1) / 2 * 2) * 4u;
+    unsigned smem = unsigned((p.experts * (kRouteWords + 2) + there * p.topk + 1) / 2 * 2) * 4u;
     // values of the groups' choice, one row per warp, as large as its second time in 64 bits needs
     if (p.topk_groups < p.groups && !p.whole_runs) smem += unsigned(most_warps * (p.experts + p.experts / 32 + 1)) * 8u;
     auto kern = by_logit ? route_choose_kernel<PER, L, decltype(wide)::value, true>
@@ -807,7 +842,8 @@ tkg_status launch_choose(RouteParams& p, cudaStream_t stream) {
       }
     }
     const int warps = p.tokens < 4 ? 4 : (p.tokens < most_warps ? p.tokens : most_warps);
-    return launch_small(kern, dim3(unsigned(p.blocks)), dim3(32u * unsigned(warps)), stream, smem, p);
+    return launch_small_cluster(kern, dim3(unsigned(p.blocks)), dim3(32u * unsigned(warps)), unsigned(p.cluster), stream,
+                                smem, p);
   });
 }
 

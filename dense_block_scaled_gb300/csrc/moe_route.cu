@@ -9,7 +9,8 @@
 //
 // Two kernels.  The first (moe_choose.cuh) chooses; within a block of tokens, the rank of (t, e) is the number of earlier
 // tokens that chose e: a population count of one bit per token and expert.  The block leaves its ranks (in `rows`) and its
-// count per expert.  The second adds what earlier blocks and experts have.  A single block of tokens does both at once.
+// count per expert.  The second adds what earlier blocks and experts have.  Up to 256 tokens a cluster of blocks does both
+// at once, its counts exchanged through shared memory.
 // Nothing depends on the order of atomics: those are bit sets.
 #include "moe_route.cuh"
 
@@ -135,8 +136,8 @@ extern "C" {
 size_t tkg_moe_route_workspace_bytes(int tokens, int experts) {
   if (tokens < 0 || experts < 1 || experts > kMaxRouteExperts || tokens > kMaxSize) return 0;
   int blocks = 0, per_block = 0;
-  if (tokens > 0) route_blocks(tokens, 2 * kSMs, &blocks, &per_block);   // the most there can be
-  return size_t(blocks > 1 ? blocks : 0) * size_t((experts + 7) / 8 * 8) * 2 + 16;
+  if (tokens > kRouteCluster) route_blocks(tokens, 2 * kSMs, &blocks, &per_block);   // the most there can be
+  return size_t(blocks) * size_t((experts + 7) / 8 * 8) * 2 + 16;
 }
 
 tkg_status tkg_moe_route(int tokens, int experts, int topk, const void* logits, tkg_type type, int ld,
@@ -182,11 +183,12 @@ tkg_status tkg_moe_route(int tokens, int experts, int topk, const void* logits, 
   p.slots = slots;
   p.counts = static_cast<uint16_t*>(workspace);
   p.inverse = uint32_t((0x100000000ull + unsigned(p.per_group) - 1) / unsigned(p.per_group));
-  if ((st = type == TKG_TYPE_F32 ? launch_choose_f32(p, stream) : launch_choose_bf16(p, stream)) != TKG_OK || p.blocks == 1)
-    return st;
+  st = type == TKG_TYPE_F32 ? launch_choose_f32(p, stream) : launch_choose_bf16(p, stream);
+  if (st != TKG_OK || p.blocks == p.cluster) return st;
   int each = kPlaceEntries / (p.per_block * p.topk);
   each = each < 1 ? 1 : (each > kPlaceEach ? kPlaceEach : each);
-  return launch_small(route_place_kernel, dim3(unsigned(ceil_div(p.blocks, each))), dim3(kPlaceThreads), stream, 0u, p, each);
+  return launch_small(route_place_kernel, dim3(unsigned(ceil_div(p.blocks, each))), dim3(kPlaceThreads), stream, 0u, p,
+                      each);
 }
 
 }  // extern "C"

@@ -37,6 +37,7 @@ struct RouteParams {
   uint16_t* counts;           // [blocks][experts, rounded up to 8]
   int per_block;              // tokens, a multiple of 32
   int blocks;
+  int cluster;                // blocks of a cluster: all of them, or 1
 };
 
 template <typename F>
@@ -113,11 +114,12 @@ __device__ __forceinline__ float logit_at(const RouteParams& p, int t, int e) {
 }
 // ---- host
 constexpr int kSMs = 152;
-constexpr int kRouteAlone = 64;   // tokens at most that one block takes alone
-// Tokens in one block while that takes less time than a second kernel; past that, blocks of 32 at least, `most` of them,
-// and of no more than 16 bits can count.
+constexpr int kMaxCluster = 8, kRouteCluster = 32 * kMaxCluster;   // blocks of a cluster at most, and its tokens
+// Tokens in blocks of 32 that make a cluster, which needs no second kernel (256 x 128 5.0 us from a graph and 7.9 from the
+// host, with a second kernel 6.1 and 10.3; but 512, in blocks of 64, 7.0 and 8.0 against 6.2 and 9.6, and 512 x 256 in
+// groups 14.7 against 11.3), or in `most` blocks of 32 at least, of no more tokens than 16 bits can count.
 inline void route_blocks(int tokens, int most, int* blocks, int* per_block) {
-  *per_block = tokens <= kRouteAlone ? (tokens + 31) / 32 * 32 : ceil_div(ceil_div(tokens, most), 32) * 32;
+  *per_block = ceil_div(ceil_div(tokens, tokens <= kRouteCluster ? kMaxCluster : most), 32) * 32;
   if (*per_block > 65504) *per_block = 65504;
   *blocks = ceil_div(tokens, *per_block);
 }

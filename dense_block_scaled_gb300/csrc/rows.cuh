@@ -4,8 +4,7 @@
 
 namespace tkg {
 
-// x = quotient * d + remainder, in 32 bits where x fits (a 64-bit division takes some 70 instructions, as many as the
-// work on 16 bytes of a row).
+// x = quotient * d + remainder, in 32 bits where x fits (a 64-bit division takes some 70 instructions).
 __device__ __forceinline__ void divide(unsigned long long x, unsigned d, int& quotient, int& remainder) {
   if ((x >> 32) == 0) {
     const unsigned q = unsigned(x) / d;

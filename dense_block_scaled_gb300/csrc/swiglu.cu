@@ -17,9 +17,9 @@
 namespace tkg {
 namespace {
 
-// Columns of a piece; warps of a block and pieces of a warp, one after another.  Blocks go out at about 130 a us, so they
-// may not be too small (8192 x 4096 to 8 bits with 2 warps of 2 pieces 34 us, with 8 warps 16.5), and a warp that takes
-// more pieces leaves a longer last round (4 pieces: 17.5).
+// Columns of a piece; warps of a block and pieces of a warp, one after another.  Blocks go out at about 1000 a us, so they
+// may not be too small (8192 x 4096 to 8 bits, 131072 pieces: with 2 warps of 2 pieces 34 us, with 8 warps 16.5), and a
+// warp that takes more pieces leaves a longer last round (4 pieces: 17.5).
 constexpr int kPiece = 256, kSaveWarps = 8, kGateWarps = 8;
 
 __device__ __forceinline__ void unpack(const uint4& v, float (&x)[8]) {
@@ -30,6 +30,7 @@ __device__ __forceinline__ void unpack(const uint4& v, float (&x)[8]) {
     x[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
   }
 }
+
 // Codes of a lane's 8 columns, and their block's scale code (the same in its four lanes).
 __device__ __forceinline__ uint2 to_codes(const float (&x)[8], uint32_t& scale) {
   float a = 0.f;
@@ -45,6 +46,7 @@ __device__ __forceinline__ uint2 to_codes(const float (&x)[8], uint32_t& scale) 
   q.y = cvt_e4m3x2(x[4] * inv, x[5] * inv) | (cvt_e4m3x2(x[6] * inv, x[7] * inv) << 16);
   return q;
 }
+
 // Two FP32 values in one register pair, and the instructions that take such pairs: the activation is bound by how many
 // instructions its arithmetic takes as soon as HBM is not.
 struct Two {
@@ -101,8 +103,9 @@ __device__ __forceinline__ Two two_of_codes(uint32_t codes, Two scale) {
 
 constexpr int kSavePieces = 2;
 using SavePieces = Pieces<kSavePieces, kSaveWarps, kPiece>;
-__global__ void __launch_bounds__(32 * kSaveWarps) save_kernel(int rows, int k, const uint16_t* __restrict__ X, size_t ldx,
-                                                           uint8_t* __restrict__ Q, uint8_t* __restrict__ sf) {
+__global__ void __launch_bounds__(32 * kSaveWarps) save_kernel(int rows, int k, const uint16_t* __restrict__ X,
+                                                               size_t ldx, uint8_t* __restrict__ Q,
+                                                               uint8_t* __restrict__ sf) {
   ptx::pdl_launch_dependents();
   const int lane = threadIdx.x & 31;
   SavePieces at(rows, k);

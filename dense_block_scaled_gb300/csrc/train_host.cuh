@@ -178,24 +178,33 @@ inline bool train_narrow_gradient(int n, int hidden, int tiles) {
 // what it loses is 1/30 of their own rounding's 2^-9 at 16384 terms of one sign, and less where signs differ.
 constexpr int kSumStages = 32;
 
-// Launch of a small kernel that waits for the previous grid itself (griddepcontrol.wait).
+// Launch of a small kernel that waits for the previous grid itself (griddepcontrol.wait), in clusters of `cluster` blocks.
 template <typename... P, typename... Args>
-tkg_status launch_small(void (*kern)(P...), dim3 grid, dim3 block, cudaStream_t stream, unsigned smem, Args... args) {
+tkg_status launch_small_cluster(void (*kern)(P...), dim3 grid, dim3 block, unsigned cluster, cudaStream_t stream,
+                                unsigned smem, Args... args) {
   cudaLaunchConfig_t cfg = {};
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   cfg.gridDim = grid;
   cfg.blockDim = block;
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = cluster;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
   if (cudaLaunchKernelEx(&cfg, kern, P(args)...) != cudaSuccess) {
     cudaGetLastError();
     return TKG_ERR_CUDA;
   }
   return TKG_OK;
+}
+template <typename... P, typename... Args>
+tkg_status launch_small(void (*kern)(P...), dim3 grid, dim3 block, cudaStream_t stream, unsigned smem, Args... args) {
+  return launch_small_cluster(kern, grid, block, 1u, stream, smem, args...);
 }
 
 }  // namespace tkg
