@@ -615,7 +615,8 @@ __device__ __noinline__ int choose_slowly(const RouteParams& p, int t, bool by_l
 
 // BY_LOGIT: no bias and no limit to groups.
 template <int PER, typename L, bool WIDE, bool BY_LOGIT>
-__global__ void __launch_bounds__(32 * kRouteWarps<PER, BY_LOGIT && sizeof(L) == 2>) route_choose_kernel(const RouteParams p) {
+__global__ void __launch_bounds__(32 * kRouteWarps<PER, BY_LOGIT && sizeof(L) == 2>)
+    route_choose_kernel(const __grid_constant__ RouteParams p) {
   constexpr bool kPacked = BY_LOGIT && sizeof(L) == 2;
   extern __shared__ int s_dyn[];
   // bits of the tokens that chose an expert, how many did before, each expert's first row (one block of tokens or cluster),
@@ -820,8 +821,7 @@ tkg_status launch_choose(RouteParams& p, cudaStream_t stream) {
     const bool by_logit = !p.bias && p.topk_groups == p.groups;
     const bool packed = by_logit && sizeof(L) == 2;
     const int most_warps = packed ? kRouteWarps<PER, true> : kRouteWarps<PER, false>;
-    route_blocks(p.tokens, kSMs * (packed ? kRouteOnSM<PER, true> : kRouteOnSM<PER, false>), &p.blocks, &p.per_block);
-    p.cluster = p.tokens <= kRouteCluster ? p.blocks : 1;
+    route_blocks(p, kSMs * (packed ? kRouteOnSM<PER, true> : kRouteOnSM<PER, false>), packed);
     const int there = p.per_block < kRouteTokens ? p.per_block : kRouteTokens;
     unsigned smem = unsigned((p.experts * (kRouteWords + 2) + there * p.topk + 1) / 2 * 2) * 4u;
     // values of the groups' choice, one row per warp, as large as its second time in 64 bits needs
@@ -841,7 +841,7 @@ tkg_status launch_choose(RouteParams& p, cudaStream_t stream) {
         set[dev] = true;
       }
     }
-    const int warps = p.tokens < 4 ? 4 : (p.tokens < most_warps ? p.tokens : most_warps);
+    const int warps = p.per_block < 4 ? 4 : (p.per_block < most_warps ? p.per_block : most_warps);
     return launch_small_cluster(kern, dim3(unsigned(p.blocks)), dim3(32u * unsigned(warps)), unsigned(p.cluster), stream,
                                 smem, p);
   });

@@ -9,8 +9,8 @@
 //
 // Two kernels.  The first (moe_choose.cuh) chooses; within a block of tokens, the rank of (t, e) is the number of earlier
 // tokens that chose e: a population count of one bit per token and expert.  The block leaves its ranks (in `rows`) and its
-// count per expert.  The second adds what earlier blocks and experts have.  Up to 256 tokens a cluster of blocks does both
-// at once, its counts exchanged through shared memory.
+// count per expert.  The second adds what earlier blocks and experts have.  For a few tokens (route_blocks) one block or a
+// cluster does both at once, its counts exchanged through shared memory.
 // Nothing depends on the order of atomics: those are bit sets.
 #include "moe_route.cuh"
 
@@ -22,7 +22,7 @@ constexpr int kPlaceEntries = 1024;        // choices that a placing block takes
 
 // Block b places the choices of the blocks of tokens [b each, (b + 1) each).  It adds up all counts itself: 16-byte loads
 // of 8 experts, all of a thread's on their way at once.
-__global__ void __launch_bounds__(kPlaceThreads) route_place_kernel(const RouteParams p, int each) {
+__global__ void __launch_bounds__(kPlaceThreads) route_place_kernel(const __grid_constant__ RouteParams p, int each) {
   // sums of a thread's counts: of all blocks, and of the earlier ones; then [each][experts]: first row of an expert's
   // choices of a block of tokens
   __shared__ __align__(16) int s_part[2][kPlaceThreads * 8];
@@ -135,9 +135,7 @@ extern "C" {
 
 size_t tkg_moe_route_workspace_bytes(int tokens, int experts) {
   if (tokens < 0 || experts < 1 || experts > kMaxRouteExperts || tokens > kMaxSize) return 0;
-  int blocks = 0, per_block = 0;
-  if (tokens > kRouteCluster) route_blocks(tokens, 2 * kSMs, &blocks, &per_block);   // the most there can be
-  return size_t(blocks) * size_t((experts + 7) / 8 * 8) * 2 + 16;
+  return size_t(route_most_blocks(tokens)) * size_t((experts + 7) / 8 * 8) * 2 + 16;
 }
 
 tkg_status tkg_moe_route(int tokens, int experts, int topk, const void* logits, tkg_type type, int ld,

@@ -35,7 +35,7 @@ struct RouteParams {
   int* rows;
   int* slots;
   uint16_t* counts;           // [blocks][experts, rounded up to 8]
-  int per_block;              // tokens, a multiple of 32
+  int per_block;              // tokens
   int blocks;
   int cluster;                // blocks of a cluster: all of them, or 1
 };
@@ -114,14 +114,38 @@ __device__ __forceinline__ float logit_at(const RouteParams& p, int t, int e) {
 }
 // ---- host
 constexpr int kSMs = 152;
-constexpr int kMaxCluster = 8, kRouteCluster = 32 * kMaxCluster;   // blocks of a cluster at most, and its tokens
-// Tokens in blocks of 32 that make a cluster, which needs no second kernel (256 x 128 5.0 us from a graph and 7.9 from the
-// host, with a second kernel 6.1 and 10.3; but 512, in blocks of 64, 7.0 and 8.0 against 6.2 and 9.6, and 512 x 256 in
-// groups 14.7 against 11.3), or in `most` blocks of 32 at least, of no more tokens than 16 bits can count.
-inline void route_blocks(int tokens, int most, int* blocks, int* per_block) {
-  *per_block = ceil_div(ceil_div(tokens, tokens <= kRouteCluster ? kMaxCluster : most), 32) * 32;
-  if (*per_block > 65504) *per_block = 65504;
-  *blocks = ceil_div(tokens, *per_block);
+// How tokens are cut into blocks.  Choosing is spread over the SMs, but each block of tokens has a row of counts that
+// the second kernel's blocks all read.  So: one block up to 16 tokens; a cluster of 8, which needs no second kernel, up to
+// 256 (by BF16 logits alone; other choices take several times the instructions: 128); then blocks of T / 64 tokens, but 8 to
+// 32 (16) of them; and no more blocks than `most`, nor tokens in one than 16 bits can count.
+// From a graph, us, 128 experts by BF16 softmax / 256 by FP32 sigmoid with a bias in groups:
+//     16 tokens: one block 2.9 / 6.1, cluster 3.4 / 6.9        64: cluster of 8 3.6 / 6.6, of 2 4.7 / 9.7
+//    256: cluster 5.0 / 10.2, two kernels 5.1 / 8.1 (2 more from the host)
+//    512: blocks of 8 5.5 / 9.1, of 16 5.6 / 9.5, of 32 6.2 / 11.3     1024: of 8 6.8 / 10.6, of 16 6.4 / 10.2
+//   2048: of 8 7.3 / 13.6, of 16 6.8 / 14.2, of 32 6.6 / -             4096: of 14 10.6, of 32 8.6 / of 27 16.7, of 32 17.3
+constexpr int kMaxCluster = 8, kRouteAlone = 16, kRouteLeast = 8;
+inline void route_blocks(RouteParams& p, int most, bool packed) {
+  const int t = p.tokens, in_cluster = packed ? 256 : 128, widest = packed ? 32 : 16;
+  p.cluster = 1;
+  if (t <= kRouteAlone) {
+    p.per_block = t;
+  } else if (t <= in_cluster) {
+    p.per_block = ceil_div(t, kMaxCluster);
+    p.cluster = ceil_div(t, p.per_block);
+  } else {
+    int least = ceil_div(t, 64);
+    least = least < kRouteLeast ? kRouteLeast : (least > widest ? widest : least);
+    p.per_block = ceil_div(t, most);
+    if (p.per_block < least) p.per_block = least;
+    if (p.per_block > 65504) p.per_block = 65504;
+  }
+  p.blocks = ceil_div(t, p.per_block);
+}
+// Blocks at most, for any kind of choice.
+inline int route_most_blocks(int tokens) {
+  const int at_least = ceil_div(tokens, 2 * kSMs);
+  const int per_block = at_least < kRouteLeast ? kRouteLeast : (at_least > 65504 ? 65504 : at_least);
+  return ceil_div(tokens, per_block);
 }
 
 // moe_choose_bf16.cu, moe_choose_f32.cu: the choices of all tokens; sets p's blocks of tokens.

@@ -15,8 +15,8 @@ namespace tkg {
 namespace {
 
 template <int PER, typename L, bool WIDE>
-__global__ void __launch_bounds__(256) route_grad_kernel(const RouteParams p, const float* dweights, void* dlogits,
-                                                         size_t ldd) {
+__global__ void __launch_bounds__(256) route_grad_kernel(const __grid_constant__ RouteParams p,
+                                                         const float* dweights, void* dlogits, size_t ldd) {
   ptx::pdl_launch_dependents();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int t = blockIdx.x * 8 + warp;

@@ -102,7 +102,7 @@ def normal(*shape, seed=0, dtype=F32, scale=1.5):
 
 
 @pytest.mark.parametrize("dtype", [BF16, F32], ids=["bf16", "f32"])
-@pytest.mark.parametrize("tokens", [1, 2, 31, 32, 33, 65, 256, 257, 511, 512, 513, 1000])
+@pytest.mark.parametrize("tokens", [1, 2, 16, 17, 31, 32, 33, 65, 128, 129, 256, 257, 511, 512, 513, 1000])
 @pytest.mark.parametrize("experts,topk", [(1, 1), (2, 2), (7, 3), (32, 8), (33, 1), (60, 4), (64, 6), (100, 32), (128, 8),
                                           (200, 5), (256, 8), (511, 9), (512, 2)])
 def test_sizes(tokens, experts, topk, dtype):
