@@ -448,7 +448,9 @@ __device__ __forceinline__ int choose_few(const RouteParams& p, int t, const flo
     if (mine == bound) mine = 0;
   }
   const float margin = wrong > 0.f ? 2.f * wrong : 0.f;
-  const float least = bound > key_of(-INFINITY) ? value_of(bound) - margin : -FLT_MAX;
+  // (no lower than the least finite number, which the difference may pass: what is -infinity -- lanes past the last expert,
+  // experts of groups that go -- is no candidate)
+  const float least = bound > key_of(-INFINITY) ? fmaxf(value_of(bound) - margin, -FLT_MAX) : -FLT_MAX;
   int count = 0;
 #pragma unroll
   for (int i = 0; i < PER; ++i) count += c[i] >= least ? 1 : 0;
