@@ -51,7 +51,6 @@ __device__ __forceinline__ unsigned long long warp_max(unsigned long long k) {
 __device__ __forceinline__ float warp_most(float x) {
   return __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(x)));
 }
-__device__ __forceinline__ float exp_of(float x) { return expf(x); }
 // exp in 64 bits, without a branch, so that several run side by side (CUDA's took 1 us each here, one after the other), by
 // the reduction of Cody and Waite, log 2 in two parts, and the Taylor series:
 // x = n log 2 + r with |r| <= log(2) / 2, the series of e^r to r^13 (its rest is below 2^-58), and 2^n in two halves, as a
@@ -93,8 +92,7 @@ __device__ __forceinline__ F softmax_sum(const float (&z)[PER], int lane, int ex
   sum = warp_sum(sum);
   return sum == F(0) ? F(1) : sum;
 }
-template <typename F>
-__device__ __forceinline__ F sigmoid_of(F z) { return F(1) / (F(1) + exp_of(-z)); }
+__device__ __forceinline__ double sigmoid_of(double z) { return 1.0 / (1.0 + exp_of(-z)); }
 
 // Choice scores c = s + b of a lane's run, for the choice alone: in FP32 by approximate exponentials and quotients (a
 // correctly rounded quotient and exp took 20 instructions each).  `wrong`: what each may be off by.
@@ -705,7 +703,7 @@ __global__ void __launch_bounds__(32 * kRouteWarps<PER, BY_LOGIT && sizeof(L) ==
         // lane j: its expert's score
         const bool mine = lane < p.topk;
         if (p.sigmoid) {
-          w = sigmoid_of(zj);
+          w = sigmoid_part(zj, p.renormalise ? sigmoid_top(zj, mine) : 0.f);
         } else {
           if (p.renormalise) {   // relative to the largest of the chosen: none of them is lost
             sub = warp_fmax(mine ? zj : -INFINITY);

@@ -345,8 +345,10 @@ tkg_status tkg_gemm_grouped_dev_bf16_wgrad(int groups, const int *m_sizes_dev, i
  *   weight_j = scale * s_j, or renormalised scale * s_j / sum_i s_i over the chosen
  * The choice is that of the exact scores: where FP32 does not decide between two
  * neighbours they are computed again in 64 bits, and without bias and groups the
- * logits themselves are compared.  NaN comes after every number; a row (softmax),
- * or sum of the chosen (renormalised), of zeros gives weights 0.
+ * logits themselves are compared.  NaN comes after every number.  A row (softmax),
+ * or the chosen of one (renormalised), of logits that are all -infinity gives
+ * weights 0; other renormalised weights are formed relative to the largest of the
+ * chosen, however low their logits are.
  * keep (or NULL): a byte per token; 0 for one that is not routed (padding).
  * Written: ids and weights (tokens x topk; not routed: -1 and 0);
  *   sizes (experts): the rows of each expert, as tkg_gemm_grouped_dev_* take them;
