@@ -82,3 +82,42 @@ def test_sigmas_themselves(base):
     ids, w, *_ = route(z, 8, scores="sigmoid", renormalise=False, scale=2.5)
     want = 2.5 * torch.exp(log_sigmoid(z).gather(1, ids.long()))
     assert ((w - want).abs() <= 2.0 ** -16 * want + 10 * STEP).all()
+
+
+def weights_of(z, ids, renormalise):
+    low = (z.clamp(max=0) - torch.log1p(torch.exp(-z.abs()))).gather(1, ids.clamp(min=0))
+    w = torch.softmax(low, dim=1) if renormalise else torch.exp(low)
+    return torch.where(ids >= 0, 2.5 * w, 0.0)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16], ids=["f32", "bf16"])
+@pytest.mark.parametrize("base", BASES)
+@pytest.mark.parametrize("tokens,experts,topk", [(1, 8, 2), (60, 64, 6), (300, 200, 32)])
+def test_gradient_of_low_logits(tokens, experts, topk, base, dtype):
+    z = (normal(tokens, experts) + base).to(dtype)
+    z[1::3] = normal(tokens, experts, dtype=dtype)[1::3]               # and of ordinary ones
+    z[2::3, ::2] = normal(tokens, experts, dtype=dtype)[2::3, ::2]     # and of both in a row
+    keep = torch.arange(tokens, device="cuda") % 5 != 3
+    ids = torch.rand(tokens, experts, device="cuda").topk(topk, dim=1).indices   # not the largest ones alone
+    ids = torch.where(keep[:, None], ids, -1)
+    dw = normal(tokens, topk, scale=1.0)
+    half = 2.0 ** -8 if dtype == BF16 else 2.0 ** -23
+    for renormalise in (True, False):
+        got = torch.empty_like(z)
+        tkg.moe_route_grad(z, ids.to(torch.int32), dw, got, scores="sigmoid", renormalise=renormalise, scale=2.5)
+        x = z.to(F64).requires_grad_(True)
+        w = weights_of(x, ids, renormalise)
+        (w * dw.to(F64)).sum().backward()
+        w = w.detach()
+        of = dw.abs() + (w * dw.abs()).sum(dim=1, keepdim=True) if renormalise else dw.abs()
+        size = torch.zeros_like(x).scatter_add_(1, ids.clamp(min=0), w * of)
+        assert ((got.to(F64) - x.grad).abs() <= 2.0 ** -16 * size + half * x.grad.abs() + 1e-38).all()
+        # and against differences of the weights: along v, which spreads over 8 at most, a share's third derivative is below
+        # 1100 (8^3 + 3 x 8 x 4^2 and v's third moment) of it, and a sixth of that counts
+        v = torch.randn(tokens, experts, device="cuda", dtype=F64).clamp(-4, 4)
+        h = 1e-4
+        up, down = (weights_of(z.to(F64) + d * v, ids, renormalise) for d in (h, -h))
+        along, diff = (got.to(F64) * v).sum(dim=1), ((up - down) / (2 * h) * dw.to(F64)).sum(dim=1)
+        room = h * h * 1100 / 6 * 2.5 * dw.abs().sum(dim=1) + ((2.0 ** -16 * size + half * x.grad.abs()) * v.abs()).sum(dim=1)
+        assert ((along - diff).abs() <= room + 1e-9).all()
+    assert (got[~keep] == 0).all()
