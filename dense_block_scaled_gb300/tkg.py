@@ -12,6 +12,7 @@ from __future__ import annotations
 
 import ctypes
 import functools
+import operator
 import os
 import threading
 
@@ -539,10 +540,22 @@ def gemm_grouped_dev_bf16_wgrad(sizes_dev, dD, A, dB, alpha: float = 1.0, accumu
 # As above; the current GPU is asked for without torch's check that CUDA is initialised (0.1 us), as a tensor is on one.
 
 @functools.lru_cache(maxsize=64)
+def _kept_rule(scores, groups, topk_groups, renormalise, scale):
+    return ctypes.byref(RouteRule(scores, groups, topk_groups, renormalise, scale))
+
+
 def _rule(scores, groups, topk_groups, renormalise, scale):
+    """The rule as C takes it.  It is kept by its values alone: numbers of Python, made of what a caller may change."""
     if scores not in SCORES:
         raise ValueError(f"scores: one of {sorted(SCORES)} is wanted, got {scores!r}")
-    return ctypes.byref(RouteRule(SCORES[scores], groups, topk_groups, int(bool(renormalise)), scale))
+    if type(groups) is not int:
+        groups = operator.index(groups)
+    if type(topk_groups) is not int:
+        topk_groups = operator.index(topk_groups)
+    if not (-1 << 31 <= groups < 1 << 31 and -1 << 31 <= topk_groups < 1 << 31):
+        raise ValueError("groups, topk_groups: below 2^31 are wanted")
+    return _kept_rule(SCORES[scores], groups, topk_groups, 1 if renormalise else 0,
+                      scale if type(scale) is float else float(scale))
 
 
 @functools.lru_cache(maxsize=256)
@@ -588,8 +601,6 @@ def moe_route(logits, ids, weights, sizes, rows, slots, bias=None, keep=None, sc
             wanted.append(("keep", keep, torch.uint8 if keep.dtype is torch.uint8 else torch.bool, (tokens,), False))
         _refuse(wanted)
         ld = _pitch(logits, experts)
-    if type(scale) is not float:   # (a rule is kept by its values: not by a tensor that may change)
-        scale = float(scale)
     lib, handle = load(), _stream(stream, dev)
     at, nbytes, _keep = _workspace(workspace, moe_route_workspace_bytes(tokens, experts), logits, stream, handle)
     _check(lib.tkg_moe_route(tokens, experts, topk, logits.data_ptr(), kind, ld,
@@ -613,8 +624,6 @@ def moe_route_grad(logits, ids, dweights, dlogits, scores: str = "softmax", reno
                  ("dweights", dweights, torch.float32, (tokens, topk), False),
                  ("dlogits", dlogits, logits.dtype, (tokens, experts), True)))
         ld, lddz = _pitch(logits, experts), _pitch(dlogits, experts)
-    if type(scale) is not float:
-        scale = float(scale)
     _check(load().tkg_moe_route_grad(tokens, experts, topk, logits.data_ptr(), kind, ld,
                                      _rule(scores, 1, 1, renormalise, scale), ids.data_ptr(), dweights.data_ptr(),
                                      dlogits.data_ptr(), lddz, _stream(stream, dev)),
