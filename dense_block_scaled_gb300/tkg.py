@@ -759,6 +759,8 @@ def gemm_grouped_dev_mxfp8_wgrad(sizes_dev, dD, Q, sf, dB, slots=None, topk: int
     row slots[r] // topk (slots None: r).  accumulate: add to the float32 dB."""
     import torch
     groups, (cap, n), (tokens, k), dev = sizes_dev.shape[0], dD.shape, Q.shape, dD.get_device()
+    if topk > 0x7fffffff:   # (ctypes would drop the upper bits)
+        raise ValueError(f"topk: below 2^31 is wanted, got {topk}")
     gtype = _grad_type(dB, "dB", accumulate)
     if not (-1 < dev == torch._C._cuda_getDevice() == sizes_dev.get_device() == Q.get_device() == sf.get_device()
             == dB.get_device() and not (cap | n | k | tokens) >> 31 and dD.dtype is torch.bfloat16

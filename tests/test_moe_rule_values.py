@@ -34,3 +34,12 @@ def test_what_is_no_whole_number_is_refused(groups, stay):
 def test_numbers_past_32_bits_are_refused(groups, stay):
     with pytest.raises(ValueError, match="below 2\\^31"):
         tkg._rule("softmax", groups, stay, True, 1.0)
+
+
+@pytest.mark.parametrize("topk", [2 ** 31, 2 ** 32 + 2])
+def test_choices_per_token_past_32_bits_are_refused(topk):
+    m = lambda *s, dtype=torch.bfloat16: torch.empty(*s, dtype=dtype)
+    u8 = torch.uint8
+    with pytest.raises(ValueError, match="topk: below 2\\^31"):
+        tkg.gemm_grouped_dev_mxfp8_wgrad(m(4, dtype=torch.int32), m(10, 64), m(5, 32, dtype=u8), m(5, 1, dtype=u8),
+                                         m(4, 64, 32), topk=topk)
