@@ -246,8 +246,8 @@ __global__ void __launch_bounds__(32 * kGradWarps, 4) swiglu_grad_kernel(const G
           const Two d = two_of(dv[j]), s = sigma(g), silu = g * s, h = silu * u, wd = w * d;
           dots = fma2(d, h, dots);
           oh[j] = pack(h * w);
-          // sigma (1 + g (1 - sigma)) = sigma + silu (1 - sigma)
-          og[j] = pack(wd * u * fma2(silu, fma2(s, two(-1.f), two(1.f)), s));
+          // sigma (1 + g (1 - sigma)) = sigma + silu (1 - sigma), times u first: w dh u alone may be past FP32's range
+          og[j] = pack(wd * (u * fma2(silu, fma2(s, two(-1.f), two(1.f)), s)));
           ou[j] = pack(wd * silu);
         }
         *reinterpret_cast<uint4*>(dx + c) = make_uint4(og[0], og[1], og[2], og[3]);
