@@ -8,8 +8,8 @@
 //
 // All of it is bound by HBM: each input byte is read once, each output byte written once.  A warp takes pieces of 256
 // columns, a lane 8 of them (16 bytes of BF16, 8 of codes), four lanes a block of 32.  65536 rows of 2 x 2048 with their
-// checkpoint 151 us (1082 MB, 159 at the copy rate), without 111 (118); 8192 x 4096 to 8 bits 16.5 us (15.0); the
-// gradient of 16004 rows x 1408, 30% of them padding, 28.2 us (23.4), of 65536 rows 101 (96).
+// checkpoint 154 us (1082 MB, 159 at the copy rate), without 112 (118); 8192 x 4096 to 8 bits 16.6 us (15.0); the
+// gradient of 16004 rows x 1408, 30% of them padding, 28.8 us (23.4), of 65536 rows 103 (96).
 #include "mxfp8.cuh"
 #include "rows.cuh"
 #include "train_host.cuh"
@@ -83,8 +83,10 @@ __device__ __forceinline__ uint32_t pack(Two x) {
   return ptx::pack_bf16x2(f.x, f.y);
 }
 
-// sigma by the approximations of the exponential and the reciprocal.  (Flushing subnormals: a sigma below 2^-126 is 0.
-// The forms that keep them take four instructions more each.)
+// sigma by the approximations of the exponential and the reciprocal, for x from kFar on.  (They flush subnormals: a sigma
+// below 2^-126 is 0.  The forms that keep them take four instructions more each; gates below kFar are rare, and where a
+// lane has one, it makes those again.)
+constexpr float kFar = -87.f;
 __device__ __forceinline__ Two sigma(Two x) {
   const float2 y = both(x * two(-kLog2e));
   const float2 z = both(two(ptx::ex2(y.x), ptx::ex2(y.y)) + two(1.f));
@@ -99,6 +101,34 @@ __device__ __forceinline__ Two two_of(uint32_t bf16x2) {
 __device__ __forceinline__ Two two_of_codes(uint32_t codes, Two scale) {
   const float2 f = e4m3x2_values(codes);
   return two(f.x, f.y) * scale;
+}
+
+// Gates below kFar.  There sigma(x) is exp(x), and 1 - sigma(x) is 1, to FP32's last bit.  exp(x) = t^4 with t = exp(x / 4),
+// x / 4 being exact: t is normal down to x = -349, and a product with large numbers between its factors is right where
+// exp(x) itself would be below FP32's numbers.  A lane that has one of them among its eight columns makes these again, out
+// of the way of the registers of the rest: the 65536 rows above take 154 us (152 without it; 170 where it stood in the
+// loop), with one gate of 100 far 232 and with all of them 383.
+__device__ __forceinline__ float far_gate(float g, float u) {   // silu(g) u
+  const float t = expf(0.25f * g);
+  return (((u * t) * (g * t)) * t) * t;
+}
+__device__ __forceinline__ uint16_t bf16_of(float x) { return uint16_t(ptx::pack_bf16x2(x, 0.f)); }
+// The largest of eight BF16 taken as unsigned numbers, two at a time: the farthest below 0 (or NaN), if any is.
+__device__ __forceinline__ bool any_far(const uint4& v) {
+  const uint32_t m = __vmaxu2(__vmaxu2(v.x, v.y), __vmaxu2(v.z, v.w));
+  constexpr uint32_t kBits = 0xc2aeu;   // kFar
+  return (m & 0xffffu) > kBits || (m >> 16) > kBits;
+}
+__device__ __forceinline__ uint32_t pick(const uint4& v, int i) { return i == 0 ? v.x : (i == 1 ? v.y : (i == 2 ? v.z : v.w)); }
+__device__ __forceinline__ float bf16_at(const uint4& v, int i) {
+  const uint32_t two = pick(v, i >> 1);
+  return __uint_as_float((i & 1) ? (two & 0xffff0000u) : (two << 16));
+}
+// (The inputs come in registers: the output may stand in their place.)
+__device__ __noinline__ void far_gates(uint4 g, uint4 u, uint16_t* h) {
+#pragma unroll 1
+  for (int i = 0; i < 8; ++i)
+    if (bf16_at(g, i) < kFar) h[i] = bf16_of(far_gate(bf16_at(g, i), bf16_at(u, i)));
 }
 
 constexpr int kSavePieces = 2;
@@ -153,7 +183,7 @@ __global__ void __launch_bounds__(32 * kGateWarps)
                     : make_uint4(0, 0, 0, 0);
 #pragma unroll
   for (int i = 0; i < kGatePieces; ++i) {
-    const bool there = at.row[i] >= 0 && at.col[i] < inner;
+    const bool there = at.row[i] >= 0 && at.col[i] < inner, far = any_far(v[i][0]);
     if constexpr (SAVE) {
 #pragma unroll
       for (int b = 0; b < 2; ++b) {
@@ -175,7 +205,10 @@ __global__ void __launch_bounds__(32 * kGateWarps)
       const Two x = two_of(g[j]);
       h[j] = pack(x * sigma(x) * two_of(u[j]));
     }
-    if (there) *reinterpret_cast<uint4*>(H + size_t(at.row[i]) * ldh + at.col[i]) = make_uint4(h[0], h[1], h[2], h[3]);
+    if (there) {
+      *reinterpret_cast<uint4*>(H + size_t(at.row[i]) * ldh + at.col[i]) = make_uint4(h[0], h[1], h[2], h[3]);
+      if (far) far_gates(v[i][0], v[i][1], H + size_t(at.row[i]) * ldh + at.col[i]);
+    }
   }
 }
 
@@ -196,8 +229,29 @@ struct GateGrad {
   float* dweights;            // may be null
 };
 
+// The same of the gradients; returns what these columns add to the sum of dh silu(g) u.
+__device__ __noinline__ float far_gradients(const GateGrad& p, long long row, int c, float w, uint4 dh) {
+  const uint8_t* q = p.Q + size_t(row) * 2 * size_t(p.inner) + c;
+  const uint8_t* sf = p.sf + size_t(row) * 2 * size_t(p.inner / 32);
+  const float scale_g = e8m0_value(__ldcg(sf + c / 32)), scale_u = e8m0_value(__ldcg(sf + (p.inner + c) / 32));
+  float dots = 0.f;
+#pragma unroll 1
+  for (int i = 0; i < 8; ++i) {
+    const float g = e4m3x2_values(__ldcg(q + i)).x * scale_g;
+    if (!(g < kFar)) continue;
+    const float u = e4m3x2_values(__ldcg(q + p.inner + i)).x * scale_u, d = bf16_at(dh, i);
+    const float h = far_gate(g, u), t = expf(0.25f * g), wd = w * d;
+    dots = fmaf(d, h, dots);
+    uint16_t* dx = p.dGU + size_t(row) * p.lddgu + c + i;
+    dx[0] = bf16_of(((u * t) * ((1.f + g) * t)) * ((wd * t) * t));   // sigma (1 + g (1 - sigma)) is exp(g) (1 + g)
+    dx[p.inner] = bf16_of((((wd * t) * (g * t)) * t) * t);
+    if (p.H) p.H[size_t(row) * p.ldh + c + i] = bf16_of(h * w);
+  }
+  return dots;
+}
+
 // The warps of a row take its pieces in turn; dw's parts are joined in a fixed order.
-__global__ void __launch_bounds__(32 * kGradWarps, 4) swiglu_grad_kernel(const GateGrad p) {
+__global__ void __launch_bounds__(32 * kGradWarps, 4) swiglu_grad_kernel(const __grid_constant__ GateGrad p) {
   __shared__ float s_part[kGradWarps];
   ptx::pdl_launch_dependents();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -243,7 +297,8 @@ __global__ void __launch_bounds__(32 * kGradWarps, 4) swiglu_grad_kernel(const G
         for (int j = 0; j < 4; ++j) {
           const Two g = two_of_codes((j < 2 ? qg[i].x : qg[i].y) >> (16 * (j & 1)), scale_g);
           const Two u = two_of_codes((j < 2 ? qu[i].x : qu[i].y) >> (16 * (j & 1)), scale_u);
-          const Two d = two_of(dv[j]), s = sigma(g), silu = g * s, h = silu * u, wd = w * d;
+          const Two d = two_of(dv[j]), s = sigma(g), silu = g * s, wd = w * d;
+          const Two h = silu * u;
           dots = fma2(d, h, dots);
           oh[j] = pack(h * w);
           // sigma (1 + g (1 - sigma)) = sigma + silu (1 - sigma), times u first: w dh u alone may be past FP32's range
@@ -253,6 +308,8 @@ __global__ void __launch_bounds__(32 * kGradWarps, 4) swiglu_grad_kernel(const G
         *reinterpret_cast<uint4*>(dx + c) = make_uint4(og[0], og[1], og[2], og[3]);
         *reinterpret_cast<uint4*>(dx + p.inner + c) = make_uint4(ou[0], ou[1], ou[2], ou[3]);
         if (ho) *reinterpret_cast<uint4*>(ho + c) = make_uint4(oh[0], oh[1], oh[2], oh[3]);
+        // a block with room for them, as 448 x 2^-3 is above kFar (what they added to the dots is 0)
+        if (sg[i] >= 125u) dots = dots + two(far_gradients(p, row, c, both(w).x, vd[i]), 0.f);
       }
     }
   }

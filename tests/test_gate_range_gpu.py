@@ -15,6 +15,7 @@ BF16, F64 = torch.bfloat16, torch.float64
 @pytest.mark.parametrize("up,grad,weight", [(2.0 ** 40, 2.0 ** 90, 1.0), (2.0 ** 100, 2.0 ** 30, 0.5), (2.0 ** 70, 1.0, 2.0 ** 60)])
 @pytest.mark.parametrize("inner", [32, 288])
 def test_large_factors_of_low_gates(up, grad, weight, inner):
+    torch.manual_seed(1)
     rows = 50
     X = normal(rows, 2 * inner).float()
     X[:, :inner] = -40 - 5 * X[:, :inner].abs()
