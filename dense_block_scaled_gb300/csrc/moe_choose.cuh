@@ -92,7 +92,7 @@ __device__ __forceinline__ F softmax_sum(const float (&z)[PER], int lane, int ex
   sum = warp_sum(sum);
   return sum == F(0) ? F(1) : sum;
 }
-__device__ __forceinline__ double sigmoid_of(double z) { return 1.0 / (1.0 + exp_of(-z)); }
+__device__ __forceinline__ double sigmoid64(double z) { return 1.0 / (1.0 + exp_of(-z)); }
 
 // Choice scores c = s + b of a lane's run, for the choice alone: in FP32 by approximate exponentials and quotients (a
 // correctly rounded quotient and exp took 20 instructions each).  `wrong`: what each may be off by.
@@ -141,7 +141,7 @@ __device__ __forceinline__ void choice_scores(const RouteParams& p, const float 
                                               double (&c)[PER]) {
   if (p.sigmoid) {
 #pragma unroll
-    for (int i = 0; i < PER; ++i) c[i] = sigmoid_of(double(z[i])) + double(bias[i]);
+    for (int i = 0; i < PER; ++i) c[i] = sigmoid64(double(z[i])) + double(bias[i]);
   } else {
     const double sum = softmax_sum(z, lane, p.experts, softmax_top(z), c, [](double x) { return exp_of(x); });
 #pragma unroll
@@ -200,7 +200,7 @@ struct Again {
 };
 template <int PER, typename L>
 __device__ __forceinline__ Again score_again(const RouteParams& p, int t, float zj, int lane, bool exact) {
-  if (p.sigmoid) return {sigmoid_of(double(zj)), true};
+  if (p.sigmoid) return {sigmoid64(double(zj)), true};
   float z[PER];
 #pragma unroll
   for (int i = 0; i < PER; ++i) z[i] = lane * PER + i < p.experts ? logit_at<L>(p, t, lane * PER + i) : -INFINITY;
@@ -703,7 +703,7 @@ __global__ void __launch_bounds__(32 * kRouteWarps<PER, BY_LOGIT && sizeof(L) ==
         // lane j: its expert's score
         const bool mine = lane < p.topk;
         if (p.sigmoid) {
-          w = sigmoid_part(zj, p.renormalise ? sigmoid_top(zj, mine) : 0.f);
+          w = chosen_sigmoids(zj, mine, p.renormalise);
         } else {
           if (p.renormalise) {   // relative to the largest of the chosen: none of them is lost
             sub = warp_fmax(mine ? zj : -INFINITY);

@@ -51,20 +51,16 @@ __device__ __forceinline__ float warp_fmax(float x) {
   for (int o = 16; o; o >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
   return x;
 }
-// sigma(z).  (exp(-z) overflows from z = -88.7 on, where exp(z) is subnormal and 1 + exp(z) rounds to 1.)
-__device__ __forceinline__ float sigmoid_of(float z) {
-  const bool far = z < -87.f;
-  const float e = expf(far ? z : -z);
-  return far ? e : 1.f / (1.f + e);
-}
-// Sigmas of the chosen that are divided by their sum: relative to e^top, top the largest of their logits where that is
-// negative (else 0), so that far logits, whose sigmas are all below FP32's numbers, keep their ratios.
-__device__ __forceinline__ float sigmoid_top(float z, bool chosen) {
-  const float top = fminf(warp_fmax(chosen ? z : -INFINITY), 0.f);
-  return top == -INFINITY ? 0.f : top;
-}
-__device__ __forceinline__ float sigmoid_part(float z, float top) {
-  return top < 0.f ? expf(z - top) / (1.f + expf(z)) : sigmoid_of(z);
+// Sigmas of the chosen (a lane each).  Where a logit is below kFarLogit sigma(z) is e^z, subnormal or less, and 1 / (1 +
+// exp(-z)) is 0 from -88.7 on.  Where they are divided by their sum, they are made relative to e^top, top the largest of the
+// logits where that is negative (else 0), so that they keep their ratios: e^(z - top) / (1 + e^z).  (A function of its own: in
+// place it cost routing by softmax, which has none of it, 2%.)
+constexpr float kFarLogit = -87.f;
+static __device__ __noinline__ float chosen_sigmoids(float z, bool chosen, bool renormalise) {
+  if (!__any_sync(0xffffffffu, chosen && z < kFarLogit)) return 1.f / (1.f + expf(-z));
+  float top = fminf(warp_fmax(chosen ? z : -INFINITY), 0.f);
+  if (!renormalise || top == -INFINITY) top = 0.f;
+  return top < 0.f || z < kFarLogit ? expf(z - top) / (1.f + expf(z)) : 1.f / (1.f + expf(-z));
 }
 // A lane's run of logits, in FP32; -inf past the end.  WIDE: rows allow loads of the whole run.
 template <int PER, typename L, bool WIDE>

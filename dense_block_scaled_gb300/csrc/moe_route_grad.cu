@@ -70,8 +70,8 @@ __global__ void __launch_bounds__(256) route_grad_kernel(const __grid_constant__
     const float dot = warp_sum(chosen ? pj * dw : 0.f);
     dz = p.scale * pj * (dw - dot);
   } else {
-    const float top = p.renormalise ? sigmoid_top(zj, chosen) : 0.f;
-    const float a = chosen ? sigmoid_part(zj, top) : 0.f;   // (renormalised: their ratios count)
+    float a = chosen_sigmoids(zj, chosen, p.renormalise);   // (renormalised: their ratios count)
+    if (!chosen) a = 0.f;
     const float b = chosen ? __fdiv_rn(1.f, 1.f + expf(zj)) : 0.f;   // 1 - a, also where a rounds to 1
     float da = dw * p.scale;
     if (p.renormalise) {
