@@ -26,7 +26,7 @@ SOURCES = ["tkg_api.cu", "quantize.cu", "gemm_bf16.cu", "gemm_mxfp8.cu", "gemm_n
            "linear_ce_few.cu", "grouped_grad.cu", "moe_route.cu", "moe_choose_bf16.cu", "moe_choose_f32.cu",
            "moe_route_grad.cu", "moe_rows.cu", "swiglu.cu"]
 HEADERS = ["ptx.cuh", "gemm_kernel.cuh", "gemm_splitk.cuh", "host_common.cuh", "train_kernel.cuh", "train_host.cuh",
-           "linear_ce.cuh", "mxfp8.cuh", "moe_route.cuh", "moe_choose.cuh", "rows.cuh"]
+           "linear_ce.cuh", "mxfp8.cuh", "moe_route.cuh", "moe_choose.cuh", "rows.cuh", "exp64.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",
               "-Xptxas", "-v", "-I", os.path.join(ROOT, "include")]

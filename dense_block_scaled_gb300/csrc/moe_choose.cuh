@@ -12,6 +12,7 @@
 #pragma once
 #include <cfloat>
 
+#include "exp64.cuh"
 #include "moe_route.cuh"
 
 namespace tkg {
@@ -51,35 +52,6 @@ __device__ __forceinline__ unsigned long long warp_max(unsigned long long k) {
 __device__ __forceinline__ float warp_most(float x) {
   return __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(x)));
 }
-// exp in 64 bits, without a branch, so that several run side by side (CUDA's took 1 us each here, one after the other), by
-// the reduction of Cody and Waite, log 2 in two parts, and the Taylor series:
-// x = n log 2 + r with |r| <= log(2) / 2, the series of e^r to r^13 (its rest is below 2^-58), and 2^n in two halves, as a
-// subnormal result takes two steps.  Infinities and NaN come out as they should: n is kept within what the halves can hold.
-__device__ __forceinline__ double exp_of(double x) {
-  const double top = 6755399441055744.0;   // 1.5 2^52: adding it rounds to a whole number
-  const double y = fma(fmin(fmax(x, -800.0), 800.0), 1.4426950408889634, top);
-  const int n = __double2loint(y);
-  const double m = y - top;
-  const double r = fma(m, -2.3190468138462996e-17, fma(m, -0.6931471805599453, fmin(fmax(x, -800.0), 800.0)));
-  double e = 1.0 / 6227020800.0;
-  e = fma(e, r, 1.0 / 479001600.0);
-  e = fma(e, r, 1.0 / 39916800.0);
-  e = fma(e, r, 1.0 / 3628800.0);
-  e = fma(e, r, 1.0 / 362880.0);
-  e = fma(e, r, 1.0 / 40320.0);
-  e = fma(e, r, 1.0 / 5040.0);
-  e = fma(e, r, 1.0 / 720.0);
-  e = fma(e, r, 1.0 / 120.0);
-  e = fma(e, r, 1.0 / 24.0);
-  e = fma(e, r, 1.0 / 6.0);
-  e = fma(e, r, 0.5);
-  e = fma(e, r, 1.0);
-  e = fma(e, r, 1.0);
-  const int h = n >> 1;
-  e = e * __hiloint2double((1023 + h) << 20, 0) * __hiloint2double((1023 + n - h) << 20, 0);
-  return x != x ? x : e;
-}
-
 // The exponentials of a lane's run and their sum over the row: 1 where all of them are 0.
 template <int PER, typename F, typename E>
 __device__ __forceinline__ F softmax_sum(const float (&z)[PER], int lane, int experts, float top, F (&e)[PER], E&& exponential) {
@@ -92,7 +64,7 @@ __device__ __forceinline__ F softmax_sum(const float (&z)[PER], int lane, int ex
   sum = warp_sum(sum);
   return sum == F(0) ? F(1) : sum;
 }
-__device__ __forceinline__ double sigmoid64(double z) { return 1.0 / (1.0 + exp_of(-z)); }
+__device__ __forceinline__ double sigmoid64(double z) { return 1.0 / (1.0 + exp64(-z)); }
 
 // Choice scores c = s + b of a lane's run, for the choice alone: in FP32 by approximate exponentials and quotients (a
 // correctly rounded quotient and exp took 20 instructions each).  `wrong`: what each may be off by.
@@ -143,7 +115,7 @@ __device__ __forceinline__ void choice_scores(const RouteParams& p, const float 
 #pragma unroll
     for (int i = 0; i < PER; ++i) c[i] = sigmoid64(double(z[i])) + double(bias[i]);
   } else {
-    const double sum = softmax_sum(z, lane, p.experts, softmax_top(z), c, [](double x) { return exp_of(x); });
+    const double sum = softmax_sum(z, lane, p.experts, softmax_top(z), c, [](double x) { return exp64(x); });
 #pragma unroll
     for (int i = 0; i < PER; ++i) c[i] = c[i] / sum + double(bias[i]);
   }
@@ -208,7 +180,7 @@ __device__ __forceinline__ Again score_again(const RouteParams& p, int t, float 
   double sum = 0.0;
   if (exact) {
 #pragma unroll
-    for (int i = 0; i < PER; ++i) sum += exp_of(double(z[i]) - double(top));
+    for (int i = 0; i < PER; ++i) sum += exp64(double(z[i]) - double(top));
   } else {
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
@@ -218,7 +190,7 @@ __device__ __forceinline__ Again score_again(const RouteParams& p, int t, float 
     }
   }
   sum = warp_sum(sum);
-  return {exp_of(double(zj) - double(top)) / (sum == 0.0 ? 1.0 : sum), exact};
+  return {exp64(double(zj) - double(top)) / (sum == 0.0 ? 1.0 : sum), exact};
 }
 __device__ __forceinline__ bool in_order(const Again& by, double c0, double s0, double c1, double s1) {
   return by.exact || fabs(c0 - c1) > fabs(s0 - s1) * kSumWrong;
