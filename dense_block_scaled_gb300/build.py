@@ -1,7 +1,8 @@
 """Builds libtkg.so in-tree: each CUDA translation unit compiled for sm_103a
 in parallel with nvcc, then linked into one shared library.  With --check it
-builds libtkg_check.so instead: the same sources with TKG_CHECK=1, every
-kernel verifying its internal invariants (include/tkg_gemm.h, check builds).
+builds libtkg_check.so instead: the same sources with TKG_CHECK=1, the GEMMs,
+the training-side kernels and routing verifying their internal invariants
+(include/tkg_gemm.h, check builds).
 
     python -m dense_block_scaled_gb300.build [--force] [--verbose] [--check]
 """

@@ -421,9 +421,10 @@ __device__ __forceinline__ int choose_few(const RouteParams& p, int t, const flo
   // (no lower than the least finite number, which the difference may pass: what is -infinity -- lanes past the last expert,
   // experts of groups that go -- is no candidate)
   const float least = bound > key_of(-INFINITY) ? fmaxf(value_of(bound) - margin, -FLT_MAX) : -FLT_MAX;
+  auto candidate = [&](int i) { return c[i] >= least && invariant(lane * PER + i < p.experts, p.status); };
   int count = 0;
 #pragma unroll
-  for (int i = 0; i < PER; ++i) count += c[i] >= least ? 1 : 0;
+  for (int i = 0; i < PER; ++i) count += candidate(i) ? 1 : 0;
   int upto = count;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -436,7 +437,7 @@ __device__ __forceinline__ int choose_few(const RouteParams& p, int t, const flo
   __syncwarp();
 #pragma unroll
   for (int i = 0; i < PER; ++i)
-    if (c[i] >= least) *to++ = make_float2(c[i], __int_as_float(lane * PER + i));
+    if (candidate(i)) *to++ = make_float2(c[i], __int_as_float(lane * PER + i));
   __syncwarp();
   const float2 own = few[lane];   // (past n: whatever is there)
   int rank = 0;
@@ -670,6 +671,7 @@ __global__ void __launch_bounds__(32 * kRouteWarps<PER, BY_LOGIT && sizeof(L) ==
           id = clear && p.topk <= kFewTopk ? choose_few<PER, L>(p, t, c, wrong, lane, s_few[warp], zj) : -1;
           const bool slow = __shfl_sync(0xffffffffu, id, 0) < 0;
           if (slow) id = choose_slowly<PER, L>(p, t, BY_LOGIT, s_bias, most_bias, lane, box, s_few[warp]);
+          if (!invariant(unsigned(id) < unsigned(p.experts), p.status)) id = 0;
           if (!BY_LOGIT || slow) zj = logit_at<L>(p, t, id);
         }
         // lane j: its expert's score
@@ -689,7 +691,8 @@ __global__ void __launch_bounds__(32 * kRouteWarps<PER, BY_LOGIT && sizeof(L) ==
           w = all == 0.f ? 0.f : __fdiv_rn(w, all);
         }
         w *= p.scale;
-        if (mine) atomicOr(s_bits + id * kRouteWords + (i >> 5), 1u << (i & 31));
+        if (mine && invariant(unsigned(id) < unsigned(p.experts), p.status))
+          atomicOr(s_bits + id * kRouteWords + (i >> 5), 1u << (i & 31));
       }
       if (lane < p.topk) {
         s_ids[i * p.topk + lane] = id;
@@ -769,7 +772,7 @@ __global__ void __launch_bounds__(32 * kRouteWarps<PER, BY_LOGIT && sizeof(L) ==
     const int e = s_ids[i];
     const int row = e < 0 ? -1 : s_first[e] + rank_of(e, i / p.topk);
     p.rows[base + i] = row;
-    if (row >= 0) p.slots[row] = base + i;
+    if (row >= 0 && invariant(row < p.tokens * p.topk, p.status)) p.slots[row] = base + i;
     if (base + i >= carry) p.slots[base + i] = -1;
   }
   if (p.cluster > 1) {   // no block leaves while another reads its counts

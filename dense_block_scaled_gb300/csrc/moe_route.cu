@@ -112,7 +112,7 @@ __global__ void __launch_bounds__(kPlaceThreads) route_place_kernel(const __grid
     if (e >= 0) {
       const int row = s_base[int(i - begin) / per * p.experts + e] + rank;
       p.rows[i] = row;
-      p.slots[row] = int(i);
+      if (invariant(unsigned(row) < unsigned(p.tokens * p.topk), p.status)) p.slots[row] = int(i);
     }
     if (i >= s_all) p.slots[i] = -1;
   };
@@ -181,6 +181,7 @@ tkg_status tkg_moe_route(int tokens, int experts, int topk, const void* logits, 
   p.slots = slots;
   p.counts = static_cast<uint16_t*>(workspace);
   p.inverse = uint32_t((0x100000000ull + unsigned(p.per_group) - 1) / unsigned(p.per_group));
+  if (TKG_CHECK && (st = device_status_word(&p.status)) != TKG_OK) return st;
   st = type == TKG_TYPE_F32 ? launch_choose_f32(p, stream) : launch_choose_bf16(p, stream);
   if (st != TKG_OK || p.blocks == p.cluster) return st;
   int each = kPlaceEntries / (p.per_block * p.topk);

@@ -38,6 +38,7 @@ struct RouteParams {
   int per_block;              // tokens
   int blocks;
   int cluster;                // blocks of a cluster: all of them, or 1
+  unsigned int* status;       // check builds
 };
 
 template <typename F>

@@ -436,10 +436,11 @@ tkg_status tkg_gemm_grouped_dev_mxfp8_wgrad(int groups, const int *m_sizes_dev, 
 size_t tkg_gemm_grouped_dev_mxfp8_wgrad_workspace_bytes(int m_capacity, int k);
 
 /* Check builds.  `python -m dense_block_scaled_gb300.build --check` builds the
- * same library as libtkg_check.so with every kernel verifying its internal
- * invariants (tensor-memory column ranges of each MMA, scale copy and
- * accumulator load; ring-slot, accumulator, tile, group and GEMM-list
- * indices; the 16-byte alignment of TMA x coordinates).  A failed invariant
+ * same library as libtkg_check.so with the GEMMs, the training-side kernels and
+ * routing verifying their internal invariants (tensor-memory column ranges of
+ * each MMA, scale copy and accumulator load; ring-slot, accumulator, tile, group
+ * and GEMM-list indices; routing's candidates, choices and rows;
+ * the 16-byte alignment of TMA x coordinates).  A failed invariant
  * skips the access it guards and is reported by tkg_get_device_status as
  * TKG_ERR_CHECK; nothing traps.  Meant for testing, not for speed.
  *
