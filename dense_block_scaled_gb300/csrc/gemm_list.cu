@@ -54,7 +54,7 @@ tkg_status launch_list(const tkg_gemm_desc* const* gemms, int count, cudaStream_
 
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return TKG_ERR_CUDA;
-  static bool attr_set[64] = {};
+  static std::atomic<bool> attr_set[64] = {};
   if (!attr_set[dev]) {
     if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kLaunchSmem) != cudaSuccess)
       return TKG_ERR_CUDA;

@@ -5,6 +5,7 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cstdint>
 #include <cstdio>
 
@@ -137,7 +138,7 @@ tkg_status launch_gemm(const Problem& pr, cudaStream_t stream) {
 
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return TKG_ERR_CUDA;
-  static bool attr_set[64] = {};   // per instantiation and device (idempotent if two threads race)
+  static std::atomic<bool> attr_set[64] = {};   // per instantiation and device (set twice alike if two threads race)
   if (!attr_set[dev]) {
     if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kLaunchSmem) != cudaSuccess)
       return TKG_ERR_CUDA;
@@ -367,7 +368,7 @@ tkg_status launch_splitk(const Problem& pr, cudaStream_t stream) {
   auto kern = gemm_splitk_kernel<FMT, SPLIT, STAGES, AROWS>;
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return TKG_ERR_CUDA;
-  static bool attr_set[64] = {};
+  static std::atomic<bool> attr_set[64] = {};
   if (!attr_set[dev]) {
     if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes) != cudaSuccess)
       return TKG_ERR_CUDA;

@@ -166,7 +166,7 @@ tkg_status launch_few(int blocks, int smem, const TrainParams& p, const void* X,
   auto kern = ce_few_kernel<TT, DEPTH>;
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return TKG_ERR_CUDA;
-  static bool attr_set[64] = {};   // per instantiation and device (idempotent if two threads race)
+  static std::atomic<bool> attr_set[64] = {};   // per instantiation and device (set twice alike if two threads race)
   if (!attr_set[dev]) {
     if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kFewElements * 4) != cudaSuccess) {
       cudaGetLastError();

@@ -804,8 +804,8 @@ tkg_status launch_choose(RouteParams& p, cudaStream_t stream) {
     auto kern = by_logit ? route_choose_kernel<PER, L, decltype(wide)::value, true>
                          : route_choose_kernel<PER, L, decltype(wide)::value, false>;
     if (smem > 36000) {   // (beside 10 KB of its own)
-      static bool sets[2][64] = {};   // per instantiation and device
-      bool* set = sets[by_logit];
+      static std::atomic<bool> sets[2][64] = {};   // per instantiation and device (set twice alike if two threads race)
+      std::atomic<bool>* set = sets[by_logit];
       int dev = 0;
       if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return TKG_ERR_CUDA;
       if (!set[dev]) {

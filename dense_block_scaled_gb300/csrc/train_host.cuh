@@ -62,7 +62,7 @@ tkg_status launch_train(const CUtensorMap& tmA, const CUtensorMap& tmB, const CU
   if (p.n_tile > C::kSubs * C::kBN) return TKG_ERR_UNSUPPORTED;   // (no caller asks for it)
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return TKG_ERR_CUDA;
-  static bool attr_set[64] = {};   // per instantiation and device (idempotent if two threads race)
+  static std::atomic<bool> attr_set[64] = {};   // per instantiation and device (set twice alike if two threads race)
   if (!attr_set[dev]) {
     if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes) != cudaSuccess) {
       cudaGetLastError();
