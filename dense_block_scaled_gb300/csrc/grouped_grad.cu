@@ -194,7 +194,7 @@ tkg_status tkg_gemm_grouped_dev_mxfp8_wgrad(int groups, const int* m_sizes_dev, 
       return TKG_ERR_INVALID_ARG;
     if (!aligned_to(dD, 16) || !aligned_to(dB, 16)) return TKG_ERR_ALIGNMENT;
     int split = 0;   // (log2) as many warps per row as it has columns for, while the rows leave SMs idle
-    while (((long long)m_capacity << split) < 152 * 32 && (512 << split) < k) ++split;
+    while (((long long)m_capacity << split) < kSMs * 32 && (512 << split) < k) ++split;
     const long long blocks = (((long long)m_capacity << split) + kUnpackWarps - 1) / kUnpackWarps;
     if (blocks > kMaxSize) return TKG_ERR_UNSUPPORTED;
     st = launch_small(unpack_rows_kernel, dim3(unsigned(blocks)), dim3(32 * kUnpackWarps), stream, 0u, m_capacity, k, tokens,

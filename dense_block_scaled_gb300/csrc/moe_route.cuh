@@ -125,7 +125,6 @@ __device__ __forceinline__ float logit_at(const RouteParams& p, int t, int e) {
     return __uint_as_float(uint32_t(__ldcg(reinterpret_cast<const unsigned short*>(row) + e)) << 16);
 }
 // ---- host
-constexpr int kSMs = 152;
 // How tokens are cut into blocks.  Choosing is spread over the SMs, but each block of tokens has a row of counts that
 // the second kernel's blocks all read.  So: one block up to 16 tokens; a cluster of 8, which needs no second kernel, up to
 // 256 (by BF16 logits alone; other choices take several times the instructions: 128); then blocks of T / 64 tokens, but 8 to

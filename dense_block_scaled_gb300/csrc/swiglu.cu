@@ -397,7 +397,7 @@ tkg_status tkg_swiglu_grad(int rows, int inner, const void* Q, const void* sf, c
   p.split = 1;
   // As many warps per row as it has pieces for, while the rows leave SMs idle (a piece to each warp, 6 of them, whatever the
   // rows: 16004 rows x 1408 43 us in place of 28).  Blocks of 4 warps: of 8 the last round is longer (34 us).
-  while (p.split < kGradWarps && (long long)rows * p.split < 152 * 32 && p.split * kPiece < inner) p.split *= 2;
+  while (p.split < kGradWarps && (long long)rows * p.split < kSMs * 32 && p.split * kPiece < inner) p.split *= 2;
   const int warps = p.split > kGradLeast ? p.split : kGradLeast;
   return launch_small(swiglu_grad_kernel, dim3(unsigned(ceil_div(rows, warps / p.split))), dim3(unsigned(32 * warps)), stream, 0u, p);
 }

@@ -17,6 +17,8 @@ inline bool aligned_to(const void* p, size_t a) { return (reinterpret_cast<uintp
 // rounded up, and are 32 bits.
 constexpr int kMaxSize = 0x7fff0000;
 
+constexpr int kSMs = 152;   // of a GB300
+
 // k rows of an MN-major box: 64, or all there are rounded up to the MMA's 16 (rows past the end arrive as
 // zeros; a box that runs mostly past the end slows the load stream)
 inline uint32_t mn_box_rows(int k) { return k >= 64 ? 64u : uint32_t((k + 15) / 16 * 16); }
