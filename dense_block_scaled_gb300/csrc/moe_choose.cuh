@@ -163,8 +163,8 @@ __device__ __forceinline__ float bias_at(const RouteParams& p, int e) { return p
 // Candidates' scores (lane j < n: logit z) are made again in 64 bits.  These are slow here (16 cycles for an instruction of
 // an SM), and softmax has a sum over the row: that is first made of FP32 exponentials, whose arguments' roundings are put
 // back, added in 64 bits, so that it is off by little more than exp's 2 ulp, `kSumWrong` of itself.  It scales all
-// scores alike, so the order of two values c = s + b is right if they differ by more than that share of their
-// scores' difference; only else all of its terms are made in 64 bits.
+// scores alike, so the order of two values c = s + b is that of the exact sum if they differ by more than that share of
+// their scores' difference and what the sums with b are rounded by; only else all of its terms are made in 64 bits.
 constexpr double kSumWrong = 0x1p-21;
 struct Again {
   double score;
@@ -192,8 +192,9 @@ __device__ __forceinline__ Again score_again(const RouteParams& p, int t, float 
   sum = warp_sum(sum);
   return {exp64(double(zj) - double(top)) / (sum == 0.0 ? 1.0 : sum), exact};
 }
-__device__ __forceinline__ bool in_order(const Again& by, double c0, double s0, double c1, double s1) {
-  return by.exact || fabs(c0 - c1) > fabs(s0 - s1) * kSumWrong;
+// `size`: the sum of sizes of what was rounded on the way to c0 and c1, a unit of whose last places each may differ.
+__device__ __forceinline__ bool in_order(const Again& by, double c0, double s0, double c1, double s1, double size) {
+  return by.exact || fabs(c0 - c1) > fabs(s0 - s1) * kSumWrong + size * 0x1p-52;
 }
 
 // The order of n candidates (lane j < n: expert id) by their exact scores; lane j gets the j-th.  Rare: kept out of the
@@ -224,7 +225,7 @@ __device__ __noinline__ int order_again(const RouteParams& p, int t, int n, int 
     const float zj = __shfl_sync(0xffffffffu, z, from), bj = __shfl_sync(0xffffffffu, b, from);
     const double cn = __shfl_down_sync(0xffffffffu, cj, 1), sn = __shfl_down_sync(0xffffffffu, sj, 1);
     const float zn = __shfl_down_sync(0xffffffffu, zj, 1), bn = __shfl_down_sync(0xffffffffu, bj, 1);
-    const bool fine = lane + 1 >= n || in_order(by, cj, sj, cn, sn) || (zj == zn && bj == bn);
+    const bool fine = lane + 1 >= n || in_order(by, cj, sj, cn, sn, fabs(cj) + fabs(cn)) || (zj == zn && bj == bn);
     if (by.exact || __all_sync(0xffffffffu, fine)) break;
   }
   return out;
@@ -252,11 +253,11 @@ __device__ __noinline__ uint32_t groups_again(const RouteParams& p, int t, int n
       const int gi = __shfl_sync(0xffffffffu, g, i), e = __shfl_sync(0xffffffffu, id, i);
       if (gi == g && e != id) {
         rank += other > mine || (other == mine && e < id) ? 1 : 0;
-        fine &= in_order(by, c, by.score, ci, si);
+        fine &= in_order(by, c, by.score, ci, si, fabs(c) + fabs(ci));
       }
     }
     const bool counts = lane < n && rank < 2, leads = lane < n && rank == 0;
-    double two = 0.0, scores = 0.0;   // of the group
+    double two = 0.0, scores = 0.0, size = 0.0;   // of the group
 #pragma unroll 1
     for (int i = 0; i < n; ++i) {
       const double ci = __shfl_sync(0xffffffffu, counts ? c : 0.0, i);
@@ -264,6 +265,7 @@ __device__ __noinline__ uint32_t groups_again(const RouteParams& p, int t, int n
       if (__shfl_sync(0xffffffffu, g, i) == g) {
         two += ci;
         scores += si;
+        size += 2.0 * fabs(ci);   // (c, and the sum of two)
       }
     }
     const unsigned long long whole = key_of(two);
@@ -273,9 +275,10 @@ __device__ __noinline__ uint32_t groups_again(const RouteParams& p, int t, int n
       const int gi = __shfl_sync(0xffffffffu, leads ? g : -1, i);
       const unsigned long long other = __shfl_sync(0xffffffffu, whole, i);
       const double ti = __shfl_sync(0xffffffffu, two, i), si = __shfl_sync(0xffffffffu, scores, i);
+      const double zi = __shfl_sync(0xffffffffu, size, i);
       if (gi >= 0 && gi != g) {
         before += other > whole || (other == whole && gi < g) ? 1 : 0;
-        fine &= in_order(by, two, scores, ti, si);
+        fine &= in_order(by, two, scores, ti, si, size + zi);
       }
     }
     stay = __reduce_or_sync(0xffffffffu, leads && before < open ? 1u << (g << shift) : 0u);
