@@ -8,7 +8,7 @@
 //
 // Without bias and groups the logits themselves decide (both scores rise with them).  Otherwise FP32 scores decide
 // wherever they are further apart than they can be wrong; where two around a choice are closer, and not of the same logit
-// and bias, the candidates are ordered again in 64 bits, so that the choice is that of the exact scores.
+// and bias, the candidates are ordered again in 64 bits, so that the choice is that of c in 64 bits.
 #pragma once
 #include <cfloat>
 
@@ -19,8 +19,8 @@ namespace tkg {
 namespace {
 
 // Warps per block: as many as the registers of a lane's run allow, for a token's choice is a long chain of short steps;
-// and the blocks of an SM: two where BF16 logits decide by themselves (16384 x 128 15 us, with one 21; the others' FP32
-// choice takes 64 registers, and 16384 x 256 in groups 32 us with one, 37 in twice as many blocks).
+// and the blocks of an SM: two where BF16 logits decide by themselves (16384 x 128 15 us, with one 19; 65536 35 and 63;
+// the others' FP32 choice takes 64 registers, and 16384 x 256 in groups 29 us with one, 35 in twice as many blocks).
 template <int PER, bool PACKED>
 constexpr int kRouteWarps = PER <= 8 || PACKED ? 32 : 16;
 template <int PER, bool PACKED>

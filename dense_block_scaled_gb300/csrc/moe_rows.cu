@@ -4,7 +4,8 @@
 //   combine   Y[t] = sum_j w(t, j) O[rows(t, j)]     (FP32 sums in the order of j, rounded once)
 //
 // Each is the other's gradient (combine with weights 1).  A place outside [0, capacity), such as the -1 of a token that is
-// not routed, is left out: nothing is written for it, nothing is read.
+// not routed, is left out: dispatch writes nothing for it, combine reads nothing.  (Dispatch reads every token's row, on
+// its way beside the places.)
 //
 // Both are bound by HBM.  Threads go by token and, within its row, by 16 bytes, without a gap between tokens, so that X's
 // row is read once and sent to all its places, and all of a token's rows of O are on their way together.  Dispatch of 8192

@@ -343,9 +343,13 @@ tkg_status tkg_gemm_grouped_dev_bf16_wgrad(int groups, const int *m_sizes_dev, i
  *   the topk largest c of the experts left are chosen, in falling order; ties,
  *     of groups too, go to the lowest index
  *   weight_j = scale * s_j, or renormalised scale * s_j / sum_i s_i over the chosen
- * The choice is that of the exact scores: where FP32 does not decide between two
- * neighbours they are computed again in 64 bits, and without bias and groups the
- * logits themselves are compared.  NaN comes after every number.  A row (softmax),
+ * The choice is that of c in 64 bits: where FP32 does not decide between two
+ * neighbours they are computed again, and what is equal in 64 bits ties (two
+ * sigmoids that both round to 1; scores that a far bias rounds away).  Without
+ * bias and groups the logits themselves are compared.  NaN comes after every
+ * number, and a group with a NaN after every other.  Experts are best masked by a
+ * bias (or logits) of -infinity: a far finite one (-1e9) leaves FP32 nothing to
+ * decide by, and whole rows are computed in 64 bits.  A row (softmax),
  * or the chosen of one (renormalised), of logits that are all -infinity gives
  * weights 0; other renormalised weights are formed relative to the largest of the
  * chosen, however low their logits are.
@@ -407,7 +411,8 @@ tkg_status tkg_checkpoint_mxfp8(int rows, int k, const void *X, int ldx, void *Q
 
 /* Gated activation of rows [g | u] (2 * inner columns, BF16):
  *   H = bf16_rn(silu(g) * u), silu(x) = x / (1 + exp(-x))
- * and, unless Q and sf are NULL, the checkpoint of [g | u] (rows x 2 inner).
+ * and, unless Q and sf are NULL, the checkpoint of [g | u] (rows x 2 inner).  All
+ * rows are read and written, whatever they hold.
  * Requires inner % 8 == 0 (with a checkpoint inner % 32 == 0), pitches % 8 == 0. */
 tkg_status tkg_swiglu(int rows, int inner, const void *GU, int ldgu, void *H, int ldh, void *Q, void *sf,
                       cudaStream_t stream);
@@ -427,7 +432,9 @@ tkg_status tkg_swiglu_grad(int rows, int inner, const void *Q, const void *sf, c
 /* tkg_gemm_grouped_dev_bf16_wgrad with A's rows from a checkpoint of `tokens` rows
  * (Q, sf): row r is that of token slots[r] / topk (slots NULL: r), so that one saved
  * row serves all of its token's experts.  A row whose token is outside [0, tokens)
- * adds nothing.  The values are exact in BF16.  slots: m_capacity of them.
+ * is one of zeros: it adds nothing as long as its row of dD is finite.  The values
+ * that the calls above save are exact in BF16, and the workspace takes all rows as
+ * such (2 * k bytes for each of m_capacity).  slots: m_capacity of them.
  * Requires k % 32 == 0; workspace as for tkg_linear_ce_loss. */
 tkg_status tkg_gemm_grouped_dev_mxfp8_wgrad(int groups, const int *m_sizes_dev, int m_capacity, int n, int k,
                                             const void *dD, int tokens, const void *Q, const void *sf, const int *slots,

@@ -7,7 +7,7 @@ import pytest
 import torch
 
 from dense_block_scaled_gb300 import tkg
-from test_moe_route_gpu import check, normal
+from test_moe_route_gpu import check, normal, route
 
 pytestmark = pytest.mark.gpu
 F32, BF16 = torch.float32, torch.bfloat16
@@ -67,3 +67,26 @@ def test_all_but_a_few_masked_of_many(scores):
         for value in (LOWEST, -1e9, -torch.inf):
             for left, topk in ((3, 4), (7, 8), (8, 8), (experts // 2, 8), (20, 24)):
                 check(logits(200, experts, F32, left), topk, bias=masked(experts, left, value), scores=scores)
+
+
+@pytest.mark.parametrize("experts,groups,stay,topk", [(64, 8, 3, 6), (60, 6, 2, 4), (24, 24, 5, 4), (512, 8, 4, 8)])
+def test_a_group_with_a_nan_comes_last(experts, groups, stay, topk):
+    per = experts // groups
+    z = normal(100, experts)
+    b = normal(experts, scale=0.1)
+    b[per // 2] = float("nan")                                             # the first group, for all tokens
+    at = torch.arange(100, device="cuda") % (groups - stay - 1) + 1
+    z[torch.arange(100, device="cuda"), at * per + per - 1] = float("nan")     # and one more for each token
+    ids, *_ = route(z, topk, bias=b, scores="sigmoid", groups=groups, topk_groups=stay)
+    group = ids.long() // per
+    assert (group != 0).all() and (group != at[:, None]).all()
+    # the rest as without those groups
+    out = torch.zeros(100, groups, dtype=torch.bool, device="cuda")
+    out[:, 0] = True
+    out[torch.arange(100, device="cuda"), at] = True
+    out = out.repeat_interleave(per, dim=1)
+    c = torch.where(out, -100.0, torch.sigmoid(z.double()) + b.double()).unflatten(1, (groups, per))
+    best = c.sort(dim=2, descending=True).values[:, :, :2].sum(dim=2)
+    stays = torch.zeros_like(best, dtype=torch.bool).scatter_(1, best.topk(stay, dim=1).indices, True)
+    want = torch.where(stays[:, :, None], c, -1000.0).flatten(1).sort(dim=1, descending=True, stable=True).indices[:, :topk]
+    assert torch.equal(ids.long(), want)
